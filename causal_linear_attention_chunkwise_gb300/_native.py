@@ -12,6 +12,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_lib", "lib
 
 # Symbols the header declares, with (restype, argtypes).
 _vp, _i, _u, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_uint, ctypes.c_size_t
+_ll, _f = ctypes.c_longlong, ctypes.c_float
 SIGNATURES = {
     "la_set_feature_map": (_i, [_i]),
     "la_get_feature_map": (_i, []),
@@ -33,6 +34,16 @@ SIGNATURES = {
                                  _vp, _sz, _vp]),
     "la_channel_gate_fwd_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i, _i]),
     "la_delta_fwd": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "la_causal_conv_fwd": (_i, [_vp, _ll, _i, _i, _i, _i, _i, _vp, _vp, _i, _vp, _vp, _vp, _ll,
+                                _vp, _vp]),
+    "la_selective_scan_fwd": (_i, [_vp, _ll, _vp, _ll, _vp, _ll, _vp, _ll, _vp, _ll, _i, _i, _i,
+                                   _i, _i, _i, _vp, _vp, _i, _vp, _vp, _vp, _vp, _ll, _vp, _vp,
+                                   _sz, _vp]),
+    "la_selective_scan_fwd_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
+    "la_gated_norm_fwd": (_i, [_vp, _ll, _ll, _ll, _vp, _ll, _i, _i, _i, _i, _i, _i, _i, _i,
+                               _vp, _vp, _i, _f, _vp, _ll, _vp]),
+    "la_residual_norm_fwd": (_i, [_vp, _i, _vp, _i, _ll, _i, _vp, _vp, _f, _vp, _vp, _i, _f,
+                                  _vp, _vp, _vp]),
     "la_device_status": (_i, [_vp]),
     "la_selftest_wait_timeout": (_i, [_u, _vp]),
     "la_last_error": (ctypes.c_char_p, []),

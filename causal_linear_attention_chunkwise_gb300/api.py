@@ -8,6 +8,8 @@ end-to-end path the benchmark times with host buffers).
 """
 from __future__ import annotations
 
+import math
+
 import torch
 
 from . import _native
@@ -15,6 +17,8 @@ from . import _native
 PHI = {"identity": 0, "elu1": 1}
 DTYPE = {torch.float32: 0, torch.bfloat16: 1}
 DECAY = {"none": 0, "head": 1, "token": 2, "logit": 3}
+ACT = {"none": 0, "silu": 1, "sigmoid": 2}
+NORM = {"rms": 0, "layer": 1}
 
 LA_OK, LA_ERR_INVALID_ARG, LA_ERR_UNSUPPORTED, LA_ERR_CUDA, LA_ERR_DEVICE_TIMEOUT = range(5)
 
@@ -304,6 +308,232 @@ def la_delta_fwd(q, k, v, beta, log_alpha=None, S0=None, O=None, S_final=None,
         _ptr(q), _ptr(k), _ptr(v), DTYPE[q.dtype], B, H, L, dk, v.shape[-1], _ptr(beta),
         _ptr(log_alpha), _ptr(S0), _ptr(O), _ptr(S_final), _stream(stream)))
     return O, S_final
+
+
+# ---------------------------------------------------------------- state space block
+def _on_device(*ts):
+    """Every tensor given lies on the current device (the one the library launches on)."""
+    dev = None
+    for t in ts:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("expected CUDA tensors")
+        if dev is None:
+            dev = torch.cuda.current_device()
+        if t.get_device() != dev:
+            raise ValueError("expected tensors on the current device")
+
+
+def _param(t, shape, what):
+    if t is not None and (t.dtype != torch.float32 or t.shape != shape or not t.is_contiguous()):
+        raise ValueError(f"{what} must be contiguous fp32 {list(shape)}")
+
+
+def _row_stride(t, shape, dtype, what):
+    """Elements between the tokens of ``t`` = [B,L,...] (token rows contiguous,
+    sequences L rows apart), after its shape and dtype have been checked."""
+    if t.shape != shape or t.dtype != dtype:
+        raise ValueError(f"{what} must be {dtype} {list(shape)}")
+    if t.is_contiguous():
+        return math.prod(shape[2:])
+    inner = 1
+    for n, st in zip(reversed(shape[2:]), reversed(t.stride()[2:])):
+        if n > 1 and st != inner:
+            raise ValueError(f"the values of one token of {what} must be contiguous")
+        inner *= n
+    st = t.stride()
+    row = st[1] if shape[1] > 1 else st[0] if shape[0] > 1 else inner
+    if row < inner or (shape[0] > 1 and st[0] != shape[1] * row):
+        raise ValueError(f"the tokens of {what} must lie evenly apart")
+    return row
+
+
+def _lengths_arg(lengths, B):
+    if lengths is not None and (lengths.dtype != torch.int32 or lengths.shape != (B,)
+                                or not lengths.is_contiguous()):
+        raise ValueError("lengths must be contiguous int32 [B]")
+
+
+def _new(shape, dtype, device, stream, zero=False):
+    """An output on the stream that the call runs on."""
+    make = torch.zeros if zero else torch.empty
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=dtype, device=device)
+
+
+def _scratch(nbytes, device, stream):
+    """Workspace of one call: the cached buffer of its stream, but a buffer of
+    the graph's own while a graph is captured (graphs may be replayed side by
+    side, and a cached buffer may be replaced by a larger one)."""
+    if nbytes == 0:
+        return None
+    s = torch.cuda.current_stream() if stream is None else stream
+    with torch.cuda.stream(s):
+        if torch.cuda.is_current_stream_capturing():
+            return torch.empty(nbytes, dtype=torch.uint8, device=device)
+        key = ("scratch", device.index, s.cuda_stream)
+        buf = _ws_cache.get(key)
+        if buf is None or buf.numel() < nbytes:
+            buf = _ws_cache[key] = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return buf
+
+
+def la_causal_conv_fwd(x, weight, bias=None, activation="silu", state0=None, lengths=None,
+                       y=None, state_final=None, want_final_state=True, stream=None):
+    """Causal depthwise convolution over time, y_t = act(bias + sum_w weight[:,w]
+    x_{t-W+1+w}).  Returns ``(y, state_final)``.
+
+    ``x`` [B,L,D] fp32 or bf16; its rows may be a slice of a wider tensor.
+    ``weight`` fp32 [D,W] with W in 2..8, ``bias`` fp32 [D].  ``activation``:
+    "silu" | "none".  ``state0`` and ``state_final`` [B,W-1,D] in x's dtype are
+    the W-1 inputs before the first and up to the last token; they may be one
+    tensor (with L = 1 that is one decode step in place).  ``lengths`` int32 [B]
+    are the real tokens of a padded batch: the rows of ``y`` behind them are
+    left as they are (zero when ``y`` is made here)."""
+    B, L, D = x.shape
+    W = weight.shape[-1]
+    xs = _row_stride(x, x.shape, x.dtype, "x")
+    _param(weight, (D, W), "weight")
+    _param(bias, (D,), "bias")
+    _lengths_arg(lengths, B)
+    for t in (state0, state_final):
+        if t is not None and (t.dtype != x.dtype or t.shape != (B, W - 1, D)
+                              or not t.is_contiguous()):
+            raise ValueError("the states must be contiguous [B,W-1,D] in x's dtype")
+    _on_device(x, weight, bias, state0, lengths, y, state_final)
+    if y is None:
+        y = _new((B, L, D), x.dtype, x.device, stream, lengths is not None)
+    if state_final is None and want_final_state:
+        state_final = _new((B, W - 1, D), x.dtype, x.device, stream)
+    _check(_native.load().la_causal_conv_fwd(
+        x.data_ptr(), xs, DTYPE[x.dtype], B, L, D, W, weight.data_ptr(), _ptr(bias),
+        ACT[activation], _ptr(lengths), _ptr(state0), y.data_ptr(),
+        _row_stride(y, x.shape, x.dtype, "y"), _ptr(state_final), _stream(stream)))
+    return y, state_final
+
+
+def la_selective_scan_fwd_workspace_bytes(B, L, D, N, groups=1) -> int:
+    return int(_native.load().la_selective_scan_fwd_workspace_bytes(B, L, D, N, groups))
+
+
+def la_selective_scan_fwd(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, dt_softplus=True,
+                          h0=None, lengths=None, y=None, h_final=None, want_final_state=True,
+                          workspace=None, segments=True, stream=None):
+    """Selective state space scan h = exp(delta A) h + delta B x, y = (C h + D x)
+    silu(z), delta = softplus(dt + dt_bias).  Returns ``(y, h_final)``.
+
+    ``x``, ``dt``, ``z`` [B,L,channels] and ``Bm``, ``Cm`` [B,L,N] or
+    [B,L,groups,N], all fp32 or all bf16; each may be a slice of a wider
+    tensor.  ``A`` fp32 [channels,N] (N <= 256), ``D`` and ``dt_bias`` fp32
+    [channels].  ``h0`` and ``h_final`` fp32 [B,channels,N] may be one tensor
+    (with L = 1 that is one decode step in place).  ``lengths`` int32 [B] are
+    the real tokens of a padded batch: the rows of ``y`` behind them are left
+    as they are (zero when ``y`` is made here).  With ``segments`` (the
+    default) a cached workspace lets a long sequence run as several segments
+    side by side."""
+    B, L, ch = x.shape
+    N = A.shape[-1]
+    G = Bm.shape[2] if Bm.dim() == 4 else 1
+    bc = (B, L, G, N) if Bm.dim() == 4 else (B, L, N)
+    xs = _row_stride(x, x.shape, x.dtype, "x")
+    ds = _row_stride(dt, x.shape, x.dtype, "dt")
+    zs = 0 if z is None else _row_stride(z, x.shape, x.dtype, "z")
+    bs = _row_stride(Bm, bc, x.dtype, "Bm")
+    cs = _row_stride(Cm, bc, x.dtype, "Cm")
+    _param(A, (ch, N), "A")
+    _param(D, (ch,), "D")
+    _param(dt_bias, (ch,), "dt_bias")
+    _param(h0, (B, ch, N), "h0")
+    _param(h_final, (B, ch, N), "h_final")
+    _lengths_arg(lengths, B)
+    _on_device(x, dt, z, Bm, Cm, A, D, dt_bias, h0, lengths, y, h_final, workspace)
+    if y is None:
+        y = _new((B, L, ch), x.dtype, x.device, stream, lengths is not None)
+    if h_final is None and want_final_state:
+        h_final = _new((B, ch, N), torch.float32, x.device, stream)
+    if workspace is None and segments and L > 1:
+        workspace = _scratch(la_selective_scan_fwd_workspace_bytes(B, L, ch, N, G), x.device,
+                             stream)
+    _check(_native.load().la_selective_scan_fwd(
+        x.data_ptr(), xs, dt.data_ptr(), ds, _ptr(z), zs, Bm.data_ptr(), bs, Cm.data_ptr(), cs,
+        DTYPE[x.dtype], B, L, ch, N, G, A.data_ptr(), _ptr(dt_bias), int(dt_softplus), _ptr(D),
+        _ptr(h0), _ptr(lengths), y.data_ptr(), _row_stride(y, x.shape, x.dtype, "y"),
+        _ptr(h_final), _ptr(workspace),
+        0 if workspace is None else workspace.numel() * workspace.element_size(),
+        _stream(stream)))
+    return y, h_final
+
+
+def la_gated_norm_fwd(x, gate=None, weight=None, bias=None, norm="rms", activation="silu",
+                      gate_first=False, eps=1e-5, y=None, stream=None):
+    """Norm over the last axis of ``x`` [B,H,L,d] times ``weight`` and act(gate),
+    written token major as [B,L,H*d] for the output projection.  Returns ``y``.
+
+    ``x`` fp32 or bf16 with any strides whose last is 1: O of the attention
+    calls as it is, or a permuted view of a token-major tensor.  ``gate``
+    [B,L,H*d]; ``weight`` and ``bias`` fp32 [d] (shared by the heads) or [H*d].
+    ``norm``: "rms" | "layer"; ``activation``: "silu" | "sigmoid" | "none";
+    ``gate_first`` gates x before its norm instead of after it.  ``y`` may be
+    ``gate``."""
+    B, H, L, d = x.shape
+    xb, xh, xt, x1 = x.stride()
+    if x1 != 1 and d > 1 and x.numel() > 0:
+        raise ValueError("the last axis of x must be contiguous")
+    shape = (B, L, H * d)
+    heads = 1
+    for t in (weight, bias):
+        if t is not None:
+            if t.dtype != torch.float32 or not t.is_contiguous() or t.numel() not in (d, H * d):
+                raise ValueError("weight and bias must be contiguous fp32 [d] or [H*d]")
+            if t.numel() != d:
+                heads = H
+    if weight is not None and bias is not None and weight.numel() != bias.numel():
+        raise ValueError("weight and bias must have one shape")
+    gs = 0 if gate is None else _row_stride(gate, shape, x.dtype, "gate")
+    _on_device(x, gate, weight, bias, y)
+    if y is None:
+        y = _new(shape, x.dtype, x.device, stream)
+    _check(_native.load().la_gated_norm_fwd(
+        x.data_ptr(), xb, xh, xt, _ptr(gate), gs, DTYPE[x.dtype], B, H, L, d, NORM[norm],
+        ACT[activation], int(gate_first), _ptr(weight), _ptr(bias), heads, eps, y.data_ptr(),
+        _row_stride(y, shape, x.dtype, "y"), _stream(stream)))
+    return y
+
+
+def la_residual_norm_fwd(x, residual=None, weight=None, bias=None, post_weight=None, scale=None,
+                         alpha=1.0, norm="rms", eps=1e-5, y=None, residual_out=None,
+                         residual_dtype=None, stream=None):
+    """The step between two blocks: r = residual + alpha scale post(x) with
+    post(x) = norm(x) post_weight (x itself without ``post_weight``), then
+    y = norm(r) weight + bias.  Returns ``(y, residual_out)`` with residual_out
+    = r.
+
+    ``x`` [...,D] contiguous, fp32 or bf16; ``residual`` the same shape, in x's
+    dtype or fp32 (None: zero; ``residual_dtype`` then chooses residual_out's,
+    x's by default).  The parameters are fp32 [D].  ``y`` may be ``x`` and
+    ``residual_out`` may be ``residual``."""
+    D = x.shape[-1]
+    rd = residual.dtype if residual is not None else \
+        residual_out.dtype if residual_out is not None else residual_dtype or x.dtype
+    for t in (post_weight, scale, weight, bias):
+        _param(t, (D,), "weights and scale")
+    for t, dt in ((x, x.dtype), (residual, rd), (y, x.dtype), (residual_out, rd)):
+        if t is not None and (t.shape != x.shape or t.dtype != dt or not t.is_contiguous()):
+            raise ValueError("x, residual and the outputs must be contiguous and of one shape, "
+                             "y in x's dtype and residual_out in residual's")
+    _on_device(x, residual, weight, bias, post_weight, scale, y, residual_out)
+    if y is None:
+        y = _new(x.shape, x.dtype, x.device, stream)
+    if residual_out is None:
+        residual_out = _new(x.shape, rd, x.device, stream)
+    _check(_native.load().la_residual_norm_fwd(
+        x.data_ptr(), DTYPE[x.dtype], _ptr(residual), DTYPE[rd],
+        x.numel() // D if D else 0, D, _ptr(post_weight), _ptr(scale), alpha, _ptr(weight),
+        _ptr(bias), NORM[norm], eps, y.data_ptr(), residual_out.data_ptr(), _stream(stream)))
+    return y, residual_out
 
 
 def la_device_status(stream=None) -> None:

@@ -93,6 +93,34 @@ la_status run_variant(const char *fn, const VariantArgs &a) {
   return ok();
 }
 
+// The bytes that `rows` rows of `width` elements, `stride` elements apart, lie in.
+struct Rows {
+  const void *p;
+  long long rows, width, stride;
+  size_t elt;
+};
+
+// Whether an output shares an element with an input.  Rows of equal pitch may
+// interleave (two slices of one wider tensor).
+bool overlap(const Rows &a, const Rows &b) {
+  if (!a.p || !b.p || a.rows <= 0 || b.rows <= 0) return false;
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
+  const uintptr_t a1 = a0 + ((size_t)(a.rows - 1) * a.stride + a.width) * a.elt;
+  const uintptr_t b1 = b0 + ((size_t)(b.rows - 1) * b.stride + b.width) * b.elt;
+  if (a1 <= b0 || b1 <= a0) return false;
+  const uintptr_t pitch = (uintptr_t)a.stride * a.elt;
+  if (pitch != (uintptr_t)b.stride * b.elt || pitch == 0) return true;
+  const uintptr_t ahead = b0 >= a0 ? (b0 - a0) % pitch : (pitch - (a0 - b0) % pitch) % pitch;
+  return ahead < a.width * a.elt || ahead + b.width * b.elt > pitch;
+}
+
+// The same for dense ranges of bytes.
+Rows dense(const void *p, size_t bytes) { return {p, 1, (long long)bytes, (long long)bytes, 1}; }
+
+bool aligned_elt(const void *p, size_t elt) {
+  return (reinterpret_cast<uintptr_t>(p) & (elt - 1)) == 0;
+}
+
 const char *kernel_name(unsigned int id) {
   switch (id) {
     case KID_PREFILL_TC_STATE: return "prefill segment-state kernel";
@@ -407,6 +435,202 @@ la_status la_delta_fwd(const void *q, const void *k, const void *v, int dtype, i
   VariantArgs a{VARIANT_DELTA, q, k, v, dtype, B, H, L, d_k, d_v, 0, g_phi.load(), log_alpha,
                 beta, S0, O, S_final, st};
   return run_variant(fn, a);
+}
+
+la_status la_causal_conv_fwd(const void *x, long long x_stride, int dtype, int B, int L, int D,
+                             int width, const float *weight, const float *bias, int activation,
+                             const int *lengths, const void *state0, void *y,
+                             long long y_stride, void *state_final, void *cuda_stream) {
+  const char *fn = "la_causal_conv_fwd";
+  if (dtype != LA_F32 && dtype != LA_BF16)
+    return fail(LA_ERR_INVALID_ARG, "%s: unknown dtype %d", fn, dtype);
+  if (B < 0 || L < 0 || D < 0)
+    return fail(LA_ERR_INVALID_ARG, "%s: bad sizes B=%d L=%d D=%d", fn, B, L, D);
+  if (activation != LA_ACT_NONE && activation != LA_ACT_SILU)
+    return fail(LA_ERR_INVALID_ARG, "%s: activation %d is not none or silu", fn, activation);
+  if (width < 2 || width > 8)
+    return fail(LA_ERR_UNSUPPORTED, "%s: width %d outside 2..8", fn, width);
+  if (x_stride < D || y_stride < D)
+    return fail(LA_ERR_INVALID_ARG, "%s: row strides %lld, %lld shorter than a row of %d", fn,
+                x_stride, y_stride, D);
+  if ((size_t)B * D == 0) return ok();
+  const size_t elt = dtype == LA_F32 ? 4 : 2;
+  if (!weight || (L > 0 && (!x || !y)))
+    return fail(LA_ERR_INVALID_ARG, "%s: x, weight and y must be non-null", fn);
+  if (!aligned_elt(x, elt) || !aligned_elt(y, elt) || !aligned_elt(state0, elt) ||
+      !aligned_elt(state_final, elt) || !aligned_elt(lengths, 4))
+    return fail(LA_ERR_INVALID_ARG, "%s: pointers must be aligned to their elements", fn);
+  if (!aligned16(weight) || !aligned16(bias))
+    return fail(LA_ERR_INVALID_ARG, "%s: weight and bias must be 16-byte aligned", fn);
+  const long long rows = (long long)B * L;
+  const size_t state_bytes = (size_t)B * (width - 1) * D * elt;
+  const Rows xr{x, rows, D, x_stride, elt}, yr{y, rows, D, y_stride, elt};
+  const Rows s0 = dense(state0, state_bytes), s1 = dense(state_final, state_bytes);
+  if (overlap(yr, xr) || overlap(yr, s0) || overlap(yr, s1) || overlap(s1, xr) ||
+      (state_final != state0 && overlap(s1, s0)))
+    return fail(LA_ERR_INVALID_ARG, "%s: an output overlaps an input or another output", fn);
+  ConvArgs a{x, x_stride, dtype, B, L, D, width, weight, bias, activation, lengths, state0, y,
+             y_stride, state_final, static_cast<cudaStream_t>(cuda_stream)};
+  cudaError_t e = launch_causal_conv(a);
+  if (e != cudaSuccess) return cuda_fail(e, fn);
+  return ok();
+}
+
+size_t la_selective_scan_fwd_workspace_bytes(int B, int L, int D, int N, int groups) {
+  if (B <= 0 || L <= 0 || D <= 0 || N < 1 || N > 256 || groups < 1 || D % groups) return 0;
+  return selective_scan_workspace_bytes(B, L, D, N, groups);
+}
+
+la_status la_selective_scan_fwd(const void *x, long long x_stride, const void *dt,
+                                long long dt_stride, const void *z, long long z_stride,
+                                const void *Bm, long long b_stride, const void *Cm,
+                                long long c_stride, int dtype, int B, int L, int D, int N,
+                                int groups, const float *A, const float *dt_bias,
+                                int dt_softplus, const float *skip, const float *h0,
+                                const int *lengths, void *y, long long y_stride,
+                                float *h_final, void *workspace, size_t ws_bytes,
+                                void *cuda_stream) {
+  const char *fn = "la_selective_scan_fwd";
+  if (dtype != LA_F32 && dtype != LA_BF16)
+    return fail(LA_ERR_INVALID_ARG, "%s: unknown dtype %d", fn, dtype);
+  if (B < 0 || L < 0 || D < 0 || N <= 0 || groups <= 0)
+    return fail(LA_ERR_INVALID_ARG, "%s: bad sizes B=%d L=%d D=%d N=%d groups=%d", fn, B, L, D,
+                N, groups);
+  if (N > 256) return fail(LA_ERR_UNSUPPORTED, "%s: N=%d outside 1..256", fn, N);
+  if (D % groups)
+    return fail(LA_ERR_UNSUPPORTED, "%s: D=%d is not a multiple of groups=%d", fn, D, groups);
+  const long long gn = (long long)groups * N;
+  if (x_stride < D || dt_stride < D || (z && z_stride < D) || y_stride < D || b_stride < gn ||
+      c_stride < gn)
+    return fail(LA_ERR_INVALID_ARG, "%s: a token stride is shorter than its row", fn);
+  if ((size_t)B * D == 0) return ok();
+  if (!aligned16(A) || !aligned16(dt_bias) || !aligned16(skip) || !aligned16(h0) ||
+      !aligned16(h_final))
+    return fail(LA_ERR_INVALID_ARG,
+                "%s: A, dt_bias, skip and the states must be 16-byte aligned", fn);
+  cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+  const size_t state_bytes = (size_t)B * D * N * sizeof(float);
+  const Rows s0 = dense(h0, state_bytes), s1 = dense(h_final, state_bytes);
+  if (h_final != h0 && overlap(s1, s0))
+    return fail(LA_ERR_INVALID_ARG, "%s: h_final overlaps h0", fn);
+  if (L == 0) {
+    cudaError_t e = pass_through_state(h_final, h0, state_bytes, st);
+    if (e != cudaSuccess) return cuda_fail(e, fn);
+    return ok();
+  }
+  if (!x || !dt || !Bm || !Cm || !A || !y)
+    return fail(LA_ERR_INVALID_ARG, "%s: x, dt, Bm, Cm, A and y must be non-null", fn);
+  const size_t elt = dtype == LA_F32 ? 4 : 2;
+  for (const void *p : {x, dt, z, Bm, Cm, static_cast<const void *>(y)})
+    if (!aligned_elt(p, elt))
+      return fail(LA_ERR_INVALID_ARG, "%s: pointers must be aligned to their elements", fn);
+  if (!aligned_elt(lengths, 4))
+    return fail(LA_ERR_INVALID_ARG, "%s: lengths must be 4-byte aligned", fn);
+  const long long rows = (long long)B * L;
+  const Rows yr{y, rows, D, y_stride, elt};
+  const Rows in[] = {{x, rows, D, x_stride, elt},   {dt, rows, D, dt_stride, elt},
+                     {z, rows, D, z_stride, elt},   {Bm, rows, gn, b_stride, elt},
+                     {Cm, rows, gn, c_stride, elt}, s0};
+  for (const Rows &r : in)
+    if (overlap(yr, r) || (r.p != h0 && overlap(s1, r)))
+      return fail(LA_ERR_INVALID_ARG, "%s: an output overlaps an input", fn);
+  if (overlap(yr, s1)) return fail(LA_ERR_INVALID_ARG, "%s: y overlaps h_final", fn);
+  const size_t need = selective_scan_workspace_bytes(B, L, D, N, groups);
+  if (workspace && ws_bytes < need)
+    return fail(LA_ERR_INVALID_ARG, "%s: workspace of %zu bytes needed, %zu given", fn, need,
+                ws_bytes);
+  if (workspace && !aligned16(workspace))
+    return fail(LA_ERR_INVALID_ARG, "%s: workspace must be 16-byte aligned", fn);
+  ScanArgs a{x, dt, z, Bm, Cm, x_stride, dt_stride, z_stride, b_stride, c_stride, dtype, B, L,
+             D, N, groups, A, dt_bias, dt_softplus, skip, h0, lengths, y, y_stride, h_final,
+             need ? workspace : nullptr, st};
+  cudaError_t e = launch_selective_scan(a);
+  if (e != cudaSuccess) return cuda_fail(e, fn);
+  return ok();
+}
+
+la_status la_gated_norm_fwd(const void *x, long long x_b_stride, long long x_h_stride,
+                            long long x_t_stride, const void *gate, long long gate_stride,
+                            int dtype, int B, int H, int L, int d, int norm, int activation,
+                            int gate_first, const float *weight, const float *bias,
+                            int weight_heads, float eps, void *y, long long y_stride,
+                            void *cuda_stream) {
+  const char *fn = "la_gated_norm_fwd";
+  if (dtype != LA_F32 && dtype != LA_BF16)
+    return fail(LA_ERR_INVALID_ARG, "%s: unknown dtype %d", fn, dtype);
+  if (B < 0 || H < 0 || L < 0 || d <= 0)
+    return fail(LA_ERR_INVALID_ARG, "%s: bad sizes B=%d H=%d L=%d d=%d", fn, B, H, L, d);
+  if (norm != LA_NORM_RMS && norm != LA_NORM_LAYER)
+    return fail(LA_ERR_INVALID_ARG, "%s: unknown norm %d", fn, norm);
+  if (activation < LA_ACT_NONE || activation > LA_ACT_SIGMOID)
+    return fail(LA_ERR_INVALID_ARG, "%s: unknown activation %d", fn, activation);
+  if (!(eps >= 0.f)) return fail(LA_ERR_INVALID_ARG, "%s: eps must be >= 0", fn);
+  if (d > 16384) return fail(LA_ERR_UNSUPPORTED, "%s: d=%d outside 1..16384", fn, d);
+  if (weight_heads != 1 && weight_heads != H)
+    return fail(LA_ERR_INVALID_ARG, "%s: weight_heads=%d is neither 1 nor H=%d", fn,
+                weight_heads, H);
+  const long long width = (long long)H * d;
+  if (x_b_stride < 0 || x_h_stride < 0 || x_t_stride < 0 || y_stride < width ||
+      (gate && gate_stride < width))
+    return fail(LA_ERR_INVALID_ARG, "%s: negative stride, or a row stride shorter than H*d", fn);
+  if ((size_t)B * H == 0 || L == 0) return ok();
+  if (!x || !y) return fail(LA_ERR_INVALID_ARG, "%s: x and y must be non-null", fn);
+  const size_t elt = dtype == LA_F32 ? 4 : 2;
+  if (!aligned_elt(x, elt) || !aligned_elt(gate, elt) || !aligned_elt(y, elt))
+    return fail(LA_ERR_INVALID_ARG, "%s: pointers must be aligned to their elements", fn);
+  if (!aligned16(weight) || !aligned16(bias))
+    return fail(LA_ERR_INVALID_ARG, "%s: weight and bias must be 16-byte aligned", fn);
+  const long long rows = (long long)B * L;
+  const Rows yr{y, rows, width, y_stride, elt}, gr{gate, rows, width, gate_stride, elt};
+  const long long span = (B - 1) * x_b_stride + (H - 1) * x_h_stride + (L - 1) * x_t_stride + d;
+  Rows xr{x, 1, span, span, elt};
+  if (x_h_stride == d && x_b_stride == L * x_t_stride && x_t_stride >= width)
+    xr = {x, rows, width, x_t_stride, elt};  // token-major rows, which may be a slice
+  if (overlap(yr, xr) || (!(y == gate && y_stride == gate_stride) && overlap(yr, gr)))
+    return fail(LA_ERR_INVALID_ARG, "%s: y overlaps an input", fn);
+  GatedNormArgs a{x, x_b_stride, x_h_stride, x_t_stride, gate, gate_stride, dtype, B, H, L, d,
+                  norm, activation, gate_first, weight, bias, weight_heads, eps, y, y_stride,
+                  static_cast<cudaStream_t>(cuda_stream)};
+  cudaError_t e = launch_gated_norm(a);
+  if (e != cudaSuccess) return cuda_fail(e, fn);
+  return ok();
+}
+
+la_status la_residual_norm_fwd(const void *x, int dtype, const void *residual, int res_dtype,
+                               long long rows, int D, const float *post_weight,
+                               const float *scale, float alpha, const float *weight,
+                               const float *bias, int norm, float eps, void *y,
+                               void *residual_out, void *cuda_stream) {
+  const char *fn = "la_residual_norm_fwd";
+  if (dtype != LA_F32 && dtype != LA_BF16)
+    return fail(LA_ERR_INVALID_ARG, "%s: unknown dtype %d", fn, dtype);
+  if (res_dtype != LA_F32 && res_dtype != dtype)
+    return fail(LA_ERR_INVALID_ARG, "%s: the residual's dtype %d is neither fp32 nor x's", fn,
+                res_dtype);
+  if (rows < 0 || D <= 0)
+    return fail(LA_ERR_INVALID_ARG, "%s: bad sizes rows=%lld D=%d", fn, rows, D);
+  if (norm != LA_NORM_RMS && norm != LA_NORM_LAYER)
+    return fail(LA_ERR_INVALID_ARG, "%s: unknown norm %d", fn, norm);
+  if (!(eps >= 0.f)) return fail(LA_ERR_INVALID_ARG, "%s: eps must be >= 0", fn);
+  if (D > 16384) return fail(LA_ERR_UNSUPPORTED, "%s: D=%d outside 1..16384", fn, D);
+  if (rows == 0) return ok();
+  if (!x || !y) return fail(LA_ERR_INVALID_ARG, "%s: x and y must be non-null", fn);
+  const size_t elt = dtype == LA_F32 ? 4 : 2, relt = res_dtype == LA_F32 ? 4 : 2;
+  if (!aligned_elt(x, elt) || !aligned_elt(y, elt) || !aligned_elt(residual, relt) ||
+      !aligned_elt(residual_out, relt))
+    return fail(LA_ERR_INVALID_ARG, "%s: pointers must be aligned to their elements", fn);
+  if (!aligned16(post_weight) || !aligned16(scale) || !aligned16(weight) || !aligned16(bias))
+    return fail(LA_ERR_INVALID_ARG, "%s: parameters must be 16-byte aligned", fn);
+  const Rows xr = dense(x, rows * D * elt), yr = dense(y, rows * D * elt);
+  const Rows rr = dense(residual, rows * D * relt), ro = dense(residual_out, rows * D * relt);
+  if ((y != x && overlap(yr, xr)) || overlap(yr, rr) || overlap(yr, ro) || overlap(ro, xr) ||
+      (residual_out != residual && overlap(ro, rr)))
+    return fail(LA_ERR_INVALID_ARG, "%s: an output overlaps an input or the other output", fn);
+  ResidualNormArgs a{x, dtype, residual, res_dtype, rows, D, post_weight, scale, alpha, weight,
+                     bias, norm, eps, y, residual_out, static_cast<cudaStream_t>(cuda_stream)};
+  cudaError_t e = launch_residual_norm(a);
+  if (e != cudaSuccess) return cuda_fail(e, fn);
+  return ok();
 }
 
 la_status la_device_status(void *cuda_stream) {

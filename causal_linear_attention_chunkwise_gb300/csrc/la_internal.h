@@ -124,6 +124,77 @@ cudaError_t launch_normaliser(const NormaliserArgs &a);
 bool decode_supported(int dk, int dv);
 cudaError_t launch_decode(const DecodeArgs &a);
 
+// Causal depthwise convolution (width 2..8).
+struct ConvArgs {
+  const void *x;
+  long long x_stride;
+  int dtype;
+  int B, L, D, width;
+  const float *weight, *bias;
+  int act;
+  const int *lengths;
+  const void *state0;
+  void *y;
+  long long y_stride;
+  void *state_final;
+  cudaStream_t stream;
+};
+cudaError_t launch_causal_conv(const ConvArgs &a);
+
+// Selective state space scan (1 <= N <= 256).
+struct ScanArgs {
+  const void *x, *dt, *z, *Bm, *Cm;
+  long long x_stride, dt_stride, z_stride, b_stride, c_stride;
+  int dtype;
+  int B, L, D, N, groups;
+  const float *A, *dt_bias;
+  int softplus;
+  const float *skip, *h0;
+  const int *lengths;
+  void *y;
+  long long y_stride;
+  float *h_final;
+  void *workspace;  // segment states, or null: each sequence in one piece
+  cudaStream_t stream;
+};
+size_t selective_scan_workspace_bytes(int B, int L, int D, int N, int groups);
+cudaError_t launch_selective_scan(const ScanArgs &a);
+
+// Gated norm of heads and the residual step's norms (width 1..16384).
+struct GatedNormArgs {
+  const void *x;
+  long long x_bs, x_hs, x_ts;
+  const void *gate;
+  long long gate_stride;
+  int dtype;
+  int B, H, L, d;
+  int norm, act, gate_first;
+  const float *weight, *bias;
+  int weight_heads;
+  float eps;
+  void *y;
+  long long y_stride;
+  cudaStream_t stream;
+};
+cudaError_t launch_gated_norm(const GatedNormArgs &a);
+
+struct ResidualNormArgs {
+  const void *x;
+  int dtype;
+  const void *residual;
+  int res_dtype;
+  long long rows;
+  int D;
+  const float *post_weight, *scale;
+  float alpha;
+  const float *weight, *bias;
+  int norm;
+  float eps;
+  void *y, *residual_out;
+  cudaStream_t stream;
+};
+cudaError_t launch_residual_norm(const ResidualNormArgs &a);
+
 // Set the message la_last_error() returns on the calling thread.
 void set_last_error(const char *msg);
 

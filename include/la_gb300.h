@@ -263,6 +263,152 @@ la_status la_delta_fwd(const void *q, const void *k, const void *v, int dtype,
                        const float *S0, void *O, float *S_final, void *cuda_stream);
 
 /*
+ * The operators of a state space block, and the norms around a block.
+ *
+ * They extend the conventions above in two points.  Activations are token
+ * major: [B,L,D] with a row per token, whose rows may lie `*_stride` elements
+ * apart (>= the row's width; sequence b starts at row b*L), so that a slice of a wider projection's
+ * output is read or written in place.  And a pointer to activations needs no
+ * more than its element's alignment (rows that keep 16-byte alignment are
+ * read in 16-byte vectors).  Parameters (weights, biases, A, the skip and the
+ * norm weights) and recurrent states are fp32, 16-byte aligned.
+ *
+ *   lengths   int32 [B] device memory, or NULL.  lengths[b] <= L tokens of
+ *             sequence b are real (values outside [0, L] count as the nearer
+ *             bound).  Rows behind them are neither read nor written, and the
+ *             final state is the state after lengths[b] tokens.
+ *
+ * Outputs may not overlap inputs, except as stated: a final state may be the
+ * buffer of its initial state, so that L = 1 is a decode step in place.
+ * Errors: LA_ERR_INVALID_ARG (null, misaligned or overlapping pointer,
+ * negative size, stride shorter than a row, unknown enum, workspace too
+ * small), LA_ERR_UNSUPPORTED (a size outside the stated range), LA_ERR_CUDA.
+ * The calls are asynchronous on `cuda_stream`, allocate nothing, and give the
+ * same bits on every run.  They do not depend on la_set_feature_map.
+ */
+#define LA_ACT_NONE    0         /* act(x) = x                   */
+#define LA_ACT_SILU    1         /* act(x) = x / (1 + exp(-x))   */
+#define LA_ACT_SIGMOID 2         /* act(x) = 1 / (1 + exp(-x))   */
+
+#define LA_NORM_RMS    0         /* x / sqrt(mean(x^2) + eps)                  */
+#define LA_NORM_LAYER  1         /* (x - mean(x)) / sqrt(var(x) + eps)         */
+
+/*
+ * Causal depthwise convolution over time, the short mixing step in front of a
+ * recurrence:
+ *
+ *     y[b,t,c] = act(bias[c] + sum_{w < width} weight[c,w] x[b,t-width+1+w,c])
+ *
+ * where the rows before the first token come from state0.
+ *
+ *   x, y         [B,L,D] dtype, rows x_stride / y_stride elements apart
+ *   weight       [D,width] fp32, width in 2..8; bias [D] fp32 or NULL (zero)
+ *   activation   LA_ACT_NONE or LA_ACT_SILU
+ *   state0       [B,width-1,D] dtype: the width-1 inputs before the first
+ *                token, oldest first; NULL = zero
+ *   state_final  [B,width-1,D] dtype: the last width-1 inputs (of state0 and
+ *                x together), or NULL; may be state0's buffer
+ */
+la_status la_causal_conv_fwd(const void *x, long long x_stride, int dtype, int B, int L, int D,
+                             int width, const float *weight, const float *bias, int activation,
+                             const int *lengths, const void *state0, void *y,
+                             long long y_stride, void *state_final, void *cuda_stream);
+
+/*
+ * Selective state space scan: a diagonal recurrence with its own decay for
+ * every (channel, state) pair and token,
+ *
+ *     delta    = dt[b,t,c] + dt_bias[c], through softplus if dt_softplus
+ *     h[c,n]   = exp(delta A[c,n]) h[c,n] + delta B[b,t,g,n] x[b,t,c]
+ *     y[b,t,c] = (sum_n C[b,t,g,n] h[c,n] + skip[c] x[b,t,c]) * silu(z[b,t,c])
+ *
+ * with g = c / (D / groups).  la_chunk_fwd covers the recurrences whose decay
+ * one head shares, la_channel_gate_fwd those whose decay the value channels
+ * share.
+ *
+ *   x, dt, y     [B,L,D] dtype, rows *_stride elements apart
+ *   z            [B,L,D] dtype gate, or NULL (no gate)
+ *   Bm, Cm       [B,L,groups,N] dtype; the groups*N values of a token are
+ *                contiguous, tokens b_stride / c_stride elements apart
+ *   A            [D,N] fp32 (negative for a decaying state; used as given)
+ *   dt_bias      [D] fp32 or NULL (zero);  skip [D] fp32 or NULL (zero)
+ *   h0, h_final  [B,D,N] fp32 initial and final state; each may be NULL, and
+ *                h_final may be h0's buffer
+ *   workspace    device scratch of la_selective_scan_fwd_workspace_bytes(...)
+ *                bytes (16-byte aligned), or NULL; ws_bytes = its size.  With
+ *                it (when the query is not 0) a long sequence runs as several
+ *                segments side by side; with NULL it runs in one piece.  A
+ *                non-NULL workspace smaller than the query is
+ *                LA_ERR_INVALID_ARG.  Its contents need no initialisation and
+ *                are not kept.
+ *
+ * Supported: N in 1..256, D a multiple of groups.
+ */
+la_status la_selective_scan_fwd(const void *x, long long x_stride, const void *dt,
+                                long long dt_stride, const void *z, long long z_stride,
+                                const void *Bm, long long b_stride, const void *Cm,
+                                long long c_stride, int dtype, int B, int L, int D, int N,
+                                int groups, const float *A, const float *dt_bias,
+                                int dt_softplus, const float *skip, const float *h0,
+                                const int *lengths, void *y, long long y_stride,
+                                float *h_final, void *workspace, size_t ws_bytes,
+                                void *cuda_stream);
+size_t la_selective_scan_fwd_workspace_bytes(int B, int L, int D, int N, int groups);
+
+/*
+ * Norm and gate of a block's heads, on the way to its output projection:
+ *
+ *     y[b,t,h*d+i] = norm(x[b,h,t,:])[i] w[i] (+ bias[i]) * act(gate[b,t,h*d+i])
+ * or, with gate_first,
+ *     y[b,t,h*d+i] = norm(x[b,h,t,:] * act(gate[b,t,h*d:h*d+d]))[i] w[i] (+ bias[i])
+ *
+ * x is read where it lies: O as la_chunk_fwd and its kin write it
+ * ([B,H,L,d]: strides H*L*d, L*d, d) or a token-major [B,L,H*d] (strides
+ * L*H*d, d, H*d); y and gate are token major, so the heads move behind the
+ * tokens in the same pass.
+ *
+ *   x            dtype, element (b,h,t,i) at b*x_b_stride + h*x_h_stride +
+ *                t*x_t_stride + i (strides >= 0)
+ *   gate         [B,L,H*d] dtype, rows gate_stride apart, or NULL (no gate)
+ *   weight, bias [weight_heads,d] fp32, weight_heads = 1 (shared by the
+ *                heads) or H; each may be NULL (one / zero)
+ *   norm         LA_NORM_*;  activation LA_ACT_*;  eps >= 0
+ *   y            [B,L,H*d] dtype, rows y_stride apart; may be gate's buffer
+ *                when y_stride = gate_stride
+ *
+ * Supported: d in 1..16384.
+ */
+la_status la_gated_norm_fwd(const void *x, long long x_b_stride, long long x_h_stride,
+                            long long x_t_stride, const void *gate, long long gate_stride,
+                            int dtype, int B, int H, int L, int d, int norm, int activation,
+                            int gate_first, const float *weight, const float *bias,
+                            int weight_heads, float eps, void *y, long long y_stride,
+                            void *cuda_stream);
+
+/*
+ * The residual step between two blocks in one pass: the norm after a block,
+ * its residual scale, the addition, and the norm before the next block,
+ *
+ *     u = norm(x) post_weight   (u = x when post_weight is NULL)
+ *     r = residual + alpha scale u            (residual NULL: 0; scale NULL: 1)
+ *     residual_out = r,   y = norm(r) weight + bias
+ *
+ * y is formed from r before its rounding to res_dtype.
+ *
+ *   x, y                    [rows,D] dtype, contiguous; y may be x's buffer
+ *   residual, residual_out  [rows,D] res_dtype (dtype or LA_F32), contiguous;
+ *                           residual_out may be residual's buffer, or NULL
+ *   post_weight, scale, weight, bias   [D] fp32, each may be NULL
+ *
+ * Supported: D in 1..16384.
+ */
+la_status la_residual_norm_fwd(const void *x, int dtype, const void *residual, int res_dtype,
+                               long long rows, int D, const float *post_weight,
+                               const float *scale, float alpha, const float *weight,
+                               const float *bias, int norm, float eps, void *y,
+                               void *residual_out, void *cuda_stream);
+
+/*
  * la_chunk_fwd for callers that cannot allocate device memory.  (The pages
  * have no counterpart: this is a deployment variant of la_chunk_fwd.)
  *
