@@ -7,8 +7,19 @@
 // (channel, state) pair, so no matrix product carries the recurrence: per
 // state and token it takes one exp and four multiply-adds' worth of fp32 work.
 //
-// S neighbouring lanes share a channel, each holding P of its states in
-// registers; the products with C are summed over the lanes by shuffles.
+// A block holds CH channels of one sequence and walks it in tiles of T tokens.
+// Four staging warps turn a tile's inputs into delta and delta x, once per
+// (token, channel), and into fp32 B and C, in shared memory; four recurrence
+// warps run the states over the tile, each lane holding P states of NC
+// channels in registers, S lanes to a channel; the staging warps sum the
+// lanes' parts of y, apply skip and gate, and store.  The tiles are double
+// buffered, so the recurrence of one tile runs beside the staging of the next
+// and the output of the one before.
+//
+// A sequence too long for the channels there are to fill the GPU runs as
+// segments: a first launch gives every segment's own end state (and all of the
+// first segment's output), a second the other segments' outputs, each starting
+// from the states of the segments before it, decayed by exp(A sum delta).
 #include <cstdint>
 
 #include "../../include/la_gb300.h"
@@ -18,7 +29,43 @@
 namespace la {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kStage = 128;           // staging threads
+constexpr int kMain = 128;            // recurrence threads
+constexpr int kThreads = kStage + kMain;
+constexpr int kRing = 5;              // tiles of inputs in shared memory: the one whose output is
+                                      // due, the one being staged, and three on their way
+
+template <int I> struct Int { static constexpr int value = I; };
+
+// Block barriers between the staging and the recurrence warps: one side
+// arrives, the other waits.
+__device__ __forceinline__ void bar_arrive(int id) {
+  asm volatile("barrier.cta.arrive %0, %1;" ::"r"(id), "n"(kThreads) : "memory");
+}
+__device__ __forceinline__ void bar_wait(int id) {
+  asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "n"(kThreads) : "memory");
+}
+
+// Two fp32 values in one 64-bit register pair: one instruction for both.
+__device__ __forceinline__ unsigned long long pack2(float lo, float hi) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(unsigned long long v, float &lo, float &hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b,
+                                                   unsigned long long c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
 
 template <typename T>
 struct ScanParams {
@@ -33,91 +80,592 @@ struct ScanParams {
   T *y;
   long long y_stride;
   float *h_final;
+  // Segments: nseg of seg_len tokens; states [nseg - 1][B][D][N] and sums of
+  // delta [nseg - 1][B][D] in the workspace.
+  int B, nseg, seg_len;
+  float *seg_state, *seg_sum;
 };
 
-template <typename T, int P, int S>
-__global__ void __launch_bounds__(kThreads) selective_scan_kernel(const ScanParams<T> p) {
-  constexpr int CH = kThreads / S;  // channels per block
+// softplus of two values: log(1 + e^v) = max(v, 0) + log1p(e) with e = e^-|v| in
+// (0, 1].  e's exponent is taken in two parts, -|v| log2 e = hi + lo, so that
+// the rounding of hi does not reach e; log1p(e) is 2 atanh(s) with s = e / (2 +
+// e) <= 1/3, whose odd series to s^13 leaves a relative remainder below
+// (1/9)^7 / 15 = 1.4e-8: steps near e^-7 keep the relative precision that
+// log(1 + e) would lose.
+__device__ __forceinline__ unsigned long long dup2(float v) { return pack2(v, v); }
+__device__ __forceinline__ void softplus2(float &v0, float &v1) {
+  const unsigned long long v = pack2(-fabsf(v0), -fabsf(v1));
+  const unsigned long long hi = mul2(v, dup2(kLog2e));
+  unsigned long long lo = fma2(v, dup2(kLog2e), mul2(hi, dup2(-1.f)));
+  lo = fma2(v, dup2(1.925963033500e-8f), lo);  // log2 e - float(log2 e)
+  float h0, h1;
+  unpack2(hi, h0, h1);
+  unsigned long long e = pack2(ex2_approx(h0), ex2_approx(h1));
+  e = fma2(e, mul2(lo, dup2(0.6931471805599453f)), e);  // 2^lo = 1 + lo ln 2
+  float e0, e1;
+  unpack2(e, e0, e1);
+  const unsigned long long s = mul2(e, pack2(rcp_approx(2.f + e0), rcp_approx(2.f + e1)));
+  const unsigned long long q = mul2(s, s);
+  unsigned long long p = fma2(q, dup2(2.f / 13.f), dup2(2.f / 11.f));
+  p = fma2(q, p, dup2(2.f / 9.f));
+  p = fma2(q, p, dup2(2.f / 7.f));
+  p = fma2(q, p, dup2(2.f / 5.f));
+  p = fma2(q, p, dup2(2.f / 3.f));
+  p = fma2(q, p, dup2(2.f));
+  unpack2(fma2(s, p, pack2(fmaxf(v0, 0.f), fmaxf(v1, 0.f))), v0, v1);
+}
+
+constexpr int min_c(int a, int b) { return a < b ? a : b; }
+
+// P states of NC channels per lane, S lanes per channel, elements of E bytes.
+template <int P, int S, int NC, int E>
+struct ScanShape {
+  static constexpr int NP = P * S;                              // states, padded
+  static constexpr int LC = 32 / S;                             // lanes side by side in channels
+  static constexpr int WCH = LC * NC;                           // channels per warp
+  static constexpr int CH = kMain / 32 * WCH;                   // channels per block
+  static constexpr int T = min_c(CH * E >= 256 ? 8 : 16, 1024 / NP);  // tokens per tile
+  static constexpr int Q = min_c(S, 4);                         // parts of y per (token, channel)
+  static constexpr int V = 16 / E;                              // channels a thread stages at once
+  static constexpr int K = CH / V;                              // such chunks per token
+  static constexpr int XR = (T * K + kStage - 1) / kStage;      // chunks per thread
+  static constexpr int BV = min_c(16 / E, NP);                  // states of B or C staged at once
+  static constexpr int BK = NP / BV;
+  static constexpr int BR = (2 * T * BK + kStage - 1) / kStage;
+  // The parts of a warp's channels lie together, [Q][WCH]; its row is padded so
+  // that the staging threads, V channels each, read them from different banks.
+  static constexpr int GROUP = Q * WCH + 4;
+  static constexpr int SLOT_BYTES = T * CH * 8;
+  static constexpr int BC_BYTES = 2 * T * NP * 4;
+  static constexpr int PART_BYTES = T * (kMain / 32) * GROUP * 4;
+  // The inputs as fetched: a ring of kRing tiles, in which every staging thread
+  // has places of its own (x, dt and z chunks, then its B and C chunks).
+  static constexpr int RAW_X = XR * kStage * 16;
+  static constexpr int RAW_BYTES = 3 * RAW_X + BR * kStage * 16;
+  static constexpr int SMEM = 2 * (SLOT_BYTES + BC_BYTES + PART_BYTES) + kRing * RAW_BYTES;
+  static_assert(WCH % 4 == 0 && CH % V == 0 && kStage % K == 0 && NP % 4 == 0, "tile shape");
+  static_assert(SMEM <= 113 * 1024, "two blocks per SM");
+};
+
+// N elements of T as they lie in memory, in 32-bit words.
+template <typename T, int N> struct alignas(sizeof(T) * N) Chunk {
+  uint32_t w[N * sizeof(T) / 4];
+  __device__ __forceinline__ float get(int i) const {  // i known at compile time
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+    else return __uint_as_float(i % 2 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+  }
+  __device__ __forceinline__ void set2(int i, float lo, float hi) {  // elements i, i + 1
+    if constexpr (sizeof(T) == 4) {
+      w[i] = __float_as_uint(lo), w[i + 1] = __float_as_uint(hi);
+    } else {
+      const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+      w[i / 2] = *reinterpret_cast<const uint32_t *>(&v);
+    }
+  }
+};
+
+// How the rows of the inputs are aligned: to 16 bytes, to 4 bytes, or to an element.
+enum : int { ALIGN16 = 16, ALIGN4 = 4, ALIGN_ELT = 1 };
+
+// Bring `count` of N elements of T into this thread's 16-byte (or smaller)
+// place in shared memory; the rest of it becomes 0.  Asynchronous where the
+// alignment allows it.
+template <typename T, int N, int ALIGN>
+__device__ __forceinline__ void fetch_chunk(void *dst, const T *src, int count) {
+  constexpr int BYTES = N * sizeof(T);
+  const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+  if constexpr (ALIGN == ALIGN16 && BYTES == 16) {
+    const int bytes = count * (int)sizeof(T);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(bytes)
+                 : "memory");
+  } else if constexpr (ALIGN >= 4) {
+#pragma unroll
+    for (int i = 0; i < BYTES / 4; ++i) {
+      const int bytes = min(max(count * (int)sizeof(T) - 4 * i, 0), 4);
+      const T *from = src + (bytes > 0 ? i * 4 / (int)sizeof(T) : 0);
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(d + 4 * i), "l"(from),
+                   "r"(bytes)
+                   : "memory");
+    }
+  } else {
+    T *out = static_cast<T *>(dst);
+#pragma unroll
+    for (int i = 0; i < N; ++i) out[i] = i < count ? src[i] : from_f32<T>(0.f);
+  }
+}
+__device__ __forceinline__ void fetch_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int PENDING> __device__ __forceinline__ void fetch_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
+}
+
+// Where the 16 bytes (delta and delta x of channels 2g, 2g + 1) of granule g
+// lie in a token's row: the 8 staging threads of a quarter warp, four granules
+// apart, write to different banks, and neighbouring lanes read neighbours.
+__device__ __forceinline__ int slot_granule(int g) { return g ^ (g >> 3 & 3); }
+
+// One block's share of one segment.  FULL: outputs from the state `from` the
+// segment starts in; else only its end state, from zero, and its sum of delta.
+template <typename T, int P, int S, int NC, int ALIGN, bool FULL>
+__device__ __forceinline__ void scan_segment(const ScanParams<T> &p, long long b, int g, int cg0,
+                                             int seg, int s0, int s1, int len, char *smem) {
+  using Sh = ScanShape<P, S, NC, sizeof(T)>;
+  constexpr int CH = Sh::CH, NP = Sh::NP, TT = Sh::T, Q = Sh::Q, V = Sh::V, K = Sh::K;
+  constexpr int BV = Sh::BV, BK = Sh::BK, WCH = Sh::WCH;
+  const int per_group = p.D / p.groups;
+  const int nch = min(CH, per_group - cg0);
+  const int c0 = g * per_group + cg0;
+  const int end = min(s1, len);  // s0 < end
+  const int tiles = (end - s0 + TT - 1) / TT;
+  char *slots = smem, *bcs = smem + 2 * Sh::SLOT_BYTES, *prt = bcs + 2 * Sh::BC_BYTES;
+  char *raw = prt + 2 * Sh::PART_BYTES;
+
+  if (threadIdx.x >= kMain) {
+    // ------------------------------------------------------------ staging warps
+    const int tid = threadIdx.x - kMain;
+    const int k = tid % K;                        // the chunk of channels it stages in every tile
+    const int sc = k * V;                         // its first channel in the block
+    const int st = tid / K;                       // its first token in the tile
+    const int have = min(max(nch - sc, 0), V);    // channels past the last are staged as zeros
+    float bias[V], skip[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      bias[e] = p.dt_bias && e < have ? p.dt_bias[c0 + sc + e] : 0.f;
+      skip[e] = p.skip && e < have ? p.skip[c0 + sc + e] : 0.f;
+    }
+    const int from_c = c0 + (have > 0 ? sc : 0);  // an address in bounds even where nothing is read
+    const T *xb = p.x + b * p.L * p.x_stride + from_c;
+    const T *db = p.dt + b * p.L * p.dt_stride + from_c;
+    const T *zb = p.z ? p.z + b * p.L * p.z_stride + from_c : nullptr;
+    T *yb = p.y + b * p.L * p.y_stride + c0 + sc;
+    const T *Bb = p.Bm + b * p.L * p.b_stride + (long long)g * p.N;
+    const T *Cb = p.Cm + b * p.L * p.c_stride + (long long)g * p.N;
+
+    char *mine = raw + tid * 16;
+    auto fetch = [&](int tile) {  // rows past the last token repeat it
+      if (tile < tiles) {
+        char *to = mine + tile % kRing * Sh::RAW_BYTES;
+        const int t0 = s0 + tile * TT;
+#pragma unroll
+        for (int r = 0; r < Sh::XR; ++r) {
+          const long long t = min(t0 + st + r * (kStage / K), end - 1);
+          char *at = to + r * kStage * 16;
+          fetch_chunk<T, V, ALIGN>(at, xb + t * p.x_stride, have);
+          fetch_chunk<T, V, ALIGN>(at + Sh::RAW_X, db + t * p.dt_stride, have);
+          if (FULL && zb) fetch_chunk<T, V, ALIGN>(at + 2 * Sh::RAW_X, zb + t * p.z_stride, have);
+        }
+#pragma unroll
+        for (int r = 0; r < Sh::BR; ++r) {
+          const int i = tid + r * kStage;
+          const bool is_c = i / BK >= TT;
+          if (!FULL && is_c) break;
+          const int cnt = min(max(p.N - i % BK * BV, 0), BV), n = cnt > 0 ? i % BK * BV : 0;
+          const long long t = min(t0 + i / BK % TT, end - 1);
+          const T *src = is_c ? Cb + t * p.c_stride : Bb + t * p.b_stride;
+          fetch_chunk<T, BV, ALIGN>(to + 3 * Sh::RAW_X + r * kStage * 16, src + n, cnt);
+        }
+      }
+      fetch_commit();
+    };
+
+    auto output = [&](int tile) {
+      const int t0 = s0 + tile * TT;
+      const float *pt = reinterpret_cast<const float *>(prt + (tile & 1) * Sh::PART_BYTES);
+#pragma unroll
+      for (int r = 0; r < Sh::XR; ++r) {
+        const int t = st + r * (kStage / K);
+        if (t >= TT || t0 + t >= end) break;
+        float v[V];
+#pragma unroll
+        for (int e = 0; e < V; e += 4) {
+          const int c = sc + e;
+          const float *s = pt + (t * (kMain / 32) + c / WCH) * Sh::GROUP + c % WCH;
+          float4 f = *reinterpret_cast<const float4 *>(s);
+#pragma unroll
+          for (int i = 1; i < Q; ++i) {
+            const float4 o = *reinterpret_cast<const float4 *>(s + i * WCH);
+            f.x += o.x, f.y += o.y, f.z += o.z, f.w += o.w;
+          }
+          v[e] = f.x, v[e + 1] = f.y, v[e + 2] = f.z, v[e + 3] = f.w;
+        }
+        const char *from = mine + tile % kRing * Sh::RAW_BYTES + r * kStage * 16;
+        const auto x = *reinterpret_cast<const Chunk<T, V> *>(from);
+        const auto z = *reinterpret_cast<const Chunk<T, V> *>(from + 2 * Sh::RAW_X);
+        Chunk<T, V> o;
+#pragma unroll
+        for (int e = 0; e < V; e += 2) {
+#pragma unroll
+          for (int f = e; f < e + 2; ++f) {
+            v[f] = fmaf(skip[f], x.get(f), v[f]);
+            if (zb) v[f] *= activate(1, z.get(f));
+          }
+          o.set2(e, v[e], v[e + 1]);
+        }
+        T *yr = yb + (long long)(t0 + t) * p.y_stride;
+        if constexpr (ALIGN == ALIGN16) {
+          if (have == V) *reinterpret_cast<uint4 *>(yr) = *reinterpret_cast<const uint4 *>(&o);
+        } else {
+#pragma unroll
+          for (int e = 0; e < V; ++e)
+            if (e < have) yr[e] = from_f32<T>(o.get(e));
+        }
+      }
+    };
+
+    for (int i = 0; i < kRing - 2; ++i) fetch(i);
+    for (int tile = 0; tile < tiles; ++tile) {
+      const int buf = tile & 1;
+      fetch(tile + kRing - 2);  // into the place of the tile whose output came last
+      fetch_wait<kRing - 2>();
+      const char *in = mine + tile % kRing * Sh::RAW_BYTES;
+      if (!FULL && tile >= 2) bar_wait(3 + buf);  // the recurrence is done with this buffer
+      char *sl = slots + buf * Sh::SLOT_BYTES;
+#pragma unroll
+      for (int r = 0; r < Sh::XR; ++r) {
+        const int t = st + r * (kStage / K);
+        if (t >= TT) break;
+        const auto rx = *reinterpret_cast<const Chunk<T, V> *>(in + r * kStage * 16);
+        const auto rd = *reinterpret_cast<const Chunk<T, V> *>(in + Sh::RAW_X + r * kStage * 16);
+#pragma unroll
+        for (int e = 0; e < V; e += 2) {
+          float d0 = rd.get(e) + bias[e], d1 = rd.get(e + 1) + bias[e + 1];
+          if (p.softplus) softplus2(d0, d1);
+          *reinterpret_cast<float4 *>(sl + t * CH * 8 + slot_granule((sc + e) / 2) * 16) =
+              make_float4(d0, d0 * rx.get(e), d1, d1 * rx.get(e + 1));
+        }
+      }
+      float4 *bc = reinterpret_cast<float4 *>(bcs + buf * Sh::BC_BYTES);
+#pragma unroll
+      for (int r = 0; r < Sh::BR; ++r) {
+        const int i = tid + r * kStage;
+        if (i >= (FULL ? 2 : 1) * TT * BK) break;
+        const auto v = *reinterpret_cast<const Chunk<T, BV> *>(in + 3 * Sh::RAW_X +
+                                                               r * kStage * 16);
+#pragma unroll
+        for (int e = 0; e < BV; e += 4)
+          bc[(i * BV + e) / 4] = make_float4(v.get(e), v.get(e + 1), v.get(e + 2), v.get(e + 3));
+      }
+      bar_arrive(1 + buf);
+      if (FULL && tile >= 1) {
+        bar_wait(3 + (buf ^ 1));
+        output(tile - 1);
+      }
+    }
+    if (FULL) {
+      bar_wait(3 + ((tiles - 1) & 1));
+      output(tiles - 1);
+    } else {  // leave no arrival behind
+      if (tiles >= 2) bar_wait(3 + (tiles & 1));
+      bar_wait(3 + ((tiles - 1) & 1));
+    }
+    return;
+  }
+
+  // -------------------------------------------------------------- recurrence warps
+  // Lane (q, cl): lanes that read the same B and C are neighbours.  It holds the
+  // states 4 (q + S j) + i of the channels lc + m.
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int q = lane / Sh::LC, cl = lane % Sh::LC;
+  const int lc = warp * WCH + cl * NC;
+  unsigned long long a[NC][P / 2], h[NC][P / 2];
+#pragma unroll
+  for (int m = 0; m < NC; ++m) {
+    const bool on = lc + m < nch;
+    const long long ch = c0 + (on ? lc + m : 0);
+    const long long at = (b * p.D + ch) * p.N;
+    const long long pitch = (long long)p.B * p.D * p.N;
+#pragma unroll
+    for (int k = 0; k < P; k += 2) {
+      float av[2], hv[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int n = 4 * (q + S * (k / 4)) + k % 4 + e;
+        const bool in = on && n < p.N;
+        av[e] = in ? p.A[ch * p.N + n] * kLog2e : 0.f;
+        hv[e] = 0.f;
+        if (FULL && in) {
+          if (seg == 0) {
+            if (p.h0) hv[e] = p.h0[at + n];
+          } else {
+            hv[e] = p.seg_state[at + n];
+            for (int i = 1; i < seg; ++i)
+              hv[e] = fmaf(ex2_approx(av[e] * p.seg_sum[((long long)i * p.B + b) * p.D + ch]),
+                           hv[e], p.seg_state[i * pitch + at + n]);
+          }
+        }
+      }
+      a[m][k / 2] = pack2(av[0], av[1]);
+      h[m][k / 2] = pack2(hv[0], hv[1]);
+    }
+  }
+  float sum[NC];
+#pragma unroll
+  for (int m = 0; m < NC; ++m) sum[m] = 0.f;
+
+  for (int tile = 0; tile < tiles; ++tile) {
+    const int buf = tile & 1;
+    const char *sl = slots + buf * Sh::SLOT_BYTES;
+    const float4 *bc = reinterpret_cast<const float4 *>(bcs + buf * Sh::BC_BYTES);
+    float *pt = reinterpret_cast<float *>(prt + buf * Sh::PART_BYTES) + warp * Sh::GROUP +
+                q * WCH + cl * NC;
+    float part_sum[NC];
+#pragma unroll
+    for (int m = 0; m < NC; ++m) part_sum[m] = 0.f;
+    bar_wait(1 + buf);
+    // A token passes three stages, one token apart: its loads; its decays and
+    // writes, which do not wait for the state; the recurrence and the read.
+    // A warp alone on its scheduler so keeps loads, exponentials and products
+    // of three tokens in flight.
+    struct Loaded {
+      float d[NC], dx[NC];
+      float4 b[P / 4], c[P / 4];
+    };
+    struct Ready {
+      unsigned long long dec[NC][P / 2], w[NC][P / 2];
+    };
+    auto load = [&](Loaded &l, int t) {
+      const char *row = sl + t * CH * 8;
+      if constexpr (NC == 1) {
+        const float2 s =
+            *reinterpret_cast<const float2 *>(row + slot_granule(lc / 2) * 16 + lc % 2 * 8);
+        l.d[0] = s.x, l.dx[0] = s.y;
+      } else {
+#pragma unroll
+        for (int m = 0; m < NC; m += 2) {
+          const float4 s = *reinterpret_cast<const float4 *>(row + slot_granule((lc + m) / 2) * 16);
+          l.d[m] = s.x, l.dx[m] = s.y, l.d[m + 1] = s.z, l.dx[m + 1] = s.w;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < P / 4; ++j) {
+        l.b[j] = bc[t * (NP / 4) + q + S * j];
+        if (FULL) l.c[j] = bc[(TT + t) * (NP / 4) + q + S * j];
+      }
+    };
+    auto prepare = [&](Ready &r, const Loaded &l) {
+#pragma unroll
+      for (int m = 0; m < NC; ++m) {
+        const unsigned long long d2 = dup2(l.d[m]), x2 = dup2(l.dx[m]);
+#pragma unroll
+        for (int j = 0; j < P / 4; ++j) {
+          float e0, e1, e2, e3;
+          unpack2(mul2(d2, a[m][2 * j]), e0, e1);
+          unpack2(mul2(d2, a[m][2 * j + 1]), e2, e3);
+          r.dec[m][2 * j] = pack2(ex2_approx(e0), ex2_approx(e1));
+          r.dec[m][2 * j + 1] = pack2(ex2_approx(e2), ex2_approx(e3));
+          r.w[m][2 * j] = mul2(x2, pack2(l.b[j].x, l.b[j].y));
+          r.w[m][2 * j + 1] = mul2(x2, pack2(l.b[j].z, l.b[j].w));
+        }
+        if (!FULL) part_sum[m] += l.d[m];
+      }
+    };
+    auto advance = [&](const Ready &r, const Loaded &l, int t) {
+      float part[NC];
+#pragma unroll
+      for (int m = 0; m < NC; ++m) {
+        unsigned long long acc;
+#pragma unroll
+        for (int k = 0; k < P / 2; ++k) {
+          h[m][k] = fma2(r.dec[m][k], h[m][k], r.w[m][k]);
+          if (FULL) {
+            const float4 cv = l.c[k / 2];
+            const unsigned long long c2 = k % 2 ? pack2(cv.z, cv.w) : pack2(cv.x, cv.y);
+            acc = k == 0 ? mul2(c2, h[m][0]) : fma2(c2, h[m][k], acc);
+          }
+        }
+        if (FULL) {
+          float lo, hi;
+          unpack2(acc, lo, hi);
+          part[m] = lo + hi;
+#pragma unroll
+          for (int off = 16; off >= Q * Sh::LC; off >>= 1)
+            part[m] += __shfl_xor_sync(0xffffffffu, part[m], off);
+        }
+      }
+      if (FULL && q < Q) {
+        float *o = pt + t * (kMain / 32) * Sh::GROUP;
+        if constexpr (NC == 1) o[0] = part[0];
+        else if constexpr (NC == 2) *reinterpret_cast<float2 *>(o) = make_float2(part[0], part[1]);
+        else *reinterpret_cast<float4 *>(o) = make_float4(part[0], part[1], part[2], part[3]);
+      }
+    };
+    const int tend = min(TT, end - s0 - tile * TT);
+    Loaded l[3];
+    Ready r[2];
+    if (P * NC <= 16 && tend == TT) {  // more states than that leave no registers for it
+      load(l[0], 0);
+      if (TT > 1) load(l[1], 1);
+      prepare(r[0], l[0]);
+#pragma unroll
+      for (int t = 0; t < TT; ++t) {
+        if (t + 2 < TT) load(l[(t + 2) % 3], t + 2);
+        if (t + 1 < TT) prepare(r[(t + 1) % 2], l[(t + 1) % 3]);
+        advance(r[t % 2], l[t % 3], t);
+      }
+    } else {
+#pragma unroll 1
+      for (int t = 0; t < tend; ++t) {
+        load(l[0], t);
+        prepare(r[0], l[0]);
+        advance(r[0], l[0], t);
+      }
+    }
+    bar_arrive(3 + buf);
+#pragma unroll
+    for (int m = 0; m < NC; ++m) sum[m] += part_sum[m];
+  }
+
+  // The state after the last token, or what later segments start from (a
+  // segment that pass 1 outputs has left its own in pass 0).
+  float *dst = s1 >= len ? p.h_final : nullptr;
+  if (s1 < len && (!FULL || seg == 0))
+    dst = p.seg_state + (long long)seg * p.B * p.D * p.N;
+#pragma unroll
+  for (int m = 0; m < NC; ++m) {
+    if (lc + m >= nch) continue;
+    const long long ch = c0 + lc + m, at = (b * p.D + ch) * p.N;
+    if (!FULL && q == 0) p.seg_sum[((long long)seg * p.B + b) * p.D + ch] = sum[m];
+    if (!dst) continue;
+#pragma unroll
+    for (int k = 0; k < P; k += 2) {
+      const int n = 4 * (q + S * (k / 4)) + k % 4;
+      float lo, hi;
+      unpack2(h[m][k / 2], lo, hi);
+      if (n < p.N) dst[at + n] = lo;
+      if (n + 1 < p.N) dst[at + n + 1] = hi;
+    }
+  }
+}
+
+// Pass 0: segments 0 .. max(nseg - 2, 0), the first in full, the others for
+// their end states.  Pass 1: the outputs of segments 1 .. nseg - 1.
+template <typename T, int P, int S, int NC, int ALIGN>
+__global__ void __launch_bounds__(kThreads, 2)
+selective_scan_kernel(const ScanParams<T> p, int pass) {
+  extern __shared__ __align__(16) char smem[];
+  constexpr int CH = ScanShape<P, S, NC, sizeof(T)>::CH;
   const int per_group = p.D / p.groups;
   const int blocks_g = (per_group + CH - 1) / CH;
   const int blk = blockIdx.x % (blocks_g * p.groups);
   const long long b = blockIdx.x / (blocks_g * p.groups);
   const int g = blk / blocks_g;
-  const int cg = blk % blocks_g * CH + threadIdx.x / S;  // channel within the group
-  const bool live = cg < per_group;
-  const int c = g * per_group + (live ? cg : 0);
-  const int n0 = threadIdx.x % S * P;
+  const int cg0 = blk % blocks_g * CH;  // the block's first channel within its group
+  const int seg = blockIdx.y + pass;
   const int len = p.lengths ? min(max(p.lengths[b], 0), p.L) : p.L;
-
-  float a[P], h[P];
-#pragma unroll
-  for (int i = 0; i < P; ++i) {
-    const bool in = n0 + i < p.N;
-    a[i] = in ? p.A[(long long)c * p.N + n0 + i] * kLog2e : 0.f;
-    h[i] = in && p.h0 ? p.h0[(b * p.D + c) * p.N + n0 + i] : 0.f;
+  const int s0 = seg * p.seg_len;
+  const int s1 = seg == p.nseg - 1 ? p.L : s0 + p.seg_len;
+  if (seg == 0 && len == 0) {  // no tokens: the state passes through
+    const long long at = (b * p.D + g * per_group + cg0) * p.N;
+    const int n = min(CH, per_group - cg0) * p.N;
+    if (p.h_final && p.h_final != p.h0)
+      for (int i = threadIdx.x; i < n; i += kThreads)
+        p.h_final[at + i] = p.h0 ? p.h0[at + i] : 0.f;
+    return;
   }
-  const float bias = p.dt_bias ? p.dt_bias[c] : 0.f;
-  const float skip = p.skip ? p.skip[c] : 0.f;
-  for (int t = 0; t < len; ++t) {
-    const long long row = b * p.L + t;
-    const float x = to_f32(p.x[row * p.x_stride + c]);
-    float delta = to_f32(p.dt[row * p.dt_stride + c]) + bias;
-    if (p.softplus) delta = softplus(delta);
-    const float u = delta * x;
-    float acc = 0.f;
-#pragma unroll
-    for (int i = 0; i < P; ++i) {
-      const bool in = n0 + i < p.N;
-      const float bn = in ? to_f32(p.Bm[row * p.b_stride + g * p.N + n0 + i]) : 0.f;
-      const float cn = in ? to_f32(p.Cm[row * p.c_stride + g * p.N + n0 + i]) : 0.f;
-      h[i] = fmaf(ex2_approx(delta * a[i]), h[i], u * bn);
-      acc = fmaf(cn, h[i], acc);
-    }
-#pragma unroll
-    for (int off = S / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
-    if (live && n0 == 0) {
-      float o = fmaf(skip, x, acc);
-      if (p.z) o *= activate(1, to_f32(p.z[row * p.z_stride + c]));
-      p.y[row * p.y_stride + c] = from_f32<T>(o);
-    }
-  }
-  if (live && p.h_final) {
-#pragma unroll
-    for (int i = 0; i < P; ++i)
-      if (n0 + i < p.N) p.h_final[(b * p.D + c) * p.N + n0 + i] = h[i];
-  }
+  if (s0 >= len) return;
+  if (seg == 0 || pass == 1)
+    scan_segment<T, P, S, NC, ALIGN, true>(p, b, g, cg0, seg, s0, s1, len, smem);
+  else if (s1 < len)  // a segment after this one needs its state
+    scan_segment<T, P, S, NC, ALIGN, false>(p, b, g, cg0, seg, s0, s1, len, smem);
 }
 
-template <typename T, int P, int S>
+// Channels per block, by the number of states.
+constexpr int block_channels(int N) { return N <= 4 ? 128 : N <= 16 ? 64 : N <= 32 ? 32 : 16; }
+
+struct ScanPlan {
+  int nseg, seg_len;
+};
+
+// How many segments.  One block on an SM takes a token in about 50 ns, two in
+// 90 (N = 16, bf16: 1 x 16384 x 2048 in one piece 815 us, 4 x 2048 x 4096 184
+// us), and the SMs hold two, so n blocks take rounds(n) ns per token of theirs.  One
+// piece costs that over L tokens; nseg > 1 segments cost it twice, for nseg - 1
+// segments side by side, over L / nseg tokens, and a launch.  1 x 16384 x 2048
+// (32 blocks): 815 us in one piece, 420 us in 4, 276 in 10 (the first that
+// fills both blocks of all SMs), 322 in 12 (a round and a bit), 275 in 20.
+// 4 x 2048 x 4096 (256 blocks) is fastest in one piece: 184 us, 230 in 3.
+ScanPlan make_plan(int B, int L, int D, int N, int groups) {
+  constexpr int kSMs = 152, kMinLen = 64, kMaxSeg = 64;
+  const int CH = block_channels(N);
+  const double blocks = (double)B * groups * ((D / groups + CH - 1) / CH);
+  auto rounds = [&](double n) {
+    const double full = (double)(long long)(n / (2 * kSMs)), rest = n - full * 2 * kSMs;
+    return 90 * full + (rest > kSMs ? 90 : rest > 0 ? 50 : 0);
+  };
+  ScanPlan best{1, L};
+  double cost = rounds(blocks) * L;
+  for (int n = 2; n <= kMaxSeg && L / n >= kMinLen; ++n) {
+    const int len = ((L + n - 1) / n + 15) / 16 * 16;
+    const double c = 2 * rounds(blocks * (n - 1)) * len + 4000 + 100 * n;
+    if (c < cost && (L + len - 1) / len == n) cost = c, best = {n, len};
+  }
+  return best;
+}
+
+template <typename T, int P, int S, int NC, int ALIGN>
+cudaError_t launch_kernel(const ScanParams<T> &p, cudaStream_t stream) {
+  using Sh = ScanShape<P, S, NC, sizeof(T)>;
+  const int per_group = p.D / p.groups;
+  const long long blocks = (long long)p.B * p.groups * ((per_group + Sh::CH - 1) / Sh::CH);
+  if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+  auto *kernel = selective_scan_kernel<T, P, S, NC, ALIGN>;
+  if (Sh::SMEM > 48 * 1024) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::SMEM);
+    if (e != cudaSuccess) return e;
+  }
+  const unsigned segs = p.nseg > 1 ? p.nseg - 1 : 1;
+  kernel<<<dim3((unsigned)blocks, segs), kThreads, Sh::SMEM, stream>>>(p, 0);
+  if (p.nseg > 1) kernel<<<dim3((unsigned)blocks, segs), kThreads, Sh::SMEM, stream>>>(p, 1);
+  return cudaGetLastError();
+}
+
+template <typename T, int P, int S, int NC>
 cudaError_t launch_ps(const ScanArgs &a) {
-  constexpr int CH = kThreads / S;
+  static_assert(ScanShape<P, S, NC, sizeof(T)>::CH == block_channels(P * S), "the plan's blocks");
+  ScanPlan plan{1, a.L};
+  if (a.workspace) plan = make_plan(a.B, a.L, a.D, a.N, a.groups);
+  float *ws = static_cast<float *>(a.workspace);
+  const size_t states = (size_t)(plan.nseg - 1) * a.B * a.D * a.N;
   const ScanParams<T> p{static_cast<const T *>(a.x), static_cast<const T *>(a.dt),
                         static_cast<const T *>(a.z), static_cast<const T *>(a.Bm),
                         static_cast<const T *>(a.Cm), a.x_stride, a.dt_stride, a.z_stride,
                         a.b_stride, a.c_stride, a.L, a.D, a.N, a.groups, a.A, a.dt_bias,
                         a.softplus, a.skip, a.h0, a.lengths, static_cast<T *>(a.y), a.y_stride,
-                        a.h_final};
-  const long long blocks =
-      (long long)a.B * a.groups * ((a.D / a.groups + CH - 1) / CH);
-  if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-  selective_scan_kernel<T, P, S><<<(unsigned)blocks, kThreads, 0, a.stream>>>(p);
-  return cudaGetLastError();
+                        a.h_final, a.B, plan.nseg, plan.seg_len, ws, ws ? ws + states : nullptr};
+  // The widest loads that every row's alignment allows (a block's first channel
+  // is a multiple of 16 bytes into its group, a chunk 16 bytes or N * 4).
+  const int per_group = a.D / a.groups;
+  auto rows_fit = [&](int bytes) {
+    const int v = bytes / (int)sizeof(T);
+    auto fits = [&](const void *q, long long stride) {
+      return (reinterpret_cast<uintptr_t>(q) & (bytes - 1)) == 0 && stride % v == 0;
+    };
+    return per_group % v == 0 && a.N % v == 0 && fits(a.x, a.x_stride) &&
+           fits(a.dt, a.dt_stride) && fits(a.z, a.z_stride) && fits(a.y, a.y_stride) &&
+           fits(a.Bm, a.b_stride) && fits(a.Cm, a.c_stride);
+  };
+  if (rows_fit(16)) return launch_kernel<T, P, S, NC, ALIGN16>(p, a.stream);
+  if (rows_fit(4)) return launch_kernel<T, P, S, NC, ALIGN4>(p, a.stream);
+  return launch_kernel<T, P, S, NC, ALIGN_ELT>(p, a.stream);
 }
 
 template <typename T>
 cudaError_t launch_t(const ScanArgs &a) {
-  if (a.N <= 4) return launch_ps<T, 4, 1>(a);
-  if (a.N <= 8) return launch_ps<T, 4, 2>(a);
-  if (a.N <= 16) return launch_ps<T, 4, 4>(a);
-  if (a.N <= 32) return launch_ps<T, 8, 4>(a);
-  if (a.N <= 64) return launch_ps<T, 8, 8>(a);
-  if (a.N <= 128) return launch_ps<T, 8, 16>(a);
-  return launch_ps<T, 8, 32>(a);
+  if (a.N <= 4) return launch_ps<T, 4, 1, 1>(a);
+  if (a.N <= 8) return launch_ps<T, 4, 2, 1>(a);
+  if (a.N <= 16) return launch_ps<T, 8, 2, 1>(a);
+  if (a.N <= 32) return launch_ps<T, 8, 4, 1>(a);
+  if (a.N <= 64) return launch_ps<T, 8, 8, 1>(a);
+  if (a.N <= 128) return launch_ps<T, 8, 16, 2>(a);
+  return launch_ps<T, 8, 32, 4>(a);
 }
 
 }  // namespace
 
-size_t selective_scan_workspace_bytes(int, int, int, int, int) { return 0; }
+size_t selective_scan_workspace_bytes(int B, int L, int D, int N, int groups) {
+  const ScanPlan plan = make_plan(B, L, D, N, groups);
+  return (size_t)(plan.nseg - 1) * B * D * (N + 1) * sizeof(float);
+}
 
 cudaError_t launch_selective_scan(const ScanArgs &a) {
   return a.dtype == LA_F32 ? launch_t<float>(a) : launch_t<__nv_bfloat16>(a);
