@@ -60,6 +60,8 @@ class LibraryNotBuilt(RuntimeError):
 def load():
     """Load the library once; raise LibraryNotBuilt if it is missing."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):

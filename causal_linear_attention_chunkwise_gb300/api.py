@@ -8,8 +8,6 @@ end-to-end path the benchmark times with host buffers).
 """
 from __future__ import annotations
 
-import math
-
 import torch
 
 from . import _native
@@ -311,23 +309,34 @@ def la_delta_fwd(q, k, v, beta, log_alpha=None, S0=None, O=None, S_final=None,
 
 
 # ---------------------------------------------------------------- state space block
-def _on_device(*ts):
-    """Every tensor given lies on the current device (the one the library launches on)."""
-    dev = None
+# These calls also serve single tokens, where the time of the checks counts:
+# each tensor is asked for no more than it has to be.
+def _device_of(x, *ts):
+    """The current device (the one the library launches on), where every tensor
+    given has to lie."""
+    dev = x.get_device()
+    if dev < 0:
+        raise ValueError("expected CUDA tensors")
     for t in ts:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("expected CUDA tensors")
-        if dev is None:
-            dev = torch.cuda.current_device()
-        if t.get_device() != dev:
-            raise ValueError("expected tensors on the current device")
+        if t is not None and t.get_device() != dev:
+            raise ValueError("expected CUDA tensors on one device")
+    if dev != torch.cuda.current_device():
+        raise ValueError("expected tensors on the current device")
+    return dev
+
+
+def _raw_stream(dev, stream):
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _param(t, shape, what):
-    if t is not None and (t.dtype != torch.float32 or t.shape != shape or not t.is_contiguous()):
+    if t.dtype != torch.float32 or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous fp32 {list(shape)}")
+    return t.data_ptr()
+
+
+def _opt_param(t, shape, what):
+    return None if t is None else _param(t, shape, what)
 
 
 def _row_stride(t, shape, dtype, what):
@@ -336,23 +345,25 @@ def _row_stride(t, shape, dtype, what):
     if t.shape != shape or t.dtype != dtype:
         raise ValueError(f"{what} must be {dtype} {list(shape)}")
     if t.is_contiguous():
-        return math.prod(shape[2:])
+        return shape[2] if len(shape) == 3 else shape[2] * shape[3]
+    st = t.stride()
     inner = 1
-    for n, st in zip(reversed(shape[2:]), reversed(t.stride()[2:])):
-        if n > 1 and st != inner:
+    for n, s in zip(reversed(shape[2:]), reversed(st[2:])):
+        if n != 1 and s != inner:
             raise ValueError(f"the values of one token of {what} must be contiguous")
         inner *= n
-    st = t.stride()
     row = st[1] if shape[1] > 1 else st[0] if shape[0] > 1 else inner
     if row < inner or (shape[0] > 1 and st[0] != shape[1] * row):
         raise ValueError(f"the tokens of {what} must lie evenly apart")
     return row
 
 
-def _lengths_arg(lengths, B):
-    if lengths is not None and (lengths.dtype != torch.int32 or lengths.shape != (B,)
-                                or not lengths.is_contiguous()):
+def _lengths_ptr(lengths, B):
+    if lengths is None:
+        return None
+    if lengths.dtype != torch.int32 or lengths.shape != (B,) or not lengths.is_contiguous():
         raise ValueError("lengths must be contiguous int32 [B]")
+    return lengths.data_ptr()
 
 
 def _new(shape, dtype, device, stream, zero=False):
@@ -368,8 +379,6 @@ def _scratch(nbytes, device, stream):
     """Workspace of one call: the cached buffer of its stream, but a buffer of
     the graph's own while a graph is captured (graphs may be replayed side by
     side, and a cached buffer may be replaced by a larger one)."""
-    if nbytes == 0:
-        return None
     s = torch.cuda.current_stream() if stream is None else stream
     with torch.cuda.stream(s):
         if torch.cuda.is_current_stream_capturing():
@@ -393,25 +402,26 @@ def la_causal_conv_fwd(x, weight, bias=None, activation="silu", state0=None, len
     tensor (with L = 1 that is one decode step in place).  ``lengths`` int32 [B]
     are the real tokens of a padded batch: the rows of ``y`` behind them are
     left as they are (zero when ``y`` is made here)."""
-    B, L, D = x.shape
+    shape, dtype = x.shape, x.dtype
+    B, L, D = shape
     W = weight.shape[-1]
-    xs = _row_stride(x, x.shape, x.dtype, "x")
-    _param(weight, (D, W), "weight")
-    _param(bias, (D,), "bias")
-    _lengths_arg(lengths, B)
+    xs = _row_stride(x, shape, dtype, "x")
+    w = _param(weight, (D, W), "weight")
+    bi = _opt_param(bias, (D,), "bias")
+    n = _lengths_ptr(lengths, B)
     for t in (state0, state_final):
-        if t is not None and (t.dtype != x.dtype or t.shape != (B, W - 1, D)
+        if t is not None and (t.dtype != dtype or t.shape != (B, W - 1, D)
                               or not t.is_contiguous()):
             raise ValueError("the states must be contiguous [B,W-1,D] in x's dtype")
-    _on_device(x, weight, bias, state0, lengths, y, state_final)
+    dev = _device_of(x, weight, bias, state0, lengths, y, state_final)
     if y is None:
-        y = _new((B, L, D), x.dtype, x.device, stream, lengths is not None)
+        y = _new(shape, dtype, x.device, stream, lengths is not None)
     if state_final is None and want_final_state:
-        state_final = _new((B, W - 1, D), x.dtype, x.device, stream)
+        state_final = _new((B, W - 1, D), dtype, x.device, stream)
     _check(_native.load().la_causal_conv_fwd(
-        x.data_ptr(), xs, DTYPE[x.dtype], B, L, D, W, weight.data_ptr(), _ptr(bias),
-        ACT[activation], _ptr(lengths), _ptr(state0), y.data_ptr(),
-        _row_stride(y, x.shape, x.dtype, "y"), _ptr(state_final), _stream(stream)))
+        x.data_ptr(), xs, DTYPE[dtype], B, L, D, W, w, bi, ACT[activation], n, _ptr(state0),
+        y.data_ptr(), _row_stride(y, shape, dtype, "y"), _ptr(state_final),
+        _raw_stream(dev, stream)))
     return y, state_final
 
 
@@ -434,36 +444,43 @@ def la_selective_scan_fwd(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, dt_sof
     as they are (zero when ``y`` is made here).  With ``segments`` (the
     default) a cached workspace lets a long sequence run as several segments
     side by side."""
-    B, L, ch = x.shape
+    shape, dtype = x.shape, x.dtype
+    B, L, ch = shape
     N = A.shape[-1]
-    G = Bm.shape[2] if Bm.dim() == 4 else 1
-    bc = (B, L, G, N) if Bm.dim() == 4 else (B, L, N)
-    xs = _row_stride(x, x.shape, x.dtype, "x")
-    ds = _row_stride(dt, x.shape, x.dtype, "dt")
-    zs = 0 if z is None else _row_stride(z, x.shape, x.dtype, "z")
-    bs = _row_stride(Bm, bc, x.dtype, "Bm")
-    cs = _row_stride(Cm, bc, x.dtype, "Cm")
-    _param(A, (ch, N), "A")
-    _param(D, (ch,), "D")
-    _param(dt_bias, (ch,), "dt_bias")
-    _param(h0, (B, ch, N), "h0")
-    _param(h_final, (B, ch, N), "h_final")
-    _lengths_arg(lengths, B)
-    _on_device(x, dt, z, Bm, Cm, A, D, dt_bias, h0, lengths, y, h_final, workspace)
+    bc = Bm.shape
+    G = bc[2] if len(bc) == 4 else 1
+    if bc != ((B, L, G, N) if len(bc) == 4 else (B, L, N)):
+        raise ValueError("Bm must be [B,L,N] or [B,L,groups,N]")
+    xs = _row_stride(x, shape, dtype, "x")
+    ds = _row_stride(dt, shape, dtype, "dt")
+    zs = 0 if z is None else _row_stride(z, shape, dtype, "z")
+    bs = _row_stride(Bm, bc, dtype, "Bm")
+    cs = _row_stride(Cm, bc, dtype, "Cm")
+    Ap = _param(A, (ch, N), "A")
+    Dp = _opt_param(D, (ch,), "D")
+    bias = _opt_param(dt_bias, (ch,), "dt_bias")
+    state = (B, ch, N)
+    h0p = _opt_param(h0, state, "h0")
+    hfp = _opt_param(h_final, state, "h_final")
+    n = _lengths_ptr(lengths, B)
+    dev = _device_of(x, dt, z, Bm, Cm, A, D, dt_bias, h0, lengths, y, h_final, workspace)
     if y is None:
-        y = _new((B, L, ch), x.dtype, x.device, stream, lengths is not None)
+        y = _new(shape, dtype, x.device, stream, lengths is not None)
     if h_final is None and want_final_state:
-        h_final = _new((B, ch, N), torch.float32, x.device, stream)
+        h_final = _new(state, torch.float32, x.device, stream)
+        hfp = h_final.data_ptr()
+    lib = _native.load()
+    ws = ws_bytes = 0
     if workspace is None and segments and L > 1:
-        workspace = _scratch(la_selective_scan_fwd_workspace_bytes(B, L, ch, N, G), x.device,
-                             stream)
-    _check(_native.load().la_selective_scan_fwd(
+        need = lib.la_selective_scan_fwd_workspace_bytes(B, L, ch, N, G)
+        if need:
+            workspace = _scratch(need, x.device, stream)
+    if workspace is not None:
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _check(lib.la_selective_scan_fwd(
         x.data_ptr(), xs, dt.data_ptr(), ds, _ptr(z), zs, Bm.data_ptr(), bs, Cm.data_ptr(), cs,
-        DTYPE[x.dtype], B, L, ch, N, G, A.data_ptr(), _ptr(dt_bias), int(dt_softplus), _ptr(D),
-        _ptr(h0), _ptr(lengths), y.data_ptr(), _row_stride(y, x.shape, x.dtype, "y"),
-        _ptr(h_final), _ptr(workspace),
-        0 if workspace is None else workspace.numel() * workspace.element_size(),
-        _stream(stream)))
+        DTYPE[dtype], B, L, ch, N, G, Ap, bias, dt_softplus, Dp, h0p, n, y.data_ptr(),
+        _row_stride(y, shape, dtype, "y"), hfp, ws, ws_bytes, _raw_stream(dev, stream)))
     return y, h_final
 
 
@@ -479,27 +496,30 @@ def la_gated_norm_fwd(x, gate=None, weight=None, bias=None, norm="rms", activati
     ``gate_first`` gates x before its norm instead of after it.  ``y`` may be
     ``gate``."""
     B, H, L, d = x.shape
+    dtype = x.dtype
     xb, xh, xt, x1 = x.stride()
     if x1 != 1 and d > 1 and x.numel() > 0:
         raise ValueError("the last axis of x must be contiguous")
-    shape = (B, L, H * d)
+    width = H * d
+    shape = (B, L, width)
     heads = 1
     for t in (weight, bias):
         if t is not None:
-            if t.dtype != torch.float32 or not t.is_contiguous() or t.numel() not in (d, H * d):
+            n = t.numel()
+            if t.dtype != torch.float32 or not t.is_contiguous() or n not in (d, width):
                 raise ValueError("weight and bias must be contiguous fp32 [d] or [H*d]")
-            if t.numel() != d:
+            if n != d:
                 heads = H
     if weight is not None and bias is not None and weight.numel() != bias.numel():
         raise ValueError("weight and bias must have one shape")
-    gs = 0 if gate is None else _row_stride(gate, shape, x.dtype, "gate")
-    _on_device(x, gate, weight, bias, y)
+    gs = 0 if gate is None else _row_stride(gate, shape, dtype, "gate")
+    dev = _device_of(x, gate, weight, bias, y)
     if y is None:
-        y = _new(shape, x.dtype, x.device, stream)
+        y = _new(shape, dtype, x.device, stream)
     _check(_native.load().la_gated_norm_fwd(
-        x.data_ptr(), xb, xh, xt, _ptr(gate), gs, DTYPE[x.dtype], B, H, L, d, NORM[norm],
-        ACT[activation], int(gate_first), _ptr(weight), _ptr(bias), heads, eps, y.data_ptr(),
-        _row_stride(y, shape, x.dtype, "y"), _stream(stream)))
+        x.data_ptr(), xb, xh, xt, _ptr(gate), gs, DTYPE[dtype], B, H, L, d, NORM[norm],
+        ACT[activation], gate_first, _ptr(weight), _ptr(bias), heads, eps, y.data_ptr(),
+        _row_stride(y, shape, dtype, "y"), _raw_stream(dev, stream)))
     return y
 
 
@@ -515,24 +535,28 @@ def la_residual_norm_fwd(x, residual=None, weight=None, bias=None, post_weight=N
     dtype or fp32 (None: zero; ``residual_dtype`` then chooses residual_out's,
     x's by default).  The parameters are fp32 [D].  ``y`` may be ``x`` and
     ``residual_out`` may be ``residual``."""
-    D = x.shape[-1]
+    shape, dtype = x.shape, x.dtype
+    D = shape[-1]
     rd = residual.dtype if residual is not None else \
-        residual_out.dtype if residual_out is not None else residual_dtype or x.dtype
-    for t in (post_weight, scale, weight, bias):
-        _param(t, (D,), "weights and scale")
-    for t, dt in ((x, x.dtype), (residual, rd), (y, x.dtype), (residual_out, rd)):
-        if t is not None and (t.shape != x.shape or t.dtype != dt or not t.is_contiguous()):
+        residual_out.dtype if residual_out is not None else residual_dtype or dtype
+    per = (D,)
+    pw = _opt_param(post_weight, per, "post_weight (one of the weights)")
+    sc = _opt_param(scale, per, "scale (one of the weights)")
+    w = _opt_param(weight, per, "weight (one of the weights)")
+    bi = _opt_param(bias, per, "bias (one of the weights)")
+    for t, want in ((x, dtype), (residual, rd), (y, dtype), (residual_out, rd)):
+        if t is not None and (t.shape != shape or t.dtype != want or not t.is_contiguous()):
             raise ValueError("x, residual and the outputs must be contiguous and of one shape, "
                              "y in x's dtype and residual_out in residual's")
-    _on_device(x, residual, weight, bias, post_weight, scale, y, residual_out)
+    dev = _device_of(x, residual, weight, bias, post_weight, scale, y, residual_out)
     if y is None:
-        y = _new(x.shape, x.dtype, x.device, stream)
+        y = _new(shape, dtype, x.device, stream)
     if residual_out is None:
-        residual_out = _new(x.shape, rd, x.device, stream)
+        residual_out = _new(shape, rd, x.device, stream)
     _check(_native.load().la_residual_norm_fwd(
-        x.data_ptr(), DTYPE[x.dtype], _ptr(residual), DTYPE[rd],
-        x.numel() // D if D else 0, D, _ptr(post_weight), _ptr(scale), alpha, _ptr(weight),
-        _ptr(bias), NORM[norm], eps, y.data_ptr(), residual_out.data_ptr(), _stream(stream)))
+        x.data_ptr(), DTYPE[dtype], _ptr(residual), DTYPE[rd], x.numel() // D if D else 0, D,
+        pw, sc, alpha, w, bi, NORM[norm], eps, y.data_ptr(), residual_out.data_ptr(),
+        _raw_stream(dev, stream)))
     return y, residual_out
 
 

@@ -31,45 +31,134 @@ __device__ __forceinline__ float activate(int act, float x) {
   return act == 2 ? sigmoid(x) : x;
 }
 
-// log(1 + e^v) = max(v, 0) + log1p(e), e = e^-|v| in (0, 1].  log1p(e) is
-// taken as 2 atanh(s) with s = e / (2 + e) <= 1/3, whose odd series to s^13
-// leaves a relative remainder below (1/9)^7 / 15 = 1.4e-8: step sizes near
-// e^-7 keep their relative precision, which log(1 + e) would lose.
-__device__ __forceinline__ float softplus(float v) {
-  const float e = expf(-fabsf(v));
-  const float s = e * rcp_approx(2.f + e);
-  const float q = s * s;
-  float p = fmaf(q, 1.f / 13.f, 1.f / 11.f);
-  p = fmaf(q, p, 1.f / 9.f);
-  p = fmaf(q, p, 1.f / 7.f);
-  p = fmaf(q, p, 1.f / 5.f);
-  p = fmaf(q, p, 1.f / 3.f);
-  p = fmaf(q, p, 1.f);
-  return fmaxf(v, 0.f) + 2.f * s * p;
+// Two fp32 values in one 64-bit register pair: one instruction for both.
+__device__ __forceinline__ unsigned long long pack2(float lo, float hi) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(unsigned long long v, float &lo, float &hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b,
+                                                   unsigned long long c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ unsigned long long dup2(float v) { return pack2(v, v); }
+
+// act of two values.
+__device__ __forceinline__ unsigned long long activate2(int act, unsigned long long v) {
+  if (act == 0) return v;
+  float a, b;
+  unpack2(mul2(v, dup2(-kLog2e)), a, b);
+  unpack2(add2(pack2(ex2_approx(a), ex2_approx(b)), dup2(1.f)), a, b);
+  const unsigned long long s = pack2(rcp_approx(a), rcp_approx(b));
+  return act == 1 ? mul2(v, s) : s;
 }
 
-// VEC consecutive elements of T (16 bytes, or one element) to and from fp32.
+// The same operations where the vectors are single elements.
+__device__ __forceinline__ float mul2(float a, float b) { return a * b; }
+__device__ __forceinline__ float add2(float a, float b) { return a + b; }
+__device__ __forceinline__ float fma2(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ float activate2(int act, float v) { return activate(act, v); }
+template <int VEC> struct CellOf {  // what VEC > 1 holds two values in
+  using type = unsigned long long;
+  __device__ static __forceinline__ type both(float v) { return dup2(v); }
+  __device__ static __forceinline__ float sum(type c) {
+    float lo, hi;
+    unpack2(c, lo, hi);
+    return lo + hi;
+  }
+};
+template <> struct CellOf<1> {
+  using type = float;
+  __device__ static __forceinline__ type both(float v) { return v; }
+  __device__ static __forceinline__ float sum(type c) { return c; }
+};
+
+// a / b for a >= 0: in 32 bits where a allows it (a 64-bit division is some
+// hundred instructions).
+__device__ __forceinline__ long long div_index(long long a, int b) {
+  return a >> 32 == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+// VEC elements of T as they lie in memory: 16, 8 or 4 bytes, or one element.
+template <typename T, int VEC> struct Raw {
+  static constexpr int WORDS = VEC * sizeof(T) / 4;
+  static_assert(WORDS == 4 || WORDS == 2 || WORDS == 1, "16-, 8- or 4-byte vectors");
+  alignas(VEC * sizeof(T)) uint32_t w[WORDS];
+  __device__ __forceinline__ void unpack(float *f) const {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      if constexpr (sizeof(T) == 4) f[i] = __uint_as_float(w[i]);
+      else f[i] = __uint_as_float(i % 2 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+    }
+  }
+};
+template <typename T> struct Raw<T, 1> {
+  T u;
+  __device__ __forceinline__ void unpack(float *f) const { f[0] = to_f32(u); }
+};
+
+// VEC elements to and from fp32.
+template <typename T, int VEC>
+__device__ __forceinline__ Raw<T, VEC> load_raw(const T *p) {
+  Raw<T, VEC> r;
+  if constexpr (VEC == 1) {
+    r.u = *p;
+  } else if constexpr (VEC * sizeof(T) == 16) {
+    const uint4 u = *reinterpret_cast<const uint4 *>(p);
+    r.w[0] = u.x, r.w[1] = u.y, r.w[2] = u.z, r.w[3] = u.w;
+  } else if constexpr (VEC * sizeof(T) == 8) {
+    const uint2 u = *reinterpret_cast<const uint2 *>(p);
+    r.w[0] = u.x, r.w[1] = u.y;
+  } else {
+    r.w[0] = *reinterpret_cast<const uint32_t *>(p);
+  }
+  return r;
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void store_raw(T *p, const Raw<T, VEC> &r) {
+  if constexpr (VEC == 1) *p = r.u;
+  else if constexpr (VEC * sizeof(T) == 16)
+    *reinterpret_cast<uint4 *>(p) = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+  else if constexpr (VEC * sizeof(T) == 8)
+    *reinterpret_cast<uint2 *>(p) = make_uint2(r.w[0], r.w[1]);
+  else *reinterpret_cast<uint32_t *>(p) = r.w[0];
+}
 template <typename T, int VEC>
 __device__ __forceinline__ void load_vec(const T *p, float *f) {
-  if constexpr (VEC == 1) {
-    f[0] = to_f32(*p);
-  } else {
-    static_assert(VEC == Pack16<T>::N, "16-byte vectors");
-    Pack16<T>::unpack(*reinterpret_cast<const uint4 *>(p), f);
-  }
+  load_raw<T, VEC>(p).unpack(f);
 }
 
 template <typename T, int VEC>
 __device__ __forceinline__ void store_vec(T *p, const float *f) {
+  Raw<T, VEC> r;
   if constexpr (VEC == 1) {
-    *p = from_f32<T>(f[0]);
-  } else {
-    static_assert(VEC == Pack16<T>::N, "16-byte vectors");
-    alignas(16) T u[VEC];
+    r.u = from_f32<T>(f[0]);
+  } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) u[i] = from_f32<T>(f[i]);
-    *reinterpret_cast<uint4 *>(p) = *reinterpret_cast<const uint4 *>(u);
+    for (int i = 0; i < VEC; ++i) r.w[i] = __float_as_uint(f[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; i += 2) {
+      const __nv_bfloat162 v = __floats2bfloat162_rn(f[i], f[i + 1]);
+      r.w[i / 2] = *reinterpret_cast<const uint32_t *>(&v);
+    }
   }
+  store_raw<T, VEC>(p, r);
 }
 
 }  // namespace la

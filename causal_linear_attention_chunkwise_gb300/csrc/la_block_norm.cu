@@ -3,7 +3,11 @@
 // two blocks (post norm, residual scale, addition, next block's norm).
 //
 // Both are streams over their inputs and outputs with one or two reductions
-// per row, held in fp32: a row's mean first, then the mean square about it.
+// per row, held in fp32: a row's mean first, then the mean square about it.  A
+// team of threads takes a row and keeps it in registers, so every input is read
+// once: 4 to 32 lanes of a warp (rows up to 1024 wide, several to a warp) or
+// a whole block.  Every thread issues all its loads, the weights' too, before
+// the first sum.
 #include <cstdint>
 
 #include "../../include/la_gb300.h"
@@ -13,120 +17,372 @@
 namespace la {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kTeamThreads = 256;  // threads per block of teams inside a warp
 
-__device__ float block_sum(float v, float *red) {
+// The sum of v over the team: LANES neighbouring lanes, or the block (LANES = 0).
+template <int LANES>
+__device__ __forceinline__ float team_sum(float v) {
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-  __syncthreads();  // red may still be read from the sum before
-  if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = v;
-  __syncthreads();
-  return red[0] + red[1] + red[2] + red[3];
+  for (int off = (LANES ? LANES : 32) / 2; off > 0; off >>= 1)
+    v += __shfl_xor_sync(0xffffffffu, v, off);
+  if constexpr (LANES == 0) {
+    __shared__ float red[32];
+    const int warp = threadIdx.x / 32, warps = blockDim.x / 32;
+    __syncthreads();  // red may still be read from the sum before
+    if (threadIdx.x % 32 == 0) red[warp] = v;
+    __syncthreads();
+    v = threadIdx.x % 32 < warps ? red[threadIdx.x % 32] : 0.f;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  }
+  return v;
 }
 
-// mean (0 for RMS) and 1 / sqrt(mean square about it + eps) of row[0..d).
-__device__ void moments(const float *row, int d, int norm, float eps, float *red, float *mean,
-                        float *rstd) {
-  float m = 0.f;
-  if (norm == LA_NORM_LAYER) {
-    for (int i = threadIdx.x; i < d; i += kThreads) m += row[i];
-    m = block_sum(m, red) / d;
+// One row of width d in the team's registers, two values to a register pair:
+// thread `lane` of `size` holds the vectors lane, lane + size, ... of V
+// elements; places past the row hold 0.
+template <int V, int LANES, int I>
+struct Row {
+  using Cell = CellOf<V>;
+  using C = typename Cell::type;
+  static constexpr int H = V > 1 ? V / 2 : 1;
+  C v[I][H];
+
+  __device__ __forceinline__ void set(int i, const float *f) {
+#pragma unroll
+    for (int e = 0; e < H; ++e) {
+      if constexpr (V == 1) v[i][e] = f[e];
+      else v[i][e] = pack2(f[2 * e], f[2 * e + 1]);
+    }
   }
-  float q = 0.f;
-  for (int i = threadIdx.x; i < d; i += kThreads) q = fmaf(row[i] - m, row[i] - m, q);
-  *mean = m;
-  *rstd = rsqrtf(block_sum(q, red) / d + eps);
+  __device__ __forceinline__ void get(int i, float *f) const {
+#pragma unroll
+    for (int e = 0; e < H; ++e) {
+      if constexpr (V == 1) f[e] = v[i][e];
+      else unpack2(v[i][e], f[2 * e], f[2 * e + 1]);
+    }
+  }
+  // v <- (v - mean) / sqrt(mean square about it + eps), mean = 0 for RMS.
+  __device__ __forceinline__ void normalise(int d, int norm, float eps, int lane, int size) {
+    const float inv = 1.f / d;
+    if (norm == LA_NORM_LAYER) {
+      C s = 0;
+#pragma unroll
+      for (int i = 0; i < I; ++i)
+#pragma unroll
+        for (int e = 0; e < H; ++e) s = add2(s, v[i][e]);
+      const C m = Cell::both(-team_sum<LANES>(Cell::sum(s)) * inv);
+#pragma unroll
+      for (int i = 0; i < I; ++i) {
+        const bool in = (lane + i * size) * V < d;
+#pragma unroll
+        for (int e = 0; e < H; ++e) v[i][e] = in ? add2(v[i][e], m) : C(0);
+      }
+    }
+    C q = 0;
+#pragma unroll
+    for (int i = 0; i < I; ++i)
+#pragma unroll
+      for (int e = 0; e < H; ++e) q = fma2(v[i][e], v[i][e], q);
+    const C r = Cell::both(rsqrtf(fmaf(team_sum<LANES>(Cell::sum(q)), inv, eps)));
+#pragma unroll
+    for (int i = 0; i < I; ++i)
+#pragma unroll
+      for (int e = 0; e < H; ++e) v[i][e] = mul2(v[i][e], r);
+  }
+};
+
+// V fp32 parameters, 16-byte vectors where V allows them (V = 1, 2, 4 or 8).
+template <int V>
+__device__ __forceinline__ void load_params(const float *p, float *f) {
+  if constexpr (V % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+      const float4 u = __ldg(reinterpret_cast<const float4 *>(p + i));
+      f[i] = u.x, f[i + 1] = u.y, f[i + 2] = u.z, f[i + 3] = u.w;
+    }
+  } else if constexpr (V == 2) {
+    const float2 u = __ldg(reinterpret_cast<const float2 *>(p));
+    f[0] = u.x, f[1] = u.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] = __ldg(p + i);
+  }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads)
-gated_norm_kernel(const T *x, long long x_bs, long long x_hs, long long x_ts, const T *gate,
-                  long long gate_stride, int H, int L, int d, int norm, int act, int gate_first,
-                  const float *weight, const float *bias, int weight_heads, float eps, T *y,
-                  long long y_stride) {
-  extern __shared__ float row[];
-  __shared__ float red[4];
-  const int h = blockIdx.x % H;
-  const long long bt = blockIdx.x / H;
-  const T *xr = x + bt / L * x_bs + h * x_hs + bt % L * x_ts;
-  const T *gr = gate ? gate + bt * gate_stride + (long long)h * d : nullptr;
-  T *yr = y + bt * y_stride + (long long)h * d;
-  for (int i = threadIdx.x; i < d; i += kThreads) {
-    float v = to_f32(xr[i]);
-    if (gr && gate_first) v *= activate(act, to_f32(gr[i]));
-    row[i] = v;
+template <typename T, int V, int LANES, int I, int ACT>
+__global__ void __launch_bounds__(LANES ? kTeamThreads : 1024, LANES && V > 2 && I <= 2 ? 5 : 1)
+gated_norm_kernel(const GatedNormArgs a, long long rows) {
+  constexpr int H = Row<V, LANES, I>::H;
+  const int size = LANES ? LANES : blockDim.x;
+  const int lane = LANES ? threadIdx.x % size : threadIdx.x;
+  long long r = LANES ? (long long)blockIdx.x * (kTeamThreads / size) + threadIdx.x / size
+                      : (long long)blockIdx.x;
+  const bool live = r < rows;
+  if (!live) r = rows - 1;  // its lanes take part in the sums
+  const long long bt = div_index(r, a.H), b = div_index(bt, a.L);
+  const int h = (int)(r - bt * a.H), d = a.d;
+  const T *xr = static_cast<const T *>(a.x) + b * a.x_bs + h * a.x_hs + (bt - b * a.L) * a.x_ts;
+  const T *gr = static_cast<const T *>(a.gate) + (a.gate ? bt * a.gate_stride : 0) +
+                (long long)h * d;
+  T *y = static_cast<T *>(a.y) + bt * a.y_stride + (long long)h * d;
+  const long long w0 = a.weight_heads > 1 ? (long long)h * d : 0;
+  Raw<T, V> x[I], gate[I];
+#pragma unroll
+  for (int i = 0; i < I; ++i) {
+    const int c = (lane + i * size) * V;
+    x[i] = gate[i] = Raw<T, V>{};
+    if (c < d) {
+      x[i] = load_raw<T, V>(xr + c);
+      if (a.gate) gate[i] = load_raw<T, V>(gr + c);
+    }
   }
-  float mean, rstd;
-  moments(row, d, norm, eps, red, &mean, &rstd);
-  const long long w0 = weight_heads > 1 ? (long long)h * d : 0;
-  for (int i = threadIdx.x; i < d; i += kThreads) {
-    float v = (row[i] - mean) * rstd;
-    if (weight) v *= weight[w0 + i];
-    if (bias) v += bias[w0 + i];
-    if (gr && !gate_first) v *= activate(act, to_f32(gr[i]));
-    yr[i] = from_f32<T>(v);
+  Row<V, LANES, I> row, g;
+#pragma unroll
+  for (int i = 0; i < I; ++i) {
+    float f[V];
+    x[i].unpack(f);
+    row.set(i, f);
+    gate[i].unpack(f);
+    g.set(i, f);
+  }
+  if (a.gate) {
+#pragma unroll
+    for (int i = 0; i < I; ++i)
+#pragma unroll
+      for (int e = 0; e < H; ++e) g.v[i][e] = activate2(ACT, g.v[i][e]);
+    if (a.gate_first) {
+#pragma unroll
+      for (int i = 0; i < I; ++i)
+#pragma unroll
+        for (int e = 0; e < H; ++e) row.v[i][e] = mul2(row.v[i][e], g.v[i][e]);
+    }
+  }
+  row.normalise(d, a.norm, a.eps, lane, size);
+  if (!live) return;
+  const bool gate_last = a.gate && !a.gate_first;
+#pragma unroll
+  for (int i = 0; i < I; ++i) {
+    const int c = (lane + i * size) * V;
+    if (c >= d) continue;
+    Row<V, 1, 1> o, f;
+    float p[V];
+#pragma unroll
+    for (int e = 0; e < H; ++e) o.v[0][e] = row.v[i][e];
+    if (a.weight) {
+      load_params<V>(a.weight + w0 + c, p);
+      f.set(0, p);
+#pragma unroll
+      for (int e = 0; e < H; ++e) o.v[0][e] = mul2(o.v[0][e], f.v[0][e]);
+    }
+    if (a.bias) {
+      load_params<V>(a.bias + w0 + c, p);
+      f.set(0, p);
+#pragma unroll
+      for (int e = 0; e < H; ++e) o.v[0][e] = add2(o.v[0][e], f.v[0][e]);
+    }
+    if (gate_last) {
+#pragma unroll
+      for (int e = 0; e < H; ++e) o.v[0][e] = mul2(o.v[0][e], g.v[i][e]);
+    }
+    float out[V];
+    o.get(0, out);
+    store_vec<T, V>(y + c, out);
   }
 }
 
-template <typename T, typename R>
-__global__ void __launch_bounds__(kThreads)
-residual_norm_kernel(const T *x, const R *residual, int D, const float *post_weight,
-                     const float *scale, float alpha, const float *weight, const float *bias,
-                     int norm, float eps, T *y, R *residual_out) {
-  extern __shared__ float row[];
-  __shared__ float red[4];
-  const long long at = (long long)blockIdx.x * D;
-  float mean = 0.f, rstd = 1.f;
-  for (int i = threadIdx.x; i < D; i += kThreads) row[i] = to_f32(x[at + i]);
-  if (post_weight) moments(row, D, norm, eps, red, &mean, &rstd);
-  for (int i = threadIdx.x; i < D; i += kThreads) {
-    float u = row[i];
-    if (post_weight) u = (u - mean) * rstd * post_weight[i];
-    if (scale) u *= scale[i];
-    const float r = fmaf(alpha, u, residual ? to_f32(residual[at + i]) : 0.f);
-    if (residual_out) residual_out[at + i] = from_f32<R>(r);
-    row[i] = r;
+// A team takes the rows r, r + step, ...: the loads of its next row are in
+// flight while it works on the present one.
+template <typename T, typename R, int V, int LANES, int I>
+__global__ void __launch_bounds__(LANES ? kTeamThreads : 1024)
+residual_norm_kernel(const ResidualNormArgs a) {
+  using ThisRow = Row<V, LANES, I>;
+  constexpr int H = ThisRow::H, RV = V < Pack16<R>::N ? V : Pack16<R>::N, RN = V / RV;
+  const int size = LANES ? LANES : blockDim.x;
+  const int lane = LANES ? threadIdx.x % size : threadIdx.x;
+  const int teams = LANES ? kTeamThreads / size : 1;
+  const long long step = (long long)gridDim.x * teams;
+  long long r = (long long)blockIdx.x * teams + (LANES ? threadIdx.x / size : 0);
+  const int D = a.D;
+  Raw<T, V> x[I];
+  Raw<R, RV> res[I][RN];
+  auto fetch = [&](long long at) {
+    const T *xr = static_cast<const T *>(a.x) + at * D;
+    const R *rr = static_cast<const R *>(a.residual) + at * D;
+#pragma unroll
+    for (int i = 0; i < I; ++i) {
+      const int c = (lane + i * size) * V;
+      if (c < D) {
+        x[i] = load_raw<T, V>(xr + c);
+        if (a.residual) {
+#pragma unroll
+          for (int k = 0; k < RN; ++k) res[i][k] = load_raw<R, RV>(rr + c + k * RV);
+        }
+      }
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < I; ++i) {
+    x[i] = Raw<T, V>{};
+#pragma unroll
+    for (int k = 0; k < RN; ++k) res[i][k] = Raw<R, RV>{};
   }
-  moments(row, D, norm, eps, red, &mean, &rstd);
-  for (int i = threadIdx.x; i < D; i += kThreads) {
-    float v = (row[i] - mean) * rstd;
-    if (weight) v *= weight[i];
-    if (bias) v += bias[i];
-    y[at + i] = from_f32<T>(v);
+  if (r < a.rows) fetch(r);
+  // A team out of rows stays while another of its warp has one: the sums need
+  // the whole warp.
+  for (long long first = r - (LANES ? threadIdx.x % 32 / size : 0); first < a.rows;
+       first += step, r += step) {
+    const bool live = r < a.rows;
+    ThisRow row, rs;
+#pragma unroll
+    for (int i = 0; i < I; ++i) {
+      float f[V];
+      x[i].unpack(f);
+      row.set(i, f);
+#pragma unroll
+      for (int k = 0; k < RN; ++k) res[i][k].unpack(f + k * RV);
+      rs.set(i, f);
+    }
+    if (r + step < a.rows) fetch(r + step);
+    if (a.post_weight) row.normalise(D, a.norm, a.eps, lane, size);
+    R *out = static_cast<R *>(a.residual_out) + r * D;
+#pragma unroll
+    for (int i = 0; i < I; ++i) {
+      const int c = (lane + i * size) * V;
+      if (c >= D) continue;
+      Row<V, 1, 1> p;
+      float f[V];
+      if (a.post_weight) {
+        load_params<V>(a.post_weight + c, f);
+        p.set(0, f);
+#pragma unroll
+        for (int e = 0; e < H; ++e) row.v[i][e] = mul2(row.v[i][e], p.v[0][e]);
+      }
+      if (a.scale) {
+        load_params<V>(a.scale + c, f);
+        p.set(0, f);
+#pragma unroll
+        for (int e = 0; e < H; ++e) row.v[i][e] = mul2(row.v[i][e], p.v[0][e]);
+      }
+#pragma unroll
+      for (int e = 0; e < H; ++e) row.v[i][e] = fma2(ThisRow::Cell::both(a.alpha), row.v[i][e], rs.v[i][e]);
+      if (live && a.residual_out) {
+        row.get(i, f);
+#pragma unroll
+        for (int k = 0; k < RN; ++k) store_vec<R, RV>(out + c + k * RV, f + k * RV);
+      }
+    }
+    row.normalise(D, a.norm, a.eps, lane, size);
+    T *y = static_cast<T *>(a.y) + r * D;
+#pragma unroll
+    for (int i = 0; i < I; ++i) {
+      const int c = (lane + i * size) * V;
+      if (c >= D || !live) continue;
+      Row<V, 1, 1> p;
+      float f[V];
+      if (a.weight) {
+        load_params<V>(a.weight + c, f);
+        p.set(0, f);
+#pragma unroll
+        for (int e = 0; e < H; ++e) row.v[i][e] = mul2(row.v[i][e], p.v[0][e]);
+      }
+      if (a.bias) {
+        load_params<V>(a.bias + c, f);
+        p.set(0, f);
+#pragma unroll
+        for (int e = 0; e < H; ++e) row.v[i][e] = add2(row.v[i][e], p.v[0][e]);
+      }
+      row.get(i, f);
+      store_vec<T, V>(y + c, f);
+    }
   }
 }
 
-template <typename K>
-cudaError_t allow_smem(K kernel, size_t bytes) {
-  if (bytes <= 48 * 1024) return cudaSuccess;
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+// Calls f(Int<LANES>, Int<I>, threads per row) with the team for rows of
+// width d in vectors of V elements: as few lanes as hold the row in two vectors
+// each, up to a warp; then a warp with more, up to a width of 1024; then a
+// block whose threads hold kBlockVecs<V> vectors.
+template <int V> constexpr int kBlockVecs = V == 8 ? 2 : V == 4 ? 4 : V == 2 ? 8 : 16;
+template <int N> struct Int { static constexpr int value = N; };
+
+template <int V, typename F>
+cudaError_t with_team(int d, F f) {
+  const int vecs = (d + V - 1) / V;
+  if constexpr (V > 2) {
+    if (vecs <= 4) return f(Int<2>{}, Int<2>{}, 2);
+    if (vecs <= 8) return f(Int<4>{}, Int<2>{}, 4);
+    if (vecs <= 16) return f(Int<8>{}, Int<2>{}, 8);
+    if (vecs <= 32) return f(Int<16>{}, Int<2>{}, 16);
+    if (vecs <= 64) return f(Int<32>{}, Int<2>{}, 32);
+    if (vecs <= 128) return f(Int<32>{}, Int<4>{}, 32);
+  } else {
+    if (vecs <= 128) return f(Int<32>{}, Int<4>{}, 32);
+    if (vecs <= 1024 / V) return f(Int<32>{}, Int<32 / V>{}, 32);
+  }
+  const int per = kBlockVecs<V>;
+  const int threads = ((vecs + per - 1) / per + 31) / 32 * 32;
+  return f(Int<0>{}, Int<kBlockVecs<V>>{}, threads);
 }
 
+template <typename T, int V, int ACT>
+cudaError_t launch_gated_v(const GatedNormArgs &a) {
+  const long long rows = (long long)a.B * a.L * a.H;
+  return with_team<V>(a.d, [&](auto lanes, auto items, int threads) {
+    constexpr int LANES = decltype(lanes)::value, I = decltype(items)::value;
+    const long long per = LANES ? kTeamThreads / LANES : 1, blocks = (rows + per - 1) / per;
+    if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+    gated_norm_kernel<T, V, LANES, I, ACT>
+        <<<(unsigned)blocks, LANES ? kTeamThreads : threads, 0, a.stream>>>(a, rows);
+    return cudaGetLastError();
+  });
+}
+
+template <typename T, typename R, int V>
+cudaError_t launch_residual_v(const ResidualNormArgs &a) {
+  return with_team<V>(a.D, [&](auto lanes, auto items, int threads) {
+    constexpr int LANES = decltype(lanes)::value, I = decltype(items)::value;
+    const long long per = LANES ? kTeamThreads / LANES : 1, blocks = (a.rows + per - 1) / per;
+    const int block = LANES ? kTeamThreads : threads;
+    const long long fill = 152 * (1024 / block);  // the blocks the SMs hold at 64 registers
+    residual_norm_kernel<T, R, V, LANES, I>
+        <<<(unsigned)(blocks < fill ? blocks : fill), block, 0, a.stream>>>(a);
+    return cudaGetLastError();
+  });
+}
+
+bool fits(const void *p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+
+// The rows are read in the widest vectors that their alignment allows: 16
+// bytes, two elements, or one.
 template <typename T>
 cudaError_t launch_gated_t(const GatedNormArgs &a) {
-  const long long rows = (long long)a.B * a.L * a.H;
-  if (rows > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-  const size_t smem = (size_t)a.d * sizeof(float);
-  cudaError_t e = allow_smem(gated_norm_kernel<T>, smem);
-  if (e != cudaSuccess) return e;
-  gated_norm_kernel<T><<<(unsigned)rows, kThreads, smem, a.stream>>>(
-      static_cast<const T *>(a.x), a.x_bs, a.x_hs, a.x_ts, static_cast<const T *>(a.gate),
-      a.gate_stride, a.H, a.L, a.d, a.norm, a.act, a.gate_first, a.weight, a.bias,
-      a.weight_heads, a.eps, static_cast<T *>(a.y), a.y_stride);
-  return cudaGetLastError();
+  auto rows_fit = [&](int v) {  // the strides of axes of one element are never used
+    const int bytes = v * sizeof(T);
+    return a.d % v == 0 && (a.B == 1 || a.x_bs % v == 0) && (a.H == 1 || a.x_hs % v == 0) &&
+           (a.L == 1 || a.x_ts % v == 0) && a.gate_stride % v == 0 && a.y_stride % v == 0 &&
+           fits(a.x, bytes) && fits(a.gate, bytes) && fits(a.y, bytes);
+  };
+  auto act = [&](auto v) {
+    constexpr int VEC = decltype(v)::value;
+    if (a.act == LA_ACT_SILU) return launch_gated_v<T, VEC, LA_ACT_SILU>(a);
+    if (a.act == LA_ACT_SIGMOID) return launch_gated_v<T, VEC, LA_ACT_SIGMOID>(a);
+    return launch_gated_v<T, VEC, LA_ACT_NONE>(a);
+  };
+  constexpr int V = Pack16<T>::N;
+  return rows_fit(V) ? act(Int<V>{}) : rows_fit(2) ? act(Int<2>{}) : act(Int<1>{});
 }
 
 template <typename T, typename R>
 cudaError_t launch_residual_t(const ResidualNormArgs &a) {
-  if (a.rows > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-  const size_t smem = (size_t)a.D * sizeof(float);
-  cudaError_t e = allow_smem(residual_norm_kernel<T, R>, smem);
-  if (e != cudaSuccess) return e;
-  residual_norm_kernel<T, R><<<(unsigned)a.rows, kThreads, smem, a.stream>>>(
-      static_cast<const T *>(a.x), static_cast<const R *>(a.residual), a.D, a.post_weight,
-      a.scale, a.alpha, a.weight, a.bias, a.norm, a.eps, static_cast<T *>(a.y),
-      static_cast<R *>(a.residual_out));
-  return cudaGetLastError();
+  auto rows_fit = [&](int v) {
+    const int rb = v * sizeof(R) > 16 ? 16 : v * sizeof(R);
+    return a.D % v == 0 && fits(a.x, v * sizeof(T)) && fits(a.y, v * sizeof(T)) &&
+           fits(a.residual, rb) && fits(a.residual_out, rb);
+  };
+  constexpr int V = Pack16<T>::N;
+  return rows_fit(V)   ? launch_residual_v<T, R, V>(a)
+         : rows_fit(2) ? launch_residual_v<T, R, 2>(a)
+                       : launch_residual_v<T, R, 1>(a);
 }
 
 }  // namespace

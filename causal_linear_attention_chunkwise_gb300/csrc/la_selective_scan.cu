@@ -46,27 +46,6 @@ __device__ __forceinline__ void bar_wait(int id) {
   asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "n"(kThreads) : "memory");
 }
 
-// Two fp32 values in one 64-bit register pair: one instruction for both.
-__device__ __forceinline__ unsigned long long pack2(float lo, float hi) {
-  unsigned long long r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ void unpack2(unsigned long long v, float &lo, float &hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b) {
-  unsigned long long r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b,
-                                                   unsigned long long c) {
-  unsigned long long r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-
 template <typename T>
 struct ScanParams {
   const T *x, *dt, *z, *Bm, *Cm;
@@ -92,7 +71,6 @@ struct ScanParams {
 // e) <= 1/3, whose odd series to s^13 leaves a relative remainder below
 // (1/9)^7 / 15 = 1.4e-8: steps near e^-7 keep the relative precision that
 // log(1 + e) would lose.
-__device__ __forceinline__ unsigned long long dup2(float v) { return pack2(v, v); }
 __device__ __forceinline__ void softplus2(float &v0, float &v1) {
   const unsigned long long v = pack2(-fabsf(v0), -fabsf(v1));
   const unsigned long long hi = mul2(v, dup2(kLog2e));
@@ -568,9 +546,153 @@ selective_scan_kernel(const ScanParams<T> p, int pass) {
     scan_segment<T, P, S, NC, ALIGN, false>(p, b, g, cg0, seg, s0, s1, len, smem);
 }
 
+// A few tokens (a decode step): the states are read and written once, and that
+// is the cost.  S neighbouring lanes share a channel, four or eight states each
+// in one or two 16-byte vectors, so a warp reads 512 consecutive bytes of state;
+// a thread takes R sequences, whose loads are all in flight at once and which
+// share its A.
+template <typename T, int P, int S, int R, bool VEC>
+__global__ void __launch_bounds__(256)
+selective_step_kernel(const ScanParams<T> p, unsigned blocks) {  // blocks: per row of sequences
+  const long long slot = (long long)(blockIdx.x % blocks) * 256 + threadIdx.x;
+  const int per_group = p.D / p.groups;
+  const int q = (int)(slot % S);
+  const long long c_all = slot / S;
+  const bool live = c_all < p.D;
+  const int c = live ? (int)c_all : 0;
+  const int g = c / per_group;
+  const int b0 = blockIdx.x / blocks * R;
+  auto state = [&](int k) { return 4 * (q + S * (k / 4)) + k % 4; };
+
+  float a[P], h[R][P];
+  auto load_states = [&](float *f, const float *src) {  // N values from src on, those of this lane
+#pragma unroll
+    for (int k = 0; k < P; k += 4) {
+      if constexpr (VEC) {
+        float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (state(k) < p.N) u = *reinterpret_cast<const float4 *>(src + state(k));
+        f[k] = u.x, f[k + 1] = u.y, f[k + 2] = u.z, f[k + 3] = u.w;
+      } else {
+#pragma unroll
+        for (int e = k; e < k + 4; ++e) f[e] = state(e) < p.N ? src[state(e)] : 0.f;
+      }
+    }
+  };
+  auto load_row = [&](float *f, const T *src) {  // the same of T
+#pragma unroll
+    for (int k = 0; k < P; k += 4) {
+      if constexpr (VEC) {
+        f[k] = f[k + 1] = f[k + 2] = f[k + 3] = 0.f;
+        if (state(k) < p.N) load_raw<T, 4>(src + state(k)).unpack(f + k);
+      } else {
+#pragma unroll
+        for (int e = k; e < k + 4; ++e) f[e] = state(e) < p.N ? to_f32(src[state(e)]) : 0.f;
+      }
+    }
+  };
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+#pragma unroll
+    for (int k = 0; k < P; ++k) h[r][k] = 0.f;
+    if (p.h0 && b0 + r < p.B) load_states(h[r], p.h0 + ((long long)(b0 + r) * p.D + c) * p.N);
+  }
+  load_states(a, p.A + (long long)c * p.N);
+  const float bias = p.dt_bias ? p.dt_bias[c] : 0.f;
+  const float skip = p.skip ? p.skip[c] : 0.f;
+  for (int t = 0; t < p.L; ++t) {
+    float x[R], d[R], z[R], bn[R][P], cn[R][P];
+    bool on[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int b = b0 + r;
+      on[r] = b < p.B && t < (p.lengths ? p.lengths[b] : p.L);
+      if (!on[r]) continue;
+      const long long row = (long long)b * p.L + t;
+      x[r] = to_f32(p.x[row * p.x_stride + c]);
+      d[r] = to_f32(p.dt[row * p.dt_stride + c]);
+      z[r] = p.z ? to_f32(p.z[row * p.z_stride + c]) : 0.f;
+      load_row(bn[r], p.Bm + row * p.b_stride + (long long)g * p.N);
+      load_row(cn[r], p.Cm + row * p.c_stride + (long long)g * p.N);
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float y = 0.f, unused = 0.f;
+      if (on[r]) {
+        d[r] += bias;
+        if (p.softplus) softplus2(d[r], unused);
+        const float u = d[r] * x[r], dl = d[r] * kLog2e;
+#pragma unroll
+        for (int k = 0; k < P; ++k) {
+          h[r][k] = fmaf(ex2_approx(dl * a[k]), h[r][k], u * bn[r][k]);
+          y = fmaf(cn[r][k], h[r][k], y);
+        }
+      }
+#pragma unroll
+      for (int off = S / 2; off > 0; off >>= 1) y += __shfl_xor_sync(0xffffffffu, y, off);
+      if (on[r] && live && q == 0) {
+        y = fmaf(skip, x[r], y);
+        if (p.z) y *= activate(1, z[r]);
+        p.y[((long long)(b0 + r) * p.L + t) * p.y_stride + c] = from_f32<T>(y);
+      }
+    }
+  }
+  if (!p.h_final || !live) return;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    if (b0 + r >= p.B) break;
+    float *dst = p.h_final + ((long long)(b0 + r) * p.D + c) * p.N;
+#pragma unroll
+    for (int k = 0; k < P; k += 4) {
+      if constexpr (VEC) {
+        if (state(k) < p.N)
+          *reinterpret_cast<float4 *>(dst + state(k)) =
+              make_float4(h[r][k], h[r][k + 1], h[r][k + 2], h[r][k + 3]);
+      } else {
+#pragma unroll
+        for (int e = k; e < k + 4; ++e)
+          if (state(e) < p.N) dst[state(e)] = h[r][e];
+      }
+    }
+  }
+}
+
+template <typename T, int P, int S>
+cudaError_t launch_step(const ScanParams<T> &p, cudaStream_t stream) {
+  auto fits = [](const void *q) {
+    return (reinterpret_cast<uintptr_t>(q) & (4 * sizeof(T) - 1)) == 0;
+  };
+  const bool vec = p.N % 4 == 0 && p.b_stride % 4 == 0 && p.c_stride % 4 == 0 && fits(p.Bm) &&
+                   fits(p.Cm);
+  const long long blocks = ((long long)p.D * S + 255) / 256;
+  // Four sequences a thread once there are enough threads without them.
+  const bool many = (double)p.B / 4 * p.D * S >= 152 * 1024;
+  const long long rows = many ? (p.B + 3ll) / 4 : p.B;
+  if (blocks * rows > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+  auto *kernel = many ? (vec ? selective_step_kernel<T, P, S, 4, true>
+                             : selective_step_kernel<T, P, S, 4, false>)
+                      : (vec ? selective_step_kernel<T, P, S, 1, true>
+                             : selective_step_kernel<T, P, S, 1, false>);
+  kernel<<<(unsigned)(blocks * rows), 256, 0, stream>>>(p, (unsigned)blocks);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_steps(const ScanParams<T> &p, cudaStream_t stream) {
+  if (p.N <= 4) return launch_step<T, 4, 1>(p, stream);
+  if (p.N <= 8) return launch_step<T, 4, 2>(p, stream);
+  if (p.N <= 16) return launch_step<T, 4, 4>(p, stream);
+  if (p.N <= 32) return launch_step<T, 4, 8>(p, stream);
+  if (p.N <= 64) return launch_step<T, 4, 16>(p, stream);
+  if (p.N <= 128) return launch_step<T, 4, 32>(p, stream);
+  return launch_step<T, 8, 32>(p, stream);
+}
+
 // Channels per block, by the number of states.
 constexpr int block_channels(int N) { return N <= 4 ? 128 : N <= 16 ? 64 : N <= 32 ? 32 : 16; }
 
+#ifndef STEP_MAX
+#define STEP_MAX 4
+#endif
 struct ScanPlan {
   int nseg, seg_len;
 };
@@ -620,18 +742,8 @@ cudaError_t launch_kernel(const ScanParams<T> &p, cudaStream_t stream) {
 }
 
 template <typename T, int P, int S, int NC>
-cudaError_t launch_ps(const ScanArgs &a) {
+cudaError_t launch_ps(const ScanArgs &a, const ScanParams<T> &p) {
   static_assert(ScanShape<P, S, NC, sizeof(T)>::CH == block_channels(P * S), "the plan's blocks");
-  ScanPlan plan{1, a.L};
-  if (a.workspace) plan = make_plan(a.B, a.L, a.D, a.N, a.groups);
-  float *ws = static_cast<float *>(a.workspace);
-  const size_t states = (size_t)(plan.nseg - 1) * a.B * a.D * a.N;
-  const ScanParams<T> p{static_cast<const T *>(a.x), static_cast<const T *>(a.dt),
-                        static_cast<const T *>(a.z), static_cast<const T *>(a.Bm),
-                        static_cast<const T *>(a.Cm), a.x_stride, a.dt_stride, a.z_stride,
-                        a.b_stride, a.c_stride, a.L, a.D, a.N, a.groups, a.A, a.dt_bias,
-                        a.softplus, a.skip, a.h0, a.lengths, static_cast<T *>(a.y), a.y_stride,
-                        a.h_final, a.B, plan.nseg, plan.seg_len, ws, ws ? ws + states : nullptr};
   // The widest loads that every row's alignment allows (a block's first channel
   // is a multiple of 16 bytes into its group, a chunk 16 bytes or N * 4).
   const int per_group = a.D / a.groups;
@@ -651,13 +763,24 @@ cudaError_t launch_ps(const ScanArgs &a) {
 
 template <typename T>
 cudaError_t launch_t(const ScanArgs &a) {
-  if (a.N <= 4) return launch_ps<T, 4, 1, 1>(a);
-  if (a.N <= 8) return launch_ps<T, 4, 2, 1>(a);
-  if (a.N <= 16) return launch_ps<T, 8, 2, 1>(a);
-  if (a.N <= 32) return launch_ps<T, 8, 4, 1>(a);
-  if (a.N <= 64) return launch_ps<T, 8, 8, 1>(a);
-  if (a.N <= 128) return launch_ps<T, 8, 16, 2>(a);
-  return launch_ps<T, 8, 32, 4>(a);
+  ScanPlan plan{1, a.L};
+  if (a.workspace) plan = make_plan(a.B, a.L, a.D, a.N, a.groups);
+  float *ws = static_cast<float *>(a.workspace);
+  const size_t states = (size_t)(plan.nseg - 1) * a.B * a.D * a.N;
+  const ScanParams<T> p{static_cast<const T *>(a.x), static_cast<const T *>(a.dt),
+                        static_cast<const T *>(a.z), static_cast<const T *>(a.Bm),
+                        static_cast<const T *>(a.Cm), a.x_stride, a.dt_stride, a.z_stride,
+                        a.b_stride, a.c_stride, a.L, a.D, a.N, a.groups, a.A, a.dt_bias,
+                        a.softplus, a.skip, a.h0, a.lengths, static_cast<T *>(a.y), a.y_stride,
+                        a.h_final, a.B, plan.nseg, plan.seg_len, ws, ws ? ws + states : nullptr};
+  if (a.L <= STEP_MAX) return launch_steps<T>(p, a.stream);
+  if (a.N <= 4) return launch_ps<T, 4, 1, 1>(a, p);
+  if (a.N <= 8) return launch_ps<T, 4, 2, 1>(a, p);
+  if (a.N <= 16) return launch_ps<T, 8, 2, 1>(a, p);
+  if (a.N <= 32) return launch_ps<T, 8, 4, 1>(a, p);
+  if (a.N <= 64) return launch_ps<T, 8, 8, 1>(a, p);
+  if (a.N <= 128) return launch_ps<T, 8, 16, 2>(a, p);
+  return launch_ps<T, 8, 32, 4>(a, p);
 }
 
 }  // namespace

@@ -277,5 +277,5 @@ def test_binding_refuses_before_the_library():
         api.la_residual_norm_fwd(x)
     with pytest.raises(ValueError, match="one shape"):
         api.la_residual_norm_fwd(x, residual=x[:, :4])
-    with pytest.raises(ValueError, match="weights"):
+    with pytest.raises(ValueError, match="weight"):
         api.la_residual_norm_fwd(x, weight=torch.zeros(5))
