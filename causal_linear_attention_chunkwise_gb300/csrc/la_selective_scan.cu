@@ -65,12 +65,12 @@ struct ScanParams {
   float *seg_state, *seg_sum;
 };
 
-// softplus of two values: log(1 + e^v) = max(v, 0) + log1p(e) with e = e^-|v| in
-// (0, 1].  e's exponent is taken in two parts, -|v| log2 e = hi + lo, so that
-// the rounding of hi does not reach e; log1p(e) is 2 atanh(s) with s = e / (2 +
-// e) <= 1/3, whose odd series to s^13 leaves a relative remainder below
-// (1/9)^7 / 15 = 1.4e-8: steps near e^-7 keep the relative precision that
-// log(1 + e) would lose.
+// softplus of two values: log(1 + e^v) = max(v, 0) + e p(e), e = e^-|v| in (0,
+// 1].  e's exponent is taken in two parts, -|v| log2 e = hi + lo, so that the
+// rounding of hi does not reach e.  p(e) = log1p(e) / e is the polynomial of
+// degree 9 through the ten Chebyshev nodes of [0, 1]: it errs by 5e-9 before
+// rounding, relative, so steps near e^-7 keep the precision that log(1 + e)
+// would lose.  (2 atanh(e / (2 + e)) by its series took a reciprocal more.)
 __device__ __forceinline__ void softplus2(float &v0, float &v1) {
   const unsigned long long v = pack2(-fabsf(v0), -fabsf(v1));
   const unsigned long long hi = mul2(v, dup2(kLog2e));
@@ -80,18 +80,20 @@ __device__ __forceinline__ void softplus2(float &v0, float &v1) {
   unpack2(hi, h0, h1);
   unsigned long long e = pack2(ex2_approx(h0), ex2_approx(h1));
   e = fma2(e, mul2(lo, dup2(0.6931471805599453f)), e);  // 2^lo = 1 + lo ln 2
-  float e0, e1;
-  unpack2(e, e0, e1);
-  const unsigned long long s = mul2(e, pack2(rcp_approx(2.f + e0), rcp_approx(2.f + e1)));
-  const unsigned long long q = mul2(s, s);
-  unsigned long long p = fma2(q, dup2(2.f / 13.f), dup2(2.f / 11.f));
-  p = fma2(q, p, dup2(2.f / 9.f));
-  p = fma2(q, p, dup2(2.f / 7.f));
-  p = fma2(q, p, dup2(2.f / 5.f));
-  p = fma2(q, p, dup2(2.f / 3.f));
-  p = fma2(q, p, dup2(2.f));
-  unpack2(fma2(s, p, pack2(fmaxf(v0, 0.f), fmaxf(v1, 0.f))), v0, v1);
+  unsigned long long p = fma2(e, dup2(-0.0031760570127516985f), dup2(0.019542526453733444f));
+  p = fma2(e, p, dup2(-0.056373611092567444f));
+  p = fma2(e, p, dup2(0.10543623566627502f));
+  p = fma2(e, p, dup2(-0.1526966691017151f));
+  p = fma2(e, p, dup2(0.1966327428817749f));
+  p = fma2(e, p, dup2(-0.24951615929603577f));
+  p = fma2(e, p, dup2(0.33329710364341736f));
+  p = fma2(e, p, dup2(-0.49999892711639404f));
+  p = fma2(e, p, dup2(1.f));
+  unpack2(fma2(e, p, pack2(fmaxf(v0, 0.f), fmaxf(v1, 0.f))), v0, v1);
 }
+
+__device__ __forceinline__ uint32_t bits(float v) { return __float_as_uint(v); }
+__device__ __forceinline__ uint32_t bits(__nv_bfloat16 v) { return __bfloat16_as_ushort(v); }
 
 constexpr int min_c(int a, int b) { return a < b ? a : b; }
 
@@ -274,7 +276,7 @@ __device__ __forceinline__ void scan_segment(const ScanParams<T> &p, long long b
 #pragma unroll
           for (int f = e; f < e + 2; ++f) {
             v[f] = fmaf(skip[f], x.get(f), v[f]);
-            if (zb) v[f] *= activate(1, z.get(f));
+            if (zb) v[f] *= activate(LA_ACT_SILU, z.get(f));
           }
           o.set2(e, v[e], v[e + 1]);
         }
@@ -548,24 +550,25 @@ selective_scan_kernel(const ScanParams<T> p, int pass) {
 
 // A few tokens (a decode step): the states are read and written once, and that
 // is the cost.  S neighbouring lanes share a channel, four or eight states each
-// in one or two 16-byte vectors, so a warp reads 512 consecutive bytes of state;
-// a thread takes R sequences, whose loads are all in flight at once and which
-// share its A.
+// in one or two 16-byte vectors, so a warp reads 512 consecutive bytes of state.
+// A thread takes R <= S sequences, whose loads are all in flight at once and
+// which share its A; the scalars of sequence r (delta, delta x, and the output)
+// are worked out by the channel's lane r and passed on by shuffles.
 template <typename T, int P, int S, int R, bool VEC>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 4)
 selective_step_kernel(const ScanParams<T> p, unsigned blocks) {  // blocks: per row of sequences
+  static_assert(R == 1 || R == 2 || R == 4, "halvings");
   const long long slot = (long long)(blockIdx.x % blocks) * 256 + threadIdx.x;
   const int per_group = p.D / p.groups;
   const int q = (int)(slot % S);
-  const long long c_all = slot / S;
-  const bool live = c_all < p.D;
-  const int c = live ? (int)c_all : 0;
+  const bool live = slot / S < p.D;
+  const int c = live ? (int)(slot / S) : 0;
   const int g = c / per_group;
   const int b0 = blockIdx.x / blocks * R;
+  const int mine = min(b0 + q % R, p.B - 1);  // the sequence whose scalars this lane works out
   auto state = [&](int k) { return 4 * (q + S * (k / 4)) + k % 4; };
 
-  float a[P], h[R][P];
-  auto load_states = [&](float *f, const float *src) {  // N values from src on, those of this lane
+  auto load_states = [&](float *f, const float *src) {  // this lane's of the N values at src
 #pragma unroll
     for (int k = 0; k < P; k += 4) {
       if constexpr (VEC) {
@@ -578,18 +581,21 @@ selective_step_kernel(const ScanParams<T> p, unsigned blocks) {  // blocks: per 
       }
     }
   };
-  auto load_row = [&](float *f, const T *src) {  // the same of T
+  auto load_row = [&](Raw<T, 4> *f, const T *src) {  // the same of T
 #pragma unroll
     for (int k = 0; k < P; k += 4) {
+      f[k / 4] = Raw<T, 4>{};
       if constexpr (VEC) {
-        f[k] = f[k + 1] = f[k + 2] = f[k + 3] = 0.f;
-        if (state(k) < p.N) load_raw<T, 4>(src + state(k)).unpack(f + k);
+        if (state(k) < p.N) f[k / 4] = load_raw<T, 4>(src + state(k));
       } else {
 #pragma unroll
-        for (int e = k; e < k + 4; ++e) f[e] = state(e) < p.N ? to_f32(src[state(e)]) : 0.f;
+        for (int e = 0; e < 4; ++e)
+          if (state(k + e) < p.N)
+            f[k / 4].w[e * sizeof(T) / 4] |= bits(src[state(k + e)]) << (e * sizeof(T) % 4 * 8);
       }
     }
   };
+  float a[P], h[R][P];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
 #pragma unroll
@@ -597,43 +603,71 @@ selective_step_kernel(const ScanParams<T> p, unsigned blocks) {  // blocks: per 
     if (p.h0 && b0 + r < p.B) load_states(h[r], p.h0 + ((long long)(b0 + r) * p.D + c) * p.N);
   }
   load_states(a, p.A + (long long)c * p.N);
+#pragma unroll
+  for (int k = 0; k < P; ++k) a[k] *= kLog2e;
   const float bias = p.dt_bias ? p.dt_bias[c] : 0.f;
   const float skip = p.skip ? p.skip[c] : 0.f;
+  const int len = p.lengths ? min(max(p.lengths[mine], 0), p.L) : p.L;
   for (int t = 0; t < p.L; ++t) {
-    float x[R], d[R], z[R], bn[R][P], cn[R][P];
-    bool on[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int b = b0 + r;
-      on[r] = b < p.B && t < (p.lengths ? p.lengths[b] : p.L);
-      if (!on[r]) continue;
-      const long long row = (long long)b * p.L + t;
-      x[r] = to_f32(p.x[row * p.x_stride + c]);
-      d[r] = to_f32(p.dt[row * p.dt_stride + c]);
-      z[r] = p.z ? to_f32(p.z[row * p.z_stride + c]) : 0.f;
-      load_row(bn[r], p.Bm + row * p.b_stride + (long long)g * p.N);
-      load_row(cn[r], p.Cm + row * p.c_stride + (long long)g * p.N);
+    const long long row = (long long)mine * p.L + t;
+    const bool on = t < len && b0 + q % R < p.B;
+    float x = 0.f, d = 0.f, z = 0.f;
+    if (on) {
+      x = to_f32(p.x[row * p.x_stride + c]);
+      d = to_f32(p.dt[row * p.dt_stride + c]) + bias;
+      if (p.z) z = to_f32(p.z[row * p.z_stride + c]);
     }
+    Raw<T, 4> bn[R][P / 4], cn[R][P / 4];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      float y = 0.f, unused = 0.f;
-      if (on[r]) {
-        d[r] += bias;
-        if (p.softplus) softplus2(d[r], unused);
-        const float u = d[r] * x[r], dl = d[r] * kLog2e;
+      // Rows behind a sequence's end are not read.
+      if (R == 1 ? on : __shfl_sync(0xffffffffu, (int)on, r, S)) {
+        const long long at = (long long)(b0 + r) * p.L + t;
+        load_row(bn[r], p.Bm + at * p.b_stride + (long long)g * p.N);
+        load_row(cn[r], p.Cm + at * p.c_stride + (long long)g * p.N);
+      } else {
 #pragma unroll
-        for (int k = 0; k < P; ++k) {
-          h[r][k] = fmaf(ex2_approx(dl * a[k]), h[r][k], u * bn[r][k]);
-          y = fmaf(cn[r][k], h[r][k], y);
+        for (int k = 0; k < P / 4; ++k) bn[r][k] = cn[r][k] = Raw<T, 4>{};
+      }
+    }
+    float unused = 0.f;
+    if (p.softplus) softplus2(d, unused);
+    if (!on) d = 0.f;  // a step of zero keeps the state
+    const float u = d * x;
+    float y[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const float dr = R == 1 ? d : __shfl_sync(0xffffffffu, d, r, S);
+      const float ur = R == 1 ? u : __shfl_sync(0xffffffffu, u, r, S);
+      y[r] = 0.f;
+#pragma unroll
+      for (int k = 0; k < P; k += 4) {
+        float bf[4], cf[4];
+        bn[r][k / 4].unpack(bf);
+        cn[r][k / 4].unpack(cf);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          h[r][k + e] = fmaf(ex2_approx(dr * a[k + e]), h[r][k + e], ur * bf[e]);
+          y[r] = fmaf(cf[e], h[r][k + e], y[r]);
         }
       }
+    }
+    // Sum over the S lanes; lane r ends with sequence r's.
 #pragma unroll
-      for (int off = S / 2; off > 0; off >>= 1) y += __shfl_xor_sync(0xffffffffu, y, off);
-      if (on[r] && live && q == 0) {
-        y = fmaf(skip, x[r], y);
-        if (p.z) y *= activate(1, z[r]);
-        p.y[((long long)(b0 + r) * p.L + t) * p.y_stride + c] = from_f32<T>(y);
+    for (int off = S / 2; off >= R && off > 0; off >>= 1)
+#pragma unroll
+      for (int r = 0; r < R; ++r) y[r] += __shfl_xor_sync(0xffffffffu, y[r], off);
+#pragma unroll
+    for (int off = R / 2; off > 0; off >>= 1)
+#pragma unroll
+      for (int r = 0; r < off; ++r) {
+        const float keep = q & off ? y[r + off] : y[r], send = q & off ? y[r] : y[r + off];
+        y[r] = keep + __shfl_xor_sync(0xffffffffu, send, off);
       }
+    if (on && live && q < R) {
+      float o = fmaf(skip, x, y[0]);
+      if (p.z) o *= activate(1, z);
+      p.y[row * p.y_stride + c] = from_f32<T>(o);
     }
   }
   if (!p.h_final || !live) return;
@@ -658,18 +692,19 @@ selective_step_kernel(const ScanParams<T> p, unsigned blocks) {  // blocks: per 
 
 template <typename T, int P, int S>
 cudaError_t launch_step(const ScanParams<T> &p, cudaStream_t stream) {
+  constexpr int R = P > 4 ? 1 : min_c(S, 4);  // more states leave no registers for more
   auto fits = [](const void *q) {
     return (reinterpret_cast<uintptr_t>(q) & (4 * sizeof(T) - 1)) == 0;
   };
   const bool vec = p.N % 4 == 0 && p.b_stride % 4 == 0 && p.c_stride % 4 == 0 && fits(p.Bm) &&
                    fits(p.Cm);
   const long long blocks = ((long long)p.D * S + 255) / 256;
-  // Four sequences a thread once there are enough threads without them.
-  const bool many = (double)p.B / 4 * p.D * S >= 152 * 1024;
-  const long long rows = many ? (p.B + 3ll) / 4 : p.B;
+  // R sequences a thread once there are enough threads without them.
+  const bool many = (double)p.B / R * p.D * S >= 152 * 1024;
+  const long long rows = many ? (p.B + R - 1ll) / R : p.B;
   if (blocks * rows > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-  auto *kernel = many ? (vec ? selective_step_kernel<T, P, S, 4, true>
-                             : selective_step_kernel<T, P, S, 4, false>)
+  auto *kernel = many ? (vec ? selective_step_kernel<T, P, S, R, true>
+                             : selective_step_kernel<T, P, S, R, false>)
                       : (vec ? selective_step_kernel<T, P, S, 1, true>
                              : selective_step_kernel<T, P, S, 1, false>);
   kernel<<<(unsigned)(blocks * rows), 256, 0, stream>>>(p, (unsigned)blocks);
@@ -690,9 +725,10 @@ cudaError_t launch_steps(const ScanParams<T> &p, cudaStream_t stream) {
 // Channels per block, by the number of states.
 constexpr int block_channels(int N) { return N <= 4 ? 128 : N <= 16 ? 64 : N <= 32 ? 32 : 16; }
 
-#ifndef STEP_MAX
-#define STEP_MAX 4
-#endif
+// Up to this many tokens the step kernel runs: 64 x L x 4096 (N = 16, bf16) takes
+// 22 us at L = 4, 39 at 8, 72 at 16; the tiled kernel 49 at 8 and 51 at 16.
+constexpr int kStepTokens = 8;
+
 struct ScanPlan {
   int nseg, seg_len;
 };
@@ -773,7 +809,7 @@ cudaError_t launch_t(const ScanArgs &a) {
                         a.b_stride, a.c_stride, a.L, a.D, a.N, a.groups, a.A, a.dt_bias,
                         a.softplus, a.skip, a.h0, a.lengths, static_cast<T *>(a.y), a.y_stride,
                         a.h_final, a.B, plan.nseg, plan.seg_len, ws, ws ? ws + states : nullptr};
-  if (a.L <= STEP_MAX) return launch_steps<T>(p, a.stream);
+  if (a.L <= kStepTokens) return launch_steps<T>(p, a.stream);
   if (a.N <= 4) return launch_ps<T, 4, 1, 1>(a, p);
   if (a.N <= 8) return launch_ps<T, 4, 2, 1>(a, p);
   if (a.N <= 16) return launch_ps<T, 8, 2, 1>(a, p);

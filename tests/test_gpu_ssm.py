@@ -69,6 +69,9 @@ def conv_inputs(B, L, D, Wd, dtype, packed=False, state=True, ragged=False, seed
     (1, 1100, 520, 2, "silu", False, True, False),
     (2, 300, 24, 6, "silu", False, True, False),
     (2, 129, 33, 7, "silu", False, True, False),
+    (3, 50, 30, 4, "silu", False, True, False),      # pairs of channels, not fours
+    (2, 4100, 1024, 4, "silu", True, True, False),   # runs of several batches of tokens
+    (5, 1500, 516, 3, "silu", False, True, True),
 ])
 def test_conv(B, L, D, Wd, act, packed, state, ragged, dtype):
     x, weight, bias, st, n = conv_inputs(B, L, D, Wd, dtype, packed, state, ragged)
@@ -175,6 +178,15 @@ SCANS = [  # B, L, ch, N, G, packed, gate, state, ragged
     (6, 900, 24, 16, 1, True, True, True, True),
     (1, 1111, 40, 24, 2, False, True, True, False),
     (1, 700, 6, 128, 1, False, True, True, False),
+    (2, 65, 34, 6, 1, False, True, True, False),     # bf16 rows aligned to 4 bytes only
+    (1, 300, 70, 10, 1, False, True, True, False),
+    (130, 1, 1300, 16, 1, False, True, True, False),  # several sequences to a thread
+    (131, 3, 650, 16, 2, True, True, True, False),
+    (301, 1, 1030, 7, 1, False, True, True, False),
+    (70, 2, 300, 128, 1, False, True, False, False),
+    (600, 1, 520, 3, 1, False, False, True, False),
+    (6, 8, 7000, 16, 1, False, True, True, True),
+    (9, 9, 24, 16, 1, False, True, True, False),
 ]
 
 
@@ -186,6 +198,22 @@ def test_scan(B, L, ch, N, G, packed, gate, state, ragged, dtype):
     y, h = scan(i, y=y)
     ref, href = scan_reference(i, dtype)
     live = _live(i["lengths"], B, L)
+    R.check(y, ref, "y", live)
+    assert (y.float().cpu().numpy()[~live] == 7.0).all()
+    R.check(h, href, "h_final")
+
+
+def test_scan_many_sequences_with_lengths_and_states_in_place():
+    B, L, ch, N = 140, 4, 1200, 16
+    i = scan_inputs(B, L, ch, N, 1, "bf16")
+    i["lengths"] = (torch.arange(B, dtype=torch.int32) % (L + 1)).cuda()
+    live = _live(i["lengths"], B, L)
+    for k in ("x", "dt", "z", "Bm", "Cm"):
+        i[k] = _poison(i[k], live)
+    ref, href = scan_reference(i, "bf16")
+    h = i["h0"].clone()
+    y = torch.full((B, L, ch), 7.0, dtype=torch.bfloat16, device="cuda")
+    scan(dict(i, h0=h), y=y, h_final=h)
     R.check(y, ref, "y", live)
     assert (y.float().cpu().numpy()[~live] == 7.0).all()
     R.check(h, href, "h_final")
@@ -307,6 +335,11 @@ def test_scan_same_bits_every_run():
     (1, 1, 2, 16384, "layer", "silu", True, False, False, True),
     (2, 16, 130, 16, "rms", "silu", False, False, True, False),
     (64, 8, 1, 128, "rms", "silu", False, False, True, False),
+    (2, 3, 5, 66, "layer", "silu", False, True, True, True),     # pairs of elements
+    (1, 2, 3, 1030, "layer", "silu", True, False, True, False),
+    (1, 2, 3, 515, "rms", "silu", False, True, True, False),     # single elements
+    (1, 1, 2, 16383, "layer", "sigmoid", False, False, True, True),
+    (1, 3, 2, 512, "layer", "silu", False, False, True, False),
 ])
 def test_gated_norm(B, H, L, d, norm, act, first, heads, head_major, bias, dtype):
     g = _gen(3)
@@ -367,6 +400,12 @@ def test_gated_norm_rows_of_zeros_and_non_finite_rows():
     (2, 9001, True, True, "layer", True),
     (700, 520, True, True, "rms", False),
     (3, 8192, False, False, "layer", False),
+    (11, 66, True, True, "layer", True),
+    (5, 3150, True, True, "rms", False),
+    (4, 515, True, False, "layer", True),
+    (2, 16383, True, True, "rms", False),
+    (5000, 24, True, True, "rms", False),      # teams of a warp with several rows each
+    (1500, 2056, True, True, "layer", False),  # blocks with several rows each
 ])
 def test_residual_norm(R_, D, post, scale, norm, bias, dtype, rd):
     g = _gen(6)
