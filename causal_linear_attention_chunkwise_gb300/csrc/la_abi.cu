@@ -93,6 +93,9 @@ la_status run_variant(const char *fn, const VariantArgs &a) {
   return ok();
 }
 
+// Tokens and channels of the calls whose kernels add a tile to them in 32 bits.
+constexpr int kMaxLen = 1 << 30;
+
 // The bytes that `rows` rows of `width` elements, `stride` elements apart, lie in.
 struct Rows {
   const void *p;
@@ -450,6 +453,8 @@ la_status la_causal_conv_fwd(const void *x, long long x_stride, int dtype, int B
     return fail(LA_ERR_INVALID_ARG, "%s: activation %d is not none or silu", fn, activation);
   if (width < 2 || width > 8)
     return fail(LA_ERR_UNSUPPORTED, "%s: width %d outside 2..8", fn, width);
+  if (L > kMaxLen || D > kMaxLen)
+    return fail(LA_ERR_UNSUPPORTED, "%s: L=%d or D=%d above 2^30", fn, L, D);
   if (x_stride < D || y_stride < D)
     return fail(LA_ERR_INVALID_ARG, "%s: row strides %lld, %lld shorter than a row of %d", fn,
                 x_stride, y_stride, D);
@@ -477,7 +482,9 @@ la_status la_causal_conv_fwd(const void *x, long long x_stride, int dtype, int B
 }
 
 size_t la_selective_scan_fwd_workspace_bytes(int B, int L, int D, int N, int groups) {
-  if (B <= 0 || L <= 0 || D <= 0 || N < 1 || N > 256 || groups < 1 || D % groups) return 0;
+  if (B <= 0 || L <= 0 || D <= 0 || N < 1 || N > 256 || groups < 1 || D % groups ||
+      L > kMaxLen || D > kMaxLen)
+    return 0;
   return selective_scan_workspace_bytes(B, L, D, N, groups);
 }
 
@@ -497,6 +504,8 @@ la_status la_selective_scan_fwd(const void *x, long long x_stride, const void *d
     return fail(LA_ERR_INVALID_ARG, "%s: bad sizes B=%d L=%d D=%d N=%d groups=%d", fn, B, L, D,
                 N, groups);
   if (N > 256) return fail(LA_ERR_UNSUPPORTED, "%s: N=%d outside 1..256", fn, N);
+  if (L > kMaxLen || D > kMaxLen)
+    return fail(LA_ERR_UNSUPPORTED, "%s: L=%d or D=%d above 2^30", fn, L, D);
   if (D % groups)
     return fail(LA_ERR_UNSUPPORTED, "%s: D=%d is not a multiple of groups=%d", fn, D, groups);
   const long long gn = (long long)groups * N;

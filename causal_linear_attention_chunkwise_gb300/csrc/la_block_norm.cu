@@ -5,9 +5,17 @@
 // Both are streams over their inputs and outputs with one or two reductions
 // per row, held in fp32: a row's mean first, then the mean square about it.  A
 // team of threads takes a row and keeps it in registers, so every input is read
-// once: 4 to 32 lanes of a warp (rows up to 1024 wide, several to a warp) or
-// a whole block.  Every thread issues all its loads, the weights' too, before
-// the first sum.
+// once: 2 to 32 lanes of a warp (rows up to 1024 wide, several to a warp) or
+// a whole block.
+//
+// The residual step reads as many bytes of parameters as of data where the
+// residual is fp32, so its teams take many rows, keep the factors of x in
+// registers and load the next row meanwhile: 16384 x 4096 at 6.4 TB/s (94% of
+// the measured copy).  The gated norm's teams take one row each: the same loop
+// cost it more registers than it gave (4 x 16 x 4096 x 64 bf16: 23 us, 4.3 TB/s,
+// against 25 to 29; 2 x 2047 x 4096 fp32: 35.5, 5.7 TB/s, against 37).  Its short
+// rows are bound by instructions and latency: index arithmetic and two sums of
+// shuffles for 64 values.
 #include <cstdint>
 
 #include "../../include/la_gb300.h"
@@ -110,8 +118,8 @@ __device__ __forceinline__ void load_params(const float *p, float *f) {
   }
 }
 
-template <typename T, int V, int LANES, int I, int ACT>
-__global__ void __launch_bounds__(LANES ? kTeamThreads : 1024, LANES && V > 2 && I <= 2 ? 5 : 1)
+template <typename T, int V, int LANES, int I, int ACT, int MAXT>
+__global__ void __launch_bounds__(MAXT, LANES && V > 2 && I <= 2 ? 5 : 1)
 gated_norm_kernel(const GatedNormArgs a, long long rows) {
   constexpr int H = Row<V, LANES, I>::H;
   const int size = LANES ? LANES : blockDim.x;
@@ -192,9 +200,10 @@ gated_norm_kernel(const GatedNormArgs a, long long rows) {
 }
 
 // A team takes the rows r, r + step, ...: the loads of its next row are in
-// flight while it works on the present one.
-template <typename T, typename R, int V, int LANES, int I>
-__global__ void __launch_bounds__(LANES ? kTeamThreads : 1024)
+// flight while it works on the present one.  The factors of x stay in registers for all of a team's rows: read anew for each, the
+// three parameters of an fp32 residual step are as many bytes as its data.
+template <typename T, typename R, int V, int LANES, int I, int MAXT>
+__global__ void __launch_bounds__(MAXT)
 residual_norm_kernel(const ResidualNormArgs a) {
   using ThisRow = Row<V, LANES, I>;
   constexpr int H = ThisRow::H, RV = V < Pack16<R>::N ? V : Pack16<R>::N, RN = V / RV;
@@ -204,6 +213,8 @@ residual_norm_kernel(const ResidualNormArgs a) {
   const long long step = (long long)gridDim.x * teams;
   long long r = (long long)blockIdx.x * teams + (LANES ? threadIdx.x / size : 0);
   const int D = a.D;
+  // alpha scale post_weight, the factor of x in every row this team takes
+  Row<V, LANES, I> s;
   Raw<T, V> x[I];
   Raw<R, RV> res[I][RN];
   auto fetch = [&](long long at) {
@@ -228,6 +239,24 @@ residual_norm_kernel(const ResidualNormArgs a) {
     for (int k = 0; k < RN; ++k) res[i][k] = Raw<R, RV>{};
   }
   if (r < a.rows) fetch(r);
+#pragma unroll
+  for (int i = 0; i < I; ++i) {
+    const int c = (lane + i * size) * V;
+    float f[V], g[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) f[e] = c < D ? a.alpha : 0.f;
+    if (a.scale && c < D) {
+      load_params<V>(a.scale + c, g);
+#pragma unroll
+      for (int e = 0; e < V; ++e) f[e] *= g[e];
+    }
+    if (a.post_weight && c < D) {
+      load_params<V>(a.post_weight + c, g);
+#pragma unroll
+      for (int e = 0; e < V; ++e) f[e] *= g[e];
+    }
+    s.set(i, f);
+  }
   // A team out of rows stays while another of its warp has one: the sums need
   // the whole warp.
   for (long long first = r - (LANES ? threadIdx.x % 32 / size : 0); first < a.rows;
@@ -250,22 +279,9 @@ residual_norm_kernel(const ResidualNormArgs a) {
     for (int i = 0; i < I; ++i) {
       const int c = (lane + i * size) * V;
       if (c >= D) continue;
-      Row<V, 1, 1> p;
+#pragma unroll
+      for (int e = 0; e < H; ++e) row.v[i][e] = fma2(s.v[i][e], row.v[i][e], rs.v[i][e]);
       float f[V];
-      if (a.post_weight) {
-        load_params<V>(a.post_weight + c, f);
-        p.set(0, f);
-#pragma unroll
-        for (int e = 0; e < H; ++e) row.v[i][e] = mul2(row.v[i][e], p.v[0][e]);
-      }
-      if (a.scale) {
-        load_params<V>(a.scale + c, f);
-        p.set(0, f);
-#pragma unroll
-        for (int e = 0; e < H; ++e) row.v[i][e] = mul2(row.v[i][e], p.v[0][e]);
-      }
-#pragma unroll
-      for (int e = 0; e < H; ++e) row.v[i][e] = fma2(ThisRow::Cell::both(a.alpha), row.v[i][e], rs.v[i][e]);
       if (live && a.residual_out) {
         row.get(i, f);
 #pragma unroll
@@ -329,10 +345,16 @@ cudaError_t launch_gated_v(const GatedNormArgs &a) {
   const long long rows = (long long)a.B * a.L * a.H;
   return with_team<V>(a.d, [&](auto lanes, auto items, int threads) {
     constexpr int LANES = decltype(lanes)::value, I = decltype(items)::value;
+    const int block = LANES ? kTeamThreads : threads;
     const long long per = LANES ? kTeamThreads / LANES : 1, blocks = (rows + per - 1) / per;
     if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-    gated_norm_kernel<T, V, LANES, I, ACT>
-        <<<(unsigned)blocks, LANES ? kTeamThreads : threads, 0, a.stream>>>(a, rows);
+    const unsigned grid = (unsigned)blocks;
+    if constexpr (LANES != 0)
+      gated_norm_kernel<T, V, LANES, I, ACT, kTeamThreads><<<grid, block, 0, a.stream>>>(a, rows);
+    else if (threads <= 512)
+      gated_norm_kernel<T, V, 0, I, ACT, 512><<<grid, block, 0, a.stream>>>(a, rows);
+    else
+      gated_norm_kernel<T, V, 0, I, ACT, 1024><<<grid, block, 0, a.stream>>>(a, rows);
     return cudaGetLastError();
   });
 }
@@ -341,11 +363,18 @@ template <typename T, typename R, int V>
 cudaError_t launch_residual_v(const ResidualNormArgs &a) {
   return with_team<V>(a.D, [&](auto lanes, auto items, int threads) {
     constexpr int LANES = decltype(lanes)::value, I = decltype(items)::value;
-    const long long per = LANES ? kTeamThreads / LANES : 1, blocks = (a.rows + per - 1) / per;
     const int block = LANES ? kTeamThreads : threads;
-    const long long fill = 152 * (1024 / block);  // the blocks the SMs hold at 64 registers
-    residual_norm_kernel<T, R, V, LANES, I>
-        <<<(unsigned)(blocks < fill ? blocks : fill), block, 0, a.stream>>>(a);
+    // 512 threads an SM: 16384 x 4096 (fp32 residual, post norm, scale) takes 126
+    // us, with 768 or 1024 threads 133 to 154, in blocks that end with their row 144.
+    const long long per = LANES ? kTeamThreads / LANES : 1, blocks = (a.rows + per - 1) / per;
+    const long long fill = 152ll * (block < 512 ? 512 / block : 1);
+    const unsigned grid = (unsigned)(blocks < fill ? blocks : fill);
+    if constexpr (LANES != 0)
+      residual_norm_kernel<T, R, V, LANES, I, kTeamThreads><<<grid, block, 0, a.stream>>>(a);
+    else if (threads <= 512)
+      residual_norm_kernel<T, R, V, 0, I, 512><<<grid, block, 0, a.stream>>>(a);
+    else
+      residual_norm_kernel<T, R, V, 0, I, 1024><<<grid, block, 0, a.stream>>>(a);
     return cudaGetLastError();
   });
 }

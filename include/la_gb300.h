@@ -308,6 +308,8 @@ la_status la_delta_fwd(const void *q, const void *k, const void *v, int dtype,
  *                token, oldest first; NULL = zero
  *   state_final  [B,width-1,D] dtype: the last width-1 inputs (of state0 and
  *                x together), or NULL; may be state0's buffer
+ *
+ * Supported: L and D up to 2^30.
  */
 la_status la_causal_conv_fwd(const void *x, long long x_stride, int dtype, int B, int L, int D,
                              int width, const float *weight, const float *bias, int activation,
@@ -342,7 +344,9 @@ la_status la_causal_conv_fwd(const void *x, long long x_stride, int dtype, int B
  *                LA_ERR_INVALID_ARG.  Its contents need no initialisation and
  *                are not kept.
  *
- * Supported: N in 1..256, D a multiple of groups.
+ * Supported: N in 1..256, D a multiple of groups, L and D up to 2^30.  A NaN or
+ * an infinity in x or dt makes its channel's outputs and states non-finite from
+ * its token on, an infinity possibly as a NaN; other channels are not touched.
  */
 la_status la_selective_scan_fwd(const void *x, long long x_stride, const void *dt,
                                 long long dt_stride, const void *z, long long z_stride,

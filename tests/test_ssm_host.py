@@ -121,6 +121,7 @@ def _conv(lib, **kw):
 
 @pytest.mark.parametrize("kw,status,word", [
     (dict(dtype=7), 1, b"dtype"), (dict(B=-1), 1, b"sizes"), (dict(L=-3), 1, b"sizes"),
+    (dict(L=(1 << 30) + 1), 2, b"2^30"),
     (dict(W=1), 2, b"width"), (dict(W=9), 2, b"width"), (dict(act=2), 1, b"activation"),
     (dict(xs=63), 1, b"stride"), (dict(ys=10), 1, b"stride"), (dict(weight=None), 1, b"non-null"),
     (dict(x=None), 1, b"non-null"), (dict(y=None), 1, b"non-null"), (dict(x=P + 1), 1, b"aligned"),
@@ -153,6 +154,7 @@ def _scan(lib, **kw):
 @pytest.mark.parametrize("kw,status,word", [
     (dict(dtype=2), 1, b"dtype"), (dict(N=0), 1, b"sizes"), (dict(N=257, bs=257, cs=257), 2, b"N="),
     (dict(G=3, bs=48, cs=48), 2, b"groups"), (dict(G=0), 1, b"sizes"), (dict(D=-1), 1, b"sizes"),
+    (dict(L=(1 << 30) + 1), 2, b"2^30"),
     (dict(xs=8), 1, b"stride"), (dict(bs=15), 1, b"stride"), (dict(G=2, bs=16, cs=32), 1, b"stride"),
     (dict(z=P, zs=63), 1, b"stride"), (dict(A=None), 1, b"non-null"), (dict(dt=None), 1, b"non-null"),
     (dict(A=P + 4), 1, b"16-byte"), (dict(h0=P + 8), 1, b"16-byte"), (dict(x=P + 1), 1, b"aligned"),
