@@ -553,45 +553,53 @@ selective_scan_kernel(const ScanParams<T> p, int pass) {
 // in one or two 16-byte vectors, so a warp reads 512 consecutive bytes of state.
 // A thread takes R <= S sequences, whose loads are all in flight at once and
 // which share its A; the scalars of sequence r (delta, delta x, and the output)
-// are worked out by the channel's lane r and passed on by shuffles.
-template <typename T, int P, int S, int R, bool VEC>
-__global__ void __launch_bounds__(256, 4)
+// are worked out by the channel's lane r and passed on by shuffles.  256
+// sequences of 4096 x 16 states, one token, bf16: 33 us, 4.4 TB/s; with four
+// blocks per SM instead of five 38, two sequences a thread 42, one 59, packed
+// fp32 pairs 42.  Latency bounds it: the loads of a thread's sequences leave
+// together, but registers limit the threads.
+template <typename T, int P, int S, int R, bool VEC, bool ONE>
+__global__ void __launch_bounds__(256, ONE && sizeof(T) == 2 && P == 4 ? 5 : 4)
 selective_step_kernel(const ScanParams<T> p, unsigned blocks) {  // blocks: per row of sequences
   static_assert(R == 1 || R == 2 || R == 4, "halvings");
-  const long long slot = (long long)(blockIdx.x % blocks) * 256 + threadIdx.x;
-  const int per_group = p.D / p.groups;
-  const int q = (int)(slot % S);
-  const bool live = slot / S < p.D;
-  const int c = live ? (int)(slot / S) : 0;
-  const int g = c / per_group;
-  const int b0 = blockIdx.x / blocks * R;
+  const unsigned row = blockIdx.x / blocks, slot = (blockIdx.x - row * blocks) * 256 + threadIdx.x;
+  const int q = slot % S;
+  const bool live = slot / S < (unsigned)p.D;
+  const int c = live ? slot / S : 0;
+  const int g = p.groups == 1 ? 0 : c / (p.D / p.groups);
+  const int b0 = row * R;
   const int mine = min(b0 + q % R, p.B - 1);  // the sequence whose scalars this lane works out
-  auto state = [&](int k) { return 4 * (q + S * (k / 4)) + k % 4; };
+  const bool real = b0 + q % R < p.B;
+  // This lane's states are 4 (q + S j) + i: the vector j lies 4 S j values on.
+  auto inside = [&](int j) { return 4 * (q + S * j) < p.N; };
+  const long long per_seq = (long long)p.D * p.N, at0 = b0 * per_seq + (long long)c * p.N + 4 * q;
 
-  auto load_states = [&](float *f, const float *src) {  // this lane's of the N values at src
+  auto load_states = [&](float *f, const float *src) {
 #pragma unroll
-    for (int k = 0; k < P; k += 4) {
+    for (int j = 0; j < P / 4; ++j) {
+      float v[4] = {0.f, 0.f, 0.f, 0.f};
       if constexpr (VEC) {
-        float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (state(k) < p.N) u = *reinterpret_cast<const float4 *>(src + state(k));
-        f[k] = u.x, f[k + 1] = u.y, f[k + 2] = u.z, f[k + 3] = u.w;
+        if (inside(j)) load_raw<float, 4>(src + 4 * S * j).unpack(v);
       } else {
 #pragma unroll
-        for (int e = k; e < k + 4; ++e) f[e] = state(e) < p.N ? src[state(e)] : 0.f;
+        for (int e = 0; e < 4; ++e)
+          if (4 * (q + S * j) + e < p.N) v[e] = src[4 * S * j + e];
       }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f[4 * j + e] = v[e];
     }
   };
   auto load_row = [&](Raw<T, 4> *f, const T *src) {  // the same of T
 #pragma unroll
-    for (int k = 0; k < P; k += 4) {
-      f[k / 4] = Raw<T, 4>{};
+    for (int j = 0; j < P / 4; ++j) {
+      f[j] = Raw<T, 4>{};
       if constexpr (VEC) {
-        if (state(k) < p.N) f[k / 4] = load_raw<T, 4>(src + state(k));
+        if (inside(j)) f[j] = load_raw<T, 4>(src + 4 * S * j);
       } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (state(k + e) < p.N)
-            f[k / 4].w[e * sizeof(T) / 4] |= bits(src[state(k + e)]) << (e * sizeof(T) % 4 * 8);
+          if (4 * (q + S * j) + e < p.N)
+            f[j].w[e * sizeof(T) / 4] |= bits(src[4 * S * j + e]) << (e * sizeof(T) % 4 * 8);
       }
     }
   };
@@ -600,34 +608,39 @@ selective_step_kernel(const ScanParams<T> p, unsigned blocks) {  // blocks: per 
   for (int r = 0; r < R; ++r) {
 #pragma unroll
     for (int k = 0; k < P; ++k) h[r][k] = 0.f;
-    if (p.h0 && b0 + r < p.B) load_states(h[r], p.h0 + ((long long)(b0 + r) * p.D + c) * p.N);
+    if (p.h0 && b0 + r < p.B) load_states(h[r], p.h0 + at0 + r * per_seq);
   }
-  load_states(a, p.A + (long long)c * p.N);
+  load_states(a, p.A + (long long)c * p.N + 4 * q);
 #pragma unroll
   for (int k = 0; k < P; ++k) a[k] *= kLog2e;
   const float bias = p.dt_bias ? p.dt_bias[c] : 0.f;
   const float skip = p.skip ? p.skip[c] : 0.f;
-  const int len = p.lengths ? min(max(p.lengths[mine], 0), p.L) : p.L;
-  for (int t = 0; t < p.L; ++t) {
-    const long long row = (long long)mine * p.L + t;
-    const bool on = t < len && b0 + q % R < p.B;
+  const int len = !real ? 0 : p.lengths ? min(max(p.lengths[mine], 0), p.L) : p.L;
+  const long long tok = (long long)mine * p.L;
+  const T *xp = p.x + tok * p.x_stride + c, *dp = p.dt + tok * p.dt_stride + c;
+  const T *zp = p.z ? p.z + tok * p.z_stride + c : nullptr;
+  T *yp = p.y + tok * p.y_stride + c;
+  const long long tok0 = (long long)b0 * p.L, bstep = p.L * p.b_stride, cstep = p.L * p.c_stride;
+  const T *bp = p.Bm + tok0 * p.b_stride + (long long)g * p.N + 4 * q;
+  const T *cp = p.Cm + tok0 * p.c_stride + (long long)g * p.N + 4 * q;
+  for (int t = 0; t < (ONE ? 1 : p.L); ++t) {
+    const bool on = t < len;
     float x = 0.f, d = 0.f, z = 0.f;
     if (on) {
-      x = to_f32(p.x[row * p.x_stride + c]);
-      d = to_f32(p.dt[row * p.dt_stride + c]) + bias;
-      if (p.z) z = to_f32(p.z[row * p.z_stride + c]);
+      x = to_f32(*xp);
+      d = to_f32(*dp) + bias;
+      if (zp) z = to_f32(*zp);
     }
     Raw<T, 4> bn[R][P / 4], cn[R][P / 4];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       // Rows behind a sequence's end are not read.
       if (R == 1 ? on : __shfl_sync(0xffffffffu, (int)on, r, S)) {
-        const long long at = (long long)(b0 + r) * p.L + t;
-        load_row(bn[r], p.Bm + at * p.b_stride + (long long)g * p.N);
-        load_row(cn[r], p.Cm + at * p.c_stride + (long long)g * p.N);
+        load_row(bn[r], bp + r * bstep);
+        load_row(cn[r], cp + r * cstep);
       } else {
 #pragma unroll
-        for (int k = 0; k < P / 4; ++k) bn[r][k] = cn[r][k] = Raw<T, 4>{};
+        for (int j = 0; j < P / 4; ++j) bn[r][j] = cn[r][j] = Raw<T, 4>{};
       }
     }
     float unused = 0.f;
@@ -641,14 +654,15 @@ selective_step_kernel(const ScanParams<T> p, unsigned blocks) {  // blocks: per 
       const float ur = R == 1 ? u : __shfl_sync(0xffffffffu, u, r, S);
       y[r] = 0.f;
 #pragma unroll
-      for (int k = 0; k < P; k += 4) {
+      for (int j = 0; j < P / 4; ++j) {
         float bf[4], cf[4];
-        bn[r][k / 4].unpack(bf);
-        cn[r][k / 4].unpack(cf);
+        bn[r][j].unpack(bf);
+        cn[r][j].unpack(cf);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          h[r][k + e] = fmaf(ex2_approx(dr * a[k + e]), h[r][k + e], ur * bf[e]);
-          y[r] = fmaf(cf[e], h[r][k + e], y[r]);
+          const int k = 4 * j + e;
+          h[r][k] = fmaf(ex2_approx(dr * a[k]), h[r][k], ur * bf[e]);
+          y[r] = fmaf(cf[e], h[r][k], y[r]);
         }
       }
     }
@@ -666,25 +680,28 @@ selective_step_kernel(const ScanParams<T> p, unsigned blocks) {  // blocks: per 
       }
     if (on && live && q < R) {
       float o = fmaf(skip, x, y[0]);
-      if (p.z) o *= activate(1, z);
-      p.y[row * p.y_stride + c] = from_f32<T>(o);
+      if (zp) o *= activate(LA_ACT_SILU, z);
+      *yp = from_f32<T>(o);
     }
+    if (ONE) break;
+    xp += p.x_stride, dp += p.dt_stride, yp += p.y_stride;
+    if (zp) zp += p.z_stride;
+    bp += p.b_stride, cp += p.c_stride;
   }
   if (!p.h_final || !live) return;
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     if (b0 + r >= p.B) break;
-    float *dst = p.h_final + ((long long)(b0 + r) * p.D + c) * p.N;
+    float *dst = p.h_final + at0 + r * per_seq;
 #pragma unroll
-    for (int k = 0; k < P; k += 4) {
+    for (int j = 0; j < P / 4; ++j) {
+      const float *v = h[r] + 4 * j;
       if constexpr (VEC) {
-        if (state(k) < p.N)
-          *reinterpret_cast<float4 *>(dst + state(k)) =
-              make_float4(h[r][k], h[r][k + 1], h[r][k + 2], h[r][k + 3]);
+        if (inside(j)) store_vec<float, 4>(dst + 4 * S * j, v);
       } else {
 #pragma unroll
-        for (int e = k; e < k + 4; ++e)
-          if (state(e) < p.N) dst[state(e)] = h[r][e];
+        for (int e = 0; e < 4; ++e)
+          if (4 * (q + S * j) + e < p.N) dst[4 * S * j + e] = v[e];
       }
     }
   }
@@ -703,10 +720,14 @@ cudaError_t launch_step(const ScanParams<T> &p, cudaStream_t stream) {
   const bool many = (double)p.B / R * p.D * S >= 152 * 1024;
   const long long rows = many ? (p.B + R - 1ll) / R : p.B;
   if (blocks * rows > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-  auto *kernel = many ? (vec ? selective_step_kernel<T, P, S, R, true>
-                             : selective_step_kernel<T, P, S, R, false>)
-                      : (vec ? selective_step_kernel<T, P, S, 1, true>
-                             : selective_step_kernel<T, P, S, 1, false>);
+  auto pick = [&](auto one) {
+    constexpr bool ONE = decltype(one)::value;
+    return many ? (vec ? selective_step_kernel<T, P, S, R, true, ONE>
+                       : selective_step_kernel<T, P, S, R, false, ONE>)
+                : (vec ? selective_step_kernel<T, P, S, 1, true, ONE>
+                       : selective_step_kernel<T, P, S, 1, false, ONE>);
+  };
+  auto *kernel = p.L == 1 ? pick(Int<1>{}) : pick(Int<0>{});
   kernel<<<(unsigned)(blocks * rows), 256, 0, stream>>>(p, (unsigned)blocks);
   return cudaGetLastError();
 }
