@@ -593,8 +593,10 @@ la_status la_gated_norm_fwd(const void *x, long long x_b_stride, long long x_h_s
   const Rows yr{y, rows, width, y_stride, elt}, gr{gate, rows, width, gate_stride, elt};
   const long long span = (B - 1) * x_b_stride + (H - 1) * x_h_stride + (L - 1) * x_t_stride + d;
   Rows xr{x, 1, span, span, elt};
-  if (x_h_stride == d && x_b_stride == L * x_t_stride && x_t_stride >= width)
-    xr = {x, rows, width, x_t_stride, elt};  // token-major rows, which may be a slice
+  if ((H == 1 || x_h_stride == d) && (B == 1 || x_b_stride == L * x_t_stride) &&
+      (L == 1 || x_t_stride >= width))
+    xr = {x, rows, width, rows == 1 ? width : L == 1 ? x_b_stride : x_t_stride,
+          elt};  // token-major rows, which may be a slice
   if (overlap(yr, xr) || (!(y == gate && y_stride == gate_stride) && overlap(yr, gr)))
     return fail(LA_ERR_INVALID_ARG, "%s: y overlaps an input", fn);
   GatedNormArgs a{x, x_b_stride, x_h_stride, x_t_stride, gate, gate_stride, dtype, B, H, L, d,

@@ -320,6 +320,45 @@ def test_scan_same_bits_every_run():
         assert torch.equal(y, y2) and torch.equal(h, h2)
 
 
+@pytest.mark.parametrize("L", [2, 40, 1000])
+def test_outputs_in_slices_and_no_final_states(L):
+    """The halves of one wider tensor: x and z read from it, y written over what was x's
+    neighbour; no final states asked for."""
+    ch = 48
+    i = scan_inputs(2, L, ch, 16, 1, "bf16")
+    wide = torch.full((2, L, 3 * ch), 5.0, dtype=torch.bfloat16, device="cuda")
+    wide[..., :ch], wide[..., 2 * ch:] = i["x"], i["z"]
+    y, h = scan(dict(i, x=wide[..., :ch], z=wide[..., 2 * ch:]), y=wide[..., ch:2 * ch],
+                want_final_state=False)
+    assert h is None
+    ref, _ = scan_reference(i, "bf16")
+    R.check(wide[..., ch:2 * ch], ref, "y")
+    assert torch.equal(wide[..., :ch], i["x"]) and torch.equal(wide[..., 2 * ch:], i["z"])
+    weight = torch.randn(ch, 4, generator=_gen(30)).cuda()
+    y, sf = api.la_causal_conv_fwd(wide[..., :ch], weight, y=wide[..., ch:2 * ch],
+                                   want_final_state=False)
+    assert sf is None
+    ref, _ = R.causal_conv(i["x"], weight, None, "silu", None, None, "bf16")
+    R.check(wide[..., ch:2 * ch], ref, "conv")
+    assert torch.equal(wide[..., :ch], i["x"]) and torch.equal(wide[..., 2 * ch:], i["z"])
+    api.la_gated_norm_fwd(wide[:, None, :, :ch], wide[..., 2 * ch:], y=wide[..., ch:2 * ch])
+    ref = R.gated_norm(i["x"][:, None], i["z"], None, None, "rms", "silu", False, 1e-5, "bf16")
+    R.check(wide[..., ch:2 * ch], ref, "gated")
+    assert torch.equal(wide[..., :ch], i["x"]) and torch.equal(wide[..., 2 * ch:], i["z"])
+
+
+def test_scan_ragged_segments_in_place():
+    i = scan_inputs(6, 900, 64, 16, 1, "f32", ragged=True)
+    assert api.la_selective_scan_fwd_workspace_bytes(6, 900, 64, 16) > 0
+    ref, href = scan_reference(i, "f32")
+    h = i["h0"].clone()
+    y, _ = scan(dict(i, h0=h), h_final=h)
+    live = _live(i["lengths"], 6, 900)
+    R.check(y, ref, "y", live)
+    assert (y.cpu().numpy()[~live] == 0).all()
+    R.check(h, href, "h_final")
+
+
 # ---------------------------------------------------------------- norms
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("B,H,L,d,norm,act,first,heads,head_major,bias", [

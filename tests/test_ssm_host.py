@@ -198,6 +198,9 @@ def _gated(lib, **kw):
     (dict(y=None), 1, b"non-null"), (dict(gate=P + 0x10001), 1, b"aligned"),
     (dict(weight=P + 4), 1, b"16-byte"), (dict(y=P + 64), 1, b"overlaps"),
     (dict(y=P + 0x10000, ys=520), 1, b"overlaps"), (dict(y=P + 0x10002), 1, b"overlaps"),
+    # one head, token major, rows 1024 apart: the other half of the rows is free, its own is not
+    (dict(H=1, d=512, xh=7, xt=1024, xb=8192, ys=1024, y=P + 1022), 1, b"overlaps"),
+    (dict(H=1, d=512, xh=7, xt=1024, xb=8192, ys=1024, y=P + 1024, eps=-1.0), 1, b"eps"),
 ])
 def test_gated_norm_refusals(lib, kw, status, word):
     assert _gated(lib, **kw) == status
