@@ -320,23 +320,22 @@ def _device_of(x, *ts):
     for t in ts:
         if t is not None and t.get_device() != dev:
             raise ValueError("expected CUDA tensors on one device")
-    if dev != torch.cuda.current_device():
+    if dev != _current_device():
         raise ValueError("expected tensors on the current device")
     return dev
 
 
-def _raw_stream(dev, stream):
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+# What torch.cuda.current_device and current_stream ask, without their objects (a
+# CUDA tensor is at hand, so CUDA is initialised).
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _param(t, shape, what):
     if t.dtype != torch.float32 or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous fp32 {list(shape)}")
     return t.data_ptr()
-
-
-def _opt_param(t, shape, what):
-    return None if t is None else _param(t, shape, what)
 
 
 def _row_stride(t, shape, dtype, what):
@@ -359,8 +358,6 @@ def _row_stride(t, shape, dtype, what):
 
 
 def _lengths_ptr(lengths, B):
-    if lengths is None:
-        return None
     if lengths.dtype != torch.int32 or lengths.shape != (B,) or not lengths.is_contiguous():
         raise ValueError("lengths must be contiguous int32 [B]")
     return lengths.data_ptr()
@@ -390,6 +387,12 @@ def _scratch(nbytes, device, stream):
     return buf
 
 
+def _conv_state(t, shape, dtype):
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError("the states must be contiguous [B,W-1,D] in x's dtype")
+    return t.data_ptr()
+
+
 def la_causal_conv_fwd(x, weight, bias=None, activation="silu", state0=None, lengths=None,
                        y=None, state_final=None, want_final_state=True, stream=None):
     """Causal depthwise convolution over time, y_t = act(bias + sum_w weight[:,w]
@@ -405,23 +408,25 @@ def la_causal_conv_fwd(x, weight, bias=None, activation="silu", state0=None, len
     shape, dtype = x.shape, x.dtype
     B, L, D = shape
     W = weight.shape[-1]
-    xs = _row_stride(x, shape, dtype, "x")
+    xs = D if x.is_contiguous() else _row_stride(x, shape, dtype, "x")
     w = _param(weight, (D, W), "weight")
-    bi = _opt_param(bias, (D,), "bias")
-    n = _lengths_ptr(lengths, B)
-    for t in (state0, state_final):
-        if t is not None and (t.dtype != dtype or t.shape != (B, W - 1, D)
-                              or not t.is_contiguous()):
-            raise ValueError("the states must be contiguous [B,W-1,D] in x's dtype")
+    bi = None if bias is None else _param(bias, (D,), "bias")
+    n = None if lengths is None else _lengths_ptr(lengths, B)
+    state = (B, W - 1, D)
+    s0 = None if state0 is None else _conv_state(state0, state, dtype)
+    s1 = None if state_final is None else _conv_state(state_final, state, dtype)
     dev = _device_of(x, weight, bias, state0, lengths, y, state_final)
     if y is None:
         y = _new(shape, dtype, x.device, stream, lengths is not None)
     if state_final is None and want_final_state:
-        state_final = _new((B, W - 1, D), dtype, x.device, stream)
-    _check(_native.load().la_causal_conv_fwd(
-        x.data_ptr(), xs, DTYPE[dtype], B, L, D, W, w, bi, ACT[activation], n, _ptr(state0),
-        y.data_ptr(), _row_stride(y, shape, dtype, "y"), _ptr(state_final),
-        _raw_stream(dev, stream)))
+        state_final = _new(state, dtype, x.device, stream)
+        s1 = state_final.data_ptr()
+    status = _native.load().la_causal_conv_fwd(
+        x.data_ptr(), xs, DTYPE[dtype], B, L, D, W, w, bi, ACT[activation], n, s0, y.data_ptr(),
+        _row_stride(y, shape, dtype, "y"), s1,
+        _current_stream(dev) if stream is None else stream.cuda_stream)
+    if status:
+        _check(status)
     return y, state_final
 
 
@@ -456,13 +461,13 @@ def la_selective_scan_fwd(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, dt_sof
     zs = 0 if z is None else _row_stride(z, shape, dtype, "z")
     bs = _row_stride(Bm, bc, dtype, "Bm")
     cs = _row_stride(Cm, bc, dtype, "Cm")
+    per, state = (ch,), (B, ch, N)
     Ap = _param(A, (ch, N), "A")
-    Dp = _opt_param(D, (ch,), "D")
-    bias = _opt_param(dt_bias, (ch,), "dt_bias")
-    state = (B, ch, N)
-    h0p = _opt_param(h0, state, "h0")
-    hfp = _opt_param(h_final, state, "h_final")
-    n = _lengths_ptr(lengths, B)
+    Dp = None if D is None else _param(D, per, "D")
+    bias = None if dt_bias is None else _param(dt_bias, per, "dt_bias")
+    h0p = None if h0 is None else _param(h0, state, "h0")
+    hfp = None if h_final is None else _param(h_final, state, "h_final")
+    n = None if lengths is None else _lengths_ptr(lengths, B)
     dev = _device_of(x, dt, z, Bm, Cm, A, D, dt_bias, h0, lengths, y, h_final, workspace)
     if y is None:
         y = _new(shape, dtype, x.device, stream, lengths is not None)
@@ -477,11 +482,22 @@ def la_selective_scan_fwd(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, dt_sof
             workspace = _scratch(need, x.device, stream)
     if workspace is not None:
         ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _check(lib.la_selective_scan_fwd(
-        x.data_ptr(), xs, dt.data_ptr(), ds, _ptr(z), zs, Bm.data_ptr(), bs, Cm.data_ptr(), cs,
-        DTYPE[dtype], B, L, ch, N, G, Ap, bias, dt_softplus, Dp, h0p, n, y.data_ptr(),
-        _row_stride(y, shape, dtype, "y"), hfp, ws, ws_bytes, _raw_stream(dev, stream)))
+    status = lib.la_selective_scan_fwd(
+        x.data_ptr(), xs, dt.data_ptr(), ds, None if z is None else z.data_ptr(), zs,
+        Bm.data_ptr(), bs, Cm.data_ptr(), cs, DTYPE[dtype], B, L, ch, N, G, Ap, bias,
+        dt_softplus, Dp, h0p, n, y.data_ptr(), _row_stride(y, shape, dtype, "y"), hfp, ws,
+        ws_bytes, _current_stream(dev) if stream is None else stream.cuda_stream)
+    if status:
+        _check(status)
     return y, h_final
+
+
+def _head_param(t, H, d):
+    """A gated norm's weight or bias: its address and the heads it is given for."""
+    n = t.numel()
+    if t.dtype != torch.float32 or not t.is_contiguous() or (n != d and n != H * d):
+        raise ValueError("weight and bias must be contiguous fp32 [d] or [H*d]")
+    return t.data_ptr(), 1 if n == d else H
 
 
 def la_gated_norm_fwd(x, gate=None, weight=None, bias=None, norm="rms", activation="silu",
@@ -503,24 +519,32 @@ def la_gated_norm_fwd(x, gate=None, weight=None, bias=None, norm="rms", activati
     width = H * d
     shape = (B, L, width)
     heads = 1
-    for t in (weight, bias):
-        if t is not None:
-            n = t.numel()
-            if t.dtype != torch.float32 or not t.is_contiguous() or n not in (d, width):
-                raise ValueError("weight and bias must be contiguous fp32 [d] or [H*d]")
-            if n != d:
-                heads = H
-    if weight is not None and bias is not None and weight.numel() != bias.numel():
-        raise ValueError("weight and bias must have one shape")
+    w = b = None
+    if weight is not None:
+        w, heads = _head_param(weight, H, d)
+    if bias is not None:
+        b, heads = _head_param(bias, H, d)
+        if weight is not None and weight.numel() != bias.numel():
+            raise ValueError("weight and bias must have one shape")
     gs = 0 if gate is None else _row_stride(gate, shape, dtype, "gate")
     dev = _device_of(x, gate, weight, bias, y)
     if y is None:
         y = _new(shape, dtype, x.device, stream)
-    _check(_native.load().la_gated_norm_fwd(
-        x.data_ptr(), xb, xh, xt, _ptr(gate), gs, DTYPE[dtype], B, H, L, d, NORM[norm],
-        ACT[activation], gate_first, _ptr(weight), _ptr(bias), heads, eps, y.data_ptr(),
-        _row_stride(y, shape, dtype, "y"), _raw_stream(dev, stream)))
+    status = _native.load().la_gated_norm_fwd(
+        x.data_ptr(), xb, xh, xt, None if gate is None else gate.data_ptr(), gs, DTYPE[dtype],
+        B, H, L, d, NORM[norm], ACT[activation], gate_first, w, b, heads, eps, y.data_ptr(),
+        _row_stride(y, shape, dtype, "y"),
+        _current_stream(dev) if stream is None else stream.cuda_stream)
+    if status:
+        _check(status)
     return y
+
+
+def _same(t, shape, dtype):
+    if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError("x, residual and the outputs must be contiguous and of one shape, y in "
+                         "x's dtype and residual_out in residual's")
+    return t.data_ptr()
 
 
 def la_residual_norm_fwd(x, residual=None, weight=None, bias=None, post_weight=None, scale=None,
@@ -540,23 +564,26 @@ def la_residual_norm_fwd(x, residual=None, weight=None, bias=None, post_weight=N
     rd = residual.dtype if residual is not None else \
         residual_out.dtype if residual_out is not None else residual_dtype or dtype
     per = (D,)
-    pw = _opt_param(post_weight, per, "post_weight (one of the weights)")
-    sc = _opt_param(scale, per, "scale (one of the weights)")
-    w = _opt_param(weight, per, "weight (one of the weights)")
-    bi = _opt_param(bias, per, "bias (one of the weights)")
-    for t, want in ((x, dtype), (residual, rd), (y, dtype), (residual_out, rd)):
-        if t is not None and (t.shape != shape or t.dtype != want or not t.is_contiguous()):
-            raise ValueError("x, residual and the outputs must be contiguous and of one shape, "
-                             "y in x's dtype and residual_out in residual's")
+    pw = None if post_weight is None else _param(post_weight, per, "post_weight")
+    sc = None if scale is None else _param(scale, per, "scale")
+    w = None if weight is None else _param(weight, per, "weight")
+    bi = None if bias is None else _param(bias, per, "bias")
+    xp = _same(x, shape, dtype)
+    rp = None if residual is None else _same(residual, shape, rd)
+    yp = None if y is None else _same(y, shape, dtype)
+    op = None if residual_out is None else _same(residual_out, shape, rd)
     dev = _device_of(x, residual, weight, bias, post_weight, scale, y, residual_out)
     if y is None:
         y = _new(shape, dtype, x.device, stream)
+        yp = y.data_ptr()
     if residual_out is None:
         residual_out = _new(shape, rd, x.device, stream)
-    _check(_native.load().la_residual_norm_fwd(
-        x.data_ptr(), DTYPE[dtype], _ptr(residual), DTYPE[rd], x.numel() // D if D else 0, D,
-        pw, sc, alpha, w, bi, NORM[norm], eps, y.data_ptr(), residual_out.data_ptr(),
-        _raw_stream(dev, stream)))
+        op = residual_out.data_ptr()
+    status = _native.load().la_residual_norm_fwd(
+        xp, DTYPE[dtype], rp, DTYPE[rd], x.numel() // D if D else 0, D, pw, sc, alpha, w, bi,
+        NORM[norm], eps, yp, op, _current_stream(dev) if stream is None else stream.cuda_stream)
+    if status:
+        _check(status)
     return y, residual_out
 
 

@@ -788,7 +788,7 @@ ScanPlan make_plan(int B, int L, int D, int N, int groups) {
   double cost = rounds(blocks) * L;
   for (int n = 2; n <= kMaxSeg && L / n >= kMinLen; ++n) {
     const int len = ((L + n - 1) / n + 15) / 16 * 16;
-    const double c = 2 * rounds(blocks * (n - 1)) * len + 4000 + 100 * n;
+    const double c = 2 * rounds(blocks * (n - 1)) * len + 12000 + 100 * n;
     if (c < cost && (L + len - 1) / len == n) cost = c, best = {n, len};
   }
   return best;
