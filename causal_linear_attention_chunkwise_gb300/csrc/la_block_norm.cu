@@ -70,8 +70,11 @@ struct Row {
       else unpack2(v[i][e], f[2 * e], f[2 * e + 1]);
     }
   }
-  // v <- (v - mean) / sqrt(mean square about it + eps), mean = 0 for RMS.
-  __device__ __forceinline__ void normalise(int d, int norm, float eps, int lane, int size) {
+  // v <- (v - mean) / sqrt(mean square about it + eps), mean = 0 for RMS.  The
+  // first vector starts `shift` places in front of the row (SHIFT; else 0).
+  template <bool SHIFT = false>
+  __device__ __forceinline__ void normalise(int d, int norm, float eps, int lane, int size,
+                                            int shift = 0) {
     const float inv = 1.f / d;
     if (norm == LA_NORM_LAYER) {
       C s = 0;
@@ -82,9 +85,19 @@ struct Row {
       const C m = Cell::both(-team_sum<LANES>(Cell::sum(s)) * inv);
 #pragma unroll
       for (int i = 0; i < I; ++i) {
-        const bool in = (lane + i * size) * V < d;
+        const int c = (lane + i * size) * V - shift;
+        if constexpr (SHIFT) {
+          float f[V];
 #pragma unroll
-        for (int e = 0; e < H; ++e) v[i][e] = in ? add2(v[i][e], m) : C(0);
+          for (int e = 0; e < H; ++e) v[i][e] = add2(v[i][e], m);
+          get(i, f);
+#pragma unroll
+          for (int e = 0; e < V; ++e) f[e] = c + e >= 0 && c + e < d ? f[e] : 0.f;
+          set(i, f);
+        } else {
+#pragma unroll
+          for (int e = 0; e < H; ++e) v[i][e] = c < d ? add2(v[i][e], m) : C(0);
+        }
       }
     }
     C q = 0;
@@ -199,10 +212,31 @@ gated_norm_kernel(const GatedNormArgs a, long long rows) {
   }
 }
 
+// The elements lo <= e < hi of a vector, one by one; the others are 0.
+template <typename T, int V>
+__device__ __forceinline__ Raw<T, V> load_part(const T *p, int lo, int hi) {
+  Raw<T, V> r{};
+#pragma unroll
+  for (int e = 0; e < V; ++e)
+    if (e >= lo && e < hi) {
+      if constexpr (V == 1) r.u = p[e];
+      else if constexpr (sizeof(T) == 4) r.w[e] = __float_as_uint(p[e]);
+      else r.w[e / 2] |= (uint32_t)__bfloat16_as_ushort(p[e]) << (e % 2 * 16);
+    }
+  return r;
+}
+
 // A team takes the rows r, r + step, ...: the loads of its next row are in
-// flight while it works on the present one.  The factors of x stay in registers for all of a team's rows: read anew for each, the
-// three parameters of an fp32 residual step are as many bytes as its data.
-template <typename T, typename R, int V, int LANES, int I, int MAXT>
+// flight while it works on the present one.  The factors of x stay in registers
+// for all of a team's rows: read anew for each, the three parameters of an fp32
+// residual step are as many bytes as its data.
+//
+// SHIFT: rows whose width no vector divides start anywhere in a vector, row r
+// at its element r D mod V.  A team's vectors then lie on the tensors' 16-byte
+// boundaries, from `shift` elements in front of the row on, its first and last
+// one read and written element by element; step is a multiple of V, so all rows of
+// a team have one shift, and the weights stay in registers as well.
+template <typename T, typename R, int V, int LANES, int I, int MAXT, bool SHIFT>
 __global__ void __launch_bounds__(MAXT)
 residual_norm_kernel(const ResidualNormArgs a) {
   using ThisRow = Row<V, LANES, I>;
@@ -213,8 +247,11 @@ residual_norm_kernel(const ResidualNormArgs a) {
   const long long step = (long long)gridDim.x * teams;
   long long r = (long long)blockIdx.x * teams + (LANES ? threadIdx.x / size : 0);
   const int D = a.D;
-  // alpha scale post_weight, the factor of x in every row this team takes
-  Row<V, LANES, I> s;
+  const int shift = SHIFT ? (int)(r % V) * (D % V) % V : 0;
+  auto place = [&](int i) { return (lane + i * size) * V - shift; };
+  auto whole = [&](int c) { return SHIFT ? c >= 0 && c + V <= D : c < D; };
+  auto partly = [&](int c) { return SHIFT && c > -V && c < D; };  // where not whole
+  Row<V, LANES, I> s, wt;
   Raw<T, V> x[I];
   Raw<R, RV> res[I][RN];
   auto fetch = [&](long long at) {
@@ -222,14 +259,33 @@ residual_norm_kernel(const ResidualNormArgs a) {
     const R *rr = static_cast<const R *>(a.residual) + at * D;
 #pragma unroll
     for (int i = 0; i < I; ++i) {
-      const int c = (lane + i * size) * V;
-      if (c < D) {
+      const int c = place(i);
+      if (whole(c)) {
         x[i] = load_raw<T, V>(xr + c);
         if (a.residual) {
 #pragma unroll
           for (int k = 0; k < RN; ++k) res[i][k] = load_raw<R, RV>(rr + c + k * RV);
         }
+      } else if (partly(c)) {
+        x[i] = load_part<T, V>(xr + c, -c, D - c);
+        if (a.residual) {
+#pragma unroll
+          for (int k = 0; k < RN; ++k)
+            res[i][k] = load_part<R, RV>(rr + c + k * RV, -c - k * RV, D - c - k * RV);
+        }
       }
+    }
+  };
+  auto params = [&](const float *p, int i, float *f) {
+    const int c = place(i);
+#pragma unroll
+    for (int e = 0; e < V; ++e) f[e] = 0.f;
+    if constexpr (SHIFT) {
+#pragma unroll
+      for (int e = 0; e < V; ++e)
+        if (c + e >= 0 && c + e < D) f[e] = __ldg(p + c + e);
+    } else {
+      if (c < D) load_params<V>(p + c, f);
     }
   };
 #pragma unroll
@@ -241,21 +297,25 @@ residual_norm_kernel(const ResidualNormArgs a) {
   if (r < a.rows) fetch(r);
 #pragma unroll
   for (int i = 0; i < I; ++i) {
-    const int c = (lane + i * size) * V;
+    const int c = place(i);
     float f[V], g[V];
 #pragma unroll
-    for (int e = 0; e < V; ++e) f[e] = c < D ? a.alpha : 0.f;
-    if (a.scale && c < D) {
-      load_params<V>(a.scale + c, g);
+    for (int e = 0; e < V; ++e) f[e] = c + e >= 0 && c + e < D ? a.alpha : 0.f;
+    if (a.scale) {
+      params(a.scale, i, g);
 #pragma unroll
       for (int e = 0; e < V; ++e) f[e] *= g[e];
     }
-    if (a.post_weight && c < D) {
-      load_params<V>(a.post_weight + c, g);
+    if (a.post_weight) {
+      params(a.post_weight, i, g);
 #pragma unroll
       for (int e = 0; e < V; ++e) f[e] *= g[e];
     }
     s.set(i, f);
+    if (SHIFT && a.weight) {
+      params(a.weight, i, f);
+      wt.set(i, f);
+    }
   }
   // A team out of rows stays while another of its warp has one: the sums need
   // the whole warp.
@@ -273,55 +333,73 @@ residual_norm_kernel(const ResidualNormArgs a) {
       rs.set(i, f);
     }
     if (r + step < a.rows) fetch(r + step);
-    if (a.post_weight) row.normalise(D, a.norm, a.eps, lane, size);
+    if (a.post_weight) row.template normalise<SHIFT>(D, a.norm, a.eps, lane, size, shift);
     R *out = static_cast<R *>(a.residual_out) + r * D;
 #pragma unroll
     for (int i = 0; i < I; ++i) {
-      const int c = (lane + i * size) * V;
-      if (c >= D) continue;
+      const int c = place(i);
+      if (!whole(c) && !partly(c)) continue;
 #pragma unroll
       for (int e = 0; e < H; ++e) row.v[i][e] = fma2(s.v[i][e], row.v[i][e], rs.v[i][e]);
-      float f[V];
       if (live && a.residual_out) {
+        float f[V];
         row.get(i, f);
+        if (whole(c)) {
 #pragma unroll
-        for (int k = 0; k < RN; ++k) store_vec<R, RV>(out + c + k * RV, f + k * RV);
+          for (int k = 0; k < RN; ++k) store_vec<R, RV>(out + c + k * RV, f + k * RV);
+        } else {
+#pragma unroll
+          for (int e = 0; e < V; ++e)
+            if (c + e >= 0 && c + e < D) out[c + e] = from_f32<R>(f[e]);
+        }
       }
     }
-    row.normalise(D, a.norm, a.eps, lane, size);
+    row.template normalise<SHIFT>(D, a.norm, a.eps, lane, size, shift);
     T *y = static_cast<T *>(a.y) + r * D;
 #pragma unroll
     for (int i = 0; i < I; ++i) {
-      const int c = (lane + i * size) * V;
-      if (c >= D || !live) continue;
+      const int c = place(i);
+      if ((!whole(c) && !partly(c)) || !live) continue;
       Row<V, 1, 1> p;
       float f[V];
       if (a.weight) {
-        load_params<V>(a.weight + c, f);
-        p.set(0, f);
+        if constexpr (SHIFT) {
 #pragma unroll
-        for (int e = 0; e < H; ++e) row.v[i][e] = mul2(row.v[i][e], p.v[0][e]);
+          for (int e = 0; e < H; ++e) row.v[i][e] = mul2(row.v[i][e], wt.v[i][e]);
+        } else {
+          params(a.weight, i, f);
+          p.set(0, f);
+#pragma unroll
+          for (int e = 0; e < H; ++e) row.v[i][e] = mul2(row.v[i][e], p.v[0][e]);
+        }
       }
       if (a.bias) {
-        load_params<V>(a.bias + c, f);
+        params(a.bias, i, f);
         p.set(0, f);
 #pragma unroll
         for (int e = 0; e < H; ++e) row.v[i][e] = add2(row.v[i][e], p.v[0][e]);
       }
       row.get(i, f);
-      store_vec<T, V>(y + c, f);
+      if (whole(c)) {
+        store_vec<T, V>(y + c, f);
+      } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+          if (c + e >= 0 && c + e < D) y[c + e] = from_f32<T>(f[e]);
+      }
     }
   }
 }
 
 // Calls f(Int<LANES>, Int<I>, threads per row) with the team for rows of
 // width d in vectors of V elements: as few lanes as hold the row in two vectors
-// each, up to a warp; then a warp with more, up to a width of 1024; then a
-// block whose threads hold kBlockVecs<V> vectors.
+// each, up to a warp; then (FOUR) a warp with four, up to a width of 1024; then a
+// block whose threads hold kBlockVecs<V> vectors.  The residual step has no
+// registers for four: 16384 x 1024 bf16 takes 33 us with them, 29 in blocks.
 template <int V> constexpr int kBlockVecs = V == 8 ? 2 : V == 4 ? 4 : V == 2 ? 8 : 16;
 template <int N> struct Int { static constexpr int value = N; };
 
-template <int V, typename F>
+template <int V, bool FOUR, typename F>
 cudaError_t with_team(int d, F f) {
   const int vecs = (d + V - 1) / V;
   if constexpr (V > 2) {
@@ -330,7 +408,9 @@ cudaError_t with_team(int d, F f) {
     if (vecs <= 16) return f(Int<8>{}, Int<2>{}, 8);
     if (vecs <= 32) return f(Int<16>{}, Int<2>{}, 16);
     if (vecs <= 64) return f(Int<32>{}, Int<2>{}, 32);
-    if (vecs <= 128) return f(Int<32>{}, Int<4>{}, 32);
+    if constexpr (FOUR) {
+      if (vecs <= 128) return f(Int<32>{}, Int<4>{}, 32);
+    }
   } else {
     if (vecs <= 128) return f(Int<32>{}, Int<4>{}, 32);
     if (vecs <= 1024 / V) return f(Int<32>{}, Int<32 / V>{}, 32);
@@ -343,7 +423,7 @@ cudaError_t with_team(int d, F f) {
 template <typename T, int V, int ACT>
 cudaError_t launch_gated_v(const GatedNormArgs &a) {
   const long long rows = (long long)a.B * a.L * a.H;
-  return with_team<V>(a.d, [&](auto lanes, auto items, int threads) {
+  return with_team<V, true>(a.d, [&](auto lanes, auto items, int threads) {
     constexpr int LANES = decltype(lanes)::value, I = decltype(items)::value;
     const int block = LANES ? kTeamThreads : threads;
     const long long per = LANES ? kTeamThreads / LANES : 1, blocks = (rows + per - 1) / per;
@@ -359,22 +439,23 @@ cudaError_t launch_gated_v(const GatedNormArgs &a) {
   });
 }
 
-template <typename T, typename R, int V>
+template <typename T, typename R, int V, bool SHIFT>
 cudaError_t launch_residual_v(const ResidualNormArgs &a) {
-  return with_team<V>(a.D, [&](auto lanes, auto items, int threads) {
+  return with_team<V, false>(a.D + (SHIFT ? V - 1 : 0), [&](auto lanes, auto items, int threads) {
     constexpr int LANES = decltype(lanes)::value, I = decltype(items)::value;
     const int block = LANES ? kTeamThreads : threads;
     // 512 threads an SM: 16384 x 4096 (fp32 residual, post norm, scale) takes 126
     // us, with 768 or 1024 threads 133 to 154, in blocks that end with their row 144.
+    // A multiple of 8 blocks where a team takes more than one row.
     const long long per = LANES ? kTeamThreads / LANES : 1, blocks = (a.rows + per - 1) / per;
     const long long fill = 152ll * (block < 512 ? 512 / block : 1);
     const unsigned grid = (unsigned)(blocks < fill ? blocks : fill);
     if constexpr (LANES != 0)
-      residual_norm_kernel<T, R, V, LANES, I, kTeamThreads><<<grid, block, 0, a.stream>>>(a);
+      residual_norm_kernel<T, R, V, LANES, I, kTeamThreads, SHIFT><<<grid, block, 0, a.stream>>>(a);
     else if (threads <= 512)
-      residual_norm_kernel<T, R, V, 0, I, 512><<<grid, block, 0, a.stream>>>(a);
+      residual_norm_kernel<T, R, V, 0, I, 512, SHIFT><<<grid, block, 0, a.stream>>>(a);
     else
-      residual_norm_kernel<T, R, V, 0, I, 1024><<<grid, block, 0, a.stream>>>(a);
+      residual_norm_kernel<T, R, V, 0, I, 1024, SHIFT><<<grid, block, 0, a.stream>>>(a);
     return cudaGetLastError();
   });
 }
@@ -401,17 +482,17 @@ cudaError_t launch_gated_t(const GatedNormArgs &a) {
   return rows_fit(V) ? act(Int<V>{}) : rows_fit(2) ? act(Int<2>{}) : act(Int<1>{});
 }
 
+// Rows on 16-byte boundaries, rows anywhere in tensors that start on one, or
+// element by element.
 template <typename T, typename R>
 cudaError_t launch_residual_t(const ResidualNormArgs &a) {
-  auto rows_fit = [&](int v) {
-    const int rb = v * sizeof(R) > 16 ? 16 : v * sizeof(R);
-    return a.D % v == 0 && fits(a.x, v * sizeof(T)) && fits(a.y, v * sizeof(T)) &&
-           fits(a.residual, rb) && fits(a.residual_out, rb);
-  };
   constexpr int V = Pack16<T>::N;
-  return rows_fit(V)   ? launch_residual_v<T, R, V>(a)
-         : rows_fit(2) ? launch_residual_v<T, R, 2>(a)
-                       : launch_residual_v<T, R, 1>(a);
+  const bool base = fits(a.x, 16) && fits(a.y, 16) && fits(a.residual, 16) &&
+                    fits(a.residual_out, 16);
+  if (base && a.D % V == 0) return launch_residual_v<T, R, V, false>(a);
+  // Shifted, a row may take a vector more than a block of 1024 threads holds.
+  return base && a.D + V - 1 <= 16384 ? launch_residual_v<T, R, V, true>(a)
+                                      : launch_residual_v<T, R, 1, false>(a);
 }
 
 }  // namespace

@@ -295,8 +295,8 @@ __device__ __forceinline__ void scan_segment(const ScanParams<T> &p, long long b
           o.set2(e, v[e], v[e + 1]);
         }
         T *yr = yb + (long long)(t0 + t) * p.y_stride;
-        if constexpr (ALIGN == ALIGN16) {
-          if (have == V) *reinterpret_cast<uint4 *>(yr) = *reinterpret_cast<const uint4 *>(&o);
+        if (ALIGN == ALIGN16 && have == V) {
+          *reinterpret_cast<uint4 *>(yr) = *reinterpret_cast<const uint4 *>(&o);
         } else {
 #pragma unroll
           for (int e = 0; e < V; ++e)
@@ -815,15 +815,15 @@ cudaError_t launch_kernel(const ScanParams<T> &p, cudaStream_t stream) {
 template <typename T, int P, int S, int NC>
 cudaError_t launch_ps(const ScanArgs &a, const ScanParams<T> &p) {
   static_assert(ScanShape<P, S, NC, sizeof(T)>::CH == block_channels(P * S), "the plan's blocks");
-  // The widest loads that every row's alignment allows (a block's first channel
-  // is a multiple of 16 bytes into its group, a chunk 16 bytes or N * 4).
+  // The widest loads that the alignment of every row, and of every group in it,
+  // allows (a block's first channel is a multiple of 16 bytes into its group).
   const int per_group = a.D / a.groups;
   auto rows_fit = [&](int bytes) {
     const int v = bytes / (int)sizeof(T);
     auto fits = [&](const void *q, long long stride) {
       return (reinterpret_cast<uintptr_t>(q) & (bytes - 1)) == 0 && stride % v == 0;
     };
-    return per_group % v == 0 && a.N % v == 0 && fits(a.x, a.x_stride) &&
+    return (a.groups == 1 || (per_group % v == 0 && a.N % v == 0)) && fits(a.x, a.x_stride) &&
            fits(a.dt, a.dt_stride) && fits(a.z, a.z_stride) && fits(a.y, a.y_stride) &&
            fits(a.Bm, a.b_stride) && fits(a.Cm, a.c_stride);
   };

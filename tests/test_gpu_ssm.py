@@ -191,6 +191,24 @@ SCANS = [  # B, L, ch, N, G, packed, gate, state, ragged
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("ch,N,L", [(70, 13, 50), (70, 3, 1200), (5, 20, 33), (130, 16, 20)])
+def test_scan_aligned_rows_of_uneven_width(ch, N, L, dtype):
+    """Rows that start on 16-byte boundaries although no vector divides the width or N."""
+    i = scan_inputs(2, L, ch, N, 1, dtype)
+    for k in ("x", "dt", "z", "Bm", "Cm"):
+        v = i[k]
+        wide = torch.full((2, L, (v.shape[-1] + 15) // 8 * 8), NAN, dtype=v.dtype, device="cuda")
+        wide[..., :v.shape[-1]] = v
+        i[k] = wide[..., :v.shape[-1]]
+    wide = torch.full((2, L, (ch + 15) // 8 * 8), 5.0, dtype=DT[dtype], device="cuda")
+    y, h = scan(i, y=wide[..., :ch])
+    ref, href = scan_reference(i, dtype)
+    R.check(y, ref, "y")
+    R.check(h, href, "h_final")
+    assert (wide[..., ch:] == 5).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("B,L,ch,N,G,packed,gate,state,ragged", SCANS)
 def test_scan(B, L, ch, N, G, packed, gate, state, ragged, dtype):
     i = scan_inputs(B, L, ch, N, G, dtype, packed, gate, state, ragged)
@@ -445,6 +463,13 @@ def test_gated_norm_rows_of_zeros_and_non_finite_rows():
     (2, 16383, True, True, "rms", False),
     (5000, 24, True, True, "rms", False),      # teams of a warp with several rows each
     (1500, 2056, True, True, "layer", False),  # blocks with several rows each
+    (1301, 1027, True, True, "layer", True),   # and the same where rows start in mid-vector
+    (3001, 77, True, True, "rms", False),
+    (21001, 13, False, True, "layer", False),
+    (701, 9001, True, True, "rms", False),
+    (3, 16377, True, False, "layer", True),
+    (4, 16378, False, False, "rms", False),
+    (4, 16381, True, True, "rms", False),
 ])
 def test_residual_norm(R_, D, post, scale, norm, bias, dtype, rd):
     g = _gen(6)
@@ -456,10 +481,15 @@ def test_residual_norm(R_, D, post, scale, norm, bias, dtype, rd):
     ry, rr = R.residual_norm(x, res, pw, sc, 0.7, w, b, norm, 1e-5, dtype, rd)
     R.check(r, rr, "residual_out")
     R.check(y, ry, "y")
-    x2, res2 = x.clone(), res.clone()  # in place over both inputs
+    # in place over both inputs, between rows that stay as they are
+    xw, rw = (torch.full(((R_ + 16) * D,), 3.0, dtype=v.dtype, device="cuda") for v in (x, res))
+    x2, res2 = (w[8 * D:(8 + R_) * D].view(R_, D) for w in (xw, rw))
+    x2.copy_(x), res2.copy_(res)
     y2, r2 = api.la_residual_norm_fwd(x2, res2, w, b, post_weight=pw, scale=sc, alpha=0.7,
                                       norm=norm, y=x2, residual_out=res2)
     assert y2 is x2 and r2 is res2 and torch.equal(y2, y) and torch.equal(r2, r)
+    for w in (xw, rw):
+        assert (w[:8 * D] == 3).all() and (w[(8 + R_) * D:] == 3).all()
 
 
 def test_residual_norm_first_block_and_shapes():
