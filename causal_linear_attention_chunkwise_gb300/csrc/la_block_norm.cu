@@ -131,6 +131,8 @@ __device__ __forceinline__ void load_params(const float *p, float *f) {
   }
 }
 
+// Five blocks of teams per SM: 4 x 16 x 4096 x 64 takes 23.4 us, with four 23.7,
+// with six (spills) 27.
 template <typename T, int V, int LANES, int I, int ACT, int MAXT>
 __global__ void __launch_bounds__(MAXT, LANES && V > 2 && I <= 2 ? 5 : 1)
 gated_norm_kernel(const GatedNormArgs a, long long rows) {

@@ -22,18 +22,18 @@
 // from the states of the segments before it, decayed by exp(A sum delta).
 //
 // What bounds it: per 4 states of 32 lanes and token, 16 cycles of the
-// special-function unit for the exps (32 lanes a clock on an SM), 16 of the fp32
-// pipe (128 lanes a clock), 22 with three-operand packed instructions as they
-// issue.  Both floors are 57 us for 4 x 2048 x 4096 (N = 16, bf16; its bytes 40):
-// it runs 184 us, 1 x 16384 x 2048 276 us.  The counters show no unit full (issue
-// slots and shared-memory wavefronts about 70% on an SM with two blocks): the
-// recurrence warps' own instruction stream sets the pace, and taking out
-// staging work (softplus, gate, address arithmetic) does not change the time.
-// One block holds 64 channels, so 256 blocks leave 48 of the 152 SMs with one
-// block instead of two (14%).  Measured on these two cases: 4 states of two
-// channels per lane 198 and 293 us, of one channel 260; 8 of two channels 202;
-// blocks of 2 + 2 warps 195; tiles in one role per thread (no staging warps)
-// 262 and 898; loads of one token at a time instead of three in flight 206.
+// special-function unit for the exps (32 lanes a clock on an SM) and 16 of the
+// fp32 pipe (128 lanes a clock; 22 as three-operand packed instructions issue).
+// Both floors are 57 us for 4 x 2048 x 4096 (N = 16, bf16; its bytes take 40): it
+// runs 184 us, and 1 x 16384 x 2048 276 us.  The counters show no unit full
+// (issue slots and shared-memory wavefronts about 70% on an SM with two
+// blocks): the recurrence warps' own instruction stream sets the pace, and taking
+// out staging work (softplus, gate, address arithmetic) does not change the time.
+// A block has 64 channels, so 256 blocks leave 48 of the 152 SMs with one
+// instead of two (14%).  Measured on the first case: lanes with 4 states of two
+// channels 198 us, of one 260, with 8 of two 202; blocks of 2 + 2 warps 195; one
+// role for all threads (no staging warps) 262; a token's loads not ahead of the
+// token before 213.
 #include <cstdint>
 
 #include "../../include/la_gb300.h"
@@ -828,8 +828,10 @@ cudaError_t launch_ps(const ScanArgs &a, const ScanParams<T> &p) {
            fits(a.Bm, a.b_stride) && fits(a.Cm, a.c_stride);
   };
   if (rows_fit(16)) return launch_kernel<T, P, S, NC, ALIGN16>(p, a.stream);
-  if (rows_fit(4)) return launch_kernel<T, P, S, NC, ALIGN4>(p, a.stream);
-  return launch_kernel<T, P, S, NC, ALIGN_ELT>(p, a.stream);
+  if constexpr (sizeof(T) < 4) {  // an fp32 row is always on 4-byte boundaries
+    if (!rows_fit(4)) return launch_kernel<T, P, S, NC, ALIGN_ELT>(p, a.stream);
+  }
+  return launch_kernel<T, P, S, NC, ALIGN4>(p, a.stream);
 }
 
 template <typename T>
