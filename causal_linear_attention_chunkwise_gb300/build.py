@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import glob
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -44,6 +45,13 @@ def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
+def _newest(src: str) -> float:
+    """When ``src``, or a .cu file that it includes, was last changed."""
+    with open(src) as f:
+        included = re.findall(r'^#include "(\w+\.cu)"', f.read(), flags=re.M)
+    return max(os.path.getmtime(p) for p in [src, *(os.path.join(CSRC, i) for i in included)])
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile and link the library; returns its path.  Raises on failure."""
     nvcc = _nvcc()
@@ -56,7 +64,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         obj = os.path.join(BUILD_DIR, os.path.basename(src)[:-3] + ".o")
         objs.append(obj)
         stale = force or not os.path.exists(obj) or \
-            os.path.getmtime(obj) < max(os.path.getmtime(src), newest_header)
+            os.path.getmtime(obj) < max(_newest(src), newest_header)
         if stale:
             cmd = [nvcc, *ARCH, *NVCC_FLAGS, "-c", src, "-o", obj]
             if verbose:

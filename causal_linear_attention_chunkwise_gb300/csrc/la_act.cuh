@@ -112,7 +112,7 @@ template <typename T> struct Raw<T, 1> {
   __device__ __forceinline__ void unpack(float *f) const { f[0] = to_f32(u); }
 };
 
-// VEC elements to and from fp32.
+// VEC elements between memory and registers, and from fp32.
 template <typename T, int VEC>
 __device__ __forceinline__ Raw<T, VEC> load_raw(const T *p) {
   Raw<T, VEC> r;
@@ -138,11 +138,6 @@ __device__ __forceinline__ void store_raw(T *p, const Raw<T, VEC> &r) {
     *reinterpret_cast<uint2 *>(p) = make_uint2(r.w[0], r.w[1]);
   else *reinterpret_cast<uint32_t *>(p) = r.w[0];
 }
-template <typename T, int VEC>
-__device__ __forceinline__ void load_vec(const T *p, float *f) {
-  load_raw<T, VEC>(p).unpack(f);
-}
-
 template <typename T, int VEC>
 __device__ __forceinline__ void store_vec(T *p, const float *f) {
   Raw<T, VEC> r;

@@ -159,6 +159,7 @@ struct ScanArgs {
 };
 size_t selective_scan_workspace_bytes(int B, int L, int D, int N, int groups);
 cudaError_t launch_selective_scan(const ScanArgs &a);
+cudaError_t launch_selective_scan_f32(const ScanArgs &a);  // fp32 activations
 
 // Gated norm of heads and the residual step's norms (width 1..16384).
 struct GatedNormArgs {

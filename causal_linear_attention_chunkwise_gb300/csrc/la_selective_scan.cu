@@ -858,13 +858,19 @@ cudaError_t launch_t(const ScanArgs &a) {
 
 }  // namespace
 
+// The fp32 kernels are a translation unit of their own (la_selective_scan_f32.cu
+// includes this file), so that the two compile side by side.
+#ifdef LA_SELECTIVE_SCAN_F32
+cudaError_t launch_selective_scan_f32(const ScanArgs &a) { return launch_t<float>(a); }
+#else
 size_t selective_scan_workspace_bytes(int B, int L, int D, int N, int groups) {
   const ScanPlan plan = make_plan(B, L, D, N, groups);
   return (size_t)(plan.nseg - 1) * B * D * (N + 1) * sizeof(float);
 }
 
 cudaError_t launch_selective_scan(const ScanArgs &a) {
-  return a.dtype == LA_F32 ? launch_t<float>(a) : launch_t<__nv_bfloat16>(a);
+  return a.dtype == LA_F32 ? launch_selective_scan_f32(a) : launch_t<__nv_bfloat16>(a);
 }
+#endif
 
 }  // namespace la
