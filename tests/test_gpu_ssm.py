@@ -365,6 +365,42 @@ def test_outputs_in_slices_and_no_final_states(L):
     assert torch.equal(wide[..., :ch], i["x"]) and torch.equal(wide[..., 2 * ch:], i["z"])
 
 
+def test_one_token_taken_out_of_a_prompt():
+    """x[:, t:t+1] of longer tensors as it lies: rows a whole sequence apart."""
+    i = scan_inputs(5, 9, 72, 16, 1, "bf16")
+    cut = lambda v: v[:, 4:5]  # noqa: E731
+    part = {k: (cut(v) if k in ("x", "dt", "z", "Bm", "Cm") else v) for k, v in i.items()}
+    dense = {k: (v.contiguous() if k in ("x", "dt", "z", "Bm", "Cm") else v)
+             for k, v in part.items()}
+    y = torch.full((5, 9, 72), 5.0, dtype=torch.bfloat16, device="cuda")
+    _, h = scan(part, y=cut(y))
+    want = scan(dense)
+    assert torch.equal(cut(y), want[0]) and torch.equal(h, want[1])
+    w = torch.randn(72, 4, generator=_gen(32)).cuda()
+    st = torch.randn(5, 3, 72, generator=_gen(33)).bfloat16().cuda()
+    _, sf = api.la_causal_conv_fwd(part["x"], w, state0=st, y=cut(y))
+    want = api.la_causal_conv_fwd(dense["x"], w, state0=st)
+    assert torch.equal(cut(y), want[0]) and torch.equal(sf, want[1])
+    api.la_gated_norm_fwd(part["x"][:, None], part["z"], y=cut(y))
+    assert torch.equal(cut(y), api.la_gated_norm_fwd(dense["x"][:, None], dense["z"]))
+    rest = torch.ones(9, dtype=torch.bool)
+    rest[4] = False
+    assert (y[:, rest.cuda()] == 5).all()
+
+
+def test_many_sequences_of_one_token():
+    i = scan_inputs(70000, 1, 8, 4, 1, "f32")
+    ref, href = scan_reference({k: (v[-300:] if k in ("x", "dt", "z", "Bm", "Cm", "h0") else v)
+                                for k, v in i.items()}, "f32")
+    y, h = scan(i)
+    R.check(y[-300:], ref, "y")
+    R.check(h[-300:], href, "h_final")
+    x, weight, bias, st, _ = conv_inputs(70000, 1, 8, 4, "f32")
+    y, _ = api.la_causal_conv_fwd(x, weight, bias, state0=st)
+    ref, _ = R.causal_conv(x[-300:], weight, bias, "silu", st[-300:], None, "f32")
+    R.check(y[-300:], ref, "conv")
+
+
 def test_scan_ragged_segments_in_place():
     i = scan_inputs(6, 900, 64, 16, 1, "f32", ragged=True)
     assert api.la_selective_scan_fwd_workspace_bytes(6, 900, 64, 16) > 0
