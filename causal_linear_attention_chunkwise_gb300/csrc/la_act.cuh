@@ -18,6 +18,13 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
+// max(a, b), NaN where one of them is (fmaxf gives the other).
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
 constexpr float kLog2e = 1.4426950408889634f;
 
 // 1 / (1 + e^-x): e^-x overflows to infinity for x < -88, whose reciprocal is 0.

@@ -80,13 +80,17 @@ struct ScanParams {
 };
 
 // softplus of two values: log(1 + e^v) = max(v, 0) + e p(e), e = e^-|v| in (0,
-// 1].  e's exponent is taken in two parts, -|v| log2 e = hi + lo, so that the
-// rounding of hi does not reach e.  p(e) = log1p(e) / e is the polynomial of
-// degree 9 through the ten Chebyshev nodes of [0, 1]: it errs by 5e-9 before
-// rounding, relative, so steps near e^-7 keep the precision that log(1 + e)
-// would lose.  (2 atanh(e / (2 + e)) by its series took a reciprocal more.)
+// 1].  e's exponent is taken in two parts, -|v| log2 e = hi + lo, where a fused
+// multiply-add gives the rounding error of the product hi exactly, so that it
+// does not reach e.  p(e) = log1p(e) / e is the polynomial of degree 9 through
+// the ten Chebyshev nodes of [0, 1]; with the constant 1 and the other
+// coefficients in fp32 it errs by 1.43e-8 before rounding, relative (as computed
+// in 64 bits), so steps near e^-7 keep the precision that log(1 + e) would lose.
+// (2 atanh(e / (2 + e)) by its series took a reciprocal more.)
+// |v| counts as 128 beyond it: e is 0 there in fp32, and hi stays finite for
+// infinities and for the lowest values that a mask writes.
 __device__ __forceinline__ void softplus2(float &v0, float &v1) {
-  const unsigned long long v = pack2(-fabsf(v0), -fabsf(v1));
+  const unsigned long long v = pack2(max_nan(-fabsf(v0), -128.f), max_nan(-fabsf(v1), -128.f));
   const unsigned long long hi = mul2(v, dup2(kLog2e));
   unsigned long long lo = fma2(v, dup2(kLog2e), mul2(hi, dup2(-1.f)));
   lo = fma2(v, dup2(1.925963033500e-8f), lo);  // log2 e - float(log2 e)

@@ -344,9 +344,11 @@ la_status la_causal_conv_fwd(const void *x, long long x_stride, int dtype, int B
  *                LA_ERR_INVALID_ARG.  Its contents need no initialisation and
  *                are not kept.
  *
- * Supported: N in 1..256, D a multiple of groups, L and D up to 2^30.  A NaN or
- * an infinity in x or dt makes its channel's outputs and states non-finite from
- * its token on, an infinity possibly as a NaN; other channels are not touched.
+ * Supported: N in 1..256, D a multiple of groups, L and D up to 2^30.  With
+ * dt_softplus a dt of minus infinity, or of the type's lowest value, is a step
+ * of zero: the token keeps the state.  A NaN in x or dt, an infinity in x or an
+ * infinite delta makes its channel's outputs and states non-finite from its
+ * token on, an infinity possibly as a NaN; other channels are not touched.
  */
 la_status la_selective_scan_fwd(const void *x, long long x_stride, const void *dt,
                                 long long dt_stride, const void *z, long long z_stride,

@@ -1,0 +1,58 @@
+"""The state space block's operators on the GPU at the ends of their ranges: masks and
+infinities among the steps, states that grow, the largest sizes, calls side by side."""
+import pytest
+import torch
+
+from causal_linear_attention_chunkwise_gb300 import api
+from tests import ssm_reference as R
+from tests.test_gpu_ssm import DT, scan, scan_inputs, scan_reference
+
+pytestmark = pytest.mark.gpu
+
+INF = float("inf")
+
+
+# ---------------------------------------------------------------- steps
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("mask", ["-inf", "lowest", "-2.4e38"])
+@pytest.mark.parametrize("L", [1, 6, 40, 700])
+def test_scan_masked_steps_keep_the_state(L, mask, dtype):
+    """softplus(-200) is below every fp32 number, so its step is 0, and so are those of the
+    values that a mask writes: the same bits."""
+    i = scan_inputs(2, L, 40, 16, 1, dtype)
+    at = (torch.arange(L) % 3 != 1).cuda()
+    fill = torch.finfo(DT[dtype]).min if mask == "lowest" else float(mask)
+    got, want = (dict(i, dt=i["dt"].clone()) for _ in range(2))
+    got["dt"][:, at], want["dt"][:, at] = fill, -200.0
+    (y, h), (y2, h2) = scan(got), scan(want)
+    assert torch.equal(y, y2) and torch.equal(h, h2)
+    ref, href = scan_reference(want, dtype)
+    R.check(y, ref, "y")
+    R.check(h, href, "h_final")
+    if L == 1:
+        assert torch.equal(h, i["h0"])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("L", [1, 5, 40, 700])
+def test_scan_largest_finite_step_forgets_the_state(L, dtype):
+    """delta of the type's largest value: every decay is 0, and with x = 0 so is the write."""
+    i = scan_inputs(2, L, 40, 16, 1, dtype, gate=False)
+    t = L // 2
+    i["dt"][:, t], i["x"][:, t] = torch.finfo(DT[dtype]).max, 0
+    y, h = scan(i)
+    assert (y[:, t] == 0).all() and torch.isfinite(y).all() and torch.isfinite(h).all()
+    if t == L - 1:
+        assert (h == 0).all()
+
+
+@pytest.mark.parametrize("L", [5, 40, 700])
+def test_scan_infinite_steps_stay_in_their_channel(L):
+    i = scan_inputs(2, L, 40, 16, 1, "f32", gate=False)
+    t = L // 2
+    i["dt"][0, t, 7], i["dt"][1, t, 9] = INF, -INF
+    y, h = scan(i)
+    want = torch.zeros(2, L, 40, dtype=torch.bool)
+    want[0, t:, 7] = True
+    assert torch.equal(~torch.isfinite(y).cpu(), want)
+    assert (~torch.isfinite(h)).any(-1).nonzero().tolist() == [[0, 7]]
