@@ -580,10 +580,12 @@ template <typename T, int P, int S, int R, bool VEC, bool ONE>
 __global__ void __launch_bounds__(256, ONE && sizeof(T) == 2 && P == 4 ? 5 : 4)
 selective_step_kernel(const ScanParams<T> p, unsigned blocks) {  // blocks: per row of sequences
   static_assert(R == 1 || R == 2 || R == 4, "halvings");
-  const unsigned row = blockIdx.x / blocks, slot = (blockIdx.x - row * blocks) * 256 + threadIdx.x;
-  const int q = slot % S;
-  const bool live = slot / S < (unsigned)p.D;
-  const int c = live ? slot / S : 0;
+  // Channel and lane apart: D S places would pass 32 bits.
+  const unsigned row = blockIdx.x / blocks;
+  const unsigned place = (blockIdx.x - row * blocks) * (256 / S) + threadIdx.x / S;
+  const int q = threadIdx.x % S;
+  const bool live = place < (unsigned)p.D;
+  const int c = live ? place : 0;
   const int g = p.groups == 1 ? 0 : c / (p.D / p.groups);
   const int b0 = row * R;
   const int mine = min(b0 + q % R, p.B - 1);  // the sequence whose scalars this lane works out

@@ -56,3 +56,27 @@ def test_scan_infinite_steps_stay_in_their_channel(L):
     want[0, t:, 7] = True
     assert torch.equal(~torch.isfinite(y).cpu(), want)
     assert (~torch.isfinite(h)).any(-1).nonzero().tolist() == [[0, 7]]
+
+
+# ---------------------------------------------------------------- sizes
+def test_scan_token_of_more_channels_than_32_bits_of_lanes():
+    """2^27 + 64 channels of 65 states, 32 lanes to a channel; the states in place.  With A = 0,
+    delta = 1/2, B = 1 and sum C = 1 every value is exact: h = x / 2 and y = x / 2."""
+    ch, N = (1 << 27) + 64, 65
+    torch.cuda.empty_cache()
+    x = torch.randn(1, 1, ch, device="cuda", dtype=torch.bfloat16)
+    u = 0.5 * x
+    bc = torch.ones(2, 1, 1, N, dtype=torch.bfloat16, device="cuda")
+    bc[1] = 1 / 64
+    bc[1, ..., 64] = 0
+    A = torch.zeros(ch, N, device="cuda")
+    h = torch.zeros(1, ch, N, device="cuda")
+    y = torch.full_like(x, 7.0)
+    api.la_selective_scan_fwd(x, torch.full_like(x, 0.5), A, bc[0], bc[1], dt_softplus=False,
+                              h0=h, h_final=h, y=y)
+    assert torch.equal(y, u)
+    del A
+    for part, want in zip(h.split(1 << 24, 1), u[0, 0].float().split(1 << 24)):
+        assert (part[0] == want[:, None]).all()
+    del h, part
+    torch.cuda.empty_cache()
