@@ -373,18 +373,11 @@ def _new(shape, dtype, device, stream, zero=False):
 
 
 def _scratch(nbytes, device, stream):
-    """Workspace of one call: the cached buffer of its stream, but a buffer of
-    the graph's own while a graph is captured (graphs may be replayed side by
-    side, and a cached buffer may be replaced by a larger one)."""
-    s = torch.cuda.current_stream() if stream is None else stream
-    with torch.cuda.stream(s):
-        if torch.cuda.is_current_stream_capturing():
-            return torch.empty(nbytes, dtype=torch.uint8, device=device)
-        key = ("scratch", device.index, s.cuda_stream)
-        buf = _ws_cache.get(key)
-        if buf is None or buf.numel() < nbytes:
-            buf = _ws_cache[key] = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    return buf
+    """Workspace of one call, from the allocator on the call's stream: calls of two
+    threads on one stream, whose launches may interleave, get two buffers, a
+    captured call one of its graph's own, and a freed one goes to no call before
+    this one on the stream has run."""
+    return _new((nbytes,), torch.uint8, device, stream)
 
 
 def _conv_state(t, shape, dtype):
@@ -447,8 +440,8 @@ def la_selective_scan_fwd(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, dt_sof
     (with L = 1 that is one decode step in place).  ``lengths`` int32 [B] are
     the real tokens of a padded batch: the rows of ``y`` behind them are left
     as they are (zero when ``y`` is made here).  With ``segments`` (the
-    default) a cached workspace lets a long sequence run as several segments
-    side by side."""
+    default) a workspace from the allocator lets a long sequence run as several
+    segments side by side."""
     shape, dtype = x.shape, x.dtype
     B, L, ch = shape
     N = A.shape[-1]

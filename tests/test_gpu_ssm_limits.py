@@ -1,9 +1,11 @@
 """The state space block's operators on the GPU at the ends of their ranges: masks and
 infinities among the steps, states that grow, the largest sizes, calls side by side."""
+import threading
+
 import pytest
 import torch
 
-from causal_linear_attention_chunkwise_gb300 import api
+from causal_linear_attention_chunkwise_gb300 import _native, api
 from tests import ssm_reference as R
 from tests.test_gpu_ssm import DT, scan, scan_inputs, scan_reference
 
@@ -80,3 +82,57 @@ def test_scan_token_of_more_channels_than_32_bits_of_lanes():
         assert (part[0] == want[:, None]).all()
     del h, part
     torch.cuda.empty_cache()
+
+
+# ---------------------------------------------------------------- side by side
+class _Meeting:
+    """The library, with one entry point that two threads enter together: both have their
+    workspaces before either launches.  Keeps the workspaces' addresses."""
+
+    def __init__(self, name, workspace_at):
+        self.lib, self.name, self.at = _native.load(), name, workspace_at
+        self.both, self.seen = threading.Barrier(2), []
+
+    def __getattr__(self, name):
+        fn = getattr(self.lib, name)
+        if name != self.name:
+            return fn
+
+        def call(*args):
+            self.seen.append(args[self.at])
+            self.both.wait(timeout=60)
+            return fn(*args)
+        return call
+
+
+def run_together(monkeypatch, name, workspace_at, calls):
+    """What the two calls give in two threads at once, on one stream; they may share no workspace."""
+    lib = _Meeting(name, workspace_at)
+    got, errors = [None, None], []
+
+    def work(k):
+        try:
+            got[k] = calls[k]()
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+    with monkeypatch.context() as m:
+        m.setattr(_native, "load", lambda: lib)
+        threads = [threading.Thread(target=work, args=(k,)) for k in range(2)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+    torch.cuda.synchronize()
+    assert not errors, errors
+    assert all(lib.seen) and lib.seen[0] != lib.seen[1]
+    return got
+
+
+def test_scans_of_two_threads_on_one_stream(monkeypatch):
+    """Each of the two launches of a segmented scan may have one of another thread in front of it."""
+    runs = [scan_inputs(1, 2500, 256, 16, 1, "bf16", seed=s) for s in (40, 41)]
+    want = [scan(i) for i in runs]
+    got = run_together(monkeypatch, "la_selective_scan_fwd", -3,
+                       [lambda i=i: scan(i) for i in runs])
+    for (y, h), (y2, h2) in zip(got, want):
+        assert torch.equal(y, y2) and torch.equal(h, h2)
