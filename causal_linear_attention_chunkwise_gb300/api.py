@@ -69,23 +69,21 @@ def la_chunk_fwd_kernel_count(B, H, L, d_k, d_v, chunk=64, dtype=torch.bfloat16)
     return int(_native.load().la_chunk_fwd_kernel_count(B, H, L, d_k, d_v, chunk, DTYPE[dtype]))
 
 
-_ws_cache: dict = {}
+def _new(shape, dtype, device, stream, zero=False):
+    """A tensor on the stream that the call runs on."""
+    make = torch.zeros if zero else torch.empty
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=dtype, device=device)
 
 
 def _workspace(nbytes, device, stream=None):
-    """A cached scratch buffer per (device, stream): calls ordered on one
-    stream may share it, calls on different streams never do."""
-    if nbytes == 0:
-        return None
-    s = torch.cuda.current_stream(device) if stream is None else stream
-    key = (device.index, s.cuda_stream)
-    buf = _ws_cache.get(key)
-    if buf is None or buf.numel() < nbytes:
-        buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
-        if stream is not None:
-            buf.record_stream(s)  # the allocator must not hand it out while s may use it
-        _ws_cache[key] = buf
-    return buf
+    """Workspace of one call, from the allocator on the call's stream: calls of two
+    threads on one stream, whose launches may interleave, get two buffers, a
+    captured call one of its graph's own, and a freed one goes to no call before
+    this one on the stream has run."""
+    return _new((nbytes,), torch.uint8, device, stream) if nbytes else None
 
 
 def la_chunk_fwd(q, k, v, chunk=64, decay_kind="none", decay=None, S0=None, O=None,
@@ -269,7 +267,7 @@ def la_channel_gate_fwd(q, k, v, log_alpha, chunk=64, S0=None, O=None, S_final=N
                         want_final_state=True, workspace=None, segments=True, stream=None):
     """Per-channel gate S_t = diag(alpha_t) S_{t-1} + phi(k_t) v_t^T with
     ``log_alpha`` fp32 [B,H,L,d_k].  Returns ``(O, S_final)``.  With
-    ``segments`` (the default) a cached workspace lets the library run each
+    ``segments`` (the default) a workspace lets the library run each
     sequence as several segments side by side; ``segments=False`` runs each
     sequence in one piece."""
     O = _qkv(q, k, v, O)
@@ -363,23 +361,6 @@ def _lengths_ptr(lengths, B):
     return lengths.data_ptr()
 
 
-def _new(shape, dtype, device, stream, zero=False):
-    """An output on the stream that the call runs on."""
-    make = torch.zeros if zero else torch.empty
-    if stream is None:
-        return make(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return make(shape, dtype=dtype, device=device)
-
-
-def _scratch(nbytes, device, stream):
-    """Workspace of one call, from the allocator on the call's stream: calls of two
-    threads on one stream, whose launches may interleave, get two buffers, a
-    captured call one of its graph's own, and a freed one goes to no call before
-    this one on the stream has run."""
-    return _new((nbytes,), torch.uint8, device, stream)
-
-
 def _conv_state(t, shape, dtype):
     if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError("the states must be contiguous [B,W-1,D] in x's dtype")
@@ -440,8 +421,8 @@ def la_selective_scan_fwd(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, dt_sof
     (with L = 1 that is one decode step in place).  ``lengths`` int32 [B] are
     the real tokens of a padded batch: the rows of ``y`` behind them are left
     as they are (zero when ``y`` is made here).  With ``segments`` (the
-    default) a workspace from the allocator lets a long sequence run as several
-    segments side by side."""
+    default) a workspace lets a long sequence run as several segments side by
+    side."""
     shape, dtype = x.shape, x.dtype
     B, L, ch = shape
     N = A.shape[-1]
@@ -470,9 +451,8 @@ def la_selective_scan_fwd(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, dt_sof
     lib = _native.load()
     ws = ws_bytes = 0
     if workspace is None and segments and L > 1:
-        need = lib.la_selective_scan_fwd_workspace_bytes(B, L, ch, N, G)
-        if need:
-            workspace = _scratch(need, x.device, stream)
+        workspace = _workspace(lib.la_selective_scan_fwd_workspace_bytes(B, L, ch, N, G),
+                               x.device, stream)
     if workspace is not None:
         ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     status = lib.la_selective_scan_fwd(
