@@ -39,8 +39,11 @@ def _ptr(t):
 
 
 def _stream(stream):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if torch.cuda.is_initialized():
+        return _current_stream(_current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _need_cuda(*ts):
