@@ -120,6 +120,17 @@ bool overlap(const Rows &a, const Rows &b) {
 // The same for dense ranges of bytes.
 Rows dense(const void *p, size_t bytes) { return {p, 1, (long long)bytes, (long long)bytes, 1}; }
 
+// n fp32 parameters or int32 lengths.
+Rows params(const void *p, long long n) { return dense(p, (size_t)n * 4); }
+
+// Whether an output shares an element with one of several inputs.
+template <size_t N>
+bool overlap_any(const Rows &out, const Rows (&in)[N]) {
+  for (const Rows &r : in)
+    if (overlap(out, r)) return true;
+  return false;
+}
+
 bool aligned_elt(const void *p, size_t elt) {
   return (reinterpret_cast<uintptr_t>(p) & (elt - 1)) == 0;
 }
@@ -471,8 +482,9 @@ la_status la_causal_conv_fwd(const void *x, long long x_stride, int dtype, int B
   const size_t state_bytes = (size_t)B * (width - 1) * D * elt;
   const Rows xr{x, rows, D, x_stride, elt}, yr{y, rows, D, y_stride, elt};
   const Rows s0 = dense(state0, state_bytes), s1 = dense(state_final, state_bytes);
+  const Rows par[] = {params(weight, (long long)D * width), params(bias, D), params(lengths, B)};
   if (overlap(yr, xr) || overlap(yr, s0) || overlap(yr, s1) || overlap(s1, xr) ||
-      (state_final != state0 && overlap(s1, s0)))
+      (state_final != state0 && overlap(s1, s0)) || overlap_any(yr, par) || overlap_any(s1, par))
     return fail(LA_ERR_INVALID_ARG, "%s: an output overlaps an input or another output", fn);
   ConvArgs a{x, x_stride, dtype, B, L, D, width, weight, bias, activation, lengths, state0, y,
              y_stride, state_final, static_cast<cudaStream_t>(cuda_stream)};
@@ -522,6 +534,10 @@ la_status la_selective_scan_fwd(const void *x, long long x_stride, const void *d
   const Rows s0 = dense(h0, state_bytes), s1 = dense(h_final, state_bytes);
   if (h_final != h0 && overlap(s1, s0))
     return fail(LA_ERR_INVALID_ARG, "%s: h_final overlaps h0", fn);
+  const Rows par[] = {params(A, (long long)D * N), params(dt_bias, D), params(skip, D),
+                      params(lengths, B)};
+  if (overlap_any(s1, par))
+    return fail(LA_ERR_INVALID_ARG, "%s: h_final overlaps a parameter or lengths", fn);
   if (L == 0) {
     cudaError_t e = pass_through_state(h_final, h0, state_bytes, st);
     if (e != cudaSuccess) return cuda_fail(e, fn);
@@ -539,10 +555,11 @@ la_status la_selective_scan_fwd(const void *x, long long x_stride, const void *d
   const Rows yr{y, rows, D, y_stride, elt};
   const Rows in[] = {{x, rows, D, x_stride, elt},   {dt, rows, D, dt_stride, elt},
                      {z, rows, D, z_stride, elt},   {Bm, rows, gn, b_stride, elt},
-                     {Cm, rows, gn, c_stride, elt}, s0};
-  for (const Rows &r : in)
-    if (overlap(yr, r) || (r.p != h0 && overlap(s1, r)))
-      return fail(LA_ERR_INVALID_ARG, "%s: an output overlaps an input", fn);
+                     {Cm, rows, gn, c_stride, elt}};
+  if (overlap_any(yr, in) || overlap(yr, s0) || overlap_any(s1, in))
+    return fail(LA_ERR_INVALID_ARG, "%s: an output overlaps an input", fn);
+  if (overlap_any(yr, par))
+    return fail(LA_ERR_INVALID_ARG, "%s: y overlaps a parameter or lengths", fn);
   if (overlap(yr, s1)) return fail(LA_ERR_INVALID_ARG, "%s: y overlaps h_final", fn);
   const size_t need = selective_scan_workspace_bytes(B, L, D, N, groups);
   if (workspace && ws_bytes < need)
@@ -550,6 +567,9 @@ la_status la_selective_scan_fwd(const void *x, long long x_stride, const void *d
                 ws_bytes);
   if (workspace && !aligned16(workspace))
     return fail(LA_ERR_INVALID_ARG, "%s: workspace must be 16-byte aligned", fn);
+  const Rows ws = dense(workspace, need);
+  if (overlap(ws, yr) || overlap(ws, s0) || overlap(ws, s1) || overlap_any(ws, in) || overlap_any(ws, par))
+    return fail(LA_ERR_INVALID_ARG, "%s: the workspace overlaps an input or an output", fn);
   ScanArgs a{x, dt, z, Bm, Cm, x_stride, dt_stride, z_stride, b_stride, c_stride, dtype, B, L,
              D, N, groups, A, dt_bias, dt_softplus, skip, h0, lengths, y, y_stride, h_final,
              need ? workspace : nullptr, st};
@@ -597,7 +617,10 @@ la_status la_gated_norm_fwd(const void *x, long long x_b_stride, long long x_h_s
       (L == 1 || x_t_stride >= width))
     xr = {x, rows, width, rows == 1 ? width : L == 1 ? x_b_stride : x_t_stride,
           elt};  // token-major rows, which may be a slice
-  if (overlap(yr, xr) || (!(y == gate && y_stride == gate_stride) && overlap(yr, gr)))
+  const Rows par[] = {params(weight, (long long)weight_heads * d),
+                      params(bias, (long long)weight_heads * d)};
+  if (overlap(yr, xr) || (!(y == gate && y_stride == gate_stride) && overlap(yr, gr)) ||
+      overlap_any(yr, par))
     return fail(LA_ERR_INVALID_ARG, "%s: y overlaps an input", fn);
   GatedNormArgs a{x, x_b_stride, x_h_stride, x_t_stride, gate, gate_stride, dtype, B, H, L, d,
                   norm, activation, gate_first, weight, bias, weight_heads, eps, y, y_stride,
@@ -634,8 +657,11 @@ la_status la_residual_norm_fwd(const void *x, int dtype, const void *residual, i
     return fail(LA_ERR_INVALID_ARG, "%s: parameters must be 16-byte aligned", fn);
   const Rows xr = dense(x, rows * D * elt), yr = dense(y, rows * D * elt);
   const Rows rr = dense(residual, rows * D * relt), ro = dense(residual_out, rows * D * relt);
+  const Rows par[] = {params(post_weight, D), params(scale, D), params(weight, D),
+                      params(bias, D)};
   if ((y != x && overlap(yr, xr)) || overlap(yr, rr) || overlap(yr, ro) || overlap(ro, xr) ||
-      (residual_out != residual && overlap(ro, rr)))
+      (residual_out != residual && overlap(ro, rr)) || overlap_any(yr, par) ||
+      overlap_any(ro, par))
     return fail(LA_ERR_INVALID_ARG, "%s: an output overlaps an input or the other output", fn);
   ResidualNormArgs a{x, dtype, residual, res_dtype, rows, D, post_weight, scale, alpha, weight,
                      bias, norm, eps, y, residual_out, static_cast<cudaStream_t>(cuda_stream)};

@@ -278,8 +278,9 @@ la_status la_delta_fwd(const void *q, const void *k, const void *v, int dtype,
  *             bound).  Rows behind them are neither read nor written, and the
  *             final state is the state after lengths[b] tokens.
  *
- * Outputs may not overlap inputs, except as stated: a final state may be the
- * buffer of its initial state, so that L = 1 is a decode step in place.
+ * Outputs may not overlap inputs, parameters and lengths among them, nor a
+ * workspace anything, except as stated: a final state may be the buffer of its
+ * initial state, so that L = 1 is a decode step in place.
  * Errors: LA_ERR_INVALID_ARG (null, misaligned or overlapping pointer,
  * negative size, stride shorter than a row, unknown enum, workspace too
  * small), LA_ERR_UNSUPPORTED (a size outside the stated range), LA_ERR_CUDA.
