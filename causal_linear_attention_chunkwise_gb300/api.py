@@ -333,6 +333,13 @@ _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                           lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
+_INT_MAX = 2 ** 31 - 1  # sizes cross the C ABI as int, which ctypes would cut silently
+
+
+def _too_large(*sizes):
+    return ValueError(f"a size above 2^31 - 1 among {list(sizes)}")
+
+
 def _param(t, shape, what):
     if t.dtype != torch.float32 or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous fp32 {list(shape)}")
@@ -385,6 +392,8 @@ def la_causal_conv_fwd(x, weight, bias=None, activation="silu", state0=None, len
     shape, dtype = x.shape, x.dtype
     B, L, D = shape
     W = weight.shape[-1]
+    if max(B, L, D, W) > _INT_MAX:
+        raise _too_large(B, L, D, W)
     xs = D if x.is_contiguous() else _row_stride(x, shape, dtype, "x")
     w = _param(weight, (D, W), "weight")
     bi = None if bias is None else _param(bias, (D,), "bias")
@@ -433,6 +442,8 @@ def la_selective_scan_fwd(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, dt_sof
     G = bc[2] if len(bc) == 4 else 1
     if bc != ((B, L, G, N) if len(bc) == 4 else (B, L, N)):
         raise ValueError("Bm must be [B,L,N] or [B,L,groups,N]")
+    if max(B, L, ch, N, G) > _INT_MAX:
+        raise _too_large(B, L, ch, N, G)
     xs = _row_stride(x, shape, dtype, "x")
     ds = _row_stride(dt, shape, dtype, "dt")
     zs = 0 if z is None else _row_stride(z, shape, dtype, "z")
@@ -492,6 +503,8 @@ def la_gated_norm_fwd(x, gate=None, weight=None, bias=None, norm="rms", activati
     xb, xh, xt, x1 = x.stride()
     if x1 != 1 and d > 1 and x.numel() > 0:
         raise ValueError("the last axis of x must be contiguous")
+    if max(B, H, L, d) > _INT_MAX:
+        raise _too_large(B, H, L, d)
     width = H * d
     shape = (B, L, width)
     heads = 1
@@ -537,6 +550,8 @@ def la_residual_norm_fwd(x, residual=None, weight=None, bias=None, post_weight=N
     ``residual_out`` may be ``residual``."""
     shape, dtype = x.shape, x.dtype
     D = shape[-1]
+    if D > _INT_MAX:
+        raise _too_large(D)
     rd = residual.dtype if residual is not None else \
         residual_out.dtype if residual_out is not None else residual_dtype or dtype
     per = (D,)

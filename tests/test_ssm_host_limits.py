@@ -4,8 +4,9 @@ which is refused before any launch (status 3)."""
 import os
 
 import pytest
+import torch
 
-from causal_linear_attention_chunkwise_gb300 import _native, build
+from causal_linear_attention_chunkwise_gb300 import _native, api, build
 from tests.test_ssm_host import P, _conv, _gated, _resid, _scan
 
 FAR = 1 << 60  # behind every range of these calls; never dereferenced
@@ -93,3 +94,29 @@ def test_interleaved_slices_are_accepted(lib):
     assert _gated(lib, y=P + 1024, **gated) == 3, lib.la_last_error()
     for y in (P + 1022, P + 1026):
         assert _gated(lib, y=y, **gated) == 1 and b"overlaps" in lib.la_last_error()
+
+
+# ---------------------------------------------------------------- sizes
+def test_binding_refuses_sizes_past_32_bits():
+    """Without memory behind them ("meta"): cut to 32 bits, these would be small calls."""
+    new = lambda *s: torch.empty(s, device="meta")  # noqa: E731
+    big = (1 << 32) + 3
+    for B, L, D in [(big, 1, 4), (1, big, 4), (1, 1, big)]:
+        x = new(B, L, D)
+        with pytest.raises(ValueError, match="2.31"):
+            api.la_causal_conv_fwd(x, new(D, 4))
+        with pytest.raises(ValueError, match="2.31"):
+            api.la_selective_scan_fwd(x, x, new(D, 2), new(B, L, 2), new(B, L, 2))
+        with pytest.raises(ValueError, match="2.31"):
+            api.la_gated_norm_fwd(x[:, None])
+    x = new(2, 3, 4)
+    with pytest.raises(ValueError, match="2.31"):
+        api.la_causal_conv_fwd(x, new(4, big))
+    with pytest.raises(ValueError, match="2.31"):
+        api.la_selective_scan_fwd(x, x, new(4, big), new(2, 3, big), new(2, 3, big))
+    with pytest.raises(ValueError, match="2.31"):
+        api.la_selective_scan_fwd(x, x, new(4, 2), new(2, 3, big, 2), new(2, 3, big, 2))
+    with pytest.raises(ValueError, match="2.31"):
+        api.la_gated_norm_fwd(new(1, big, 2, 4))
+    with pytest.raises(ValueError, match="2.31"):
+        api.la_residual_norm_fwd(new(1, big))
