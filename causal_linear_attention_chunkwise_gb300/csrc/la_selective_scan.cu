@@ -201,6 +201,20 @@ template <int PENDING> __device__ __forceinline__ void fetch_wait() {
 // apart, write to different banks, and neighbouring lanes read neighbours.
 __device__ __forceinline__ int slot_granule(int g) { return g ^ (g >> 3 & 3); }
 
+// The state behind a segment that starts in h: exp2(a sum) h + end, end being the
+// segment's end state from zero.  Where a state grows (a sum > 0) the factor may
+// pass fp32's range although its product with a small h or with 0 does not: it
+// is then applied in three parts.  A state that does not decay (a = 0) stays h
+// where the sum is infinite.
+__device__ __forceinline__ float after_segment(float h, float a, float sum, float end) {
+  const float e = a * sum;
+  if (e <= 120.f) return fmaf(ex2_approx(e), h, end);
+  if (a == 0.f) return h + end;
+  if (h == 0.f) return end;
+  const float third = ex2_approx(e * (1.f / 3.f));
+  return fmaf(third, third * (third * h), end);
+}
+
 // One block's share of one segment.  FULL: outputs from the state `from` the
 // segment starts in; else only its end state, from zero, and its sum of delta.
 template <typename T, int P, int S, int NC, int ALIGN, bool FULL>
@@ -386,8 +400,9 @@ __device__ __forceinline__ void scan_segment(const ScanParams<T> &p, long long b
           } else {
             hv[e] = p.seg_state[at + n];
             for (int i = 1; i < seg; ++i)
-              hv[e] = fmaf(ex2_approx(av[e] * p.seg_sum[((long long)i * p.B + b) * p.D + ch]),
-                           hv[e], p.seg_state[i * pitch + at + n]);
+              hv[e] = after_segment(hv[e], av[e],
+                                    p.seg_sum[((long long)i * p.B + b) * p.D + ch],
+                                    p.seg_state[i * pitch + at + n]);
           }
         }
       }

@@ -60,6 +60,52 @@ def test_scan_infinite_steps_stay_in_their_channel(L):
     assert (~torch.isfinite(h)).any(-1).nonzero().tolist() == [[0, 7]]
 
 
+# ---------------------------------------------------------------- growth over segments
+def _segment(B, L, ch, N):
+    """Tokens in a segment of the scan's plan, from the size of its workspace."""
+    need = api.la_selective_scan_fwd_workspace_bytes(B, L, ch, N)
+    nseg = need // (4 * B * ch * (N + 1)) + 1
+    assert nseg > 3
+    return ((L + nseg - 1) // nseg + 15) // 16 * 16
+
+
+def test_scan_states_that_grow_over_a_segment():
+    """exp(delta A) over a whole segment passes fp32's range although every state stays in it:
+    66 steps of exponent 1.5 take 1e-30 to 1e13 in the third segment.  Tokens and states of zeros
+    stay zeros."""
+    B, L, ch, N = 1, 1500, 24, 16
+    seg = _segment(B, L, ch, N)
+    assert seg >= 66
+    i = scan_inputs(B, L, ch, N, 1, "f32", gate=False, skip=False)
+    i["dt_bias"] = None
+    i["dt"][:] = 0
+    i["dt"][:, 2 * seg:2 * seg + 66] = 0.25
+    i["x"][:] = 0
+    i["A"][:] = 6.0
+    i["h0"][:] = 1e-30 * i["h0"]
+    i["h0"][:, ::2] = 0
+    y, h = scan(i, dt_softplus=False)
+    ref, href = scan_reference(i, "f32", softplus=False)
+    assert href[0].max() > 1e12
+    R.check(y, ref, "y")
+    R.check(h, href, "h_final")
+    assert (y[..., ::2] == 0).all() and (h[:, ::2] == 0).all()
+
+
+def test_scan_sum_of_steps_past_fp32():
+    """The steps of a segment sum to infinity: a decaying state ends at 0, one that does not
+    decay (A = 0) stays."""
+    B, L, ch, N = 1, 1500, 24, 16
+    seg = _segment(B, L, ch, N)
+    i = scan_inputs(B, L, ch, N, 1, "f32", gate=False, skip=False)
+    i["x"][:] = 0
+    i["dt"][:, 2 * seg + 3:2 * seg + 6] = torch.finfo(torch.float32).max
+    i["A"][::2] = 0
+    y, h = scan(i)
+    assert torch.equal(h[:, ::2], i["h0"][:, ::2]) and (h[:, 1::2] == 0).all()
+    assert torch.isfinite(y).all() and (y[:, 3 * seg:, 1::2] == 0).all()
+
+
 # ---------------------------------------------------------------- sizes
 def test_scan_token_of_more_channels_than_32_bits_of_lanes():
     """2^27 + 64 channels of 65 states, 32 lanes to a channel; the states in place.  With A = 0,
