@@ -7,7 +7,7 @@ import torch
 
 from causal_linear_attention_chunkwise_gb300 import _native, api
 from tests import ssm_reference as R
-from tests.test_gpu_ssm import DT, scan, scan_inputs, scan_reference
+from tests.test_gpu_ssm import DT, _live, scan, scan_inputs, scan_reference
 
 pytestmark = pytest.mark.gpu
 
@@ -58,6 +58,45 @@ def test_scan_infinite_steps_stay_in_their_channel(L):
     want[0, t:, 7] = True
     assert torch.equal(~torch.isfinite(y).cpu(), want)
     assert (~torch.isfinite(h)).any(-1).nonzero().tolist() == [[0, 7]]
+
+
+def test_gates_at_the_ends_of_their_range_touch_their_element_alone():
+    """A gate of the lowest value is a factor of 0, a NaN or an infinity leaves one element."""
+    i = scan_inputs(1, 20, 40, 16, 1, "f32")
+    y0, h0 = scan(i)
+    z = i["z"].clone()
+    z[0, 3, 1], z[0, 4, 2], z[0, 5, 3] = torch.finfo(torch.float32).min, float("nan"), INF
+    y, h = scan(dict(i, z=z))
+    assert y[0, 3, 1] == 0 and torch.isnan(y[0, 4, 2]) and not torch.isfinite(y[0, 5, 3])
+    o0 = api.la_gated_norm_fwd(i["x"][:, None], i["z"])
+    o = api.la_gated_norm_fwd(i["x"][:, None], z)
+    assert o[0, 3, 1] == 0 and torch.isnan(o[0, 4, 2]) and not torch.isfinite(o[0, 5, 3])
+    rest = torch.ones(20, 40, dtype=torch.bool, device="cuda")
+    rest[3, 1] = rest[4, 2] = rest[5, 3] = False
+    assert torch.equal(y[0, rest], y0[0, rest]) and torch.equal(h, h0)
+    assert torch.equal(o[0, rest], o0[0, rest])
+
+
+# ---------------------------------------------------------------- groups
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,L,ch,N,G,packed,ragged", [
+    (2, 40, 272, 16, 2, False, False),    # 136 channels a group: three blocks, 16-byte rows
+    (2, 40, 150, 24, 2, False, False),    # 75: no vector divides it
+    (2, 40, 300, 10, 2, True, False),     # 150: rows on 4-byte boundaries at best
+    (2, 33, 520, 4, 2, False, False),
+    (2, 20, 120, 128, 3, False, False),
+    (1, 18, 99, 256, 3, False, False),
+    (6, 1200, 400, 16, 4, False, True),   # segments too
+    (1, 900, 264, 32, 3, True, False),
+])
+def test_scan_groups_of_several_blocks(B, L, ch, N, G, packed, ragged, dtype):
+    i = scan_inputs(B, L, ch, N, G, dtype, packed, ragged=ragged)
+    if L > 100:
+        assert api.la_selective_scan_fwd_workspace_bytes(B, L, ch, N, G) > 0
+    y, h = scan(i)
+    ref, href = scan_reference(i, dtype)
+    R.check(y, ref, "y", _live(i["lengths"], B, L))
+    R.check(h, href, "h_final")
 
 
 # ---------------------------------------------------------------- growth over segments
@@ -127,6 +166,57 @@ def test_scan_token_of_more_channels_than_32_bits_of_lanes():
     for part, want in zip(h.split(1 << 24, 1), u[0, 0].float().split(1 << 24)):
         assert (part[0] == want[:, None]).all()
     del h, part
+    torch.cuda.empty_cache()
+
+
+def test_scan_offsets_past_32_bits():
+    """The last tokens of the last sequence, behind 2^31 elements; a step of 1e30 in front of them
+    leaves nothing of the tokens before."""
+    B, L, ch, N, last = 2, 1 << 18, 1 << 13, 4, 40
+    torch.cuda.empty_cache()
+    tail = scan_inputs(1, last, ch, N, 1, "bf16", gate=False, state=False)
+    x = torch.zeros(B, L, ch, dtype=torch.bfloat16, device="cuda")
+    dt, bc = torch.zeros_like(x), torch.zeros(B, L, 2, N, dtype=torch.bfloat16, device="cuda")
+    dt[:, -last - 1] = 1e30
+    x[1, -last:], dt[1, -last:] = tail["x"][0], tail["dt"][0]
+    bc[1, -last:, 0], bc[1, -last:, 1] = tail["Bm"][0], tail["Cm"][0]
+    y = torch.zeros_like(x)
+    args = dict(tail, x=x, dt=dt, Bm=bc[:, :, 0], Cm=bc[:, :, 1])
+    ref, href = scan_reference(tail, "bf16")
+    for segments in (True, False):
+        _, h = scan(args, y=y, segments=segments)
+        R.check(y[1:, -last:], ref, "y")
+        R.check(h[1:], href, "h_final")
+        y.zero_()
+    del x, dt, y, args
+    torch.cuda.empty_cache()
+
+
+def test_tokens_of_more_sequences_than_32_bits_of_elements():
+    """One token for each of 2^19 sequences of 2^13 channels: 2^32 states, in place."""
+    B, ch, k = 1 << 19, 1 << 13, 3
+    torch.cuda.empty_cache()
+    tail = scan_inputs(k, 1, ch, 1, 1, "bf16")
+    grow = lambda t: torch.zeros(B, *t.shape[1:], dtype=t.dtype, device="cuda")  # noqa: E731
+    full = dict(tail)
+    for name in ("x", "dt", "z", "Bm", "Cm", "h0"):
+        full[name] = grow(tail[name])
+        full[name][-k:] = tail[name]
+    y = grow(tail["x"])
+    ref, href = scan_reference(tail, "bf16")
+    scan(full, y=y, h_final=full["h0"])
+    R.check(y[-k:], ref, "y")
+    R.check(full["h0"][-k:], href, "h_final")
+    x = full["x"]
+    del full
+    weight = torch.randn(ch, 2, generator=torch.Generator().manual_seed(50)).cuda()
+    state = torch.zeros(B, 1, ch, dtype=torch.bfloat16, device="cuda")
+    state[-k:] = tail["z"]
+    api.la_causal_conv_fwd(x, weight, state0=state, state_final=state, y=y)
+    ref, _ = R.causal_conv(tail["x"], weight, None, "silu", tail["z"], None, "bf16")
+    R.check(y[-k:], ref, "conv")
+    assert torch.equal(state[-k:], tail["x"])
+    del x, y, state
     torch.cuda.empty_cache()
 
 
