@@ -27,7 +27,8 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-// 1 / (1 + e^-x): e^-x overflows to infinity for x < -88, whose reciprocal is 0.
+// 1 / (1 + e^-x), off by at most some 2^-21 relative above x = -87.3.  Below, the
+// result has no normal fp32 number and is 0 (e^-x overflows from -88 on).
 __device__ __forceinline__ float sigmoid(float x) {
   return rcp_approx(1.f + ex2_approx(-x * kLog2e));
 }

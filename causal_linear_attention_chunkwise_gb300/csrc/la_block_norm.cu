@@ -131,8 +131,8 @@ __device__ __forceinline__ void load_params(const float *p, float *f) {
   }
 }
 
-// Five blocks of teams per SM: 4 x 16 x 4096 x 64 takes 23.4 us, with four 23.7,
-// with six (spills) 27.
+// Five blocks of teams per SM (48 registers, 8 to 32 bytes of them spilled): 4 x
+// 16 x 4096 x 64 takes 23.4 us, with four 23.7, with six 27.
 template <typename T, int V, int LANES, int I, int ACT, int MAXT>
 __global__ void __launch_bounds__(MAXT, LANES && V > 2 && I <= 2 ? 5 : 1)
 gated_norm_kernel(const GatedNormArgs a, long long rows) {
@@ -397,7 +397,10 @@ residual_norm_kernel(const ResidualNormArgs a) {
 // width d in vectors of V elements: as few lanes as hold the row in two vectors
 // each, up to a warp; then (FOUR) a warp with four, up to a width of 1024; then a
 // block whose threads hold kBlockVecs<V> vectors.  The residual step has no
-// registers for four: 16384 x 1024 bf16 takes 33 us with them, 29 in blocks.
+// registers for four: 16384 x 1024 bf16 with a bf16 residual takes 27.2 us with
+// them, 24.4 in blocks (fp32 residual: 35.1 and 32.8).  Its blocks of more than
+// 512 threads (rows above 8192) have 64 registers a thread and spill 216 to 426
+// bytes: 2000 x 15001 fp32 takes 124 us, 1.8 times its bytes.
 template <int V> constexpr int kBlockVecs = V == 8 ? 2 : V == 4 ? 4 : V == 2 ? 8 : 16;
 template <int N> struct Int { static constexpr int value = N; };
 
@@ -465,7 +468,9 @@ cudaError_t launch_residual_v(const ResidualNormArgs &a) {
 bool fits(const void *p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 
 // The rows are read in the widest vectors that their alignment allows: 16
-// bytes, two elements, or one.
+// bytes, two elements, or one.  2 x 1 x 2048 x 4096 bf16 takes 23.5 us; 4098 in
+// pairs 35, element by element 46; 4097 46.5.  Short rows gain nothing from pairs:
+// 4 x 8 x 2000 x 82 takes 23 us either way (a warp to a row in both; 80: 10.8).
 template <typename T>
 cudaError_t launch_gated_t(const GatedNormArgs &a) {
   auto rows_fit = [&](int v) {  // the strides of axes of one element are never used
@@ -485,7 +490,8 @@ cudaError_t launch_gated_t(const GatedNormArgs &a) {
 }
 
 // Rows on 16-byte boundaries, rows anywhere in tensors that start on one, or
-// element by element.
+// element by element (16384 x 4096 bf16: 86 us, and 200 where one tensor starts
+// off a boundary).
 template <typename T, typename R>
 cudaError_t launch_residual_t(const ResidualNormArgs &a) {
   constexpr int V = Pack16<T>::N;

@@ -23,7 +23,8 @@ namespace {
 constexpr int kThreads = 256;
 // Tokens per batch, and the bytes a thread loads of each.  4 x 4096 x 4096 bf16
 // (x a slice of rows twice as wide): 8 bytes in batches of 8, 55 us; 16 bytes
-// in batches of 4 or 8, 55 and 61; 8 bytes in batches of 4, 62.
+// in batches of 4 or 8, 55 and 61; 8 bytes in batches of 4, 62.  The batches in
+// flight are held in registers: 114 a thread, two blocks per SM.
 constexpr int kBatch = 8, kVecBytes = 8;
 
 // 1 << lane_bits threads lie side by side in channels; runs of `batches` batches.
@@ -152,7 +153,11 @@ cudaError_t launch_run(const ConvArgs &a) {
   while (lane_bits > 0 && 1 << (lane_bits - 1) >= nv) --lane_bits;
   // Runs as long as they leave the GPU full (some 150,000 threads at a time):
   // each reads W - 1 rows twice and starts with nothing in flight.  The case
-  // above: runs of 16, 32, 64, 128 tokens in 69, 58, 58, 55 us.
+  // above: runs of 16, 32, 64, 128 tokens in 69, 58, 58, 55 us.  The limit of
+  // 100e3 threads against 50e3, 200e3 and 400e3, W = 4, in us:
+  //   1 x 4096 x 4096 bf16   17.8, 16.7, 20.7, 25.2    fp32  28.2, 27.8, 25.6, 26.0
+  //   16 x 512 x 1024 bf16   12.9, 11.5, 15.1, 15.0    fp32  17.1, 16.8, 16.5, 17.7
+  //   4 x 4096 x 4096 bf16   53.2, 52.8, 55.8, 56.0    fp32  97.0, 96.7, 88.7, 86.6
   int batches = 1;
   auto threads = [&](int m) { return (double)a.B * nv * ((a.L + m * BATCH - 1) / (m * BATCH)); };
   while (batches < 32 && threads(2 * batches) >= 100e3) batches *= 2;
@@ -170,7 +175,9 @@ cudaError_t launch_run(const ConvArgs &a) {
 
 template <typename T, int W>
 cudaError_t launch_w(const ConvArgs &a) {
-  // The widest vectors, up to 8 bytes, that every row's alignment allows.
+  // The widest vectors, up to 8 bytes, that every row's alignment allows (4 x
+  // 4096 x 4096 bf16 52 us; 4098 wide in pairs 54, element by element 73; 4097
+  // wide 74).  One token's call is a launch, pairs or not.
   auto rows_fit = [&](int v) {
     auto fits = [&](const void *p) {
       return reinterpret_cast<uintptr_t>(p) % (v * sizeof(T)) == 0;

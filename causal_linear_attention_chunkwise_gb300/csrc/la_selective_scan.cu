@@ -25,7 +25,7 @@
 // special-function unit for the exps (32 lanes a clock on an SM) and 16 of the
 // fp32 pipe (128 lanes a clock; 22 as three-operand packed instructions issue).
 // Both floors are 57 us for 4 x 2048 x 4096 (N = 16, bf16; its bytes take 40): it
-// runs 184 us, and 1 x 16384 x 2048 276 us.  The counters show no unit full
+// runs 185 us, and 1 x 16384 x 2048 280 us.  The counters show no unit full
 // (issue slots and shared-memory wavefronts about 70% on an SM with two
 // blocks): the recurrence warps' own instruction stream sets the pace, and taking
 // out staging work (softplus, gate, address arithmetic) does not change the time.
@@ -587,10 +587,13 @@ selective_scan_kernel(const ScanParams<T> p, int pass) {
 // A thread takes R <= S sequences, whose loads are all in flight at once and
 // which share its A; the scalars of sequence r (delta, delta x, and the output)
 // are worked out by the channel's lane r and passed on by shuffles.  256
-// sequences of 4096 x 16 states, one token, bf16: 33 us, 4.4 TB/s; with four
-// blocks per SM instead of five 38, two sequences a thread 42, one 59, packed
-// fp32 pairs 42.  Latency bounds it: the loads of a thread's sequences leave
-// together, but registers limit the threads.
+// sequences of 4096 x 16 states, one token: bf16 32 us, 4.5 TB/s, fp32 37; with
+// one sequence a thread 47 and 53; when it took 33, with four blocks per SM
+// instead of five 38, two sequences a thread 42, packed fp32 pairs 42.  Latency
+// bounds it: the loads of a thread's sequences leave together and wait in
+// registers, which limits the threads (48 registers with 48 to 60 bytes spilled
+// in bf16's aligned form of one token, 64 with 56 to 72 in fp32's; 64 with 16
+// and 144 for more tokens, whose loads all wait for the token before).
 template <typename T, int P, int S, int R, bool VEC, bool ONE>
 __global__ void __launch_bounds__(256, ONE && sizeof(T) == 2 && P == 4 ? 5 : 4)
 selective_step_kernel(const ScanParams<T> p, unsigned blocks) {  // blocks: per row of sequences
@@ -751,7 +754,9 @@ cudaError_t launch_step(const ScanParams<T> &p, cudaStream_t stream) {
   const bool vec = p.N % 4 == 0 && p.b_stride % 4 == 0 && p.c_stride % 4 == 0 && fits(p.Bm) &&
                    fits(p.Cm);
   const long long blocks = ((long long)p.D * S + 255) / 256;
-  // R sequences a thread once there are enough threads without them.
+  // R sequences a thread once there are enough threads without them, against one
+  // (bf16, one token, us): 38 x 4096 x 16 states 7.0 and 9.0, 64 x 4096 x 16 11.1
+  // and 13.8, 16 x 4096 x 128 19.4 and 24.7.
   const bool many = (double)p.B / R * p.D * S >= 152 * 1024;
   const long long rows = many ? (p.B + R - 1ll) / R : p.B;
   if (blocks * rows > 0x7fffffffll) return cudaErrorInvalidConfiguration;
@@ -781,8 +786,15 @@ cudaError_t launch_steps(const ScanParams<T> &p, cudaStream_t stream) {
 // Channels per block, by the number of states.
 constexpr int block_channels(int N) { return N <= 4 ? 128 : N <= 16 ? 64 : N <= 32 ? 32 : 16; }
 
-// Up to this many tokens the step kernel runs: 64 x L x 4096 (N = 16, bf16) takes
-// 22 us at L = 4, 39 at 8, 72 at 16; the tiled kernel 49 at 8 and 51 at 16.
+// Up to this many tokens the step kernel runs.  It and the tiled kernel, us:
+//                                L = 2      4          8          16
+//   64 x L x 4096, N 16, bf16    15, 40     22, 41     37, 45     67, 49
+//                        fp32    17, 36     26, 39     43, 41     77, 50
+//   16 x L x 4096, N 16, bf16    7.4, 13    11, 13     18, 14     31, 15
+//    1 x L x 4096, N 16, bf16    2.2, 3.1   3.0, 3.1   4.5, 3.4   7.8, 4.0
+//   64 x L x 4096, N 128, bf16   84, 241    133, 254   236, 270   443, 328
+//                        fp32    104, 235   164, 250   288, 267   541, 322
+// The crossing lies between 4 and 16 tokens; one limit serves all sizes.
 constexpr int kStepTokens = 8;
 
 struct ScanPlan {
@@ -790,13 +802,20 @@ struct ScanPlan {
 };
 
 // How many segments.  One block on an SM takes a token in about 50 ns, two in
-// 90 (N = 16, bf16: 1 x 16384 x 2048 in one piece 815 us, 4 x 2048 x 4096 184
+// 90 (N = 16, bf16: 1 x 16384 x 2048 in one piece 878 us, 4 x 2048 x 4096 185
 // us), and the SMs hold two, so n blocks take rounds(n) ns per token of theirs.  One
 // piece costs that over L tokens; nseg > 1 segments cost it twice, for nseg - 1
 // segments side by side, over L / nseg tokens, and a launch.  1 x 16384 x 2048
-// (32 blocks): 815 us in one piece, 420 us in 4, 276 in 10 (the first that
-// fills both blocks of all SMs), 322 in 12 (a round and a bit), 275 in 20.
-// 4 x 2048 x 4096 (256 blocks) is fastest in one piece: 184 us, 230 in 3.
+// (32 blocks): 444 us in 4, 277 in 10 (the first that fills both blocks of all
+// SMs), 325 in 12 (a round and a bit), 292 in 20.  4 x 2048 x 4096 (256 blocks) is
+// fastest in one piece: 185 us, 228 in 3.  The same prices serve every N and
+// type, and sequences count as full whatever their lengths are.  In segments and
+// in one piece, us:
+//   1 x 512 x 512, N 16, 8 segments      bf16 17.5, 29.5   fp32 18.7, 33.8
+//   2 x 2048 x 2048, N 16, 3             bf16 82, 113      fp32 93, 128
+//   1 x 4096 x 2048, N 4, 20             bf16 76, 418      fp32 63, 326
+//   1 x 4096 x 1024, N 64, 3             bf16 173, 253     fp32 144, 206
+//   1 x 4096 x 1024, N 128, 3            bf16 351, 512     fp32 285, 411
 ScanPlan make_plan(int B, int L, int D, int N, int groups) {
   constexpr int kSMs = 152, kMinLen = 64, kMaxSeg = 64;
   const int CH = block_channels(N);
