@@ -75,7 +75,7 @@ def la_chunk_fwd_kernel_count(B, H, L, d_k, d_v, chunk=64, dtype=torch.bfloat16)
 def _new(shape, dtype, device, stream, zero=False):
     """A tensor on the stream that the call runs on."""
     make = torch.zeros if zero else torch.empty
-    if stream is None:
+    if stream is None or stream.cuda_stream == _current_stream(device.index):
         return make(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
         return make(shape, dtype=dtype, device=device)
