@@ -383,7 +383,8 @@ size_t la_selective_scan_fwd_workspace_bytes(int B, int L, int D, int N, int gro
  *   y            [B,L,H*d] dtype, rows y_stride apart; may be gate's buffer
  *                when y_stride = gate_stride
  *
- * Supported: d in 1..16384.
+ * Supported: d in 1..16384.  Squares are summed in fp32, here and in
+ * la_residual_norm_fwd: a row with values above 1e19 gives zeros.
  */
 la_status la_gated_norm_fwd(const void *x, long long x_b_stride, long long x_h_stride,
                             long long x_t_stride, const void *gate, long long gate_stride,
