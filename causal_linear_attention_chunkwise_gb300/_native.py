@@ -12,7 +12,9 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_lib", "lib
 
 # Symbols the header declares, with (restype, argtypes).
 _vp, _i, _u, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_uint, ctypes.c_size_t
-_ll, _f = ctypes.c_longlong, ctypes.c_float
+_ll, _f, _d = ctypes.c_longlong, ctypes.c_float, ctypes.c_double
+_ROTARY = [_vp, _ll, _ll, _ll, _i, _vp, _ll, _ll, _ll, _i, _i, _i, _i, _i, _i, _i, _vp, _f, _vp,
+           _vp, _vp, _vp, _ll, _ll, _ll, _vp, _ll, _ll, _ll, _vp]
 SIGNATURES = {
     "la_set_feature_map": (_i, [_i]),
     "la_get_feature_map": (_i, []),
@@ -44,6 +46,19 @@ SIGNATURES = {
                                _vp, _vp, _i, _f, _vp, _ll, _vp]),
     "la_residual_norm_fwd": (_i, [_vp, _i, _vp, _i, _ll, _i, _vp, _vp, _f, _vp, _vp, _i, _f,
                                   _vp, _vp, _vp]),
+    "la_rotary_frequencies": (_i, [_i, _d, _i, _d, _d, _d, _d, _vp, _vp]),
+    "la_rotary_fwd": (_i, _ROTARY),
+    "la_rotary_bwd": (_i, _ROTARY),
+    "la_chunk_bwd": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp,
+                          _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "la_chunk_bwd_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i, _i]),
+    "la_gated_norm_bwd": (_i, [_vp, _ll, _vp, _ll, _ll, _ll, _vp, _ll, _i, _i, _i, _i, _i, _i, _i,
+                               _i, _vp, _vp, _i, _f, _vp, _ll, _ll, _ll, _vp, _ll, _vp, _vp, _vp,
+                               _sz, _vp]),
+    "la_gated_norm_bwd_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
+    "la_residual_norm_bwd": (_i, [_vp, _i, _vp, _vp, _i, _vp, _ll, _i, _vp, _vp, _f, _vp, _i, _f,
+                                  _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "la_residual_norm_bwd_workspace_bytes": (_sz, [_ll, _i]),
     "la_device_status": (_i, [_vp]),
     "la_selftest_wait_timeout": (_i, [_u, _vp]),
     "la_last_error": (ctypes.c_char_p, []),

@@ -17,6 +17,7 @@ DTYPE = {torch.float32: 0, torch.bfloat16: 1}
 DECAY = {"none": 0, "head": 1, "token": 2, "logit": 3}
 ACT = {"none": 0, "silu": 1, "sigmoid": 2}
 NORM = {"rms": 0, "layer": 1}
+ROTARY = {"plain": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
 LA_OK, LA_ERR_INVALID_ARG, LA_ERR_UNSUPPORTED, LA_ERR_CUDA, LA_ERR_DEVICE_TIMEOUT = range(5)
 
@@ -576,6 +577,291 @@ def la_residual_norm_fwd(x, residual=None, weight=None, bias=None, post_weight=N
     if status:
         _check(status)
     return y, residual_out
+
+
+# ---------------------------------------------------------------- training pass
+def la_rotary_frequencies(rotary_dim, base=10000.0, scaling="plain", factor=1.0,
+                          trained_length=0.0, fast=32.0, slow=1.0):
+    """Rotary frequencies ``(inv_freq, scale)``: fp32 [rotary_dim/2] in host memory
+    (``.cuda()`` them once) and the factor of q and k.  ``scaling``: "plain" |
+    "linear" (positions interpolated by ``factor``) | "ntk" (a larger base) |
+    "yarn" (pairs of fewer than ``slow`` turns over ``trained_length`` interpolated,
+    those of more than ``fast`` left, a blend between)."""
+    inv_freq = torch.empty(max(rotary_dim // 2, 0), dtype=torch.float32)
+    scale = torch.empty(1, dtype=torch.float32)
+    _check(_native.load().la_rotary_frequencies(
+        rotary_dim, base, ROTARY[scaling], factor, trained_length, fast, slow,
+        inv_freq.data_ptr(), scale.data_ptr()))
+    return inv_freq, scale.item()
+
+
+def _int32(t, shape, what):
+    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous int32 {list(shape)}")
+    return t.data_ptr()
+
+
+def _heads(t, shape, dtype, what):
+    """Address and strides of ``t`` = [B,H,L,d] whose last axis is contiguous."""
+    if t.shape != shape or t.dtype != dtype:
+        raise ValueError(f"{what} must be {dtype} {list(shape)}")
+    b, h, n, one = t.stride()
+    if one != 1 and shape[3] > 1 and t.numel() > 0:
+        raise ValueError(f"the last axis of {what} must be contiguous")
+    return t.data_ptr(), b, h, n
+
+
+_NO_HEADS = (None, 0, 0, 0)
+
+
+def _rotary(fn, q, k, inv_freq, positions, offsets, lengths, interleaved, scale, q_out, k_out,
+            stream):
+    shape, dtype = q.shape, q.dtype
+    B, H, L, d = shape
+    k_shape = None if k is None else k.shape
+    if k is not None and (len(k_shape) != 4 or k_shape[0] != B or k_shape[2:] != shape[2:]):
+        raise ValueError("q and k must agree in [B,.,L,d]")
+    Hk = 0 if k is None else k_shape[1]
+    if max(B, H, Hk, L, d) > _INT_MAX:
+        raise _too_large(B, H, Hk, L, d)
+    qa = _heads(q, shape, dtype, "q")
+    ka = _NO_HEADS if k is None else _heads(k, k_shape, dtype, "k")
+    pairs = inv_freq.numel()
+    f = _param(inv_freq, (pairs,), "inv_freq")
+    ps = None if positions is None else _int32(positions, (B, L), "positions")
+    of = None if offsets is None else _int32(offsets, (B,), "offsets")
+    n = None if lengths is None else _int32(lengths, (B,), "lengths")
+    if k is None and k_out is not None:
+        raise ValueError("k_out without k")
+    dev = _device_of(q, k, inv_freq, positions, offsets, lengths, q_out, k_out)
+    zero = lengths is not None
+    if q_out is None:
+        q_out = _new(shape, dtype, q.device, stream, zero)
+    if k is not None and k_out is None:
+        k_out = _new(k_shape, dtype, q.device, stream, zero)
+    status = getattr(_native.load(), fn)(
+        *qa, H, *ka, Hk, DTYPE[dtype], B, L, d, 2 * pairs, interleaved, f, scale, ps, of, n,
+        *_heads(q_out, shape, dtype, "q_out"),
+        *(_NO_HEADS if k is None else _heads(k_out, k_shape, dtype, "k_out")),
+        _current_stream(dev) if stream is None else stream.cuda_stream)
+    if status:
+        _check(status)
+    return q_out, k_out
+
+
+def la_rotary_fwd(q, k, inv_freq, positions=None, offsets=None, lengths=None, interleaved=False,
+                  scale=1.0, q_out=None, k_out=None, stream=None):
+    """Rotary positions of ``q`` [B,H,L,d] and ``k`` [B,H_k,L,d] (or None) in one
+    call.  Returns ``(q_out, k_out)``, [B,H,L,d] as ``la_chunk_fwd`` reads them
+    unless given.
+
+    ``q``, ``k`` and the outputs are fp32 or bf16 with any strides whose last is 1: a
+    permuted view of a projection's token-major output as it is.  ``inv_freq``
+    fp32 [r/2] (``la_rotary_frequencies``) turns the first r values of a head, in
+    pairs of neighbours if ``interleaved``, else (i, i + r/2).  Token t of sequence
+    b has position ``offsets[b] + t``, or ``offsets[b] + positions[b,t]`` (int32 [B] and
+    [B,L]).  ``lengths`` int32 [B]: the tokens behind them are left as they are in the
+    outputs (zero where these are made here).  ``q_out`` may be ``q``, ``k_out`` ``k``."""
+    return _rotary("la_rotary_fwd", q, k, inv_freq, positions, offsets, lengths, interleaved,
+                   scale, q_out, k_out, stream)
+
+
+def la_rotary_bwd(dq, dk, inv_freq, positions=None, offsets=None, lengths=None,
+                  interleaved=False, scale=1.0, q_out=None, k_out=None, stream=None):
+    """Backward pass of ``la_rotary_fwd``: the gradients of its outputs to those of
+    its inputs, of the same arguments.  ``q_out`` and ``k_out`` may be views of a
+    projection's gradient.  Returns ``(q_out, k_out)``."""
+    return _rotary("la_rotary_bwd", dq, dk, inv_freq, positions, offsets, lengths, interleaved,
+                   scale, q_out, k_out, stream)
+
+
+def la_chunk_bwd_workspace_bytes(B, H, L, d_k, d_v, chunk=64, dtype=torch.bfloat16) -> int:
+    return int(_native.load().la_chunk_bwd_workspace_bytes(B, H, L, d_k, d_v, chunk,
+                                                           DTYPE[dtype]))
+
+
+def _dense(t, shape, dtype, what):
+    if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous {dtype} {list(shape)}")
+    return t.data_ptr()
+
+
+def la_chunk_bwd(q, k, v, dO, chunk=64, decay_kind="none", decay=None, S0=None, dS_final=None,
+                 dq=None, dk=None, dv=None, ddecay=None, dS0=None, want_decay_grad=True,
+                 want_state_grad=None, workspace=None, stream=None):
+    """Backward pass of ``la_chunk_fwd`` (with the feature map set now): from ``dO``,
+    the gradient of O, ``dS_final``, that of S_final (None: zero), and the forward
+    call's arguments.  Returns ``(dq, dk, dv, ddecay, dS0)``.
+
+    ``ddecay`` has ``decay``'s shape: the gradient of log gamma [H], log alpha or the
+    gate logits [B,H,L]; None without a decay or without ``want_decay_grad``.  ``dS0``
+    is formed with ``S0`` unless ``want_state_grad`` says otherwise.  With bf16 tensors
+    both cost about twice the work: their products keep 24 bits."""
+    shape, dtype = q.shape, q.dtype
+    B, H, L, d_k = shape
+    d_v = v.shape[-1]
+    if max(B, H, L, d_k, d_v) > _INT_MAX:
+        raise _too_large(B, H, L, d_k, d_v)
+    v_shape, state, f32 = (B, H, L, d_v), (B, H, d_k, d_v), torch.float32
+    kind = DECAY[decay_kind]
+    if (decay is None) != (kind == 0):
+        raise ValueError("decay goes with its decay_kind")
+    decay_shape = (H,) if kind == 1 else (B, H, L)
+    qp, kp = _dense(q, shape, dtype, "q"), _dense(k, shape, dtype, "k")
+    vp, dOp = _dense(v, v_shape, dtype, "v"), _dense(dO, v_shape, dtype, "dO")
+    dp = None if decay is None else _dense(decay, decay_shape, f32, "decay")
+    s0 = None if S0 is None else _dense(S0, state, f32, "S0")
+    sf = None if dS_final is None else _dense(dS_final, state, f32, "dS_final")
+    dev = _device_of(q, k, v, dO, decay, S0, dS_final, dq, dk, dv, ddecay, dS0, workspace)
+    new = lambda n, t: _new(n, t, q.device, stream)  # noqa: E731
+    dq = new(shape, dtype) if dq is None else dq
+    dk = new(shape, dtype) if dk is None else dk
+    dv = new(v_shape, dtype) if dv is None else dv
+    if ddecay is not None and decay is None:
+        raise ValueError("ddecay without a decay")
+    if ddecay is None and want_decay_grad and decay is not None:
+        ddecay = new(decay_shape, f32)
+    if dS0 is None and (S0 is not None if want_state_grad is None else want_state_grad):
+        dS0 = new(state, f32)
+    lib = _native.load()
+    ws = ws_bytes = 0
+    if workspace is None:
+        workspace = _workspace(lib.la_chunk_bwd_workspace_bytes(B, H, L, d_k, d_v, chunk,
+                                                                DTYPE[dtype]), q.device, stream)
+    if workspace is not None:
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    status = lib.la_chunk_bwd(
+        qp, kp, vp, DTYPE[dtype], B, H, L, d_k, d_v, chunk, kind, dp, s0, dOp, sf,
+        _dense(dq, shape, dtype, "dq"), _dense(dk, shape, dtype, "dk"),
+        _dense(dv, v_shape, dtype, "dv"),
+        None if ddecay is None else _dense(ddecay, decay_shape, f32, "ddecay"),
+        None if dS0 is None else _dense(dS0, state, f32, "dS0"), ws, ws_bytes,
+        _current_stream(dev) if stream is None else stream.cuda_stream)
+    if status:
+        _check(status)
+    return dq, dk, dv, ddecay, dS0
+
+
+def la_gated_norm_bwd_workspace_bytes(B, H, L, d, weight_heads=1) -> int:
+    return int(_native.load().la_gated_norm_bwd_workspace_bytes(B, H, L, d, weight_heads))
+
+
+def la_gated_norm_bwd(dy, x, gate=None, weight=None, bias=None, norm="rms", activation="silu",
+                      gate_first=False, eps=1e-5, dx=None, dgate=None, dweight=None, dbias=None,
+                      want_param_grads=True, workspace=None, stream=None):
+    """Backward pass of ``la_gated_norm_fwd``: from ``dy`` [B,L,H*d], the gradient of
+    its output, and its arguments.  Returns ``(dx, dgate, dweight, dbias)``.
+
+    ``dx`` [B,H,L,d] in x's dtype (any strides whose last is 1; made contiguous),
+    ``dgate`` [B,L,H*d], ``dweight`` and ``dbias`` fp32 of the parameters' shapes; None
+    for what is not there, and for the parameters' without ``want_param_grads``.  ``dx``
+    may be ``x``, ``dgate`` ``gate`` or ``dy``."""
+    B, H, L, d = x.shape
+    dtype = x.dtype
+    if max(B, H, L, d) > _INT_MAX:
+        raise _too_large(B, H, L, d)
+    width = H * d
+    shape = (B, L, width)
+    heads = 1
+    w = b = None
+    if weight is not None:
+        w, heads = _head_param(weight, H, d)
+    if bias is not None:
+        b, heads = _head_param(bias, H, d)
+        if weight is not None and weight.numel() != bias.numel():
+            raise ValueError("weight and bias must have one shape")
+    if gate is None and dgate is not None:
+        raise ValueError("dgate without a gate")
+    xa = _heads(x, x.shape, dtype, "x")
+    dys = _row_stride(dy, shape, dtype, "dy")
+    gs = 0 if gate is None else _row_stride(gate, shape, dtype, "gate")
+    dev = _device_of(x, dy, gate, weight, bias, dx, dgate, dweight, dbias, workspace)
+    for g, p, what in ((dweight, weight, "dweight"), (dbias, bias, "dbias")):
+        if g is not None and (p is None or g.shape != p.shape):
+            raise ValueError(f"{what} must have its parameter's shape")
+    if dx is None:
+        dx = _new(x.shape, dtype, x.device, stream)
+    if gate is not None and dgate is None:
+        dgate = _new(shape, dtype, x.device, stream)
+    if want_param_grads:
+        if weight is not None and dweight is None:
+            dweight = _new(weight.shape, torch.float32, x.device, stream)
+        if bias is not None and dbias is None:
+            dbias = _new(bias.shape, torch.float32, x.device, stream)
+    lib = _native.load()
+    ws = ws_bytes = 0
+    if workspace is None and (dweight is not None or dbias is not None):
+        workspace = _workspace(lib.la_gated_norm_bwd_workspace_bytes(B, H, L, d, heads), x.device,
+                               stream)
+    if workspace is not None:
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    status = lib.la_gated_norm_bwd(
+        dy.data_ptr(), dys, *xa, None if gate is None else gate.data_ptr(), gs, DTYPE[dtype], B, H,
+        L, d, NORM[norm], ACT[activation], gate_first, w, b, heads, eps,
+        *_heads(dx, x.shape, dtype, "dx"), None if gate is None else dgate.data_ptr(),
+        0 if gate is None else _row_stride(dgate, shape, dtype, "dgate"),
+        None if dweight is None else _param(dweight, dweight.shape, "dweight"),
+        None if dbias is None else _param(dbias, dbias.shape, "dbias"), ws, ws_bytes,
+        _current_stream(dev) if stream is None else stream.cuda_stream)
+    if status:
+        _check(status)
+    return dx, dgate, dweight, dbias
+
+
+def la_residual_norm_bwd_workspace_bytes(rows, D) -> int:
+    return int(_native.load().la_residual_norm_bwd_workspace_bytes(rows, D))
+
+
+def la_residual_norm_bwd(dy, r, weight=None, dr=None, x=None, post_weight=None, scale=None,
+                         alpha=1.0, norm="rms", eps=1e-5, dx=None, dresidual=None,
+                         want_dresidual=True, want_param_grads=True, want_dbias=False,
+                         workspace=None, stream=None):
+    """Backward pass of ``la_residual_norm_fwd``: from ``dy``, the gradient of its y,
+    ``r``, the residual_out that it wrote, and ``dr``, the gradient of that (None:
+    zero).  Returns ``(dx, dresidual, dweight, dbias, dpost_weight, dscale)``.
+
+    ``dy``, ``x`` and ``dx`` [...,D] fp32 or bf16, ``r``, ``dr`` and ``dresidual`` in
+    that dtype or fp32, all contiguous; ``x`` is needed with ``post_weight`` or
+    ``scale``.  The parameters' gradients are fp32 [D], None for what is not there
+    (``dbias`` is formed if ``want_dbias``: the bias itself is not needed).  ``dx`` may
+    be ``dy`` or ``x``, ``dresidual`` may be ``dr``.  By itself, with ``weight`` and
+    ``want_dbias``, this is a layer norm's backward pass."""
+    shape, dtype = dy.shape, dy.dtype
+    D = shape[-1]
+    if D > _INT_MAX:
+        raise _too_large(D)
+    rd = r.dtype
+    per = (D,)
+    params = want_param_grads
+    w = None if weight is None else _param(weight, per, "weight")
+    pw = None if post_weight is None else _param(post_weight, per, "post_weight")
+    sc = None if scale is None else _param(scale, per, "scale")
+    yp, rp = _same(dy, shape, dtype), _same(r, shape, rd)
+    drp = None if dr is None else _same(dr, shape, rd)
+    xp = None if x is None else _same(x, shape, dtype)
+    dev = _device_of(dy, r, dr, x, weight, post_weight, scale, dx, dresidual, workspace)
+    dx = _new(shape, dtype, dy.device, stream) if dx is None else dx
+    if dresidual is None and want_dresidual:
+        dresidual = _new(shape, rd, dy.device, stream)
+    grads = [_new(per, torch.float32, dy.device, stream) if wanted else None
+             for wanted in (params and weight is not None, want_dbias,
+                            params and post_weight is not None, params and scale is not None)]
+    rows = dy.numel() // D if D else 0
+    lib = _native.load()
+    ws = ws_bytes = 0
+    if workspace is None and any(g is not None for g in grads):
+        workspace = _workspace(lib.la_residual_norm_bwd_workspace_bytes(rows, D), dy.device,
+                               stream)
+    if workspace is not None:
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    status = lib.la_residual_norm_bwd(
+        yp, DTYPE[dtype], rp, drp, DTYPE[rd], xp, rows, D, pw, sc, alpha, w, NORM[norm], eps,
+        _same(dx, shape, dtype), None if dresidual is None else _same(dresidual, shape, rd),
+        *map(_ptr, grads), ws, ws_bytes,
+        _current_stream(dev) if stream is None else stream.cuda_stream)
+    if status:
+        _check(status)
+    return (dx, dresidual, *grads)
 
 
 def la_device_status(stream=None) -> None:

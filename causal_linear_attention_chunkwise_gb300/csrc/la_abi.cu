@@ -1,6 +1,7 @@
 // la_abi.cu -- the extern "C" boundary: argument validation, dispatch to the
 // kernel launchers, the process-wide feature map, error reporting.
 #include <atomic>
+#include <cmath>
 #include <cstdarg>
 #include <cstdint>
 #include <cstdio>
@@ -133,6 +134,96 @@ bool overlap_any(const Rows &out, const Rows (&in)[N]) {
 
 bool aligned_elt(const void *p, size_t elt) {
   return (reinterpret_cast<uintptr_t>(p) & (elt - 1)) == 0;
+}
+
+// A [B,H,L,d] tensor with strides: its token-major rows where it has them (they may
+// be a slice of a wider tensor), else all that it spans as one row.
+Rows head_rows(const void *p, int B, int H, int L, int d, long long bs, long long hs,
+               long long ts, size_t elt) {
+  const long long rows = (long long)B * L, width = (long long)H * d;
+  if ((H == 1 || hs == d) && (B == 1 || L == 1 || bs == L * ts) && (L == 1 || ts >= width) &&
+      (L > 1 || B == 1 || bs >= width))
+    return {p, rows, width, rows == 1 ? width : L == 1 ? bs : ts, elt};
+  const long long span = (B - 1) * bs + (H - 1) * hs + (L - 1) * ts + d;
+  return {p, 1, span, span, elt};
+}
+
+// Whether no two elements of a [B,H,L,d] tensor lie in one place, as an output's may not.
+bool own_places(int B, int H, int L, int d, long long bs, long long hs, long long ts) {
+  long long n[3] = {B, H, L}, s[3] = {bs, hs, ts}, extent = d;
+  for (int i = 0; i < 3; ++i)
+    for (int j = i + 1; j < 3; ++j)
+      if (s[j] < s[i]) {
+        const long long a = s[i], b = n[i];
+        s[i] = s[j], n[i] = n[j], s[j] = a, n[j] = b;
+      }
+  for (int i = 0; i < 3; ++i) {
+    if (n[i] == 1) continue;
+    if (s[i] < extent) return false;
+    extent += (n[i] - 1) * s[i];
+  }
+  return true;
+}
+
+la_status rotary(const char *fn, RotaryArgs a) {
+  if (a.dtype != LA_F32 && a.dtype != LA_BF16)
+    return fail(LA_ERR_INVALID_ARG, "%s: unknown dtype %d", fn, a.dtype);
+  if (a.B < 0 || a.heads_q < 0 || a.heads_k < 0 || a.L < 0 || a.d <= 0)
+    return fail(LA_ERR_INVALID_ARG, "%s: bad sizes B=%d heads=%d, %d L=%d d=%d", fn, a.B,
+                a.heads_q, a.heads_k, a.L, a.d);
+  if (a.rot < 2 || a.rot > a.d || a.rot % 2)
+    return fail(LA_ERR_INVALID_ARG, "%s: rotary_dim=%d is no even number in 2..d=%d", fn, a.rot,
+                a.d);
+  if (a.d > 16384 || a.heads_q > 16384 || a.heads_k > 16384 || a.L > kMaxLen)
+    return fail(LA_ERR_UNSUPPORTED,
+                "%s: d=%d or heads=%d, %d above 16384, or L=%d above 2^30", fn, a.d, a.heads_q,
+                a.heads_k, a.L);
+  if (!a.k.p && !a.k_out.p) a.heads_k = 0;
+  if (a.B == 0 || a.L == 0 || a.heads_q + a.heads_k == 0) return ok();
+  const size_t elt = a.dtype == LA_F32 ? 4 : 2;
+  Rows in[2], out[2];
+  const RotaryTensor x[] = {a.q, a.k}, y[] = {a.q_out, a.k_out};
+  const int heads[] = {a.heads_q, a.heads_k};
+  for (int i = 0; i < 2; ++i) {
+    if (heads[i] == 0) {
+      in[i] = out[i] = Rows{nullptr, 0, 0, 0, elt};
+      continue;
+    }
+    if (!x[i].p || !y[i].p)
+      return fail(LA_ERR_INVALID_ARG, "%s: q, q_out, or one of k and k_out, is null", fn);
+    if (!aligned_elt(x[i].p, elt) || !aligned_elt(y[i].p, elt))
+      return fail(LA_ERR_INVALID_ARG, "%s: pointers must be aligned to their elements", fn);
+    for (const RotaryTensor *t : {&x[i], &y[i]})
+      if (t->bs < 0 || t->hs < 0 || t->ts < 0)
+        return fail(LA_ERR_INVALID_ARG, "%s: negative stride", fn);
+    if (!own_places(a.B, heads[i], a.L, a.d, y[i].bs, y[i].hs, y[i].ts))
+      return fail(LA_ERR_INVALID_ARG, "%s: an output's strides put two elements in one place", fn);
+    in[i] = head_rows(x[i].p, a.B, heads[i], a.L, a.d, x[i].bs, x[i].hs, x[i].ts, elt);
+    out[i] = head_rows(y[i].p, a.B, heads[i], a.L, a.d, y[i].bs, y[i].hs, y[i].ts, elt);
+  }
+  if (!a.inv_freq) return fail(LA_ERR_INVALID_ARG, "%s: inv_freq must be non-null", fn);
+  for (const void *p : {static_cast<const void *>(a.inv_freq),
+                        static_cast<const void *>(a.positions),
+                        static_cast<const void *>(a.offsets),
+                        static_cast<const void *>(a.lengths)})
+    if (!aligned_elt(p, 4))
+      return fail(LA_ERR_INVALID_ARG, "%s: inv_freq, positions, offsets and lengths must be "
+                  "4-byte aligned", fn);
+  const Rows par[] = {params(a.inv_freq, a.rot / 2), params(a.positions, (long long)a.B * a.L),
+                      params(a.offsets, a.B), params(a.lengths, a.B)};
+  for (int i = 0; i < 2; ++i) {
+    const bool in_place = x[i].p == y[i].p && (a.B == 1 || x[i].bs == y[i].bs) &&
+                          (heads[i] == 1 || x[i].hs == y[i].hs) &&
+                          (a.L == 1 || x[i].ts == y[i].ts);
+    if ((!in_place && overlap(out[i], in[i])) || overlap(out[i], in[1 - i]) ||
+        overlap_any(out[i], par))
+      return fail(LA_ERR_INVALID_ARG, "%s: an output overlaps an input", fn);
+  }
+  if (overlap(out[0], out[1]))
+    return fail(LA_ERR_INVALID_ARG, "%s: q_out and k_out overlap", fn);
+  cudaError_t e = launch_rotary(a);
+  if (e != cudaSuccess) return cuda_fail(e, fn);
+  return ok();
 }
 
 const char *kernel_name(unsigned int id) {
@@ -666,6 +757,354 @@ la_status la_residual_norm_fwd(const void *x, int dtype, const void *residual, i
   ResidualNormArgs a{x, dtype, residual, res_dtype, rows, D, post_weight, scale, alpha, weight,
                      bias, norm, eps, y, residual_out, static_cast<cudaStream_t>(cuda_stream)};
   cudaError_t e = launch_residual_norm(a);
+  if (e != cudaSuccess) return cuda_fail(e, fn);
+  return ok();
+}
+
+la_status la_rotary_fwd(const void *q, long long q_b_stride, long long q_h_stride,
+                        long long q_t_stride, int heads_q, const void *k, long long k_b_stride,
+                        long long k_h_stride, long long k_t_stride, int heads_k, int dtype, int B,
+                        int L, int d, int rotary_dim, int interleaved, const float *inv_freq,
+                        float scale, const int *positions, const int *offsets,
+                        const int *lengths, void *q_out, long long qo_b_stride,
+                        long long qo_h_stride, long long qo_t_stride, void *k_out,
+                        long long ko_b_stride, long long ko_h_stride, long long ko_t_stride,
+                        void *cuda_stream) {
+  return rotary("la_rotary_fwd",
+                {{const_cast<void *>(q), q_b_stride, q_h_stride, q_t_stride},
+                 {q_out, qo_b_stride, qo_h_stride, qo_t_stride},
+                 {const_cast<void *>(k), k_b_stride, k_h_stride, k_t_stride},
+                 {k_out, ko_b_stride, ko_h_stride, ko_t_stride},
+                 heads_q, heads_k, dtype, B, L, d, rotary_dim, interleaved, 0, inv_freq, scale,
+                 positions, offsets, lengths, static_cast<cudaStream_t>(cuda_stream)});
+}
+
+la_status la_rotary_bwd(const void *dq, long long q_b_stride, long long q_h_stride,
+                        long long q_t_stride, int heads_q, const void *dk, long long k_b_stride,
+                        long long k_h_stride, long long k_t_stride, int heads_k, int dtype, int B,
+                        int L, int d, int rotary_dim, int interleaved, const float *inv_freq,
+                        float scale, const int *positions, const int *offsets,
+                        const int *lengths, void *dq_out, long long qo_b_stride,
+                        long long qo_h_stride, long long qo_t_stride, void *dk_out,
+                        long long ko_b_stride, long long ko_h_stride, long long ko_t_stride,
+                        void *cuda_stream) {
+  return rotary("la_rotary_bwd",
+                {{const_cast<void *>(dq), q_b_stride, q_h_stride, q_t_stride},
+                 {dq_out, qo_b_stride, qo_h_stride, qo_t_stride},
+                 {const_cast<void *>(dk), k_b_stride, k_h_stride, k_t_stride},
+                 {dk_out, ko_b_stride, ko_h_stride, ko_t_stride},
+                 heads_q, heads_k, dtype, B, L, d, rotary_dim, interleaved, 1, inv_freq, scale,
+                 positions, offsets, lengths, static_cast<cudaStream_t>(cuda_stream)});
+}
+
+la_status la_rotary_frequencies(int rotary_dim, double base, int scaling, double factor,
+                                double trained_length, double fast, double slow, float *inv_freq,
+                                float *scale) {
+  const char *fn = "la_rotary_frequencies";
+  if (rotary_dim < 2 || rotary_dim % 2)
+    return fail(LA_ERR_INVALID_ARG, "%s: rotary_dim=%d is no positive even number", fn,
+                rotary_dim);
+  if (scaling < LA_ROTARY_PLAIN || scaling > LA_ROTARY_YARN)
+    return fail(LA_ERR_INVALID_ARG, "%s: unknown scaling %d", fn, scaling);
+  if (!inv_freq) return fail(LA_ERR_INVALID_ARG, "%s: inv_freq must be non-null", fn);
+  if (!(base > 0) || !std::isfinite(base))
+    return fail(LA_ERR_INVALID_ARG, "%s: base must be positive and finite", fn);
+  if (scaling != LA_ROTARY_PLAIN && (!(factor >= 1) || !std::isfinite(factor)))
+    return fail(LA_ERR_INVALID_ARG, "%s: factor must be finite and at least 1", fn);
+  if (scaling == LA_ROTARY_YARN &&
+      (!(trained_length > 0) || !(slow >= 0) || !(fast > slow) || !std::isfinite(fast) ||
+       !std::isfinite(trained_length)))
+    return fail(LA_ERR_INVALID_ARG, "%s: needs trained_length > 0 and fast > slow >= 0", fn);
+  if (scaling == LA_ROTARY_NTK && rotary_dim > 2)
+    base *= std::pow(factor, rotary_dim / (rotary_dim - 2.0));
+  for (int i = 0; i < rotary_dim / 2; ++i) {
+    double f = std::pow(base, -2.0 * i / rotary_dim);
+    if (scaling == LA_ROTARY_LINEAR) f /= factor;
+    if (scaling == LA_ROTARY_YARN) {
+      const double turns = trained_length * f / (6.283185307179586);
+      const double ramp = turns <= slow ? 0 : turns >= fast ? 1 : (turns - slow) / (fast - slow);
+      f = f / factor * (1 - ramp) + f * ramp;
+    }
+    inv_freq[i] = (float)f;
+  }
+  if (scale) *scale = scaling == LA_ROTARY_YARN ? (float)(1 + 0.1 * std::log(factor)) : 1.f;
+  return ok();
+}
+
+size_t la_chunk_bwd_workspace_bytes(int B, int H, int L, int d_k, int d_v, int chunk, int dtype) {
+  if (B <= 0 || H <= 0 || L <= 0 || L > kMaxLen || (long long)B * H > 0x7fffffffll ||
+      !supported_d(d_k) || !supported_d(d_v) || chunk < 1 || chunk > 64 ||
+      (dtype != LA_F32 && dtype != LA_BF16))
+    return 0;
+  ChunkBwdArgs a{};
+  a.dtype = dtype; a.B = B; a.H = H; a.L = L; a.dk = d_k; a.dv = d_v;
+  return chunk_bwd_workspace_bytes(a);
+}
+
+la_status la_chunk_bwd(const void *q, const void *k, const void *v, int dtype, int B, int H,
+                       int L, int d_k, int d_v, int chunk, int decay_kind, const float *decay,
+                       const float *S0, const void *dO, const float *dS_final, void *dq, void *dk,
+                       void *dv, float *ddecay, float *dS0, void *workspace, size_t ws_bytes,
+                       void *cuda_stream) {
+  const char *fn = "la_chunk_bwd";
+  cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+  if (dtype != LA_F32 && dtype != LA_BF16)
+    return fail(LA_ERR_INVALID_ARG, "%s: unknown dtype %d", fn, dtype);
+  if (B < 0 || H < 0 || L < 0 || d_k <= 0 || d_v <= 0 || chunk <= 0)
+    return fail(LA_ERR_INVALID_ARG, "%s: bad sizes B=%d H=%d L=%d d_k=%d d_v=%d chunk=%d", fn, B,
+                H, L, d_k, d_v, chunk);
+  if (decay_kind < LA_DECAY_NONE || decay_kind > LA_DECAY_GATE_LOGIT)
+    return fail(LA_ERR_INVALID_ARG, "%s: unknown decay kind %d", fn, decay_kind);
+  if (decay_kind == LA_DECAY_NONE && ddecay)
+    return fail(LA_ERR_INVALID_ARG, "%s: ddecay without a decay", fn);
+  if (!supported_d(d_k) || !supported_d(d_v))
+    return fail(LA_ERR_UNSUPPORTED, "%s: d_k=%d d_v=%d not in {16,32,64,128}", fn, d_k, d_v);
+  if (chunk > 64) return fail(LA_ERR_UNSUPPORTED, "%s: chunk %d > 64 is not supported", fn, chunk);
+  if (L > kMaxLen || (long long)B * H > 0x7fffffffll)
+    return fail(LA_ERR_UNSUPPORTED, "%s: L=%d above 2^30, or B*H above 2^31 - 1", fn, L);
+  const size_t seqs = (size_t)B * H, states = seqs * d_k * d_v * sizeof(float);
+  const size_t decays = decay_kind == LA_DECAY_NONE ? 0 : decay_kind == LA_DECAY_HEAD
+                                                             ? (size_t)H : seqs * L;
+  if (!aligned16(S0) || !aligned16(dS_final) || !aligned16(dS0) ||
+      !aligned_elt(decay, 4) || !aligned_elt(ddecay, 4))
+    return fail(LA_ERR_INVALID_ARG,
+                "%s: states must be 16-byte aligned, decays to their elements", fn);
+  const Rows s0 = dense(S0, states), sf = dense(dS_final, states), ds = dense(dS0, states);
+  if (overlap(ds, s0) || overlap(ds, sf))
+    return fail(LA_ERR_INVALID_ARG, "%s: dS0 overlaps S0 or dS_final", fn);
+  if (seqs == 0 || L == 0) {  // no tokens: the state's gradient passes through
+    cudaError_t e = seqs ? pass_through_state(dS0, dS_final, states, st) : cudaSuccess;
+    if (e == cudaSuccess && ddecay && decay_kind == LA_DECAY_HEAD && H > 0)
+      e = cudaMemsetAsync(ddecay, 0, (size_t)H * sizeof(float), st);
+    if (e != cudaSuccess) return cuda_fail(e, fn);
+    return ok();
+  }
+  if (!q || !k || !v || !dO || !dq || !dk || !dv)
+    return fail(LA_ERR_INVALID_ARG, "%s: q, k, v, dO, dq, dk and dv must be non-null", fn);
+  if (decay_kind != LA_DECAY_NONE && !decay)
+    return fail(LA_ERR_INVALID_ARG, "%s: decay kind %d needs a decay pointer", fn, decay_kind);
+  for (const void *p : {q, k, v, dO, static_cast<const void *>(dq),
+                        static_cast<const void *>(dk), static_cast<const void *>(dv)})
+    if (!aligned16(p))
+      return fail(LA_ERR_INVALID_ARG, "%s: tensors must start on a 16-byte boundary", fn);
+  const size_t elt = dtype == LA_F32 ? 4 : 2;
+  const size_t nk = seqs * L * d_k * elt, nv = seqs * L * d_v * elt;
+  const Rows in[] = {dense(q, nk), dense(k, nk), dense(v, nv), dense(dO, nv), s0,
+                     dense(decay_kind == LA_DECAY_NONE ? nullptr : decay, decays * 4)};
+  const Rows out[] = {dense(dq, nk), dense(dk, nk), dense(dv, nv), dense(ddecay, decays * 4), ds};
+  for (int i = 0; i < 5; ++i) {
+    bool bad = overlap_any(out[i], in) || overlap(out[i], sf);
+    for (int j = 0; j < i; ++j) bad = bad || overlap(out[i], out[j]);
+    if (bad)
+      return fail(LA_ERR_INVALID_ARG, "%s: an output overlaps an input or another output", fn);
+  }
+  ChunkBwdArgs a{q, k, v, dO, dtype, B, H, L, d_k, d_v, g_phi.load(), decay_kind,
+                 decay_kind == LA_DECAY_NONE ? nullptr : decay, S0, dS_final, dq, dk, dv, ddecay,
+                 dS0, workspace, st};
+  const size_t need = chunk_bwd_workspace_bytes(a);
+  if (need > 0) {
+    if (!workspace || ws_bytes < need)
+      return fail(LA_ERR_INVALID_ARG, "%s: workspace of %zu bytes needed, %zu given", fn, need,
+                  workspace ? ws_bytes : (size_t)0);
+    if (!aligned16(workspace))
+      return fail(LA_ERR_INVALID_ARG, "%s: workspace must be 16-byte aligned", fn);
+    const Rows ws = dense(workspace, need);
+    if (overlap_any(ws, in) || overlap_any(ws, out) || overlap(ws, sf))
+      return fail(LA_ERR_INVALID_ARG, "%s: the workspace overlaps an input or an output", fn);
+  }
+  cudaError_t e = launch_chunk_bwd(a);
+  if (e != cudaSuccess) return cuda_fail(e, fn);
+  return ok();
+}
+
+size_t la_gated_norm_bwd_workspace_bytes(int B, int H, int L, int d, int weight_heads) {
+  if (B <= 0 || H <= 0 || L <= 0 || d < 1 || d > 16384 ||
+      (weight_heads != 1 && weight_heads != H))
+    return 0;
+  return gated_norm_bwd_workspace_bytes(B, H, L, d, weight_heads);
+}
+
+la_status la_gated_norm_bwd(const void *dy, long long dy_stride, const void *x,
+                            long long x_b_stride, long long x_h_stride, long long x_t_stride,
+                            const void *gate, long long gate_stride, int dtype, int B, int H,
+                            int L, int d, int norm, int activation, int gate_first,
+                            const float *weight, const float *bias, int weight_heads, float eps,
+                            void *dx, long long dx_b_stride, long long dx_h_stride,
+                            long long dx_t_stride, void *dgate, long long dgate_stride,
+                            float *dweight, float *dbias, void *workspace, size_t ws_bytes,
+                            void *cuda_stream) {
+  const char *fn = "la_gated_norm_bwd";
+  if (dtype != LA_F32 && dtype != LA_BF16)
+    return fail(LA_ERR_INVALID_ARG, "%s: unknown dtype %d", fn, dtype);
+  if (B < 0 || H < 0 || L < 0 || d <= 0)
+    return fail(LA_ERR_INVALID_ARG, "%s: bad sizes B=%d H=%d L=%d d=%d", fn, B, H, L, d);
+  if (norm != LA_NORM_RMS && norm != LA_NORM_LAYER)
+    return fail(LA_ERR_INVALID_ARG, "%s: unknown norm %d", fn, norm);
+  if (activation < LA_ACT_NONE || activation > LA_ACT_SIGMOID)
+    return fail(LA_ERR_INVALID_ARG, "%s: unknown activation %d", fn, activation);
+  if (!(eps >= 0.f)) return fail(LA_ERR_INVALID_ARG, "%s: eps must be >= 0", fn);
+  if (d > 16384) return fail(LA_ERR_UNSUPPORTED, "%s: d=%d outside 1..16384", fn, d);
+  if (H > 65535) return fail(LA_ERR_UNSUPPORTED, "%s: H=%d above 65535", fn, H);
+  if (weight_heads != 1 && weight_heads != H)
+    return fail(LA_ERR_INVALID_ARG, "%s: weight_heads=%d is neither 1 nor H=%d", fn,
+                weight_heads, H);
+  const long long width = (long long)H * d, wn = (long long)weight_heads * d;
+  if (x_b_stride < 0 || x_h_stride < 0 || x_t_stride < 0 || dx_b_stride < 0 || dx_h_stride < 0 ||
+      dx_t_stride < 0 || dy_stride < width || (gate && gate_stride < width) ||
+      (dgate && dgate_stride < width))
+    return fail(LA_ERR_INVALID_ARG, "%s: negative stride, or a row stride shorter than H*d", fn);
+  cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+  if (!aligned16(weight) || !aligned16(bias) || !aligned16(dweight) || !aligned16(dbias))
+    return fail(LA_ERR_INVALID_ARG, "%s: parameters and their gradients must be 16-byte aligned",
+                fn);
+  if ((size_t)B * H == 0 || L == 0) {  // no rows: the sums over them are zero
+    for (float *p : {dweight, dbias})
+      if (p && wn > 0) {
+        cudaError_t e = cudaMemsetAsync(p, 0, wn * sizeof(float), st);
+        if (e != cudaSuccess) return cuda_fail(e, fn);
+      }
+    return ok();
+  }
+  if (!dy || !x || !dx) return fail(LA_ERR_INVALID_ARG, "%s: dy, x and dx must be non-null", fn);
+  if (!gate != !dgate)
+    return fail(LA_ERR_INVALID_ARG, "%s: dgate goes with gate: both or none", fn);
+  const size_t elt = dtype == LA_F32 ? 4 : 2;
+  for (const void *p : {dy, x, gate, static_cast<const void *>(dx),
+                        static_cast<const void *>(dgate)})
+    if (!aligned_elt(p, elt))
+      return fail(LA_ERR_INVALID_ARG, "%s: pointers must be aligned to their elements", fn);
+  if (!own_places(B, H, L, d, dx_b_stride, dx_h_stride, dx_t_stride))
+    return fail(LA_ERR_INVALID_ARG, "%s: dx's strides put two elements in one place", fn);
+  const long long rows = (long long)B * L;
+  const Rows in[] = {{dy, rows, width, dy_stride, elt},
+                     head_rows(x, B, H, L, d, x_b_stride, x_h_stride, x_t_stride, elt),
+                     {gate, rows, width, gate_stride, elt}};
+  const Rows par[] = {params(weight, wn), params(bias, wn)};
+  const Rows dxr = head_rows(dx, B, H, L, d, dx_b_stride, dx_h_stride, dx_t_stride, elt);
+  const Rows dzr{dgate, rows, width, dgate_stride, elt};
+  const Rows dw = params(dweight, wn), dbr = params(dbias, wn);
+  const bool x_place = dx == x && (B == 1 || dx_b_stride == x_b_stride) &&
+                       (H == 1 || dx_h_stride == x_h_stride) &&
+                       (L == 1 || dx_t_stride == x_t_stride);
+  const bool dy_place = dgate && dgate == dy && dgate_stride == dy_stride;
+  const bool z_place = dgate && dgate == gate && dgate_stride == gate_stride;
+  if (overlap(dxr, in[0]) || (!x_place && overlap(dxr, in[1])) || overlap(dxr, in[2]) ||
+      (!dy_place && overlap(dzr, in[0])) || overlap(dzr, in[1]) ||
+      (!z_place && overlap(dzr, in[2])) || overlap(dxr, dzr) || overlap_any(dxr, par) ||
+      overlap_any(dzr, par))
+    return fail(LA_ERR_INVALID_ARG, "%s: an output overlaps an input or another output", fn);
+  for (const Rows &w : {dw, dbr})
+    if (overlap_any(w, in) || overlap_any(w, par) || overlap(w, dxr) || overlap(w, dzr))
+      return fail(LA_ERR_INVALID_ARG, "%s: an output overlaps an input or another output", fn);
+  if (overlap(dw, dbr)) return fail(LA_ERR_INVALID_ARG, "%s: dweight and dbias overlap", fn);
+  if (dweight || dbias) {
+    const size_t need = gated_norm_bwd_workspace_bytes(B, H, L, d, weight_heads);
+    if (!workspace || ws_bytes < need)
+      return fail(LA_ERR_INVALID_ARG, "%s: workspace of %zu bytes needed, %zu given", fn, need,
+                  workspace ? ws_bytes : (size_t)0);
+    if (!aligned16(workspace))
+      return fail(LA_ERR_INVALID_ARG, "%s: workspace must be 16-byte aligned", fn);
+    const Rows ws = dense(workspace, need);
+    if (overlap_any(ws, in) || overlap_any(ws, par) || overlap(ws, dxr) || overlap(ws, dzr) ||
+        overlap(ws, dw) || overlap(ws, dbr))
+      return fail(LA_ERR_INVALID_ARG, "%s: the workspace overlaps an input or an output", fn);
+  }
+  GatedNormBwdArgs a{dy, dy_stride, x, x_b_stride, x_h_stride, x_t_stride, gate, gate_stride,
+                     dtype, B, H, L, d, norm, activation, gate_first, weight, bias, weight_heads,
+                     eps, dx, dx_b_stride, dx_h_stride, dx_t_stride, dgate, dgate_stride,
+                     dweight, dbias, workspace, st};
+  cudaError_t e = launch_gated_norm_bwd(a);
+  if (e != cudaSuccess) return cuda_fail(e, fn);
+  return ok();
+}
+
+size_t la_residual_norm_bwd_workspace_bytes(long long rows, int D) {
+  return rows <= 0 || D < 1 || D > 16384 ? 0 : residual_norm_bwd_workspace_bytes(rows, D);
+}
+
+la_status la_residual_norm_bwd(const void *dy, int dtype, const void *r, const void *dr,
+                               int res_dtype, const void *x, long long rows, int D,
+                               const float *post_weight, const float *scale, float alpha,
+                               const float *weight, int norm, float eps, void *dx,
+                               void *dresidual, float *dweight, float *dbias,
+                               float *dpost_weight, float *dscale, void *workspace,
+                               size_t ws_bytes, void *cuda_stream) {
+  const char *fn = "la_residual_norm_bwd";
+  if (dtype != LA_F32 && dtype != LA_BF16)
+    return fail(LA_ERR_INVALID_ARG, "%s: unknown dtype %d", fn, dtype);
+  if (res_dtype != LA_F32 && res_dtype != dtype)
+    return fail(LA_ERR_INVALID_ARG, "%s: the residual's dtype %d is neither fp32 nor dy's", fn,
+                res_dtype);
+  if (rows < 0 || D <= 0)
+    return fail(LA_ERR_INVALID_ARG, "%s: bad sizes rows=%lld D=%d", fn, rows, D);
+  if (norm != LA_NORM_RMS && norm != LA_NORM_LAYER)
+    return fail(LA_ERR_INVALID_ARG, "%s: unknown norm %d", fn, norm);
+  if (!(eps >= 0.f)) return fail(LA_ERR_INVALID_ARG, "%s: eps must be >= 0", fn);
+  if (D > 16384) return fail(LA_ERR_UNSUPPORTED, "%s: D=%d outside 1..16384", fn, D);
+  if ((!post_weight && dpost_weight) || (!scale && dscale))
+    return fail(LA_ERR_INVALID_ARG, "%s: a gradient of a parameter that is not there", fn);
+  float *const grads[] = {dweight, dbias, dpost_weight, dscale};
+  for (const void *p : {static_cast<const void *>(post_weight), static_cast<const void *>(scale),
+                        static_cast<const void *>(weight), static_cast<const void *>(dweight),
+                        static_cast<const void *>(dbias),
+                        static_cast<const void *>(dpost_weight),
+                        static_cast<const void *>(dscale)})
+    if (!aligned16(p))
+      return fail(LA_ERR_INVALID_ARG,
+                  "%s: parameters and their gradients must be 16-byte aligned", fn);
+  cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+  if (rows == 0) {  // the sums over no rows are zero
+    for (float *p : grads)
+      if (p) {
+        cudaError_t e = cudaMemsetAsync(p, 0, (size_t)D * sizeof(float), st);
+        if (e != cudaSuccess) return cuda_fail(e, fn);
+      }
+    return ok();
+  }
+  if (!dy || !r || !dx) return fail(LA_ERR_INVALID_ARG, "%s: dy, r and dx must be non-null", fn);
+  if (!x && (post_weight || dscale))
+    return fail(LA_ERR_INVALID_ARG, "%s: a post norm and dscale need x", fn);
+  const size_t elt = dtype == LA_F32 ? 4 : 2, relt = res_dtype == LA_F32 ? 4 : 2;
+  if (!aligned_elt(dy, elt) || !aligned_elt(x, elt) || !aligned_elt(dx, elt) ||
+      !aligned_elt(r, relt) || !aligned_elt(dr, relt) || !aligned_elt(dresidual, relt))
+    return fail(LA_ERR_INVALID_ARG, "%s: pointers must be aligned to their elements", fn);
+  const size_t n = (size_t)rows * D;
+  const Rows dyr = dense(dy, n * elt), xr = dense(x, n * elt), rr = dense(r, n * relt),
+             drr = dense(dr, n * relt), dxr = dense(dx, n * elt), dres = dense(dresidual, n * relt);
+  const Rows par[] = {params(post_weight, D), params(scale, D), params(weight, D)};
+  if ((dx != dy && overlap(dxr, dyr)) || (dx != x && overlap(dxr, xr)) || overlap(dxr, rr) ||
+      overlap(dxr, drr) || overlap(dres, dyr) || overlap(dres, xr) || overlap(dres, rr) ||
+      (dresidual != dr && overlap(dres, drr)) || overlap(dxr, dres) || overlap_any(dxr, par) ||
+      overlap_any(dres, par))
+    return fail(LA_ERR_INVALID_ARG, "%s: an output overlaps an input or another output", fn);
+  bool sums = false;
+  for (int i = 0; i < 4; ++i) {
+    const Rows g = params(grads[i], D);
+    sums = sums || grads[i];
+    bool bad = overlap_any(g, par);
+    for (const Rows &o : {dyr, xr, rr, drr, dxr, dres}) bad = bad || overlap(g, o);
+    for (int j = 0; j < i; ++j) bad = bad || overlap(g, params(grads[j], D));
+    if (bad)
+      return fail(LA_ERR_INVALID_ARG, "%s: an output overlaps an input or another output", fn);
+  }
+  if (sums) {
+    const size_t need = residual_norm_bwd_workspace_bytes(rows, D);
+    if (!workspace || ws_bytes < need)
+      return fail(LA_ERR_INVALID_ARG, "%s: workspace of %zu bytes needed, %zu given", fn, need,
+                  workspace ? ws_bytes : (size_t)0);
+    if (!aligned16(workspace))
+      return fail(LA_ERR_INVALID_ARG, "%s: workspace must be 16-byte aligned", fn);
+    const Rows ws = dense(workspace, need);
+    bool bad = overlap_any(ws, par);
+    for (const Rows &o : {dyr, xr, rr, drr, dxr, dres}) bad = bad || overlap(ws, o);
+    for (float *g : grads) bad = bad || overlap(ws, params(g, D));
+    if (bad)
+      return fail(LA_ERR_INVALID_ARG, "%s: the workspace overlaps an input or an output", fn);
+  }
+  ResidualNormBwdArgs a{dy, dtype, r, dr, res_dtype, x, rows, D, post_weight, scale, alpha,
+                        weight, norm, eps, dx, dresidual, dweight, dbias, dpost_weight, dscale,
+                        workspace, st};
+  cudaError_t e = launch_residual_norm_bwd(a);
   if (e != cudaSuccess) return cuda_fail(e, fn);
   return ok();
 }

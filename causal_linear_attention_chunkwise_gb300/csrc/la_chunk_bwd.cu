@@ -1,0 +1,265 @@
+// la_chunk_bwd.cu -- backward pass of chunkwise linear attention: the plan, the
+// states between segments, and the decays' gradients from their shares.
+#include <algorithm>
+#include <cmath>
+
+#include "la_chunk_bwd.cuh"
+
+namespace la {
+
+cudaError_t launch_chunk_bwd_bf16(const ChunkBwd &p, int seqs, bool wide, bool planes,
+                                  cudaStream_t stream);
+cudaError_t launch_chunk_bwd_f32(const ChunkBwd &p, int seqs, bool wide, bool bf16,
+                                 cudaStream_t stream);
+
+namespace {
+
+constexpr int kMaxPer = 512;  // chunks of a segment (the decays' kernel keeps sums of them)
+
+// How a call runs: which planes, the chunk, the segments.
+struct Plan {
+  bool wide;    // padded width 128, else 64
+  bool full;    // inputs as three planes
+  bool planes;  // states as three planes
+  int chunk, chunks, segments, per;
+};
+
+// The segments that take the least time on 152 SMs, in units of a chunk of both
+// walks: whole waves of blocks, each a segment's chunks; with more than one segment also
+// the pass over their own shares (about 0.4 of a chunk's time) and its two launches.
+Plan make_plan(const ChunkBwdArgs &a, bool f32_out) {
+  Plan p;
+  p.wide = std::max(a.dk, a.dv) > 64;
+  p.full = a.dtype == LA_F32 || (f32_out && a.phi == LA_PHI_ELU1);
+  p.planes = p.full || f32_out;
+  p.chunk = p.full ? 32 : 64;
+  p.chunks = (a.L + p.chunk - 1) / p.chunk;
+  const long long seqs = (long long)a.B * a.H;
+  const long long slots = 152ll * (p.wide ? 1 : p.planes && !p.full ? 2 : 3);
+  double best = 0;
+  p.per = 0;
+  for (int n = (p.chunks + kMaxPer - 1) / kMaxPer; n <= p.chunks; ++n) {
+    const int per = (p.chunks + n - 1) / n;
+    if ((p.chunks + per - 1) / per != n) continue;
+    const long long waves = (seqs * n + slots - 1) / slots;
+    const long long share_waves = (2 * seqs * (n - 1) + 2 * slots - 1) / (2 * slots);
+    const double cost = (double)waves * (per + 1) + (n > 1 ? 0.4 * share_waves * per + 4 : 0);
+    if (p.per == 0 || cost < best) best = cost, p.per = per, p.segments = n;
+    if (waves > 4 && n > 1) break;  // finer cuts only add to the work
+  }
+  return p;
+}
+
+size_t round_up(size_t n) { return (n + 255) & ~(size_t)255; }
+
+// The workspace's parts, one behind the other; `base` NULL: their size alone.
+size_t lay_out(const ChunkBwdArgs &a, const Plan &plan, bool decay_grad, char *base, ChunkBwd *p,
+               float **by_segment) {
+  const size_t seqs = (size_t)a.B * a.H, es = (size_t)a.dk * a.dv;
+  size_t at = 0;
+  auto part = [&](size_t floats) {
+    float *r = reinterpret_cast<float *>(base + at);
+    at += round_up(floats * sizeof(float));
+    return base ? r : nullptr;
+  };
+  if (plan.segments > 1) {
+    float *u = part(seqs * (plan.segments - 1) * es), *w = part(seqs * (plan.segments - 1) * es);
+    float *total = part(seqs * plan.segments);
+    if (p) p->U = u, p->W = w, p->total = total;
+  }
+  if (decay_grad) {
+    float *rq = part(seqs * a.L), *rk = part(seqs * a.L), *rc = part(seqs * a.L);
+    float *around = part(seqs * plan.segments), *sums = part(seqs * plan.segments);
+    if (p) p->rq = rq, p->rk = rk, p->rc = rc, p->around = around, *by_segment = sums;
+  }
+  return at;
+}
+
+// U: each segment's own share of S becomes the state behind it; W: its own share of G (of
+// segment s + 1 at s) becomes the gradient of the state behind segment s.  Thread: four elements.
+__global__ void __launch_bounds__(256) segment_scan_kernel(const ChunkBwd p, int vecs) {
+  const int vec = blockIdx.x * 256 + threadIdx.x, seq = blockIdx.y;
+  if (vec >= vecs) return;
+  const int n = p.segments - 1;
+  const bool back = blockIdx.z != 0;
+  const float4 *first = reinterpret_cast<const float4 *>(back ? p.dSf : p.S0);
+  float4 cur = first ? first[(size_t)seq * vecs + vec] : make_float4(0.f, 0.f, 0.f, 0.f);
+  float4 *share = reinterpret_cast<float4 *>(back ? p.W : p.U) + (size_t)seq * n * vecs + vec;
+  const float *total = p.total + (size_t)seq * p.segments;
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) {
+    const int s = back ? n - 1 - i : i;
+    const float f = ex2_approx(total[back ? s + 1 : s]);
+    const float4 x = share[(size_t)s * vecs];
+    cur.x = fmaf(f, cur.x, x.x), cur.y = fmaf(f, cur.y, x.y);
+    cur.z = fmaf(f, cur.z, x.z), cur.w = fmaf(f, cur.w, x.w);
+    share[(size_t)s * vecs] = cur;
+  }
+}
+
+// A block: the tokens of one segment.  Their decays' gradients from the shares:
+//     sum over s >= t of rq + sum over s < t of rk + pairs within the chunk + around,
+// with `around` = <G, e^L_C S> given for the segment's last chunk; with the chunk's rq it
+// is <G, S> in front of the chunk, and that less the next chunk's rk is its `around`.
+template <int C>
+__global__ void __launch_bounds__(256)
+decay_grad_kernel(const ChunkBwd p, float *ddecay, float *by_segment) {
+  __shared__ float sum_q[kMaxPer], sum_k[kMaxPer], all[kMaxPer];
+  __shared__ double share[8];
+  constexpr int N = C / 32;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int seq = blockIdx.x / p.segments, seg = blockIdx.x % p.segments;
+  const int c0 = seg * p.per, n = min(p.per, p.chunks - c0);
+  const size_t base = (size_t)seq * p.L;
+  for (int c = warp; c < n; c += 8) {
+    float q = 0.f, k = 0.f, a = 0.f;
+    for (int i = 0; i < N; ++i) {
+      const int t = (c0 + c) * C + lane * N + i;
+      if (t >= p.L) break;
+      q += p.rq[base + t];
+      k += p.rk[base + t];
+      a += (float)log2_decay(p, seq, t);
+    }
+    for (int off = 16; off > 0; off >>= 1) {
+      q += __shfl_xor_sync(0xffffffffu, q, off);
+      k += __shfl_xor_sync(0xffffffffu, k, off);
+      a += __shfl_xor_sync(0xffffffffu, a, off);
+    }
+    if (lane == 0) sum_q[c] = q, sum_k[c] = k, all[c] = a;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    float around = p.around[(size_t)seq * p.segments + seg];
+    for (int c = n - 1; c >= 0; --c) {
+      const float y = around + sum_q[c];
+      // Past a decay of 2^-40 nothing of <G, S> is left but the rounding of y.
+      const float next = c > 0 && all[c - 1] >= -40.f ? y - sum_k[c - 1] : 0.f;
+      all[c] = around;
+      around = next;
+    }
+  }
+  __syncthreads();
+  double total = 0.0;
+  for (int c = warp; c < n; c += 8) {
+    float q[N], k[N], r[N];
+    float sq = 0.f, sk = 0.f, sr = 0.f;
+    for (int i = 0; i < N; ++i) {
+      const int t = (c0 + c) * C + lane * N + i;
+      q[i] = t < p.L ? p.rq[base + t] : 0.f;
+      k[i] = t < p.L ? p.rk[base + t] : 0.f;
+      r[i] = t < p.L ? p.rc[base + t] : 0.f;
+      sq += q[i], sk += k[i], sr += r[i];
+    }
+    // sums over the lanes behind (q, r) and in front (k, r)
+    float q_behind = 0.f, k_before = 0.f, r_behind = 0.f, r_before = 0.f;
+    float xq = sq, xk = sk, xr = sr, yr = sr;
+    for (int off = 1; off < 32; off <<= 1) {
+      const float dq = __shfl_down_sync(0xffffffffu, xq, off);
+      const float dr = __shfl_down_sync(0xffffffffu, xr, off);
+      const float dk = __shfl_up_sync(0xffffffffu, xk, off);
+      const float er = __shfl_up_sync(0xffffffffu, yr, off);
+      if (lane + off < 32) xq += dq, xr += dr;
+      if (lane >= off) xk += dk, yr += er;
+    }
+    q_behind = __shfl_down_sync(0xffffffffu, xq, 1);
+    r_behind = __shfl_down_sync(0xffffffffu, xr, 1);
+    k_before = __shfl_up_sync(0xffffffffu, xk, 1);
+    r_before = __shfl_up_sync(0xffffffffu, yr, 1);
+    if (lane == 31) q_behind = r_behind = 0.f;
+    if (lane == 0) k_before = r_before = 0.f;
+    for (int i = 0; i < N; ++i) {
+      const int t = (c0 + c) * C + lane * N + i;
+      float g = q_behind, pairs = lane < 16 ? -r_before : r_behind, before = k_before;
+      for (int j = 0; j < N; ++j) {
+        if (j >= i) g += q[j];
+        if (j < i) before += k[j];
+        if (lane < 16 && j < i) pairs -= r[j];
+        if (lane >= 16 && j >= i) pairs += r[j];
+      }
+      g += before + pairs + all[c];
+      if (t >= p.L) continue;
+      if (p.decay_kind == LA_DECAY_GATE_LOGIT) {
+        const float x = p.decay[base + t];
+        g *= -1.f / (1.f + expf(-x));
+      }
+      if (p.decay_kind == LA_DECAY_HEAD) total += g;
+      else ddecay[base + t] = g;
+    }
+  }
+  if (p.decay_kind != LA_DECAY_HEAD) return;
+  for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
+  if (lane == 0) share[warp] = total;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int i = 1; i < 8; ++i) total += share[i];
+    by_segment[blockIdx.x] = (float)total;
+  }
+}
+
+// ddecay[h]: the shares of head h's segments in all sequences, in order.
+__global__ void __launch_bounds__(32)
+head_decay_kernel(const float *by_segment, float *ddecay, int B, int H, int segments) {
+  const int h = blockIdx.x;
+  double s = 0.0;
+  for (long long i = threadIdx.x; i < (long long)B * segments; i += 32)
+    s += by_segment[(i / segments * H + h) * segments + i % segments];
+  for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+  if (threadIdx.x == 0) ddecay[h] = (float)s;
+}
+
+}  // namespace
+
+cudaError_t launch_segment_scan(const ChunkBwd &p, int seqs, cudaStream_t stream) {
+  const int vecs = p.n_k * p.n_v / 4;
+  // y: sequences; z: forward, backward
+  const int y = std::min(seqs, 32768);
+  for (int s = 0; s < seqs; s += y) {
+    ChunkBwd part = p;
+    const size_t es = (size_t)p.n_k * p.n_v, n = p.segments - 1;
+    part.U += s * n * es, part.W += s * n * es, part.total += (size_t)s * p.segments;
+    if (part.S0) part.S0 += s * es;
+    if (part.dSf) part.dSf += s * es;
+    segment_scan_kernel<<<dim3((vecs + 255) / 256, std::min(y, seqs - s), 2), 256, 0, stream>>>(
+        part, vecs);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+size_t chunk_bwd_workspace_bytes(const ChunkBwdArgs &a) {
+  // Enough for either feature map and any set of outputs.
+  size_t most = 0;
+  for (int phi : {LA_PHI_IDENTITY, LA_PHI_ELU1})
+    for (bool f32_out : {false, true}) {
+      ChunkBwdArgs b = a;
+      b.phi = phi;
+      most = std::max(most, lay_out(b, make_plan(b, f32_out), true, nullptr, nullptr, nullptr));
+    }
+  return most;
+}
+
+cudaError_t launch_chunk_bwd(const ChunkBwdArgs &a) {
+  const bool decay_grad = a.ddecay != nullptr, f32_out = decay_grad || a.dS0;
+  const Plan plan = make_plan(a, f32_out);
+  const long long seqs = (long long)a.B * a.H, blocks = seqs * plan.segments;
+  if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+  ChunkBwd p{a.q, a.k, a.v, a.dO, a.dq, a.dk_out, a.dv_out, a.decay, a.S0, a.dS_final, a.dS0,
+             a.H, a.L, a.dk, a.dv, a.phi, a.decay_kind, plan.chunks, plan.segments, plan.per,
+             nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr};
+  float *by_segment = nullptr;
+  lay_out(a, plan, decay_grad, static_cast<char *>(a.workspace), &p, &by_segment);
+  cudaError_t e =
+      plan.full ? launch_chunk_bwd_f32(p, (int)seqs, plan.wide, a.dtype == LA_BF16, a.stream)
+                : launch_chunk_bwd_bf16(p, (int)seqs, plan.wide, plan.planes, a.stream);
+  if (e != cudaSuccess || !decay_grad) return e;
+  if (plan.chunk == 32)
+    decay_grad_kernel<32><<<(unsigned)blocks, 256, 0, a.stream>>>(p, a.ddecay, by_segment);
+  else
+    decay_grad_kernel<64><<<(unsigned)blocks, 256, 0, a.stream>>>(p, a.ddecay, by_segment);
+  if ((e = cudaGetLastError()) != cudaSuccess || a.decay_kind != LA_DECAY_HEAD) return e;
+  head_decay_kernel<<<a.H, 32, 0, a.stream>>>(by_segment, a.ddecay, a.B, a.H, plan.segments);
+  return cudaGetLastError();
+}
+
+}  // namespace la

@@ -1,0 +1,770 @@
+// la_chunk_bwd.cuh -- backward pass of chunkwise linear attention: the kernels.
+//
+// With S_t = a_t S_{t-1} + k_t v_t^T, o_t = S_t^T q_t (q, k after phi) and G_t the
+// gradient of S_t, G_t = q_t do_t^T + a_{t+1} G_{t+1}:
+//
+//     dq_t = S_t do_t,   dk_t = G_t v_t,   dv_t = G_t^T k_t,   dlog a_t = a_t <G_t, S_{t-1}>.
+//
+// In chunks of C tokens, with L_t the sum of the log decays of the chunk's tokens up to t, D_ji =
+// e^(L_j - L_i) for j >= i (else 0), S the state before the chunk and G the gradient
+// of the state behind it:
+//
+//     dq = (dO V^T . D) K + e^L dO S^T             S <- e^L_C S + (e^(L_C - L) K)^T V
+//     dk = (dO V^T . D)^T Q + e^(L_C - L) V G^T    G <- e^L_C G + (e^L Q)^T dO
+//     dv = (Q K^T . D)^T dO + e^(L_C - L) K G
+//
+// dq needs S, which runs forward; dk and dv need G, which runs backward.  So two
+// kernels, each one walk over the chunks with its state in registers (fp32).  A warp
+// owns 16 tokens and computes its rows of the chunk's score matrices in the
+// orientation that its products need (dO V^T for dq, V dO^T and K Q^T for dk and
+// dv), so scores go from accumulators to operands within a thread, never through
+// shared memory.  A long sequence is cut into segments that run side by side: a
+// first kernel forms every segment's own share of S and G, a second one strings them
+// together.
+//
+// A decay's gradient counts the pairs (i < t <= j) that it lies between: pairs within
+// the chunk (row and column sums of Q K^T . dO V^T . D), pairs with one token in it (dot
+// products of the rows of dq's and dk's second terms with q and k), and pairs
+// around it (<G, e^L_C S>, which follows from chunk to chunk by the same sums).
+// Formed this way nothing cancels beyond one chunk; q dq - k dk summed from the
+// sequence's end would lose the short decays to the long sums.
+//
+// Precision.  Products run in bf16 with fp32 sums.  With bf16 inputs and outputs the
+// decayed scores and the states round once to bf16 as operands (the state itself
+// stays fp32).  The fp32 outputs (ddecay, dS0) take those operands as three bf16
+// planes, which hold all of an fp32 value's bits; fp32 inputs, and phi = elu + 1
+// where an fp32 output is wanted, enter as three planes too.
+#pragma once
+
+#include <cstdint>
+
+#include "../../include/la_gb300.h"
+#include "la_act.cuh"
+#include "la_internal.h"
+#include "la_mma.cuh"
+
+namespace la {
+
+// What the kernels get: the tensors, and the plan.
+struct ChunkBwd {
+  const void *q, *k, *v, *dO;
+  void *dq, *dk, *dv;
+  const float *decay, *S0, *dSf;
+  float *dS0;
+  int H, L, n_k, n_v;          // n_k, n_v: d_k and d_v
+  int phi, decay_kind;
+  int chunks, segments, per;   // per: chunks of a segment
+  float *U, *W;                // [seq][segments - 1][d_k d_v]: states between segments
+  float *total;                // [seq][segments] log2 of a segment's decay
+  float *rq, *rk, *rc;         // [seq][L] shares of ddecay, or null
+  float *around;               // [seq][segments] <G, e^L_C S> of a segment's last chunk
+};
+
+// T: element type; D: padded width (d_k, d_v <= D); C: tokens of a chunk; NI: planes of the
+// inputs; NM: planes of the states and of what enters them.
+template <typename T_, int D_, int C_, int NI_, int NM_> struct BwdConfig {
+  using T = T_;
+  static constexpr int D = D_, C = C_, NI = NI_, NM = NM_;
+  static constexpr int NO = NI == 1 ? 1 : 3;   // planes of scores
+  static constexpr int WARPS = D / 16;         // each owns 16 rows of the state
+  static constexpr int ROWS = C / 16;          // groups of 16 tokens
+  static constexpr int SPLIT = WARPS / ROWS;   // warps that share a group, by columns
+  static constexpr int COLS = D / SPLIT;       // columns of a warp's outputs
+  static constexpr int THREADS = WARPS * 32;
+  // Tiles of the next chunk arrive while this one is worked on.
+  static constexpr int STAGES = sizeof(T) == 2 && NI == 1 ? 2 : 1;
+  static constexpr int BLOCKS = D == 64 ? 3 : 1;  // to an SM
+  static constexpr uint32_t TILE = C * D * 2;  // bytes of one plane
+  static constexpr uint32_t STATE = D * D * 2;
+  static_assert(WARPS % ROWS == 0 && COLS % 16 == 0, "whole column tiles");
+};
+
+// Per-chunk decay factors in shared memory.
+template <int C> struct ChunkDecay {
+  float2 lam[C];  // log2 of the decay from the chunk's start, as a sum of two floats
+  float head[C];  // e^L
+  float tail[C];  // e^(L_C - L)
+  float all;      // e^L_C
+};
+
+// log2 of token t's decay.  Below e^-200 it counts as e^-200, which is 0 in fp32 in
+// whatever it multiplies; a sum of infinities would be NaN.
+__device__ __forceinline__ double log2_decay(const ChunkBwd &p, int seq, int t) {
+  if (p.decay_kind == LA_DECAY_NONE || t >= p.L) return 0.0;
+  const long long at = (long long)seq * p.L + t;
+  float a;
+  if (p.decay_kind == LA_DECAY_HEAD) a = p.decay[seq % p.H];
+  else if (p.decay_kind == LA_DECAY_TOKEN) a = p.decay[at];
+  else a = neg_softplus(p.decay[at]);
+  return (double)(a < -200.f ? -200.f : a) * 1.4426950408889634;
+}
+
+// One warp fills the factors of the chunk at token t0.  The sums run in 64 bits:
+// in fp32 a sum of 50 would leave differences of neighbours 4e-6.
+template <int C>
+__device__ __forceinline__ void chunk_decay(const ChunkBwd &p, int seq, int t0, ChunkDecay<C> &s,
+                                            int lane) {
+  constexpr int N = C / 32;
+  double a[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    a[i] = log2_decay(p, seq, t0 + lane * N + i);
+    if (i) a[i] += a[i - 1];
+  }
+  double run = a[N - 1];
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const double x = __shfl_up_sync(0xffffffffu, run, off);
+    if (lane >= off) run += x;
+  }
+  const double before = run - a[N - 1], total = __shfl_sync(0xffffffffu, run, 31);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const double x = before + a[i];
+    const float hi = (float)x;
+    s.lam[lane * N + i] = make_float2(hi, (float)(x - hi));
+    s.head[lane * N + i] = ex2_approx(hi);
+    s.tail[lane * N + i] = ex2_approx((float)(total - x));
+  }
+  if (lane == 0) s.all = ex2_approx((float)total);
+}
+
+// The decay between two tokens.
+__device__ __forceinline__ float decay_between(float2 later, float2 earlier) {
+  return ex2_approx((later.x - earlier.x) + (later.y - earlier.y));
+}
+
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(live ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_done() {
+  asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+}
+
+// Rows t0 .. t0 + C - 1 of a [L, width] tensor into a tile; zeros past the last token
+// and past the width.  phi (if MAP) is applied on the way where the planes are
+// formed here, and by map_tile afterwards where the copy is asynchronous.
+template <typename F, bool MAP>
+__device__ __forceinline__ void load_tile(uint32_t tile, const void *src, const ChunkBwd &p,
+                                          int width, int t0) {
+  using T = typename F::T;
+  constexpr int VECS = F::C * F::D / 8;
+  const T *rows = static_cast<const T *>(src);
+#pragma unroll
+  for (int i = 0; i < VECS / F::THREADS; ++i) {
+    const int vec = threadIdx.x + i * F::THREADS;
+    const int r = vec / (F::D / 8), c = vec % (F::D / 8) * 8;
+    const bool live = t0 + r < p.L && c < width;
+    const T *from = rows + (live ? (long long)(t0 + r) * width + c : 0);
+    const uint32_t to = tile + tile_offset<F::D>(r, c);
+    if constexpr (F::STAGES == 2) {
+      cp_async_16(to, from, live);
+    } else {
+      float f[8];
+      if constexpr (sizeof(T) == 2) load_raw<T, 8>(from).unpack(f);
+      else load_raw<T, 4>(from).unpack(f), load_raw<T, 4>(from + 4).unpack(f + 4);
+      uint32_t out[F::NI][4];
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) {
+        const float x = live ? MAP ? feature_map_precise(p.phi, f[e]) : f[e] : 0.f;
+        const float y = live ? MAP ? feature_map_precise(p.phi, f[e + 1]) : f[e + 1] : 0.f;
+        split<F::NI>(x, y, &out[0][e / 2], 4);
+      }
+#pragma unroll
+      for (int n = 0; n < F::NI; ++n)
+        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(to + n * F::TILE),
+                     "r"(out[n][0]), "r"(out[n][1]), "r"(out[n][2]), "r"(out[n][3])
+                     : "memory");
+    }
+  }
+}
+
+// phi = elu + 1 of a tile that arrived as it is, rounded to bf16; rows past the last
+// token stay zero.
+template <typename F>
+__device__ __forceinline__ void map_tile(uint32_t tile, const ChunkBwd &p, int width, int t0) {
+  constexpr int VECS = F::C * F::D / 8;
+#pragma unroll
+  for (int i = 0; i < VECS / F::THREADS; ++i) {
+    const int vec = threadIdx.x + i * F::THREADS;
+    const int r = vec / (F::D / 8), c = vec % (F::D / 8) * 8;
+    if (t0 + r >= p.L || c >= width) continue;
+    const uint32_t at = tile + tile_offset<F::D>(r, c);
+    uint32_t w[4];
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(at));
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      w[e] = pack_bf16(feature_map(p.phi, bf16_lo(w[e])), feature_map(p.phi, bf16_hi(w[e])));
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(w[0]), "r"(w[1]),
+                 "r"(w[2]), "r"(w[3])
+                 : "memory");
+  }
+}
+
+// A warp's 16 rows of a state, as accumulators: row g or g + 8, columns 8 n + 2 (lane % 4).
+template <typename F> struct StateRows {
+  float c[F::D / 8][4];
+
+  __device__ __forceinline__ void load(const float *src, const ChunkBwd &p, int warp, int lane) {
+#pragma unroll
+    for (int n = 0; n < F::D / 8; ++n)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int row = warp * 16 + lane / 4 + 8 * h, col = n * 8 + lane % 4 * 2;
+        float2 x = make_float2(0.f, 0.f);
+        if (src && row < p.n_k && col < p.n_v)
+          x = *reinterpret_cast<const float2 *>(src + (size_t)row * p.n_v + col);
+        c[n][2 * h] = x.x, c[n][2 * h + 1] = x.y;
+      }
+  }
+  __device__ __forceinline__ void store(float *dst, const ChunkBwd &p, int warp, int lane) const {
+#pragma unroll
+    for (int n = 0; n < F::D / 8; ++n)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int row = warp * 16 + lane / 4 + 8 * h, col = n * 8 + lane % 4 * 2;
+        if (row < p.n_k && col < p.n_v)
+          *reinterpret_cast<float2 *>(dst + (size_t)row * p.n_v + col) =
+              make_float2(c[n][2 * h], c[n][2 * h + 1]);
+      }
+  }
+  // The state as planes of a bf16 tile [d_k][d_v].
+  __device__ __forceinline__ void planes(char *tile, int warp, int lane) const {
+#pragma unroll
+    for (int n = 0; n < F::D / 8; ++n)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t w[F::NM];
+        split<F::NM>(c[n][2 * h], c[n][2 * h + 1], w, 1);
+        const uint32_t at = tile_offset<F::D>(warp * 16 + lane / 4 + 8 * h, n * 8 + lane % 4 * 2);
+#pragma unroll
+        for (int m = 0; m < F::NM; ++m)
+          *reinterpret_cast<uint32_t *>(tile + m * F::STATE + at) = w[m];
+      }
+  }
+  // c <- all c + sum over tokens of weight x (x) y: x's tile [token][d_k], y's [token][d_v].
+  // A chunk's sum is formed by itself and then added, with an fp32 rounding: the tensor
+  // cores' cuts would add up over the chunks.
+  __device__ __forceinline__ void update(uint32_t x, uint32_t y, const float *weight, float all,
+                                         int warp, int lane) {
+    uint32_t w[F::C / 16][F::NM][4];
+#pragma unroll
+    for (int k = 0; k < F::C / 16; ++k) {
+      uint32_t a[F::NI][4];
+#pragma unroll
+      for (int i = 0; i < F::NI; ++i)
+        frag_a_t<F::D>(a[i], x + i * F::TILE, warp * 16, k * 16, lane);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {  // registers 2 and 3 hold the tokens 8 further on
+        const float2 f =
+            *reinterpret_cast<const float2 *>(weight + k * 16 + (r / 2) * 8 + lane % 4 * 2);
+        float lo = 0.f, hi = 0.f;
+#pragma unroll
+        for (int i = F::NI - 1; i >= 0; --i) lo += bf16_lo(a[i][r]), hi += bf16_hi(a[i][r]);
+        split<F::NM>(lo * f.x, hi * f.y, &w[k][0][r], 4);
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < F::D / 8; n += 2) {
+      float sum[2][4] = {}, small[2][4] = {};
+#pragma unroll
+      for (int k = 0; k < F::C / 16; ++k) {
+        uint32_t b[F::NI][4];
+#pragma unroll
+        for (int i = 0; i < F::NI; ++i)
+          frag_b_t<F::D>(b[i], y + i * F::TILE, n * 8, k * 16, lane);
+        mma_planes<F::NM, F::NI>(sum[0], sum[1], small[0], small[1], w[k], b);
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          c[n + j][e] = fmaf(all, c[n + j][e], F::NM > 1 ? sum[j][e] + small[j][e] : sum[j][e]);
+    }
+  }
+};
+
+// acc += small where there were small products.
+template <bool ANY, int NT>
+__device__ __forceinline__ void add_small(float (&acc)[NT][4], const float (&small)[NT][4]) {
+  if constexpr (ANY) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[n][e] += small[n][e];
+  }
+}
+
+// acc[n] += X Y^T over the widths: rows m0 .. of X's tile, rows n0 + 16 j of Y's (live(j)).
+template <typename F, int NT, int NX, int NY, typename Live>
+__device__ __forceinline__ void rows_times_rows(float (&acc)[NT][4], uint32_t x, uint32_t x_plane,
+                                                int m0, uint32_t y, uint32_t y_plane, int n0,
+                                                int lane, Live live) {
+  float small[NT][4] = {};
+#pragma unroll
+  for (int k0 = 0; k0 < F::D; k0 += 16) {
+    uint32_t a[NX][4];
+#pragma unroll
+    for (int i = 0; i < NX; ++i) frag_a<F::D>(a[i], x + i * x_plane, m0, k0, lane);
+#pragma unroll
+    for (int j = 0; j < NT / 2; ++j) {
+      if (!live(j)) continue;
+      uint32_t b[NY][4];
+#pragma unroll
+      for (int i = 0; i < NY; ++i) frag_b<F::D>(b[i], y + i * y_plane, n0 + j * 16, k0, lane);
+      mma_planes<NX, NY>(acc[2 * j], acc[2 * j + 1], small[2 * j], small[2 * j + 1], a, b);
+    }
+  }
+  add_small<(NX > 1 || NY > 1)>(acc, small);
+}
+
+// acc[n] += X Y: rows m0 .. of X's tile, columns n0 + 8 n of Y's.
+template <typename F, int NT, int NX, int NY>
+__device__ __forceinline__ void rows_times_cols(float (&acc)[NT][4], uint32_t x, uint32_t x_plane,
+                                                int m0, uint32_t y, uint32_t y_plane, int n0,
+                                                int lane) {
+  float small[NT][4] = {};
+#pragma unroll
+  for (int k0 = 0; k0 < F::D; k0 += 16) {
+    uint32_t a[NX][4];
+#pragma unroll
+    for (int i = 0; i < NX; ++i) frag_a<F::D>(a[i], x + i * x_plane, m0, k0, lane);
+#pragma unroll
+    for (int n = 0; n < NT; n += 2) {
+      uint32_t b[NY][4];
+#pragma unroll
+      for (int i = 0; i < NY; ++i) frag_b_t<F::D>(b[i], y + i * y_plane, n0 + n * 8, k0, lane);
+      mma_planes<NX, NY>(acc[n], acc[n + 1], small[n], small[n + 1], a, b);
+    }
+  }
+  add_small<(NX > 1 || NY > 1)>(acc, small);
+}
+
+// acc[n] += W Y over the chunk's tokens: W scores in accumulators (tiles of 8 tokens), Y's tile
+// [token][.], columns n0 + 8 n.
+template <typename F, int NT, typename Live>
+__device__ __forceinline__ void scores_times_cols(float (&acc)[NT][4],
+                                                  const float (&w)[F::C / 8][4], uint32_t y,
+                                                  int n0, int lane, Live live) {
+  float small[NT][4] = {};
+#pragma unroll
+  for (int j = 0; j < F::C / 16; ++j) {
+    if (!live(j)) continue;
+    uint32_t a[F::NO][4];
+    split<F::NO>(w[2 * j][0], w[2 * j][1], &a[0][0], 4);
+    split<F::NO>(w[2 * j][2], w[2 * j][3], &a[0][1], 4);
+    split<F::NO>(w[2 * j + 1][0], w[2 * j + 1][1], &a[0][2], 4);
+    split<F::NO>(w[2 * j + 1][2], w[2 * j + 1][3], &a[0][3], 4);
+#pragma unroll
+    for (int n = 0; n < NT; n += 2) {
+      uint32_t b[F::NI][4];
+#pragma unroll
+      for (int i = 0; i < F::NI; ++i) frag_b_t<F::D>(b[i], y + i * F::TILE, n0 + n * 8, j * 16, lane);
+      mma_planes<F::NO, F::NI>(acc[n], acc[n + 1], small[n], small[n + 1], a, b);
+    }
+  }
+  add_small<(F::NO > 1 || F::NI > 1)>(acc, small);
+}
+
+// A warp's 16 x COLS outputs to rows t0 + r0 + .. of a [L, width] tensor; with phi = elu + 1
+// times its derivative at raw (e^x up to 0, then 1).
+template <typename F, int NT>
+__device__ __forceinline__ void store_rows(const float (&acc)[NT][4], void *dst, const void *raw,
+                                           const ChunkBwd &p, int width, int t, int n0, int lane) {
+  using T = typename F::T;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int row = t + lane / 4 + 8 * h;
+    if (row >= p.L) continue;
+    T *to = static_cast<T *>(dst) + (long long)row * width;
+    const T *x = static_cast<const T *>(raw) + (long long)row * width;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int c = n0 + n * 8 + lane % 4 * 2;
+      if (c >= width) continue;
+      float f[2] = {acc[n][2 * h], acc[n][2 * h + 1]};
+      if (raw && p.phi == LA_PHI_ELU1) {
+        float y[2];
+        if constexpr (sizeof(T) == 4) load_raw<T, 2>(x + c).unpack(y);
+        else load_raw<T, 2>(x + c).unpack(y);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) f[e] *= y[e] > 0.f ? 1.f : expf(y[e]);
+      }
+      store_vec<T, 2>(to + c, f);
+    }
+  }
+}
+
+// <a row of acc, the same row of x after phi>, summed over a warp's columns: rows g and g + 8.
+template <typename F, int NT>
+__device__ __forceinline__ float2 row_dots(const float (&acc)[NT][4], const void *raw,
+                                           const ChunkBwd &p, int width, int t, int n0, int lane) {
+  using T = typename F::T;
+  float s[2] = {0.f, 0.f};
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int row = t + lane / 4 + 8 * h;
+    if (row < p.L) {
+      const T *x = static_cast<const T *>(raw) + (long long)row * width;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const int c = n0 + n * 8 + lane % 4 * 2;
+        if (c >= width) continue;
+        float y[2];
+        load_raw<T, 2>(x + c).unpack(y);
+        s[h] = fmaf(acc[n][2 * h], feature_map_precise(p.phi, y[0]), s[h]);
+        s[h] = fmaf(acc[n][2 * h + 1], feature_map_precise(p.phi, y[1]), s[h]);
+      }
+    }
+    s[h] += __shfl_xor_sync(0xffffffffu, s[h], 1);
+    s[h] += __shfl_xor_sync(0xffffffffu, s[h], 2);
+  }
+  return make_float2(s[0], s[1]);
+}
+
+template <typename F> struct BwdShared {
+  ChunkDecay<F::C> decay;
+  float rows[F::SPLIT][F::C];  // row sums of the warps that share a group
+  float cols[F::ROWS][F::C];   // column sums of the groups
+  float sum[F::WARPS];
+};
+template <typename F> constexpr uint32_t bwd_shared_bytes() {
+  return (sizeof(BwdShared<F>) + 127) / 128 * 128;
+}
+
+// The segment's own share of S (blockIdx.y = 0: segments 0 .. n - 2) or of G (1: segments 1 .. n - 1).
+template <typename F> constexpr uint32_t share_smem() {
+  return bwd_shared_bytes<F>() + 2 * F::STAGES * F::NI * F::TILE;
+}
+template <typename F>
+__global__ void __launch_bounds__(F::THREADS) segment_share_kernel(const ChunkBwd p) {
+  extern __shared__ __align__(128) char smem[];
+  auto &sh = *reinterpret_cast<BwdShared<F> *>(smem);
+  const uint32_t tiles = smem_u32(smem) + bwd_shared_bytes<F>();
+  constexpr uint32_t X = F::NI * F::TILE, STAGE = 2 * X;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int seq = blockIdx.x / (p.segments - 1), of = blockIdx.x % (p.segments - 1);
+  const bool back = blockIdx.y != 0;
+  const int seg = back ? of + 1 : of;
+  const int c0 = seg * p.per, c1 = min(c0 + p.per, p.chunks), n = c1 - c0;
+  const size_t ek = (size_t)seq * p.L * p.n_k, ev = (size_t)seq * p.L * p.n_v;
+  using T = typename F::T;
+  const T *x = static_cast<const T *>(back ? p.q : p.k) + ek;
+  const T *y = static_cast<const T *>(back ? p.dO : p.v) + ev;
+  auto token = [&](int i) { return (back ? c1 - 1 - i : c0 + i) * F::C; };
+  auto load = [&](int i) {
+    const uint32_t at = tiles + (F::STAGES == 2 ? (i & 1) * STAGE : 0);
+    load_tile<F, true>(at, x, p, p.n_k, token(i));
+    load_tile<F, false>(at + X, y, p, p.n_v, token(i));
+  };
+  StateRows<F> state;
+  state.load(nullptr, p, warp, lane);
+  double total = 0.0;
+  if (F::STAGES == 2) load(0);
+  for (int i = 0; i < n; ++i) {
+    const uint32_t at = tiles + (F::STAGES == 2 ? (i & 1) * STAGE : 0);
+    if (F::STAGES == 1) load(i);
+    if (warp == 0) {
+      chunk_decay<F::C>(p, seq, token(i), sh.decay, lane);
+      total += (double)sh.decay.lam[F::C - 1].x + sh.decay.lam[F::C - 1].y;
+    }
+    cp_async_done();
+    __syncthreads();
+    if (F::STAGES == 2 && p.phi == LA_PHI_ELU1) {
+      map_tile<F>(at, p, p.n_k, token(i));
+      __syncthreads();
+    }
+    if (F::STAGES == 2 && i + 1 < n) load(i + 1);
+    state.update(at, at + X, back ? sh.decay.head : sh.decay.tail, sh.decay.all, warp, lane);
+    __syncthreads();
+  }
+  const size_t slot = (size_t)seq * (p.segments - 1) + of;
+  state.store((back ? p.W : p.U) + slot * p.n_k * p.n_v, p, warp, lane);
+  if (threadIdx.x == 31 && (!back || seg == p.segments - 1))
+    p.total[(size_t)seq * p.segments + seg] = (float)total;
+}
+
+// dq: a walk forward over a segment's chunks.
+template <typename F> constexpr uint32_t grad_q_smem() {
+  return bwd_shared_bytes<F>() + 3 * F::STAGES * F::NI * F::TILE + F::NM * F::STATE;
+}
+template <typename F>
+__global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_q_kernel(const ChunkBwd p) {
+  extern __shared__ __align__(128) char smem[];
+  auto &sh = *reinterpret_cast<BwdShared<F> *>(smem);
+  char *state_tile = smem + bwd_shared_bytes<F>();
+  const uint32_t S = smem_u32(state_tile), tiles = S + F::NM * F::STATE;
+  constexpr uint32_t X = F::NI * F::TILE, STAGE = 3 * X;
+  constexpr int NT = F::COLS / 8;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int group = warp % F::ROWS, part = warp / F::ROWS;
+  const int r0 = group * 16, n0 = part * F::COLS;
+  const int seq = blockIdx.x / p.segments, seg = blockIdx.x % p.segments;
+  const int c0 = seg * p.per, c1 = min(c0 + p.per, p.chunks);
+  const size_t ek = (size_t)seq * p.L * p.n_k, ev = (size_t)seq * p.L * p.n_v;
+  const size_t es = (size_t)p.n_k * p.n_v;
+  using T = typename F::T;
+  const T *k = static_cast<const T *>(p.k) + ek, *v = static_cast<const T *>(p.v) + ev;
+  const T *q = static_cast<const T *>(p.q) + ek, *dO = static_cast<const T *>(p.dO) + ev;
+  auto load = [&](int c) {
+    const uint32_t at = tiles + (F::STAGES == 2 ? (c & 1) * STAGE : 0);
+    load_tile<F, true>(at, k, p, p.n_k, c * F::C);
+    load_tile<F, false>(at + X, v, p, p.n_v, c * F::C);
+    load_tile<F, false>(at + 2 * X, dO, p, p.n_v, c * F::C);
+  };
+  StateRows<F> state;
+  if (F::STAGES == 2) load(c0);
+  state.load(seg ? p.U + ((size_t)seq * (p.segments - 1) + seg - 1) * es
+                 : p.S0 ? p.S0 + (size_t)seq * es : nullptr, p, warp, lane);
+  state.planes(state_tile, warp, lane);
+  for (int c = c0; c < c1; ++c) {
+    const int t0 = c * F::C;
+    const uint32_t tk = tiles + (F::STAGES == 2 ? (c & 1) * STAGE : 0), tv = tk + X, td = tv + X;
+    if (F::STAGES == 1) load(c);
+    if (warp == 0) chunk_decay<F::C>(p, seq, t0, sh.decay, lane);
+    cp_async_done();
+    __syncthreads();
+    if (F::STAGES == 2 && p.phi == LA_PHI_ELU1) {
+      map_tile<F>(tk, p, p.n_k, t0);
+      __syncthreads();
+    }
+    if (F::STAGES == 2 && c + 1 < c1) load(c + 1);
+    // dO V^T . D: rows j of the group, tokens i <= j
+    float w[F::C / 8][4] = {};
+    auto live = [&](int j) { return j <= group; };
+    rows_times_rows<F, F::C / 8, F::NI, F::NI>(w, td, F::TILE, r0, tv, F::TILE, 0, lane, live);
+#pragma unroll
+    for (int n = 0; n < F::C / 8; ++n) {
+      if (n / 2 > group) continue;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int j = r0 + lane / 4 + e / 2 * 8, i = n * 8 + lane % 4 * 2 + e % 2;
+        if (p.decay_kind != LA_DECAY_NONE)
+          w[n][e] *= decay_between(sh.decay.lam[j], sh.decay.lam[i <= j ? i : j]);
+        w[n][e] = i <= j ? w[n][e] : 0.f;
+      }
+    }
+    float acc[NT][4] = {};
+    rows_times_rows<F, NT, F::NI, F::NM>(acc, td, F::TILE, r0, S, F::STATE, n0, lane,
+                                         [](int) { return true; });
+    const float h0 = sh.decay.head[r0 + lane / 4], h1 = sh.decay.head[r0 + lane / 4 + 8];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) acc[n][0] *= h0, acc[n][1] *= h0, acc[n][2] *= h1, acc[n][3] *= h1;
+    if (p.rq) {
+      const float2 d = row_dots<F, NT>(acc, q, p, p.n_k, t0 + r0, n0, lane);
+      if (lane % 4 == 0) {
+        sh.rows[part][r0 + lane / 4] = d.x;
+        sh.rows[part][r0 + lane / 4 + 8] = d.y;
+      }
+    }
+    scores_times_cols<F, NT>(acc, w, tk, n0, lane, live);
+    store_rows<F, NT>(acc, static_cast<T *>(p.dq) + ek, q, p, p.n_k, t0 + r0, n0, lane);
+    float around = 0.f;
+    if (c + 1 < c1) {
+      state.update(tk, tv, sh.decay.tail, sh.decay.all, warp, lane);
+    } else if (p.rq) {  // <G, e^L_C S>: the pairs around the segment's last chunk
+      const float *G = seg + 1 < p.segments ? p.W + ((size_t)seq * (p.segments - 1) + seg) * es
+                       : p.dSf ? p.dSf + (size_t)seq * es : nullptr;
+      if (G) {
+        StateRows<F> g;
+        g.load(G, p, warp, lane);
+#pragma unroll
+        for (int n = 0; n < F::D / 8; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) around = fmaf(g.c[n][e], state.c[n][e], around);
+      }
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) around += __shfl_xor_sync(0xffffffffu, around, off);
+      if (lane == 0) sh.sum[warp] = around * sh.decay.all;
+    }
+    __syncthreads();
+    if (p.rq && threadIdx.x < F::C && t0 + (int)threadIdx.x < p.L) {
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < F::SPLIT; ++i) s += sh.rows[i][threadIdx.x];
+      p.rq[(size_t)seq * p.L + t0 + threadIdx.x] = s;
+    }
+    if (c + 1 < c1) state.planes(state_tile, warp, lane);
+  }
+  if (p.rq && threadIdx.x == 0) {
+    float s = 0.f;
+    for (int i = 0; i < F::WARPS; ++i) s += sh.sum[i];
+    p.around[(size_t)seq * p.segments + seg] = s;
+  }
+}
+
+// dk and dv: a walk backward over a segment's chunks.
+template <typename F> constexpr uint32_t grad_kv_smem() {
+  return bwd_shared_bytes<F>() + 4 * F::STAGES * F::NI * F::TILE + F::NM * F::STATE;
+}
+template <typename F>
+__global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_kv_kernel(const ChunkBwd p) {
+  extern __shared__ __align__(128) char smem[];
+  auto &sh = *reinterpret_cast<BwdShared<F> *>(smem);
+  char *state_tile = smem + bwd_shared_bytes<F>();
+  const uint32_t G = smem_u32(state_tile), tiles = G + F::NM * F::STATE;
+  constexpr uint32_t X = F::NI * F::TILE, STAGE = 4 * X;
+  constexpr int NT = F::COLS / 8, CT = F::C / 8;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int group = warp % F::ROWS, part = warp / F::ROWS;
+  const int r0 = group * 16, n0 = part * F::COLS;
+  const int seq = blockIdx.x / p.segments, seg = blockIdx.x % p.segments;
+  const int c0 = seg * p.per, c1 = min(c0 + p.per, p.chunks);
+  const size_t ek = (size_t)seq * p.L * p.n_k, ev = (size_t)seq * p.L * p.n_v;
+  const size_t es = (size_t)p.n_k * p.n_v;
+  using T = typename F::T;
+  const T *k = static_cast<const T *>(p.k) + ek, *v = static_cast<const T *>(p.v) + ev;
+  const T *q = static_cast<const T *>(p.q) + ek, *dO = static_cast<const T *>(p.dO) + ev;
+  auto load = [&](int c) {
+    const uint32_t at = tiles + (F::STAGES == 2 ? (c & 1) * STAGE : 0);
+    load_tile<F, true>(at, q, p, p.n_k, c * F::C);
+    load_tile<F, true>(at + X, k, p, p.n_k, c * F::C);
+    load_tile<F, false>(at + 2 * X, v, p, p.n_v, c * F::C);
+    load_tile<F, false>(at + 3 * X, dO, p, p.n_v, c * F::C);
+  };
+  StateRows<F> state;
+  if (F::STAGES == 2) load(c1 - 1);
+  state.load(seg + 1 < p.segments ? p.W + ((size_t)seq * (p.segments - 1) + seg) * es
+             : p.dSf ? p.dSf + (size_t)seq * es : nullptr, p, warp, lane);
+  state.planes(state_tile, warp, lane);
+  for (int c = c1 - 1; c >= c0; --c) {
+    const int t0 = c * F::C;
+    const uint32_t tq = tiles + (F::STAGES == 2 ? (c & 1) * STAGE : 0);
+    const uint32_t tk = tq + X, tv = tk + X, td = tv + X;
+    if (F::STAGES == 1) load(c);
+    if (warp == 0) chunk_decay<F::C>(p, seq, t0, sh.decay, lane);
+    cp_async_done();
+    __syncthreads();
+    if (F::STAGES == 2 && p.phi == LA_PHI_ELU1) {
+      map_tile<F>(tq, p, p.n_k, t0);
+      map_tile<F>(tk, p, p.n_k, t0);
+      __syncthreads();
+    }
+    if (F::STAGES == 2 && c > c0) load(c - 1);
+    // K Q^T . D and V dO^T . D: rows i of the group, tokens j >= i
+    float w[CT][4] = {}, dw[CT][4] = {};
+    auto live = [&](int j) { return j >= group; };
+    rows_times_rows<F, CT, F::NI, F::NI>(w, tk, F::TILE, r0, tq, F::TILE, 0, lane, live);
+    rows_times_rows<F, CT, F::NI, F::NI>(dw, tv, F::TILE, r0, td, F::TILE, 0, lane, live);
+    float row_sum[2] = {0.f, 0.f};
+#pragma unroll
+    for (int n = 0; n < CT; ++n) {
+      float col[2] = {0.f, 0.f};
+      if (n / 2 >= group) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int i = r0 + lane / 4 + e / 2 * 8, j = n * 8 + lane % 4 * 2 + e % 2;
+          float f = 1.f;
+          if (p.decay_kind != LA_DECAY_NONE)
+            f = decay_between(sh.decay.lam[j], sh.decay.lam[i <= j ? i : j]);
+          const float pair = i < j ? w[n][e] * dw[n][e] * f : 0.f;
+          row_sum[e / 2] += pair;
+          col[e % 2] += pair;
+          w[n][e] = i <= j ? w[n][e] * f : 0.f;
+          dw[n][e] = i <= j ? dw[n][e] * f : 0.f;
+        }
+      }
+      if (p.rc && part == 0) {
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) {
+          col[0] += __shfl_xor_sync(0xffffffffu, col[0], off);
+          col[1] += __shfl_xor_sync(0xffffffffu, col[1], off);
+        }
+        if (lane < 4) {
+          sh.cols[group][n * 8 + lane * 2] = col[0];
+          sh.cols[group][n * 8 + lane * 2 + 1] = col[1];
+        }
+      }
+    }
+    const float t_0 = sh.decay.tail[r0 + lane / 4], t_1 = sh.decay.tail[r0 + lane / 4 + 8];
+    {
+      float acc[NT][4] = {};
+      rows_times_cols<F, NT, F::NI, F::NO>(acc, tk, F::TILE, r0, G, F::STATE, n0, lane);
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        acc[n][0] *= t_0, acc[n][1] *= t_0, acc[n][2] *= t_1, acc[n][3] *= t_1;
+      scores_times_cols<F, NT>(acc, w, td, n0, lane, live);
+      store_rows<F, NT>(acc, static_cast<T *>(p.dv) + ev, nullptr, p, p.n_v, t0 + r0, n0, lane);
+    }
+    {
+      float acc[NT][4] = {};
+      rows_times_rows<F, NT, F::NI, F::NM>(acc, tv, F::TILE, r0, G, F::STATE, n0, lane,
+                                           [](int) { return true; });
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        acc[n][0] *= t_0, acc[n][1] *= t_0, acc[n][2] *= t_1, acc[n][3] *= t_1;
+      if (p.rk) {
+        const float2 d = row_dots<F, NT>(acc, k, p, p.n_k, t0 + r0, n0, lane);
+        if (lane % 4 == 0) {
+          sh.rows[part][r0 + lane / 4] = d.x;
+          sh.rows[part][r0 + lane / 4 + 8] = d.y;
+        }
+      }
+      scores_times_cols<F, NT>(acc, dw, tq, n0, lane, live);
+      store_rows<F, NT>(acc, static_cast<T *>(p.dk) + ek, k, p, p.n_k, t0 + r0, n0, lane);
+    }
+    const bool more = c > c0;
+    if (more || (p.dS0 && seg == 0)) state.update(tq, td, sh.decay.head, sh.decay.all, warp, lane);
+    __syncthreads();
+    if (p.rk) {
+      const int t = threadIdx.x;
+      if (t < F::C && t0 + t < p.L) {
+        float s = 0.f, cols = 0.f;
+#pragma unroll
+        for (int i = 0; i < F::SPLIT; ++i) s += sh.rows[i][t];
+#pragma unroll
+        for (int i = 0; i < F::ROWS; ++i) cols += sh.cols[i][t];
+        p.rk[(size_t)seq * p.L + t0 + t] = s;
+        p.rc[(size_t)seq * p.L + t0 + t] = cols;
+      }
+      __syncthreads();
+      // the row sums leave by the same place
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        row_sum[h] += __shfl_xor_sync(0xffffffffu, row_sum[h], 1);
+        row_sum[h] += __shfl_xor_sync(0xffffffffu, row_sum[h], 2);
+      }
+      if (part == 0 && lane % 4 == 0) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int i = r0 + lane / 4 + 8 * h;
+          if (t0 + i < p.L) p.rc[(size_t)seq * p.L + t0 + i] -= row_sum[h];
+        }
+      }
+    }
+    if (more) state.planes(state_tile, warp, lane);
+  }
+  if (p.dS0 && seg == 0) state.store(p.dS0 + (size_t)seq * es, p, warp, lane);
+}
+
+cudaError_t launch_segment_scan(const ChunkBwd &p, int seqs, cudaStream_t stream);
+
+// The launches of one configuration.
+template <typename F> cudaError_t run_chunk_bwd(const ChunkBwd &p, int seqs, cudaStream_t stream) {
+  cudaError_t e;
+  if (p.segments > 1) {
+    e = cudaFuncSetAttribute(segment_share_kernel<F>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             share_smem<F>());
+    if (e != cudaSuccess) return e;
+    segment_share_kernel<F><<<dim3((unsigned)(seqs * (p.segments - 1)), 2), F::THREADS,
+                              share_smem<F>(), stream>>>(p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = launch_segment_scan(p, seqs, stream)) != cudaSuccess) return e;
+  }
+  e = cudaFuncSetAttribute(grad_q_kernel<F>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           grad_q_smem<F>());
+  if (e != cudaSuccess) return e;
+  grad_q_kernel<F><<<seqs * p.segments, F::THREADS, grad_q_smem<F>(), stream>>>(p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(grad_kv_kernel<F>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           grad_kv_smem<F>());
+  if (e != cudaSuccess) return e;
+  grad_kv_kernel<F><<<seqs * p.segments, F::THREADS, grad_kv_smem<F>(), stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace la

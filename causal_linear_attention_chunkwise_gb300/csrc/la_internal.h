@@ -196,6 +196,85 @@ struct ResidualNormArgs {
 };
 cudaError_t launch_residual_norm(const ResidualNormArgs &a);
 
+// Rotary positions of q and k.
+struct RotaryTensor {
+  void *p;  // inputs are only read
+  long long bs, hs, ts;
+};
+struct RotaryArgs {
+  RotaryTensor q, q_out, k, k_out;
+  int heads_q, heads_k;
+  int dtype;
+  int B, L, d, rot, interleaved, backward;
+  const float *inv_freq;
+  float scale;
+  const int *positions, *offsets, *lengths;
+  cudaStream_t stream;
+};
+cudaError_t launch_rotary(const RotaryArgs &a);
+
+// Backward pass of la_chunk_fwd's recurrence (d_k, d_v in {16, 32, 64, 128}).
+struct ChunkBwdArgs {
+  const void *q, *k, *v, *dO;
+  int dtype;
+  int B, H, L, dk, dv;
+  int phi;
+  int decay_kind;
+  const float *decay, *S0, *dS_final;
+  void *dq, *dk_out, *dv_out;
+  float *ddecay, *dS0;
+  void *workspace;
+  cudaStream_t stream;
+};
+size_t chunk_bwd_workspace_bytes(const ChunkBwdArgs &a);
+cudaError_t launch_chunk_bwd(const ChunkBwdArgs &a);
+
+// Backward passes of the norms around a block (width 1..16384).
+struct GatedNormBwdArgs {
+  const void *dy;
+  long long dy_stride;
+  const void *x;
+  long long x_bs, x_hs, x_ts;
+  const void *gate;
+  long long gate_stride;
+  int dtype;
+  int B, H, L, d;
+  int norm, act, gate_first;
+  const float *weight, *bias;
+  int weight_heads;
+  float eps;
+  void *dx;
+  long long dx_bs, dx_hs, dx_ts;
+  void *dgate;
+  long long dgate_stride;
+  float *dweight, *dbias;
+  void *workspace;  // used where dweight or dbias is wanted
+  cudaStream_t stream;
+};
+size_t gated_norm_bwd_workspace_bytes(int B, int H, int L, int d, int weight_heads);
+cudaError_t launch_gated_norm_bwd(const GatedNormBwdArgs &a);
+
+struct ResidualNormBwdArgs {
+  const void *dy;
+  int dtype;
+  const void *r, *dr;
+  int res_dtype;
+  const void *x;
+  long long rows;
+  int D;
+  const float *post_weight, *scale;
+  float alpha;
+  const float *weight;
+  int norm;
+  float eps;
+  void *dx, *dresidual;
+  float *dweight, *dbias, *dpost_weight, *dscale;
+  void *workspace;  // used where a parameter's gradient is wanted
+  cudaStream_t stream;
+};
+size_t residual_norm_bwd_workspace_bytes(long long rows, int D);
+cudaError_t launch_residual_norm_bwd(const ResidualNormBwdArgs &a);
+
 // Set the message la_last_error() returns on the calling thread.
 void set_last_error(const char *msg);
 

@@ -417,6 +417,182 @@ la_status la_residual_norm_fwd(const void *x, int dtype, const void *residual, i
                                void *residual_out, void *cuda_stream);
 
 /*
+ * The training pass of a layer: positions, and backward passes.
+ *
+ * The conventions of the state space block's operators hold here too:
+ * pointers to activations and their gradients need their element's alignment
+ * only, parameters, their gradients, decays and states are fp32 and 16-byte
+ * aligned (positions, offsets, lengths and frequencies 4-byte), outputs may
+ * not overlap inputs except as stated, and a call gives the same bits on every
+ * run.  Nothing of a forward call is kept: a backward call gets what it needs
+ * as arguments.
+ *
+ * A parameter's gradient is a sum over rows; it is formed in fp32 in a fixed
+ * order and overwrites its buffer (nothing is accumulated).  Its shares need
+ * `workspace`, device scratch of the query's bytes (16-byte aligned); its
+ * contents need no initialisation and are not kept.  Gradients that are NULL
+ * are not formed, and without any of them the workspace may be NULL.
+ */
+
+/* How rotary frequencies are scaled for contexts longer than the trained one. */
+#define LA_ROTARY_PLAIN  0  /* f_i = base^(-2 i / rotary_dim)                                */
+#define LA_ROTARY_LINEAR 1  /* f_i / factor: positions interpolated                          */
+#define LA_ROTARY_NTK    2  /* base * factor^(rotary_dim / (rotary_dim - 2)) as the base     */
+#define LA_ROTARY_YARN   3  /* f_i / factor for pairs of fewer than `slow` turns over the
+                               trained length, f_i for those of more than `fast`, a blend
+                               linear in the turns between them; scale 0.1 ln(factor) + 1    */
+
+/*
+ * Rotary frequencies of the pairs, rounded once from 64 bits, into HOST memory:
+ * inv_freq[rotary_dim / 2], and `scale` (NULL: not wanted), what la_rotary_fwd
+ * takes as its scale.  factor >= 1 (unused by PLAIN); trained_length, fast and
+ * slow are used by YARN alone (32 and 1 are customary).  Errors:
+ * LA_ERR_INVALID_ARG.  (The pages leave out the rotation of their retention
+ * layer, "Linear / sparse attention tutorial" sections 2.4 and 10; these are the
+ * operators that bring it.)
+ */
+la_status la_rotary_frequencies(int rotary_dim, double base, int scaling, double factor,
+                                double trained_length, double fast, double slow,
+                                float *inv_freq, float *scale);
+
+/*
+ * Rotary positions of q and k in one call: the pairs (x_i, x_j) of the first
+ * rotary_dim values of every head become
+ *
+ *     scale * (x_i cos a - x_j sin a, x_i sin a + x_j cos a),   a = position * inv_freq[pair]
+ *
+ * and the values behind them are copied.  Pair p is (2p, 2p+1) if `interleaved`,
+ * else (p, p + rotary_dim / 2).  la_rotary_bwd turns by -a: it takes the
+ * gradients of q_out and k_out to those of q and k.  The angle is exact however
+ * far the position lies (to position * 2^-64 turns); sine and cosine are
+ * fp32.
+ *
+ *   q, q_out   dtype, element (b,h,t,i) at b*b_stride + h*h_stride +
+ *              t*t_stride + i (strides >= 0): a slice of a projection's
+ *              token-major output, or [B,H,L,d] as la_chunk_fwd reads it.
+ *              q_out may be q with q's strides (in place).
+ *   k, k_out   the same with heads_k heads; both NULL: no k
+ *   inv_freq   [rotary_dim / 2] fp32 device memory, radians for each token
+ *              (finite; infinities and NaN count as zero)
+ *   positions  int32 [B,L], or NULL: token t's position is t
+ *   offsets    int32 [B] added to the positions, or NULL (decode: the tokens
+ *              that each sequence already has)
+ *   lengths    int32 [B], or NULL: tokens from lengths[b] on are neither read
+ *              nor written
+ *
+ * Supported: even rotary_dim in 2..d, d and heads up to 16384, L up to 2^30.
+ */
+la_status la_rotary_fwd(const void *q, long long q_b_stride, long long q_h_stride,
+                        long long q_t_stride, int heads_q, const void *k, long long k_b_stride,
+                        long long k_h_stride, long long k_t_stride, int heads_k, int dtype, int B,
+                        int L, int d, int rotary_dim, int interleaved, const float *inv_freq,
+                        float scale, const int *positions, const int *offsets,
+                        const int *lengths, void *q_out, long long qo_b_stride,
+                        long long qo_h_stride, long long qo_t_stride, void *k_out,
+                        long long ko_b_stride, long long ko_h_stride, long long ko_t_stride,
+                        void *cuda_stream);
+la_status la_rotary_bwd(const void *dq, long long q_b_stride, long long q_h_stride,
+                        long long q_t_stride, int heads_q, const void *dk, long long k_b_stride,
+                        long long k_h_stride, long long k_t_stride, int heads_k, int dtype, int B,
+                        int L, int d, int rotary_dim, int interleaved, const float *inv_freq,
+                        float scale, const int *positions, const int *offsets,
+                        const int *lengths, void *dq_out, long long qo_b_stride,
+                        long long qo_h_stride, long long qo_t_stride, void *dk_out,
+                        long long ko_b_stride, long long ko_h_stride, long long ko_t_stride,
+                        void *cuda_stream);
+
+/*
+ * Backward pass of la_chunk_fwd, of the same arguments: with S_t = a_t S_{t-1} +
+ * phi(k_t) v_t^T, o_t = S_t^T phi(q_t) and G_t the gradient of S_t,
+ *
+ *     G_t = phi(q_t) do_t^T + a_{t+1} G_{t+1},     dphi(q)_t = S_t do_t,
+ *     dphi(k)_t = G_t v_t,   dv_t = G_t^T phi(k_t),   dlog a_t = a_t <G_t, S_{t-1}>,
+ *
+ * and dq = dphi(q) phi'(q), dk likewise.
+ *
+ *   q, k, v, chunk, decay_kind, decay, S0   as the forward call had them (the
+ *              result does not depend on chunk); phi is the one set by
+ *              la_set_feature_map at this call
+ *   dO         [B,H,L,d_v] dtype, the gradient of O
+ *   dS_final   [B,H,d_k,d_v] fp32, the gradient of S_final, or NULL (zero)
+ *   dq, dk, dv dtype, of the shapes of q, k and v
+ *   ddecay     fp32 of decay's shape: the gradient of log gamma [H] (summed over
+ *              the batch and the tokens), of log alpha or of the gate logit
+ *              [B,H,L]; or NULL
+ *   dS0        [B,H,d_k,d_v] fp32, the gradient of S0 (given or not), or NULL:
+ *              a long sequence's pieces run back to front, each handing its
+ *              dS0 on as the dS_final of the one before
+ *   workspace  device scratch of la_chunk_bwd_workspace_bytes(...) bytes (for
+ *              any feature map, decay and set of outputs)
+ *
+ * With bf16 tensors, dq, dk and dv come from operands rounded once to bf16 (the
+ * decayed scores, the states and, for elu + 1, phi's values), with fp32 sums and
+ * states.  Where ddecay or dS0 is wanted those that they depend on keep fp32's
+ * 24 bits, at about twice the work; with fp32 tensors all do.  A log decay below -200
+ * counts as a decay of zero.
+ *
+ * q, k, v, dO, dq, dk, dv and the states are 16-byte aligned, decays 4-byte.
+ * Supported: d_k, d_v in {16, 32, 64, 128}, L up to 2^30.  L = 0 passes
+ * dS_final through to dS0 (or zeroes it).
+ */
+la_status la_chunk_bwd(const void *q, const void *k, const void *v, int dtype, int B, int H,
+                       int L, int d_k, int d_v, int chunk, int decay_kind, const float *decay,
+                       const float *S0, const void *dO, const float *dS_final, void *dq, void *dk,
+                       void *dv, float *ddecay, float *dS0, void *workspace, size_t ws_bytes,
+                       void *cuda_stream);
+size_t la_chunk_bwd_workspace_bytes(int B, int H, int L, int d_k, int d_v, int chunk, int dtype);
+
+/*
+ * Backward pass of la_gated_norm_fwd, of the same arguments:
+ *
+ *   dy         [B,L,H*d] dtype, the gradient of y, rows dy_stride apart
+ *   x, gate, weight, bias, weight_heads, norm, activation, gate_first, eps
+ *              as the forward call had them
+ *   dx         dtype, x's gradient, with strides like x's (its own: [B,H,L,d]
+ *              goes to la_chunk_bwd as dO); may be x with x's strides
+ *   dgate      [B,L,H*d] dtype, rows dgate_stride apart; given where gate is.
+ *              May be gate's or dy's buffer with its stride.
+ *   dweight, dbias  [weight_heads,d] fp32, or NULL
+ *
+ * Supported: d in 1..16384, H up to 65535.
+ */
+la_status la_gated_norm_bwd(const void *dy, long long dy_stride, const void *x,
+                            long long x_b_stride, long long x_h_stride, long long x_t_stride,
+                            const void *gate, long long gate_stride, int dtype, int B, int H,
+                            int L, int d, int norm, int activation, int gate_first,
+                            const float *weight, const float *bias, int weight_heads, float eps,
+                            void *dx, long long dx_b_stride, long long dx_h_stride,
+                            long long dx_t_stride, void *dgate, long long dgate_stride,
+                            float *dweight, float *dbias, void *workspace, size_t ws_bytes,
+                            void *cuda_stream);
+size_t la_gated_norm_bwd_workspace_bytes(int B, int H, int L, int d, int weight_heads);
+
+/*
+ * Backward pass of la_residual_norm_fwd; without residual and post norm it is
+ * that of a layer norm (or RMS norm) by itself.
+ *
+ *   dy            [rows,D] dtype, the gradient of y
+ *   r             [rows,D] res_dtype, residual_out as the forward call wrote it
+ *   dr            [rows,D] res_dtype, the gradient of residual_out, or NULL (zero)
+ *   x             [rows,D] dtype, the forward call's x: needed where post_weight
+ *                 or dscale is given, else not read
+ *   dx            [rows,D] dtype, x's gradient; may be dy's or x's buffer
+ *   dresidual     [rows,D] res_dtype, residual's gradient, or NULL; may be dr's
+ *                 buffer
+ *   dweight, dbias, dpost_weight, dscale   [D] fp32, each may be NULL
+ *
+ * Supported: D in 1..16384.
+ */
+la_status la_residual_norm_bwd(const void *dy, int dtype, const void *r, const void *dr,
+                               int res_dtype, const void *x, long long rows, int D,
+                               const float *post_weight, const float *scale, float alpha,
+                               const float *weight, int norm, float eps, void *dx,
+                               void *dresidual, float *dweight, float *dbias,
+                               float *dpost_weight, float *dscale, void *workspace,
+                               size_t ws_bytes, void *cuda_stream);
+size_t la_residual_norm_bwd_workspace_bytes(long long rows, int D);
+
+/*
  * la_chunk_fwd for callers that cannot allocate device memory.  (The pages
  * have no counterpart: this is a deployment variant of la_chunk_fwd.)
  *
