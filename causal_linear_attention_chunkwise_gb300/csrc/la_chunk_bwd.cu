@@ -9,6 +9,7 @@ namespace la {
 
 cudaError_t launch_chunk_bwd_bf16(const ChunkBwd &p, int seqs, bool wide, bool planes,
                                   cudaStream_t stream);
+cudaError_t launch_chunk_bwd_tc(const ChunkBwd &p, int seqs, bool planes, cudaStream_t stream);
 cudaError_t launch_chunk_bwd_f32(const ChunkBwd &p, int seqs, bool wide, bool bf16,
                                  cudaStream_t stream);
 
@@ -18,6 +19,7 @@ constexpr int kMaxPer = 512;  // chunks of a segment (the decays' kernel keeps s
 
 // How a call runs: which planes, the chunk, the segments.
 struct Plan {
+  bool tc;      // the tcgen05 kernels
   bool wide;    // padded width 128, else 64
   bool full;    // inputs as three planes
   bool planes;  // states as three planes
@@ -32,10 +34,11 @@ Plan make_plan(const ChunkBwdArgs &a, bool f32_out) {
   p.wide = std::max(a.dk, a.dv) > 64;
   p.full = a.dtype == LA_F32 || (f32_out && a.phi == LA_PHI_ELU1);
   p.planes = p.full || f32_out;
-  p.chunk = p.full ? 32 : 64;
+  p.tc = !p.full && a.dk == a.dv && a.dk >= 64;
+  p.chunk = p.tc ? 128 : p.full ? 32 : 64;
   p.chunks = (a.L + p.chunk - 1) / p.chunk;
   const long long seqs = (long long)a.B * a.H;
-  const long long slots = 152ll * (p.wide ? 1 : p.planes && !p.full ? 2 : 3);
+  const long long slots = 152ll * (p.wide || p.tc ? 1 : p.planes && !p.full ? 2 : 3);
   double best = 0;
   p.per = 0;
   for (int n = (p.chunks + kMaxPer - 1) / kMaxPer; n <= p.chunks; ++n) {
@@ -250,10 +253,13 @@ cudaError_t launch_chunk_bwd(const ChunkBwdArgs &a) {
   float *by_segment = nullptr;
   lay_out(a, plan, decay_grad, static_cast<char *>(a.workspace), &p, &by_segment);
   cudaError_t e =
-      plan.full ? launch_chunk_bwd_f32(p, (int)seqs, plan.wide, a.dtype == LA_BF16, a.stream)
-                : launch_chunk_bwd_bf16(p, (int)seqs, plan.wide, plan.planes, a.stream);
+      plan.tc ? launch_chunk_bwd_tc(p, (int)seqs, plan.planes, a.stream)
+      : plan.full ? launch_chunk_bwd_f32(p, (int)seqs, plan.wide, a.dtype == LA_BF16, a.stream)
+                  : launch_chunk_bwd_bf16(p, (int)seqs, plan.wide, plan.planes, a.stream);
   if (e != cudaSuccess || !decay_grad) return e;
-  if (plan.chunk == 32)
+  if (plan.chunk == 128)
+    decay_grad_kernel<128><<<(unsigned)blocks, 256, 0, a.stream>>>(p, a.ddecay, by_segment);
+  else if (plan.chunk == 32)
     decay_grad_kernel<32><<<(unsigned)blocks, 256, 0, a.stream>>>(p, a.ddecay, by_segment);
   else
     decay_grad_kernel<64><<<(unsigned)blocks, 256, 0, a.stream>>>(p, a.ddecay, by_segment);

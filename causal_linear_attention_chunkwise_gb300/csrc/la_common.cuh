@@ -15,6 +15,7 @@ enum : unsigned int {
   KID_NONCAUSAL = 4,
   KID_CHANNEL_GATE_TC = 5,
   KID_DELTA_TC = 6,
+  KID_CHUNK_BWD_TC = 7,
 };
 
 __device__ __forceinline__ void record_device_error(unsigned int *word, unsigned int kernel,
