@@ -65,6 +65,10 @@ size_t lay_out(const ChunkBwdArgs &a, const Plan &plan, bool decay_grad, char *b
     at += round_up(floats * sizeof(float));
     return base ? r : nullptr;
   };
+  if (a.decay_kind != LA_DECAY_NONE) {
+    float *lam = part(2 * seqs * plan.chunks * plan.chunk);
+    if (p) p->lam = reinterpret_cast<float2 *>(lam);
+  }
   if (plan.segments > 1) {
     float *u = part(seqs * (plan.segments - 1) * es), *w = part(seqs * (plan.segments - 1) * es);
     float *total = part(seqs * plan.segments);
@@ -76,6 +80,44 @@ size_t lay_out(const ChunkBwdArgs &a, const Plan &plan, bool decay_grad, char *b
     if (p) p->rq = rq, p->rk = rk, p->rc = rc, p->around = around, *by_segment = sums;
   }
   return at;
+}
+
+// The chunks' log2 decays, a warp to a chunk.  The sums run in 64 bits: in fp32 a sum of 50
+// would leave differences of neighbours 4e-6.  A kernel of its own, since the
+// walks would wait for these sums chunk by chunk.
+template <int C>
+__global__ void __launch_bounds__(256) chunk_decay_kernel(const ChunkBwd p, int seqs) {
+  constexpr int N = C / 32;
+  const long long item = (long long)blockIdx.x * 8 + threadIdx.x / 32;
+  const int lane = threadIdx.x % 32;
+  if (item >= (long long)seqs * p.chunks) return;
+  const int seq = (int)(item / p.chunks), t0 = (int)(item % p.chunks) * C;
+  double a[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    a[i] = log2_decay(p, seq, t0 + lane * N + i);
+    if (i) a[i] += a[i - 1];
+  }
+  double run = a[N - 1];
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const double x = __shfl_up_sync(0xffffffffu, run, off);
+    if (lane >= off) run += x;
+  }
+  const double before = run - a[N - 1];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const double x = before + a[i];
+    const float hi = (float)x;
+    p.lam[item * C + lane * N + i] = make_float2(hi, (float)(x - hi));
+  }
+}
+
+template <int C> cudaError_t launch_chunk_decay(const ChunkBwd &p, int seqs, cudaStream_t stream) {
+  const long long blocks = ((long long)seqs * p.chunks + 7) / 8;
+  if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+  chunk_decay_kernel<C><<<(unsigned)blocks, 256, 0, stream>>>(p, seqs);
+  return cudaGetLastError();
 }
 
 // U: each segment's own share of S becomes the state behind it; W: its own share of G (of
@@ -115,20 +157,21 @@ decay_grad_kernel(const ChunkBwd p, float *ddecay, float *by_segment) {
   const int c0 = seg * p.per, n = min(p.per, p.chunks - c0);
   const size_t base = (size_t)seq * p.L;
   for (int c = warp; c < n; c += 8) {
-    float q = 0.f, k = 0.f, a = 0.f;
+    float q = 0.f, k = 0.f;
     for (int i = 0; i < N; ++i) {
       const int t = (c0 + c) * C + lane * N + i;
       if (t >= p.L) break;
       q += p.rq[base + t];
       k += p.rk[base + t];
-      a += (float)log2_decay(p, seq, t);
     }
     for (int off = 16; off > 0; off >>= 1) {
       q += __shfl_xor_sync(0xffffffffu, q, off);
       k += __shfl_xor_sync(0xffffffffu, k, off);
-      a += __shfl_xor_sync(0xffffffffu, a, off);
     }
-    if (lane == 0) sum_q[c] = q, sum_k[c] = k, all[c] = a;
+    if (lane == 0) {
+      sum_q[c] = q, sum_k[c] = k;
+      all[c] = p.lam[((size_t)seq * p.chunks + c0 + c) * C + C - 1].x;
+    }
   }
   __syncthreads();
   if (threadIdx.x == 0) {
@@ -237,6 +280,7 @@ size_t chunk_bwd_workspace_bytes(const ChunkBwdArgs &a) {
     for (bool f32_out : {false, true}) {
       ChunkBwdArgs b = a;
       b.phi = phi;
+      b.decay_kind = LA_DECAY_TOKEN;
       most = std::max(most, lay_out(b, make_plan(b, f32_out), true, nullptr, nullptr, nullptr));
     }
   return most;
@@ -249,11 +293,16 @@ cudaError_t launch_chunk_bwd(const ChunkBwdArgs &a) {
   if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
   ChunkBwd p{a.q, a.k, a.v, a.dO, a.dq, a.dk_out, a.dv_out, a.decay, a.S0, a.dS_final, a.dS0,
              a.H, a.L, a.dk, a.dv, a.phi, a.decay_kind, plan.chunks, plan.segments, plan.per,
-             nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr};
+             nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr};
   float *by_segment = nullptr;
   lay_out(a, plan, decay_grad, static_cast<char *>(a.workspace), &p, &by_segment);
-  cudaError_t e =
-      plan.tc ? launch_chunk_bwd_tc(p, (int)seqs, plan.planes, a.stream)
+  cudaError_t e = cudaSuccess;
+  if (a.decay_kind != LA_DECAY_NONE)
+    e = plan.chunk == 128  ? launch_chunk_decay<128>(p, (int)seqs, a.stream)
+        : plan.chunk == 64 ? launch_chunk_decay<64>(p, (int)seqs, a.stream)
+                           : launch_chunk_decay<32>(p, (int)seqs, a.stream);
+  if (e != cudaSuccess) return e;
+  e = plan.tc ? launch_chunk_bwd_tc(p, (int)seqs, plan.planes, a.stream)
       : plan.full ? launch_chunk_bwd_f32(p, (int)seqs, plan.wide, a.dtype == LA_BF16, a.stream)
                   : launch_chunk_bwd_bf16(p, (int)seqs, plan.wide, plan.planes, a.stream);
   if (e != cudaSuccess || !decay_grad) return e;

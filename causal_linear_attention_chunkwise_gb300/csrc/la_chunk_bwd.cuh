@@ -56,6 +56,8 @@ struct ChunkBwd {
   int chunks, segments, per;   // per: chunks of a segment
   float *U, *W;                // [seq][segments - 1][d_k d_v]: states between segments
   float *total;                // [seq][segments] log2 of a segment's decay
+  float2 *lam;                 // [seq][chunks][C] log2 of the decay from a chunk's start to a
+                               // token, as a sum of two floats (unused without a decay)
   float *rq, *rk, *rc;         // [seq][L] shares of ddecay, or null
   float *around;               // [seq][segments] <G, e^L_C S> of a segment's last chunk
 };
@@ -99,39 +101,25 @@ __device__ __forceinline__ double log2_decay(const ChunkBwd &p, int seq, int t) 
   return (double)(a < -200.f ? -200.f : a) * 1.4426950408889634;
 }
 
-// One warp fills the factors of the chunk at token t0.  The sums run in 64 bits:
-// in fp32 a sum of 50 would leave differences of neighbours 4e-6.
-template <int C>
-__device__ __forceinline__ void chunk_decay(const ChunkBwd &p, int seq, int t0, ChunkDecay<C> &s,
-                                            int lane) {
-  constexpr int N = C / 32;
-  double a[N];
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    a[i] = log2_decay(p, seq, t0 + lane * N + i);
-    if (i) a[i] += a[i - 1];
-  }
-  double run = a[N - 1];
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const double x = __shfl_up_sync(0xffffffffu, run, off);
-    if (lane >= off) run += x;
-  }
-  const double before = run - a[N - 1], total = __shfl_sync(0xffffffffu, run, 31);
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const double x = before + a[i];
-    const float hi = (float)x;
-    s.lam[lane * N + i] = make_float2(hi, (float)(x - hi));
-    s.head[lane * N + i] = ex2_approx(hi);
-    s.tail[lane * N + i] = ex2_approx((float)(total - x));
-  }
-  if (lane == 0) s.all = ex2_approx((float)total);
-}
-
 // The decay between two tokens.
 __device__ __forceinline__ float decay_between(float2 later, float2 earlier) {
   return ex2_approx((later.x - earlier.x) + (later.y - earlier.y));
+}
+
+// The factors of a chunk, by its first C threads.
+template <int C>
+__device__ __forceinline__ void chunk_decay(const ChunkBwd &p, int seq, int c, ChunkDecay<C> &s) {
+  const int t = threadIdx.x;
+  if (t >= C) return;
+  float2 own = make_float2(0.f, 0.f), end = own;
+  if (p.decay_kind != LA_DECAY_NONE) {
+    const float2 *lam = p.lam + ((size_t)seq * p.chunks + c) * C;
+    own = lam[t], end = lam[C - 1];
+  }
+  s.lam[t] = own;
+  s.head[t] = ex2_approx(own.x);
+  s.tail[t] = decay_between(end, own);
+  if (t == 0) s.all = ex2_approx(end.x);
 }
 
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src, bool live) {
@@ -468,10 +456,7 @@ __global__ void __launch_bounds__(F::THREADS) segment_share_kernel(const ChunkBw
   for (int i = 0; i < n; ++i) {
     const uint32_t at = tiles + (F::STAGES == 2 ? (i & 1) * STAGE : 0);
     if (F::STAGES == 1) load(i);
-    if (warp == 0) {
-      chunk_decay<F::C>(p, seq, token(i), sh.decay, lane);
-      total += (double)sh.decay.lam[F::C - 1].x + sh.decay.lam[F::C - 1].y;
-    }
+    chunk_decay<F::C>(p, seq, token(i) / F::C, sh.decay);
     cp_async_done();
     __syncthreads();
     if (F::STAGES == 2 && p.phi == LA_PHI_ELU1) {
@@ -479,12 +464,13 @@ __global__ void __launch_bounds__(F::THREADS) segment_share_kernel(const ChunkBw
       __syncthreads();
     }
     if (F::STAGES == 2 && i + 1 < n) load(i + 1);
+    total += (double)sh.decay.lam[F::C - 1].x + sh.decay.lam[F::C - 1].y;
     state.update(at, at + X, back ? sh.decay.head : sh.decay.tail, sh.decay.all, warp, lane);
     __syncthreads();
   }
   const size_t slot = (size_t)seq * (p.segments - 1) + of;
   state.store((back ? p.W : p.U) + slot * p.n_k * p.n_v, p, warp, lane);
-  if (threadIdx.x == 31 && (!back || seg == p.segments - 1))
+  if (threadIdx.x == 0 && (!back || seg == p.segments - 1))
     p.total[(size_t)seq * p.segments + seg] = (float)total;
 }
 
@@ -525,7 +511,7 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_q_kernel(const Chu
     const int t0 = c * F::C;
     const uint32_t tk = tiles + (F::STAGES == 2 ? (c & 1) * STAGE : 0), tv = tk + X, td = tv + X;
     if (F::STAGES == 1) load(c);
-    if (warp == 0) chunk_decay<F::C>(p, seq, t0, sh.decay, lane);
+    chunk_decay<F::C>(p, seq, c, sh.decay);
     cp_async_done();
     __syncthreads();
     if (F::STAGES == 2 && p.phi == LA_PHI_ELU1) {
@@ -636,7 +622,7 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_kv_kernel(const Ch
     const uint32_t tq = tiles + (F::STAGES == 2 ? (c & 1) * STAGE : 0);
     const uint32_t tk = tq + X, tv = tk + X, td = tv + X;
     if (F::STAGES == 1) load(c);
-    if (warp == 0) chunk_decay<F::C>(p, seq, t0, sh.decay, lane);
+    chunk_decay<F::C>(p, seq, c, sh.decay);
     cp_async_done();
     __syncthreads();
     if (F::STAGES == 2 && p.phi == LA_PHI_ELU1) {

@@ -44,19 +44,22 @@ constexpr uint32_t HI = smem_desc_sw128_hi(1024);
 template <int D, int NM, int TILES, int STAGES> struct Smem {
   static constexpr uint32_t BOX = CT * 128;         // 128 tokens x 64 columns
   static constexpr uint32_t TILE = D / 64 * BOX;
-  static constexpr uint32_t SBOX = D * 128;         // 64 columns of a state
-  static constexpr uint32_t SPLANE = D / 64 * SBOX;
   static constexpr uint32_t OFF_TILES = NM * TILE;  // planes: of the decayed tile or the state
   static constexpr uint32_t STAGE = TILES * TILE;
-  static constexpr uint32_t OFF_LAM = OFF_TILES + STAGES * STAGE;
-  static constexpr uint32_t OFF_COLS = OFF_LAM + CT * 8;
-  static constexpr uint32_t OFF_BAR = OFF_COLS + 2 * CT * 4;
+  static constexpr uint32_t OFF_LAM = OFF_TILES + STAGES * STAGE;  // float2 [CT]
+  static constexpr uint32_t OFF_FAC = OFF_LAM + CT * 8;            // float [CT]
+  static constexpr uint32_t OFF_MORE = OFF_FAC + CT * 4;           // float [2 CT]
+  static constexpr uint32_t OFF_BAR = OFF_MORE + 2 * CT * 4;
   static constexpr uint32_t BYTES = OFF_BAR + 128;
   static_assert(BYTES <= 232448, "exceeds the per-block shared memory limit");
 };
+template <int D> struct StateTile {
+  static constexpr uint32_t BOX = D * 128;  // 64 columns of a state
+  static constexpr uint32_t PLANE = D / 64 * BOX;
+};
 
 struct Maps {
-  CUtensorMap q, k, v, dO;
+  CUtensorMap q, k, v, dO, dq, dk, dv;
 };
 
 // A walk's block: its place, barriers and tensor memory.
@@ -121,6 +124,11 @@ struct Block {
   __device__ __forceinline__ uint32_t at(uint32_t col) const {
     return tmem + col + ((uint32_t)quarter << 21);
   }
+  // 16 bytes at column `col` (a multiple of 8) of this thread's row in a tile of tokens.
+  __device__ __forceinline__ uint4 *cell(uint32_t tile, int col) const {
+    return reinterpret_cast<uint4 *>(smem + tile + col / 64 * (CT * 128) + row * 128 +
+                                     (((col % 64 / 8) ^ (row & 7)) << 4));
+  }
 };
 
 // ---------------------------------------------------------------- products
@@ -164,20 +172,30 @@ __device__ __forceinline__ void load_tile_tma(const Block &b, uint32_t off, cons
   for (int x = 0; x < D / 64; ++x)
     tma_load_3d(b.smem + off + x * CT * 128, map, bar, x * 64, token, seq);
 }
+// Rows past the last token are not written.
+template <int D>
+__device__ __forceinline__ void store_tile_tma(const Block &b, uint32_t off,
+                                               const CUtensorMap *map, int token, int seq) {
+#pragma unroll
+  for (int x = 0; x < D / 64; ++x)
+    tma_store_3d(map, b.smem + off + x * CT * 128, x * 64, token, seq);
+}
 
-// phi = elu + 1 of a tile in place; rows past the last token stay zero.
-template <int D> __device__ __forceinline__ void map_tile_tc(unsigned char *tile, int rows) {
+// dst = elu + 1 of a tile (dst may be the tile); rows past the last token are zero.
+template <int D>
+__device__ __forceinline__ void map_tile_tc(const unsigned char *tile, unsigned char *dst,
+                                            int rows) {
 #pragma unroll
   for (int i = 0; i < CT * D / 8 / kThreads; ++i) {
     const int x = threadIdx.x + i * kThreads;
-    if ((x / 8) % CT >= rows) continue;
-    uint4 *at = reinterpret_cast<uint4 *>(tile) + x;
-    const uint4 u = *at;
+    const uint4 u = reinterpret_cast<const uint4 *>(tile)[x];
     uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
+    for (int e = 0; e < 4; ++e) {
       w[e] = la::pack_bf16(tc::elu1_fast(bf16_lo(w[e])), tc::elu1_fast(bf16_hi(w[e])));
-    *at = make_uint4(w[0], w[1], w[2], w[3]);
+      if ((x / 8) % CT >= rows) w[e] = 0;
+    }
+    reinterpret_cast<uint4 *>(dst)[x] = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
@@ -203,28 +221,66 @@ __device__ __forceinline__ void decayed_planes(const unsigned char *tile, unsign
   }
 }
 
-// log2 decays of a chunk by one warp: lam[t] from the chunk's start, as two floats.
-__device__ __forceinline__ void chunk_lam(const ChunkBwd &p, int seq, int t0, float2 *lam,
-                                          int lane) {
-  constexpr int N = CT / 32;
-  double a[N];
+__device__ __forceinline__ void as_floats(const uint32_t (&r)[32], float (&f)[32]) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    a[i] = log2_decay(p, seq, t0 + lane * N + i);
-    if (i) a[i] += a[i - 1];
+  for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(r[e]);
+}
+__device__ __forceinline__ void load_32(const Block &b, uint32_t col, float (&f)[32]) {
+  uint32_t r[32];
+  tmem_ld32(b.at(col), r);
+  tmem_ld_wait();
+  as_floats(r, f);
+}
+
+// ---------------------------------------------------------------- decays
+// A chunk's log2 decays on their way to shared memory: the threads of half 0 hold a
+// token each, loaded a chunk ahead.  Between blocks of 32 tokens a decay is the product of
+// a factor of the row and one of the column, e^(L_j - E) e^(E - L_i) with E at the end of a
+// block between them, so both are at most 1; only blocks on the diagonal
+// take an exponential for each pair.
+struct TokenDecay {
+  float2 own, before;  // at the token, and at the end of the block in front of it
+
+  __device__ __forceinline__ void load(const ChunkBwd &p, const Block &b, int seq, int c) {
+    own = before = make_float2(0.f, 0.f);
+    if (b.half || p.decay_kind == LA_DECAY_NONE) return;
+    const float2 *lam = p.lam + ((size_t)seq * p.chunks + c) * CT;
+    own = lam[b.row];
+    if (b.quarter) before = lam[b.quarter * 32 - 1];
   }
-  double run = a[N - 1];
+};
+
+// The 32 scores of this thread's row (a token of block b.quarter) and column block `block`, times
+// their decays; LATER: the columns come after the row (else before it).  0 outside the
+// mask.  `fac`: the columns' factors, `lam` their log decays.
+template <bool LATER>
+__device__ __forceinline__ void decay_factors(const Block &b, int block, const float2 *lam,
+                                              const float *fac, float2 own, bool decays,
+                                              float (&d)[32]) {
+  if (block == b.quarter) {
 #pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const double x = __shfl_up_sync(0xffffffffu, run, off);
-    if (lane >= off) run += x;
-  }
-  const double before = run - a[N - 1];
+    for (int e = 0; e < 32; ++e) {
+      const bool in = LATER ? e >= b.lane : e <= b.lane;
+      float x = 1.f;
+      if (decays) {
+        const float2 other = lam[block * 32 + e];
+        x = ex2_approx(in ? LATER ? (other.x - own.x) + (other.y - own.y)
+                                  : (own.x - other.x) + (own.y - other.y)
+                          : 0.f);
+      }
+      d[e] = in ? x : 0.f;
+    }
+  } else if (decays) {
+    const float2 at = lam[LATER ? block * 32 - 1 : block * 32 + 31];
+    const float mine = LATER ? decay_between(at, own) : decay_between(own, at);
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const double x = before + a[i];
-    const float hi = (float)x;
-    lam[lane * N + i] = make_float2(hi, (float)(x - hi));
+    for (int e = 0; e < 32; e += 4) {
+      const float4 x = *reinterpret_cast<const float4 *>(fac + block * 32 + e);
+      d[e] = mine * x.x, d[e + 1] = mine * x.y, d[e + 2] = mine * x.z, d[e + 3] = mine * x.w;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 32; ++e) d[e] = 1.f;
   }
 }
 
@@ -270,14 +326,13 @@ template <int D, int NM> struct StateRow {
   // c <- all c + the update in tensor memory.  The tensor cores cut a sum's last bits
   // off; formed chunk by chunk and added here, the cuts do not add up.
   __device__ __forceinline__ void update(const Block &b, uint32_t col, float all) {
-    uint32_t r[32];
+    if (b.quarter * 32 >= D) return;
+    uint32_t r[N / 32][32];
 #pragma unroll
-    for (int i = 0; i < N; i += 32) {
-      tmem_ld32(b.at(col + b.half * N + i), r);
-      tmem_ld_wait();
+    for (int i = 0; i < N / 32; ++i) tmem_ld32(b.at(col + b.half * N + i * 32), r[i]);
+    tmem_ld_wait();
 #pragma unroll
-      for (int e = 0; e < 32; ++e) c[i + e] = fmaf(all, c[i + e], __uint_as_float(r[e]));
-    }
+    for (int i = 0; i < N; ++i) c[i] = fmaf(all, c[i], __uint_as_float(r[i / 32][i % 32]));
   }
   __device__ __forceinline__ float dot(const float *src, const Block &b) const {
     float s = 0.f;
@@ -293,86 +348,83 @@ template <int D, int NM> struct StateRow {
   }
 };
 
-// 32 columns of a gradient row, in bf16, times phi's derivative at raw (elu + 1: e^x up
-// to 0, then 1).
-template <bool PHI>
-__device__ __forceinline__ void store_32(__nv_bfloat16 *dst, const __nv_bfloat16 *raw,
-                                         const float *f) {
+// 8 values of a gradient into a staging cell; SLOPE: times phi's derivative at the raw values
+// that the cell holds (elu + 1: e^x up to 0, then 1).
+template <bool SLOPE> __device__ __forceinline__ void stage_8(uint4 *cell, const float *f) {
+  float y[8];
 #pragma unroll
-  for (int i = 0; i < 32; i += 8) {
-    float y[8];
+  for (int e = 0; e < 8; ++e) y[e] = f[e];
+  if constexpr (SLOPE) {
+    const uint4 u = *cell;
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = f[i + e];
-    if constexpr (PHI) {
-      float x[8];
-      load_raw<__nv_bfloat16, 8>(raw + i).unpack(x);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] *= x[e] > 0.f ? 1.f : __expf(x[e]);
+    for (int e = 0; e < 8; ++e) {
+      const float x = e % 2 ? bf16_hi(w[e / 2]) : bf16_lo(w[e / 2]);
+      y[e] *= x > 0.f ? 1.f : __expf(x);
     }
-    store_vec<__nv_bfloat16, 8>(dst + i, y);
   }
+  *cell = make_uint4(la::pack_bf16(y[0], y[1]), la::pack_bf16(y[2], y[3]),
+                     la::pack_bf16(y[4], y[5]), la::pack_bf16(y[6], y[7]));
 }
-
-// The dot product of 32 columns with a bf16 row.
-__device__ __forceinline__ float dot_32(const __nv_bfloat16 *x, const float *f, float s) {
+__device__ __forceinline__ float dot_8(const uint4 &u, const float *f, float s) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-  for (int i = 0; i < 32; i += 8) {
-    float y[8];
-    load_raw<__nv_bfloat16, 8>(x + i).unpack(y);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) s = fmaf(f[i + e], y[e], s);
-  }
+  for (int e = 0; e < 4; ++e)
+    s = fmaf(f[2 * e], bf16_lo(w[e]), fmaf(f[2 * e + 1], bf16_hi(w[e]), s));
   return s;
 }
 
-__device__ __forceinline__ void as_floats(const uint32_t (&r)[32], float (&f)[32]) {
-#pragma unroll
-  for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(r[e]);
-}
-
 // ---------------------------------------------------------------- a segment's own share
-template <int D, int NM>
+template <int D, int NM, bool PHI>
 __global__ void __launch_bounds__(kThreads, 1)
 segment_share_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned int *err) {
   using SM = Smem<D, NM, 2, 2>;
   constexpr uint32_t id_kv = idesc_bf16_f32(128, D, true, true);
-  constexpr bool PHI = NM == 1;  // elu + 1 comes with one plane alone
   extern __shared__ __align__(1024) unsigned char smem[];
   Block b;
   b.start(smem, SM::OFF_BAR, D, err);
-  float2 *lam = reinterpret_cast<float2 *>(smem + SM::OFF_LAM);
+  float *fac = reinterpret_cast<float *>(smem + SM::OFF_FAC);  // the tokens' weights
+  float2 *end_at = reinterpret_cast<float2 *>(smem + SM::OFF_MORE);
   const int seq = blockIdx.x / (p.segments - 1), of = blockIdx.x % (p.segments - 1);
   const bool back = blockIdx.y != 0;
   const int seg = back ? of + 1 : of;
   const int c0 = seg * p.per, c1 = min(c0 + p.per, p.chunks), n = c1 - c0;
-  const bool decays = p.decay_kind != LA_DECAY_NONE, phi = PHI && p.phi == LA_PHI_ELU1;
-  auto token = [&](int i) { return (back ? c1 - 1 - i : c0 + i) * CT; };
+  const bool decays = p.decay_kind != LA_DECAY_NONE;
+  auto chunk = [&](int i) { return back ? c1 - 1 - i : c0 + i; };
   auto load = [&](int i) {
     const uint32_t at = SM::OFF_TILES + (i & 1) * SM::STAGE;
     mbar_arrive_expect_tx(&b.full[i & 1], SM::STAGE);
-    load_tile_tma<D>(b, at, back ? &maps.q : &maps.k, &b.full[i & 1], token(i), seq);
-    load_tile_tma<D>(b, at + SM::TILE, back ? &maps.dO : &maps.v, &b.full[i & 1], token(i), seq);
+    load_tile_tma<D>(b, at, back ? &maps.q : &maps.k, &b.full[i & 1], chunk(i) * CT, seq);
+    load_tile_tma<D>(b, at + SM::TILE, back ? &maps.dO : &maps.v, &b.full[i & 1], chunk(i) * CT,
+                     seq);
   };
   if (threadIdx.x == 0) load(0);
   StateRow<D, NM> state;
   state.load(nullptr, b);
   double total = 0.0;
+  // each thread of half 0: its token's log decay and the chunk's, a chunk ahead
+  float2 own = make_float2(0.f, 0.f), end = own;
+  auto fetch = [&](int i) {
+    if (!decays || b.half) return;
+    const float2 *lam = p.lam + ((size_t)seq * p.chunks + chunk(i)) * CT;
+    own = lam[b.row], end = lam[CT - 1];
+  };
+  fetch(0);
   int i = 0;
   for (; i < n; ++i) {
-    if (threadIdx.x == 0 && i + 1 < n) load(i + 1);  // its stage was read two chunks ago
-    if (b.warp == 4 && decays) chunk_lam(p, seq, token(i), lam, b.lane);
+    if (threadIdx.x == 0 && i + 1 < n) load(i + 1);  // its stage was read a chunk ago
+    if (decays && b.half == 0) {
+      fac[b.row] = back ? ex2_approx(own.x) : decay_between(end, own);
+      if (b.row == 0) *end_at = end;
+      if (i + 1 < n) fetch(i + 1);
+    }
     b.wait_full(i & 1, (i >> 1) & 1);
     unsigned char *tile = smem + SM::OFF_TILES + (i & 1) * SM::STAGE;
-    if (phi) map_tile_tc<D>(tile, p.L - token(i));
-    __syncthreads();
-    const float2 end = decays ? lam[CT - 1] : make_float2(0.f, 0.f);
-    if (decays) {
-      if (back)
-        decayed_planes<D, NM>(tile, smem, [&](int t) { return ex2_approx(lam[t].x); });
-      else
-        decayed_planes<D, NM>(tile, smem, [&](int t) { return decay_between(end, lam[t]); });
-    }
-    total += (double)end.x + end.y;
+    if (PHI) map_tile_tc<D>(tile, tile, p.L - chunk(i) * CT);
+    if (PHI || decays) __syncthreads();
+    const float2 last = decays ? *end_at : make_float2(0.f, 0.f);
+    if (decays) decayed_planes<D, NM>(tile, smem, [&](int t) { return fac[t]; });
+    total += (double)last.x + last.y;
     fence_proxy_async_smem();
     tc_fence_before();
     if (__syncthreads_or(b.failed)) break;
@@ -390,9 +442,9 @@ segment_share_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, uns
       mma_commit(b.mma);
     }
     b.wait_mma();
-    state.update(b, 0, decays ? ex2_approx(end.x) : 1.f);
+    state.update(b, 0, ex2_approx(last.x));
     tc_fence_before();
-    __syncthreads();  // lam and the planes are free, the update is read
+    __syncthreads();  // the weights and the planes are free, the update is read
   }
   if (i == n) {
     const size_t slot = (size_t)seq * (p.segments - 1) + of;
@@ -406,10 +458,13 @@ segment_share_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, uns
 }
 
 // ---------------------------------------------------------------- dq
-template <int D, int NM>
+template <int D, int NM, bool PHI>
 __global__ void __launch_bounds__(kThreads, 1)
 grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned int *err) {
-  using SM = Smem<D, NM, 3, 1>;
+  // The fourth tile: q, where it is needed (for ddecay, for phi's derivative), then dq on its way out.
+  using SM = Smem<D, NM, 4, 1>;
+  using ST = StateTile<D>;
+  constexpr bool HAS_Q = NM == 3 || PHI;
   // Tensor memory: dO V^T, the state's share, the scores' share, the scores as operand; the
   // state's update takes the place of dO V^T.
   constexpr uint32_t T_S = 0, T_IN = 128, T_OUT = 128 + D, T_A = 128 + 2 * D, COLUMNS = 512;
@@ -418,36 +473,52 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
   constexpr uint32_t id_out = idesc_bf16_f32(128, D, false, true);
   constexpr uint32_t id_kv = idesc_bf16_f32(128, D, true, true);
   constexpr int N = D / 2;
-  constexpr bool PHI = NM == 1;
   static_assert(T_A + 64 <= COLUMNS, "tensor memory");
   extern __shared__ __align__(1024) unsigned char smem[];
   Block b;
   b.start(smem, SM::OFF_BAR, COLUMNS, err);
   float2 *lam = reinterpret_cast<float2 *>(smem + SM::OFF_LAM);
-  float *sums = reinterpret_cast<float *>(smem + SM::OFF_COLS);
+  float *fac = reinterpret_cast<float *>(smem + SM::OFF_FAC);
+  float *sums = reinterpret_cast<float *>(smem + SM::OFF_MORE);
   const int seq = blockIdx.x / p.segments, seg = blockIdx.x % p.segments;
   const int c0 = seg * p.per, c1 = min(c0 + p.per, p.chunks);
-  const size_t e0 = (size_t)seq * p.L * D, es = (size_t)D * D;
-  const bool decays = p.decay_kind != LA_DECAY_NONE, phi = PHI && p.phi == LA_PHI_ELU1;
-  const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q) + e0;
-  __nv_bfloat16 *dq = static_cast<__nv_bfloat16 *>(p.dq) + e0;
-  constexpr uint32_t TK = SM::OFF_TILES, TV = TK + SM::TILE, TD = TV + SM::TILE;
+  const size_t es = (size_t)D * D;
+  const bool decays = p.decay_kind != LA_DECAY_NONE;
+  constexpr uint32_t TK = SM::OFF_TILES, TV = TK + SM::TILE, TD = TV + SM::TILE,
+                     TQ = TD + SM::TILE;
   auto load = [&](int c) {
-    mbar_arrive_expect_tx(&b.full[0], SM::STAGE);
+    mbar_arrive_expect_tx(&b.full[0], (HAS_Q ? 4 : 3) * SM::TILE);
     load_tile_tma<D>(b, TK, &maps.k, &b.full[0], c * CT, seq);
     load_tile_tma<D>(b, TV, &maps.v, &b.full[0], c * CT, seq);
     load_tile_tma<D>(b, TD, &maps.dO, &b.full[0], c * CT, seq);
   };
-  if (threadIdx.x == 0) load(c0);
+  auto load_q = [&](int c) { load_tile_tma<D>(b, TQ, &maps.q, &b.full[0], c * CT, seq); };
+  if (threadIdx.x == 0) {
+    load(c0);
+    if (HAS_Q) load_q(c0);
+  }
+  TokenDecay next;
+  next.load(p, b, seq, c0);
   StateRow<D, NM> state;
   state.load(seg ? p.U + ((size_t)seq * (p.segments - 1) + seg - 1) * es
                  : p.S0 ? p.S0 + (size_t)seq * es : nullptr, b);
   state.planes(b);
+  float around = 0.f;
   int c = c0;
   for (; c < c1; ++c) {
     const int t0 = c * CT, t = t0 + b.row;
+    const bool more = c + 1 < c1;
+    if (decays && b.half == 0) {
+      lam[b.row] = next.own;
+      float2 block_end;  // of the token's block
+      block_end.x = __shfl_sync(0xffffffffu, next.own.x, 31);
+      block_end.y = __shfl_sync(0xffffffffu, next.own.y, 31);
+      fac[b.row] = decay_between(block_end, next.own);
+      if (more) next.load(p, b, seq, c + 1);
+    }
     b.wait_full(0, (c - c0) & 1);
-    if (phi) map_tile_tc<D>(smem + TK, p.L - t0);
+    if (PHI) map_tile_tc<D>(smem + TK, smem + TK, p.L - t0);
+    if (!HAS_Q && threadIdx.x == 0) tma_store_wait_read_all();
     fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
@@ -457,41 +528,32 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
       product<D>(b.tmem + T_S, a, along_row<SM::BOX>(b.base + TV), id_s, false);
 #pragma unroll
       for (int m = NM - 1; m >= 0; --m)
-        product<D>(b.tmem + T_IN, a, along_row<SM::SBOX>(b.base + m * SM::SPLANE), id_in,
+        product<D>(b.tmem + T_IN, a, along_row<ST::BOX>(b.base + m * ST::PLANE), id_in,
                    m < NM - 1);
       mma_commit(b.mma);
     }
-    if (b.warp == 4 && decays) chunk_lam(p, seq, t0, lam, b.lane);
-    __syncthreads();
     const float2 own = decays ? lam[b.row] : make_float2(0.f, 0.f);
     const float2 end = decays ? lam[CT - 1] : make_float2(0.f, 0.f);
     b.wait_mma();
     // the scores as operand: row j, tokens i <= j
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      const int i0 = b.half * 64 + x * 32;
+      const int block = b.half * 2 + x;
       uint32_t w[16];
-      if (i0 / 32 > b.quarter) {  // all behind the warp's rows
+      if (block > b.quarter) {  // all behind the warp's rows
 #pragma unroll
         for (int e = 0; e < 16; ++e) w[e] = 0;
       } else {
-        uint32_t r[32];
-        float f[32];
-        tmem_ld32(b.at(T_S + i0), r);
-        tmem_ld_wait();
-        as_floats(r, f);
+        float f[32], d[32];
+        load_32(b, T_S + block * 32, f);
+        decay_factors<false>(b, block, lam, fac, own, decays, d);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const int i = i0 + e;
-          if (decays) f[e] *= decay_between(own, i <= b.row ? lam[i] : own);
-          f[e] = i <= b.row ? f[e] : 0.f;
-        }
+        for (int e = 0; e < 32; ++e) f[e] = d[e] == 0.f ? 0.f : f[e] * d[e];
 #pragma unroll
         for (int e = 0; e < 16; ++e) w[e] = la::pack_bf16(f[2 * e], f[2 * e + 1]);
       }
-      tmem_st16(b.at(T_A + i0 / 2), w);
+      tmem_st16(b.at(T_A + block * 16), w);
     }
-    const bool more = c + 1 < c1;
     if (more && decays)
       decayed_planes<D, NM>(smem + TK, smem, [&](int i) { return decay_between(end, lam[i]); });
     tmem_st_wait();
@@ -520,60 +582,72 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
     float dot = 0.f;
 #pragma unroll
     for (int x = 0; x < N; x += 32) {
-      uint32_t r[32];
       float f[32], g[32];
-      tmem_ld32(b.at(T_IN + b.half * N + x), r);
-      tmem_ld_wait();
-      as_floats(r, f);
-      tmem_ld32(b.at(T_OUT + b.half * N + x), r);
-      tmem_ld_wait();
-      as_floats(r, g);
+      load_32(b, T_IN + b.half * N + x, f);
+      load_32(b, T_OUT + b.half * N + x, g);
 #pragma unroll
       for (int e = 0; e < 32; ++e) f[e] *= head;
-      if (t < p.L) {
-        const size_t at = (size_t)t * D + b.half * N + x;
-        if (p.rq) dot = dot_32(q + at, f, dot);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) g[e] += f[e];
-        if (phi) store_32<PHI>(dq + at, q + at, g);
-        else store_32<false>(dq + at, nullptr, g);
+      for (int e = 0; e < 32; ++e) g[e] += f[e];
+#pragma unroll
+      for (int e = 0; e < 32; e += 8) {
+        uint4 *cell = b.cell(TQ, b.half * N + x + e);
+        if (NM == 3) dot = dot_8(*cell, f + e, dot);
+        stage_8<PHI>(cell, g + e);
       }
     }
-    float around = 0.f;
+    if (NM == 3 && b.half == 1) sums[b.row] = dot;
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      store_tile_tma<D>(b, TQ, &maps.dq, t0, seq);
+      tma_store_commit();
+    }
+    if (NM == 3 && p.rq && b.half == 0 && t < p.L)
+      p.rq[(size_t)seq * p.L + t] = dot + sums[b.row];
     if (more) {
-      state.update(b, T_S, decays ? all : 1.f);
+      state.update(b, T_S, all);
       state.planes(b);
-    } else if (p.rq) {  // <G, e^L_C S>: the pairs around the segment's last chunk
+    } else if (NM == 3 && p.rq) {  // <G, e^L_C S>: the pairs around the segment's last chunk
       const float *G = seg + 1 < p.segments ? p.W + ((size_t)seq * (p.segments - 1) + seg) * es
                        : p.dSf ? p.dSf + (size_t)seq * es : nullptr;
-      if (G) around = state.dot(G, b);
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) around += __shfl_xor_sync(0xffffffffu, around, off);
-      if (b.lane == 0) sums[CT + b.warp] = around * all;
+      if (G) around = state.dot(G, b) * all;
     }
-    if (p.rq) {
-      if (b.half == 1) sums[b.row] = dot;
-      __syncthreads();
-      if (b.half == 0 && t < p.L) p.rq[(size_t)seq * p.L + t] = dot + sums[b.row];
-      if (!more && threadIdx.x == 0) {
-        float s = 0.f;
-        for (int i = 0; i < kThreads / 32; ++i) s += sums[CT + i];
-        p.around[(size_t)seq * p.segments + seg] = s;
-      }
+    if (HAS_Q && threadIdx.x == 0 && more && !b.failed) {
+      tma_store_wait_read_all();
+      load_q(c + 1);
     }
   }
-  if (c < c1 && threadIdx.x == 0) {
-    tc::drain_wait(&b.full[0], (c - c0) & 1);
-    tc::drain_wait(b.mma, b.mma_phase ^ 1);
+  if (threadIdx.x == 0) {
+    if (c < c1) {
+      tc::drain_wait(&b.full[0], (c - c0) & 1);
+      tc::drain_wait(b.mma, b.mma_phase ^ 1);
+    }
+    tma_store_wait_all();
+  }
+  if (NM == 3 && p.rq) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) around += __shfl_xor_sync(0xffffffffu, around, off);
+    if (b.lane == 0) sums[CT + b.warp] = around;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      float s = 0.f;
+      for (int i = 0; i < kThreads / 32; ++i) s += sums[CT + i];
+      p.around[(size_t)seq * p.segments + seg] = s;
+    }
   }
   b.finish(COLUMNS);
 }
 
 // ---------------------------------------------------------------- dk and dv
-template <int D, int NM>
+template <int D, int NM, bool PHI>
 __global__ void __launch_bounds__(kThreads, 1)
 grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned int *err) {
-  using SM = Smem<D, NM, 4, 1>;
+  // A fifth tile holds phi(k) beside k, which its derivative needs.  dk and dv leave by k's and
+  // v's tiles.
+  using SM = Smem<D, NM, PHI ? 5 : 4, 1>;
+  using ST = StateTile<D>;
   // Tensor memory: K Q^T and V dO^T, dv, dk.  When the scores have been read their operands
   // take columns 0..63 and 192..255, the state's update those between.
   constexpr uint32_t T_P = 0, T_DP = 128, T_V = 256, T_K = 256 + D, COLUMNS = 512;
@@ -583,29 +657,30 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
   constexpr uint32_t id_out = idesc_bf16_f32(128, D, false, true);
   constexpr uint32_t id_kv = idesc_bf16_f32(128, D, true, true);
   constexpr int N = D / 2;
-  constexpr bool PHI = NM == 1;
   extern __shared__ __align__(1024) unsigned char smem[];
   Block b;
   b.start(smem, SM::OFF_BAR, COLUMNS, err);
   float2 *lam = reinterpret_cast<float2 *>(smem + SM::OFF_LAM);
-  float *part = reinterpret_cast<float *>(smem + SM::OFF_LAM);  // [4][CT], once lam is used
+  float *fac = reinterpret_cast<float *>(smem + SM::OFF_FAC);
+  float *part = reinterpret_cast<float *>(smem + SM::OFF_LAM);  // [4][CT], once lam and fac are used
   const int seq = blockIdx.x / p.segments, seg = blockIdx.x % p.segments;
   const int c0 = seg * p.per, c1 = min(c0 + p.per, p.chunks), n = c1 - c0;
-  const size_t e0 = (size_t)seq * p.L * D, es = (size_t)D * D;
-  const bool decays = p.decay_kind != LA_DECAY_NONE, phi = PHI && p.phi == LA_PHI_ELU1;
-  const __nv_bfloat16 *k = static_cast<const __nv_bfloat16 *>(p.k) + e0;
-  __nv_bfloat16 *dk = static_cast<__nv_bfloat16 *>(p.dk) + e0;
-  __nv_bfloat16 *dv = static_cast<__nv_bfloat16 *>(p.dv) + e0;
+  const size_t es = (size_t)D * D;
+  const bool decays = p.decay_kind != LA_DECAY_NONE;
   constexpr uint32_t TQ = SM::OFF_TILES, TK = TQ + SM::TILE, TV = TK + SM::TILE,
-                     TD = TV + SM::TILE;
-  auto load = [&](int c) {
-    mbar_arrive_expect_tx(&b.full[0], SM::STAGE);
+                     TD = TV + SM::TILE, TKP = PHI ? TD + SM::TILE : TK;
+  auto load_qo = [&](int c) {
+    mbar_arrive_expect_tx(&b.full[0], 4 * SM::TILE);
     load_tile_tma<D>(b, TQ, &maps.q, &b.full[0], c * CT, seq);
-    load_tile_tma<D>(b, TK, &maps.k, &b.full[0], c * CT, seq);
-    load_tile_tma<D>(b, TV, &maps.v, &b.full[0], c * CT, seq);
     load_tile_tma<D>(b, TD, &maps.dO, &b.full[0], c * CT, seq);
   };
-  if (threadIdx.x == 0) load(c1 - 1);
+  auto load_kv = [&](int c) {
+    load_tile_tma<D>(b, TK, &maps.k, &b.full[0], c * CT, seq);
+    load_tile_tma<D>(b, TV, &maps.v, &b.full[0], c * CT, seq);
+  };
+  if (threadIdx.x == 0) load_qo(c1 - 1), load_kv(c1 - 1);
+  TokenDecay next;
+  next.load(p, b, seq, c1 - 1);
   StateRow<D, NM> state;
   state.load(seg + 1 < p.segments ? p.W + ((size_t)seq * (p.segments - 1) + seg) * es
              : p.dSf ? p.dSf + (size_t)seq * es : nullptr, b);
@@ -613,28 +688,32 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
   int done = 0;
   for (; done < n; ++done) {
     const int c = c1 - 1 - done, t0 = c * CT, t = t0 + b.row;
+    const bool more = done + 1 < n, update = more || (p.dS0 && seg == 0);
+    if (decays && b.half == 0) {
+      lam[b.row] = next.own;
+      fac[b.row] = decay_between(next.own, next.before);
+      if (more) next.load(p, b, seq, c - 1);
+    }
     b.wait_full(0, done & 1);
-    if (phi) {
-      map_tile_tc<D>(smem + TQ, p.L - t0);
-      map_tile_tc<D>(smem + TK, p.L - t0);
+    if (PHI) {
+      map_tile_tc<D>(smem + TQ, smem + TQ, p.L - t0);
+      map_tile_tc<D>(smem + TK, smem + TKP, p.L - t0);
     }
     fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
     if (threadIdx.x == 0) {
       tc_fence_after();
-      const Operand ak = along_row<SM::BOX>(b.base + TK), av = along_row<SM::BOX>(b.base + TV);
+      const Operand ak = along_row<SM::BOX>(b.base + TKP), av = along_row<SM::BOX>(b.base + TV);
       product<D>(b.tmem + T_P, ak, along_row<SM::BOX>(b.base + TQ), id_s, false);
       product<D>(b.tmem + T_DP, av, along_row<SM::BOX>(b.base + TD), id_s, false);
-      product<D>(b.tmem + T_V, ak, along_col<SM::SBOX>(b.base), id_out, false);
+      product<D>(b.tmem + T_V, ak, along_col<ST::BOX>(b.base), id_out, false);
 #pragma unroll
       for (int m = NM - 1; m >= 0; --m)
-        product<D>(b.tmem + T_K, av, along_row<SM::SBOX>(b.base + m * SM::SPLANE), id_in,
+        product<D>(b.tmem + T_K, av, along_row<ST::BOX>(b.base + m * ST::PLANE), id_in,
                    m < NM - 1);
       mma_commit(b.mma);
     }
-    if (b.warp == 4 && decays) chunk_lam(p, seq, t0, lam, b.lane);
-    __syncthreads();
     const float2 own = decays ? lam[b.row] : make_float2(0.f, 0.f);
     const float2 end = decays ? lam[CT - 1] : make_float2(0.f, 0.f);
     b.wait_mma();
@@ -643,48 +722,44 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
     float row_sum = 0.f, col_sum[2] = {0.f, 0.f};
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      const int j0 = b.half * 64 + x * 32;
-      if (j0 / 32 < b.quarter) {  // all in front of the warp's rows
+      const int block = b.half * 2 + x;
+      if (block < b.quarter) {  // all in front of the warp's rows
 #pragma unroll
         for (int e = 0; e < 16; ++e) wp[x][e] = wd[x][e] = 0;
         continue;
       }
-      uint32_t r[32];
-      float f[32], g[32];
-      tmem_ld32(b.at(T_P + j0), r);
-      tmem_ld_wait();
-      as_floats(r, f);
-      tmem_ld32(b.at(T_DP + j0), r);
-      tmem_ld_wait();
-      as_floats(r, g);
-      float pair[32];
+      float f[32], g[32], d[32];
+      load_32(b, T_P + block * 32, f);
+      load_32(b, T_DP + block * 32, g);
+      decay_factors<true>(b, block, lam, fac, own, decays, d);
 #pragma unroll
       for (int e = 0; e < 32; ++e) {
-        const int j = j0 + e;
-        const float d = decays ? decay_between(j >= b.row ? lam[j] : own, own) : 1.f;
-        pair[e] = j > b.row ? f[e] * g[e] * d : 0.f;
-        f[e] = j >= b.row ? f[e] * d : 0.f;
-        g[e] = j >= b.row ? g[e] * d : 0.f;
+        const bool in = d[e] != 0.f;
+        f[e] = in ? f[e] * d[e] : 0.f;
+        d[e] = in ? g[e] * d[e] : 0.f;
       }
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
         wp[x][e] = la::pack_bf16(f[2 * e], f[2 * e + 1]);
-        wd[x][e] = la::pack_bf16(g[2 * e], g[2 * e + 1]);
+        wd[x][e] = la::pack_bf16(d[2 * e], d[2 * e + 1]);
       }
-      if (p.rc) {
+      if (NM == 3) {  // the pairs i < j: their sums over the row and, over the warp's rows, the columns
 #pragma unroll
-        for (int e = 0; e < 32; ++e) row_sum += pair[e];
-        // sums over the warp's rows: lane e ends with column e's
+        for (int e = 0; e < 32; ++e) {
+          f[e] = block == b.quarter && e <= b.lane ? 0.f : f[e] * g[e];
+          row_sum += f[e];
+        }
+        // lane e ends with column e's
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) {
           const bool up = b.lane & off;
 #pragma unroll
           for (int e = 0; e < off; ++e) {
-            const float give = up ? pair[e] : pair[e + off];
-            pair[e] = (up ? pair[e + off] : pair[e]) + __shfl_xor_sync(0xffffffffu, give, off);
+            const float give = up ? f[e] : f[e + off];
+            f[e] = (up ? f[e + off] : f[e]) + __shfl_xor_sync(0xffffffffu, give, off);
           }
         }
-        col_sum[x] = pair[0];
+        col_sum[x] = f[0];
       }
     }
     tc_fence_before();
@@ -701,22 +776,22 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
 #pragma unroll
       for (int x = 0; x < 2 * N; x += 32) {
         const bool of_k = x >= N;
-        const uint32_t at = b.at((of_k ? T_K : T_V) + b.half * N + x % N);
+        const int col = b.half * N + x % N;
         uint32_t r[32];
         float f[32];
-        tmem_ld32(at, r);
-        tmem_ld_wait();
-        as_floats(r, f);
+        load_32(b, (of_k ? T_K : T_V) + col, f);
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
           f[e] *= tail;
           r[e] = __float_as_uint(f[e]);
         }
-        tmem_st32(at, r);
-        if (of_k && p.rk && t < p.L) dot = dot_32(k + (size_t)t * D + b.half * N + x % N, f, dot);
+        tmem_st32(b.at((of_k ? T_K : T_V) + col), r);
+        if (NM == 3 && of_k) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) dot = dot_8(*b.cell(TK, col + e), f + e, dot);
+        }
       }
     }
-    const bool more = done + 1 < n, update = more || (p.dS0 && seg == 0);
     if (update && decays)
       decayed_planes<D, NM>(smem + TQ, smem, [&](int i) { return ex2_approx(lam[i].x); });
     tmem_st_wait();
@@ -740,7 +815,7 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
       }
       mma_commit(b.mma);
     }
-    if (p.rk) {  // over the halves of a row and the quarters of a column, by way of lam's room
+    if (NM == 3 && p.rk) {  // over the halves of a row and the quarters of a column
       const size_t to = (size_t)seq * p.L + t;
       part[b.quarter * CT + b.half * 64 + b.lane] = col_sum[0];
       part[b.quarter * CT + b.half * 64 + 32 + b.lane] = col_sum[1];
@@ -757,26 +832,32 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
       }
     }
     b.wait_mma();
-    if (threadIdx.x == 0 && more && !b.failed) load(c - 1);
+    if (threadIdx.x == 0 && more && !b.failed) load_qo(c - 1);
 #pragma unroll
     for (int x = 0; x < N; x += 32) {
-      uint32_t r[32];
+      const int col = b.half * N + x;
       float f[32];
-      const size_t at = (size_t)t * D + b.half * N + x;
-      tmem_ld32(b.at(T_V + b.half * N + x), r);
-      tmem_ld_wait();
-      as_floats(r, f);
-      if (t < p.L) store_32<false>(dv + at, nullptr, f);
-      tmem_ld32(b.at(T_K + b.half * N + x), r);
-      tmem_ld_wait();
-      as_floats(r, f);
-      if (t < p.L) {
-        if (phi) store_32<PHI>(dk + at, k + at, f);
-        else store_32<false>(dk + at, nullptr, f);
-      }
+      load_32(b, T_V + col, f);
+#pragma unroll
+      for (int e = 0; e < 32; e += 8) stage_8<false>(b.cell(TV, col + e), f + e);
+      load_32(b, T_K + col, f);
+#pragma unroll
+      for (int e = 0; e < 32; e += 8) stage_8<PHI>(b.cell(TK, col + e), f + e);
     }
-    if (update) state.update(b, T_U, decays ? ex2_approx(end.x) : 1.f);
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      store_tile_tma<D>(b, TV, &maps.dv, t0, seq);
+      store_tile_tma<D>(b, TK, &maps.dk, t0, seq);
+      tma_store_commit();
+    }
+    if (update) state.update(b, T_U, ex2_approx(end.x));
     if (more) state.planes(b);
+    if (threadIdx.x == 0 && more && !b.failed) {
+      tma_store_wait_read_all();
+      load_kv(c - 1);
+    }
   }
   if (done == n) {
     if (p.dS0 && seg == 0) state.store(p.dS0 + (size_t)seq * es, b);
@@ -784,32 +865,35 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
     tc::drain_wait(&b.full[0], done & 1);
     tc::drain_wait(b.mma, b.mma_phase ^ 1);
   }
+  if (threadIdx.x == 0) tma_store_wait_all();
   b.finish(COLUMNS);
 }
 
-template <int D, int NM>
+template <int D, int NM, bool PHI>
 cudaError_t launch_tc(const ChunkBwd &p, int seqs, cudaStream_t stream) {
   using SS = Smem<D, NM, 2, 2>;
-  using SQ = Smem<D, NM, 3, 1>;
-  using SK = Smem<D, NM, 4, 1>;
+  using SQ = Smem<D, NM, 4, 1>;
+  using SK = Smem<D, NM, PHI ? 5 : 4, 1>;
   Maps m;
-  if (!make_tmap_bf16_3d(&m.q, p.q, D, p.L, seqs, 64, CT) ||
-      !make_tmap_bf16_3d(&m.k, p.k, D, p.L, seqs, 64, CT) ||
-      !make_tmap_bf16_3d(&m.v, p.v, D, p.L, seqs, 64, CT) ||
-      !make_tmap_bf16_3d(&m.dO, p.dO, D, p.L, seqs, 64, CT))
-    return cudaErrorInvalidValue;
+  const struct {
+    CUtensorMap *map;
+    const void *p;
+  } all[] = {{&m.q, p.q},   {&m.k, p.k},   {&m.v, p.v},  {&m.dO, p.dO},
+             {&m.dq, p.dq}, {&m.dk, p.dk}, {&m.dv, p.dv}};
+  for (const auto &x : all)
+    if (!make_tmap_bf16_3d(x.map, x.p, D, p.L, seqs, 64, CT)) return cudaErrorInvalidValue;
   unsigned int *err = device_error_word();
   cudaError_t e;
   if (p.segments > 1) {
-    auto share = segment_share_tc_kernel<D, NM>;
+    auto share = segment_share_tc_kernel<D, NM, PHI>;
     static int set[64];
     if ((e = tc::set_smem_once(share, SS::BYTES, set)) != cudaSuccess) return e;
     share<<<dim3((unsigned)(seqs * (p.segments - 1)), 2), kThreads, SS::BYTES, stream>>>(m, p, err);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if ((e = launch_segment_scan(p, seqs, stream)) != cudaSuccess) return e;
   }
-  auto gq = grad_q_tc_kernel<D, NM>;
-  auto gkv = grad_kv_tc_kernel<D, NM>;
+  auto gq = grad_q_tc_kernel<D, NM, PHI>;
+  auto gkv = grad_kv_tc_kernel<D, NM, PHI>;
   static int set_q[64], set_kv[64];
   if ((e = tc::set_smem_once(gq, SQ::BYTES, set_q)) != cudaSuccess) return e;
   if ((e = tc::set_smem_once(gkv, SK::BYTES, set_kv)) != cudaSuccess) return e;
@@ -819,12 +903,17 @@ cudaError_t launch_tc(const ChunkBwd &p, int seqs, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
+template <int D> cudaError_t launch_d(const ChunkBwd &p, int seqs, bool planes, cudaStream_t stream) {
+  if (planes) return launch_tc<D, 3, false>(p, seqs, stream);
+  return p.phi == LA_PHI_ELU1 ? launch_tc<D, 1, true>(p, seqs, stream)
+                              : launch_tc<D, 1, false>(p, seqs, stream);
+}
+
 }  // namespace
 
 cudaError_t launch_chunk_bwd_tc(const ChunkBwd &p, int seqs, bool planes, cudaStream_t stream) {
-  if (p.n_k == 128)
-    return planes ? launch_tc<128, 3>(p, seqs, stream) : launch_tc<128, 1>(p, seqs, stream);
-  return planes ? launch_tc<64, 3>(p, seqs, stream) : launch_tc<64, 1>(p, seqs, stream);
+  return p.n_k == 128 ? launch_d<128>(p, seqs, planes, stream)
+                      : launch_d<64>(p, seqs, planes, stream);
 }
 
 }  // namespace la

@@ -88,7 +88,7 @@ __device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v 
 __device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
 // Two fp32 values as sums of NP bf16 planes (three hold all 24 bits): plane p at out[p * stride].
-// An infinite or NaN first plane takes no remainder.
+// An infinity becomes a NaN.
 template <int NP>
 __device__ __forceinline__ void split(float x, float y, uint32_t *out, int stride) {
 #pragma unroll
@@ -96,8 +96,8 @@ __device__ __forceinline__ void split(float x, float y, uint32_t *out, int strid
     const uint32_t v = pack_bf16(x, y);
     out[p * stride] = v;
     if (p + 1 < NP) {
-      x = fabsf(bf16_lo(v)) < INFINITY ? x - bf16_lo(v) : 0.f;
-      y = fabsf(bf16_hi(v)) < INFINITY ? y - bf16_hi(v) : 0.f;
+      x -= bf16_lo(v);
+      y -= bf16_hi(v);
     }
   }
 }
