@@ -82,9 +82,29 @@ size_t lay_out(const ChunkBwdArgs &a, const Plan &plan, bool decay_grad, char *b
   return at;
 }
 
-// The chunks' log2 decays, a warp to a chunk.  The sums run in 64 bits: in fp32 a sum of 50
-// would leave differences of neighbours 4e-6.  A kernel of its own, since the
-// walks would wait for these sums chunk by chunk.
+// The chunks' log2 decays, a warp to a chunk.  The sums are of two floats each: in one, a sum of
+// 50 would leave differences of neighbours 4e-6.  A kernel of its own, since the walks would
+// wait for these sums chunk by chunk.
+__device__ __forceinline__ float2 two_sum(float2 a, float2 b) {
+  const float s = a.x + b.x, t = s - a.x;
+  const float low = (a.x - (s - t)) + (b.x - t) + (a.y + b.y);  // what s lost, and the low parts
+  const float hi = s + low;
+  return make_float2(hi, low - (hi - s));
+}
+__device__ __forceinline__ float2 log2_decay(const ChunkBwd &p, int seq, int t) {
+  if (t >= p.L) return make_float2(0.f, 0.f);
+  const long long at = (long long)seq * p.L + t;
+  float a;
+  if (p.decay_kind == LA_DECAY_HEAD) a = p.decay[seq % p.H];
+  else if (p.decay_kind == LA_DECAY_TOKEN) a = p.decay[at];
+  else a = neg_softplus(p.decay[at]);
+  // Below e^-200 a decay counts as e^-200, which is 0 in fp32 in whatever it multiplies; a sum
+  // of infinities would be NaN.
+  if (a < -200.f) a = -200.f;
+  const float hi = a * 1.44269502f;  // log2 e = 1.44269502 + 1.92596299e-8
+  return make_float2(hi, fmaf(a, 1.92596299e-8f, fmaf(a, 1.44269502f, -hi)));
+}
+
 template <int C>
 __global__ void __launch_bounds__(256) chunk_decay_kernel(const ChunkBwd p, int seqs) {
   constexpr int N = C / 32;
@@ -92,25 +112,23 @@ __global__ void __launch_bounds__(256) chunk_decay_kernel(const ChunkBwd p, int 
   const int lane = threadIdx.x % 32;
   if (item >= (long long)seqs * p.chunks) return;
   const int seq = (int)(item / p.chunks), t0 = (int)(item % p.chunks) * C;
-  double a[N];
+  float2 a[N];
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    a[i] = log2_decay(p, seq, t0 + lane * N + i);
-    if (i) a[i] += a[i - 1];
-  }
-  double run = a[N - 1];
+  for (int i = 0; i < N; ++i) a[i] = log2_decay(p, seq, t0 + lane * N + i);
+#pragma unroll
+  for (int i = 1; i < N; ++i) a[i] = two_sum(a[i - 1], a[i]);
+  float2 run = a[N - 1];
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
-    const double x = __shfl_up_sync(0xffffffffu, run, off);
-    if (lane >= off) run += x;
+    const float2 x = make_float2(__shfl_up_sync(0xffffffffu, run.x, off),
+                                 __shfl_up_sync(0xffffffffu, run.y, off));
+    if (lane >= off) run = two_sum(x, run);
   }
-  const double before = run - a[N - 1];
+  float2 before = make_float2(__shfl_up_sync(0xffffffffu, run.x, 1),
+                              __shfl_up_sync(0xffffffffu, run.y, 1));
+  if (lane == 0) before = make_float2(0.f, 0.f);
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const double x = before + a[i];
-    const float hi = (float)x;
-    p.lam[item * C + lane * N + i] = make_float2(hi, (float)(x - hi));
-  }
+  for (int i = 0; i < N; ++i) p.lam[item * C + lane * N + i] = two_sum(before, a[i]);
 }
 
 template <int C> cudaError_t launch_chunk_decay(const ChunkBwd &p, int seqs, cudaStream_t stream) {

@@ -89,18 +89,6 @@ template <int C> struct ChunkDecay {
   float all;      // e^L_C
 };
 
-// log2 of token t's decay.  Below e^-200 it counts as e^-200, which is 0 in fp32 in
-// whatever it multiplies; a sum of infinities would be NaN.
-__device__ __forceinline__ double log2_decay(const ChunkBwd &p, int seq, int t) {
-  if (p.decay_kind == LA_DECAY_NONE || t >= p.L) return 0.0;
-  const long long at = (long long)seq * p.L + t;
-  float a;
-  if (p.decay_kind == LA_DECAY_HEAD) a = p.decay[seq % p.H];
-  else if (p.decay_kind == LA_DECAY_TOKEN) a = p.decay[at];
-  else a = neg_softplus(p.decay[at]);
-  return (double)(a < -200.f ? -200.f : a) * 1.4426950408889634;
-}
-
 // The decay between two tokens.
 __device__ __forceinline__ float decay_between(float2 later, float2 earlier) {
   return ex2_approx((later.x - earlier.x) + (later.y - earlier.y));

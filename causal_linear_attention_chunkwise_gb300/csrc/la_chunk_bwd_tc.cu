@@ -67,11 +67,11 @@ struct Block {
   unsigned char *smem;
   uint32_t base;       // its shared address
   uint64_t *full;      // [2] tiles have landed
-  uint64_t *mma;       // products are done
+  uint64_t *mma;       // [4] products are done
+  int *narrow;         // [4] whether a block of 32 tokens takes factors on its diagonal
   Ctl *ctl;
   unsigned int *err;
   uint32_t tmem;
-  uint32_t mma_phase;
   int warp, lane, quarter, half, row;
   bool failed;
 
@@ -81,16 +81,16 @@ struct Block {
     base = smem_u32(s);
     full = reinterpret_cast<uint64_t *>(s + off_bar);
     mma = full + 2;
+    narrow = reinterpret_cast<int *>(s + off_bar + 80);
     ctl = reinterpret_cast<Ctl *>(s + off_bar + 64);
     err = error;
     warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     quarter = warp % 4, half = warp / 4, row = quarter * 32 + lane;
-    mma_phase = 0;
     failed = false;
     if (threadIdx.x == 0) {
       mbar_init(&full[0], 1);
       mbar_init(&full[1], 1);
-      mbar_init(mma, 1);
+      for (int i = 0; i < 4; ++i) mbar_init(&mma[i], 1);
       ctl->abort = 0;
       fence_mbarrier_init();
     }
@@ -113,10 +113,9 @@ struct Block {
     if (!tc::wait1(&full[stage], parity, ctl, err, KID_CHUNK_BWD_TC, 1)) failed = true;
     __syncwarp();
   }
-  // The products issued since the last call are done.
-  __device__ __forceinline__ void wait_mma() {
-    if (!tc::wait1(mma, mma_phase, ctl, err, KID_CHUNK_BWD_TC, 2)) failed = true;
-    mma_phase ^= 1;
+  // The products committed to mma[i] are done.
+  __device__ __forceinline__ void wait_mma(int i, uint32_t parity) {
+    if (!tc::wait1(&mma[i], parity, ctl, err, KID_CHUNK_BWD_TC, 2 + i)) failed = true;
     __syncwarp();
     tc_fence_after();
   }
@@ -172,6 +171,11 @@ __device__ __forceinline__ void load_tile_tma(const Block &b, uint32_t off, cons
   for (int x = 0; x < D / 64; ++x)
     tma_load_3d(b.smem + off + x * CT * 128, map, bar, x * 64, token, seq);
 }
+template <int D>
+__device__ __forceinline__ void prefetch_tile(const CUtensorMap *map, int token, int seq) {
+#pragma unroll
+  for (int x = 0; x < D / 64; ++x) tma_prefetch_3d(map, x * 64, token, seq);
+}
 // Rows past the last token are not written.
 template <int D>
 __device__ __forceinline__ void store_tile_tma(const Block &b, uint32_t off,
@@ -199,16 +203,17 @@ __device__ __forceinline__ void map_tile_tc(const unsigned char *tile, unsigned 
   }
 }
 
-// dst (NM planes) = weight(token) * tile, at the tile's own places.
-template <int D, int NM, typename Weight>
-__device__ __forceinline__ void decayed_planes(const unsigned char *tile, unsigned char *dst,
-                                               Weight weight) {
+// dst (NM planes) = weight(token) * tile, at the tile's own places: ROWS tokens from row0 on.
+template <int D, int NM, int ROWS, typename Weight>
+__device__ __forceinline__ void decayed_rows(const unsigned char *tile, unsigned char *dst,
+                                             int row0, Weight weight) {
   constexpr uint32_t TILE = CT * D * 2;
 #pragma unroll 4
-  for (int i = 0; i < CT * D / 8 / kThreads; ++i) {
-    const int x = threadIdx.x + i * kThreads;
-    const uint4 u = reinterpret_cast<const uint4 *>(tile)[x];
-    const float f = weight((x / 8) % CT);
+  for (int i = 0; i < ROWS * D / 8 / kThreads; ++i) {
+    const int x = threadIdx.x + i * kThreads, row = row0 + x / 8 % ROWS;
+    const int at = x / 8 / ROWS * (CT * 8) + row * 8 + x % 8;  // in 16-byte cells
+    const uint4 u = reinterpret_cast<const uint4 *>(tile)[at];
+    const float f = weight(row);
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
     uint32_t out[NM][4];
 #pragma unroll
@@ -216,7 +221,7 @@ __device__ __forceinline__ void decayed_planes(const unsigned char *tile, unsign
       split<NM>(bf16_lo(w[e]) * f, bf16_hi(w[e]) * f, &out[0][e], 4);
 #pragma unroll
     for (int m = 0; m < NM; ++m)
-      reinterpret_cast<uint4 *>(dst + m * TILE)[x] =
+      reinterpret_cast<uint4 *>(dst + m * TILE)[at] =
           make_uint4(out[m][0], out[m][1], out[m][2], out[m][3]);
   }
 }
@@ -234,10 +239,11 @@ __device__ __forceinline__ void load_32(const Block &b, uint32_t col, float (&f)
 
 // ---------------------------------------------------------------- decays
 // A chunk's log2 decays on their way to shared memory: the threads of half 0 hold a
-// token each, loaded a chunk ahead.  Between blocks of 32 tokens a decay is the product of
-// a factor of the row and one of the column, e^(L_j - E) e^(E - L_i) with E at the end of a
-// block between them, so both are at most 1; only blocks on the diagonal
-// take an exponential for each pair.
+// token each, loaded a chunk ahead.  A decay is the product of a factor of the row and one of the
+// column, e^(L_j - E) e^(E - L_i) with E at the end of a block of 32 tokens between them, so
+// both are at most 1.  Pairs of one block take their own block's end (dq) or the
+// end before it: one factor is then above 1, up to what the block decays by.  A block
+// that decays by more than 2^60 takes an exponential for each pair instead.
 struct TokenDecay {
   float2 own, before;  // at the token, and at the end of the block in front of it
 
@@ -248,30 +254,31 @@ struct TokenDecay {
     own = lam[b.row];
     if (b.quarter) before = lam[b.quarter * 32 - 1];
   }
+  // LATER: for columns behind the rows (e^(L - E) of the block before), else e^(E - L).
+  template <bool LATER>
+  __device__ __forceinline__ void put(const Block &b, float2 *lam, float *fac) const {
+    float2 at = before;
+    if (!LATER) {
+      at.x = __shfl_sync(0xffffffffu, own.x, 31);
+      at.y = __shfl_sync(0xffffffffu, own.y, 31);
+    }
+    const float x = LATER ? (own.x - at.x) + (own.y - at.y) : (at.x - own.x) + (at.y - own.y);
+    lam[b.row] = own;
+    fac[b.row] = ex2_approx(x);
+    const bool all = __all_sync(0xffffffffu, fabsf(x) < 60.f);
+    if (b.lane == 0) b.narrow[b.quarter] = all;
+  }
 };
 
-// The 32 scores of this thread's row (a token of block b.quarter) and column block `block`, times
-// their decays; LATER: the columns come after the row (else before it).  0 outside the
-// mask.  `fac`: the columns' factors, `lam` their log decays.
+// The decays of this thread's row (a token of block b.quarter) and column block `block`.
+// LATER: the columns come after the row (else before it); anything outside the mask.
 template <bool LATER>
 __device__ __forceinline__ void decay_factors(const Block &b, int block, const float2 *lam,
-                                              const float *fac, float2 own, bool decays,
-                                              float (&d)[32]) {
-  if (block == b.quarter) {
-#pragma unroll
-    for (int e = 0; e < 32; ++e) {
-      const bool in = LATER ? e >= b.lane : e <= b.lane;
-      float x = 1.f;
-      if (decays) {
-        const float2 other = lam[block * 32 + e];
-        x = ex2_approx(in ? LATER ? (other.x - own.x) + (other.y - own.y)
-                                  : (own.x - other.x) + (own.y - other.y)
-                          : 0.f);
-      }
-      d[e] = in ? x : 0.f;
-    }
-  } else if (decays) {
-    const float2 at = lam[LATER ? block * 32 - 1 : block * 32 + 31];
+                                              const float *fac, float2 own, float (&d)[32]) {
+  const bool diagonal = block == b.quarter;
+  if (!diagonal || b.narrow[block]) {
+    float2 at = make_float2(0.f, 0.f);
+    if (!LATER || block) at = lam[LATER ? block * 32 - 1 : block * 32 + 31];
     const float mine = LATER ? decay_between(at, own) : decay_between(own, at);
 #pragma unroll
     for (int e = 0; e < 32; e += 4) {
@@ -280,7 +287,12 @@ __device__ __forceinline__ void decay_factors(const Block &b, int block, const f
     }
   } else {
 #pragma unroll
-    for (int e = 0; e < 32; ++e) d[e] = 1.f;
+    for (int e = 0; e < 32; ++e) {
+      const float2 other = lam[block * 32 + e];
+      const float x = LATER ? (other.x - own.x) + (other.y - own.y)
+                            : (own.x - other.x) + (own.y - other.y);
+      d[e] = ex2_approx(x);
+    }
   }
 }
 
@@ -375,78 +387,118 @@ __device__ __forceinline__ float dot_8(const uint4 &u, const float *f, float s) 
 }
 
 // ---------------------------------------------------------------- a segment's own share
-template <int D, int NM, bool PHI>
+// The decayed tile is formed in two halves of 64 tokens, each while the products of the other
+// run; a chunk's sum is added to the state while the next one's products run.
+template <int D, int NM, bool PHI, bool DECAY>
 __global__ void __launch_bounds__(kThreads, 1)
 segment_share_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned int *err) {
   using SM = Smem<D, NM, 2, 2>;
-  constexpr uint32_t id_kv = idesc_bf16_f32(128, D, true, true);
+  constexpr uint32_t id_kv = idesc_bf16_f32(128, D, true, true), COLUMNS = 2 * D;
   extern __shared__ __align__(1024) unsigned char smem[];
   Block b;
-  b.start(smem, SM::OFF_BAR, D, err);
-  float *fac = reinterpret_cast<float *>(smem + SM::OFF_FAC);  // the tokens' weights
-  float2 *end_at = reinterpret_cast<float2 *>(smem + SM::OFF_MORE);
+  b.start(smem, SM::OFF_BAR, COLUMNS, err);
+  float *weights = reinterpret_cast<float *>(smem + SM::OFF_LAM);   // [2][CT]
+  float2 *ends = reinterpret_cast<float2 *>(smem + SM::OFF_FAC);    // [2] the chunk's log decay
   const int seq = blockIdx.x / (p.segments - 1), of = blockIdx.x % (p.segments - 1);
   const bool back = blockIdx.y != 0;
   const int seg = back ? of + 1 : of;
   const int c0 = seg * p.per, c1 = min(c0 + p.per, p.chunks), n = c1 - c0;
-  const bool decays = p.decay_kind != LA_DECAY_NONE;
+  const CUtensorMap *mx = back ? &maps.q : &maps.k, *my = back ? &maps.dO : &maps.v;
   auto chunk = [&](int i) { return back ? c1 - 1 - i : c0 + i; };
   auto load = [&](int i) {
     const uint32_t at = SM::OFF_TILES + (i & 1) * SM::STAGE;
     mbar_arrive_expect_tx(&b.full[i & 1], SM::STAGE);
-    load_tile_tma<D>(b, at, back ? &maps.q : &maps.k, &b.full[i & 1], chunk(i) * CT, seq);
-    load_tile_tma<D>(b, at + SM::TILE, back ? &maps.dO : &maps.v, &b.full[i & 1], chunk(i) * CT,
-                     seq);
+    load_tile_tma<D>(b, at, mx, &b.full[i & 1], chunk(i) * CT, seq);
+    load_tile_tma<D>(b, at + SM::TILE, my, &b.full[i & 1], chunk(i) * CT, seq);
   };
-  if (threadIdx.x == 0) load(0);
+  if (threadIdx.x == 0) {
+    load(0);
+    if (n > 1) load(1);
+  }
   StateRow<D, NM> state;
   state.load(nullptr, b);
   double total = 0.0;
   // each thread of half 0: its token's log decay and the chunk's, a chunk ahead
   float2 own = make_float2(0.f, 0.f), end = own;
   auto fetch = [&](int i) {
-    if (!decays || b.half) return;
+    if (!DECAY || b.half) return;
     const float2 *lam = p.lam + ((size_t)seq * p.chunks + chunk(i)) * CT;
     own = lam[b.row], end = lam[CT - 1];
   };
+  auto put = [&](int i) {
+    if (!DECAY || b.half) return;
+    weights[(i & 1) * CT + b.row] = back ? ex2_approx(own.x) : decay_between(end, own);
+    if (b.row == 0) ends[i & 1] = end;
+  };
   fetch(0);
+  put(0);
+  if (n > 1) fetch(1);
+  __syncthreads();
+  float2 last = make_float2(0.f, 0.f);  // of the chunk whose sum is not yet added
   int i = 0;
+  bool stop = false;
   for (; i < n; ++i) {
-    if (threadIdx.x == 0 && i + 1 < n) load(i + 1);  // its stage was read a chunk ago
-    if (decays && b.half == 0) {
-      fac[b.row] = back ? ex2_approx(own.x) : decay_between(end, own);
-      if (b.row == 0) *end_at = end;
-      if (i + 1 < n) fetch(i + 1);
-    }
     b.wait_full(i & 1, (i >> 1) & 1);
     unsigned char *tile = smem + SM::OFF_TILES + (i & 1) * SM::STAGE;
-    if (PHI) map_tile_tc<D>(tile, tile, p.L - chunk(i) * CT);
-    if (PHI || decays) __syncthreads();
-    const float2 last = decays ? *end_at : make_float2(0.f, 0.f);
-    if (decays) decayed_planes<D, NM>(tile, smem, [&](int t) { return fac[t]; });
-    total += (double)last.x + last.y;
-    fence_proxy_async_smem();
-    tc_fence_before();
-    if (__syncthreads_or(b.failed)) break;
-    if (threadIdx.x == 0) {
-      tc_fence_after();
-      const uint32_t tile_at = smem_u32(tile);
-      const Operand y = along_col<SM::BOX>(tile_at + SM::TILE);
-      if (decays) {
-#pragma unroll
-        for (int m = NM - 1; m >= 0; --m)
-          product<CT>(b.tmem, along_col<SM::BOX>(b.base + m * SM::TILE), y, id_kv, m < NM - 1);
-      } else {
-        product<CT>(b.tmem, along_col<SM::BOX>(tile_at), y, id_kv, false);
-      }
-      mma_commit(b.mma);
+    const uint32_t tile_at = smem_u32(tile), sum = b.tmem + (i & 1) * D;
+    const Operand y = along_col<SM::BOX>(tile_at + SM::TILE);
+    if (PHI) {
+      map_tile_tc<D>(tile, tile, p.L - chunk(i) * CT);
+      if (DECAY) __syncthreads();
     }
-    b.wait_mma();
-    state.update(b, 0, ex2_approx(last.x));
+    if (DECAY) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (i > 0) b.wait_mma(h, (i - 1) & 1);
+        if (h == 1) {
+          if (threadIdx.x == 0 && i > 0 && i + 1 < n) load(i + 1);
+          __syncwarp();
+          if (i + 1 < n) {
+            put(i + 1);
+            if (i + 2 < n) fetch(i + 2);
+          }
+        }
+        const float *w = weights + (i & 1) * CT;
+        decayed_rows<D, NM, 64>(tile, smem, h * 64, [&](int t) { return w[t]; });
+        fence_proxy_async_smem();
+        tc_fence_before();
+        if ((stop = __syncthreads_or(b.failed))) break;
+        if (threadIdx.x == 0) {
+          tc_fence_after();
+#pragma unroll
+          for (int m = NM - 1; m >= 0; --m) {
+            const Operand x = along_col<SM::BOX>(b.base + m * SM::TILE);
+#pragma unroll
+            for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
+              mma_bf16_w(sum, word(x, kk), word(y, kk), HI, id_kv, h > 0 || m < NM - 1 || kk > 0);
+          }
+          mma_commit(&b.mma[h]);
+        }
+      }
+      if (stop) break;
+    } else {
+      if (i > 0) b.wait_mma(1, (i - 1) & 1);
+      if (threadIdx.x == 0 && i > 0 && i + 1 < n) load(i + 1);
+      __syncwarp();
+      fence_proxy_async_smem();
+      tc_fence_before();
+      if ((stop = __syncthreads_or(b.failed))) break;
+      if (threadIdx.x == 0) {
+        tc_fence_after();
+        product<CT>(sum, along_col<SM::BOX>(tile_at), y, id_kv, false);
+        mma_commit(&b.mma[1]);
+      }
+    }
+    if (i > 0) state.update(b, ((i - 1) & 1) * D, DECAY ? ex2_approx(last.x) : 1.f);
     tc_fence_before();
-    __syncthreads();  // the weights and the planes are free, the update is read
+    if (DECAY) {
+      last = ends[i & 1];
+      total += (double)last.x + last.y;
+    }
   }
-  if (i == n) {
+  if (!stop) {
+    b.wait_mma(1, (n - 1) & 1);
+    state.update(b, ((n - 1) & 1) * D, DECAY ? ex2_approx(last.x) : 1.f);
     const size_t slot = (size_t)seq * (p.segments - 1) + of;
     state.store((back ? p.W : p.U) + slot * D * D, b);
     if (threadIdx.x == 0 && (!back || seg == p.segments - 1))
@@ -454,11 +506,11 @@ segment_share_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, uns
   } else if (threadIdx.x == 0) {  // the copies in flight end before their memory does
     for (int j = i; j < min(i + 2, n); ++j) tc::drain_wait(&b.full[j & 1], (j >> 1) & 1);
   }
-  b.finish(D);
+  b.finish(COLUMNS);
 }
 
 // ---------------------------------------------------------------- dq
-template <int D, int NM, bool PHI>
+template <int D, int NM, bool PHI, bool DECAY>
 __global__ void __launch_bounds__(kThreads, 1)
 grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned int *err) {
   // The fourth tile: q, where it is needed (for ddecay, for phi's derivative), then dq on its way out.
@@ -483,19 +535,30 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
   const int seq = blockIdx.x / p.segments, seg = blockIdx.x % p.segments;
   const int c0 = seg * p.per, c1 = min(c0 + p.per, p.chunks);
   const size_t es = (size_t)D * D;
-  const bool decays = p.decay_kind != LA_DECAY_NONE;
+  constexpr bool decays = DECAY;
   constexpr uint32_t TK = SM::OFF_TILES, TV = TK + SM::TILE, TD = TV + SM::TILE,
                      TQ = TD + SM::TILE;
-  auto load = [&](int c) {
+  // A chunk's tiles, each as soon as the last one's place is free; into L2 a chunk earlier:
+  // all blocks load at about the same time, and DRAM would make them wait.
+  auto load_dO = [&](int c) {
     mbar_arrive_expect_tx(&b.full[0], (HAS_Q ? 4 : 3) * SM::TILE);
-    load_tile_tma<D>(b, TK, &maps.k, &b.full[0], c * CT, seq);
-    load_tile_tma<D>(b, TV, &maps.v, &b.full[0], c * CT, seq);
     load_tile_tma<D>(b, TD, &maps.dO, &b.full[0], c * CT, seq);
   };
-  auto load_q = [&](int c) { load_tile_tma<D>(b, TQ, &maps.q, &b.full[0], c * CT, seq); };
+  auto load_k = [&](int c) { load_tile_tma<D>(b, TK, &maps.k, &b.full[0], c * CT, seq); };
+  auto load_vq = [&](int c) {
+    load_tile_tma<D>(b, TV, &maps.v, &b.full[0], c * CT, seq);
+    if (HAS_Q) load_tile_tma<D>(b, TQ, &maps.q, &b.full[0], c * CT, seq);
+  };
+  auto prefetch = [&](int c) {
+    prefetch_tile<D>(&maps.dO, c * CT, seq);
+    prefetch_tile<D>(&maps.k, c * CT, seq);
+    prefetch_tile<D>(&maps.v, c * CT, seq);
+    if (HAS_Q) prefetch_tile<D>(&maps.q, c * CT, seq);
+  };
   if (threadIdx.x == 0) {
-    load(c0);
-    if (HAS_Q) load_q(c0);
+    load_dO(c0);
+    load_k(c0);
+    load_vq(c0);
   }
   TokenDecay next;
   next.load(p, b, seq, c0);
@@ -507,34 +570,32 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
   int c = c0;
   for (; c < c1; ++c) {
     const int t0 = c * CT, t = t0 + b.row;
+    const uint32_t phase = (c - c0) & 1;
     const bool more = c + 1 < c1;
     if (decays && b.half == 0) {
-      lam[b.row] = next.own;
-      float2 block_end;  // of the token's block
-      block_end.x = __shfl_sync(0xffffffffu, next.own.x, 31);
-      block_end.y = __shfl_sync(0xffffffffu, next.own.y, 31);
-      fac[b.row] = decay_between(block_end, next.own);
+      next.put<false>(b, lam, fac);
       if (more) next.load(p, b, seq, c + 1);
     }
-    b.wait_full(0, (c - c0) & 1);
+    b.wait_full(0, phase);
     if (PHI) map_tile_tc<D>(smem + TK, smem + TK, p.L - t0);
-    if (!HAS_Q && threadIdx.x == 0) tma_store_wait_read_all();
     fence_proxy_async_smem();
     tc_fence_before();
-    __syncthreads();
+    if (__syncthreads_or(b.failed)) break;
     if (threadIdx.x == 0) {
       tc_fence_after();
       const Operand a = along_row<SM::BOX>(b.base + TD);
       product<D>(b.tmem + T_S, a, along_row<SM::BOX>(b.base + TV), id_s, false);
+      mma_commit(&b.mma[0]);
 #pragma unroll
       for (int m = NM - 1; m >= 0; --m)
         product<D>(b.tmem + T_IN, a, along_row<ST::BOX>(b.base + m * ST::PLANE), id_in,
                    m < NM - 1);
-      mma_commit(b.mma);
+      mma_commit(&b.mma[1]);
+      if (more) prefetch(c + 1);
     }
     const float2 own = decays ? lam[b.row] : make_float2(0.f, 0.f);
     const float2 end = decays ? lam[CT - 1] : make_float2(0.f, 0.f);
-    b.wait_mma();
+    b.wait_mma(0, phase);
     // the scores as operand: row j, tokens i <= j
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
@@ -546,25 +607,37 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
       } else {
         float f[32], d[32];
         load_32(b, T_S + block * 32, f);
-        decay_factors<false>(b, block, lam, fac, own, decays, d);
+        if (DECAY) decay_factors<false>(b, block, lam, fac, own, d);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) f[e] = d[e] == 0.f ? 0.f : f[e] * d[e];
+        for (int e = 0; e < 32; ++e) {
+          if (DECAY) f[e] *= d[e];
+          if (block == b.quarter) f[e] = e <= b.lane ? f[e] : 0.f;
+        }
 #pragma unroll
         for (int e = 0; e < 16; ++e) w[e] = la::pack_bf16(f[2 * e], f[2 * e + 1]);
       }
       tmem_st16(b.at(T_A + block * 16), w);
     }
-    if (more && decays)
-      decayed_planes<D, NM>(smem + TK, smem, [&](int i) { return decay_between(end, lam[i]); });
     tmem_st_wait();
-    fence_proxy_async_smem();
     tc_fence_before();
-    if (__syncthreads_or(b.failed)) break;
-    if (threadIdx.x == 0) {
+    __syncthreads();
+    const Operand k = along_col<SM::BOX>(b.base + TK), v = along_col<SM::BOX>(b.base + TV);
+    if (threadIdx.x == 0) {  // the scores' share, while the decayed K is formed
       tc_fence_after();
-      const Operand k = along_col<SM::BOX>(b.base + TK), v = along_col<SM::BOX>(b.base + TV);
       product_ta<CT>(b.tmem + T_OUT, b.tmem + T_A, k, id_out, false);
-      if (more) {
+      mma_commit(&b.mma[2]);
+    }
+    b.wait_mma(1, phase);  // the state's planes and dO are read
+    if (threadIdx.x == 0 && more) load_dO(c + 1);
+    __syncwarp();
+    if (more) {
+      if (decays) {
+        decayed_rows<D, NM, CT>(smem + TK, smem, 0, [&](int i) { return decay_between(end, lam[i]); });
+        fence_proxy_async_smem();
+        __syncthreads();
+      }
+      if (threadIdx.x == 0) {  // the state's update, while dq leaves
+        tc_fence_after();
         if (decays) {
 #pragma unroll
           for (int m = NM - 1; m >= 0; --m)
@@ -573,11 +646,12 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
         } else {
           product<CT>(b.tmem + T_S, k, v, id_kv, false);
         }
+        mma_commit(&b.mma[3]);
       }
-      mma_commit(b.mma);
     }
-    b.wait_mma();
-    if (threadIdx.x == 0 && more && !b.failed) load(c + 1);
+    b.wait_mma(2, phase);
+    if (threadIdx.x == 0 && more && DECAY) load_k(c + 1);
+    __syncwarp();
     const float head = ex2_approx(own.x), all = ex2_approx(end.x);
     float dot = 0.f;
 #pragma unroll
@@ -607,6 +681,13 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
     if (NM == 3 && p.rq && b.half == 0 && t < p.L)
       p.rq[(size_t)seq * p.L + t] = dot + sums[b.row];
     if (more) {
+      b.wait_mma(3, phase);
+      if (threadIdx.x == 0) {
+        tma_store_wait_read_all();  // the fourth tile
+        if (!DECAY) load_k(c + 1);
+        load_vq(c + 1);
+      }
+      __syncwarp();
       state.update(b, T_S, all);
       state.planes(b);
     } else if (NM == 3 && p.rq) {  // <G, e^L_C S>: the pairs around the segment's last chunk
@@ -614,16 +695,9 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
                        : p.dSf ? p.dSf + (size_t)seq * es : nullptr;
       if (G) around = state.dot(G, b) * all;
     }
-    if (HAS_Q && threadIdx.x == 0 && more && !b.failed) {
-      tma_store_wait_read_all();
-      load_q(c + 1);
-    }
   }
   if (threadIdx.x == 0) {
-    if (c < c1) {
-      tc::drain_wait(&b.full[0], (c - c0) & 1);
-      tc::drain_wait(b.mma, b.mma_phase ^ 1);
-    }
+    if (c < c1) tc::drain_wait(&b.full[0], (c - c0) & 1);
     tma_store_wait_all();
   }
   if (NM == 3 && p.rq) {
@@ -641,7 +715,7 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
 }
 
 // ---------------------------------------------------------------- dk and dv
-template <int D, int NM, bool PHI>
+template <int D, int NM, bool PHI, bool DECAY>
 __global__ void __launch_bounds__(kThreads, 1)
 grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned int *err) {
   // A fifth tile holds phi(k) beside k, which its derivative needs.  dk and dv leave by k's and
@@ -663,22 +737,33 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
   float2 *lam = reinterpret_cast<float2 *>(smem + SM::OFF_LAM);
   float *fac = reinterpret_cast<float *>(smem + SM::OFF_FAC);
   float *part = reinterpret_cast<float *>(smem + SM::OFF_LAM);  // [4][CT], once lam and fac are used
+  float *half_1 = part + 4 * CT;                                // [CT], behind it
   const int seq = blockIdx.x / p.segments, seg = blockIdx.x % p.segments;
   const int c0 = seg * p.per, c1 = min(c0 + p.per, p.chunks), n = c1 - c0;
   const size_t es = (size_t)D * D;
-  const bool decays = p.decay_kind != LA_DECAY_NONE;
+  constexpr bool decays = DECAY;
   constexpr uint32_t TQ = SM::OFF_TILES, TK = TQ + SM::TILE, TV = TK + SM::TILE,
                      TD = TV + SM::TILE, TKP = PHI ? TD + SM::TILE : TK;
-  auto load_qo = [&](int c) {
+  auto load_q = [&](int c) {
     mbar_arrive_expect_tx(&b.full[0], 4 * SM::TILE);
     load_tile_tma<D>(b, TQ, &maps.q, &b.full[0], c * CT, seq);
-    load_tile_tma<D>(b, TD, &maps.dO, &b.full[0], c * CT, seq);
   };
   auto load_kv = [&](int c) {
     load_tile_tma<D>(b, TK, &maps.k, &b.full[0], c * CT, seq);
     load_tile_tma<D>(b, TV, &maps.v, &b.full[0], c * CT, seq);
   };
-  if (threadIdx.x == 0) load_qo(c1 - 1), load_kv(c1 - 1);
+  auto load_dO = [&](int c) { load_tile_tma<D>(b, TD, &maps.dO, &b.full[0], c * CT, seq); };
+  auto prefetch = [&](int c) {
+    prefetch_tile<D>(&maps.q, c * CT, seq);
+    prefetch_tile<D>(&maps.k, c * CT, seq);
+    prefetch_tile<D>(&maps.v, c * CT, seq);
+    prefetch_tile<D>(&maps.dO, c * CT, seq);
+  };
+  if (threadIdx.x == 0) {
+    load_q(c1 - 1);
+    load_kv(c1 - 1);
+    load_dO(c1 - 1);
+  }
   TokenDecay next;
   next.load(p, b, seq, c1 - 1);
   StateRow<D, NM> state;
@@ -688,35 +773,37 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
   int done = 0;
   for (; done < n; ++done) {
     const int c = c1 - 1 - done, t0 = c * CT, t = t0 + b.row;
+    const uint32_t phase = done & 1;
     const bool more = done + 1 < n, update = more || (p.dS0 && seg == 0);
     if (decays && b.half == 0) {
-      lam[b.row] = next.own;
-      fac[b.row] = decay_between(next.own, next.before);
+      next.put<true>(b, lam, fac);
       if (more) next.load(p, b, seq, c - 1);
     }
-    b.wait_full(0, done & 1);
+    b.wait_full(0, phase);
     if (PHI) {
       map_tile_tc<D>(smem + TQ, smem + TQ, p.L - t0);
       map_tile_tc<D>(smem + TK, smem + TKP, p.L - t0);
     }
     fence_proxy_async_smem();
     tc_fence_before();
-    __syncthreads();
+    if (__syncthreads_or(b.failed)) break;
     if (threadIdx.x == 0) {
       tc_fence_after();
       const Operand ak = along_row<SM::BOX>(b.base + TKP), av = along_row<SM::BOX>(b.base + TV);
       product<D>(b.tmem + T_P, ak, along_row<SM::BOX>(b.base + TQ), id_s, false);
       product<D>(b.tmem + T_DP, av, along_row<SM::BOX>(b.base + TD), id_s, false);
+      mma_commit(&b.mma[0]);
       product<D>(b.tmem + T_V, ak, along_col<ST::BOX>(b.base), id_out, false);
 #pragma unroll
       for (int m = NM - 1; m >= 0; --m)
         product<D>(b.tmem + T_K, av, along_row<ST::BOX>(b.base + m * ST::PLANE), id_in,
                    m < NM - 1);
-      mma_commit(b.mma);
+      mma_commit(&b.mma[1]);
+      if (more) prefetch(c - 1);
     }
     const float2 own = decays ? lam[b.row] : make_float2(0.f, 0.f);
     const float2 end = decays ? lam[CT - 1] : make_float2(0.f, 0.f);
-    b.wait_mma();
+    b.wait_mma(0, phase);
     // the scores as operands: row i, tokens j >= i
     uint32_t wp[2][16], wd[2][16];
     float row_sum = 0.f, col_sum[2] = {0.f, 0.f};
@@ -731,12 +818,15 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
       float f[32], g[32], d[32];
       load_32(b, T_P + block * 32, f);
       load_32(b, T_DP + block * 32, g);
-      decay_factors<true>(b, block, lam, fac, own, decays, d);
+      if (DECAY) decay_factors<true>(b, block, lam, fac, own, d);
 #pragma unroll
       for (int e = 0; e < 32; ++e) {
-        const bool in = d[e] != 0.f;
-        f[e] = in ? f[e] * d[e] : 0.f;
-        d[e] = in ? g[e] * d[e] : 0.f;
+        if (DECAY) f[e] *= d[e];
+        d[e] = DECAY ? d[e] * g[e] : g[e];
+        if (block == b.quarter) {
+          f[e] = e >= b.lane ? f[e] : 0.f;
+          d[e] = e >= b.lane ? d[e] : 0.f;
+        }
       }
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
@@ -746,7 +836,8 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
       if (NM == 3) {  // the pairs i < j: their sums over the row and, over the warp's rows, the columns
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
-          f[e] = block == b.quarter && e <= b.lane ? 0.f : f[e] * g[e];
+          f[e] *= g[e];
+          if (block == b.quarter) f[e] = e > b.lane ? f[e] : 0.f;
           row_sum += f[e];
         }
         // lane e ends with column e's
@@ -770,6 +861,7 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
       tmem_st16(b.at(T_AP + b.half * 32 + x * 16), wp[x]);
       tmem_st16(b.at(T_ADP + b.half * 32 + x * 16), wd[x]);
     }
+    b.wait_mma(1, phase);
     const float tail = decay_between(end, own);
     float dot = 0.f;
     if (decays) {  // the state's share, by each token's decay to the chunk's end
@@ -792,47 +884,44 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
         }
       }
     }
-    if (update && decays)
-      decayed_planes<D, NM>(smem + TQ, smem, [&](int i) { return ex2_approx(lam[i].x); });
+    if (NM == 3 && b.half == 1) half_1[b.row] = dot;
     tmem_st_wait();
-    fence_proxy_async_smem();
     tc_fence_before();
-    if (__syncthreads_or(b.failed)) break;
-    if (threadIdx.x == 0) {
+    __syncthreads();
+    const Operand q = along_col<SM::BOX>(b.base + TQ), dO = along_col<SM::BOX>(b.base + TD);
+    if (threadIdx.x == 0) {  // the scores' share, while the decayed Q is formed
       tc_fence_after();
-      const Operand q = along_col<SM::BOX>(b.base + TQ), dO = along_col<SM::BOX>(b.base + TD);
       product_ta<CT>(b.tmem + T_V, b.tmem + T_AP, dO, id_out, true);
       product_ta<CT>(b.tmem + T_K, b.tmem + T_ADP, q, id_out, true);
-      if (update) {
-        if (decays) {
-#pragma unroll
-          for (int m = NM - 1; m >= 0; --m)
-            product<CT>(b.tmem + T_U, along_col<SM::BOX>(b.base + m * SM::TILE), dO, id_kv,
-                        m < NM - 1);
-        } else {
-          product<CT>(b.tmem + T_U, q, dO, id_kv, false);
-        }
-      }
-      mma_commit(b.mma);
+      mma_commit(&b.mma[2]);
     }
-    if (NM == 3 && p.rk) {  // over the halves of a row and the quarters of a column
-      const size_t to = (size_t)seq * p.L + t;
+    if (NM == 3 && p.rk && b.half == 0 && t < p.L)
+      p.rk[(size_t)seq * p.L + t] = dot + half_1[b.row];
+    if (update && decays) {
+      decayed_rows<D, NM, CT>(smem + TQ, smem, 0, [&](int i) { return ex2_approx(lam[i].x); });
+      fence_proxy_async_smem();
+    }
+    if (decays) __syncthreads();
+    if (threadIdx.x == 0 && update) {  // the state's update, while dk and dv leave
+      tc_fence_after();
+      if (decays) {
+#pragma unroll
+        for (int m = NM - 1; m >= 0; --m)
+          product<CT>(b.tmem + T_U, along_col<SM::BOX>(b.base + m * SM::TILE), dO, id_kv,
+                      m < NM - 1);
+      } else {
+        product<CT>(b.tmem + T_U, q, dO, id_kv, false);
+      }
+      mma_commit(&b.mma[3]);
+    }
+    if (NM == 3 && p.rc) {
       part[b.quarter * CT + b.half * 64 + b.lane] = col_sum[0];
       part[b.quarter * CT + b.half * 64 + 32 + b.lane] = col_sum[1];
-      __syncthreads();
-      float col = 0.f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) col += part[i * CT + b.row];
-      __syncthreads();
-      if (b.half == 1) part[b.row] = row_sum, part[CT + b.row] = dot;
-      __syncthreads();
-      if (b.half == 0 && t < p.L) {
-        p.rc[to] = col - (row_sum + part[b.row]);
-        p.rk[to] = dot + part[CT + b.row];
-      }
+      if (b.half == 1) half_1[b.row] = row_sum;
     }
-    b.wait_mma();
-    if (threadIdx.x == 0 && more && !b.failed) load_qo(c - 1);
+    b.wait_mma(2, phase);
+    if (threadIdx.x == 0 && more && DECAY) load_q(c - 1);
+    __syncwarp();
 #pragma unroll
     for (int x = 0; x < N; x += 32) {
       const int col = b.half * N + x;
@@ -852,24 +941,38 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
       store_tile_tma<D>(b, TK, &maps.dk, t0, seq);
       tma_store_commit();
     }
-    if (update) state.update(b, T_U, ex2_approx(end.x));
-    if (more) state.planes(b);
-    if (threadIdx.x == 0 && more && !b.failed) {
-      tma_store_wait_read_all();
-      load_kv(c - 1);
+    if (NM == 3 && p.rc) {
+      if (b.half == 0 && t < p.L) {
+        float col = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) col += part[i * CT + b.row];
+        p.rc[(size_t)seq * p.L + t] = col - (row_sum + half_1[b.row]);
+      }
+      __syncthreads();  // part gives way to the next chunk's decays
+    }
+    if (update) {
+      b.wait_mma(3, phase);
+      if (threadIdx.x == 0 && more) {
+        if (!DECAY) load_q(c - 1);
+        load_dO(c - 1);
+        tma_store_wait_read_all();
+        load_kv(c - 1);
+      }
+      __syncwarp();
+      state.update(b, T_U, ex2_approx(end.x));
+      if (more) state.planes(b);
     }
   }
   if (done == n) {
     if (p.dS0 && seg == 0) state.store(p.dS0 + (size_t)seq * es, b);
   } else if (threadIdx.x == 0) {
     tc::drain_wait(&b.full[0], done & 1);
-    tc::drain_wait(b.mma, b.mma_phase ^ 1);
   }
   if (threadIdx.x == 0) tma_store_wait_all();
   b.finish(COLUMNS);
 }
 
-template <int D, int NM, bool PHI>
+template <int D, int NM, bool PHI, bool DECAY>
 cudaError_t launch_tc(const ChunkBwd &p, int seqs, cudaStream_t stream) {
   using SS = Smem<D, NM, 2, 2>;
   using SQ = Smem<D, NM, 4, 1>;
@@ -885,15 +988,15 @@ cudaError_t launch_tc(const ChunkBwd &p, int seqs, cudaStream_t stream) {
   unsigned int *err = device_error_word();
   cudaError_t e;
   if (p.segments > 1) {
-    auto share = segment_share_tc_kernel<D, NM, PHI>;
+    auto share = segment_share_tc_kernel<D, NM, PHI, DECAY>;
     static int set[64];
     if ((e = tc::set_smem_once(share, SS::BYTES, set)) != cudaSuccess) return e;
     share<<<dim3((unsigned)(seqs * (p.segments - 1)), 2), kThreads, SS::BYTES, stream>>>(m, p, err);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if ((e = launch_segment_scan(p, seqs, stream)) != cudaSuccess) return e;
   }
-  auto gq = grad_q_tc_kernel<D, NM, PHI>;
-  auto gkv = grad_kv_tc_kernel<D, NM, PHI>;
+  auto gq = grad_q_tc_kernel<D, NM, PHI, DECAY>;
+  auto gkv = grad_kv_tc_kernel<D, NM, PHI, DECAY>;
   static int set_q[64], set_kv[64];
   if ((e = tc::set_smem_once(gq, SQ::BYTES, set_q)) != cudaSuccess) return e;
   if ((e = tc::set_smem_once(gkv, SK::BYTES, set_kv)) != cudaSuccess) return e;
@@ -903,17 +1006,21 @@ cudaError_t launch_tc(const ChunkBwd &p, int seqs, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-template <int D> cudaError_t launch_d(const ChunkBwd &p, int seqs, bool planes, cudaStream_t stream) {
-  if (planes) return launch_tc<D, 3, false>(p, seqs, stream);
-  return p.phi == LA_PHI_ELU1 ? launch_tc<D, 1, true>(p, seqs, stream)
-                              : launch_tc<D, 1, false>(p, seqs, stream);
+template <int D, bool DECAY>
+cudaError_t launch_d(const ChunkBwd &p, int seqs, bool planes, cudaStream_t stream) {
+  if (planes) return launch_tc<D, 3, false, DECAY>(p, seqs, stream);
+  return p.phi == LA_PHI_ELU1 ? launch_tc<D, 1, true, DECAY>(p, seqs, stream)
+                              : launch_tc<D, 1, false, DECAY>(p, seqs, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_chunk_bwd_tc(const ChunkBwd &p, int seqs, bool planes, cudaStream_t stream) {
-  return p.n_k == 128 ? launch_d<128>(p, seqs, planes, stream)
-                      : launch_d<64>(p, seqs, planes, stream);
+  if (p.n_k == 128)
+    return p.decay_kind != LA_DECAY_NONE ? launch_d<128, true>(p, seqs, planes, stream)
+                                         : launch_d<128, false>(p, seqs, planes, stream);
+  return p.decay_kind != LA_DECAY_NONE ? launch_d<64, true>(p, seqs, planes, stream)
+                                       : launch_d<64, false>(p, seqs, planes, stream);
 }
 
 }  // namespace la
