@@ -76,8 +76,9 @@ size_t lay_out(const ChunkBwdArgs &a, const Plan &plan, bool decay_grad, char *b
   }
   if (decay_grad) {
     float *rq = part(seqs * a.L), *rk = part(seqs * a.L), *rc = part(seqs * a.L);
+    float *cs = plan.tc ? part(seqs * a.L) : nullptr, *rs = plan.tc ? part(seqs * a.L) : nullptr;
     float *around = part(seqs * plan.segments), *sums = part(seqs * plan.segments);
-    if (p) p->rq = rq, p->rk = rk, p->rc = rc, p->around = around, *by_segment = sums;
+    if (p) p->rq = rq, p->rk = rk, p->rc = rc, p->cs = cs, p->rs = rs, p->around = around, *by_segment = sums;
   }
   return at;
 }
@@ -160,32 +161,51 @@ __global__ void __launch_bounds__(256) segment_scan_kernel(const ChunkBwd p, int
   }
 }
 
-// A block: the tokens of one segment.  Their decays' gradients from the shares:
-//     sum over s >= t of rq + sum over s < t of rk + pairs within the chunk + around,
-// with `around` = <G, e^L_C S> given for the segment's last chunk; with the chunk's rq it
-// is <G, S> in front of the chunk, and that less the next chunk's rk is its `around`.
-template <int C>
+// The sum of v over the warp's lanes in front of this one (FRONT) or behind it, within groups of
+// WIDTH lanes.
+template <bool FRONT, int WIDTH> __device__ __forceinline__ float lanes_sum(float v, int lane) {
+  const int at = lane % WIDTH;
+  float x = v;
+#pragma unroll
+  for (int off = 1; off < WIDTH; off <<= 1) {
+    const float y = FRONT ? __shfl_up_sync(0xffffffffu, x, off, WIDTH)
+                          : __shfl_down_sync(0xffffffffu, x, off, WIDTH);
+    if (FRONT ? at >= off : at + off < WIDTH) x += y;
+  }
+  const float y = FRONT ? __shfl_up_sync(0xffffffffu, x, 1, WIDTH)
+                        : __shfl_down_sync(0xffffffffu, x, 1, WIDTH);
+  return FRONT ? at ? y : 0.f : at < WIDTH - 1 ? y : 0.f;
+}
+template <int WIDTH> __device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+  for (int off = WIDTH / 2; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  return v;
+}
+
+// A block: the tokens of one segment.  Their decays' gradients are sums of pairs (i < t <= j):
+//     over s >= t of rq + cs, over s < t of rk + rs, within t's block of BLOCK tokens, and `around`
+// the block.  <G, e^L_C S>, the pairs around a chunk, is given for the segment's last chunk; with
+// the chunk's rq it is <G, S> in front of the chunk, and that less the next chunk's rk is the
+// next one's.  Around a block of a chunk: those, the chunk's rq behind the block, its rk in front,
+// and its pairs across the block (from one to the next: less cs, plus rs).
+template <int C, int BLOCK>
 __global__ void __launch_bounds__(256)
 decay_grad_kernel(const ChunkBwd p, float *ddecay, float *by_segment) {
   __shared__ float sum_q[kMaxPer], sum_k[kMaxPer], all[kMaxPer];
   __shared__ double share[8];
-  constexpr int N = C / 32;
+  constexpr int N = C / 32, LANES = BLOCK / N, BLOCKS = C / BLOCK;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int seq = blockIdx.x / p.segments, seg = blockIdx.x % p.segments;
   const int c0 = seg * p.per, n = min(p.per, p.chunks - c0);
   const size_t base = (size_t)seq * p.L;
   for (int c = warp; c < n; c += 8) {
     float q = 0.f, k = 0.f;
+#pragma unroll
     for (int i = 0; i < N; ++i) {
       const int t = (c0 + c) * C + lane * N + i;
-      if (t >= p.L) break;
-      q += p.rq[base + t];
-      k += p.rk[base + t];
+      if (t < p.L) q += p.rq[base + t], k += p.rk[base + t];
     }
-    for (int off = 16; off > 0; off >>= 1) {
-      q += __shfl_xor_sync(0xffffffffu, q, off);
-      k += __shfl_xor_sync(0xffffffffu, k, off);
-    }
+    q = group_sum<32>(q), k = group_sum<32>(k);
     if (lane == 0) {
       sum_q[c] = q, sum_k[c] = k;
       all[c] = p.lam[((size_t)seq * p.chunks + c0 + c) * C + C - 1].x;
@@ -205,47 +225,56 @@ decay_grad_kernel(const ChunkBwd p, float *ddecay, float *by_segment) {
   __syncthreads();
   double total = 0.0;
   for (int c = warp; c < n; c += 8) {
-    float q[N], k[N], r[N];
-    float sq = 0.f, sk = 0.f, sr = 0.f;
+    float q[N], k[N], r[N], cs[N], rs[N];
+    float sq = 0.f, sk = 0.f, sr = 0.f, scs = 0.f, srs = 0.f;
+#pragma unroll
     for (int i = 0; i < N; ++i) {
       const int t = (c0 + c) * C + lane * N + i;
-      q[i] = t < p.L ? p.rq[base + t] : 0.f;
-      k[i] = t < p.L ? p.rk[base + t] : 0.f;
-      r[i] = t < p.L ? p.rc[base + t] : 0.f;
-      sq += q[i], sk += k[i], sr += r[i];
+      const bool live = t < p.L;
+      q[i] = live ? p.rq[base + t] : 0.f;
+      k[i] = live ? p.rk[base + t] : 0.f;
+      r[i] = live ? p.rc[base + t] : 0.f;
+      cs[i] = BLOCKS > 1 && live ? p.cs[base + t] : 0.f;
+      rs[i] = BLOCKS > 1 && live ? p.rs[base + t] : 0.f;
+      sq += q[i], sk += k[i], sr += r[i], scs += cs[i], srs += rs[i];
     }
-    // sums over the lanes behind (q, r) and in front (k, r)
-    float q_behind = 0.f, k_before = 0.f, r_behind = 0.f, r_before = 0.f;
-    float xq = sq, xk = sk, xr = sr, yr = sr;
-    for (int off = 1; off < 32; off <<= 1) {
-      const float dq = __shfl_down_sync(0xffffffffu, xq, off);
-      const float dr = __shfl_down_sync(0xffffffffu, xr, off);
-      const float dk = __shfl_up_sync(0xffffffffu, xk, off);
-      const float er = __shfl_up_sync(0xffffffffu, yr, off);
-      if (lane + off < 32) xq += dq, xr += dr;
-      if (lane >= off) xk += dk, yr += er;
+    float around = all[c];
+    if (BLOCKS > 1) {
+      const int block = lane / LANES;
+      const float bq = group_sum<LANES>(sq), bk = group_sum<LANES>(sk);
+      const float bc = group_sum<LANES>(scs), br = group_sum<LANES>(srs);
+      float across = 0.f, mine = 0.f;  // pairs across block x
+#pragma unroll
+      for (int x = 0; x < BLOCKS; ++x) {
+        if (x > 0) across -= __shfl_sync(0xffffffffu, bc, x * LANES);
+        if (x == block && x > 0 && x < BLOCKS - 1) mine = across;
+        across += __shfl_sync(0xffffffffu, br, x * LANES);
+        const float xq = __shfl_sync(0xffffffffu, bq, x * LANES);
+        const float xk = __shfl_sync(0xffffffffu, bk, x * LANES);
+        if (x > block) around += xq;
+        if (x < block) around += xk;
+      }
+      around += mine;
     }
-    q_behind = __shfl_down_sync(0xffffffffu, xq, 1);
-    r_behind = __shfl_down_sync(0xffffffffu, xr, 1);
-    k_before = __shfl_up_sync(0xffffffffu, xk, 1);
-    r_before = __shfl_up_sync(0xffffffffu, yr, 1);
-    if (lane == 31) q_behind = r_behind = 0.f;
-    if (lane == 0) k_before = r_before = 0.f;
+    const float q_behind = lanes_sum<false, LANES>(sq + scs, lane);
+    const float k_before = lanes_sum<true, LANES>(sk + srs, lane);
+    const float r_behind = lanes_sum<false, LANES>(sr, lane);
+    const float r_before = lanes_sum<true, LANES>(sr, lane);
+    const bool first = lane % LANES < LANES / 2;  // the shorter of two sums that agree
+#pragma unroll
     for (int i = 0; i < N; ++i) {
       const int t = (c0 + c) * C + lane * N + i;
-      float g = q_behind, pairs = lane < 16 ? -r_before : r_behind, before = k_before;
+      float g = q_behind, before = k_before, pairs = first ? -r_before : r_behind;
+#pragma unroll
       for (int j = 0; j < N; ++j) {
-        if (j >= i) g += q[j];
-        if (j < i) before += k[j];
-        if (lane < 16 && j < i) pairs -= r[j];
-        if (lane >= 16 && j >= i) pairs += r[j];
+        if (j >= i) g += q[j] + cs[j];
+        if (j < i) before += k[j] + rs[j];
+        if (first && j < i) pairs -= r[j];
+        if (!first && j >= i) pairs += r[j];
       }
-      g += before + pairs + all[c];
+      g += before + pairs + around;
       if (t >= p.L) continue;
-      if (p.decay_kind == LA_DECAY_GATE_LOGIT) {
-        const float x = p.decay[base + t];
-        g *= -1.f / (1.f + expf(-x));
-      }
+      if (p.decay_kind == LA_DECAY_GATE_LOGIT) g *= -1.f / (1.f + expf(-p.decay[base + t]));
       if (p.decay_kind == LA_DECAY_HEAD) total += g;
       else ddecay[base + t] = g;
     }
@@ -311,7 +340,7 @@ cudaError_t launch_chunk_bwd(const ChunkBwdArgs &a) {
   if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
   ChunkBwd p{a.q, a.k, a.v, a.dO, a.dq, a.dk_out, a.dv_out, a.decay, a.S0, a.dS_final, a.dS0,
              a.H, a.L, a.dk, a.dv, a.phi, a.decay_kind, plan.chunks, plan.segments, plan.per,
-             nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr};
+             nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr};
   float *by_segment = nullptr;
   lay_out(a, plan, decay_grad, static_cast<char *>(a.workspace), &p, &by_segment);
   cudaError_t e = cudaSuccess;
@@ -325,11 +354,11 @@ cudaError_t launch_chunk_bwd(const ChunkBwdArgs &a) {
                   : launch_chunk_bwd_bf16(p, (int)seqs, plan.wide, plan.planes, a.stream);
   if (e != cudaSuccess || !decay_grad) return e;
   if (plan.chunk == 128)
-    decay_grad_kernel<128><<<(unsigned)blocks, 256, 0, a.stream>>>(p, a.ddecay, by_segment);
+    decay_grad_kernel<128, 32><<<(unsigned)blocks, 256, 0, a.stream>>>(p, a.ddecay, by_segment);
   else if (plan.chunk == 32)
-    decay_grad_kernel<32><<<(unsigned)blocks, 256, 0, a.stream>>>(p, a.ddecay, by_segment);
+    decay_grad_kernel<32, 32><<<(unsigned)blocks, 256, 0, a.stream>>>(p, a.ddecay, by_segment);
   else
-    decay_grad_kernel<64><<<(unsigned)blocks, 256, 0, a.stream>>>(p, a.ddecay, by_segment);
+    decay_grad_kernel<64, 64><<<(unsigned)blocks, 256, 0, a.stream>>>(p, a.ddecay, by_segment);
   if ((e = cudaGetLastError()) != cudaSuccess || a.decay_kind != LA_DECAY_HEAD) return e;
   head_decay_kernel<<<a.H, 32, 0, a.stream>>>(by_segment, a.ddecay, a.B, a.H, plan.segments);
   return cudaGetLastError();

@@ -58,7 +58,10 @@ struct ChunkBwd {
   float *total;                // [seq][segments] log2 of a segment's decay
   float2 *lam;                 // [seq][chunks][C] log2 of the decay from a chunk's start to a
                                // token, as a sum of two floats (unused without a decay)
-  float *rq, *rk, *rc;         // [seq][L] shares of ddecay, or null
+  // Shares of ddecay [seq][L], or null: the pairs of a token with tokens before its chunk (rq)
+  // and behind it (rk), of its block of the chunk (rc: as the later one less as the earlier one),
+  // and of the chunk's blocks before (cs) and behind (rs) its own, where a chunk has blocks.
+  float *rq, *rk, *rc, *cs, *rs;
   float *around;               // [seq][segments] <G, e^L_C S> of a segment's last chunk
 };
 

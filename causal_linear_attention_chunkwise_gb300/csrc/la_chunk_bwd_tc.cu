@@ -37,6 +37,9 @@ using tc::Ctl;
 
 constexpr int CT = 128;       // tokens of a chunk
 constexpr int kThreads = 256;
+// The thread that issues products and copies waits when their queue is full: it is one of a warp
+// that has no scores to work on, all of its columns lying outside the mask.
+constexpr int kLeaderQ = 128, kLeaderKV = 96;
 constexpr uint32_t HI = smem_desc_sw128_hi(1024);
 
 // Shared memory of a walk with TILES input tiles (in STAGES sets).  The planes come first:
@@ -262,13 +265,20 @@ struct TokenDecay {
       at.x = __shfl_sync(0xffffffffu, own.x, 31);
       at.y = __shfl_sync(0xffffffffu, own.y, 31);
     }
-    const float x = LATER ? (own.x - at.x) + (own.y - at.y) : (at.x - own.x) + (at.y - own.y);
     lam[b.row] = own;
-    fac[b.row] = ex2_approx(x);
-    const bool all = __all_sync(0xffffffffu, fabsf(x) < 60.f);
+    fac[b.row] = LATER ? decay_between(own, at) : decay_between(at, own);
+    const bool all = __all_sync(0xffffffffu, fabsf(own.x - before.x) < 60.f);
     if (b.lane == 0) b.narrow[b.quarter] = all;
   }
 };
+
+__device__ __forceinline__ void decay_products(const float *fac, float mine, float (&d)[32]) {
+#pragma unroll
+  for (int e = 0; e < 32; e += 4) {
+    const float4 x = *reinterpret_cast<const float4 *>(fac + e);
+    d[e] = mine * x.x, d[e + 1] = mine * x.y, d[e + 2] = mine * x.z, d[e + 3] = mine * x.w;
+  }
+}
 
 // The decays of this thread's row (a token of block b.quarter) and column block `block`.
 // LATER: the columns come after the row (else before it); anything outside the mask.
@@ -279,12 +289,7 @@ __device__ __forceinline__ void decay_factors(const Block &b, int block, const f
   if (!diagonal || b.narrow[block]) {
     float2 at = make_float2(0.f, 0.f);
     if (!LATER || block) at = lam[LATER ? block * 32 - 1 : block * 32 + 31];
-    const float mine = LATER ? decay_between(at, own) : decay_between(own, at);
-#pragma unroll
-    for (int e = 0; e < 32; e += 4) {
-      const float4 x = *reinterpret_cast<const float4 *>(fac + block * 32 + e);
-      d[e] = mine * x.x, d[e + 1] = mine * x.y, d[e + 2] = mine * x.z, d[e + 3] = mine * x.w;
-    }
+    decay_products(fac + block * 32, LATER ? decay_between(at, own) : decay_between(own, at), d);
   } else {
 #pragma unroll
     for (int e = 0; e < 32; ++e) {
@@ -525,13 +530,16 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
   constexpr uint32_t id_out = idesc_bf16_f32(128, D, false, true);
   constexpr uint32_t id_kv = idesc_bf16_f32(128, D, true, true);
   constexpr int N = D / 2;
+  // NM = 3: Q K^T as well, in the scores' share's place or behind everything.
+  constexpr uint32_t T_P = D == 128 ? T_OUT : 384;
   static_assert(T_A + 64 <= COLUMNS, "tensor memory");
   extern __shared__ __align__(1024) unsigned char smem[];
   Block b;
   b.start(smem, SM::OFF_BAR, COLUMNS, err);
   float2 *lam = reinterpret_cast<float2 *>(smem + SM::OFF_LAM);
   float *fac = reinterpret_cast<float *>(smem + SM::OFF_FAC);
-  float *sums = reinterpret_cast<float *>(smem + SM::OFF_MORE);
+  float *sums = reinterpret_cast<float *>(smem + SM::OFF_MORE);  // [2][CT] half 1's sums
+  float *inside = sums + CT;  // before that: factors of pairs of one block
   const int seq = blockIdx.x / p.segments, seg = blockIdx.x % p.segments;
   const int c0 = seg * p.per, c1 = min(c0 + p.per, p.chunks);
   const size_t es = (size_t)D * D;
@@ -555,7 +563,7 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
     prefetch_tile<D>(&maps.v, c * CT, seq);
     if (HAS_Q) prefetch_tile<D>(&maps.q, c * CT, seq);
   };
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == kLeaderQ) {
     load_dO(c0);
     load_k(c0);
     load_vq(c0);
@@ -574,6 +582,7 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
     const bool more = c + 1 < c1;
     if (decays && b.half == 0) {
       next.put<false>(b, lam, fac);
+      if (NM == 3) inside[b.row] = decay_between(next.before, next.own);
       if (more) next.load(p, b, seq, c + 1);
     }
     b.wait_full(0, phase);
@@ -581,10 +590,13 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
     fence_proxy_async_smem();
     tc_fence_before();
     if (__syncthreads_or(b.failed)) break;
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == kLeaderQ) {
       tc_fence_after();
       const Operand a = along_row<SM::BOX>(b.base + TD);
       product<D>(b.tmem + T_S, a, along_row<SM::BOX>(b.base + TV), id_s, false);
+      if (NM == 3 && DECAY)
+        product<D>(b.tmem + T_P, along_row<SM::BOX>(b.base + TQ), along_row<SM::BOX>(b.base + TK),
+                   id_s, false);
       mma_commit(&b.mma[0]);
 #pragma unroll
       for (int m = NM - 1; m >= 0; --m)
@@ -597,9 +609,12 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
     const float2 end = decays ? lam[CT - 1] : make_float2(0.f, 0.f);
     b.wait_mma(0, phase);
     // the scores as operand: row j, tokens i <= j
+    const float2 before = DECAY && b.quarter ? lam[b.quarter * 32 - 1] : make_float2(0.f, 0.f);
+    float pairs = 0.f, pairs_in = 0.f;  // with tokens of the blocks before, of this block
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const int block = b.half * 2 + x;
+      const bool diagonal = block == b.quarter;
       uint32_t w[16];
       if (block > b.quarter) {  // all behind the warp's rows
 #pragma unroll
@@ -607,11 +622,26 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
       } else {
         float f[32], d[32];
         load_32(b, T_S + block * 32, f);
-        if (DECAY) decay_factors<false>(b, block, lam, fac, own, d);
+        if (DECAY) {
+          if (NM == 3 && diagonal && b.narrow[block])  // grad_kv_tc_kernel's factors: see rc
+            decay_products(inside + block * 32, decay_between(own, before), d);
+          else
+            decay_factors<false>(b, block, lam, fac, own, d);
+        }
+        if (NM == 3 && DECAY) {
+          float g[32], s[4] = {0.f, 0.f, 0.f, 0.f};
+          load_32(b, T_P + block * 32, g);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const float pair = g[e] * d[e] * f[e];
+            s[e % 4] += !diagonal || e < b.lane ? pair : 0.f;
+          }
+          (diagonal ? pairs_in : pairs) += (s[0] + s[1]) + (s[2] + s[3]);
+        }
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
           if (DECAY) f[e] *= d[e];
-          if (block == b.quarter) f[e] = e <= b.lane ? f[e] : 0.f;
+          if (diagonal) f[e] = e <= b.lane ? f[e] : 0.f;
         }
 #pragma unroll
         for (int e = 0; e < 16; ++e) w[e] = la::pack_bf16(f[2 * e], f[2 * e + 1]);
@@ -622,13 +652,13 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
     tc_fence_before();
     __syncthreads();
     const Operand k = along_col<SM::BOX>(b.base + TK), v = along_col<SM::BOX>(b.base + TV);
-    if (threadIdx.x == 0) {  // the scores' share, while the decayed K is formed
+    if (threadIdx.x == kLeaderQ) {  // the scores' share, while the decayed K is formed
       tc_fence_after();
       product_ta<CT>(b.tmem + T_OUT, b.tmem + T_A, k, id_out, false);
       mma_commit(&b.mma[2]);
     }
     b.wait_mma(1, phase);  // the state's planes and dO are read
-    if (threadIdx.x == 0 && more) load_dO(c + 1);
+    if (threadIdx.x == kLeaderQ && more) load_dO(c + 1);
     __syncwarp();
     if (more) {
       if (decays) {
@@ -636,7 +666,7 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
         fence_proxy_async_smem();
         __syncthreads();
       }
-      if (threadIdx.x == 0) {  // the state's update, while dq leaves
+      if (threadIdx.x == kLeaderQ) {  // the state's update, while dq leaves
         tc_fence_after();
         if (decays) {
 #pragma unroll
@@ -650,7 +680,7 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
       }
     }
     b.wait_mma(2, phase);
-    if (threadIdx.x == 0 && more && DECAY) load_k(c + 1);
+    if (threadIdx.x == kLeaderQ && more && DECAY) load_k(c + 1);
     __syncwarp();
     const float head = ex2_approx(own.x), all = ex2_approx(end.x);
     float dot = 0.f;
@@ -670,19 +700,25 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
         stage_8<PHI>(cell, g + e);
       }
     }
-    if (NM == 3 && b.half == 1) sums[b.row] = dot;
+    if (NM == 3 && b.half == 1) sums[b.row] = dot, inside[b.row] = pairs;
     fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == kLeaderQ) {
       store_tile_tma<D>(b, TQ, &maps.dq, t0, seq);
       tma_store_commit();
     }
-    if (NM == 3 && p.rq && b.half == 0 && t < p.L)
-      p.rq[(size_t)seq * p.L + t] = dot + sums[b.row];
+    if (NM == 3 && p.rq && t < p.L) {
+      const size_t to = (size_t)seq * p.L + t;
+      if (b.half == 0) {
+        p.rq[to] = dot + sums[b.row];
+        p.cs[to] = pairs + inside[b.row];
+      }
+      if (b.half == b.quarter / 2) p.rc[to] = pairs_in;  // the half that has the diagonal
+    }
     if (more) {
       b.wait_mma(3, phase);
-      if (threadIdx.x == 0) {
+      if (threadIdx.x == kLeaderQ) {
         tma_store_wait_read_all();  // the fourth tile
         if (!DECAY) load_k(c + 1);
         load_vq(c + 1);
@@ -696,18 +732,19 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
       if (G) around = state.dot(G, b) * all;
     }
   }
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == kLeaderQ) {
     if (c < c1) tc::drain_wait(&b.full[0], (c - c0) & 1);
     tma_store_wait_all();
   }
   if (NM == 3 && p.rq) {
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) around += __shfl_xor_sync(0xffffffffu, around, off);
-    if (b.lane == 0) sums[CT + b.warp] = around;
+    __syncthreads();  // sums are read
+    if (b.lane == 0) sums[b.warp] = around;
     __syncthreads();
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == kLeaderQ) {
       float s = 0.f;
-      for (int i = 0; i < kThreads / 32; ++i) s += sums[CT + i];
+      for (int i = 0; i < kThreads / 32; ++i) s += sums[i];
       p.around[(size_t)seq * p.segments + seg] = s;
     }
   }
@@ -736,8 +773,7 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
   b.start(smem, SM::OFF_BAR, COLUMNS, err);
   float2 *lam = reinterpret_cast<float2 *>(smem + SM::OFF_LAM);
   float *fac = reinterpret_cast<float *>(smem + SM::OFF_FAC);
-  float *part = reinterpret_cast<float *>(smem + SM::OFF_LAM);  // [4][CT], once lam and fac are used
-  float *half_1 = part + 4 * CT;                                // [CT], behind it
+  float *sums = reinterpret_cast<float *>(smem + SM::OFF_MORE);  // [2][CT] half 1's sums
   const int seq = blockIdx.x / p.segments, seg = blockIdx.x % p.segments;
   const int c0 = seg * p.per, c1 = min(c0 + p.per, p.chunks), n = c1 - c0;
   const size_t es = (size_t)D * D;
@@ -759,7 +795,7 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
     prefetch_tile<D>(&maps.v, c * CT, seq);
     prefetch_tile<D>(&maps.dO, c * CT, seq);
   };
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == kLeaderKV) {
     load_q(c1 - 1);
     load_kv(c1 - 1);
     load_dO(c1 - 1);
@@ -787,7 +823,7 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
     fence_proxy_async_smem();
     tc_fence_before();
     if (__syncthreads_or(b.failed)) break;
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == kLeaderKV) {
       tc_fence_after();
       const Operand ak = along_row<SM::BOX>(b.base + TKP), av = along_row<SM::BOX>(b.base + TV);
       product<D>(b.tmem + T_P, ak, along_row<SM::BOX>(b.base + TQ), id_s, false);
@@ -806,10 +842,11 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
     b.wait_mma(0, phase);
     // the scores as operands: row i, tokens j >= i
     uint32_t wp[2][16], wd[2][16];
-    float row_sum = 0.f, col_sum[2] = {0.f, 0.f};
+    float pairs = 0.f, pairs_in = 0.f;  // with tokens of the blocks behind, of this block
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const int block = b.half * 2 + x;
+      const bool diagonal = block == b.quarter;
       if (block < b.quarter) {  // all in front of the warp's rows
 #pragma unroll
         for (int e = 0; e < 16; ++e) wp[x][e] = wd[x][e] = 0;
@@ -819,38 +856,27 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
       load_32(b, T_P + block * 32, f);
       load_32(b, T_DP + block * 32, g);
       if (DECAY) decay_factors<true>(b, block, lam, fac, own, d);
+      if (NM == 3 && DECAY) {
+        float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const float pair = f[e] * d[e] * g[e];
+          s[e % 4] += !diagonal || e > b.lane ? pair : 0.f;
+        }
+        (diagonal ? pairs_in : pairs) += (s[0] + s[1]) + (s[2] + s[3]);
+      }
 #pragma unroll
       for (int e = 0; e < 32; ++e) {
-        if (DECAY) f[e] *= d[e];
-        d[e] = DECAY ? d[e] * g[e] : g[e];
-        if (block == b.quarter) {
+        if (DECAY) f[e] *= d[e], g[e] *= d[e];
+        if (diagonal) {
           f[e] = e >= b.lane ? f[e] : 0.f;
-          d[e] = e >= b.lane ? d[e] : 0.f;
+          g[e] = e >= b.lane ? g[e] : 0.f;
         }
       }
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
         wp[x][e] = la::pack_bf16(f[2 * e], f[2 * e + 1]);
-        wd[x][e] = la::pack_bf16(d[2 * e], d[2 * e + 1]);
-      }
-      if (NM == 3) {  // the pairs i < j: their sums over the row and, over the warp's rows, the columns
-#pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          f[e] *= g[e];
-          if (block == b.quarter) f[e] = e > b.lane ? f[e] : 0.f;
-          row_sum += f[e];
-        }
-        // lane e ends with column e's
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) {
-          const bool up = b.lane & off;
-#pragma unroll
-          for (int e = 0; e < off; ++e) {
-            const float give = up ? f[e] : f[e + off];
-            f[e] = (up ? f[e + off] : f[e]) + __shfl_xor_sync(0xffffffffu, give, off);
-          }
-        }
-        col_sum[x] = f[0];
+        wd[x][e] = la::pack_bf16(g[2 * e], g[2 * e + 1]);
       }
     }
     tc_fence_before();
@@ -884,25 +910,33 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
         }
       }
     }
-    if (NM == 3 && b.half == 1) half_1[b.row] = dot;
+    if (NM == 3 && b.half == 1) sums[b.row] = dot, sums[CT + b.row] = pairs;
     tmem_st_wait();
     tc_fence_before();
     __syncthreads();
     const Operand q = along_col<SM::BOX>(b.base + TQ), dO = along_col<SM::BOX>(b.base + TD);
-    if (threadIdx.x == 0) {  // the scores' share, while the decayed Q is formed
+    if (threadIdx.x == kLeaderKV) {  // the scores' share, while the decayed Q is formed
       tc_fence_after();
       product_ta<CT>(b.tmem + T_V, b.tmem + T_AP, dO, id_out, true);
       product_ta<CT>(b.tmem + T_K, b.tmem + T_ADP, q, id_out, true);
       mma_commit(&b.mma[2]);
     }
-    if (NM == 3 && p.rk && b.half == 0 && t < p.L)
-      p.rk[(size_t)seq * p.L + t] = dot + half_1[b.row];
+    if (NM == 3 && p.rk && t < p.L) {
+      const size_t to = (size_t)seq * p.L + t;
+      if (b.half == 0) {
+        p.rk[to] = dot + sums[b.row];
+        p.rs[to] = pairs + sums[CT + b.row];
+      }
+      // A block's pairs enter rc as their later token's less as their earlier one's, and
+      // cancel in sums: both kernels form them from the same factors.
+      if (b.half == b.quarter / 2) p.rc[to] -= pairs_in;
+    }
     if (update && decays) {
       decayed_rows<D, NM, CT>(smem + TQ, smem, 0, [&](int i) { return ex2_approx(lam[i].x); });
       fence_proxy_async_smem();
     }
     if (decays) __syncthreads();
-    if (threadIdx.x == 0 && update) {  // the state's update, while dk and dv leave
+    if (threadIdx.x == kLeaderKV && update) {  // the state's update, while dk and dv leave
       tc_fence_after();
       if (decays) {
 #pragma unroll
@@ -914,13 +948,8 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
       }
       mma_commit(&b.mma[3]);
     }
-    if (NM == 3 && p.rc) {
-      part[b.quarter * CT + b.half * 64 + b.lane] = col_sum[0];
-      part[b.quarter * CT + b.half * 64 + 32 + b.lane] = col_sum[1];
-      if (b.half == 1) half_1[b.row] = row_sum;
-    }
     b.wait_mma(2, phase);
-    if (threadIdx.x == 0 && more && DECAY) load_q(c - 1);
+    if (threadIdx.x == kLeaderKV && more && DECAY) load_q(c - 1);
     __syncwarp();
 #pragma unroll
     for (int x = 0; x < N; x += 32) {
@@ -936,23 +965,14 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
     fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == kLeaderKV) {
       store_tile_tma<D>(b, TV, &maps.dv, t0, seq);
       store_tile_tma<D>(b, TK, &maps.dk, t0, seq);
       tma_store_commit();
     }
-    if (NM == 3 && p.rc) {
-      if (b.half == 0 && t < p.L) {
-        float col = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) col += part[i * CT + b.row];
-        p.rc[(size_t)seq * p.L + t] = col - (row_sum + half_1[b.row]);
-      }
-      __syncthreads();  // part gives way to the next chunk's decays
-    }
     if (update) {
       b.wait_mma(3, phase);
-      if (threadIdx.x == 0 && more) {
+      if (threadIdx.x == kLeaderKV && more) {
         if (!DECAY) load_q(c - 1);
         load_dO(c - 1);
         tma_store_wait_read_all();
@@ -965,10 +985,10 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
   }
   if (done == n) {
     if (p.dS0 && seg == 0) state.store(p.dS0 + (size_t)seq * es, b);
-  } else if (threadIdx.x == 0) {
+  } else if (threadIdx.x == kLeaderKV) {
     tc::drain_wait(&b.full[0], done & 1);
   }
-  if (threadIdx.x == 0) tma_store_wait_all();
+  if (threadIdx.x == kLeaderKV) tma_store_wait_all();
   b.finish(COLUMNS);
 }
 
