@@ -464,8 +464,8 @@ la_status la_rotary_frequencies(int rotary_dim, double base, int scaling, double
  * and the values behind them are copied.  Pair p is (2p, 2p+1) if `interleaved`,
  * else (p, p + rotary_dim / 2).  la_rotary_bwd turns by -a: it takes the
  * gradients of q_out and k_out to those of q and k.  The angle is exact however
- * far the position lies (to position * 2^-64 turns); sine and cosine are
- * fp32.
+ * far the position lies (to position * 2^-64 turns, for frequencies up to 1);
+ * sine and cosine are fp32.
  *
  *   q, q_out   dtype, element (b,h,t,i) at b*b_stride + h*h_stride +
  *              t*t_stride + i (strides >= 0): a slice of a projection's
