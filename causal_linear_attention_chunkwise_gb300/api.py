@@ -603,7 +603,7 @@ def _int32(t, shape, what):
 
 def _heads(t, shape, dtype, what):
     """Address and strides of ``t`` = [B,H,L,d] whose last axis is contiguous."""
-    if t.shape != shape or t.dtype != dtype:
+    if t.dtype != dtype or t.shape != shape:
         raise ValueError(f"{what} must be {dtype} {list(shape)}")
     b, h, n, one = t.stride()
     if one != 1 and shape[3] > 1 and t.numel() > 0:
@@ -614,36 +614,40 @@ def _heads(t, shape, dtype, what):
 _NO_HEADS = (None, 0, 0, 0)
 
 
-def _rotary(fn, q, k, inv_freq, positions, offsets, lengths, interleaved, scale, q_out, k_out,
+def _rotary(call, q, k, inv_freq, positions, offsets, lengths, interleaved, scale, q_out, k_out,
             stream):
     shape, dtype = q.shape, q.dtype
     B, H, L, d = shape
-    k_shape = None if k is None else k.shape
-    if k is not None and (len(k_shape) != 4 or k_shape[0] != B or k_shape[2:] != shape[2:]):
-        raise ValueError("q and k must agree in [B,.,L,d]")
-    Hk = 0 if k is None else k_shape[1]
+    Hk, ka, k_shape = 0, _NO_HEADS, None
+    qa = _heads(q, shape, dtype, "q")
+    if k is not None:
+        k_shape = k.shape
+        if len(k_shape) != 4 or k_shape[0] != B or k_shape[2] != L or k_shape[3] != d:
+            raise ValueError("q and k must agree in [B,.,L,d]")
+        Hk = k_shape[1]
+        ka = _heads(k, k_shape, dtype, "k")
+    elif k_out is not None:
+        raise ValueError("k_out without k")
     if max(B, H, Hk, L, d) > _INT_MAX:
         raise _too_large(B, H, Hk, L, d)
-    qa = _heads(q, shape, dtype, "q")
-    ka = _NO_HEADS if k is None else _heads(k, k_shape, dtype, "k")
     pairs = inv_freq.numel()
     f = _param(inv_freq, (pairs,), "inv_freq")
     ps = None if positions is None else _int32(positions, (B, L), "positions")
     of = None if offsets is None else _int32(offsets, (B,), "offsets")
     n = None if lengths is None else _int32(lengths, (B,), "lengths")
-    if k is None and k_out is not None:
-        raise ValueError("k_out without k")
     dev = _device_of(q, k, inv_freq, positions, offsets, lengths, q_out, k_out)
-    zero = lengths is not None
     if q_out is None:
-        q_out = _new(shape, dtype, q.device, stream, zero)
-    if k is not None and k_out is None:
-        k_out = _new(k_shape, dtype, q.device, stream, zero)
-    status = getattr(_native.load(), fn)(
-        *qa, H, *ka, Hk, DTYPE[dtype], B, L, d, 2 * pairs, interleaved, f, scale, ps, of, n,
-        *_heads(q_out, shape, dtype, "q_out"),
-        *(_NO_HEADS if k is None else _heads(k_out, k_shape, dtype, "k_out")),
-        _current_stream(dev) if stream is None else stream.cuda_stream)
+        q_out = _new(shape, dtype, q.device, stream, lengths is not None)
+    qo = _heads(q_out, shape, dtype, "q_out")
+    ko = _NO_HEADS
+    if k is not None:
+        if k_out is None:
+            k_out = _new(k_shape, dtype, q.device, stream, lengths is not None)
+        ko = _heads(k_out, k_shape, dtype, "k_out")
+    status = call(
+        qa[0], qa[1], qa[2], qa[3], H, ka[0], ka[1], ka[2], ka[3], Hk, DTYPE[dtype], B, L, d,
+        2 * pairs, interleaved, f, scale, ps, of, n, qo[0], qo[1], qo[2], qo[3], ko[0], ko[1],
+        ko[2], ko[3], _current_stream(dev) if stream is None else stream.cuda_stream)
     if status:
         _check(status)
     return q_out, k_out
@@ -662,7 +666,7 @@ def la_rotary_fwd(q, k, inv_freq, positions=None, offsets=None, lengths=None, in
     b has position ``offsets[b] + t``, or ``offsets[b] + positions[b,t]`` (int32 [B] and
     [B,L]).  ``lengths`` int32 [B]: the tokens behind them are left as they are in the
     outputs (zero where these are made here).  ``q_out`` may be ``q``, ``k_out`` ``k``."""
-    return _rotary("la_rotary_fwd", q, k, inv_freq, positions, offsets, lengths, interleaved,
+    return _rotary(_native.load().la_rotary_fwd, q, k, inv_freq, positions, offsets, lengths, interleaved,
                    scale, q_out, k_out, stream)
 
 
@@ -671,7 +675,7 @@ def la_rotary_bwd(dq, dk, inv_freq, positions=None, offsets=None, lengths=None,
     """Backward pass of ``la_rotary_fwd``: the gradients of its outputs to those of
     its inputs, of the same arguments.  ``q_out`` and ``k_out`` may be views of a
     projection's gradient.  Returns ``(q_out, k_out)``."""
-    return _rotary("la_rotary_bwd", dq, dk, inv_freq, positions, offsets, lengths, interleaved,
+    return _rotary(_native.load().la_rotary_bwd, dq, dk, inv_freq, positions, offsets, lengths, interleaved,
                    scale, q_out, k_out, stream)
 
 
@@ -832,7 +836,6 @@ def la_residual_norm_bwd(dy, r, weight=None, dr=None, x=None, post_weight=None, 
         raise _too_large(D)
     rd = r.dtype
     per = (D,)
-    params = want_param_grads
     w = None if weight is None else _param(weight, per, "weight")
     pw = None if post_weight is None else _param(post_weight, per, "post_weight")
     sc = None if scale is None else _param(scale, per, "scale")
@@ -840,12 +843,15 @@ def la_residual_norm_bwd(dy, r, weight=None, dr=None, x=None, post_weight=None, 
     drp = None if dr is None else _same(dr, shape, rd)
     xp = None if x is None else _same(x, shape, dtype)
     dev = _device_of(dy, r, dr, x, weight, post_weight, scale, dx, dresidual, workspace)
-    dx = _new(shape, dtype, dy.device, stream) if dx is None else dx
+    own = stream is None or stream.cuda_stream == _current_stream(dev)
+    if dx is None:
+        dx = torch.empty_like(dy) if own else _new(shape, dtype, dy.device, stream)
     if dresidual is None and want_dresidual:
-        dresidual = _new(shape, rd, dy.device, stream)
+        dresidual = torch.empty_like(r) if own else _new(shape, rd, dy.device, stream)
+    params = want_param_grads
     grads = [_new(per, torch.float32, dy.device, stream) if wanted else None
-             for wanted in (params and weight is not None, want_dbias,
-                            params and post_weight is not None, params and scale is not None)]
+             for wanted in (params and w is not None, want_dbias, params and pw is not None,
+                            params and sc is not None)]
     rows = dy.numel() // D if D else 0
     lib = _native.load()
     ws = ws_bytes = 0
@@ -857,7 +863,7 @@ def la_residual_norm_bwd(dy, r, weight=None, dr=None, x=None, post_weight=None, 
     status = lib.la_residual_norm_bwd(
         yp, DTYPE[dtype], rp, drp, DTYPE[rd], xp, rows, D, pw, sc, alpha, w, NORM[norm], eps,
         _same(dx, shape, dtype), None if dresidual is None else _same(dresidual, shape, rd),
-        *map(_ptr, grads), ws, ws_bytes,
+        *[None if g is None else g.data_ptr() for g in grads], ws, ws_bytes,
         _current_stream(dev) if stream is None else stream.cuda_stream)
     if status:
         _check(status)

@@ -21,14 +21,42 @@ namespace la {
 
 constexpr int kNormTeamThreads = 256;  // threads per block of teams inside a warp
 
+// Sums of K values over groups of W neighbouring lanes, in every lane: the values are halved
+// among the lanes first, so that K sums take little more shuffles than one.
+template <int K, int W> __device__ __forceinline__ void lane_sums(float (&v)[K]) {
+  const int lane = threadIdx.x % 32;
+  constexpr unsigned all = 0xffffffffu;
+  if constexpr (K == 1 || W < 4) {
+#pragma unroll
+    for (int off = W / 2; off > 0; off >>= 1)
+#pragma unroll
+      for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(all, v[k], off);
+  } else if constexpr (K == 2) {
+    const bool up = lane & (W / 2);
+    float s = (up ? v[1] : v[0]) + __shfl_xor_sync(all, up ? v[0] : v[1], W / 2);
+#pragma unroll
+    for (int off = W / 4; off > 0; off >>= 1) s += __shfl_xor_sync(all, s, off);
+    v[0] = __shfl_sync(all, s, 0, W);
+    v[1] = __shfl_sync(all, s, W / 2, W);
+  } else {
+    static_assert(K == 3 || K == 4, "up to four sums");
+    const bool up = lane & (W / 2), odd = lane & (W / 4);
+    const float v3 = K == 4 ? v[K - 1] : 0.f;
+    const float a = (up ? v[2] : v[0]) + __shfl_xor_sync(all, up ? v[0] : v[2], W / 2);
+    const float b = (up ? v3 : v[1]) + __shfl_xor_sync(all, up ? v[1] : v3, W / 2);
+    float s = (odd ? b : a) + __shfl_xor_sync(all, odd ? a : b, W / 4);
+#pragma unroll
+    for (int off = W / 8; off > 0; off >>= 1) s += __shfl_xor_sync(all, s, off);
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] = __shfl_sync(all, s, k * (W / 4), W);
+  }
+}
+
 // Sums of K values over the team: LANES neighbouring lanes, or the block (LANES =
 // 0).  `red` holds two sets, used in turn, so that one barrier is enough.
 template <int LANES, int K>
 __device__ __forceinline__ void team_sums(float (&v)[K], float (*red)[4][32], int &turn) {
-#pragma unroll
-  for (int off = (LANES ? LANES : 32) / 2; off > 0; off >>= 1)
-#pragma unroll
-    for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], off);
+  lane_sums<K, LANES ? LANES : 32>(v);
   if constexpr (LANES == 0) {
     static_assert(K <= 4, "red holds four sums");
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, warps = blockDim.x / 32;
@@ -39,13 +67,31 @@ __device__ __forceinline__ void team_sums(float (&v)[K], float (*red)[4][32], in
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < K; ++k) v[k] = lane < warps ? red[turn][k][lane] : 0.f;
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1)
-#pragma unroll
-      for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], off);
+    lane_sums<K, 32>(v);
     turn ^= 1;
   }
 }
+
+// V values as cells: pairs of fp32 in a register pair each, one instruction for both (V = 1:
+// single values).
+template <int V> struct Cells {
+  using C = typename CellOf<V>::type;
+  static constexpr int H = V > 1 ? V / 2 : 1;
+  __device__ static __forceinline__ void pack(const float *f, C *c) {
+#pragma unroll
+    for (int i = 0; i < H; ++i) {
+      if constexpr (V == 1) c[i] = f[i];
+      else c[i] = pack2(f[2 * i], f[2 * i + 1]);
+    }
+  }
+  __device__ static __forceinline__ void unpack(const C *c, float *f) {
+#pragma unroll
+    for (int i = 0; i < H; ++i) {
+      if constexpr (V == 1) f[i] = c[i];
+      else unpack2(c[i], f[2 * i], f[2 * i + 1]);
+    }
+  }
+};
 
 // V fp32 parameters at p + c, `other` where there are none or the place is past d.
 template <int V>
@@ -111,10 +157,11 @@ struct WeightSums {
 };
 cudaError_t launch_weight_sums(const WeightSums &w, int count, cudaStream_t stream);
 
-// Blocks (for each of `heads`) for rows that would fill `wanted` blocks of `threads`
-// threads: 512 threads to an SM, at most four blocks.
-inline unsigned norm_bwd_blocks(long long wanted, int threads, int heads) {
-  const int per_sm = threads <= 128 ? 4 : threads <= 256 ? 2 : 1;
+// Blocks (for each of `heads`) for rows that would fill `wanted` blocks: `per_sm` to an SM, one to
+// kNormMostBlocks.
+constexpr int kNormMostBlocks = 4;
+inline unsigned norm_bwd_blocks(long long wanted, int per_sm, int heads) {
+  per_sm = per_sm < 1 ? 1 : per_sm > kNormMostBlocks ? kNormMostBlocks : per_sm;
   const long long fill = (152ll * per_sm + heads - 1) / heads;
   return (unsigned)(wanted < fill ? wanted : fill);
 }

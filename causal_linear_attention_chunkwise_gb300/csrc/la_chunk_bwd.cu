@@ -41,14 +41,14 @@ Plan make_plan(const ChunkBwdArgs &a, bool f32_out) {
   const long long slots = 152ll * (p.wide || p.tc ? 1 : p.planes && !p.full ? 2 : 3);
   double best = 0;
   p.per = 0;
-  for (int n = (p.chunks + kMaxPer - 1) / kMaxPer; n <= p.chunks; ++n) {
-    const int per = (p.chunks + n - 1) / n;
-    if ((p.chunks + per - 1) / per != n) continue;
+  for (int per = std::min(p.chunks, kMaxPer); per > 0;) {
+    const int n = (p.chunks + per - 1) / per;
     const long long waves = (seqs * n + slots - 1) / slots;
     const long long share_waves = (2 * seqs * (n - 1) + 2 * slots - 1) / (2 * slots);
     const double cost = (double)waves * (per + 1) + (n > 1 ? 0.4 * share_waves * per + 4 : 0);
     if (p.per == 0 || cost < best) best = cost, p.per = per, p.segments = n;
-    if (waves > 4 && n > 1) break;  // finer cuts only add to the work
+    if ((waves > 4 && n > 1) || per == 1) break;  // finer cuts only add to the work
+    per = std::min(per - 1, (p.chunks + n) / (n + 1));  // the longest segments of a finer cut
   }
   return p;
 }
@@ -150,14 +150,26 @@ __global__ void __launch_bounds__(256) segment_scan_kernel(const ChunkBwd p, int
   float4 cur = first ? first[(size_t)seq * vecs + vec] : make_float4(0.f, 0.f, 0.f, 0.f);
   float4 *share = reinterpret_cast<float4 *>(back ? p.W : p.U) + (size_t)seq * n * vecs + vec;
   const float *total = p.total + (size_t)seq * p.segments;
-#pragma unroll 4
-  for (int i = 0; i < n; ++i) {
-    const int s = back ? n - 1 - i : i;
-    const float f = ex2_approx(total[back ? s + 1 : s]);
-    const float4 x = share[(size_t)s * vecs];
-    cur.x = fmaf(f, cur.x, x.x), cur.y = fmaf(f, cur.y, x.y);
-    cur.z = fmaf(f, cur.z, x.z), cur.w = fmaf(f, cur.w, x.w);
-    share[(size_t)s * vecs] = cur;
+  // Eight segments' loads in flight: the stores behind them may be to the same places.
+  for (int i = 0; i < n; i += 8) {
+    float4 x[8];
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int s = back ? n - 1 - i - j : i + j;
+      if (i + j >= n) continue;
+      x[j] = share[(size_t)s * vecs];
+      f[j] = total[back ? s + 1 : s];
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int s = back ? n - 1 - i - j : i + j;
+      if (i + j >= n) continue;
+      const float g = ex2_approx(f[j]);
+      cur.x = fmaf(g, cur.x, x[j].x), cur.y = fmaf(g, cur.y, x[j].y);
+      cur.z = fmaf(g, cur.z, x[j].z), cur.w = fmaf(g, cur.w, x[j].w);
+      share[(size_t)s * vecs] = cur;
+    }
   }
 }
 

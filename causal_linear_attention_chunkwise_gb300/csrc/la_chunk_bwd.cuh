@@ -42,6 +42,7 @@
 #include "la_act.cuh"
 #include "la_internal.h"
 #include "la_mma.cuh"
+#include "la_tc_sync.cuh"
 
 namespace la {
 
@@ -722,25 +723,22 @@ cudaError_t launch_segment_scan(const ChunkBwd &p, int seqs, cudaStream_t stream
 
 // The launches of one configuration.
 template <typename F> cudaError_t run_chunk_bwd(const ChunkBwd &p, int seqs, cudaStream_t stream) {
+  static int set_share[64], set_q[64], set_kv[64];
   cudaError_t e;
   if (p.segments > 1) {
-    e = cudaFuncSetAttribute(segment_share_kernel<F>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             share_smem<F>());
-    if (e != cudaSuccess) return e;
-    segment_share_kernel<F><<<dim3((unsigned)(seqs * (p.segments - 1)), 2), F::THREADS,
-                              share_smem<F>(), stream>>>(p);
+    auto share = segment_share_kernel<F>;
+    if ((e = tc::set_smem_once(share, share_smem<F>(), set_share)) != cudaSuccess) return e;
+    share<<<dim3((unsigned)(seqs * (p.segments - 1)), 2), F::THREADS, share_smem<F>(), stream>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if ((e = launch_segment_scan(p, seqs, stream)) != cudaSuccess) return e;
   }
-  e = cudaFuncSetAttribute(grad_q_kernel<F>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           grad_q_smem<F>());
-  if (e != cudaSuccess) return e;
-  grad_q_kernel<F><<<seqs * p.segments, F::THREADS, grad_q_smem<F>(), stream>>>(p);
+  auto gq = grad_q_kernel<F>;
+  auto gkv = grad_kv_kernel<F>;
+  if ((e = tc::set_smem_once(gq, grad_q_smem<F>(), set_q)) != cudaSuccess) return e;
+  if ((e = tc::set_smem_once(gkv, grad_kv_smem<F>(), set_kv)) != cudaSuccess) return e;
+  gq<<<seqs * p.segments, F::THREADS, grad_q_smem<F>(), stream>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(grad_kv_kernel<F>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           grad_kv_smem<F>());
-  if (e != cudaSuccess) return e;
-  grad_kv_kernel<F><<<seqs * p.segments, F::THREADS, grad_kv_smem<F>(), stream>>>(p);
+  gkv<<<seqs * p.segments, F::THREADS, grad_kv_smem<F>(), stream>>>(p);
   return cudaGetLastError();
 }
 

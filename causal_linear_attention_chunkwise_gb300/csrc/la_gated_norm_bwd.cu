@@ -28,38 +28,54 @@ __device__ __forceinline__ void act_and_slope(int act, float z, float &a, float 
 
 // Weights shared by the heads: the rows are those of all heads, in the order of
 // the tokens.  Weights of each head: a block stays with head blockIdx.y.
-template <typename T, int V, int LANES, int I, int MAXT>
-__global__ void __launch_bounds__(MAXT, LANES ? 2 : 1)
+// BIAS: there is a bias, or a gradient of one.
+template <typename T, int V, int LANES, int I, bool BIAS, int MAXT>
+__global__ void __launch_bounds__(MAXT, LANES ? (I == 1 ? 3 : 2) : 1)
 gated_norm_bwd_kernel(const GatedNormBwdArgs a, long long rows, float *part) {
-  constexpr int N = V * I;
+  using P = Cells<V>;
+  using C = typename P::C;
+  constexpr int H = P::H, N = H * I;
   __shared__ float red[2][4][32];
-  __shared__ float sum[LANES ? kNormTeamThreads / 32 * LANES * N : 1];
+  __shared__ float sum[LANES ? kNormTeamThreads / 32 * LANES * V * I : 1];
   const int size = LANES ? LANES : blockDim.x;
   const int lane = LANES ? threadIdx.x % LANES : threadIdx.x;
   const int teams = LANES ? kNormTeamThreads / size : 1;
   const long long step = (long long)gridDim.x * teams;
   long long r = (long long)blockIdx.x * teams + (LANES ? threadIdx.x / size : 0);
-  const int d = a.d, own_head = a.weight_heads > 1 ? blockIdx.y : -1;
+  const int d = a.d, own_head = a.weight_heads > 1 ? (int)blockIdx.y : -1;
   const float inv = 1.f / d;
   const bool gate = a.gate != nullptr, gate_first = gate && a.gate_first;
   const bool layer = a.norm == LA_NORM_LAYER;
+  auto both = [](float v) { return CellOf<V>::both(v); };
+  auto total = [](C c) { return CellOf<V>::sum(c); };
   int turn = 0;
   Raw<T, V> x[I], z[I], dy[I];
+  // Row r's head and token, carried along: a step adds (db, dt, dh), without divisions.
   struct Place {
-    long long bt, x, dx;
-    int h;
+    long long b, bt;
+    int t, h;
   };
-  auto place = [&](long long row) {
+  auto split = [&](long long row) {
     Place p;
     p.bt = own_head >= 0 ? row : div_index(row, a.H);
     p.h = own_head >= 0 ? own_head : (int)(row - p.bt * a.H);
-    const long long b = div_index(p.bt, a.L), t = p.bt - b * a.L;
-    p.x = b * a.x_bs + p.h * a.x_hs + t * a.x_ts;
-    p.dx = b * a.dx_bs + p.h * a.dx_hs + t * a.dx_ts;
+    p.b = div_index(p.bt, a.L);
+    p.t = (int)(p.bt - p.b * a.L);
+    return p;
+  };
+  const Place stride = [&] {
+    Place p = split(step);
+    if (own_head >= 0) p.h = 0;
+    return p;
+  }();
+  auto advance = [&](Place p) {
+    p.h += stride.h, p.bt += stride.bt, p.t += stride.t, p.b += stride.b;
+    if (own_head < 0 && p.h >= a.H) p.h -= a.H, ++p.bt, ++p.t;
+    if (p.t >= a.L) p.t -= a.L, ++p.b;
     return p;
   };
   auto fetch = [&](const Place &p) {
-    const T *xr = static_cast<const T *>(a.x) + p.x;
+    const T *xr = static_cast<const T *>(a.x) + p.b * a.x_bs + p.h * a.x_hs + p.t * a.x_ts;
     const T *zr = static_cast<const T *>(a.gate) + p.bt * a.gate_stride + (long long)p.h * d;
     const T *yr = static_cast<const T *>(a.dy) + p.bt * a.dy_stride + (long long)p.h * d;
 #pragma unroll
@@ -73,103 +89,140 @@ gated_norm_bwd_kernel(const GatedNormBwdArgs a, long long rows, float *part) {
   };
 #pragma unroll
   for (int i = 0; i < I; ++i) x[i] = z[i] = dy[i] = Raw<T, V>{};
-  float w[N], bias[N], dw[N], db[N];
+  C w[N], bias[BIAS ? N : 1], dw[N], db[BIAS ? N : 1];
   const long long w0 = own_head >= 0 ? (long long)own_head * d : 0;
 #pragma unroll
   for (int i = 0; i < I; ++i) {
     const int c = (lane + i * size) * V;
-    params_or<V>(a.weight ? a.weight + w0 : nullptr, c, d, 1.f, w + i * V);
-    params_or<V>(a.bias ? a.bias + w0 : nullptr, c, d, 0.f, bias + i * V);
+    float f[V];
+    params_or<V>(a.weight ? a.weight + w0 : nullptr, c, d, 1.f, f);
+    P::pack(f, w + i * H);
+    if constexpr (BIAS) {
+      params_or<V>(a.bias ? a.bias + w0 : nullptr, c, d, 0.f, f);
+      P::pack(f, bias + i * H);
+    }
   }
 #pragma unroll
-  for (int j = 0; j < N; ++j) dw[j] = db[j] = 0.f;
-  Place next{};
-  if (r < rows) next = place(r), fetch(next);
+  for (int j = 0; j < N; ++j) {
+    dw[j] = C(0);
+    if constexpr (BIAS) db[j] = C(0);
+  }
+  Place at = split(r < rows ? r : 0);
+  if (r < rows) fetch(at);
   // A team out of rows stays while another of its warp has one: the sums need
   // the whole warp.
   for (long long first = r - (LANES ? threadIdx.x % 32 / size : 0); first < rows;
        first += step, r += step) {
     const bool live = r < rows;
-    const Place at = next;
-    float v[N], act[N], slope[N], g[N];
+    T *dxr = static_cast<T *>(a.dx) + at.b * a.dx_bs + at.h * a.dx_hs + at.t * a.dx_ts;
+    T *dzr = static_cast<T *>(a.dgate) + at.bt * a.dgate_stride + (long long)at.h * d;
+    C v[N], act[N], g[N];
+    C keep[N];  // what dgate has beside n: act's slope, times x where the gate comes first, else dy
 #pragma unroll
     for (int i = 0; i < I; ++i) {
-      x[i].unpack(v + i * V);
-      z[i].unpack(act + i * V);
-      dy[i].unpack(g + i * V);
-    }
-    if (r + step < rows) next = place(r + step), fetch(next);
-    if (!live) {
+      float f[V], s[V];
+      x[i].unpack(f);
+      P::pack(f, v + i * H);
+      dy[i].unpack(f);
+      P::pack(f, g + i * H);
+      z[i].unpack(f);
 #pragma unroll
-      for (int j = 0; j < N; ++j) v[j] = act[j] = g[j] = 0.f;
+      for (int e = 0; e < V; ++e) {
+        if (gate) act_and_slope(a.act, f[e], f[e], s[e]);
+        else f[e] = 1.f, s[e] = 0.f;
+      }
+      P::pack(f, act + i * H);
+      P::pack(s, keep + i * H);
     }
-    float keep[N];  // the factor of act's slope: x where the gate comes first, else dy
+    if (r + step < rows) {
+      at = advance(at);
+      fetch(at);
+    }
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      if (gate) {
-        act_and_slope(a.act, act[j], act[j], slope[j]);
-      } else {
-        act[j] = 1.f, slope[j] = 0.f;
-      }
-      keep[j] = gate_first ? v[j] : g[j];
-      if (gate_first) v[j] *= act[j];
-      else g[j] *= act[j];  // the gradient of n w + b
+      keep[j] = mul2(keep[j], gate_first ? v[j] : g[j]);
+      if (gate_first) v[j] = mul2(v[j], act[j]);
+      else g[j] = mul2(g[j], act[j]);  // the gradient of n w + b
     }
-    float mean_g = 0.f;
-    float s[3] = {0.f, 0.f, 0.f};
     if (layer) {
-      float m[1] = {0.f};
+      C m0 = C(0);
 #pragma unroll
-      for (int j = 0; j < N; ++j) m[0] += v[j];
+      for (int j = 0; j < N; ++j) m0 = add2(m0, v[j]);
+      float m[1] = {total(m0)};
       team_sums<LANES>(m, red, turn);
+      const C off = both(-m[0] * inv);
 #pragma unroll
       for (int i = 0; i < I; ++i)
 #pragma unroll
-        for (int e = 0; e < V; ++e)
-          v[i * V + e] = (lane + i * size) * V < d ? v[i * V + e] - m[0] * inv : 0.f;
+        for (int k = 0; k < H; ++k)
+          v[i * H + k] = (lane + i * size) * V < d ? add2(v[i * H + k], off) : C(0);
     }
+    C q0 = C(0), q1 = C(0), q2 = C(0);
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      const float gw = g[j] * w[j];
-      s[0] = fmaf(v[j], v[j], s[0]);
-      s[1] = fmaf(gw, v[j], s[1]);
-      s[2] += gw;
+      const C gw = mul2(g[j], w[j]);
+      q0 = fma2(v[j], v[j], q0);
+      q1 = fma2(gw, v[j], q1);
+      if (layer) q2 = add2(q2, gw);
     }
-    team_sums<LANES>(s, red, turn);
+    float s[2] = {total(q0), total(q1)}, mean = 0.f;
+    if (layer) {
+      float s3[3] = {s[0], s[1], total(q2)};
+      team_sums<LANES>(s3, red, turn);
+      s[0] = s3[0], s[1] = s3[1], mean = s3[2] * inv;
+    } else {
+      team_sums<LANES>(s, red, turn);
+    }
     const float rs = rsqrtf(fmaf(s[0], inv, a.eps));
-    if (layer) mean_g = s[2] * inv;
-    const float along = s[1] * inv * rs * rs;  // mean(g n) r, for n = v r
-    T *dxr = static_cast<T *>(a.dx) + at.dx;
-    T *dzr = static_cast<T *>(a.dgate) + at.bt * a.dgate_stride + (long long)at.h * d;
+    const C rho = both(rs), against = both(-s[1] * inv * rs * rs), mean_g = both(-mean);
 #pragma unroll
     for (int i = 0; i < I; ++i) {
       const int c = (lane + i * size) * V;
-      float ox[V], oz[V];
+      C ox[H], oz[H];
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const int j = i * V + e;
-        const float n = v[j] * rs;
-        const float u = rs * (fmaf(g[j], w[j], -mean_g) - along * v[j]);
+      for (int k = 0; k < H; ++k) {
+        const int j = i * H + k;
+        const C n = mul2(v[j], rho);
+        C u = fma2(g[j], w[j], mul2(against, v[j]));
+        if (layer) u = add2(u, mean_g);
+        u = mul2(rho, u);
         if (live) {
-          dw[j] = fmaf(g[j], n, dw[j]);
-          db[j] += g[j];
+          dw[j] = fma2(g[j], n, dw[j]);
+          if constexpr (BIAS) db[j] = add2(db[j], g[j]);
         }
-        ox[e] = gate_first ? u * act[j] : u;
-        oz[e] = (gate_first ? u : fmaf(n, w[j], bias[j])) * keep[j] * slope[j];
+        ox[k] = gate_first ? mul2(u, act[j]) : u;
+        C y;
+        if constexpr (BIAS) y = fma2(n, w[j], bias[j]);
+        else y = mul2(n, w[j]);
+        oz[k] = mul2(gate_first ? u : y, keep[j]);
       }
       if (!live || c >= d) continue;
-      store_vec<T, V>(dxr + c, ox);
-      if (gate) store_vec<T, V>(dzr + c, oz);
+      float f[V];
+      P::unpack(ox, f);
+      store_vec<T, V>(dxr + c, f);
+      if (gate) {
+        P::unpack(oz, f);
+        store_vec<T, V>(dzr + c, f);
+      }
     }
   }
   if (!part) return;
   const long long width = (long long)a.weight_heads * d;
   float *mine = part + (long long)blockIdx.x * width + w0;
+  float f[V * I];
   if (a.dweight) {
-    block_share<V, LANES, I>(dw, mine, d, sum);
+#pragma unroll
+    for (int i = 0; i < I; ++i) P::unpack(dw + i * H, f + i * V);
+    block_share<V, LANES, I>(f, mine, d, sum);
     mine += (long long)gridDim.x * width;
   }
-  if (a.dbias) block_share<V, LANES, I>(db, mine, d, sum);
+  if constexpr (BIAS) {
+    if (a.dbias) {
+#pragma unroll
+      for (int i = 0; i < I; ++i) P::unpack(db + i * H, f + i * V);
+      block_share<V, LANES, I>(f, mine, d, sum);
+    }
+  }
 }
 
 template <typename T, int V>
@@ -183,10 +236,14 @@ cudaError_t launch_v(const GatedNormBwdArgs &a) {
     constexpr int MAXT = decltype(most)::value;
     const int heads = per_head ? a.H : 1, teams = LANES ? kNormTeamThreads / LANES : 1;
     const int block = LANES ? kNormTeamThreads : threads;
-    const unsigned blocks = norm_bwd_blocks((rows + teams - 1) / teams, block, heads);
+    const unsigned blocks = norm_bwd_blocks((rows + teams - 1) / teams, LANES && I == 1 ? 3 : 512 / block, heads);
     float *part = sums ? static_cast<float *>(a.workspace) : nullptr;
-    gated_norm_bwd_kernel<T, V, LANES, I, MAXT>
-        <<<dim3(blocks, heads), block, 0, a.stream>>>(a, rows, part);
+    if (a.bias || a.dbias)
+      gated_norm_bwd_kernel<T, V, LANES, I, true, MAXT>
+          <<<dim3(blocks, heads), block, 0, a.stream>>>(a, rows, part);
+    else
+      gated_norm_bwd_kernel<T, V, LANES, I, false, MAXT>
+          <<<dim3(blocks, heads), block, 0, a.stream>>>(a, rows, part);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !sums) return e;
     WeightSums w{part, (int)blocks, width, {}};
@@ -216,7 +273,7 @@ cudaError_t launch_t(const GatedNormBwdArgs &a) {
 size_t gated_norm_bwd_workspace_bytes(int B, int H, int L, int d, int weight_heads) {
   const long long rows = (long long)B * L * (weight_heads > 1 ? 1 : H);
   const int heads = weight_heads > 1 ? H : 1;
-  return 2 * sizeof(float) * norm_bwd_blocks(rows, 1, heads) * (size_t)weight_heads * d;
+  return 2 * sizeof(float) * norm_bwd_blocks(rows, kNormMostBlocks, heads) * (size_t)weight_heads * d;
 }
 
 cudaError_t launch_gated_norm_bwd(const GatedNormBwdArgs &a) {

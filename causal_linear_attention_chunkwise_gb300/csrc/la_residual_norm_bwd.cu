@@ -10,7 +10,8 @@
 //     dx = rho_x (g - mean(g) - n_x mean(g n_x)),  g = alpha s p e   (no p: g)
 //
 // in one pass over dy, r, dr and x.  The means of x, r and g belong to layer norm
-// alone.  r is read as the forward pass stored it.
+// alone.  r is read as the forward pass stored it.  ds and dp are alpha p and alpha s times
+// one sum over rows, of e n_x (x itself without a post norm).
 #include <cstdint>
 
 #include "la_block_norm_bwd.cuh"
@@ -22,9 +23,12 @@ namespace {
 template <typename T, typename R, int V, int LANES, int I, bool X, int MAXT>
 __global__ void __launch_bounds__(MAXT, LANES ? 2 : 1)
 residual_norm_bwd_kernel(const ResidualNormBwdArgs a, float *part) {
-  constexpr int N = V * I, RV = V < Pack16<R>::N ? V : Pack16<R>::N, RN = V / RV;
+  constexpr int RV = V < Pack16<R>::N ? V : Pack16<R>::N, RN = V / RV;
+  using P = Cells<V>;
+  using C = typename P::C;
+  constexpr int H = P::H, N = H * I;
   __shared__ float red[2][4][32];
-  __shared__ float sum[LANES ? kNormTeamThreads / 32 * LANES * N : 1];
+  __shared__ float sum[LANES ? kNormTeamThreads / 32 * LANES * V * I : 1];
   const int size = LANES ? LANES : blockDim.x;
   const int lane = LANES ? threadIdx.x % LANES : threadIdx.x;
   const int teams = LANES ? kNormTeamThreads / size : 1;
@@ -33,6 +37,9 @@ residual_norm_bwd_kernel(const ResidualNormBwdArgs a, float *part) {
   const int D = a.D;
   const float inv = 1.f / D;
   const bool layer = a.norm == LA_NORM_LAYER, post = X && a.post_weight;
+  const bool bias_grad = a.dbias != nullptr;
+  auto both = [](float v) { return CellOf<V>::both(v); };
+  auto total = [](C c) { return CellOf<V>::sum(c); };
   int turn = 0;
   Raw<T, V> dy[I], x[I];
   Raw<R, RV> r[I][RN], dr[I][RN];
@@ -57,121 +64,168 @@ residual_norm_bwd_kernel(const ResidualNormBwdArgs a, float *part) {
 #pragma unroll
     for (int k = 0; k < RN; ++k) r[i][k] = dr[i][k] = Raw<R, RV>{};
   }
-  float w[N], s[N], p[N];  // weight, alpha scale, post_weight
-  float dw[N], db[N], ds[N], dp[N];
+  C w[N], f[N];             // weight; alpha scale post_weight
+  C dw[N], db[N], ex[N];    // sums over rows of dy n, dy, e n_x
 #pragma unroll
   for (int i = 0; i < I; ++i) {
     const int c = (lane + i * size) * V;
-    params_or<V>(a.weight, c, D, 1.f, w + i * V);
-    params_or<V>(a.scale, c, D, 1.f, s + i * V);
-    params_or<V>(X ? a.post_weight : nullptr, c, D, 1.f, p + i * V);
+    float p[V], s[V];
+    params_or<V>(a.weight, c, D, 1.f, p);
+    P::pack(p, w + i * H);
+    params_or<V>(a.scale, c, D, 1.f, s);
+    params_or<V>(X ? a.post_weight : nullptr, c, D, 1.f, p);
+#pragma unroll
+    for (int e = 0; e < V; ++e) p[e] *= a.alpha * s[e];
+    P::pack(p, f + i * H);
   }
 #pragma unroll
-  for (int j = 0; j < N; ++j) {
-    s[j] *= a.alpha;
-    dw[j] = db[j] = ds[j] = dp[j] = 0.f;
-  }
+  for (int j = 0; j < N; ++j) dw[j] = db[j] = ex[j] = C(0);
   if (row < a.rows) fetch(row);
   // A team out of rows stays while another of its warp has one: the sums need
   // the whole warp.
   for (long long first = row - (LANES ? threadIdx.x % 32 / size : 0); first < a.rows;
        first += step, row += step) {
     const bool live = row < a.rows;
-    float v[N], g[N], e[N], vx[N];
+    C v[N], g[N], e[N], vx[X ? N : 1];
 #pragma unroll
     for (int i = 0; i < I; ++i) {
-      dy[i].unpack(g + i * V);
-      x[i].unpack(vx + i * V);
-#pragma unroll
-      for (int k = 0; k < RN; ++k) {
-        r[i][k].unpack(v + i * V + k * RV);
-        dr[i][k].unpack(e + i * V + k * RV);
+      float t[V];
+      dy[i].unpack(t);
+      P::pack(t, g + i * H);
+      if constexpr (X) {
+        x[i].unpack(t);
+        P::pack(t, vx + i * H);
       }
+#pragma unroll
+      for (int k = 0; k < RN; ++k) r[i][k].unpack(t + k * RV);
+      P::pack(t, v + i * H);
+#pragma unroll
+      for (int k = 0; k < RN; ++k) dr[i][k].unpack(t + k * RV);
+      P::pack(t, e + i * H);
     }
     if (row + step < a.rows) fetch(row + step);
-    float sums[4] = {0.f, 0.f, 0.f, 0.f};
-    float mean_x = 0.f;
+    C q0 = C(0), q1 = C(0), q2 = C(0), q3 = C(0);
+    float rho, rho_x = 1.f, along, mean_g = 0.f;
     if (layer) {
-      float m[2] = {0.f, 0.f};
+      C m0 = C(0), m1 = C(0);
 #pragma unroll
-      for (int j = 0; j < N; ++j) m[0] += v[j], m[1] += vx[j];
+      for (int j = 0; j < N; ++j) {
+        m0 = add2(m0, v[j]);
+        if constexpr (X) m1 = add2(m1, vx[j]);
+      }
+      float m[2] = {total(m0), total(m1)};
       team_sums<LANES>(m, red, turn);
-      mean_x = post ? m[1] * inv : 0.f;
+      const C mv = both(-m[0] * inv), mx = both(post ? -m[1] * inv : 0.f);
 #pragma unroll
-      for (int i = 0; i < I; ++i)
+      for (int i = 0; i < I; ++i) {
+        const bool in = (lane + i * size) * V < D;
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
-          const bool in = (lane + i * size) * V < D;
-          v[i * V + k] = in ? v[i * V + k] - m[0] * inv : 0.f;
-          if (post) vx[i * V + k] = in ? vx[i * V + k] - mean_x : 0.f;
+        for (int k = 0; k < H; ++k) {
+          v[i * H + k] = in ? add2(v[i * H + k], mv) : C(0);
+          if constexpr (X) vx[i * H + k] = in ? add2(vx[i * H + k], mx) : C(0);
         }
+      }
     }
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      const float gw = g[j] * w[j];
-      sums[0] = fmaf(v[j], v[j], sums[0]);
-      sums[1] = fmaf(gw, v[j], sums[1]);
-      sums[2] += gw;
-      sums[3] = fmaf(vx[j], vx[j], sums[3]);
+      const C gw = mul2(g[j], w[j]);
+      q0 = fma2(v[j], v[j], q0);
+      q1 = fma2(gw, v[j], q1);
+      if (layer) q2 = add2(gw, q2);
+      if constexpr (X) q3 = fma2(vx[j], vx[j], q3);
     }
-    team_sums<LANES>(sums, red, turn);
-    const float rho = rsqrtf(fmaf(sums[0], inv, a.eps));
-    const float mean_g = layer ? sums[2] * inv : 0.f, along = sums[1] * inv * rho * rho;
-    const float rho_x = post ? rsqrtf(fmaf(sums[3], inv, a.eps)) : 1.f;
+    if (X || layer) {
+      float s[4] = {total(q0), total(q1), total(q2), total(q3)};
+      team_sums<LANES>(s, red, turn);
+      rho = rsqrtf(fmaf(s[0], inv, a.eps));
+      along = s[1];
+      if (layer) mean_g = s[2] * inv;
+      if (post) rho_x = rsqrtf(fmaf(s[3], inv, a.eps));
+    } else {
+      float s[2] = {total(q0), total(q1)};
+      team_sums<LANES>(s, red, turn);
+      rho = rsqrtf(fmaf(s[0], inv, a.eps));
+      along = s[1];
+    }
+    const C rho2 = both(rho), against = both(-along * inv * rho * rho), off = both(-mean_g);
+    const C rhox2 = both(rho_x);
     R *dres = static_cast<R *>(a.dresidual) + row * D;
+    C x0 = C(0), x1 = C(0);
 #pragma unroll
     for (int i = 0; i < I; ++i) {
       const int c = (lane + i * size) * V;
 #pragma unroll
-      for (int k = 0; k < V; ++k) {
-        const int j = i * V + k;
-        e[j] = fmaf(rho, fmaf(g[j], w[j], -mean_g) - along * v[j], e[j]);
+      for (int k = 0; k < H; ++k) {
+        const int j = i * H + k;
+        C t = fma2(g[j], w[j], mul2(against, v[j]));
+        if (layer) t = add2(t, off);
+        e[j] = fma2(rho2, t, e[j]);
         if (live) {
-          dw[j] = fmaf(g[j], v[j] * rho, dw[j]);
-          db[j] += g[j];
+          dw[j] = fma2(g[j], mul2(v[j], rho2), dw[j]);
+          if (bias_grad) db[j] = add2(db[j], g[j]);
         }
       }
-      if (!live || c >= D || !a.dresidual) continue;
+      if (live && c < D && a.dresidual) {
+        float t[V];
+        P::unpack(e + i * H, t);
 #pragma unroll
-      for (int k = 0; k < RN; ++k) store_vec<R, RV>(dres + c + k * RV, e + i * V + k * RV);
-    }
-    float xs[2] = {0.f, 0.f};
+        for (int k = 0; k < RN; ++k) store_vec<R, RV>(dres + c + k * RV, t + k * RV);
+      }
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      if constexpr (X) {
-        vx[j] *= rho_x;  // n_x, or x where there is no post norm
-        if (live) {
-          ds[j] = fmaf(a.alpha * e[j], vx[j] * p[j], ds[j]);
-          dp[j] = fmaf(s[j] * e[j], vx[j], dp[j]);
+      for (int k = 0; k < H; ++k) {
+        const int j = i * H + k;
+        if constexpr (X) {
+          vx[j] = mul2(vx[j], rhox2);  // n_x, or x where there is no post norm
+          if (live) ex[j] = fma2(e[j], vx[j], ex[j]);
+        }
+        e[j] = mul2(e[j], f[j]);
+        if constexpr (X) {
+          x0 = fma2(e[j], vx[j], x0);
+          if (layer) x1 = add2(x1, e[j]);
         }
       }
-      e[j] *= s[j] * p[j];
-      if constexpr (X) {
-        xs[0] = fmaf(e[j], vx[j], xs[0]);
-        xs[1] += e[j];
-      }
     }
-    if (post) {
-      team_sums<LANES>(xs, red, turn);
-      const float along_x = xs[0] * inv, mean = layer ? xs[1] * inv : 0.f;
+    if constexpr (X) {
+      if (post) {
+        float xs[2] = {total(x0), total(x1)};
+        team_sums<LANES>(xs, red, turn);
+        const C along_x = both(-xs[0] * inv), mean = both(layer ? -xs[1] * inv : 0.f);
 #pragma unroll
-      for (int j = 0; j < N; ++j) e[j] = rho_x * (e[j] - mean - along_x * vx[j]);
+        for (int j = 0; j < N; ++j)
+          e[j] = mul2(rhox2, fma2(along_x, vx[j], layer ? add2(e[j], mean) : e[j]));
+      }
     }
     T *dx = static_cast<T *>(a.dx) + row * D;
 #pragma unroll
     for (int i = 0; i < I; ++i) {
       const int c = (lane + i * size) * V;
-      if (live && c < D) store_vec<T, V>(dx + c, e + i * V);
+      float t[V];
+      P::unpack(e + i * H, t);
+      if (live && c < D) store_vec<T, V>(dx + c, t);
     }
   }
   if (!part) return;
   float *mine = part + (long long)blockIdx.x * D;
   const long long all = (long long)gridDim.x * D;
-  if (a.dweight) block_share<V, LANES, I>(dw, mine, D, sum), mine += all;
-  if (a.dbias) block_share<V, LANES, I>(db, mine, D, sum), mine += all;
+  // times alpha and, where it is given, a parameter: for the gradients of scale and post_weight
+  auto share = [&](const C *acc, float alpha, const float *other) {
+    float t[V * I];
+#pragma unroll
+    for (int i = 0; i < I; ++i) {
+      float p[V];
+      P::unpack(acc + i * H, t + i * V);
+      params_or<V>(other, (lane + i * size) * V, D, 1.f, p);
+#pragma unroll
+      for (int e = 0; e < V; ++e) t[i * V + e] *= alpha * p[e];
+    }
+    block_share<V, LANES, I>(t, mine, D, sum);
+    mine += all;
+  };
+  if (a.dweight) share(dw, 1.f, nullptr);
+  if (a.dbias) share(db, 1.f, nullptr);
   if constexpr (X) {
-    if (a.dpost_weight) block_share<V, LANES, I>(dp, mine, D, sum), mine += all;
-    if (a.dscale) block_share<V, LANES, I>(ds, mine, D, sum);
+    if (a.dpost_weight) share(ex, a.alpha, a.scale);
+    if (a.dscale) share(ex, a.alpha, a.post_weight);
   }
 }
 
@@ -182,7 +236,7 @@ cudaError_t launch_residual_bwd_v(const ResidualNormBwdArgs &a) {
     constexpr int MAXT = decltype(most)::value;
     const int teams = LANES ? kNormTeamThreads / LANES : 1;
     const int block = LANES ? kNormTeamThreads : threads;
-    const unsigned blocks = norm_bwd_blocks((a.rows + teams - 1) / teams, block, 1);
+    const unsigned blocks = norm_bwd_blocks((a.rows + teams - 1) / teams, 512 / block, 1);
     WeightSums w{static_cast<const float *>(a.workspace), (int)blocks, a.D, {}};
     int n = 0;
     for (float *out : {a.dweight, a.dbias, a.dpost_weight, a.dscale})
@@ -239,7 +293,7 @@ cudaError_t launch_weight_sums(const WeightSums &w, int count, cudaStream_t stre
 }
 
 size_t residual_norm_bwd_workspace_bytes(long long rows, int D) {
-  return 4 * sizeof(float) * norm_bwd_blocks(rows, 1, 1) * (size_t)D;
+  return 4 * sizeof(float) * norm_bwd_blocks(rows, kNormMostBlocks, 1) * (size_t)D;
 }
 
 cudaError_t launch_residual_norm_bwd(const ResidualNormBwdArgs &a) {
