@@ -595,6 +595,23 @@ def la_rotary_frequencies(rotary_dim, base=10000.0, scaling="plain", factor=1.0,
     return inv_freq, scale.item()
 
 
+def _like(t, stream):
+    """A tensor like ``t`` (contiguous, its shape and dtype) on the call's stream: with no stream
+    given, half of the host's time that ``_new`` takes."""
+    if stream is None:
+        return torch.empty_like(t, memory_format=torch.contiguous_format)
+    return _new(t.shape, t.dtype, t.device, stream)
+
+
+def _scratch(nbytes, t, stream):
+    """A call's workspace (see ``_workspace``), made from one of its tensors."""
+    if not nbytes:
+        return None
+    if stream is None:
+        return t.new_empty(-(-nbytes // t.element_size()))
+    return _workspace(nbytes, t.device, stream)
+
+
 def _int32(t, shape, what):
     if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous int32 {list(shape)}")
@@ -717,21 +734,20 @@ def la_chunk_bwd(q, k, v, dO, chunk=64, decay_kind="none", decay=None, S0=None, 
     s0 = None if S0 is None else _dense(S0, state, f32, "S0")
     sf = None if dS_final is None else _dense(dS_final, state, f32, "dS_final")
     dev = _device_of(q, k, v, dO, decay, S0, dS_final, dq, dk, dv, ddecay, dS0, workspace)
-    new = lambda n, t: _new(n, t, q.device, stream)  # noqa: E731
-    dq = new(shape, dtype) if dq is None else dq
-    dk = new(shape, dtype) if dk is None else dk
-    dv = new(v_shape, dtype) if dv is None else dv
+    dq = _like(q, stream) if dq is None else dq
+    dk = _like(k, stream) if dk is None else dk
+    dv = _like(v, stream) if dv is None else dv
     if ddecay is not None and decay is None:
         raise ValueError("ddecay without a decay")
     if ddecay is None and want_decay_grad and decay is not None:
-        ddecay = new(decay_shape, f32)
+        ddecay = _like(decay, stream)
     if dS0 is None and (S0 is not None if want_state_grad is None else want_state_grad):
-        dS0 = new(state, f32)
+        dS0 = _new(state, f32, q.device, stream)
     lib = _native.load()
     ws = ws_bytes = 0
     if workspace is None:
-        workspace = _workspace(lib.la_chunk_bwd_workspace_bytes(B, H, L, d_k, d_v, chunk,
-                                                                DTYPE[dtype]), q.device, stream)
+        workspace = _scratch(lib.la_chunk_bwd_workspace_bytes(B, H, L, d_k, d_v, chunk,
+                                                              DTYPE[dtype]), q, stream)
     if workspace is not None:
         ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     status = lib.la_chunk_bwd(
@@ -784,19 +800,18 @@ def la_gated_norm_bwd(dy, x, gate=None, weight=None, bias=None, norm="rms", acti
         if g is not None and (p is None or g.shape != p.shape):
             raise ValueError(f"{what} must have its parameter's shape")
     if dx is None:
-        dx = _new(x.shape, dtype, x.device, stream)
+        dx = _like(x, stream)
     if gate is not None and dgate is None:
-        dgate = _new(shape, dtype, x.device, stream)
+        dgate = _like(gate, stream)
     if want_param_grads:
         if weight is not None and dweight is None:
-            dweight = _new(weight.shape, torch.float32, x.device, stream)
+            dweight = _like(weight, stream)
         if bias is not None and dbias is None:
-            dbias = _new(bias.shape, torch.float32, x.device, stream)
+            dbias = _like(bias, stream)
     lib = _native.load()
     ws = ws_bytes = 0
     if workspace is None and (dweight is not None or dbias is not None):
-        workspace = _workspace(lib.la_gated_norm_bwd_workspace_bytes(B, H, L, d, heads), x.device,
-                               stream)
+        workspace = _scratch(lib.la_gated_norm_bwd_workspace_bytes(B, H, L, d, heads), x, stream)
     if workspace is not None:
         ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     status = lib.la_gated_norm_bwd(
@@ -843,21 +858,20 @@ def la_residual_norm_bwd(dy, r, weight=None, dr=None, x=None, post_weight=None, 
     drp = None if dr is None else _same(dr, shape, rd)
     xp = None if x is None else _same(x, shape, dtype)
     dev = _device_of(dy, r, dr, x, weight, post_weight, scale, dx, dresidual, workspace)
-    own = stream is None or stream.cuda_stream == _current_stream(dev)
-    if dx is None:
-        dx = torch.empty_like(dy) if own else _new(shape, dtype, dy.device, stream)
+    dx = _like(dy, stream) if dx is None else dx
     if dresidual is None and want_dresidual:
-        dresidual = torch.empty_like(r) if own else _new(shape, rd, dy.device, stream)
-    params = want_param_grads
-    grads = [_new(per, torch.float32, dy.device, stream) if wanted else None
-             for wanted in (params and w is not None, want_dbias, params and pw is not None,
-                            params and sc is not None)]
+        dresidual = _like(r, stream)
+    grads = [None] * 4  # of weight, bias, post_weight, scale
+    if want_param_grads:
+        grads = [_like(weight, stream) if w else None, None,
+                 _like(post_weight, stream) if pw else None, _like(scale, stream) if sc else None]
+    if want_dbias:
+        grads[1] = _like(weight, stream) if w else _new(per, torch.float32, dy.device, stream)
     rows = dy.numel() // D if D else 0
     lib = _native.load()
     ws = ws_bytes = 0
-    if workspace is None and any(g is not None for g in grads):
-        workspace = _workspace(lib.la_residual_norm_bwd_workspace_bytes(rows, D), dy.device,
-                               stream)
+    if workspace is None and (want_dbias or want_param_grads and (w or pw or sc)):
+        workspace = _scratch(lib.la_residual_norm_bwd_workspace_bytes(rows, D), dy, stream)
     if workspace is not None:
         ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     status = lib.la_residual_norm_bwd(

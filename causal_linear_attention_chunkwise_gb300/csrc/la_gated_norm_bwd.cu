@@ -15,22 +15,33 @@
 namespace la {
 namespace {
 
-// act(z) and its derivative.
-__device__ __forceinline__ void act_and_slope(int act, float z, float &a, float &slope) {
-  if (act == LA_ACT_NONE) {
-    a = z, slope = 1.f;
-    return;
+// act(z) and its derivative of a cell of values: s = sigmoid(z); z s has s + z s (1 - s).
+__device__ __forceinline__ unsigned long long sigmoid2(unsigned long long z) {
+  return activate2(LA_ACT_SIGMOID, z);
+}
+__device__ __forceinline__ float sigmoid2(float z) { return sigmoid(z); }
+
+template <int ACT, int V, typename C>
+__device__ __forceinline__ void act_and_slope(C z, C &a, C &slope) {
+  if constexpr (ACT == LA_ACT_NONE) {
+    a = z, slope = CellOf<V>::both(1.f);
+  } else {
+    const C s = sigmoid2(z), rest = fma2(s, CellOf<V>::both(-1.f), CellOf<V>::both(1.f));
+    a = ACT == LA_ACT_SILU ? mul2(z, s) : s;
+    slope = ACT == LA_ACT_SILU ? fma2(a, rest, s) : mul2(s, rest);
   }
-  const float s = sigmoid(z), rest = 1.f - s;
-  a = act == LA_ACT_SILU ? z * s : s;
-  slope = act == LA_ACT_SILU ? fmaf(a, rest, s) : s * rest;
 }
 
 // Weights shared by the heads: the rows are those of all heads, in the order of
 // the tokens.  Weights of each head: a block stays with head blockIdx.y.
-// BIAS: there is a bias, or a gradient of one.
-template <typename T, int V, int LANES, int I, bool BIAS, int MAXT>
-__global__ void __launch_bounds__(MAXT, LANES ? (I == 1 ? 3 : 2) : 1)
+// BIAS: there is a bias, or a gradient of one.  FIRST: there is a gate, in front of the norm.
+// Blocks of teams to an SM: three where their registers allow it (4 x 16 x 4096 x 64 bf16: 37 us, with
+// two 40).
+template <int V, int LANES, int I, bool BIAS, bool FIRST> constexpr int kBlocksPerSm =
+    LANES ? (I == 1 && (V <= 4 || !(BIAS || FIRST)) ? 3 : 2) : 1;
+
+template <typename T, int V, int LANES, int I, bool BIAS, bool FIRST, int MAXT>
+__global__ void __launch_bounds__(MAXT, kBlocksPerSm<V, LANES, I, BIAS, FIRST>)
 gated_norm_bwd_kernel(const GatedNormBwdArgs a, long long rows, float *part) {
   using P = Cells<V>;
   using C = typename P::C;
@@ -44,7 +55,7 @@ gated_norm_bwd_kernel(const GatedNormBwdArgs a, long long rows, float *part) {
   long long r = (long long)blockIdx.x * teams + (LANES ? threadIdx.x / size : 0);
   const int d = a.d, own_head = a.weight_heads > 1 ? (int)blockIdx.y : -1;
   const float inv = 1.f / d;
-  const bool gate = a.gate != nullptr, gate_first = gate && a.gate_first;
+  const bool gate = FIRST || a.gate;
   const bool layer = a.norm == LA_NORM_LAYER;
   auto both = [](float v) { return CellOf<V>::both(v); };
   auto total = [](C c) { return CellOf<V>::sum(c); };
@@ -120,19 +131,28 @@ gated_norm_bwd_kernel(const GatedNormBwdArgs a, long long rows, float *part) {
     C keep[N];  // what dgate has beside n: act's slope, times x where the gate comes first, else dy
 #pragma unroll
     for (int i = 0; i < I; ++i) {
-      float f[V], s[V];
+      float f[V];
       x[i].unpack(f);
       P::pack(f, v + i * H);
       dy[i].unpack(f);
       P::pack(f, g + i * H);
       z[i].unpack(f);
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        if (gate) act_and_slope(a.act, f[e], f[e], s[e]);
-        else f[e] = 1.f, s[e] = 0.f;
-      }
       P::pack(f, act + i * H);
-      P::pack(s, keep + i * H);
+    }
+    auto activate_all = [&](auto kind) {
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        act_and_slope<decltype(kind)::value, V>(act[j], act[j], keep[j]);
+    };
+    if (!gate) {
+#pragma unroll
+      for (int j = 0; j < N; ++j) act[j] = both(1.f), keep[j] = C(0);
+    } else if (a.act == LA_ACT_SILU) {
+      activate_all(IntC<LA_ACT_SILU>{});
+    } else if (a.act == LA_ACT_SIGMOID) {
+      activate_all(IntC<LA_ACT_SIGMOID>{});
+    } else {
+      activate_all(IntC<LA_ACT_NONE>{});
     }
     if (r + step < rows) {
       at = advance(at);
@@ -140,8 +160,8 @@ gated_norm_bwd_kernel(const GatedNormBwdArgs a, long long rows, float *part) {
     }
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      keep[j] = mul2(keep[j], gate_first ? v[j] : g[j]);
-      if (gate_first) v[j] = mul2(v[j], act[j]);
+      keep[j] = mul2(keep[j], FIRST ? v[j] : g[j]);
+      if (FIRST) v[j] = mul2(v[j], act[j]);
       else g[j] = mul2(g[j], act[j]);  // the gradient of n w + b
     }
     if (layer) {
@@ -190,11 +210,11 @@ gated_norm_bwd_kernel(const GatedNormBwdArgs a, long long rows, float *part) {
           dw[j] = fma2(g[j], n, dw[j]);
           if constexpr (BIAS) db[j] = add2(db[j], g[j]);
         }
-        ox[k] = gate_first ? mul2(u, act[j]) : u;
+        ox[k] = FIRST ? mul2(u, act[j]) : u;
         C y;
         if constexpr (BIAS) y = fma2(n, w[j], bias[j]);
         else y = mul2(n, w[j]);
-        oz[k] = mul2(gate_first ? u : y, keep[j]);
+        oz[k] = mul2(FIRST ? u : y, keep[j]);
       }
       if (!live || c >= d) continue;
       float f[V];
@@ -236,14 +256,18 @@ cudaError_t launch_v(const GatedNormBwdArgs &a) {
     constexpr int MAXT = decltype(most)::value;
     const int heads = per_head ? a.H : 1, teams = LANES ? kNormTeamThreads / LANES : 1;
     const int block = LANES ? kNormTeamThreads : threads;
-    const unsigned blocks = norm_bwd_blocks((rows + teams - 1) / teams, LANES && I == 1 ? 3 : 512 / block, heads);
     float *part = sums ? static_cast<float *>(a.workspace) : nullptr;
-    if (a.bias || a.dbias)
-      gated_norm_bwd_kernel<T, V, LANES, I, true, MAXT>
+    unsigned blocks = 0;
+    auto launch = [&](auto bias, auto first) {
+      constexpr bool BIAS = decltype(bias)::value != 0, FIRST = decltype(first)::value != 0;
+      blocks = norm_bwd_blocks((rows + teams - 1) / teams,
+                               LANES ? kBlocksPerSm<V, LANES, I, BIAS, FIRST> : 512 / block, heads);
+      gated_norm_bwd_kernel<T, V, LANES, I, BIAS, FIRST, MAXT>
           <<<dim3(blocks, heads), block, 0, a.stream>>>(a, rows, part);
-    else
-      gated_norm_bwd_kernel<T, V, LANES, I, false, MAXT>
-          <<<dim3(blocks, heads), block, 0, a.stream>>>(a, rows, part);
+    };
+    const bool first = a.gate && a.gate_first;
+    if (a.bias || a.dbias) first ? launch(IntC<1>{}, IntC<1>{}) : launch(IntC<1>{}, IntC<0>{});
+    else first ? launch(IntC<0>{}, IntC<1>{}) : launch(IntC<0>{}, IntC<0>{});
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !sums) return e;
     WeightSums w{part, (int)blocks, width, {}};
