@@ -27,8 +27,11 @@ struct Plan {
 };
 
 // The segments that take the least time on 152 SMs, in units of a chunk of both
-// walks: whole waves of blocks, each a segment's chunks; with more than one segment also
-// the pass over their own shares (about 0.4 of a chunk's time) and its two launches.
+// walks: whole waves of blocks, each a segment's chunks and a start; with more than one
+// segment also the pass over their own shares, S and G in blocks of their own at 0.2 of a chunk's
+// time, and two launches.  It picks 2 segments for 2 x 32 x 8192 x 128 with decays (550 us; 4: 606,
+// 7: 624), 9 for 1 x 16 x 32768 x 128 (586; 4: 1029, 19: 600), 2 for 4 x 16 x 4096 x 64 (156; 4:
+// 165), 9 for 3 x 5 x 777 x 64 x 128 fp32 (110; 5: 154, 13: 135).
 Plan make_plan(const ChunkBwdArgs &a, bool f32_out) {
   Plan p;
   p.wide = std::max(a.dk, a.dv) > 64;
@@ -44,8 +47,8 @@ Plan make_plan(const ChunkBwdArgs &a, bool f32_out) {
   for (int per = std::min(p.chunks, kMaxPer); per > 0;) {
     const int n = (p.chunks + per - 1) / per;
     const long long waves = (seqs * n + slots - 1) / slots;
-    const long long share_waves = (2 * seqs * (n - 1) + 2 * slots - 1) / (2 * slots);
-    const double cost = (double)waves * (per + 1) + (n > 1 ? 0.4 * share_waves * per + 4 : 0);
+    const long long share_waves = (2 * seqs * (n - 1) + slots - 1) / slots;
+    const double cost = waves * (per + 1.5) + (n > 1 ? 0.2 * share_waves * per + 1 : 0);
     if (p.per == 0 || cost < best) best = cost, p.per = per, p.segments = n;
     if ((waves > 4 && n > 1) || per == 1) break;  // finer cuts only add to the work
     per = std::min(per - 1, (p.chunks + n) / (n + 1));  // the longest segments of a finer cut
@@ -200,17 +203,19 @@ template <int WIDTH> __device__ __forceinline__ float group_sum(float v) {
 // the chunk's rq it is <G, S> in front of the chunk, and that less the next chunk's rk is the
 // next one's.  Around a block of a chunk: those, the chunk's rq behind the block, its rk in front,
 // and its pairs across the block (from one to the next: less cs, plus rs).
+constexpr int kDecayWarps = 32;
+
 template <int C, int BLOCK>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(32 * kDecayWarps)
 decay_grad_kernel(const ChunkBwd p, float *ddecay, float *by_segment) {
   __shared__ float sum_q[kMaxPer], sum_k[kMaxPer], all[kMaxPer];
-  __shared__ double share[8];
+  __shared__ double share[kDecayWarps];
   constexpr int N = C / 32, LANES = BLOCK / N, BLOCKS = C / BLOCK;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int seq = blockIdx.x / p.segments, seg = blockIdx.x % p.segments;
   const int c0 = seg * p.per, n = min(p.per, p.chunks - c0);
   const size_t base = (size_t)seq * p.L;
-  for (int c = warp; c < n; c += 8) {
+  for (int c = warp; c < n; c += kDecayWarps) {
     float q = 0.f, k = 0.f;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -236,7 +241,7 @@ decay_grad_kernel(const ChunkBwd p, float *ddecay, float *by_segment) {
   }
   __syncthreads();
   double total = 0.0;
-  for (int c = warp; c < n; c += 8) {
+  for (int c = warp; c < n; c += kDecayWarps) {
     float q[N], k[N], r[N], cs[N], rs[N];
     float sq = 0.f, sk = 0.f, sr = 0.f, scs = 0.f, srs = 0.f;
 #pragma unroll
@@ -296,7 +301,7 @@ decay_grad_kernel(const ChunkBwd p, float *ddecay, float *by_segment) {
   if (lane == 0) share[warp] = total;
   __syncthreads();
   if (threadIdx.x == 0) {
-    for (int i = 1; i < 8; ++i) total += share[i];
+    for (int i = 1; i < kDecayWarps; ++i) total += share[i];
     by_segment[blockIdx.x] = (float)total;
   }
 }
@@ -366,11 +371,11 @@ cudaError_t launch_chunk_bwd(const ChunkBwdArgs &a) {
                   : launch_chunk_bwd_bf16(p, (int)seqs, plan.wide, plan.planes, a.stream);
   if (e != cudaSuccess || !decay_grad) return e;
   if (plan.chunk == 128)
-    decay_grad_kernel<128, 32><<<(unsigned)blocks, 256, 0, a.stream>>>(p, a.ddecay, by_segment);
+    decay_grad_kernel<128, 32><<<(unsigned)blocks, 32 * kDecayWarps, 0, a.stream>>>(p, a.ddecay, by_segment);
   else if (plan.chunk == 32)
-    decay_grad_kernel<32, 32><<<(unsigned)blocks, 256, 0, a.stream>>>(p, a.ddecay, by_segment);
+    decay_grad_kernel<32, 32><<<(unsigned)blocks, 32 * kDecayWarps, 0, a.stream>>>(p, a.ddecay, by_segment);
   else
-    decay_grad_kernel<64, 64><<<(unsigned)blocks, 256, 0, a.stream>>>(p, a.ddecay, by_segment);
+    decay_grad_kernel<64, 64><<<(unsigned)blocks, 32 * kDecayWarps, 0, a.stream>>>(p, a.ddecay, by_segment);
   if ((e = cudaGetLastError()) != cudaSuccess || a.decay_kind != LA_DECAY_HEAD) return e;
   head_decay_kernel<<<a.H, 32, 0, a.stream>>>(by_segment, a.ddecay, a.B, a.H, plan.segments);
   return cudaGetLastError();

@@ -366,13 +366,14 @@ template <int D, int NM> struct StateRow {
 };
 
 // 8 values of a gradient into a staging cell; SLOPE: times phi's derivative at the raw values
-// that the cell holds (elu + 1: e^x up to 0, then 1).
-template <bool SLOPE> __device__ __forceinline__ void stage_8(uint4 *cell, const float *f) {
+// that another cell, or the same, holds (elu + 1: e^x up to 0, then 1).
+template <bool SLOPE>
+__device__ __forceinline__ void stage_8(uint4 *cell, const uint4 *raw, const float *f) {
   float y[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) y[e] = f[e];
   if constexpr (SLOPE) {
-    const uint4 u = *cell;
+    const uint4 u = *raw;
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -697,7 +698,7 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
       for (int e = 0; e < 32; e += 8) {
         uint4 *cell = b.cell(TQ, b.half * N + x + e);
         if (NM == 3) dot = dot_8(*cell, f + e, dot);
-        stage_8<PHI>(cell, g + e);
+        stage_8<PHI>(cell, cell, g + e);
       }
     }
     if (NM == 3 && b.half == 1) sums[b.row] = dot, inside[b.row] = pairs;
@@ -752,13 +753,21 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
 }
 
 // ---------------------------------------------------------------- dk and dv
+template <int D, int NM, bool PHI> constexpr bool kv_own_tiles() {
+  return D == 64 || (NM == 1 && !PHI);
+}
+template <int D, int NM, bool PHI> constexpr int kv_tiles() {
+  return 4 + PHI + (kv_own_tiles<D, NM, PHI>() ? 2 : 0);
+}
 template <int D, int NM, bool PHI, bool DECAY>
 __global__ void __launch_bounds__(kThreads, 1)
 grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned int *err) {
-  // A fifth tile holds phi(k) beside k, which its derivative needs.  dk and dv leave by k's and
-  // v's tiles.
-  using SM = Smem<D, NM, PHI ? 5 : 4, 1>;
+  // A tile of its own holds phi(k) beside k, which its derivative needs.  dk and dv leave by
+  // tiles of their own; where there is no room for them, by k's and v's, which then load
+  // late (through the state's planes instead they kept these waiting: 256 us against 238).
+  using SM = Smem<D, NM, kv_tiles<D, NM, PHI>(), 1>;
   using ST = StateTile<D>;
+  constexpr bool OWN = kv_own_tiles<D, NM, PHI>(), EARLY_K = OWN && !PHI;
   // Tensor memory: K Q^T and V dO^T, dv, dk.  When the scores have been read their operands
   // take columns 0..63 and 192..255, the state's update those between.
   constexpr uint32_t T_P = 0, T_DP = 128, T_V = 256, T_K = 256 + D, COLUMNS = 512;
@@ -780,14 +789,12 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
   constexpr bool decays = DECAY;
   constexpr uint32_t TQ = SM::OFF_TILES, TK = TQ + SM::TILE, TV = TK + SM::TILE,
                      TD = TV + SM::TILE, TKP = PHI ? TD + SM::TILE : TK;
-  auto load_q = [&](int c) {
-    mbar_arrive_expect_tx(&b.full[0], 4 * SM::TILE);
-    load_tile_tma<D>(b, TQ, &maps.q, &b.full[0], c * CT, seq);
-  };
-  auto load_kv = [&](int c) {
-    load_tile_tma<D>(b, TK, &maps.k, &b.full[0], c * CT, seq);
-    load_tile_tma<D>(b, TV, &maps.v, &b.full[0], c * CT, seq);
-  };
+  constexpr uint32_t OUT = TD + (PHI ? 2 : 1) * SM::TILE;
+  constexpr uint32_t TDV = OWN ? OUT : TV, TDK = OWN ? OUT + SM::TILE : TK;
+  auto arm = [&] { mbar_arrive_expect_tx(&b.full[0], 4 * SM::TILE); };
+  auto load_q = [&](int c) { load_tile_tma<D>(b, TQ, &maps.q, &b.full[0], c * CT, seq); };
+  auto load_k = [&](int c) { load_tile_tma<D>(b, TK, &maps.k, &b.full[0], c * CT, seq); };
+  auto load_v = [&](int c) { load_tile_tma<D>(b, TV, &maps.v, &b.full[0], c * CT, seq); };
   auto load_dO = [&](int c) { load_tile_tma<D>(b, TD, &maps.dO, &b.full[0], c * CT, seq); };
   auto prefetch = [&](int c) {
     prefetch_tile<D>(&maps.q, c * CT, seq);
@@ -796,8 +803,10 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
     prefetch_tile<D>(&maps.dO, c * CT, seq);
   };
   if (threadIdx.x == kLeaderKV) {
+    arm();
     load_q(c1 - 1);
-    load_kv(c1 - 1);
+    load_k(c1 - 1);
+    load_v(c1 - 1);
     load_dO(c1 - 1);
   }
   TokenDecay next;
@@ -820,6 +829,7 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
       map_tile_tc<D>(smem + TQ, smem + TQ, p.L - t0);
       map_tile_tc<D>(smem + TK, smem + TKP, p.L - t0);
     }
+    if (OWN && threadIdx.x == kLeaderKV) tma_store_wait_read_all();
     fence_proxy_async_smem();
     tc_fence_before();
     if (__syncthreads_or(b.failed)) break;
@@ -912,6 +922,7 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
     }
     if (NM == 3 && b.half == 1) sums[b.row] = dot, sums[CT + b.row] = pairs;
     tmem_st_wait();
+    fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
     const Operand q = along_col<SM::BOX>(b.base + TQ), dO = along_col<SM::BOX>(b.base + TD);
@@ -920,6 +931,11 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
       product_ta<CT>(b.tmem + T_V, b.tmem + T_AP, dO, id_out, true);
       product_ta<CT>(b.tmem + T_K, b.tmem + T_ADP, q, id_out, true);
       mma_commit(&b.mma[2]);
+      if (more) {
+        arm();
+        if (OWN) load_v(c - 1);
+        if (EARLY_K) load_k(c - 1);
+      }
     }
     if (NM == 3 && p.rk && t < p.L) {
       const size_t to = (size_t)seq * p.L + t;
@@ -957,26 +973,31 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
       float f[32];
       load_32(b, T_V + col, f);
 #pragma unroll
-      for (int e = 0; e < 32; e += 8) stage_8<false>(b.cell(TV, col + e), f + e);
+      for (int e = 0; e < 32; e += 8) stage_8<false>(b.cell(TDV, col + e), nullptr, f + e);
       load_32(b, T_K + col, f);
 #pragma unroll
-      for (int e = 0; e < 32; e += 8) stage_8<PHI>(b.cell(TK, col + e), f + e);
+      for (int e = 0; e < 32; e += 8)
+        stage_8<PHI>(b.cell(TDK, col + e), b.cell(TK, col + e), f + e);
     }
     fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
     if (threadIdx.x == kLeaderKV) {
-      store_tile_tma<D>(b, TV, &maps.dv, t0, seq);
-      store_tile_tma<D>(b, TK, &maps.dk, t0, seq);
+      store_tile_tma<D>(b, TDV, &maps.dv, t0, seq);
+      store_tile_tma<D>(b, TDK, &maps.dk, t0, seq);
       tma_store_commit();
+      if (OWN && !EARLY_K && more) load_k(c - 1);
     }
     if (update) {
       b.wait_mma(3, phase);
       if (threadIdx.x == kLeaderKV && more) {
         if (!DECAY) load_q(c - 1);
         load_dO(c - 1);
-        tma_store_wait_read_all();
-        load_kv(c - 1);
+        if (!OWN) {
+          tma_store_wait_read_all();
+          load_k(c - 1);
+          load_v(c - 1);
+        }
       }
       __syncwarp();
       state.update(b, T_U, ex2_approx(end.x));
@@ -996,7 +1017,7 @@ template <int D, int NM, bool PHI, bool DECAY>
 cudaError_t launch_tc(const ChunkBwd &p, int seqs, cudaStream_t stream) {
   using SS = Smem<D, NM, 2, 2>;
   using SQ = Smem<D, NM, 4, 1>;
-  using SK = Smem<D, NM, PHI ? 5 : 4, 1>;
+  using SK = Smem<D, NM, kv_tiles<D, NM, PHI>(), 1>;
   Maps m;
   const struct {
     CUtensorMap *map;
