@@ -16,6 +16,7 @@ cudaError_t launch_chunk_bwd_f32(const ChunkBwd &p, int seqs, bool wide, bool bf
 namespace {
 
 constexpr int kMaxPer = 512;  // chunks of a segment (the decays' kernel keeps sums of them)
+constexpr int kKeep = 1024;   // tokens from one kept state to the next
 
 // How a call runs: which planes, the chunk, the segments.
 struct Plan {
@@ -81,7 +82,13 @@ size_t lay_out(const ChunkBwdArgs &a, const Plan &plan, bool decay_grad, char *b
     float *rq = part(seqs * a.L), *rk = part(seqs * a.L), *rc = part(seqs * a.L);
     float *cs = plan.tc ? part(seqs * a.L) : nullptr, *rs = plan.tc ? part(seqs * a.L) : nullptr;
     float *around = part(seqs * plan.segments), *sums = part(seqs * plan.segments);
-    if (p) p->rq = rq, p->rk = rk, p->rc = rc, p->cs = cs, p->rs = rs, p->around = around, *by_segment = sums;
+    const size_t kept = seqs * (plan.chunks / (kKeep / plan.chunk)), width = plan.wide ? 128 : 64;
+    float *states = part(kept * width * width), *between = part(kept * kShares);
+    if (p) {
+      p->rq = rq, p->rk = rk, p->rc = rc, p->cs = cs, p->rs = rs, p->around = around;
+      p->kept = states, p->between = between;
+      *by_segment = sums;
+    }
   }
   return at;
 }
@@ -199,9 +206,9 @@ template <int WIDTH> __device__ __forceinline__ float group_sum(float v) {
 
 // A block: the tokens of one segment.  Their decays' gradients are sums of pairs (i < t <= j):
 //     over s >= t of rq + cs, over s < t of rk + rs, within t's block of BLOCK tokens, and `around`
-// the block.  <G, e^L_C S>, the pairs around a chunk, is given for the segment's last chunk; with
-// the chunk's rq it is <G, S> in front of the chunk, and that less the next chunk's rk is the
-// next one's.  Around a block of a chunk: those, the chunk's rq behind the block, its rk in front,
+// the block.  <G, e^L_C S>, the pairs around a chunk, is given for the segment's last chunk and
+// where a state was kept; with the chunk's rq it is <G, S> in front of the chunk, and that less the
+// next chunk's rk is the next one's.  Around a block of a chunk: those, the chunk's rq behind the block, its rk in front,
 // and its pairs across the block (from one to the next: less cs, plus rs).
 constexpr int kDecayWarps = 32;
 
@@ -229,12 +236,18 @@ decay_grad_kernel(const ChunkBwd p, float *ddecay, float *by_segment) {
     }
   }
   __syncthreads();
-  if (threadIdx.x == 0) {
-    float around = p.around[(size_t)seq * p.segments + seg];
-    for (int c = n - 1; c >= 0; --c) {
+  // A thread: the chunks that follow from one given sum.
+  for (int x = c0 / p.every + threadIdx.x; x * p.every < c0 + n; x += 32 * kDecayWarps) {
+    const int from = max(x * p.every - c0, 0), last = min((x + 1) * p.every - c0, n) - 1;
+    float around = 0.f;
+    if (last == n - 1) around = p.around[(size_t)seq * p.segments + seg];
+    else
+      for (int i = 0; i < kShares; ++i)
+        around += p.between[p.keep_slot(seq, c0 + last) * kShares + i];
+    for (int c = last; c >= from; --c) {
       const float y = around + sum_q[c];
       // Past a decay of 2^-40 nothing of <G, S> is left but the rounding of y.
-      const float next = c > 0 && all[c - 1] >= -40.f ? y - sum_k[c - 1] : 0.f;
+      const float next = c > from && all[c - 1] >= -40.f ? y - sum_k[c - 1] : 0.f;
       all[c] = around;
       around = next;
     }
@@ -357,7 +370,8 @@ cudaError_t launch_chunk_bwd(const ChunkBwdArgs &a) {
   if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
   ChunkBwd p{a.q, a.k, a.v, a.dO, a.dq, a.dk_out, a.dv_out, a.decay, a.S0, a.dS_final, a.dS0,
              a.H, a.L, a.dk, a.dv, a.phi, a.decay_kind, plan.chunks, plan.segments, plan.per,
-             nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr};
+             nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr,
+             nullptr, kKeep / plan.chunk};
   float *by_segment = nullptr;
   lay_out(a, plan, decay_grad, static_cast<char *>(a.workspace), &p, &by_segment);
   cudaError_t e = cudaSuccess;

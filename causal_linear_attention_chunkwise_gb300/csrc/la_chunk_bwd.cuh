@@ -27,7 +27,10 @@
 // products of the rows of dq's and dk's second terms with q and k), and pairs
 // around it (<G, e^L_C S>, which follows from chunk to chunk by the same sums).
 // Formed this way nothing cancels beyond one chunk; q dq - k dk summed from the
-// sequence's end would lose the short decays to the long sums.
+// sequence's end would lose the short decays to the long sums.  Followed from chunk to chunk the
+// sums' errors stay, and a per-head decay's gradient adds them up over all tokens: every 1024
+// tokens S is kept for the backward walk, which forms <G, e^L_C S> anew (2 x 32 x 8192 x 128
+// with per-head decays: 8e-7 off; 4.5e-6 without, growing with the length to the power 1.5).
 //
 // Precision.  Products run in bf16 with fp32 sums.  With bf16 inputs and outputs the
 // decayed scores and the states round once to bf16 as operands (the state itself
@@ -45,6 +48,8 @@
 #include "la_tc_sync.cuh"
 
 namespace la {
+
+constexpr int kShares = 8;  // warps whose sums a <G, S> is left as
 
 // What the kernels get: the tensors, and the plan.
 struct ChunkBwd {
@@ -64,6 +69,17 @@ struct ChunkBwd {
   // and of the chunk's blocks before (cs) and behind (rs) its own, where a chunk has blocks.
   float *rq, *rk, *rc, *cs, *rs;
   float *around;               // [seq][segments] <G, e^L_C S> of a segment's last chunk
+  float *kept;                 // [seq][chunks / every] S before the last of `every` chunks
+  float *between;              // [seq][chunks / every][kShares] <G, e^L_C S> of that chunk
+  int every;
+
+  // Whether chunk c, with its segment ending in front of c1, is one that S is kept for.
+  __device__ __forceinline__ bool keeps(int c, int c1) const {
+    return kept && c + 1 < c1 && (c + 1) % every == 0;
+  }
+  __device__ __forceinline__ size_t keep_slot(int seq, int c) const {
+    return (size_t)seq * (chunks / every) + c / every;
+  }
 };
 
 // T: element type; D: padded width (d_k, d_v <= D); C: tokens of a chunk; NI: planes of the
@@ -90,12 +106,34 @@ template <int C> struct ChunkDecay {
   float2 lam[C];  // log2 of the decay from the chunk's start, as a sum of two floats
   float head[C];  // e^L
   float tail[C];  // e^(L_C - L)
-  float all;      // e^L_C
+  float2 all;     // e^L_C, as a sum of two floats
 };
 
 // The decay between two tokens.
 __device__ __forceinline__ float decay_between(float2 later, float2 earlier) {
   return ex2_approx((later.x - earlier.x) + (later.y - earlier.y));
+}
+
+// 2^x as a sum of two floats, to 2^-27 relative.  A state is multiplied by its chunks' decays
+// again and again: the 2^-23 that an exponential may be off would add up over the chunks that a
+// slow decay spans.  2^n e^t with |t| <= 0.35: 1 + t, whose rounding is kept, and the rest of e^t's
+// series.
+__device__ __forceinline__ float2 exp2_two(float2 x) {
+  if (!(fabsf(x.x) <= 126.f)) return make_float2(ex2_approx(x.x), 0.f);
+  const float n = rintf(x.x), f = x.x - n;
+  const float t = f * 0.693147182f;  // ln 2 = 0.693147182 - 1.90465421e-9
+  const float low = fmaf(f, 0.693147182f, -t) + fmaf(x.y, 0.693147182f, f * -1.90465421e-9f);
+  float s = 1.f / 40320;
+  s = fmaf(s, t, 1.f / 5040), s = fmaf(s, t, 1.f / 720), s = fmaf(s, t, 1.f / 120);
+  s = fmaf(s, t, 1.f / 24), s = fmaf(s, t, 1.f / 6), s = fmaf(s, t, 0.5f);
+  s *= t * t;
+  const float one = 1.f + t, rest = (t - (one - 1.f)) + fmaf(low, one + s, s);
+  const float hi = one + rest, scale = __int_as_float(((int)n + 127) << 23);
+  return make_float2(hi * scale, (rest - (hi - one)) * scale);
+}
+// all s + u
+__device__ __forceinline__ float decayed_sum(float2 all, float s, float u) {
+  return fmaf(all.x, s, fmaf(all.y, s, u));
 }
 
 // The factors of a chunk, by its first C threads.
@@ -111,7 +149,7 @@ __device__ __forceinline__ void chunk_decay(const ChunkBwd &p, int seq, int c, C
   s.lam[t] = own;
   s.head[t] = ex2_approx(own.x);
   s.tail[t] = decay_between(end, own);
-  if (t == 0) s.all = ex2_approx(end.x);
+  if (t == 0) s.all = exp2_two(end);
 }
 
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src, bool live) {
@@ -229,7 +267,7 @@ template <typename F> struct StateRows {
   // c <- all c + sum over tokens of weight x (x) y: x's tile [token][d_k], y's [token][d_v].
   // A chunk's sum is formed by itself and then added, with an fp32 rounding: the tensor
   // cores' cuts would add up over the chunks.
-  __device__ __forceinline__ void update(uint32_t x, uint32_t y, const float *weight, float all,
+  __device__ __forceinline__ void update(uint32_t x, uint32_t y, const float *weight, float2 all,
                                          int warp, int lane) {
     uint32_t w[F::C / 16][F::NM][4];
 #pragma unroll
@@ -263,10 +301,36 @@ template <typename F> struct StateRows {
       for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          c[n + j][e] = fmaf(all, c[n + j][e], F::NM > 1 ? sum[j][e] + small[j][e] : sum[j][e]);
+          c[n + j][e] = decayed_sum(all, c[n + j][e],
+                                    F::NM > 1 ? sum[j][e] + small[j][e] : sum[j][e]);
     }
   }
 };
+
+// A state from its three planes in shared memory, which hold all of its bits, to global memory,
+// and the product of such a one with the state whose planes are there: from the registers,
+// both made the walks spill (3 x 5 x 777 x 64 x 128 fp32: 50 and 63 us against 40 and 57).
+template <typename F> __device__ __forceinline__ float plane_sum(const char *tile, int e) {
+  const uint32_t at = tile_offset<F::D>(e / F::D, e % F::D);
+  float s = 0.f;
+#pragma unroll
+  for (int m = F::NM - 1; m >= 0; --m)
+    s += __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(tile + m * F::STATE + at));
+  return s;
+}
+template <typename F> __device__ __forceinline__ void keep_state(float *dst, const char *tile) {
+#pragma unroll 4
+  for (int e = threadIdx.x; e < F::D * F::D; e += F::THREADS) dst[e] = plane_sum<F>(tile, e);
+}
+template <typename F>
+__device__ __forceinline__ float dot_kept(const float *src, const char *tile) {
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int e = threadIdx.x; e < F::D * F::D; e += 4 * F::THREADS)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      s[i] = fmaf(src[e + i * F::THREADS], plane_sum<F>(tile, e + i * F::THREADS), s[i]);
+  return (s[0] + s[1]) + (s[2] + s[3]);
+}
 
 // acc += small where there were small products.
 template <bool ANY, int NT>
@@ -511,6 +575,8 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_q_kernel(const Chu
       __syncthreads();
     }
     if (F::STAGES == 2 && c + 1 < c1) load(c + 1);
+    if (F::NM == 3 && p.keeps(c, c1))
+      keep_state<F>(p.kept + p.keep_slot(seq, c) * F::D * F::D, state_tile);
     // dO V^T . D: rows j of the group, tokens i <= j
     float w[F::C / 8][4] = {};
     auto live = [&](int j) { return j <= group; };
@@ -557,7 +623,7 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_q_kernel(const Chu
       }
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) around += __shfl_xor_sync(0xffffffffu, around, off);
-      if (lane == 0) sh.sum[warp] = around * sh.decay.all;
+      if (lane == 0) sh.sum[warp] = around * sh.decay.all.x;
     }
     __syncthreads();
     if (p.rq && threadIdx.x < F::C && t0 + (int)threadIdx.x < p.L) {
@@ -623,6 +689,14 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_kv_kernel(const Ch
       __syncthreads();
     }
     if (F::STAGES == 2 && c > c0) load(c - 1);
+    if (F::NM == 3 && p.keeps(c, c1)) {
+      float s = dot_kept<F>(p.kept + p.keep_slot(seq, c) * F::D * F::D, state_tile);
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+      float *to = p.between + p.keep_slot(seq, c) * kShares;
+      if (lane == 0) to[warp] = s * sh.decay.all.x;
+      if (lane == 0 && F::WARPS < kShares) to[F::WARPS + warp] = 0.f;
+    }
     // K Q^T . D and V dO^T . D: rows i of the group, tokens j >= i
     float w[CT][4] = {}, dw[CT][4] = {};
     auto live = [&](int j) { return j >= group; };

@@ -41,6 +41,7 @@ constexpr int kThreads = 256;
 // that has no scores to work on, all of its columns lying outside the mask.
 constexpr int kLeaderQ = 128, kLeaderKV = 96;
 constexpr uint32_t HI = smem_desc_sw128_hi(1024);
+static_assert(kThreads / 32 == kShares, "a share for each warp");
 
 // Shared memory of a walk with TILES input tiles (in STAGES sets).  The planes come first:
 // a D = 64 operand is read as one of 128 rows, whose other half may be anything.
@@ -342,14 +343,34 @@ template <int D, int NM> struct StateRow {
   }
   // c <- all c + the update in tensor memory.  The tensor cores cut a sum's last bits
   // off; formed chunk by chunk and added here, the cuts do not add up.
-  __device__ __forceinline__ void update(const Block &b, uint32_t col, float all) {
+  __device__ __forceinline__ void update(const Block &b, uint32_t col, float2 all) {
     if (b.quarter * 32 >= D) return;
     uint32_t r[N / 32][32];
 #pragma unroll
     for (int i = 0; i < N / 32; ++i) tmem_ld32(b.at(col + b.half * N + i * 32), r[i]);
     tmem_ld_wait();
 #pragma unroll
-    for (int i = 0; i < N; ++i) c[i] = fmaf(all, c[i], __uint_as_float(r[i / 32][i % 32]));
+    for (int i = 0; i < N; ++i) c[i] = decayed_sum(all, c[i], __uint_as_float(r[i / 32][i % 32]));
+  }
+  // The state as it lies in a block's threads, and its product with such a one.
+  __device__ __forceinline__ void keep(float *dst, const Block &b) const {
+    if (b.row >= D) return;
+#pragma unroll
+    for (int i = 0; i < N; i += 4)
+      reinterpret_cast<float4 *>(dst)[i / 4 * (2 * D) + b.half * D + b.row] =
+          make_float4(c[i], c[i + 1], c[i + 2], c[i + 3]);
+  }
+  __device__ __forceinline__ float dot_kept(const float *src, const Block &b) const {
+    float s = 0.f;
+    if (b.row < D) {
+#pragma unroll
+      for (int i = 0; i < N; i += 4) {
+        const float4 x =
+            reinterpret_cast<const float4 *>(src)[i / 4 * (2 * D) + b.half * D + b.row];
+        s = fmaf(x.x, c[i], fmaf(x.y, c[i + 1], fmaf(x.z, c[i + 2], fmaf(x.w, c[i + 3], s))));
+      }
+    }
+    return s;
   }
   __device__ __forceinline__ float dot(const float *src, const Block &b) const {
     float s = 0.f;
@@ -444,6 +465,7 @@ segment_share_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, uns
   int i = 0;
   bool stop = false;
   for (; i < n; ++i) {
+    const float2 all = exp2_two(last);
     b.wait_full(i & 1, (i >> 1) & 1);
     unsigned char *tile = smem + SM::OFF_TILES + (i & 1) * SM::STAGE;
     const uint32_t tile_at = smem_u32(tile), sum = b.tmem + (i & 1) * D;
@@ -495,7 +517,7 @@ segment_share_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, uns
         mma_commit(&b.mma[1]);
       }
     }
-    if (i > 0) state.update(b, ((i - 1) & 1) * D, DECAY ? ex2_approx(last.x) : 1.f);
+    if (i > 0) state.update(b, ((i - 1) & 1) * D, all);
     tc_fence_before();
     if (DECAY) {
       last = ends[i & 1];
@@ -504,7 +526,7 @@ segment_share_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, uns
   }
   if (!stop) {
     b.wait_mma(1, (n - 1) & 1);
-    state.update(b, ((n - 1) & 1) * D, DECAY ? ex2_approx(last.x) : 1.f);
+    state.update(b, ((n - 1) & 1) * D, exp2_two(last));
     const size_t slot = (size_t)seq * (p.segments - 1) + of;
     state.store((back ? p.W : p.U) + slot * D * D, b);
     if (threadIdx.x == 0 && (!back || seg == p.segments - 1))
@@ -608,6 +630,8 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
     }
     const float2 own = decays ? lam[b.row] : make_float2(0.f, 0.f);
     const float2 end = decays ? lam[CT - 1] : make_float2(0.f, 0.f);
+    const float2 all = exp2_two(end);
+    if (NM == 3 && DECAY && p.keeps(c, c1)) state.keep(p.kept + p.keep_slot(seq, c) * es, b);
     b.wait_mma(0, phase);
     // the scores as operand: row j, tokens i <= j
     const float2 before = DECAY && b.quarter ? lam[b.quarter * 32 - 1] : make_float2(0.f, 0.f);
@@ -683,7 +707,7 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
     b.wait_mma(2, phase);
     if (threadIdx.x == kLeaderQ && more && DECAY) load_k(c + 1);
     __syncwarp();
-    const float head = ex2_approx(own.x), all = ex2_approx(end.x);
+    const float head = ex2_approx(own.x);
     float dot = 0.f;
 #pragma unroll
     for (int x = 0; x < N; x += 32) {
@@ -730,7 +754,7 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
     } else if (NM == 3 && p.rq) {  // <G, e^L_C S>: the pairs around the segment's last chunk
       const float *G = seg + 1 < p.segments ? p.W + ((size_t)seq * (p.segments - 1) + seg) * es
                        : p.dSf ? p.dSf + (size_t)seq * es : nullptr;
-      if (G) around = state.dot(G, b) * all;
+      if (G) around = state.dot(G, b) * all.x;
     }
   }
   if (threadIdx.x == kLeaderQ) {
@@ -849,6 +873,14 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
     }
     const float2 own = decays ? lam[b.row] : make_float2(0.f, 0.f);
     const float2 end = decays ? lam[CT - 1] : make_float2(0.f, 0.f);
+    const float2 all = exp2_two(end);
+    if (NM == 3 && DECAY && p.keeps(c, c1)) {
+      float s = state.dot_kept(p.kept + p.keep_slot(seq, c) * es, b);
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+      if (b.lane == 0)
+        p.between[p.keep_slot(seq, c) * kShares + b.warp] = s * all.x;
+    }
     b.wait_mma(0, phase);
     // the scores as operands: row i, tokens j >= i
     uint32_t wp[2][16], wd[2][16];
@@ -1000,7 +1032,7 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
         }
       }
       __syncwarp();
-      state.update(b, T_U, ex2_approx(end.x));
+      state.update(b, T_U, all);
       if (more) state.planes(b);
     }
   }

@@ -1,0 +1,54 @@
+"""Gradients of slow per-head decays over long sequences: one number a head, summed over every
+token, in which errors that stay from chunk to chunk would add up.  Needs a GB300."""
+import pytest
+import torch
+
+from causal_linear_attention_chunkwise_gb300 import api
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+def head_decay_grad(q, k, v, dO, decay):
+    """In 64 bits: dlog gamma_h, the sum over tokens t of the pairs (i < t <= j), which is the sum
+    over j >= t of q_j dq_j less that over i >= t of k_i dk_i.  Chunk by chunk."""
+    B, H, L, _ = q.shape
+    C = 128
+    a = decay.double().view(1, H, 1, 1)
+    n = torch.arange(C, device="cuda").double()
+    D = torch.where(n[:, None] >= n, torch.exp(a * (n[:, None] - n).clamp(min=0)), 0.0)
+    head, tail, whole = (torch.exp(a * m.view(1, 1, -1, 1)) for m in (n + 1, C - 1 - n, n[:1] + C))
+    S = torch.zeros(B, H, q.shape[-1], v.shape[-1], device="cuda", dtype=torch.float64)
+    G = torch.zeros_like(S)
+    net = torch.zeros(B, H, L, device="cuda", dtype=torch.float64)
+    chunks = [[t[:, :, c:c + C].double() for t in (q, k, v, dO)] for c in range(0, L, C)]
+    for c, (Q, K, V, O) in enumerate(chunks):
+        pairs = (Q @ K.mT) * (O @ V.mT) * D
+        net[:, :, c * C:(c + 1) * C] += (
+            pairs.sum(-1) - pairs.sum(-2) + ((O @ S.mT) * head * Q).sum(-1))
+        S = whole * S + (tail * K).mT @ V
+    for c in reversed(range(len(chunks))):
+        Q, K, V, O = chunks[c]
+        net[:, :, c * C:(c + 1) * C] -= ((V @ G.mT) * tail * K).sum(-1)
+        G = whole * G + (head * Q).mT @ O
+    return net.flip(-1).cumsum(-1).sum((0, 2))
+
+
+@pytest.mark.parametrize("dtype,dk,dv", [("bf16", 64, 64), ("bf16", 64, 32), ("f32", 64, 64)])
+def test_slow_head_decays(dtype, dk, dv):
+    """The pairs around a chunk follow from those around the next one by two sums, and are
+    formed anew every 1024 tokens: at most 8 chunks of 128 tokens (16 and 32 smaller ones, with
+    as many tokens) follow one another.  A sum's products are cut, not rounded, 8 times (64 values
+    in steps of 16, in two products): 8 U of its size.  16 such sums with independent signs: 32 U,
+    2e-6 of the gradient's size.  As many sequences as there are SMs, so that they run whole."""
+    B, H, L = 4, 38, 8192
+    g = torch.Generator("cuda").manual_seed(5)
+    q, k = (torch.randn(B, H, L, dk, generator=g, device="cuda").mul_(0.2).to(DT[dtype])
+            for _ in range(2))
+    v, dO = (torch.randn(B, H, L, dv, generator=g, device="cuda").to(DT[dtype]) for _ in range(2))
+    decay = torch.log1p(-2.0 ** -torch.linspace(5, 13, H, device="cuda", dtype=torch.float64)).float()
+    got = api.la_chunk_bwd(q, k, v, dO, decay_kind="head", decay=decay)[3].double()
+    api.la_device_status()
+    want = head_decay_grad(q, k, v, dO, decay)
+    assert (got - want).norm() <= 32 * 2.0 ** -24 * want.norm()
