@@ -49,7 +49,7 @@
 
 namespace la {
 
-constexpr int kShares = 8;  // warps whose sums a <G, S> is left as
+constexpr int kShares = 16;  // warps whose sums a <G, S> is left as, at most
 
 // What the kernels get: the tensors, and the plan.
 struct ChunkBwd {
@@ -114,7 +114,7 @@ __device__ __forceinline__ float decay_between(float2 later, float2 earlier) {
   return ex2_approx((later.x - earlier.x) + (later.y - earlier.y));
 }
 
-// 2^x as a sum of two floats, to 2^-27 relative.  A state is multiplied by its chunks' decays
+// 2^x as a sum of two floats, to 2^-26 relative.  A state is multiplied by its chunks' decays
 // again and again: the 2^-23 that an exponential may be off would add up over the chunks that a
 // slow decay spans.  2^n e^t with |t| <= 0.35: 1 + t, whose rounding is kept, and the rest of e^t's
 // series.
@@ -694,8 +694,8 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_kv_kernel(const Ch
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
       float *to = p.between + p.keep_slot(seq, c) * kShares;
-      if (lane == 0) to[warp] = s * sh.decay.all.x;
-      if (lane == 0 && F::WARPS < kShares) to[F::WARPS + warp] = 0.f;
+      if (lane == 0)
+        for (int i = warp; i < kShares; i += F::WARPS) to[i] = i == warp ? s * sh.decay.all.x : 0.f;
     }
     // K Q^T . D and V dO^T . D: rows i of the group, tokens j >= i
     float w[CT][4] = {}, dw[CT][4] = {};

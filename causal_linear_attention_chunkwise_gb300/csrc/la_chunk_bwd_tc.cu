@@ -2,7 +2,7 @@
 // d_k = d_v = D in {64, 128}, chunks of 128 tokens.
 //
 // The mathematics is la_chunk_bwd.cuh's, a chunk being one 128-row tile.  A
-// block of 256 threads owns a segment of a sequence and one chunk of it at a time, in
+// block of 512 threads owns a segment of a sequence and one chunk of it at a time, in
 // steps that all its threads take together:
 //
 //   1. one thread issues the products that need only the tiles and the state: the scores
@@ -16,9 +16,11 @@
 //      in registers (fp32), and write it as the next chunk's operand, while the next tiles
 //      arrive.
 //
-// Thread (warp w, lane l) owns row 32 (w % 4) + l of every accumulator and the
-// columns of half w / 4, so a mask, a decay or a dot product is a row's own affair
-// and a state row stays in one thread.  Operands are 128-byte swizzled tiles;
+// Thread (warp w, lane l) owns row 32 (w % 4) + l of every accumulator and the columns
+// of part w / 4, so a mask and a decay are a row's own affair and a state's row stays in four
+// threads.  With 256 threads, half a row each, the steps between the products waited longer for
+// tensor memory (2 x 32 x 8192 x 128 with per-head decays: grad_q 211 us against 188,
+// grad_kv 257 against 228).  Operands are 128-byte swizzled tiles;
 // each is read in both orientations (K-major and MN-major), none is transposed.
 //
 // NM = 3: the state and the decayed operand as three bf16 planes, which hold all
@@ -36,10 +38,11 @@ namespace {
 using tc::Ctl;
 
 constexpr int CT = 128;       // tokens of a chunk
-constexpr int kThreads = 256;
+// Parts of a row: 32 tokens' scores, D / PARTS columns.
+constexpr int PARTS = 4, kThreads = CT * PARTS;
 // The thread that issues products and copies waits when their queue is full: it is one of a warp
 // that has no scores to work on, all of its columns lying outside the mask.
-constexpr int kLeaderQ = 128, kLeaderKV = 96;
+constexpr int kLeaderQ = 384, kLeaderKV = 96;
 constexpr uint32_t HI = smem_desc_sw128_hi(1024);
 static_assert(kThreads / 32 == kShares, "a share for each warp");
 
@@ -76,7 +79,7 @@ struct Block {
   Ctl *ctl;
   unsigned int *err;
   uint32_t tmem;
-  int warp, lane, quarter, half, row;
+  int warp, lane, quarter, part, row;
   bool failed;
 
   __device__ __forceinline__ void start(unsigned char *s, uint32_t off_bar, uint32_t columns,
@@ -89,7 +92,7 @@ struct Block {
     ctl = reinterpret_cast<Ctl *>(s + off_bar + 64);
     err = error;
     warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    quarter = warp % 4, half = warp / 4, row = quarter * 32 + lane;
+    quarter = warp % 4, part = warp / 4, row = quarter * 32 + lane;
     failed = false;
     if (threadIdx.x == 0) {
       mbar_init(&full[0], 1);
@@ -126,6 +129,21 @@ struct Block {
   // TMEM address of column `col` in this warp's lanes.
   __device__ __forceinline__ uint32_t at(uint32_t col) const {
     return tmem + col + ((uint32_t)quarter << 21);
+  }
+  // Two sums of each part of a row, by tensor memory's columns from `col` on: left by the parts
+  // behind the first, and added to the first one's (a barrier later).
+  __device__ __forceinline__ void leave(uint32_t col, float x, float y) const {
+    if (part) tmem_st2(at(col + (part - 1) * 2), __float_as_uint(x), __float_as_uint(y));
+    tmem_st_wait();
+  }
+  __device__ __forceinline__ void gather(uint32_t col, float &x, float &y) const {
+    uint32_t r[8];
+    tc_fence_after();
+    tmem_ld8(at(col), r);
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < PARTS - 1; ++i)
+      x += __uint_as_float(r[2 * i]), y += __uint_as_float(r[2 * i + 1]);
   }
   // 16 bytes at column `col` (a multiple of 8) of this thread's row in a tile of tokens.
   __device__ __forceinline__ uint4 *cell(uint32_t tile, int col) const {
@@ -230,19 +248,15 @@ __device__ __forceinline__ void decayed_rows(const unsigned char *tile, unsigned
   }
 }
 
-__device__ __forceinline__ void as_floats(const uint32_t (&r)[32], float (&f)[32]) {
-#pragma unroll
-  for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(r[e]);
-}
-__device__ __forceinline__ void load_32(const Block &b, uint32_t col, float (&f)[32]) {
-  uint32_t r[32];
-  tmem_ld32(b.at(col), r);
+__device__ __forceinline__ void load_16(const Block &b, uint32_t col, float (&f)[16]) {
+  uint32_t r[16];
+  tmem_ld16(b.at(col), r);
   tmem_ld_wait();
-  as_floats(r, f);
+#pragma unroll
+  for (int e = 0; e < 16; ++e) f[e] = __uint_as_float(r[e]);
 }
-
 // ---------------------------------------------------------------- decays
-// A chunk's log2 decays on their way to shared memory: the threads of half 0 hold a
+// A chunk's log2 decays on their way to shared memory: the threads of part 0 hold a
 // token each, loaded a chunk ahead.  A decay is the product of a factor of the row and one of the
 // column, e^(L_j - E) e^(E - L_i) with E at the end of a block of 32 tokens between them, so
 // both are at most 1.  Pairs of one block take their own block's end (dq) or the
@@ -253,7 +267,7 @@ struct TokenDecay {
 
   __device__ __forceinline__ void load(const ChunkBwd &p, const Block &b, int seq, int c) {
     own = before = make_float2(0.f, 0.f);
-    if (b.half || p.decay_kind == LA_DECAY_NONE) return;
+    if (b.part || p.decay_kind == LA_DECAY_NONE) return;
     const float2 *lam = p.lam + ((size_t)seq * p.chunks + c) * CT;
     own = lam[b.row];
     if (b.quarter) before = lam[b.quarter * 32 - 1];
@@ -273,39 +287,48 @@ struct TokenDecay {
   }
 };
 
-__device__ __forceinline__ void decay_products(const float *fac, float mine, float (&d)[32]) {
-#pragma unroll
-  for (int e = 0; e < 32; e += 4) {
-    const float4 x = *reinterpret_cast<const float4 *>(fac + e);
-    d[e] = mine * x.x, d[e + 1] = mine * x.y, d[e + 2] = mine * x.z, d[e + 3] = mine * x.w;
-  }
-}
+// The decays of a thread's row and a column block's 32 tokens, by its columns.
+struct RowDecay {
+  const float *factors;  // of the columns, or null: an exponential for each pair
+  float mine;
+  const float2 *lam;
+  float2 own;
+  bool later;
 
-// The decays of this thread's row (a token of block b.quarter) and column block `block`.
-// LATER: the columns come after the row (else before it); anything outside the mask.
-template <bool LATER>
-__device__ __forceinline__ void decay_factors(const Block &b, int block, const float2 *lam,
-                                              const float *fac, float2 own, float (&d)[32]) {
-  const bool diagonal = block == b.quarter;
-  if (!diagonal || b.narrow[block]) {
+  // LATER: the columns come after the row (else before it); anything outside the mask.
+  template <bool LATER>
+  __device__ __forceinline__ void start(const Block &b, int block, const float2 *lams,
+                                        const float *fac, float2 o) {
+    factors = nullptr, mine = 0.f, own = o, later = LATER;
+    lam = lams + block * 32;
+    if (block == b.quarter && !b.narrow[block]) return;
     float2 at = make_float2(0.f, 0.f);
-    if (!LATER || block) at = lam[LATER ? block * 32 - 1 : block * 32 + 31];
-    decay_products(fac + block * 32, LATER ? decay_between(at, own) : decay_between(own, at), d);
-  } else {
+    if (!LATER || block) at = lams[LATER ? block * 32 - 1 : block * 32 + 31];
+    mine = LATER ? decay_between(at, own) : decay_between(own, at);
+    factors = fac + block * 32;
+  }
+  template <int W> __device__ __forceinline__ void get(int at, float (&d)[W]) const {
+    if (factors) {
 #pragma unroll
-    for (int e = 0; e < 32; ++e) {
-      const float2 other = lam[block * 32 + e];
-      const float x = LATER ? (other.x - own.x) + (other.y - own.y)
-                            : (own.x - other.x) + (own.y - other.y);
-      d[e] = ex2_approx(x);
+      for (int e = 0; e < W; e += 4) {
+        const float4 x = *reinterpret_cast<const float4 *>(factors + at + e);
+        d[e] = mine * x.x, d[e + 1] = mine * x.y, d[e + 2] = mine * x.z, d[e + 3] = mine * x.w;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < W; ++e) {
+        const float2 other = lam[at + e];
+        const float x = (own.x - other.x) + (own.y - other.y);
+        d[e] = ex2_approx(later ? -x : x);
+      }
     }
   }
-}
+};
 
 // ---------------------------------------------------------------- the state
-// A thread's part of the state: row `row` (rows < D), columns half D/2 ..
+// A thread's part of the state: row `row` (rows < D), N columns from N part on.
 template <int D, int NM> struct StateRow {
-  static constexpr int N = D / 2;
+  static constexpr int N = D / PARTS;
   float c[N];
 
   __device__ __forceinline__ void load(const float *src, const Block &b) {
@@ -313,7 +336,7 @@ template <int D, int NM> struct StateRow {
     for (int i = 0; i < N; i += 4) {
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
       if (src && b.row < D)
-        x = *reinterpret_cast<const float4 *>(src + (size_t)b.row * D + b.half * N + i);
+        x = *reinterpret_cast<const float4 *>(src + (size_t)b.row * D + b.part * N + i);
       c[i] = x.x, c[i + 1] = x.y, c[i + 2] = x.z, c[i + 3] = x.w;
     }
   }
@@ -321,7 +344,7 @@ template <int D, int NM> struct StateRow {
     if (b.row >= D) return;
 #pragma unroll
     for (int i = 0; i < N; i += 4)
-      *reinterpret_cast<float4 *>(dst + (size_t)b.row * D + b.half * N + i) =
+      *reinterpret_cast<float4 *>(dst + (size_t)b.row * D + b.part * N + i) =
           make_float4(c[i], c[i + 1], c[i + 2], c[i + 3]);
   }
   // As planes of operand tiles [D][D] (64-column boxes).
@@ -329,7 +352,7 @@ template <int D, int NM> struct StateRow {
     if (b.row >= D) return;
 #pragma unroll
     for (int i = 0; i < N; i += 8) {
-      const int col = b.half * N + i;
+      const int col = b.part * N + i;
       uint32_t w[NM][4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) split<NM>(c[i + 2 * e], c[i + 2 * e + 1], &w[0][e], 4);
@@ -345,19 +368,19 @@ template <int D, int NM> struct StateRow {
   // off; formed chunk by chunk and added here, the cuts do not add up.
   __device__ __forceinline__ void update(const Block &b, uint32_t col, float2 all) {
     if (b.quarter * 32 >= D) return;
-    uint32_t r[N / 32][32];
-#pragma unroll
-    for (int i = 0; i < N / 32; ++i) tmem_ld32(b.at(col + b.half * N + i * 32), r[i]);
+    uint32_t r[N];
+    if constexpr (N == 32) tmem_ld32(b.at(col + b.part * N), r);
+    else tmem_ld16(b.at(col + b.part * N), r);
     tmem_ld_wait();
 #pragma unroll
-    for (int i = 0; i < N; ++i) c[i] = decayed_sum(all, c[i], __uint_as_float(r[i / 32][i % 32]));
+    for (int i = 0; i < N; ++i) c[i] = decayed_sum(all, c[i], __uint_as_float(r[i]));
   }
   // The state as it lies in a block's threads, and its product with such a one.
   __device__ __forceinline__ void keep(float *dst, const Block &b) const {
     if (b.row >= D) return;
 #pragma unroll
     for (int i = 0; i < N; i += 4)
-      reinterpret_cast<float4 *>(dst)[i / 4 * (2 * D) + b.half * D + b.row] =
+      reinterpret_cast<float4 *>(dst)[i / 4 * (PARTS * D) + b.part * D + b.row] =
           make_float4(c[i], c[i + 1], c[i + 2], c[i + 3]);
   }
   __device__ __forceinline__ float dot_kept(const float *src, const Block &b) const {
@@ -366,7 +389,7 @@ template <int D, int NM> struct StateRow {
 #pragma unroll
       for (int i = 0; i < N; i += 4) {
         const float4 x =
-            reinterpret_cast<const float4 *>(src)[i / 4 * (2 * D) + b.half * D + b.row];
+            reinterpret_cast<const float4 *>(src)[i / 4 * (PARTS * D) + b.part * D + b.row];
         s = fmaf(x.x, c[i], fmaf(x.y, c[i + 1], fmaf(x.z, c[i + 2], fmaf(x.w, c[i + 3], s))));
       }
     }
@@ -378,7 +401,7 @@ template <int D, int NM> struct StateRow {
 #pragma unroll
       for (int i = 0; i < N; i += 4) {
         const float4 x =
-            *reinterpret_cast<const float4 *>(src + (size_t)b.row * D + b.half * N + i);
+            *reinterpret_cast<const float4 *>(src + (size_t)b.row * D + b.part * N + i);
         s = fmaf(x.x, c[i], fmaf(x.y, c[i + 1], fmaf(x.z, c[i + 2], fmaf(x.w, c[i + 3], s))));
       }
     }
@@ -445,15 +468,15 @@ segment_share_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, uns
   StateRow<D, NM> state;
   state.load(nullptr, b);
   double total = 0.0;
-  // each thread of half 0: its token's log decay and the chunk's, a chunk ahead
+  // each thread of part 0: its token's log decay and the chunk's, a chunk ahead
   float2 own = make_float2(0.f, 0.f), end = own;
   auto fetch = [&](int i) {
-    if (!DECAY || b.half) return;
+    if (!DECAY || b.part) return;
     const float2 *lam = p.lam + ((size_t)seq * p.chunks + chunk(i)) * CT;
     own = lam[b.row], end = lam[CT - 1];
   };
   auto put = [&](int i) {
-    if (!DECAY || b.half) return;
+    if (!DECAY || b.part) return;
     weights[(i & 1) * CT + b.row] = back ? ex2_approx(own.x) : decay_between(end, own);
     if (b.row == 0) ends[i & 1] = end;
   };
@@ -552,17 +575,18 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
   constexpr uint32_t id_in = idesc_bf16_f32(128, D, false, false);
   constexpr uint32_t id_out = idesc_bf16_f32(128, D, false, true);
   constexpr uint32_t id_kv = idesc_bf16_f32(128, D, true, true);
-  constexpr int N = D / 2;
+  constexpr int N = D / PARTS;
   // NM = 3: Q K^T as well, in the scores' share's place or behind everything.
   constexpr uint32_t T_P = D == 128 ? T_OUT : 384;
-  static_assert(T_A + 64 <= COLUMNS, "tensor memory");
+  // the parts' sums of a row
+  constexpr uint32_t T_MORE = T_A + 64;
+  static_assert(T_MORE + 8 <= (D == 128 ? COLUMNS : T_P), "tensor memory");
   extern __shared__ __align__(1024) unsigned char smem[];
   Block b;
   b.start(smem, SM::OFF_BAR, COLUMNS, err);
   float2 *lam = reinterpret_cast<float2 *>(smem + SM::OFF_LAM);
   float *fac = reinterpret_cast<float *>(smem + SM::OFF_FAC);
-  float *sums = reinterpret_cast<float *>(smem + SM::OFF_MORE);  // [2][CT] half 1's sums
-  float *inside = sums + CT;  // before that: factors of pairs of one block
+  float *inside = reinterpret_cast<float *>(smem + SM::OFF_MORE);  // factors of pairs of one block
   const int seq = blockIdx.x / p.segments, seg = blockIdx.x % p.segments;
   const int c0 = seg * p.per, c1 = min(c0 + p.per, p.chunks);
   const size_t es = (size_t)D * D;
@@ -603,7 +627,7 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
     const int t0 = c * CT, t = t0 + b.row;
     const uint32_t phase = (c - c0) & 1;
     const bool more = c + 1 < c1;
-    if (decays && b.half == 0) {
+    if (decays && b.part == 0) {
       next.put<false>(b, lam, fac);
       if (NM == 3) inside[b.row] = decay_between(next.before, next.own);
       if (more) next.load(p, b, seq, c + 1);
@@ -636,40 +660,45 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
     // the scores as operand: row j, tokens i <= j
     const float2 before = DECAY && b.quarter ? lam[b.quarter * 32 - 1] : make_float2(0.f, 0.f);
     float pairs = 0.f, pairs_in = 0.f;  // with tokens of the blocks before, of this block
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int block = b.half * 2 + x;
+    {
+      const int block = b.part;
       const bool diagonal = block == b.quarter;
       uint32_t w[16];
       if (block > b.quarter) {  // all behind the warp's rows
 #pragma unroll
         for (int e = 0; e < 16; ++e) w[e] = 0;
       } else {
-        float f[32], d[32];
-        load_32(b, T_S + block * 32, f);
+        RowDecay decay;
         if (DECAY) {
-          if (NM == 3 && diagonal && b.narrow[block])  // grad_kv_tc_kernel's factors: see rc
-            decay_products(inside + block * 32, decay_between(own, before), d);
-          else
-            decay_factors<false>(b, block, lam, fac, own, d);
-        }
-        if (NM == 3 && DECAY) {
-          float g[32], s[4] = {0.f, 0.f, 0.f, 0.f};
-          load_32(b, T_P + block * 32, g);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const float pair = g[e] * d[e] * f[e];
-            s[e % 4] += !diagonal || e < b.lane ? pair : 0.f;
+          decay.start<false>(b, block, lam, fac, own);
+          if (NM == 3 && diagonal && b.narrow[block]) {  // grad_kv_tc_kernel's factors: see rc
+            decay.factors = inside + block * 32;
+            decay.mine = decay_between(own, before);
           }
-          (diagonal ? pairs_in : pairs) += (s[0] + s[1]) + (s[2] + s[3]);
         }
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          if (DECAY) f[e] *= d[e];
-          if (diagonal) f[e] = e <= b.lane ? f[e] : 0.f;
-        }
+        for (int y = 0; y < 32; y += 16) {
+          float f[16], d[16];
+          load_16(b, T_S + block * 32 + y, f);
+          if (DECAY) decay.get(y, d);
+          if (NM == 3 && DECAY) {
+            float g[16], s[2] = {0.f, 0.f};
+            load_16(b, T_P + block * 32 + y, g);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) w[e] = la::pack_bf16(f[2 * e], f[2 * e + 1]);
+            for (int e = 0; e < 16; ++e) {
+              const float pair = g[e] * d[e] * f[e];
+              s[e % 2] += !diagonal || y + e < b.lane ? pair : 0.f;
+            }
+            (diagonal ? pairs_in : pairs) += s[0] + s[1];
+          }
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            if (DECAY) f[e] *= d[e];
+            if (diagonal) f[e] = y + e <= b.lane ? f[e] : 0.f;
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) w[y / 2 + e] = la::pack_bf16(f[2 * e], f[2 * e + 1]);
+        }
       }
       tmem_st16(b.at(T_A + block * 16), w);
     }
@@ -710,22 +739,22 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
     const float head = ex2_approx(own.x);
     float dot = 0.f;
 #pragma unroll
-    for (int x = 0; x < N; x += 32) {
-      float f[32], g[32];
-      load_32(b, T_IN + b.half * N + x, f);
-      load_32(b, T_OUT + b.half * N + x, g);
+    for (int x = 0; x < N; x += 16) {
+      float f[16], g[16];
+      load_16(b, T_IN + b.part * N + x, f);
+      load_16(b, T_OUT + b.part * N + x, g);
 #pragma unroll
-      for (int e = 0; e < 32; ++e) f[e] *= head;
+      for (int e = 0; e < 16; ++e) f[e] *= head;
 #pragma unroll
-      for (int e = 0; e < 32; ++e) g[e] += f[e];
+      for (int e = 0; e < 16; ++e) g[e] += f[e];
 #pragma unroll
-      for (int e = 0; e < 32; e += 8) {
-        uint4 *cell = b.cell(TQ, b.half * N + x + e);
+      for (int e = 0; e < 16; e += 8) {
+        uint4 *cell = b.cell(TQ, b.part * N + x + e);
         if (NM == 3) dot = dot_8(*cell, f + e, dot);
         stage_8<PHI>(cell, cell, g + e);
       }
     }
-    if (NM == 3 && b.half == 1) sums[b.row] = dot, inside[b.row] = pairs;
+    if (NM == 3 && DECAY) b.leave(T_MORE, dot, pairs);
     fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
@@ -733,13 +762,11 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
       store_tile_tma<D>(b, TQ, &maps.dq, t0, seq);
       tma_store_commit();
     }
+    if (NM == 3 && DECAY && b.part == 0) b.gather(T_MORE, dot, pairs);
     if (NM == 3 && p.rq && t < p.L) {
       const size_t to = (size_t)seq * p.L + t;
-      if (b.half == 0) {
-        p.rq[to] = dot + sums[b.row];
-        p.cs[to] = pairs + inside[b.row];
-      }
-      if (b.half == b.quarter / 2) p.rc[to] = pairs_in;  // the half that has the diagonal
+      if (b.part == 0) p.rq[to] = dot, p.cs[to] = pairs;
+      if (b.part == b.quarter) p.rc[to] = pairs_in;  // who has the diagonal
     }
     if (more) {
       b.wait_mma(3, phase);
@@ -764,7 +791,8 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
   if (NM == 3 && p.rq) {
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) around += __shfl_xor_sync(0xffffffffu, around, off);
-    __syncthreads();  // sums are read
+    float *sums = inside;
+    __syncthreads();
     if (b.lane == 0) sums[b.warp] = around;
     __syncthreads();
     if (threadIdx.x == kLeaderQ) {
@@ -800,13 +828,12 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
   constexpr uint32_t id_in = idesc_bf16_f32(128, D, false, false);
   constexpr uint32_t id_out = idesc_bf16_f32(128, D, false, true);
   constexpr uint32_t id_kv = idesc_bf16_f32(128, D, true, true);
-  constexpr int N = D / 2;
+  constexpr int N = D / PARTS;
   extern __shared__ __align__(1024) unsigned char smem[];
   Block b;
   b.start(smem, SM::OFF_BAR, COLUMNS, err);
   float2 *lam = reinterpret_cast<float2 *>(smem + SM::OFF_LAM);
   float *fac = reinterpret_cast<float *>(smem + SM::OFF_FAC);
-  float *sums = reinterpret_cast<float *>(smem + SM::OFF_MORE);  // [2][CT] half 1's sums
   const int seq = blockIdx.x / p.segments, seg = blockIdx.x % p.segments;
   const int c0 = seg * p.per, c1 = min(c0 + p.per, p.chunks), n = c1 - c0;
   const size_t es = (size_t)D * D;
@@ -844,7 +871,7 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
     const int c = c1 - 1 - done, t0 = c * CT, t = t0 + b.row;
     const uint32_t phase = done & 1;
     const bool more = done + 1 < n, update = more || (p.dS0 && seg == 0);
-    if (decays && b.half == 0) {
+    if (decays && b.part == 0) {
       next.put<true>(b, lam, fac);
       if (more) next.load(p, b, seq, c - 1);
     }
@@ -878,81 +905,82 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
       float s = state.dot_kept(p.kept + p.keep_slot(seq, c) * es, b);
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+      float *to = p.between + p.keep_slot(seq, c) * kShares;
       if (b.lane == 0)
-        p.between[p.keep_slot(seq, c) * kShares + b.warp] = s * all.x;
+        for (int i = b.warp; i < kShares; i += kThreads / 32)
+          to[i] = i == b.warp ? s * all.x : 0.f;
     }
     b.wait_mma(0, phase);
     // the scores as operands: row i, tokens j >= i
-    uint32_t wp[2][16], wd[2][16];
+    uint32_t wp[16], wd[16];
     float pairs = 0.f, pairs_in = 0.f;  // with tokens of the blocks behind, of this block
+    const int block = b.part;
+    const bool diagonal = block == b.quarter;
+    if (block < b.quarter) {  // all in front of the warp's rows
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int block = b.half * 2 + x;
-      const bool diagonal = block == b.quarter;
-      if (block < b.quarter) {  // all in front of the warp's rows
+      for (int e = 0; e < 16; ++e) wp[e] = wd[e] = 0;
+    } else {
+      RowDecay decay;
+      if (DECAY) decay.start<true>(b, block, lam, fac, own);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) wp[x][e] = wd[x][e] = 0;
-        continue;
-      }
-      float f[32], g[32], d[32];
-      load_32(b, T_P + block * 32, f);
-      load_32(b, T_DP + block * 32, g);
-      if (DECAY) decay_factors<true>(b, block, lam, fac, own, d);
-      if (NM == 3 && DECAY) {
-        float s[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int y = 0; y < 32; y += 16) {
+        float f[16], g[16], d[16];
+        load_16(b, T_P + block * 32 + y, f);
+        load_16(b, T_DP + block * 32 + y, g);
+        if (DECAY) decay.get(y, d);
+        if (NM == 3 && DECAY) {
+          float s[2] = {0.f, 0.f};
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const float pair = f[e] * d[e] * g[e];
-          s[e % 4] += !diagonal || e > b.lane ? pair : 0.f;
+          for (int e = 0; e < 16; ++e) {
+            const float pair = f[e] * d[e] * g[e];
+            s[e % 2] += !diagonal || y + e > b.lane ? pair : 0.f;
+          }
+          (diagonal ? pairs_in : pairs) += s[0] + s[1];
         }
-        (diagonal ? pairs_in : pairs) += (s[0] + s[1]) + (s[2] + s[3]);
-      }
 #pragma unroll
-      for (int e = 0; e < 32; ++e) {
-        if (DECAY) f[e] *= d[e], g[e] *= d[e];
-        if (diagonal) {
-          f[e] = e >= b.lane ? f[e] : 0.f;
-          g[e] = e >= b.lane ? g[e] : 0.f;
+        for (int e = 0; e < 16; ++e) {
+          if (DECAY) f[e] *= d[e], g[e] *= d[e];
+          if (diagonal) {
+            f[e] = y + e >= b.lane ? f[e] : 0.f;
+            g[e] = y + e >= b.lane ? g[e] : 0.f;
+          }
         }
-      }
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        wp[x][e] = la::pack_bf16(f[2 * e], f[2 * e + 1]);
-        wd[x][e] = la::pack_bf16(g[2 * e], g[2 * e + 1]);
+        for (int e = 0; e < 8; ++e) {
+          wp[y / 2 + e] = la::pack_bf16(f[2 * e], f[2 * e + 1]);
+          wd[y / 2 + e] = la::pack_bf16(g[2 * e], g[2 * e + 1]);
+        }
       }
     }
     tc_fence_before();
     __syncthreads();  // the scores are read: their operands may take their place
     tc_fence_after();
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      tmem_st16(b.at(T_AP + b.half * 32 + x * 16), wp[x]);
-      tmem_st16(b.at(T_ADP + b.half * 32 + x * 16), wd[x]);
-    }
+    tmem_st16(b.at(T_AP + block * 16), wp);
+    tmem_st16(b.at(T_ADP + block * 16), wd);
     b.wait_mma(1, phase);
     const float tail = decay_between(end, own);
     float dot = 0.f;
     if (decays) {  // the state's share, by each token's decay to the chunk's end
 #pragma unroll
-      for (int x = 0; x < 2 * N; x += 32) {
+      for (int x = 0; x < 2 * N; x += 16) {
         const bool of_k = x >= N;
-        const int col = b.half * N + x % N;
-        uint32_t r[32];
-        float f[32];
-        load_32(b, (of_k ? T_K : T_V) + col, f);
+        const int col = b.part * N + x % N;
+        uint32_t r[16];
+        float f[16];
+        load_16(b, (of_k ? T_K : T_V) + col, f);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
+        for (int e = 0; e < 16; ++e) {
           f[e] *= tail;
           r[e] = __float_as_uint(f[e]);
         }
-        tmem_st32(b.at((of_k ? T_K : T_V) + col), r);
+        tmem_st16(b.at((of_k ? T_K : T_V) + col), r);
         if (NM == 3 && of_k) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) dot = dot_8(*b.cell(TK, col + e), f + e, dot);
+          for (int e = 0; e < 16; e += 8) dot = dot_8(*b.cell(TK, col + e), f + e, dot);
         }
       }
     }
-    if (NM == 3 && b.half == 1) sums[b.row] = dot, sums[CT + b.row] = pairs;
+    if (NM == 3 && DECAY) b.leave(T_U, dot, pairs);
     tmem_st_wait();
     fence_proxy_async_smem();
     tc_fence_before();
@@ -969,20 +997,19 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
         if (EARLY_K) load_k(c - 1);
       }
     }
+    if (NM == 3 && DECAY && b.part == 0) b.gather(T_U, dot, pairs);
     if (NM == 3 && p.rk && t < p.L) {
       const size_t to = (size_t)seq * p.L + t;
-      if (b.half == 0) {
-        p.rk[to] = dot + sums[b.row];
-        p.rs[to] = pairs + sums[CT + b.row];
-      }
+      if (b.part == 0) p.rk[to] = dot, p.rs[to] = pairs;
       // A block's pairs enter rc as their later token's less as their earlier one's, and
       // cancel in sums: both kernels form them from the same factors.
-      if (b.half == b.quarter / 2) p.rc[to] -= pairs_in;
+      if (diagonal) p.rc[to] -= pairs_in;
     }
     if (update && decays) {
       decayed_rows<D, NM, CT>(smem + TQ, smem, 0, [&](int i) { return ex2_approx(lam[i].x); });
       fence_proxy_async_smem();
     }
+    tc_fence_before();
     if (decays) __syncthreads();
     if (threadIdx.x == kLeaderKV && update) {  // the state's update, while dk and dv leave
       tc_fence_after();
@@ -1000,15 +1027,15 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
     if (threadIdx.x == kLeaderKV && more && DECAY) load_q(c - 1);
     __syncwarp();
 #pragma unroll
-    for (int x = 0; x < N; x += 32) {
-      const int col = b.half * N + x;
-      float f[32];
-      load_32(b, T_V + col, f);
+    for (int x = 0; x < N; x += 16) {
+      const int col = b.part * N + x;
+      float f[16];
+      load_16(b, T_V + col, f);
 #pragma unroll
-      for (int e = 0; e < 32; e += 8) stage_8<false>(b.cell(TDV, col + e), nullptr, f + e);
-      load_32(b, T_K + col, f);
+      for (int e = 0; e < 16; e += 8) stage_8<false>(b.cell(TDV, col + e), nullptr, f + e);
+      load_16(b, T_K + col, f);
 #pragma unroll
-      for (int e = 0; e < 32; e += 8)
+      for (int e = 0; e < 16; e += 8)
         stage_8<PHI>(b.cell(TDK, col + e), b.cell(TK, col + e), f + e);
     }
     fence_proxy_async_smem();
