@@ -12,6 +12,9 @@
 // in one pass over dy, r, dr and x.  The means of x, r and g belong to layer norm
 // alone.  r is read as the forward pass stored it.  ds and dp are alpha p and alpha s times
 // one sum over rows, of e n_x (x itself without a post norm).
+//
+// The bytes bound it: 16384 x 4096, fp32 residual, post norm and scale, takes 201 us, 6.0 TB/s
+// (sums of their own for ds and dp, when it took 236: 278).
 #include <cstdint>
 
 #include "la_block_norm_bwd.cuh"
