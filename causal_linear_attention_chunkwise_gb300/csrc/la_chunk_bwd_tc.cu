@@ -25,6 +25,11 @@
 //
 // NM = 3: the state and the decayed operand as three bf16 planes, which hold all
 // of an fp32 value's bits, for the fp32 outputs (ddecay, dS0); one product each.
+//
+// What bounds it at D = 128, NM = 3: shared memory.  A chunk of grad_kv moves some 1.1 MB through
+// it (640 KB of them operands of the products, each of which takes its 512 clocks' whole
+// bandwidth), 9000 clocks of 13200; loads issued earlier, or dv's share scaled while dk's products
+// run, change nothing (545 us for 1 x 16 x 32768 x 128 gates with either, both or none).
 #include <cuda.h>
 
 #include <algorithm>
@@ -560,14 +565,19 @@ segment_share_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, uns
   b.finish(COLUMNS);
 }
 
+// Sets of input tiles of the walks below: with two, which D = 64 has room for, a chunk's tiles are
+// loaded while the last chunk is worked on (4 x 16 x 4096 x 64 elu1: grad_q 45 us, grad_kv 58; with
+// one set 53 and 70).
+template <int D> constexpr int kStages = D == 64 ? 2 : 1;
+
 // ---------------------------------------------------------------- dq
 template <int D, int NM, bool PHI, bool DECAY>
 __global__ void __launch_bounds__(kThreads, 1)
 grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned int *err) {
   // The fourth tile: q, where it is needed (for ddecay, for phi's derivative), then dq on its way out.
-  using SM = Smem<D, NM, 4, 1>;
+  using SM = Smem<D, NM, 4, kStages<D>>;
   using ST = StateTile<D>;
-  constexpr bool HAS_Q = NM == 3 || PHI;
+  constexpr bool TWO = kStages<D> == 2, HAS_Q = NM == 3 || PHI;
   // Tensor memory: dO V^T, the state's share, the scores' share, the scores as operand; the
   // state's update takes the place of dO V^T.
   constexpr uint32_t T_S = 0, T_IN = 128, T_OUT = 128 + D, T_A = 128 + 2 * D, COLUMNS = 512;
@@ -591,18 +601,23 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
   const int c0 = seg * p.per, c1 = min(c0 + p.per, p.chunks);
   const size_t es = (size_t)D * D;
   constexpr bool decays = DECAY;
-  constexpr uint32_t TK = SM::OFF_TILES, TV = TK + SM::TILE, TD = TV + SM::TILE,
-                     TQ = TD + SM::TILE;
-  // A chunk's tiles, each as soon as the last one's place is free; into L2 a chunk earlier:
-  // all blocks load at about the same time, and DRAM would make them wait.
-  auto load_dO = [&](int c) {
-    mbar_arrive_expect_tx(&b.full[0], (HAS_Q ? 4 : 3) * SM::TILE);
-    load_tile_tma<D>(b, TD, &maps.dO, &b.full[0], c * CT, seq);
+  auto stage = [&](int c) { return TWO ? (c - c0) & 1 : 0; };
+  auto tile = [&](int c, int i) {  // k, v, dO, q
+    return SM::OFF_TILES + stage(c) * SM::STAGE + i * SM::TILE;
   };
-  auto load_k = [&](int c) { load_tile_tma<D>(b, TK, &maps.k, &b.full[0], c * CT, seq); };
+  // A chunk's tiles: all into the set that the last chunk had, or, with one set, each as soon as
+  // the last one's place is free; then into L2 a chunk earlier: all blocks load at about
+  // the same time, and DRAM would make them wait.
+  auto load_dO = [&](int c) {
+    mbar_arrive_expect_tx(&b.full[stage(c)], (HAS_Q ? 4 : 3) * SM::TILE);
+    load_tile_tma<D>(b, tile(c, 2), &maps.dO, &b.full[stage(c)], c * CT, seq);
+  };
+  auto load_k = [&](int c) {
+    load_tile_tma<D>(b, tile(c, 0), &maps.k, &b.full[stage(c)], c * CT, seq);
+  };
   auto load_vq = [&](int c) {
-    load_tile_tma<D>(b, TV, &maps.v, &b.full[0], c * CT, seq);
-    if (HAS_Q) load_tile_tma<D>(b, TQ, &maps.q, &b.full[0], c * CT, seq);
+    load_tile_tma<D>(b, tile(c, 1), &maps.v, &b.full[stage(c)], c * CT, seq);
+    if (HAS_Q) load_tile_tma<D>(b, tile(c, 3), &maps.q, &b.full[stage(c)], c * CT, seq);
   };
   auto prefetch = [&](int c) {
     prefetch_tile<D>(&maps.dO, c * CT, seq);
@@ -626,13 +641,14 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
   for (; c < c1; ++c) {
     const int t0 = c * CT, t = t0 + b.row;
     const uint32_t phase = (c - c0) & 1;
+    const uint32_t TK = tile(c, 0), TV = tile(c, 1), TD = tile(c, 2), TQ = tile(c, 3);
     const bool more = c + 1 < c1;
     if (decays && b.part == 0) {
       next.put<false>(b, lam, fac);
       if (NM == 3) inside[b.row] = decay_between(next.before, next.own);
       if (more) next.load(p, b, seq, c + 1);
     }
-    b.wait_full(0, phase);
+    b.wait_full(stage(c), TWO ? (c - c0) >> 1 & 1 : phase);
     if (PHI) map_tile_tc<D>(smem + TK, smem + TK, p.L - t0);
     fence_proxy_async_smem();
     tc_fence_before();
@@ -650,7 +666,14 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
         product<D>(b.tmem + T_IN, a, along_row<ST::BOX>(b.base + m * ST::PLANE), id_in,
                    m < NM - 1);
       mma_commit(&b.mma[1]);
-      if (more) prefetch(c + 1);
+      if (more && TWO) {
+        tma_store_wait_read_all();  // the last chunk's dq
+        load_dO(c + 1);
+        load_k(c + 1);
+        load_vq(c + 1);
+      } else if (more) {
+        prefetch(c + 1);
+      }
     }
     const float2 own = decays ? lam[b.row] : make_float2(0.f, 0.f);
     const float2 end = decays ? lam[CT - 1] : make_float2(0.f, 0.f);
@@ -712,7 +735,7 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
       mma_commit(&b.mma[2]);
     }
     b.wait_mma(1, phase);  // the state's planes and dO are read
-    if (threadIdx.x == kLeaderQ && more) load_dO(c + 1);
+    if (threadIdx.x == kLeaderQ && more && !TWO) load_dO(c + 1);
     __syncwarp();
     if (more) {
       if (decays) {
@@ -734,7 +757,7 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
       }
     }
     b.wait_mma(2, phase);
-    if (threadIdx.x == kLeaderQ && more && DECAY) load_k(c + 1);
+    if (threadIdx.x == kLeaderQ && more && DECAY && !TWO) load_k(c + 1);
     __syncwarp();
     const float head = ex2_approx(own.x);
     float dot = 0.f;
@@ -770,7 +793,7 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
     }
     if (more) {
       b.wait_mma(3, phase);
-      if (threadIdx.x == kLeaderQ) {
+      if (threadIdx.x == kLeaderQ && !TWO) {
         tma_store_wait_read_all();  // the fourth tile
         if (!DECAY) load_k(c + 1);
         load_vq(c + 1);
@@ -785,7 +808,7 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
     }
   }
   if (threadIdx.x == kLeaderQ) {
-    if (c < c1) tc::drain_wait(&b.full[0], (c - c0) & 1);
+    if (c < c1) tc::drain_wait(&b.full[stage(c)], (TWO ? (c - c0) >> 1 : c - c0) & 1);
     tma_store_wait_all();
   }
   if (NM == 3 && p.rq) {
@@ -809,7 +832,7 @@ template <int D, int NM, bool PHI> constexpr bool kv_own_tiles() {
   return D == 64 || (NM == 1 && !PHI);
 }
 template <int D, int NM, bool PHI> constexpr int kv_tiles() {
-  return 4 + PHI + (kv_own_tiles<D, NM, PHI>() ? 2 : 0);
+  return 4 * kStages<D> + PHI + (kv_own_tiles<D, NM, PHI>() ? 2 : 0);
 }
 template <int D, int NM, bool PHI, bool DECAY>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -819,7 +842,7 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
   // late (through the state's planes instead they kept these waiting: 256 us against 238).
   using SM = Smem<D, NM, kv_tiles<D, NM, PHI>(), 1>;
   using ST = StateTile<D>;
-  constexpr bool OWN = kv_own_tiles<D, NM, PHI>(), EARLY_K = OWN && !PHI;
+  constexpr bool TWO = kStages<D> == 2, OWN = kv_own_tiles<D, NM, PHI>(), EARLY_K = OWN && !PHI;
   // Tensor memory: K Q^T and V dO^T, dv, dk.  When the scores have been read their operands
   // take columns 0..63 and 192..255, the state's update those between.
   constexpr uint32_t T_P = 0, T_DP = 128, T_V = 256, T_K = 256 + D, COLUMNS = 512;
@@ -838,15 +861,20 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
   const int c0 = seg * p.per, c1 = min(c0 + p.per, p.chunks), n = c1 - c0;
   const size_t es = (size_t)D * D;
   constexpr bool decays = DECAY;
-  constexpr uint32_t TQ = SM::OFF_TILES, TK = TQ + SM::TILE, TV = TK + SM::TILE,
-                     TD = TV + SM::TILE, TKP = PHI ? TD + SM::TILE : TK;
-  constexpr uint32_t OUT = TD + (PHI ? 2 : 1) * SM::TILE;
-  constexpr uint32_t TDV = OWN ? OUT : TV, TDK = OWN ? OUT + SM::TILE : TK;
-  auto arm = [&] { mbar_arrive_expect_tx(&b.full[0], 4 * SM::TILE); };
-  auto load_q = [&](int c) { load_tile_tma<D>(b, TQ, &maps.q, &b.full[0], c * CT, seq); };
-  auto load_k = [&](int c) { load_tile_tma<D>(b, TK, &maps.k, &b.full[0], c * CT, seq); };
-  auto load_v = [&](int c) { load_tile_tma<D>(b, TV, &maps.v, &b.full[0], c * CT, seq); };
-  auto load_dO = [&](int c) { load_tile_tma<D>(b, TD, &maps.dO, &b.full[0], c * CT, seq); };
+  constexpr uint32_t MORE = SM::OFF_TILES + 4 * kStages<D> * SM::TILE;
+  constexpr uint32_t OUT = MORE + PHI * SM::TILE;
+  auto stage = [&](int c) { return TWO ? (c1 - 1 - c) & 1 : 0; };
+  auto tile = [&](int c, int i) {  // q, k, v, dO
+    return SM::OFF_TILES + (stage(c) * 4 + i) * SM::TILE;
+  };
+  auto load = [&](int c, int i, const CUtensorMap *map) {
+    load_tile_tma<D>(b, tile(c, i), map, &b.full[stage(c)], c * CT, seq);
+  };
+  auto arm = [&](int c) { mbar_arrive_expect_tx(&b.full[stage(c)], 4 * SM::TILE); };
+  auto load_q = [&](int c) { load(c, 0, &maps.q); };
+  auto load_k = [&](int c) { load(c, 1, &maps.k); };
+  auto load_v = [&](int c) { load(c, 2, &maps.v); };
+  auto load_dO = [&](int c) { load(c, 3, &maps.dO); };
   auto prefetch = [&](int c) {
     prefetch_tile<D>(&maps.q, c * CT, seq);
     prefetch_tile<D>(&maps.k, c * CT, seq);
@@ -854,7 +882,7 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
     prefetch_tile<D>(&maps.dO, c * CT, seq);
   };
   if (threadIdx.x == kLeaderKV) {
-    arm();
+    arm(c1 - 1);
     load_q(c1 - 1);
     load_k(c1 - 1);
     load_v(c1 - 1);
@@ -870,12 +898,14 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
   for (; done < n; ++done) {
     const int c = c1 - 1 - done, t0 = c * CT, t = t0 + b.row;
     const uint32_t phase = done & 1;
+    const uint32_t TQ = tile(c, 0), TK = tile(c, 1), TV = tile(c, 2), TD = tile(c, 3);
+    const uint32_t TKP = PHI ? MORE : TK, TDV = OWN ? OUT : TV, TDK = OWN ? OUT + SM::TILE : TK;
     const bool more = done + 1 < n, update = more || (p.dS0 && seg == 0);
     if (decays && b.part == 0) {
       next.put<true>(b, lam, fac);
       if (more) next.load(p, b, seq, c - 1);
     }
-    b.wait_full(0, phase);
+    b.wait_full(stage(c), TWO ? done >> 1 & 1 : phase);
     if (PHI) {
       map_tile_tc<D>(smem + TQ, smem + TQ, p.L - t0);
       map_tile_tc<D>(smem + TK, smem + TKP, p.L - t0);
@@ -896,7 +926,15 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
         product<D>(b.tmem + T_K, av, along_row<ST::BOX>(b.base + m * ST::PLANE), id_in,
                    m < NM - 1);
       mma_commit(&b.mma[1]);
-      if (more) prefetch(c - 1);
+      if (more && TWO) {
+        arm(c - 1);
+        load_q(c - 1);
+        load_k(c - 1);
+        load_v(c - 1);
+        load_dO(c - 1);
+      } else if (more) {
+        prefetch(c - 1);
+      }
     }
     const float2 own = decays ? lam[b.row] : make_float2(0.f, 0.f);
     const float2 end = decays ? lam[CT - 1] : make_float2(0.f, 0.f);
@@ -991,8 +1029,8 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
       product_ta<CT>(b.tmem + T_V, b.tmem + T_AP, dO, id_out, true);
       product_ta<CT>(b.tmem + T_K, b.tmem + T_ADP, q, id_out, true);
       mma_commit(&b.mma[2]);
-      if (more) {
-        arm();
+      if (more && !TWO) {
+        arm(c - 1);
         if (OWN) load_v(c - 1);
         if (EARLY_K) load_k(c - 1);
       }
@@ -1024,7 +1062,7 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
       mma_commit(&b.mma[3]);
     }
     b.wait_mma(2, phase);
-    if (threadIdx.x == kLeaderKV && more && DECAY) load_q(c - 1);
+    if (threadIdx.x == kLeaderKV && more && DECAY && !TWO) load_q(c - 1);
     __syncwarp();
 #pragma unroll
     for (int x = 0; x < N; x += 16) {
@@ -1045,11 +1083,11 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
       store_tile_tma<D>(b, TDV, &maps.dv, t0, seq);
       store_tile_tma<D>(b, TDK, &maps.dk, t0, seq);
       tma_store_commit();
-      if (OWN && !EARLY_K && more) load_k(c - 1);
+      if (OWN && !EARLY_K && more && !TWO) load_k(c - 1);
     }
     if (update) {
       b.wait_mma(3, phase);
-      if (threadIdx.x == kLeaderKV && more) {
+      if (threadIdx.x == kLeaderKV && more && !TWO) {
         if (!DECAY) load_q(c - 1);
         load_dO(c - 1);
         if (!OWN) {
@@ -1066,7 +1104,7 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
   if (done == n) {
     if (p.dS0 && seg == 0) state.store(p.dS0 + (size_t)seq * es, b);
   } else if (threadIdx.x == kLeaderKV) {
-    tc::drain_wait(&b.full[0], done & 1);
+    tc::drain_wait(&b.full[stage(c1 - 1 - done)], (TWO ? done >> 1 : done) & 1);
   }
   if (threadIdx.x == kLeaderKV) tma_store_wait_all();
   b.finish(COLUMNS);
@@ -1075,7 +1113,7 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
 template <int D, int NM, bool PHI, bool DECAY>
 cudaError_t launch_tc(const ChunkBwd &p, int seqs, cudaStream_t stream) {
   using SS = Smem<D, NM, 2, 2>;
-  using SQ = Smem<D, NM, 4, 1>;
+  using SQ = Smem<D, NM, 4, kStages<D>>;
   using SK = Smem<D, NM, kv_tiles<D, NM, PHI>(), 1>;
   Maps m;
   const struct {
