@@ -82,12 +82,13 @@ struct ChunkBwd {
   }
 };
 
-// T: element type; D: padded width (d_k, d_v <= D); C: tokens of a chunk; NI: planes of the
-// inputs; NM: planes of the states and of what enters them.
+// T: element type; D: padded width (d_k, d_v <= D); C: tokens of a chunk; NI: planes of q
+// and k after phi; NM: planes of the states and of what enters them.
 template <typename T_, int D_, int C_, int NI_, int NM_> struct BwdConfig {
   using T = T_;
   static constexpr int D = D_, C = C_, NI = NI_, NM = NM_;
-  static constexpr int NO = NI == 1 ? 1 : 3;   // planes of scores
+  static constexpr int NV = sizeof(T) == 2 ? 1 : NI;  // of v and dO, which are not mapped
+  static constexpr int NO = NI == 1 ? 1 : 3;          // planes of scores
   static constexpr int WARPS = D / 16;         // each owns 16 rows of the state
   static constexpr int ROWS = C / 16;          // groups of 16 tokens
   static constexpr int SPLIT = WARPS / ROWS;   // warps that share a group, by columns
@@ -183,15 +184,16 @@ __device__ __forceinline__ void load_tile(uint32_t tile, const void *src, const 
       float f[8];
       if constexpr (sizeof(T) == 2) load_raw<T, 8>(from).unpack(f);
       else load_raw<T, 4>(from).unpack(f), load_raw<T, 4>(from + 4).unpack(f + 4);
-      uint32_t out[F::NI][4];
+      constexpr int NP = MAP ? F::NI : F::NV;
+      uint32_t out[NP][4];
 #pragma unroll
       for (int e = 0; e < 8; e += 2) {
         const float x = live ? MAP ? feature_map_precise(p.phi, f[e]) : f[e] : 0.f;
         const float y = live ? MAP ? feature_map_precise(p.phi, f[e + 1]) : f[e + 1] : 0.f;
-        split<F::NI>(x, y, &out[0][e / 2], 4);
+        split<NP>(x, y, &out[0][e / 2], 4);
       }
 #pragma unroll
-      for (int n = 0; n < F::NI; ++n)
+      for (int n = 0; n < NP; ++n)
         asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(to + n * F::TILE),
                      "r"(out[n][0]), "r"(out[n][1]), "r"(out[n][2]), "r"(out[n][3])
                      : "memory");
@@ -291,11 +293,11 @@ template <typename F> struct StateRows {
       float sum[2][4] = {}, small[2][4] = {};
 #pragma unroll
       for (int k = 0; k < F::C / 16; ++k) {
-        uint32_t b[F::NI][4];
+        uint32_t b[F::NV][4];
 #pragma unroll
-        for (int i = 0; i < F::NI; ++i)
+        for (int i = 0; i < F::NV; ++i)
           frag_b_t<F::D>(b[i], y + i * F::TILE, n * 8, k * 16, lane);
-        mma_planes<F::NM, F::NI>(sum[0], sum[1], small[0], small[1], w[k], b);
+        mma_planes<F::NM, F::NV>(sum[0], sum[1], small[0], small[1], w[k], b);
       }
 #pragma unroll
       for (int j = 0; j < 2; ++j)
@@ -390,7 +392,7 @@ __device__ __forceinline__ void rows_times_cols(float (&acc)[NT][4], uint32_t x,
 
 // acc[n] += W Y over the chunk's tokens: W scores in accumulators (tiles of 8 tokens), Y's tile
 // [token][.], columns n0 + 8 n.
-template <typename F, int NT, typename Live>
+template <typename F, int NT, int NY, typename Live>
 __device__ __forceinline__ void scores_times_cols(float (&acc)[NT][4],
                                                   const float (&w)[F::C / 8][4], uint32_t y,
                                                   int n0, int lane, Live live) {
@@ -405,13 +407,13 @@ __device__ __forceinline__ void scores_times_cols(float (&acc)[NT][4],
     split<F::NO>(w[2 * j + 1][2], w[2 * j + 1][3], &a[0][3], 4);
 #pragma unroll
     for (int n = 0; n < NT; n += 2) {
-      uint32_t b[F::NI][4];
+      uint32_t b[NY][4];
 #pragma unroll
-      for (int i = 0; i < F::NI; ++i) frag_b_t<F::D>(b[i], y + i * F::TILE, n0 + n * 8, j * 16, lane);
-      mma_planes<F::NO, F::NI>(acc[n], acc[n + 1], small[n], small[n + 1], a, b);
+      for (int i = 0; i < NY; ++i) frag_b_t<F::D>(b[i], y + i * F::TILE, n0 + n * 8, j * 16, lane);
+      mma_planes<F::NO, NY>(acc[n], acc[n + 1], small[n], small[n + 1], a, b);
     }
   }
-  add_small<(F::NO > 1 || F::NI > 1)>(acc, small);
+  add_small<(F::NO > 1 || NY > 1)>(acc, small);
 }
 
 // A warp's 16 x COLS outputs to rows t0 + r0 + .. of a [L, width] tensor; with phi = elu + 1
@@ -482,14 +484,14 @@ template <typename F> constexpr uint32_t bwd_shared_bytes() {
 
 // The segment's own share of S (blockIdx.y = 0: segments 0 .. n - 2) or of G (1: segments 1 .. n - 1).
 template <typename F> constexpr uint32_t share_smem() {
-  return bwd_shared_bytes<F>() + 2 * F::STAGES * F::NI * F::TILE;
+  return bwd_shared_bytes<F>() + F::STAGES * (F::NI + F::NV) * F::TILE;
 }
 template <typename F>
 __global__ void __launch_bounds__(F::THREADS) segment_share_kernel(const ChunkBwd p) {
   extern __shared__ __align__(128) char smem[];
   auto &sh = *reinterpret_cast<BwdShared<F> *>(smem);
   const uint32_t tiles = smem_u32(smem) + bwd_shared_bytes<F>();
-  constexpr uint32_t X = F::NI * F::TILE, STAGE = 2 * X;
+  constexpr uint32_t X = F::NI * F::TILE, STAGE = X + F::NV * F::TILE;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int seq = blockIdx.x / (p.segments - 1), of = blockIdx.x % (p.segments - 1);
   const bool back = blockIdx.y != 0;
@@ -532,7 +534,7 @@ __global__ void __launch_bounds__(F::THREADS) segment_share_kernel(const ChunkBw
 
 // dq: a walk forward over a segment's chunks.
 template <typename F> constexpr uint32_t grad_q_smem() {
-  return bwd_shared_bytes<F>() + 3 * F::STAGES * F::NI * F::TILE + F::NM * F::STATE;
+  return bwd_shared_bytes<F>() + F::STAGES * (F::NI + 2 * F::NV) * F::TILE + F::NM * F::STATE;
 }
 template <typename F>
 __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_q_kernel(const ChunkBwd p) {
@@ -540,7 +542,7 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_q_kernel(const Chu
   auto &sh = *reinterpret_cast<BwdShared<F> *>(smem);
   char *state_tile = smem + bwd_shared_bytes<F>();
   const uint32_t S = smem_u32(state_tile), tiles = S + F::NM * F::STATE;
-  constexpr uint32_t X = F::NI * F::TILE, STAGE = 3 * X;
+  constexpr uint32_t X = F::NI * F::TILE, Y = F::NV * F::TILE, STAGE = X + 2 * Y;
   constexpr int NT = F::COLS / 8;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int group = warp % F::ROWS, part = warp / F::ROWS;
@@ -556,7 +558,7 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_q_kernel(const Chu
     const uint32_t at = tiles + (F::STAGES == 2 ? (c & 1) * STAGE : 0);
     load_tile<F, true>(at, k, p, p.n_k, c * F::C);
     load_tile<F, false>(at + X, v, p, p.n_v, c * F::C);
-    load_tile<F, false>(at + 2 * X, dO, p, p.n_v, c * F::C);
+    load_tile<F, false>(at + X + Y, dO, p, p.n_v, c * F::C);
   };
   StateRows<F> state;
   if (F::STAGES == 2) load(c0);
@@ -565,7 +567,7 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_q_kernel(const Chu
   state.planes(state_tile, warp, lane);
   for (int c = c0; c < c1; ++c) {
     const int t0 = c * F::C;
-    const uint32_t tk = tiles + (F::STAGES == 2 ? (c & 1) * STAGE : 0), tv = tk + X, td = tv + X;
+    const uint32_t tk = tiles + (F::STAGES == 2 ? (c & 1) * STAGE : 0), tv = tk + X, td = tv + Y;
     if (F::STAGES == 1) load(c);
     chunk_decay<F::C>(p, seq, c, sh.decay);
     cp_async_done();
@@ -580,7 +582,7 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_q_kernel(const Chu
     // dO V^T . D: rows j of the group, tokens i <= j
     float w[F::C / 8][4] = {};
     auto live = [&](int j) { return j <= group; };
-    rows_times_rows<F, F::C / 8, F::NI, F::NI>(w, td, F::TILE, r0, tv, F::TILE, 0, lane, live);
+    rows_times_rows<F, F::C / 8, F::NV, F::NV>(w, td, F::TILE, r0, tv, F::TILE, 0, lane, live);
 #pragma unroll
     for (int n = 0; n < F::C / 8; ++n) {
       if (n / 2 > group) continue;
@@ -593,7 +595,7 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_q_kernel(const Chu
       }
     }
     float acc[NT][4] = {};
-    rows_times_rows<F, NT, F::NI, F::NM>(acc, td, F::TILE, r0, S, F::STATE, n0, lane,
+    rows_times_rows<F, NT, F::NV, F::NM>(acc, td, F::TILE, r0, S, F::STATE, n0, lane,
                                          [](int) { return true; });
     const float h0 = sh.decay.head[r0 + lane / 4], h1 = sh.decay.head[r0 + lane / 4 + 8];
 #pragma unroll
@@ -605,7 +607,7 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_q_kernel(const Chu
         sh.rows[part][r0 + lane / 4 + 8] = d.y;
       }
     }
-    scores_times_cols<F, NT>(acc, w, tk, n0, lane, live);
+    scores_times_cols<F, NT, F::NI>(acc, w, tk, n0, lane, live);
     store_rows<F, NT>(acc, static_cast<T *>(p.dq) + ek, q, p, p.n_k, t0 + r0, n0, lane);
     float around = 0.f;
     if (c + 1 < c1) {
@@ -643,7 +645,7 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_q_kernel(const Chu
 
 // dk and dv: a walk backward over a segment's chunks.
 template <typename F> constexpr uint32_t grad_kv_smem() {
-  return bwd_shared_bytes<F>() + 4 * F::STAGES * F::NI * F::TILE + F::NM * F::STATE;
+  return bwd_shared_bytes<F>() + 2 * F::STAGES * (F::NI + F::NV) * F::TILE + F::NM * F::STATE;
 }
 template <typename F>
 __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_kv_kernel(const ChunkBwd p) {
@@ -651,7 +653,7 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_kv_kernel(const Ch
   auto &sh = *reinterpret_cast<BwdShared<F> *>(smem);
   char *state_tile = smem + bwd_shared_bytes<F>();
   const uint32_t G = smem_u32(state_tile), tiles = G + F::NM * F::STATE;
-  constexpr uint32_t X = F::NI * F::TILE, STAGE = 4 * X;
+  constexpr uint32_t X = F::NI * F::TILE, Y = F::NV * F::TILE, STAGE = 2 * (X + Y);
   constexpr int NT = F::COLS / 8, CT = F::C / 8;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int group = warp % F::ROWS, part = warp / F::ROWS;
@@ -668,7 +670,7 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_kv_kernel(const Ch
     load_tile<F, true>(at, q, p, p.n_k, c * F::C);
     load_tile<F, true>(at + X, k, p, p.n_k, c * F::C);
     load_tile<F, false>(at + 2 * X, v, p, p.n_v, c * F::C);
-    load_tile<F, false>(at + 3 * X, dO, p, p.n_v, c * F::C);
+    load_tile<F, false>(at + 2 * X + Y, dO, p, p.n_v, c * F::C);
   };
   StateRows<F> state;
   if (F::STAGES == 2) load(c1 - 1);
@@ -678,7 +680,7 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_kv_kernel(const Ch
   for (int c = c1 - 1; c >= c0; --c) {
     const int t0 = c * F::C;
     const uint32_t tq = tiles + (F::STAGES == 2 ? (c & 1) * STAGE : 0);
-    const uint32_t tk = tq + X, tv = tk + X, td = tv + X;
+    const uint32_t tk = tq + X, tv = tk + X, td = tv + Y;
     if (F::STAGES == 1) load(c);
     chunk_decay<F::C>(p, seq, c, sh.decay);
     cp_async_done();
@@ -701,7 +703,7 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_kv_kernel(const Ch
     float w[CT][4] = {}, dw[CT][4] = {};
     auto live = [&](int j) { return j >= group; };
     rows_times_rows<F, CT, F::NI, F::NI>(w, tk, F::TILE, r0, tq, F::TILE, 0, lane, live);
-    rows_times_rows<F, CT, F::NI, F::NI>(dw, tv, F::TILE, r0, td, F::TILE, 0, lane, live);
+    rows_times_rows<F, CT, F::NV, F::NV>(dw, tv, F::TILE, r0, td, F::TILE, 0, lane, live);
     float row_sum[2] = {0.f, 0.f};
 #pragma unroll
     for (int n = 0; n < CT; ++n) {
@@ -739,12 +741,12 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_kv_kernel(const Ch
 #pragma unroll
       for (int n = 0; n < NT; ++n)
         acc[n][0] *= t_0, acc[n][1] *= t_0, acc[n][2] *= t_1, acc[n][3] *= t_1;
-      scores_times_cols<F, NT>(acc, w, td, n0, lane, live);
+      scores_times_cols<F, NT, F::NV>(acc, w, td, n0, lane, live);
       store_rows<F, NT>(acc, static_cast<T *>(p.dv) + ev, nullptr, p, p.n_v, t0 + r0, n0, lane);
     }
     {
       float acc[NT][4] = {};
-      rows_times_rows<F, NT, F::NI, F::NM>(acc, tv, F::TILE, r0, G, F::STATE, n0, lane,
+      rows_times_rows<F, NT, F::NV, F::NM>(acc, tv, F::TILE, r0, G, F::STATE, n0, lane,
                                            [](int) { return true; });
 #pragma unroll
       for (int n = 0; n < NT; ++n)
@@ -756,7 +758,7 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_kv_kernel(const Ch
           sh.rows[part][r0 + lane / 4 + 8] = d.y;
         }
       }
-      scores_times_cols<F, NT>(acc, dw, tq, n0, lane, live);
+      scores_times_cols<F, NT, F::NI>(acc, dw, tq, n0, lane, live);
       store_rows<F, NT>(acc, static_cast<T *>(p.dk) + ek, k, p, p.n_k, t0 + r0, n0, lane);
     }
     const bool more = c > c0;
