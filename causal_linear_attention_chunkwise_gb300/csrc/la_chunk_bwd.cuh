@@ -97,6 +97,10 @@ template <typename T_, int D_, int C_, int NI_, int NM_> struct BwdConfig {
   // Tiles of the next chunk arrive while this one is worked on.
   static constexpr int STAGES = sizeof(T) == 2 && NI == 1 ? 2 : 1;
   static constexpr int BLOCKS = D == 64 ? 3 : 1;  // to an SM
+  // Three planes of scores are six products: the warps of a group form 8 of their columns each
+  // and share them in shared memory, where a block has it to spare.
+  static constexpr bool SHARE = NI == 3 && SPLIT == C / 8;
+  static constexpr uint32_t SCORE_ROW = C * 2 + 16, SCORES = C * SCORE_ROW;  // bytes
   static constexpr uint32_t TILE = C * D * 2;  // bytes of one plane
   static constexpr uint32_t STATE = D * D * 2;
   static_assert(WARPS % ROWS == 0 && COLS % 16 == 0, "whole column tiles");
@@ -390,21 +394,78 @@ __device__ __forceinline__ void rows_times_cols(float (&acc)[NT][4], uint32_t x,
   add_small<(NX > 1 || NY > 1)>(acc, small);
 }
 
-// acc[n] += W Y over the chunk's tokens: W scores in accumulators (tiles of 8 tokens), Y's tile
+// 16 x 8 scores: rows m0 .. of X's tile times rows n0 .. of Y's, over the widths.
+template <typename F, int NX, int NY>
+__device__ __forceinline__ void score_tile(float (&acc)[4], uint32_t x, int m0, uint32_t y, int n0,
+                                           int lane) {
+  constexpr int N = NX > NY ? NX : NY;
+  float small[4] = {};
+#pragma unroll
+  for (int k0 = 0; k0 < F::D; k0 += 32) {
+    uint32_t b[NY][4];
+#pragma unroll
+    for (int i = 0; i < NY; ++i)
+      ldsm4(b[i], y + i * F::TILE + tile_offset<F::D>(n0 + (lane & 7), k0 + (lane >> 3) * 8));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t a[NX][4];
+#pragma unroll
+      for (int i = 0; i < NX; ++i) frag_a<F::D>(a[i], x + i * F::TILE, m0, k0 + h * 16, lane);
+#pragma unroll
+      for (int o = N - 1; o > 0; --o)
+#pragma unroll
+        for (int i = 0; i < NX; ++i)
+          if (o - i >= 0 && o - i < NY) mma16816(small, a[i], b[o - i][2 * h], b[o - i][2 * h + 1]);
+      mma16816(acc, a[0], b[0][2 * h], b[0][2 * h + 1]);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) acc[e] += small[e];
+}
+
+// Scores as planes of an operand: from accumulators (tiles of 8 tokens), and by shared memory,
+// from 16 x 8 tiles.
+template <typename F>
+__device__ __forceinline__ void score_frag(uint32_t (&a)[F::NO][4], const float (&w)[F::C / 8][4],
+                                           int j) {
+  split<F::NO>(w[2 * j][0], w[2 * j][1], &a[0][0], 4);
+  split<F::NO>(w[2 * j][2], w[2 * j][3], &a[0][1], 4);
+  split<F::NO>(w[2 * j + 1][0], w[2 * j + 1][1], &a[0][2], 4);
+  split<F::NO>(w[2 * j + 1][2], w[2 * j + 1][3], &a[0][3], 4);
+}
+template <typename F>
+__device__ __forceinline__ void score_frag(uint32_t (&a)[F::NO][4], uint32_t scores, int m0, int j,
+                                           int lane) {
+#pragma unroll
+  for (int m = 0; m < F::NO; ++m)
+    ldsm4(a[m], scores + m * F::SCORES + (m0 + (lane & 15)) * F::SCORE_ROW +
+                    (j * 16 + (lane >> 4) * 8) * 2);
+}
+template <typename F>
+__device__ __forceinline__ void put_scores(char *scores, const float (&w)[4], int m0, int n0,
+                                           int lane) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t o[F::NO];
+    split<F::NO>(w[2 * h], w[2 * h + 1], o, 1);
+#pragma unroll
+    for (int m = 0; m < F::NO; ++m)
+      *reinterpret_cast<uint32_t *>(scores + m * F::SCORES + (m0 + lane / 4 + 8 * h) * F::SCORE_ROW +
+                                    (n0 + lane % 4 * 2) * 2) = o[m];
+  }
+}
+
+// acc[n] += W Y over the chunk's tokens: W's operand by frag(planes, 16 tokens), Y's tile
 // [token][.], columns n0 + 8 n.
-template <typename F, int NT, int NY, typename Live>
-__device__ __forceinline__ void scores_times_cols(float (&acc)[NT][4],
-                                                  const float (&w)[F::C / 8][4], uint32_t y,
+template <typename F, int NT, int NY, typename Frag, typename Live>
+__device__ __forceinline__ void scores_times_cols(float (&acc)[NT][4], Frag frag, uint32_t y,
                                                   int n0, int lane, Live live) {
   float small[NT][4] = {};
 #pragma unroll
   for (int j = 0; j < F::C / 16; ++j) {
     if (!live(j)) continue;
     uint32_t a[F::NO][4];
-    split<F::NO>(w[2 * j][0], w[2 * j][1], &a[0][0], 4);
-    split<F::NO>(w[2 * j][2], w[2 * j][3], &a[0][1], 4);
-    split<F::NO>(w[2 * j + 1][0], w[2 * j + 1][1], &a[0][2], 4);
-    split<F::NO>(w[2 * j + 1][2], w[2 * j + 1][3], &a[0][3], 4);
+    frag(a, j);
 #pragma unroll
     for (int n = 0; n < NT; n += 2) {
       uint32_t b[NY][4];
@@ -476,6 +537,7 @@ template <typename F> struct BwdShared {
   ChunkDecay<F::C> decay;
   float rows[F::SPLIT][F::C];  // row sums of the warps that share a group
   float cols[F::ROWS][F::C];   // column sums of the groups
+  float pairs[F::SHARE ? F::SPLIT : 1][F::C];  // row sums of shared scores
   float sum[F::WARPS];
 };
 template <typename F> constexpr uint32_t bwd_shared_bytes() {
@@ -534,7 +596,8 @@ __global__ void __launch_bounds__(F::THREADS) segment_share_kernel(const ChunkBw
 
 // dq: a walk forward over a segment's chunks.
 template <typename F> constexpr uint32_t grad_q_smem() {
-  return bwd_shared_bytes<F>() + F::STAGES * (F::NI + 2 * F::NV) * F::TILE + F::NM * F::STATE;
+  return bwd_shared_bytes<F>() + F::STAGES * (F::NI + 2 * F::NV) * F::TILE + F::NM * F::STATE +
+         F::SHARE * F::NO * F::SCORES;
 }
 template <typename F>
 __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_q_kernel(const ChunkBwd p) {
@@ -543,6 +606,7 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_q_kernel(const Chu
   char *state_tile = smem + bwd_shared_bytes<F>();
   const uint32_t S = smem_u32(state_tile), tiles = S + F::NM * F::STATE;
   constexpr uint32_t X = F::NI * F::TILE, Y = F::NV * F::TILE, STAGE = X + 2 * Y;
+  char *scores = state_tile + F::NM * F::STATE + F::STAGES * STAGE;
   constexpr int NT = F::COLS / 8;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int group = warp % F::ROWS, part = warp / F::ROWS;
@@ -582,16 +646,27 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_q_kernel(const Chu
     // dO V^T . D: rows j of the group, tokens i <= j
     float w[F::C / 8][4] = {};
     auto live = [&](int j) { return j <= group; };
-    rows_times_rows<F, F::C / 8, F::NV, F::NV>(w, td, F::TILE, r0, tv, F::TILE, 0, lane, live);
+    auto masked = [&](float &x, int e, int col) {
+      const int j = r0 + lane / 4 + e / 2 * 8, i = col + lane % 4 * 2 + e % 2;
+      if (p.decay_kind != LA_DECAY_NONE)
+        x *= decay_between(sh.decay.lam[j], sh.decay.lam[i <= j ? i : j]);
+      x = i <= j ? x : 0.f;
+    };
+    if constexpr (F::SHARE) {
+      if (live(part / 2)) {
+        float x[4] = {};
+        score_tile<F, F::NV, F::NV>(x, td, r0, tv, part * 8, lane);
 #pragma unroll
-    for (int n = 0; n < F::C / 8; ++n) {
-      if (n / 2 > group) continue;
+        for (int e = 0; e < 4; ++e) masked(x[e], e, part * 8);
+        put_scores<F>(scores, x, r0, part * 8, lane);
+      }
+    } else {
+      rows_times_rows<F, F::C / 8, F::NV, F::NV>(w, td, F::TILE, r0, tv, F::TILE, 0, lane, live);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int j = r0 + lane / 4 + e / 2 * 8, i = n * 8 + lane % 4 * 2 + e % 2;
-        if (p.decay_kind != LA_DECAY_NONE)
-          w[n][e] *= decay_between(sh.decay.lam[j], sh.decay.lam[i <= j ? i : j]);
-        w[n][e] = i <= j ? w[n][e] : 0.f;
+      for (int n = 0; n < F::C / 8; ++n) {
+        if (n / 2 > group) continue;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) masked(w[n][e], e, n * 8);
       }
     }
     float acc[NT][4] = {};
@@ -607,7 +682,12 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_q_kernel(const Chu
         sh.rows[part][r0 + lane / 4 + 8] = d.y;
       }
     }
-    scores_times_cols<F, NT, F::NI>(acc, w, tk, n0, lane, live);
+    if (F::SHARE) __syncthreads();
+    auto frag = [&](uint32_t (&a)[F::NO][4], int j) {
+      if constexpr (F::SHARE) score_frag<F>(a, smem_u32(scores), r0, j, lane);
+      else score_frag<F>(a, w, j);
+    };
+    scores_times_cols<F, NT, F::NI>(acc, frag, tk, n0, lane, live);
     store_rows<F, NT>(acc, static_cast<T *>(p.dq) + ek, q, p, p.n_k, t0 + r0, n0, lane);
     float around = 0.f;
     if (c + 1 < c1) {
@@ -645,7 +725,8 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_q_kernel(const Chu
 
 // dk and dv: a walk backward over a segment's chunks.
 template <typename F> constexpr uint32_t grad_kv_smem() {
-  return bwd_shared_bytes<F>() + 2 * F::STAGES * (F::NI + F::NV) * F::TILE + F::NM * F::STATE;
+  return bwd_shared_bytes<F>() + 2 * F::STAGES * (F::NI + F::NV) * F::TILE + F::NM * F::STATE +
+         2 * F::SHARE * F::NO * F::SCORES;
 }
 template <typename F>
 __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_kv_kernel(const ChunkBwd p) {
@@ -654,6 +735,7 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_kv_kernel(const Ch
   char *state_tile = smem + bwd_shared_bytes<F>();
   const uint32_t G = smem_u32(state_tile), tiles = G + F::NM * F::STATE;
   constexpr uint32_t X = F::NI * F::TILE, Y = F::NV * F::TILE, STAGE = 2 * (X + Y);
+  char *scores = state_tile + F::NM * F::STATE + F::STAGES * STAGE;
   constexpr int NT = F::COLS / 8, CT = F::C / 8;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int group = warp % F::ROWS, part = warp / F::ROWS;
@@ -702,38 +784,71 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_kv_kernel(const Ch
     // K Q^T . D and V dO^T . D: rows i of the group, tokens j >= i
     float w[CT][4] = {}, dw[CT][4] = {};
     auto live = [&](int j) { return j >= group; };
-    rows_times_rows<F, CT, F::NI, F::NI>(w, tk, F::TILE, r0, tq, F::TILE, 0, lane, live);
-    rows_times_rows<F, CT, F::NV, F::NV>(dw, tv, F::TILE, r0, td, F::TILE, 0, lane, live);
     float row_sum[2] = {0.f, 0.f};
+    // Four scores of both: masked, decayed, and their pairs added up.
+    auto masked = [&](float (&x)[4], float (&y)[4], int col, float (&sum)[2]) {
 #pragma unroll
-    for (int n = 0; n < CT; ++n) {
-      float col[2] = {0.f, 0.f};
-      if (n / 2 >= group) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int i = r0 + lane / 4 + e / 2 * 8, j = n * 8 + lane % 4 * 2 + e % 2;
-          float f = 1.f;
-          if (p.decay_kind != LA_DECAY_NONE)
-            f = decay_between(sh.decay.lam[j], sh.decay.lam[i <= j ? i : j]);
-          const float pair = i < j ? w[n][e] * dw[n][e] * f : 0.f;
-          row_sum[e / 2] += pair;
-          col[e % 2] += pair;
-          w[n][e] = i <= j ? w[n][e] * f : 0.f;
-          dw[n][e] = i <= j ? dw[n][e] * f : 0.f;
-        }
+      for (int e = 0; e < 4; ++e) {
+        const int i = r0 + lane / 4 + e / 2 * 8, j = col + lane % 4 * 2 + e % 2;
+        float f = 1.f;
+        if (p.decay_kind != LA_DECAY_NONE)
+          f = decay_between(sh.decay.lam[j], sh.decay.lam[i <= j ? i : j]);
+        const float pair = i < j ? x[e] * y[e] * f : 0.f;
+        row_sum[e / 2] += pair;
+        sum[e % 2] += pair;
+        x[e] = i <= j ? x[e] * f : 0.f;
+        y[e] = i <= j ? y[e] * f : 0.f;
       }
-      if (p.rc && part == 0) {
+    };
+    auto put_cols = [&](float (&sum)[2], int col) {
 #pragma unroll
-        for (int off = 4; off < 32; off <<= 1) {
-          col[0] += __shfl_xor_sync(0xffffffffu, col[0], off);
-          col[1] += __shfl_xor_sync(0xffffffffu, col[1], off);
-        }
-        if (lane < 4) {
-          sh.cols[group][n * 8 + lane * 2] = col[0];
-          sh.cols[group][n * 8 + lane * 2 + 1] = col[1];
-        }
+      for (int off = 4; off < 32; off <<= 1) {
+        sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], off);
+        sum[1] += __shfl_xor_sync(0xffffffffu, sum[1], off);
+      }
+      if (lane < 4) {
+        sh.cols[group][col + lane * 2] = sum[0];
+        sh.cols[group][col + lane * 2 + 1] = sum[1];
+      }
+    };
+    if constexpr (F::SHARE) {
+      float sum[2] = {0.f, 0.f};
+      if (live(part / 2)) {
+        float x[4] = {}, y[4] = {};
+        score_tile<F, F::NI, F::NI>(x, tk, r0, tq, part * 8, lane);
+        score_tile<F, F::NV, F::NV>(y, tv, r0, td, part * 8, lane);
+        masked(x, y, part * 8, sum);
+        put_scores<F>(scores, x, r0, part * 8, lane);
+        put_scores<F>(scores + F::NO * F::SCORES, y, r0, part * 8, lane);
+      }
+      if (p.rc) put_cols(sum, part * 8);
+    } else {
+      rows_times_rows<F, CT, F::NI, F::NI>(w, tk, F::TILE, r0, tq, F::TILE, 0, lane, live);
+      rows_times_rows<F, CT, F::NV, F::NV>(dw, tv, F::TILE, r0, td, F::TILE, 0, lane, live);
+#pragma unroll
+      for (int n = 0; n < CT; ++n) {
+        float sum[2] = {0.f, 0.f};
+        if (n / 2 >= group) masked(w[n], dw[n], n * 8, sum);
+        if (p.rc && part == 0) put_cols(sum, n * 8);
       }
     }
+    if (p.rc) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        row_sum[h] += __shfl_xor_sync(0xffffffffu, row_sum[h], 1);
+        row_sum[h] += __shfl_xor_sync(0xffffffffu, row_sum[h], 2);
+        if (lane % 4 == 0 && (F::SHARE || part == 0))
+          sh.pairs[F::SHARE ? part : 0][r0 + lane / 4 + 8 * h] = row_sum[h];
+      }
+    }
+    auto frag = [&](uint32_t (&a)[F::NO][4], int j) {
+      if constexpr (F::SHARE) score_frag<F>(a, smem_u32(scores), r0, j, lane);
+      else score_frag<F>(a, w, j);
+    };
+    auto dfrag = [&](uint32_t (&a)[F::NO][4], int j) {
+      if constexpr (F::SHARE) score_frag<F>(a, smem_u32(scores) + F::NO * F::SCORES, r0, j, lane);
+      else score_frag<F>(a, dw, j);
+    };
     const float t_0 = sh.decay.tail[r0 + lane / 4], t_1 = sh.decay.tail[r0 + lane / 4 + 8];
     {
       float acc[NT][4] = {};
@@ -741,7 +856,8 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_kv_kernel(const Ch
 #pragma unroll
       for (int n = 0; n < NT; ++n)
         acc[n][0] *= t_0, acc[n][1] *= t_0, acc[n][2] *= t_1, acc[n][3] *= t_1;
-      scores_times_cols<F, NT, F::NV>(acc, w, td, n0, lane, live);
+      if (F::SHARE) __syncthreads();
+      scores_times_cols<F, NT, F::NV>(acc, frag, td, n0, lane, live);
       store_rows<F, NT>(acc, static_cast<T *>(p.dv) + ev, nullptr, p, p.n_v, t0 + r0, n0, lane);
     }
     {
@@ -758,7 +874,7 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_kv_kernel(const Ch
           sh.rows[part][r0 + lane / 4 + 8] = d.y;
         }
       }
-      scores_times_cols<F, NT, F::NI>(acc, dw, tq, n0, lane, live);
+      scores_times_cols<F, NT, F::NI>(acc, dfrag, tq, n0, lane, live);
       store_rows<F, NT>(acc, static_cast<T *>(p.dk) + ek, k, p, p.n_k, t0 + r0, n0, lane);
     }
     const bool more = c > c0;
@@ -772,22 +888,11 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_kv_kernel(const Ch
         for (int i = 0; i < F::SPLIT; ++i) s += sh.rows[i][t];
 #pragma unroll
         for (int i = 0; i < F::ROWS; ++i) cols += sh.cols[i][t];
+        // a token's pairs as the later one less those as the earlier one
+#pragma unroll
+        for (int i = 0; i < (F::SHARE ? F::SPLIT : 1); ++i) cols -= sh.pairs[i][t];
         p.rk[(size_t)seq * p.L + t0 + t] = s;
         p.rc[(size_t)seq * p.L + t0 + t] = cols;
-      }
-      __syncthreads();
-      // the row sums leave by the same place
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        row_sum[h] += __shfl_xor_sync(0xffffffffu, row_sum[h], 1);
-        row_sum[h] += __shfl_xor_sync(0xffffffffu, row_sum[h], 2);
-      }
-      if (part == 0 && lane % 4 == 0) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int i = r0 + lane / 4 + 8 * h;
-          if (t0 + i < p.L) p.rc[(size_t)seq * p.L + t0 + i] -= row_sum[h];
-        }
       }
     }
     if (more) state.planes(state_tile, warp, lane);
