@@ -32,8 +32,9 @@ struct Plan {
 // segment also the pass over their own shares, S and G in blocks of their own at 0.2 of a chunk's
 // time, and two launches.  It picks 2 segments for 2 x 32 x 8192 x 128 with decays (517 us; 1: 813,
 // 4: 588, 7: 610), 9 for 1 x 16 x 32768 x 128 (543; 4: 969, 19: 571), 2 for 4 x 16 x 4096 x 64
-// (149; 1: 228, 4: 158), 9 for 3 x 5 x 777 x 64 x 128 fp32 (113; 5: 158, 13: 138), and a chunk
-// each for one sequence of 300 tokens in fp32 (17; 5: 28, 1: 102).
+// (130; 1: 189, 4: 140), 9 for 3 x 5 x 777 x 64 x 128 fp32 (103; 5: 141, 13: 125), 4 for
+// 4 x 8 x 2048 x 128 x 64 (271; 3: 323, 8: 261), and a chunk each for one sequence of 300 tokens
+// in fp32 (17; 5: 28, 1: 102).
 Plan make_plan(const ChunkBwdArgs &a, bool f32_out) {
   Plan p;
   p.wide = std::max(a.dk, a.dv) > 64;

@@ -36,7 +36,11 @@
 // decayed scores and the states round once to bf16 as operands (the state itself
 // stays fp32).  The fp32 outputs (ddecay, dS0) take those operands as three bf16
 // planes, which hold all of an fp32 value's bits; fp32 inputs, and phi = elu + 1
-// where an fp32 output is wanted, enter as three planes too.
+// where an fp32 output is wanted, enter as three planes too (v and dO of bf16 inputs as one).
+//
+// What bounds these kernels: mma.sync, 600 TFLOP/s at best, times six for three planes by three
+// (grad_kv of 3 x 5 x 777 x 64 x 128 fp32: the tensor pipe 40% busy, with two warps to a scheduler and
+// a chunk's steps one after another).
 #pragma once
 
 #include <cstdint>
@@ -98,7 +102,8 @@ template <typename T_, int D_, int C_, int NI_, int NM_> struct BwdConfig {
   static constexpr int STAGES = sizeof(T) == 2 && NI == 1 ? 2 : 1;
   static constexpr int BLOCKS = D == 64 ? 3 : 1;  // to an SM
   // Three planes of scores are six products: the warps of a group form 8 of their columns each
-  // and share them in shared memory, where a block has it to spare.
+  // and share them in shared memory, where four do (2 x 16 x 4096 x 128 fp32: 1131 us; each
+  // for itself 1237).  At D = 64 two warps share a group, and three blocks an SM.
   static constexpr bool SHARE = NI == 3 && SPLIT == C / 8;
   static constexpr uint32_t SCORE_ROW = C * 2 + 16, SCORES = C * SCORE_ROW;  // bytes
   static constexpr uint32_t TILE = C * D * 2;  // bytes of one plane
