@@ -40,7 +40,7 @@ Plan make_plan(const ChunkBwdArgs &a, bool f32_out) {
   p.wide = std::max(a.dk, a.dv) > 64;
   p.full = a.dtype == LA_F32 || (f32_out && a.phi == LA_PHI_ELU1);
   p.planes = p.full || f32_out;
-  p.tc = !p.full && a.dk == a.dv && a.dk >= 64;
+  p.tc = !p.full;
   p.chunk = p.tc ? 128 : p.full ? 32 : 64;
   p.chunks = (a.L + p.chunk - 1) / p.chunk;
   const long long seqs = (long long)a.B * a.H;
@@ -217,7 +217,7 @@ constexpr int kDecayWarps = 32;
 template <int C, int BLOCK>
 __global__ void __launch_bounds__(32 * kDecayWarps)
 decay_grad_kernel(const ChunkBwd p, float *ddecay, float *by_segment) {
-  __shared__ float sum_q[kMaxPer], sum_k[kMaxPer], all[kMaxPer];
+  __shared__ float sum_q[kMaxPer], sum_k[kMaxPer], all[kMaxPer], around_of[kMaxPer];
   __shared__ double share[kDecayWarps];
   constexpr int N = C / 32, LANES = BLOCK / N, BLOCKS = C / BLOCK;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -238,21 +238,28 @@ decay_grad_kernel(const ChunkBwd p, float *ddecay, float *by_segment) {
     }
   }
   __syncthreads();
-  // A thread: the chunks that follow from one given sum.
+  // A thread: the chunks that follow from one given sum, and what they are off by at the next
+  // one, spread over them: half of what their errors add up to is left.
+  auto given = [&](int c) {
+    float x = 0.f;
+    for (int i = 0; i < kShares; ++i) x += p.between[p.keep_slot(seq, c0 + c) * kShares + i];
+    return x;
+  };
   for (int x = c0 / p.every + threadIdx.x; x * p.every < c0 + n; x += 32 * kDecayWarps) {
     const int from = max(x * p.every - c0, 0), last = min((x + 1) * p.every - c0, n) - 1;
-    float around = 0.f;
-    if (last == n - 1) around = p.around[(size_t)seq * p.segments + seg];
-    else
-      for (int i = 0; i < kShares; ++i)
-        around += p.between[p.keep_slot(seq, c0 + last) * kShares + i];
+    float around = last == n - 1 ? p.around[(size_t)seq * p.segments + seg] : given(last);
+    int start = last;
     for (int c = last; c >= from; --c) {
-      const float y = around + sum_q[c];
-      // Past a decay of 2^-40 nothing of <G, S> is left but the rounding of y.
-      const float next = c > from && all[c - 1] >= -40.f ? y - sum_k[c - 1] : 0.f;
-      all[c] = around;
-      around = next;
+      around_of[c] = around;
+      if (c == 0) break;
+      around += sum_q[c];
+      // Past a decay of 2^-40 nothing of <G, S> is left but the rounding of the sum.
+      if (all[c - 1] >= -40.f) around -= sum_k[c - 1];
+      else around = 0.f, start = c - 1;
     }
+    if (from == 0) continue;
+    const float off = (around - given(from - 1)) / (start - from + 1);
+    for (int c = from; c < start; ++c) around_of[c] -= off * (start - c);
   }
   __syncthreads();
   double total = 0.0;
@@ -270,7 +277,7 @@ decay_grad_kernel(const ChunkBwd p, float *ddecay, float *by_segment) {
       rs[i] = BLOCKS > 1 && live ? p.rs[base + t] : 0.f;
       sq += q[i], sk += k[i], sr += r[i], scs += cs[i], srs += rs[i];
     }
-    float around = all[c];
+    float around = around_of[c];
     if (BLOCKS > 1) {
       const int block = lane / LANES;
       const float bq = group_sum<LANES>(sq), bk = group_sum<LANES>(sk);

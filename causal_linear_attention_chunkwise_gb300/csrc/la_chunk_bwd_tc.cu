@@ -1,5 +1,6 @@
 // la_chunk_bwd_tc.cu -- the backward walks on the 5th-gen tensor cores: bf16 inputs,
-// d_k = d_v = D in {64, 128}, chunks of 128 tokens.
+// chunks of 128 tokens, widths padded to D = 64 or 128 (the copies fill with zeros and
+// leave out what lies past a row's end).
 //
 // The mathematics is la_chunk_bwd.cuh's, a chunk being one 128-row tile.  A
 // block of 512 threads owns a segment of a sequence and one chunk of it at a time, in
@@ -199,32 +200,38 @@ __device__ __forceinline__ void load_tile_tma(const Block &b, uint32_t off, cons
     tma_load_3d(b.smem + off + x * CT * 128, map, bar, x * 64, token, seq);
 }
 template <int D>
-__device__ __forceinline__ void prefetch_tile(const CUtensorMap *map, int token, int seq) {
-#pragma unroll
-  for (int x = 0; x < D / 64; ++x) tma_prefetch_3d(map, x * 64, token, seq);
-}
-// Rows past the last token are not written.
-template <int D>
-__device__ __forceinline__ void store_tile_tma(const Block &b, uint32_t off,
-                                               const CUtensorMap *map, int token, int seq) {
+__device__ __forceinline__ void prefetch_tile(const CUtensorMap *map, int token, int seq,
+                                              int width) {
 #pragma unroll
   for (int x = 0; x < D / 64; ++x)
-    tma_store_3d(map, b.smem + off + x * CT * 128, x * 64, token, seq);
+    if (x * 64 < width) tma_prefetch_3d(map, x * 64, token, seq);
+}
+// Rows past the last token, and columns past the width, are not written.
+template <int D>
+__device__ __forceinline__ void store_tile_tma(const Block &b, uint32_t off,
+                                               const CUtensorMap *map, int token, int seq,
+                                               int width) {
+#pragma unroll
+  for (int x = 0; x < D / 64; ++x)
+    if (x * 64 < width) tma_store_3d(map, b.smem + off + x * CT * 128, x * 64, token, seq);
 }
 
-// dst = elu + 1 of a tile (dst may be the tile); rows past the last token are zero.
+// dst = elu + 1 of a tile (dst may be the tile); rows past the last token and columns past the
+// width are zero.
 template <int D>
 __device__ __forceinline__ void map_tile_tc(const unsigned char *tile, unsigned char *dst,
-                                            int rows) {
+                                            int rows, int width) {
 #pragma unroll
   for (int i = 0; i < CT * D / 8 / kThreads; ++i) {
     const int x = threadIdx.x + i * kThreads;
+    const int row = x / 8 % CT, col = x / 8 / CT * 64 + ((x % 8) ^ (row & 7)) * 8;
+    const bool live = row < rows && col < width;
     const uint4 u = reinterpret_cast<const uint4 *>(tile)[x];
     uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       w[e] = la::pack_bf16(tc::elu1_fast(bf16_lo(w[e])), tc::elu1_fast(bf16_hi(w[e])));
-      if ((x / 8) % CT >= rows) w[e] = 0;
+      if (!live) w[e] = 0;
     }
     reinterpret_cast<uint4 *>(dst)[x] = make_uint4(w[0], w[1], w[2], w[3]);
   }
@@ -336,21 +343,29 @@ template <int D, int NM> struct StateRow {
   static constexpr int N = D / PARTS;
   float c[N];
 
-  __device__ __forceinline__ void load(const float *src, const Block &b) {
+  // The same of a [n_k][n_v] tensor: element `at` of it, or none of its.
+  __device__ __forceinline__ static bool place(const Block &b, const ChunkBwd &p, int i,
+                                               size_t &at) {
+    const int col = b.part * N + i;
+    at = (size_t)b.row * p.n_v + col;
+    return b.row < p.n_k && col < p.n_v;
+  }
+  __device__ __forceinline__ void load(const float *src, const Block &b, const ChunkBwd &p) {
 #pragma unroll
     for (int i = 0; i < N; i += 4) {
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (src && b.row < D)
-        x = *reinterpret_cast<const float4 *>(src + (size_t)b.row * D + b.part * N + i);
+      size_t at;
+      if (src && place(b, p, i, at)) x = *reinterpret_cast<const float4 *>(src + at);
       c[i] = x.x, c[i + 1] = x.y, c[i + 2] = x.z, c[i + 3] = x.w;
     }
   }
-  __device__ __forceinline__ void store(float *dst, const Block &b) const {
-    if (b.row >= D) return;
+  __device__ __forceinline__ void store(float *dst, const Block &b, const ChunkBwd &p) const {
 #pragma unroll
-    for (int i = 0; i < N; i += 4)
-      *reinterpret_cast<float4 *>(dst + (size_t)b.row * D + b.part * N + i) =
-          make_float4(c[i], c[i + 1], c[i + 2], c[i + 3]);
+    for (int i = 0; i < N; i += 4) {
+      size_t at;
+      if (place(b, p, i, at))
+        *reinterpret_cast<float4 *>(dst + at) = make_float4(c[i], c[i + 1], c[i + 2], c[i + 3]);
+    }
   }
   // As planes of operand tiles [D][D] (64-column boxes).
   __device__ __forceinline__ void planes(const Block &b) const {
@@ -400,15 +415,14 @@ template <int D, int NM> struct StateRow {
     }
     return s;
   }
-  __device__ __forceinline__ float dot(const float *src, const Block &b) const {
+  __device__ __forceinline__ float dot(const float *src, const Block &b, const ChunkBwd &p) const {
     float s = 0.f;
-    if (b.row < D) {
 #pragma unroll
-      for (int i = 0; i < N; i += 4) {
-        const float4 x =
-            *reinterpret_cast<const float4 *>(src + (size_t)b.row * D + b.part * N + i);
-        s = fmaf(x.x, c[i], fmaf(x.y, c[i + 1], fmaf(x.z, c[i + 2], fmaf(x.w, c[i + 3], s))));
-      }
+    for (int i = 0; i < N; i += 4) {
+      size_t at;
+      if (!place(b, p, i, at)) continue;
+      const float4 x = *reinterpret_cast<const float4 *>(src + at);
+      s = fmaf(x.x, c[i], fmaf(x.y, c[i + 1], fmaf(x.z, c[i + 2], fmaf(x.w, c[i + 3], s))));
     }
     return s;
   }
@@ -471,7 +485,7 @@ segment_share_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, uns
     if (n > 1) load(1);
   }
   StateRow<D, NM> state;
-  state.load(nullptr, b);
+  state.load(nullptr, b, p);
   double total = 0.0;
   // each thread of part 0: its token's log decay and the chunk's, a chunk ahead
   float2 own = make_float2(0.f, 0.f), end = own;
@@ -499,7 +513,7 @@ segment_share_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, uns
     const uint32_t tile_at = smem_u32(tile), sum = b.tmem + (i & 1) * D;
     const Operand y = along_col<SM::BOX>(tile_at + SM::TILE);
     if (PHI) {
-      map_tile_tc<D>(tile, tile, p.L - chunk(i) * CT);
+      map_tile_tc<D>(tile, tile, p.L - chunk(i) * CT, p.n_k);
       if (DECAY) __syncthreads();
     }
     if (DECAY) {
@@ -556,7 +570,7 @@ segment_share_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, uns
     b.wait_mma(1, (n - 1) & 1);
     state.update(b, ((n - 1) & 1) * D, exp2_two(last));
     const size_t slot = (size_t)seq * (p.segments - 1) + of;
-    state.store((back ? p.W : p.U) + slot * D * D, b);
+    state.store((back ? p.W : p.U) + slot * p.n_k * p.n_v, b, p);
     if (threadIdx.x == 0 && (!back || seg == p.segments - 1))
       p.total[(size_t)seq * p.segments + seg] = (float)total;
   } else if (threadIdx.x == 0) {  // the copies in flight end before their memory does
@@ -599,7 +613,7 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
   float *inside = reinterpret_cast<float *>(smem + SM::OFF_MORE);  // factors of pairs of one block
   const int seq = blockIdx.x / p.segments, seg = blockIdx.x % p.segments;
   const int c0 = seg * p.per, c1 = min(c0 + p.per, p.chunks);
-  const size_t es = (size_t)D * D;
+  const size_t es = (size_t)p.n_k * p.n_v;
   constexpr bool decays = DECAY;
   auto stage = [&](int c) { return TWO ? (c - c0) & 1 : 0; };
   auto tile = [&](int c, int i) {  // k, v, dO, q
@@ -620,10 +634,10 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
     if (HAS_Q) load_tile_tma<D>(b, tile(c, 3), &maps.q, &b.full[stage(c)], c * CT, seq);
   };
   auto prefetch = [&](int c) {
-    prefetch_tile<D>(&maps.dO, c * CT, seq);
-    prefetch_tile<D>(&maps.k, c * CT, seq);
-    prefetch_tile<D>(&maps.v, c * CT, seq);
-    if (HAS_Q) prefetch_tile<D>(&maps.q, c * CT, seq);
+    prefetch_tile<D>(&maps.dO, c * CT, seq, p.n_v);
+    prefetch_tile<D>(&maps.k, c * CT, seq, p.n_k);
+    prefetch_tile<D>(&maps.v, c * CT, seq, p.n_v);
+    if (HAS_Q) prefetch_tile<D>(&maps.q, c * CT, seq, p.n_k);
   };
   if (threadIdx.x == kLeaderQ) {
     load_dO(c0);
@@ -634,7 +648,7 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
   next.load(p, b, seq, c0);
   StateRow<D, NM> state;
   state.load(seg ? p.U + ((size_t)seq * (p.segments - 1) + seg - 1) * es
-                 : p.S0 ? p.S0 + (size_t)seq * es : nullptr, b);
+                 : p.S0 ? p.S0 + (size_t)seq * es : nullptr, b, p);
   state.planes(b);
   float around = 0.f;
   int c = c0;
@@ -649,7 +663,7 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
       if (more) next.load(p, b, seq, c + 1);
     }
     b.wait_full(stage(c), TWO ? (c - c0) >> 1 & 1 : phase);
-    if (PHI) map_tile_tc<D>(smem + TK, smem + TK, p.L - t0);
+    if (PHI) map_tile_tc<D>(smem + TK, smem + TK, p.L - t0, p.n_k);
     fence_proxy_async_smem();
     tc_fence_before();
     if (__syncthreads_or(b.failed)) break;
@@ -678,7 +692,7 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
     const float2 own = decays ? lam[b.row] : make_float2(0.f, 0.f);
     const float2 end = decays ? lam[CT - 1] : make_float2(0.f, 0.f);
     const float2 all = exp2_two(end);
-    if (NM == 3 && DECAY && p.keeps(c, c1)) state.keep(p.kept + p.keep_slot(seq, c) * es, b);
+    if (NM == 3 && DECAY && p.keeps(c, c1)) state.keep(p.kept + p.keep_slot(seq, c) * (D * D), b);
     b.wait_mma(0, phase);
     // the scores as operand: row j, tokens i <= j
     const float2 before = DECAY && b.quarter ? lam[b.quarter * 32 - 1] : make_float2(0.f, 0.f);
@@ -782,7 +796,7 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
     tc_fence_before();
     __syncthreads();
     if (threadIdx.x == kLeaderQ) {
-      store_tile_tma<D>(b, TQ, &maps.dq, t0, seq);
+      store_tile_tma<D>(b, TQ, &maps.dq, t0, seq, p.n_k);
       tma_store_commit();
     }
     if (NM == 3 && DECAY && b.part == 0) b.gather(T_MORE, dot, pairs);
@@ -804,7 +818,7 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
     } else if (NM == 3 && p.rq) {  // <G, e^L_C S>: the pairs around the segment's last chunk
       const float *G = seg + 1 < p.segments ? p.W + ((size_t)seq * (p.segments - 1) + seg) * es
                        : p.dSf ? p.dSf + (size_t)seq * es : nullptr;
-      if (G) around = state.dot(G, b) * all.x;
+      if (G) around = state.dot(G, b, p) * all.x;
     }
   }
   if (threadIdx.x == kLeaderQ) {
@@ -859,7 +873,7 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
   float *fac = reinterpret_cast<float *>(smem + SM::OFF_FAC);
   const int seq = blockIdx.x / p.segments, seg = blockIdx.x % p.segments;
   const int c0 = seg * p.per, c1 = min(c0 + p.per, p.chunks), n = c1 - c0;
-  const size_t es = (size_t)D * D;
+  const size_t es = (size_t)p.n_k * p.n_v;
   constexpr bool decays = DECAY;
   constexpr uint32_t MORE = SM::OFF_TILES + 4 * kStages<D> * SM::TILE;
   constexpr uint32_t OUT = MORE + PHI * SM::TILE;
@@ -876,10 +890,10 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
   auto load_v = [&](int c) { load(c, 2, &maps.v); };
   auto load_dO = [&](int c) { load(c, 3, &maps.dO); };
   auto prefetch = [&](int c) {
-    prefetch_tile<D>(&maps.q, c * CT, seq);
-    prefetch_tile<D>(&maps.k, c * CT, seq);
-    prefetch_tile<D>(&maps.v, c * CT, seq);
-    prefetch_tile<D>(&maps.dO, c * CT, seq);
+    prefetch_tile<D>(&maps.q, c * CT, seq, p.n_k);
+    prefetch_tile<D>(&maps.k, c * CT, seq, p.n_k);
+    prefetch_tile<D>(&maps.v, c * CT, seq, p.n_v);
+    prefetch_tile<D>(&maps.dO, c * CT, seq, p.n_v);
   };
   if (threadIdx.x == kLeaderKV) {
     arm(c1 - 1);
@@ -892,7 +906,7 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
   next.load(p, b, seq, c1 - 1);
   StateRow<D, NM> state;
   state.load(seg + 1 < p.segments ? p.W + ((size_t)seq * (p.segments - 1) + seg) * es
-             : p.dSf ? p.dSf + (size_t)seq * es : nullptr, b);
+             : p.dSf ? p.dSf + (size_t)seq * es : nullptr, b, p);
   state.planes(b);
   int done = 0;
   for (; done < n; ++done) {
@@ -907,8 +921,8 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
     }
     b.wait_full(stage(c), TWO ? done >> 1 & 1 : phase);
     if (PHI) {
-      map_tile_tc<D>(smem + TQ, smem + TQ, p.L - t0);
-      map_tile_tc<D>(smem + TK, smem + TKP, p.L - t0);
+      map_tile_tc<D>(smem + TQ, smem + TQ, p.L - t0, p.n_k);
+      map_tile_tc<D>(smem + TK, smem + TKP, p.L - t0, p.n_k);
     }
     if (OWN && threadIdx.x == kLeaderKV) tma_store_wait_read_all();
     fence_proxy_async_smem();
@@ -940,7 +954,7 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
     const float2 end = decays ? lam[CT - 1] : make_float2(0.f, 0.f);
     const float2 all = exp2_two(end);
     if (NM == 3 && DECAY && p.keeps(c, c1)) {
-      float s = state.dot_kept(p.kept + p.keep_slot(seq, c) * es, b);
+      float s = state.dot_kept(p.kept + p.keep_slot(seq, c) * (D * D), b);
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
       float *to = p.between + p.keep_slot(seq, c) * kShares;
@@ -1080,8 +1094,8 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
     tc_fence_before();
     __syncthreads();
     if (threadIdx.x == kLeaderKV) {
-      store_tile_tma<D>(b, TDV, &maps.dv, t0, seq);
-      store_tile_tma<D>(b, TDK, &maps.dk, t0, seq);
+      store_tile_tma<D>(b, TDV, &maps.dv, t0, seq, p.n_v);
+      store_tile_tma<D>(b, TDK, &maps.dk, t0, seq, p.n_k);
       tma_store_commit();
       if (OWN && !EARLY_K && more && !TWO) load_k(c - 1);
     }
@@ -1102,7 +1116,7 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
     }
   }
   if (done == n) {
-    if (p.dS0 && seg == 0) state.store(p.dS0 + (size_t)seq * es, b);
+    if (p.dS0 && seg == 0) state.store(p.dS0 + (size_t)seq * es, b, p);
   } else if (threadIdx.x == kLeaderKV) {
     tc::drain_wait(&b.full[stage(c1 - 1 - done)], (TWO ? done >> 1 : done) & 1);
   }
@@ -1119,10 +1133,11 @@ cudaError_t launch_tc(const ChunkBwd &p, int seqs, cudaStream_t stream) {
   const struct {
     CUtensorMap *map;
     const void *p;
-  } all[] = {{&m.q, p.q},   {&m.k, p.k},   {&m.v, p.v},  {&m.dO, p.dO},
-             {&m.dq, p.dq}, {&m.dk, p.dk}, {&m.dv, p.dv}};
+    int width;
+  } all[] = {{&m.q, p.q, p.n_k},   {&m.k, p.k, p.n_k},   {&m.v, p.v, p.n_v},  {&m.dO, p.dO, p.n_v},
+             {&m.dq, p.dq, p.n_k}, {&m.dk, p.dk, p.n_k}, {&m.dv, p.dv, p.n_v}};
   for (const auto &x : all)
-    if (!make_tmap_bf16_3d(x.map, x.p, D, p.L, seqs, 64, CT)) return cudaErrorInvalidValue;
+    if (!make_tmap_bf16_3d(x.map, x.p, x.width, p.L, seqs, 64, CT)) return cudaErrorInvalidValue;
   unsigned int *err = device_error_word();
   cudaError_t e;
   if (p.segments > 1) {
@@ -1154,7 +1169,7 @@ cudaError_t launch_d(const ChunkBwd &p, int seqs, bool planes, cudaStream_t stre
 }  // namespace
 
 cudaError_t launch_chunk_bwd_tc(const ChunkBwd &p, int seqs, bool planes, cudaStream_t stream) {
-  if (p.n_k == 128)
+  if (std::max(p.n_k, p.n_v) > 64)
     return p.decay_kind != LA_DECAY_NONE ? launch_d<128, true>(p, seqs, planes, stream)
                                          : launch_d<128, false>(p, seqs, planes, stream);
   return p.decay_kind != LA_DECAY_NONE ? launch_d<64, true>(p, seqs, planes, stream)
