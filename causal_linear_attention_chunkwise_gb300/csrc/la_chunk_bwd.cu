@@ -7,8 +7,6 @@
 
 namespace la {
 
-cudaError_t launch_chunk_bwd_bf16(const ChunkBwd &p, int seqs, bool wide, bool planes,
-                                  cudaStream_t stream);
 cudaError_t launch_chunk_bwd_tc(const ChunkBwd &p, int seqs, bool planes, cudaStream_t stream);
 cudaError_t launch_chunk_bwd_f32(const ChunkBwd &p, int seqs, bool wide, bool bf16,
                                  cudaStream_t stream);
@@ -20,9 +18,8 @@ constexpr int kKeep = 1024;   // tokens from one kept state to the next
 
 // How a call runs: which planes, the chunk, the segments.
 struct Plan {
-  bool tc;      // the tcgen05 kernels
+  bool tc;      // the tcgen05 kernels; else q and k, after phi, as three planes
   bool wide;    // padded width 128, else 64
-  bool full;    // inputs as three planes
   bool planes;  // states as three planes
   int chunk, chunks, segments, per;
 };
@@ -32,19 +29,17 @@ struct Plan {
 // segment also the pass over their own shares, S and G in blocks of their own at 0.2 of a chunk's
 // time, and two launches.  It picks 2 segments for 2 x 32 x 8192 x 128 with decays (517 us; 1: 813,
 // 4: 588, 7: 610), 9 for 1 x 16 x 32768 x 128 (543; 4: 969, 19: 571), 2 for 4 x 16 x 4096 x 64
-// (130; 1: 189, 4: 140), 9 for 3 x 5 x 777 x 64 x 128 fp32 (103; 5: 141, 13: 125), 4 for
-// 4 x 8 x 2048 x 128 x 64 (271; 3: 323, 8: 261), and a chunk each for one sequence of 300 tokens
-// in fp32 (17; 5: 28, 1: 102).
+// (130; 1: 189, 4: 140), 9 for 3 x 5 x 777 x 64 x 128 fp32 (103; 5: 141, 13: 125),
+// and a chunk each for one sequence of 300 tokens in fp32 (17; 5: 28, 1: 102).
 Plan make_plan(const ChunkBwdArgs &a, bool f32_out) {
   Plan p;
   p.wide = std::max(a.dk, a.dv) > 64;
-  p.full = a.dtype == LA_F32 || (f32_out && a.phi == LA_PHI_ELU1);
-  p.planes = p.full || f32_out;
-  p.tc = !p.full;
-  p.chunk = p.tc ? 128 : p.full ? 32 : 64;
+  p.tc = a.dtype == LA_BF16 && !(f32_out && a.phi == LA_PHI_ELU1);
+  p.planes = !p.tc || f32_out;
+  p.chunk = p.tc ? 128 : 32;
   p.chunks = (a.L + p.chunk - 1) / p.chunk;
   const long long seqs = (long long)a.B * a.H;
-  const long long slots = 152ll * (p.wide || p.tc ? 1 : p.planes && !p.full ? 2 : 3);
+  const long long slots = 152ll * (p.wide || p.tc ? 1 : 3);
   double best = 0;
   p.per = 0;
   for (int per = std::min(p.chunks, kMaxPer); per > 0;) {
@@ -385,20 +380,16 @@ cudaError_t launch_chunk_bwd(const ChunkBwdArgs &a) {
   lay_out(a, plan, decay_grad, static_cast<char *>(a.workspace), &p, &by_segment);
   cudaError_t e = cudaSuccess;
   if (a.decay_kind != LA_DECAY_NONE)
-    e = plan.chunk == 128  ? launch_chunk_decay<128>(p, (int)seqs, a.stream)
-        : plan.chunk == 64 ? launch_chunk_decay<64>(p, (int)seqs, a.stream)
-                           : launch_chunk_decay<32>(p, (int)seqs, a.stream);
+    e = plan.tc ? launch_chunk_decay<128>(p, (int)seqs, a.stream)
+                : launch_chunk_decay<32>(p, (int)seqs, a.stream);
   if (e != cudaSuccess) return e;
   e = plan.tc ? launch_chunk_bwd_tc(p, (int)seqs, plan.planes, a.stream)
-      : plan.full ? launch_chunk_bwd_f32(p, (int)seqs, plan.wide, a.dtype == LA_BF16, a.stream)
-                  : launch_chunk_bwd_bf16(p, (int)seqs, plan.wide, plan.planes, a.stream);
+              : launch_chunk_bwd_f32(p, (int)seqs, plan.wide, a.dtype == LA_BF16, a.stream);
   if (e != cudaSuccess || !decay_grad) return e;
-  if (plan.chunk == 128)
+  if (plan.tc)
     decay_grad_kernel<128, 32><<<(unsigned)blocks, 32 * kDecayWarps, 0, a.stream>>>(p, a.ddecay, by_segment);
-  else if (plan.chunk == 32)
-    decay_grad_kernel<32, 32><<<(unsigned)blocks, 32 * kDecayWarps, 0, a.stream>>>(p, a.ddecay, by_segment);
   else
-    decay_grad_kernel<64, 64><<<(unsigned)blocks, 32 * kDecayWarps, 0, a.stream>>>(p, a.ddecay, by_segment);
+    decay_grad_kernel<32, 32><<<(unsigned)blocks, 32 * kDecayWarps, 0, a.stream>>>(p, a.ddecay, by_segment);
   if ((e = cudaGetLastError()) != cudaSuccess || a.decay_kind != LA_DECAY_HEAD) return e;
   head_decay_kernel<<<a.H, 32, 0, a.stream>>>(by_segment, a.ddecay, a.B, a.H, plan.segments);
   return cudaGetLastError();

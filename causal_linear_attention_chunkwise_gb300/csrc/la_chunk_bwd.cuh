@@ -14,13 +14,15 @@
 //     dv = (Q K^T . D)^T dO + e^(L_C - L) K G
 //
 // dq needs S, which runs forward; dk and dv need G, which runs backward.  So two
-// kernels, each one walk over the chunks with its state in registers (fp32).  A warp
-// owns 16 tokens and computes its rows of the chunk's score matrices in the
-// orientation that its products need (dO V^T for dq, V dO^T and K Q^T for dk and
-// dv), so scores go from accumulators to operands within a thread, never through
-// shared memory.  A long sequence is cut into segments that run side by side: a
-// first kernel forms every segment's own share of S and G, a second one strings them
-// together.
+// kernels, each one walk over the chunks with its state in registers (fp32).  A long
+// sequence is cut into segments that run side by side: a first kernel forms every
+// segment's own share of S and G, a second one strings them together.
+//
+// bf16 tensors run in la_chunk_bwd_tc.cu.  The kernels here take what enters as three bf16 planes,
+// fp32 tensors and phi = elu + 1 where an fp32 output is wanted: three planes of 128 tokens do
+// not fit beside one another there.  A warp owns 16 tokens of a 32-token chunk (with others, which
+// take other columns) and computes its rows of the score matrices in the orientation
+// that its products need (dO V^T for dq, V dO^T and K Q^T for dk and dv).
 //
 // A decay's gradient counts the pairs (i < t <= j) that it lies between: pairs within
 // the chunk (row and column sums of Q K^T . dO V^T . D), pairs with one token in it (dot
@@ -30,7 +32,7 @@
 // sequence's end would lose the short decays to the long sums.  Followed from chunk to chunk the
 // sums' errors stay, and a per-head decay's gradient adds them up over all tokens: every 1024
 // tokens S is kept for the backward walk, which forms <G, e^L_C S> anew (2 x 32 x 8192 x 128
-// with per-head decays: 8e-7 off; 4.5e-6 without, growing with the length to the power 1.5).
+// with per-head decays: 6e-7 off; 4.5e-6 without, growing with the length to the power 1.5).
 //
 // Precision.  Products run in bf16 with fp32 sums.  With bf16 inputs and outputs the
 // decayed scores and the states round once to bf16 as operands (the state itself
@@ -86,25 +88,22 @@ struct ChunkBwd {
   }
 };
 
-// T: element type; D: padded width (d_k, d_v <= D); C: tokens of a chunk; NI: planes of q
-// and k after phi; NM: planes of the states and of what enters them.
-template <typename T_, int D_, int C_, int NI_, int NM_> struct BwdConfig {
+// T: element type; D: padded width (d_k, d_v <= D).
+template <typename T_, int D_> struct BwdConfig {
   using T = T_;
-  static constexpr int D = D_, C = C_, NI = NI_, NM = NM_;
-  static constexpr int NV = sizeof(T) == 2 ? 1 : NI;  // of v and dO, which are not mapped
-  static constexpr int NO = NI == 1 ? 1 : 3;          // planes of scores
+  static constexpr int D = D_, C = 32;         // C: tokens of a chunk
+  static constexpr int NP = 3;                 // planes: of q and k after phi, scores, states
+  static constexpr int NV = sizeof(T) == 2 ? 1 : NP;  // of v and dO, which are not mapped
   static constexpr int WARPS = D / 16;         // each owns 16 rows of the state
   static constexpr int ROWS = C / 16;          // groups of 16 tokens
   static constexpr int SPLIT = WARPS / ROWS;   // warps that share a group, by columns
   static constexpr int COLS = D / SPLIT;       // columns of a warp's outputs
   static constexpr int THREADS = WARPS * 32;
-  // Tiles of the next chunk arrive while this one is worked on.
-  static constexpr int STAGES = sizeof(T) == 2 && NI == 1 ? 2 : 1;
   static constexpr int BLOCKS = D == 64 ? 3 : 1;  // to an SM
   // Three planes of scores are six products: the warps of a group form 8 of their columns each
   // and share them in shared memory, where four do (2 x 16 x 4096 x 128 fp32: 1131 us; each
   // for itself 1237).  At D = 64 two warps share a group, and three blocks an SM.
-  static constexpr bool SHARE = NI == 3 && SPLIT == C / 8;
+  static constexpr bool SHARE = SPLIT == C / 8;
   static constexpr uint32_t SCORE_ROW = C * 2 + 16, SCORES = C * SCORE_ROW;  // bytes
   static constexpr uint32_t TILE = C * D * 2;  // bytes of one plane
   static constexpr uint32_t STATE = D * D * 2;
@@ -162,18 +161,8 @@ __device__ __forceinline__ void chunk_decay(const ChunkBwd &p, int seq, int c, C
   if (t == 0) s.all = exp2_two(end);
 }
 
-__device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src, bool live) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(live ? 16 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async_done() {
-  asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
-}
-
-// Rows t0 .. t0 + C - 1 of a [L, width] tensor into a tile; zeros past the last token
-// and past the width.  phi (if MAP) is applied on the way where the planes are
-// formed here, and by map_tile afterwards where the copy is asynchronous.
+// Rows t0 .. t0 + C - 1 of a [L, width] tensor as a tile's planes, after phi if MAP; zeros past
+// the last token and past the width.
 template <typename F, bool MAP>
 __device__ __forceinline__ void load_tile(uint32_t tile, const void *src, const ChunkBwd &p,
                                           int width, int t0) {
@@ -187,50 +176,22 @@ __device__ __forceinline__ void load_tile(uint32_t tile, const void *src, const 
     const bool live = t0 + r < p.L && c < width;
     const T *from = rows + (live ? (long long)(t0 + r) * width + c : 0);
     const uint32_t to = tile + tile_offset<F::D>(r, c);
-    if constexpr (F::STAGES == 2) {
-      cp_async_16(to, from, live);
-    } else {
-      float f[8];
-      if constexpr (sizeof(T) == 2) load_raw<T, 8>(from).unpack(f);
-      else load_raw<T, 4>(from).unpack(f), load_raw<T, 4>(from + 4).unpack(f + 4);
-      constexpr int NP = MAP ? F::NI : F::NV;
-      uint32_t out[NP][4];
+    float f[8];
+    if constexpr (sizeof(T) == 2) load_raw<T, 8>(from).unpack(f);
+    else load_raw<T, 4>(from).unpack(f), load_raw<T, 4>(from + 4).unpack(f + 4);
+    constexpr int NP = MAP ? F::NP : F::NV;
+    uint32_t out[NP][4];
 #pragma unroll
-      for (int e = 0; e < 8; e += 2) {
-        const float x = live ? MAP ? feature_map_precise(p.phi, f[e]) : f[e] : 0.f;
-        const float y = live ? MAP ? feature_map_precise(p.phi, f[e + 1]) : f[e + 1] : 0.f;
-        split<NP>(x, y, &out[0][e / 2], 4);
-      }
-#pragma unroll
-      for (int n = 0; n < NP; ++n)
-        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(to + n * F::TILE),
-                     "r"(out[n][0]), "r"(out[n][1]), "r"(out[n][2]), "r"(out[n][3])
-                     : "memory");
+    for (int e = 0; e < 8; e += 2) {
+      const float x = live ? MAP ? feature_map_precise(p.phi, f[e]) : f[e] : 0.f;
+      const float y = live ? MAP ? feature_map_precise(p.phi, f[e + 1]) : f[e + 1] : 0.f;
+      split<NP>(x, y, &out[0][e / 2], 4);
     }
-  }
-}
-
-// phi = elu + 1 of a tile that arrived as it is, rounded to bf16; rows past the last
-// token stay zero.
-template <typename F>
-__device__ __forceinline__ void map_tile(uint32_t tile, const ChunkBwd &p, int width, int t0) {
-  constexpr int VECS = F::C * F::D / 8;
 #pragma unroll
-  for (int i = 0; i < VECS / F::THREADS; ++i) {
-    const int vec = threadIdx.x + i * F::THREADS;
-    const int r = vec / (F::D / 8), c = vec % (F::D / 8) * 8;
-    if (t0 + r >= p.L || c >= width) continue;
-    const uint32_t at = tile + tile_offset<F::D>(r, c);
-    uint32_t w[4];
-    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                 : "r"(at));
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      w[e] = pack_bf16(feature_map(p.phi, bf16_lo(w[e])), feature_map(p.phi, bf16_hi(w[e])));
-    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(w[0]), "r"(w[1]),
-                 "r"(w[2]), "r"(w[3])
-                 : "memory");
+    for (int n = 0; n < NP; ++n)
+      asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(to + n * F::TILE),
+                   "r"(out[n][0]), "r"(out[n][1]), "r"(out[n][2]), "r"(out[n][3])
+                   : "memory");
   }
 }
 
@@ -267,11 +228,11 @@ template <typename F> struct StateRows {
     for (int n = 0; n < F::D / 8; ++n)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        uint32_t w[F::NM];
-        split<F::NM>(c[n][2 * h], c[n][2 * h + 1], w, 1);
+        uint32_t w[F::NP];
+        split<F::NP>(c[n][2 * h], c[n][2 * h + 1], w, 1);
         const uint32_t at = tile_offset<F::D>(warp * 16 + lane / 4 + 8 * h, n * 8 + lane % 4 * 2);
 #pragma unroll
-        for (int m = 0; m < F::NM; ++m)
+        for (int m = 0; m < F::NP; ++m)
           *reinterpret_cast<uint32_t *>(tile + m * F::STATE + at) = w[m];
       }
   }
@@ -280,12 +241,12 @@ template <typename F> struct StateRows {
   // cores' cuts would add up over the chunks.
   __device__ __forceinline__ void update(uint32_t x, uint32_t y, const float *weight, float2 all,
                                          int warp, int lane) {
-    uint32_t w[F::C / 16][F::NM][4];
+    uint32_t w[F::C / 16][F::NP][4];
 #pragma unroll
     for (int k = 0; k < F::C / 16; ++k) {
-      uint32_t a[F::NI][4];
+      uint32_t a[F::NP][4];
 #pragma unroll
-      for (int i = 0; i < F::NI; ++i)
+      for (int i = 0; i < F::NP; ++i)
         frag_a_t<F::D>(a[i], x + i * F::TILE, warp * 16, k * 16, lane);
 #pragma unroll
       for (int r = 0; r < 4; ++r) {  // registers 2 and 3 hold the tokens 8 further on
@@ -293,8 +254,8 @@ template <typename F> struct StateRows {
             *reinterpret_cast<const float2 *>(weight + k * 16 + (r / 2) * 8 + lane % 4 * 2);
         float lo = 0.f, hi = 0.f;
 #pragma unroll
-        for (int i = F::NI - 1; i >= 0; --i) lo += bf16_lo(a[i][r]), hi += bf16_hi(a[i][r]);
-        split<F::NM>(lo * f.x, hi * f.y, &w[k][0][r], 4);
+        for (int i = F::NP - 1; i >= 0; --i) lo += bf16_lo(a[i][r]), hi += bf16_hi(a[i][r]);
+        split<F::NP>(lo * f.x, hi * f.y, &w[k][0][r], 4);
       }
     }
 #pragma unroll
@@ -306,14 +267,14 @@ template <typename F> struct StateRows {
 #pragma unroll
         for (int i = 0; i < F::NV; ++i)
           frag_b_t<F::D>(b[i], y + i * F::TILE, n * 8, k * 16, lane);
-        mma_planes<F::NM, F::NV>(sum[0], sum[1], small[0], small[1], w[k], b);
+        mma_planes<F::NP, F::NV>(sum[0], sum[1], small[0], small[1], w[k], b);
       }
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           c[n + j][e] = decayed_sum(all, c[n + j][e],
-                                    F::NM > 1 ? sum[j][e] + small[j][e] : sum[j][e]);
+                                    sum[j][e] + small[j][e]);
     }
   }
 };
@@ -325,7 +286,7 @@ template <typename F> __device__ __forceinline__ float plane_sum(const char *til
   const uint32_t at = tile_offset<F::D>(e / F::D, e % F::D);
   float s = 0.f;
 #pragma unroll
-  for (int m = F::NM - 1; m >= 0; --m)
+  for (int m = F::NP - 1; m >= 0; --m)
     s += __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(tile + m * F::STATE + at));
   return s;
 }
@@ -431,18 +392,18 @@ __device__ __forceinline__ void score_tile(float (&acc)[4], uint32_t x, int m0, 
 // Scores as planes of an operand: from accumulators (tiles of 8 tokens), and by shared memory,
 // from 16 x 8 tiles.
 template <typename F>
-__device__ __forceinline__ void score_frag(uint32_t (&a)[F::NO][4], const float (&w)[F::C / 8][4],
+__device__ __forceinline__ void score_frag(uint32_t (&a)[F::NP][4], const float (&w)[F::C / 8][4],
                                            int j) {
-  split<F::NO>(w[2 * j][0], w[2 * j][1], &a[0][0], 4);
-  split<F::NO>(w[2 * j][2], w[2 * j][3], &a[0][1], 4);
-  split<F::NO>(w[2 * j + 1][0], w[2 * j + 1][1], &a[0][2], 4);
-  split<F::NO>(w[2 * j + 1][2], w[2 * j + 1][3], &a[0][3], 4);
+  split<F::NP>(w[2 * j][0], w[2 * j][1], &a[0][0], 4);
+  split<F::NP>(w[2 * j][2], w[2 * j][3], &a[0][1], 4);
+  split<F::NP>(w[2 * j + 1][0], w[2 * j + 1][1], &a[0][2], 4);
+  split<F::NP>(w[2 * j + 1][2], w[2 * j + 1][3], &a[0][3], 4);
 }
 template <typename F>
-__device__ __forceinline__ void score_frag(uint32_t (&a)[F::NO][4], uint32_t scores, int m0, int j,
+__device__ __forceinline__ void score_frag(uint32_t (&a)[F::NP][4], uint32_t scores, int m0, int j,
                                            int lane) {
 #pragma unroll
-  for (int m = 0; m < F::NO; ++m)
+  for (int m = 0; m < F::NP; ++m)
     ldsm4(a[m], scores + m * F::SCORES + (m0 + (lane & 15)) * F::SCORE_ROW +
                     (j * 16 + (lane >> 4) * 8) * 2);
 }
@@ -451,10 +412,10 @@ __device__ __forceinline__ void put_scores(char *scores, const float (&w)[4], in
                                            int lane) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    uint32_t o[F::NO];
-    split<F::NO>(w[2 * h], w[2 * h + 1], o, 1);
+    uint32_t o[F::NP];
+    split<F::NP>(w[2 * h], w[2 * h + 1], o, 1);
 #pragma unroll
-    for (int m = 0; m < F::NO; ++m)
+    for (int m = 0; m < F::NP; ++m)
       *reinterpret_cast<uint32_t *>(scores + m * F::SCORES + (m0 + lane / 4 + 8 * h) * F::SCORE_ROW +
                                     (n0 + lane % 4 * 2) * 2) = o[m];
   }
@@ -469,17 +430,17 @@ __device__ __forceinline__ void scores_times_cols(float (&acc)[NT][4], Frag frag
 #pragma unroll
   for (int j = 0; j < F::C / 16; ++j) {
     if (!live(j)) continue;
-    uint32_t a[F::NO][4];
+    uint32_t a[F::NP][4];
     frag(a, j);
 #pragma unroll
     for (int n = 0; n < NT; n += 2) {
       uint32_t b[NY][4];
 #pragma unroll
       for (int i = 0; i < NY; ++i) frag_b_t<F::D>(b[i], y + i * F::TILE, n0 + n * 8, j * 16, lane);
-      mma_planes<F::NO, NY>(acc[n], acc[n + 1], small[n], small[n + 1], a, b);
+      mma_planes<F::NP, NY>(acc[n], acc[n + 1], small[n], small[n + 1], a, b);
     }
   }
-  add_small<(F::NO > 1 || NY > 1)>(acc, small);
+  add_small<true>(acc, small);
 }
 
 // A warp's 16 x COLS outputs to rows t0 + r0 + .. of a [L, width] tensor; with phi = elu + 1
@@ -551,14 +512,14 @@ template <typename F> constexpr uint32_t bwd_shared_bytes() {
 
 // The segment's own share of S (blockIdx.y = 0: segments 0 .. n - 2) or of G (1: segments 1 .. n - 1).
 template <typename F> constexpr uint32_t share_smem() {
-  return bwd_shared_bytes<F>() + F::STAGES * (F::NI + F::NV) * F::TILE;
+  return bwd_shared_bytes<F>() + (F::NP + F::NV) * F::TILE;
 }
 template <typename F>
 __global__ void __launch_bounds__(F::THREADS) segment_share_kernel(const ChunkBwd p) {
   extern __shared__ __align__(128) char smem[];
   auto &sh = *reinterpret_cast<BwdShared<F> *>(smem);
   const uint32_t tiles = smem_u32(smem) + bwd_shared_bytes<F>();
-  constexpr uint32_t X = F::NI * F::TILE, STAGE = X + F::NV * F::TILE;
+  constexpr uint32_t X = F::NP * F::TILE, STAGE = X + F::NV * F::TILE;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int seq = blockIdx.x / (p.segments - 1), of = blockIdx.x % (p.segments - 1);
   const bool back = blockIdx.y != 0;
@@ -570,25 +531,18 @@ __global__ void __launch_bounds__(F::THREADS) segment_share_kernel(const ChunkBw
   const T *y = static_cast<const T *>(back ? p.dO : p.v) + ev;
   auto token = [&](int i) { return (back ? c1 - 1 - i : c0 + i) * F::C; };
   auto load = [&](int i) {
-    const uint32_t at = tiles + (F::STAGES == 2 ? (i & 1) * STAGE : 0);
+    const uint32_t at = tiles;
     load_tile<F, true>(at, x, p, p.n_k, token(i));
     load_tile<F, false>(at + X, y, p, p.n_v, token(i));
   };
   StateRows<F> state;
   state.load(nullptr, p, warp, lane);
   double total = 0.0;
-  if (F::STAGES == 2) load(0);
   for (int i = 0; i < n; ++i) {
-    const uint32_t at = tiles + (F::STAGES == 2 ? (i & 1) * STAGE : 0);
-    if (F::STAGES == 1) load(i);
+    const uint32_t at = tiles;
+    load(i);
     chunk_decay<F::C>(p, seq, token(i) / F::C, sh.decay);
-    cp_async_done();
     __syncthreads();
-    if (F::STAGES == 2 && p.phi == LA_PHI_ELU1) {
-      map_tile<F>(at, p, p.n_k, token(i));
-      __syncthreads();
-    }
-    if (F::STAGES == 2 && i + 1 < n) load(i + 1);
     total += (double)sh.decay.lam[F::C - 1].x + sh.decay.lam[F::C - 1].y;
     state.update(at, at + X, back ? sh.decay.head : sh.decay.tail, sh.decay.all, warp, lane);
     __syncthreads();
@@ -601,17 +555,17 @@ __global__ void __launch_bounds__(F::THREADS) segment_share_kernel(const ChunkBw
 
 // dq: a walk forward over a segment's chunks.
 template <typename F> constexpr uint32_t grad_q_smem() {
-  return bwd_shared_bytes<F>() + F::STAGES * (F::NI + 2 * F::NV) * F::TILE + F::NM * F::STATE +
-         F::SHARE * F::NO * F::SCORES;
+  return bwd_shared_bytes<F>() + (F::NP + 2 * F::NV) * F::TILE + F::NP * F::STATE +
+         F::SHARE * F::NP * F::SCORES;
 }
 template <typename F>
 __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_q_kernel(const ChunkBwd p) {
   extern __shared__ __align__(128) char smem[];
   auto &sh = *reinterpret_cast<BwdShared<F> *>(smem);
   char *state_tile = smem + bwd_shared_bytes<F>();
-  const uint32_t S = smem_u32(state_tile), tiles = S + F::NM * F::STATE;
-  constexpr uint32_t X = F::NI * F::TILE, Y = F::NV * F::TILE, STAGE = X + 2 * Y;
-  char *scores = state_tile + F::NM * F::STATE + F::STAGES * STAGE;
+  const uint32_t S = smem_u32(state_tile), tiles = S + F::NP * F::STATE;
+  constexpr uint32_t X = F::NP * F::TILE, Y = F::NV * F::TILE, STAGE = X + 2 * Y;
+  char *scores = state_tile + F::NP * F::STATE + STAGE;
   constexpr int NT = F::COLS / 8;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int group = warp % F::ROWS, part = warp / F::ROWS;
@@ -624,29 +578,22 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_q_kernel(const Chu
   const T *k = static_cast<const T *>(p.k) + ek, *v = static_cast<const T *>(p.v) + ev;
   const T *q = static_cast<const T *>(p.q) + ek, *dO = static_cast<const T *>(p.dO) + ev;
   auto load = [&](int c) {
-    const uint32_t at = tiles + (F::STAGES == 2 ? (c & 1) * STAGE : 0);
+    const uint32_t at = tiles;
     load_tile<F, true>(at, k, p, p.n_k, c * F::C);
     load_tile<F, false>(at + X, v, p, p.n_v, c * F::C);
     load_tile<F, false>(at + X + Y, dO, p, p.n_v, c * F::C);
   };
   StateRows<F> state;
-  if (F::STAGES == 2) load(c0);
   state.load(seg ? p.U + ((size_t)seq * (p.segments - 1) + seg - 1) * es
                  : p.S0 ? p.S0 + (size_t)seq * es : nullptr, p, warp, lane);
   state.planes(state_tile, warp, lane);
   for (int c = c0; c < c1; ++c) {
     const int t0 = c * F::C;
-    const uint32_t tk = tiles + (F::STAGES == 2 ? (c & 1) * STAGE : 0), tv = tk + X, td = tv + Y;
-    if (F::STAGES == 1) load(c);
+    const uint32_t tk = tiles, tv = tk + X, td = tv + Y;
+    load(c);
     chunk_decay<F::C>(p, seq, c, sh.decay);
-    cp_async_done();
     __syncthreads();
-    if (F::STAGES == 2 && p.phi == LA_PHI_ELU1) {
-      map_tile<F>(tk, p, p.n_k, t0);
-      __syncthreads();
-    }
-    if (F::STAGES == 2 && c + 1 < c1) load(c + 1);
-    if (F::NM == 3 && p.keeps(c, c1))
+    if (p.keeps(c, c1))
       keep_state<F>(p.kept + p.keep_slot(seq, c) * F::D * F::D, state_tile);
     // dO V^T . D: rows j of the group, tokens i <= j
     float w[F::C / 8][4] = {};
@@ -675,7 +622,7 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_q_kernel(const Chu
       }
     }
     float acc[NT][4] = {};
-    rows_times_rows<F, NT, F::NV, F::NM>(acc, td, F::TILE, r0, S, F::STATE, n0, lane,
+    rows_times_rows<F, NT, F::NV, F::NP>(acc, td, F::TILE, r0, S, F::STATE, n0, lane,
                                          [](int) { return true; });
     const float h0 = sh.decay.head[r0 + lane / 4], h1 = sh.decay.head[r0 + lane / 4 + 8];
 #pragma unroll
@@ -688,11 +635,11 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_q_kernel(const Chu
       }
     }
     if (F::SHARE) __syncthreads();
-    auto frag = [&](uint32_t (&a)[F::NO][4], int j) {
+    auto frag = [&](uint32_t (&a)[F::NP][4], int j) {
       if constexpr (F::SHARE) score_frag<F>(a, smem_u32(scores), r0, j, lane);
       else score_frag<F>(a, w, j);
     };
-    scores_times_cols<F, NT, F::NI>(acc, frag, tk, n0, lane, live);
+    scores_times_cols<F, NT, F::NP>(acc, frag, tk, n0, lane, live);
     store_rows<F, NT>(acc, static_cast<T *>(p.dq) + ek, q, p, p.n_k, t0 + r0, n0, lane);
     float around = 0.f;
     if (c + 1 < c1) {
@@ -730,17 +677,17 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_q_kernel(const Chu
 
 // dk and dv: a walk backward over a segment's chunks.
 template <typename F> constexpr uint32_t grad_kv_smem() {
-  return bwd_shared_bytes<F>() + 2 * F::STAGES * (F::NI + F::NV) * F::TILE + F::NM * F::STATE +
-         2 * F::SHARE * F::NO * F::SCORES;
+  return bwd_shared_bytes<F>() + 2 * (F::NP + F::NV) * F::TILE + F::NP * F::STATE +
+         2 * F::SHARE * F::NP * F::SCORES;
 }
 template <typename F>
 __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_kv_kernel(const ChunkBwd p) {
   extern __shared__ __align__(128) char smem[];
   auto &sh = *reinterpret_cast<BwdShared<F> *>(smem);
   char *state_tile = smem + bwd_shared_bytes<F>();
-  const uint32_t G = smem_u32(state_tile), tiles = G + F::NM * F::STATE;
-  constexpr uint32_t X = F::NI * F::TILE, Y = F::NV * F::TILE, STAGE = 2 * (X + Y);
-  char *scores = state_tile + F::NM * F::STATE + F::STAGES * STAGE;
+  const uint32_t G = smem_u32(state_tile), tiles = G + F::NP * F::STATE;
+  constexpr uint32_t X = F::NP * F::TILE, Y = F::NV * F::TILE, STAGE = 2 * (X + Y);
+  char *scores = state_tile + F::NP * F::STATE + STAGE;
   constexpr int NT = F::COLS / 8, CT = F::C / 8;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int group = warp % F::ROWS, part = warp / F::ROWS;
@@ -753,32 +700,24 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_kv_kernel(const Ch
   const T *k = static_cast<const T *>(p.k) + ek, *v = static_cast<const T *>(p.v) + ev;
   const T *q = static_cast<const T *>(p.q) + ek, *dO = static_cast<const T *>(p.dO) + ev;
   auto load = [&](int c) {
-    const uint32_t at = tiles + (F::STAGES == 2 ? (c & 1) * STAGE : 0);
+    const uint32_t at = tiles;
     load_tile<F, true>(at, q, p, p.n_k, c * F::C);
     load_tile<F, true>(at + X, k, p, p.n_k, c * F::C);
     load_tile<F, false>(at + 2 * X, v, p, p.n_v, c * F::C);
     load_tile<F, false>(at + 2 * X + Y, dO, p, p.n_v, c * F::C);
   };
   StateRows<F> state;
-  if (F::STAGES == 2) load(c1 - 1);
   state.load(seg + 1 < p.segments ? p.W + ((size_t)seq * (p.segments - 1) + seg) * es
              : p.dSf ? p.dSf + (size_t)seq * es : nullptr, p, warp, lane);
   state.planes(state_tile, warp, lane);
   for (int c = c1 - 1; c >= c0; --c) {
     const int t0 = c * F::C;
-    const uint32_t tq = tiles + (F::STAGES == 2 ? (c & 1) * STAGE : 0);
+    const uint32_t tq = tiles;
     const uint32_t tk = tq + X, tv = tk + X, td = tv + Y;
-    if (F::STAGES == 1) load(c);
+    load(c);
     chunk_decay<F::C>(p, seq, c, sh.decay);
-    cp_async_done();
     __syncthreads();
-    if (F::STAGES == 2 && p.phi == LA_PHI_ELU1) {
-      map_tile<F>(tq, p, p.n_k, t0);
-      map_tile<F>(tk, p, p.n_k, t0);
-      __syncthreads();
-    }
-    if (F::STAGES == 2 && c > c0) load(c - 1);
-    if (F::NM == 3 && p.keeps(c, c1)) {
+    if (p.keeps(c, c1)) {
       float s = dot_kept<F>(p.kept + p.keep_slot(seq, c) * F::D * F::D, state_tile);
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
@@ -820,15 +759,15 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_kv_kernel(const Ch
       float sum[2] = {0.f, 0.f};
       if (live(part / 2)) {
         float x[4] = {}, y[4] = {};
-        score_tile<F, F::NI, F::NI>(x, tk, r0, tq, part * 8, lane);
+        score_tile<F, F::NP, F::NP>(x, tk, r0, tq, part * 8, lane);
         score_tile<F, F::NV, F::NV>(y, tv, r0, td, part * 8, lane);
         masked(x, y, part * 8, sum);
         put_scores<F>(scores, x, r0, part * 8, lane);
-        put_scores<F>(scores + F::NO * F::SCORES, y, r0, part * 8, lane);
+        put_scores<F>(scores + F::NP * F::SCORES, y, r0, part * 8, lane);
       }
       if (p.rc) put_cols(sum, part * 8);
     } else {
-      rows_times_rows<F, CT, F::NI, F::NI>(w, tk, F::TILE, r0, tq, F::TILE, 0, lane, live);
+      rows_times_rows<F, CT, F::NP, F::NP>(w, tk, F::TILE, r0, tq, F::TILE, 0, lane, live);
       rows_times_rows<F, CT, F::NV, F::NV>(dw, tv, F::TILE, r0, td, F::TILE, 0, lane, live);
 #pragma unroll
       for (int n = 0; n < CT; ++n) {
@@ -846,18 +785,18 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_kv_kernel(const Ch
           sh.pairs[F::SHARE ? part : 0][r0 + lane / 4 + 8 * h] = row_sum[h];
       }
     }
-    auto frag = [&](uint32_t (&a)[F::NO][4], int j) {
+    auto frag = [&](uint32_t (&a)[F::NP][4], int j) {
       if constexpr (F::SHARE) score_frag<F>(a, smem_u32(scores), r0, j, lane);
       else score_frag<F>(a, w, j);
     };
-    auto dfrag = [&](uint32_t (&a)[F::NO][4], int j) {
-      if constexpr (F::SHARE) score_frag<F>(a, smem_u32(scores) + F::NO * F::SCORES, r0, j, lane);
+    auto dfrag = [&](uint32_t (&a)[F::NP][4], int j) {
+      if constexpr (F::SHARE) score_frag<F>(a, smem_u32(scores) + F::NP * F::SCORES, r0, j, lane);
       else score_frag<F>(a, dw, j);
     };
     const float t_0 = sh.decay.tail[r0 + lane / 4], t_1 = sh.decay.tail[r0 + lane / 4 + 8];
     {
       float acc[NT][4] = {};
-      rows_times_cols<F, NT, F::NI, F::NO>(acc, tk, F::TILE, r0, G, F::STATE, n0, lane);
+      rows_times_cols<F, NT, F::NP, F::NP>(acc, tk, F::TILE, r0, G, F::STATE, n0, lane);
 #pragma unroll
       for (int n = 0; n < NT; ++n)
         acc[n][0] *= t_0, acc[n][1] *= t_0, acc[n][2] *= t_1, acc[n][3] *= t_1;
@@ -867,7 +806,7 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_kv_kernel(const Ch
     }
     {
       float acc[NT][4] = {};
-      rows_times_rows<F, NT, F::NV, F::NM>(acc, tv, F::TILE, r0, G, F::STATE, n0, lane,
+      rows_times_rows<F, NT, F::NV, F::NP>(acc, tv, F::TILE, r0, G, F::STATE, n0, lane,
                                            [](int) { return true; });
 #pragma unroll
       for (int n = 0; n < NT; ++n)
@@ -879,7 +818,7 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_kv_kernel(const Ch
           sh.rows[part][r0 + lane / 4 + 8] = d.y;
         }
       }
-      scores_times_cols<F, NT, F::NI>(acc, dfrag, tq, n0, lane, live);
+      scores_times_cols<F, NT, F::NP>(acc, dfrag, tq, n0, lane, live);
       store_rows<F, NT>(acc, static_cast<T *>(p.dk) + ek, k, p, p.n_k, t0 + r0, n0, lane);
     }
     const bool more = c > c0;
