@@ -41,7 +41,7 @@
 // where an fp32 output is wanted, enter as three planes too (v and dO of bf16 inputs as one).
 //
 // What bounds these kernels: mma.sync, 600 TFLOP/s at best, times six for three planes by three
-// (grad_kv of 3 x 5 x 777 x 64 x 128 fp32: the tensor pipe 40% busy, with two warps to a scheduler and
+// (grad_kv of 3 x 5 x 777 x 64 x 128 fp32: the tensor pipe 35% busy, with two warps to a scheduler and
 // a chunk's steps one after another).
 #pragma once
 

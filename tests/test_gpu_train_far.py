@@ -1,13 +1,22 @@
-"""Gradients of slow per-head decays over long sequences: one number a head, summed over every
-token, in which errors that stay from chunk to chunk would add up.  Needs a GB300."""
+"""Long sequences in the attention backward: slow per-head decays, whose gradient is one number a
+head, summed over every token, in which errors that stay from chunk to chunk would add up; and
+head widths that are padded on the way, cut into segments.  Needs a GB300."""
 import pytest
 import torch
 
 from causal_linear_attention_chunkwise_gb300 import api
+from tests.test_gpu_train import check_attn
 
 pytestmark = pytest.mark.gpu
 
 DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+@pytest.fixture(autouse=True)
+def _identity():
+    api.la_set_feature_map("identity")
+    yield
+    api.la_set_feature_map("identity")
 
 
 def head_decay_grad(q, k, v, dO, decay):
@@ -52,3 +61,35 @@ def test_slow_head_decays(dtype, dk, dv):
     api.la_device_status()
     want = head_decay_grad(q, k, v, dO, decay)
     assert (got - want).norm() <= 32 * 2.0 ** -24 * want.norm()
+
+
+@pytest.mark.parametrize("phi,kind,dk,dv", [
+    ("identity", "token", 16, 64), ("identity", "logit", 32, 16), ("identity", "head", 128, 64),
+    ("identity", "token", 64, 128), ("elu1", "none", 16, 32), ("elu1", "token", 32, 128)])
+def test_unequal_heads_in_segments(phi, kind, dk, dv):
+    """Widths that are padded on the way, in sequences that are cut; odd lengths."""
+    check_attn(1, 3, 3001, dk, dv, "bf16", phi, kind, states=True, seed=dk + dv)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dk,dv", [(16, 32), (64, 64), (128, 16)])
+def test_nothing_is_written_past_the_gradients(dtype, dk, dv):
+    B, H, L = 2, 3, 133
+    g = torch.Generator("cuda").manual_seed(9)
+    q, k = (torch.randn(B, H, L, dk, generator=g, device="cuda").to(DT[dtype]) for _ in range(2))
+    v, dO = (torch.randn(B, H, L, dv, generator=g, device="cuda").to(DT[dtype]) for _ in range(2))
+    decay = -0.1 * torch.rand(B, H, L, generator=g, device="cuda")
+    S0 = torch.randn(B, H, dk, dv, generator=g, device="cuda")
+    want = api.la_chunk_bwd(q, k, v, dO, decay_kind="token", decay=decay, S0=S0)
+    pads, outs = [], []
+    for t in want:
+        pad = torch.full((t.numel() + 128,), 7.0, dtype=t.dtype, device="cuda")
+        pads.append(pad)
+        outs.append(pad[64:-64].view(t.shape))
+    dq, dk_, dv_, dd, ds = outs
+    api.la_chunk_bwd(q, k, v, dO, decay_kind="token", decay=decay, S0=S0, dq=dq, dk=dk_, dv=dv_,
+                     ddecay=dd, dS0=ds)
+    api.la_device_status()
+    for t, out, pad in zip(want, outs, pads):
+        assert torch.equal(t, out)
+        assert (pad[:64] == 7).all() and (pad[-64:] == 7).all()
