@@ -7,6 +7,7 @@
 
 namespace la {
 
+cudaError_t launch_chunk_bwd_bf16(const ChunkBwd &p, int seqs, bool planes, cudaStream_t stream);
 cudaError_t launch_chunk_bwd_tc(const ChunkBwd &p, int seqs, bool planes, cudaStream_t stream);
 cudaError_t launch_chunk_bwd_f32(const ChunkBwd &p, int seqs, bool wide, bool bf16,
                                  cudaStream_t stream);
@@ -15,11 +16,13 @@ namespace {
 
 constexpr int kMaxPer = 512;  // chunks of a segment (the decays' kernel keeps sums of them)
 constexpr int kKeep = 1024;   // tokens from one kept state to the next
+constexpr int kShort = 64;    // tokens of the bf16 kernels' one chunk
 
 // How a call runs: which planes, the chunk, the segments.
 struct Plan {
-  bool tc;      // the tcgen05 kernels; else q and k, after phi, as three planes
+  bool tc;      // the tcgen05 kernels
   bool wide;    // padded width 128, else 64
+  bool full;    // inputs as three planes
   bool planes;  // states as three planes
   int chunk, chunks, segments, per;
 };
@@ -29,14 +32,20 @@ struct Plan {
 // segment also the pass over their own shares, S and G in blocks of their own at 0.2 of a chunk's
 // time, and two launches.  It picks 2 segments for 2 x 32 x 8192 x 128 with decays (517 us; 1: 813,
 // 4: 588, 7: 610), 9 for 1 x 16 x 32768 x 128 (543; 4: 969, 19: 571), 2 for 4 x 16 x 4096 x 64
-// (130; 1: 189, 4: 140), 9 for 3 x 5 x 777 x 64 x 128 fp32 (103; 5: 141, 13: 125),
+// (130; 1: 189, 4: 140), 9 for 3 x 5 x 777 x 64 x 128 fp32 (103 when
+// compared, 100 now; 5: 141, 13: 125),
 // and a chunk each for one sequence of 300 tokens in fp32 (17; 5: 28, 1: 102).
 Plan make_plan(const ChunkBwdArgs &a, bool f32_out) {
   Plan p;
   p.wide = std::max(a.dk, a.dv) > 64;
-  p.tc = a.dtype == LA_BF16 && !(f32_out && a.phi == LA_PHI_ELU1);
-  p.planes = !p.tc || f32_out;
-  p.chunk = p.tc ? 128 : 32;
+  p.full = a.dtype == LA_F32 || (f32_out && a.phi == LA_PHI_ELU1);
+  p.planes = p.full || f32_out;
+  // More narrow sequences of up to 64 tokens than there are SMs: tcgen05's block, of which an SM holds
+  // one, stands alone with its start, its end and its few products.  64 x 32 x 64 x 64 with token
+  // decays 166 us, on tcgen05 252 (elu1 without: 110, 132); 8 x 32 x 64 x 64 30, 37; but 4 x 32 x 64
+  // x 64 25, 21; 64 x 32 x 96 x 64 276, 256; 64 x 32 x 64 x 128 457, 458 (167, 137 without decays).
+  p.tc = !p.full && !(a.L <= kShort && !p.wide && (long long)a.B * a.H > 152);
+  p.chunk = p.tc ? 128 : p.full ? 32 : kShort;
   p.chunks = (a.L + p.chunk - 1) / p.chunk;
   const long long seqs = (long long)a.B * a.H;
   const long long slots = 152ll * (p.wide || p.tc ? 1 : 3);
@@ -380,16 +389,20 @@ cudaError_t launch_chunk_bwd(const ChunkBwdArgs &a) {
   lay_out(a, plan, decay_grad, static_cast<char *>(a.workspace), &p, &by_segment);
   cudaError_t e = cudaSuccess;
   if (a.decay_kind != LA_DECAY_NONE)
-    e = plan.tc ? launch_chunk_decay<128>(p, (int)seqs, a.stream)
-                : launch_chunk_decay<32>(p, (int)seqs, a.stream);
+    e = plan.chunk == 128  ? launch_chunk_decay<128>(p, (int)seqs, a.stream)
+        : plan.chunk == 64 ? launch_chunk_decay<64>(p, (int)seqs, a.stream)
+                           : launch_chunk_decay<32>(p, (int)seqs, a.stream);
   if (e != cudaSuccess) return e;
   e = plan.tc ? launch_chunk_bwd_tc(p, (int)seqs, plan.planes, a.stream)
-              : launch_chunk_bwd_f32(p, (int)seqs, plan.wide, a.dtype == LA_BF16, a.stream);
+      : plan.full ? launch_chunk_bwd_f32(p, (int)seqs, plan.wide, a.dtype == LA_BF16, a.stream)
+                  : launch_chunk_bwd_bf16(p, (int)seqs, plan.planes, a.stream);
   if (e != cudaSuccess || !decay_grad) return e;
-  if (plan.tc)
+  if (plan.chunk == 128)
     decay_grad_kernel<128, 32><<<(unsigned)blocks, 32 * kDecayWarps, 0, a.stream>>>(p, a.ddecay, by_segment);
-  else
+  else if (plan.chunk == 32)
     decay_grad_kernel<32, 32><<<(unsigned)blocks, 32 * kDecayWarps, 0, a.stream>>>(p, a.ddecay, by_segment);
+  else
+    decay_grad_kernel<64, 64><<<(unsigned)blocks, 32 * kDecayWarps, 0, a.stream>>>(p, a.ddecay, by_segment);
   if ((e = cudaGetLastError()) != cudaSuccess || a.decay_kind != LA_DECAY_HEAD) return e;
   head_decay_kernel<<<a.H, 32, 0, a.stream>>>(by_segment, a.ddecay, a.B, a.H, plan.segments);
   return cudaGetLastError();

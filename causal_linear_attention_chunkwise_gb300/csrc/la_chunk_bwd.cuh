@@ -18,11 +18,11 @@
 // sequence is cut into segments that run side by side: a first kernel forms every
 // segment's own share of S and G, a second one strings them together.
 //
-// bf16 tensors run in la_chunk_bwd_tc.cu.  The kernels here take what enters as three bf16 planes,
-// fp32 tensors and phi = elu + 1 where an fp32 output is wanted: three planes of 128 tokens do
-// not fit beside one another there.  A warp owns 16 tokens of a 32-token chunk (with others, which
-// take other columns) and computes its rows of the score matrices in the orientation
-// that its products need (dO V^T for dq, V dO^T and K Q^T for dk and dv).
+// Most bf16 calls run in la_chunk_bwd_tc.cu.  The kernels here take what enters as three bf16 planes,
+// fp32 tensors and phi = elu + 1 where an fp32 output is wanted (three planes of 128 tokens do
+// not fit beside one another there), and many short bf16 sequences.  A warp owns 16 tokens of a
+// chunk (with others, which take other columns) and computes its rows of the score matrices in the
+// orientation that its products need (dO V^T for dq, V dO^T and K Q^T for dk and dv).
 //
 // A decay's gradient counts the pairs (i < t <= j) that it lies between: pairs within
 // the chunk (row and column sums of Q K^T . dO V^T . D), pairs with one token in it (dot
@@ -88,12 +88,13 @@ struct ChunkBwd {
   }
 };
 
-// T: element type; D: padded width (d_k, d_v <= D).
-template <typename T_, int D_> struct BwdConfig {
+// T: element type; D: padded width (d_k, d_v <= D); C: tokens of a chunk; NI: planes of q
+// and k after phi; NM: planes of the states and of what enters them.
+template <typename T_, int D_, int C_, int NI_, int NM_> struct BwdConfig {
   using T = T_;
-  static constexpr int D = D_, C = 32;         // C: tokens of a chunk
-  static constexpr int NP = 3;                 // planes: of q and k after phi, scores, states
-  static constexpr int NV = sizeof(T) == 2 ? 1 : NP;  // of v and dO, which are not mapped
+  static constexpr int D = D_, C = C_, NI = NI_, NM = NM_;
+  static constexpr int NV = sizeof(T) == 2 ? 1 : NI;  // of v and dO, which are not mapped
+  static constexpr int NO = NI == 1 ? 1 : 3;          // planes of scores
   static constexpr int WARPS = D / 16;         // each owns 16 rows of the state
   static constexpr int ROWS = C / 16;          // groups of 16 tokens
   static constexpr int SPLIT = WARPS / ROWS;   // warps that share a group, by columns
@@ -101,9 +102,9 @@ template <typename T_, int D_> struct BwdConfig {
   static constexpr int THREADS = WARPS * 32;
   static constexpr int BLOCKS = D == 64 ? 3 : 1;  // to an SM
   // Three planes of scores are six products: the warps of a group form 8 of their columns each
-  // and share them in shared memory, where four do (2 x 16 x 4096 x 128 fp32: 1131 us; each
-  // for itself 1237).  At D = 64 two warps share a group, and three blocks an SM.
-  static constexpr bool SHARE = SPLIT == C / 8;
+  // and share them in shared memory, where four do (2 x 16 x 4096 x 128 fp32: 1237 us before,
+  // 1131 after).  At D = 64 two warps share a group, and three blocks an SM.
+  static constexpr bool SHARE = NI == 3 && SPLIT == C / 8;
   static constexpr uint32_t SCORE_ROW = C * 2 + 16, SCORES = C * SCORE_ROW;  // bytes
   static constexpr uint32_t TILE = C * D * 2;  // bytes of one plane
   static constexpr uint32_t STATE = D * D * 2;
@@ -161,39 +162,63 @@ __device__ __forceinline__ void chunk_decay(const ChunkBwd &p, int seq, int c, C
   if (t == 0) s.all = exp2_two(end);
 }
 
-// Rows t0 .. t0 + C - 1 of a [L, width] tensor as a tile's planes, after phi if MAP; zeros past
-// the last token and past the width.
-template <typename F, bool MAP>
-__device__ __forceinline__ void load_tile(uint32_t tile, const void *src, const ChunkBwd &p,
-                                          int width, int t0) {
+// Rows t0 .. t0 + C - 1 of a [L, width] tensor on their way to a tile's planes, after phi if
+// MAP; zeros past the last token and past the width.  All of a chunk's tiles are fetched before the
+// first is put: a fetch behind a put would wait for the one before it (2 x 16 x 4096 x 128
+// fp32 with token decays: 1053 us; tile by tile 1126).
+template <typename F> struct TileRows {
   using T = typename F::T;
-  constexpr int VECS = F::C * F::D / 8;
-  const T *rows = static_cast<const T *>(src);
-#pragma unroll
-  for (int i = 0; i < VECS / F::THREADS; ++i) {
+  static constexpr int N = F::C * F::D / 8 / F::THREADS, V = 16 / sizeof(T), K = 8 / V;
+  Raw<T, V> v[N][K];
+
+  __device__ __forceinline__ static bool place(const ChunkBwd &p, int width, int t0, int i, int &row,
+                                               int &col) {
     const int vec = threadIdx.x + i * F::THREADS;
-    const int r = vec / (F::D / 8), c = vec % (F::D / 8) * 8;
-    const bool live = t0 + r < p.L && c < width;
-    const T *from = rows + (live ? (long long)(t0 + r) * width + c : 0);
-    const uint32_t to = tile + tile_offset<F::D>(r, c);
-    float f[8];
-    if constexpr (sizeof(T) == 2) load_raw<T, 8>(from).unpack(f);
-    else load_raw<T, 4>(from).unpack(f), load_raw<T, 4>(from + 4).unpack(f + 4);
-    constexpr int NP = MAP ? F::NP : F::NV;
-    uint32_t out[NP][4];
-#pragma unroll
-    for (int e = 0; e < 8; e += 2) {
-      const float x = live ? MAP ? feature_map_precise(p.phi, f[e]) : f[e] : 0.f;
-      const float y = live ? MAP ? feature_map_precise(p.phi, f[e + 1]) : f[e + 1] : 0.f;
-      split<NP>(x, y, &out[0][e / 2], 4);
-    }
-#pragma unroll
-    for (int n = 0; n < NP; ++n)
-      asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(to + n * F::TILE),
-                   "r"(out[n][0]), "r"(out[n][1]), "r"(out[n][2]), "r"(out[n][3])
-                   : "memory");
+    row = vec / (F::D / 8), col = vec % (F::D / 8) * 8;
+    return t0 + row < p.L && col < width;
   }
-}
+  __device__ __forceinline__ void fetch(const T *rows, const ChunkBwd &p, int width, int t0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      int row, col;
+      const bool live = place(p, width, t0, i, row, col);
+      const T *from = rows + (live ? (long long)(t0 + row) * width + col : 0);
+#pragma unroll
+      for (int k = 0; k < K; ++k) v[i][k] = load_raw<T, V>(from + k * V);
+    }
+  }
+  template <bool MAP>
+  __device__ __forceinline__ void put(uint32_t tile, const ChunkBwd &p, int width, int t0) const {
+    constexpr int NP = MAP ? F::NI : F::NV;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      int row, col;
+      const bool live = place(p, width, t0, i, row, col);
+      uint32_t out[NP][4];
+      if (NP == 1 && !(MAP && p.phi == LA_PHI_ELU1)) {  // bf16 as it is
+#pragma unroll
+        for (int e = 0; e < 4; ++e) out[0][e] = live ? v[i][0].w[e] : 0;
+      } else {
+        float f[8];
+#pragma unroll
+        for (int k = 0; k < K; ++k) v[i][k].unpack(f + k * V);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          if (MAP) f[e] = NP == 1 ? feature_map(p.phi, f[e]) : feature_map_precise(p.phi, f[e]);
+          f[e] = live ? f[e] : 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) split<NP>(f[2 * e], f[2 * e + 1], &out[0][e], 4);
+      }
+      const uint32_t to = tile + tile_offset<F::D>(row, col);
+#pragma unroll
+      for (int n = 0; n < NP; ++n)
+        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(to + n * F::TILE),
+                     "r"(out[n][0]), "r"(out[n][1]), "r"(out[n][2]), "r"(out[n][3])
+                     : "memory");
+    }
+  }
+};
 
 // A warp's 16 rows of a state, as accumulators: row g or g + 8, columns 8 n + 2 (lane % 4).
 template <typename F> struct StateRows {
@@ -228,11 +253,11 @@ template <typename F> struct StateRows {
     for (int n = 0; n < F::D / 8; ++n)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        uint32_t w[F::NP];
-        split<F::NP>(c[n][2 * h], c[n][2 * h + 1], w, 1);
+        uint32_t w[F::NM];
+        split<F::NM>(c[n][2 * h], c[n][2 * h + 1], w, 1);
         const uint32_t at = tile_offset<F::D>(warp * 16 + lane / 4 + 8 * h, n * 8 + lane % 4 * 2);
 #pragma unroll
-        for (int m = 0; m < F::NP; ++m)
+        for (int m = 0; m < F::NM; ++m)
           *reinterpret_cast<uint32_t *>(tile + m * F::STATE + at) = w[m];
       }
   }
@@ -241,12 +266,12 @@ template <typename F> struct StateRows {
   // cores' cuts would add up over the chunks.
   __device__ __forceinline__ void update(uint32_t x, uint32_t y, const float *weight, float2 all,
                                          int warp, int lane) {
-    uint32_t w[F::C / 16][F::NP][4];
+    uint32_t w[F::C / 16][F::NM][4];
 #pragma unroll
     for (int k = 0; k < F::C / 16; ++k) {
-      uint32_t a[F::NP][4];
+      uint32_t a[F::NI][4];
 #pragma unroll
-      for (int i = 0; i < F::NP; ++i)
+      for (int i = 0; i < F::NI; ++i)
         frag_a_t<F::D>(a[i], x + i * F::TILE, warp * 16, k * 16, lane);
 #pragma unroll
       for (int r = 0; r < 4; ++r) {  // registers 2 and 3 hold the tokens 8 further on
@@ -254,8 +279,8 @@ template <typename F> struct StateRows {
             *reinterpret_cast<const float2 *>(weight + k * 16 + (r / 2) * 8 + lane % 4 * 2);
         float lo = 0.f, hi = 0.f;
 #pragma unroll
-        for (int i = F::NP - 1; i >= 0; --i) lo += bf16_lo(a[i][r]), hi += bf16_hi(a[i][r]);
-        split<F::NP>(lo * f.x, hi * f.y, &w[k][0][r], 4);
+        for (int i = F::NI - 1; i >= 0; --i) lo += bf16_lo(a[i][r]), hi += bf16_hi(a[i][r]);
+        split<F::NM>(lo * f.x, hi * f.y, &w[k][0][r], 4);
       }
     }
 #pragma unroll
@@ -267,14 +292,14 @@ template <typename F> struct StateRows {
 #pragma unroll
         for (int i = 0; i < F::NV; ++i)
           frag_b_t<F::D>(b[i], y + i * F::TILE, n * 8, k * 16, lane);
-        mma_planes<F::NP, F::NV>(sum[0], sum[1], small[0], small[1], w[k], b);
+        mma_planes<F::NM, F::NV>(sum[0], sum[1], small[0], small[1], w[k], b);
       }
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           c[n + j][e] = decayed_sum(all, c[n + j][e],
-                                    sum[j][e] + small[j][e]);
+                                    F::NM > 1 ? sum[j][e] + small[j][e] : sum[j][e]);
     }
   }
 };
@@ -286,7 +311,7 @@ template <typename F> __device__ __forceinline__ float plane_sum(const char *til
   const uint32_t at = tile_offset<F::D>(e / F::D, e % F::D);
   float s = 0.f;
 #pragma unroll
-  for (int m = F::NP - 1; m >= 0; --m)
+  for (int m = F::NM - 1; m >= 0; --m)
     s += __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(tile + m * F::STATE + at));
   return s;
 }
@@ -392,18 +417,18 @@ __device__ __forceinline__ void score_tile(float (&acc)[4], uint32_t x, int m0, 
 // Scores as planes of an operand: from accumulators (tiles of 8 tokens), and by shared memory,
 // from 16 x 8 tiles.
 template <typename F>
-__device__ __forceinline__ void score_frag(uint32_t (&a)[F::NP][4], const float (&w)[F::C / 8][4],
+__device__ __forceinline__ void score_frag(uint32_t (&a)[F::NO][4], const float (&w)[F::C / 8][4],
                                            int j) {
-  split<F::NP>(w[2 * j][0], w[2 * j][1], &a[0][0], 4);
-  split<F::NP>(w[2 * j][2], w[2 * j][3], &a[0][1], 4);
-  split<F::NP>(w[2 * j + 1][0], w[2 * j + 1][1], &a[0][2], 4);
-  split<F::NP>(w[2 * j + 1][2], w[2 * j + 1][3], &a[0][3], 4);
+  split<F::NO>(w[2 * j][0], w[2 * j][1], &a[0][0], 4);
+  split<F::NO>(w[2 * j][2], w[2 * j][3], &a[0][1], 4);
+  split<F::NO>(w[2 * j + 1][0], w[2 * j + 1][1], &a[0][2], 4);
+  split<F::NO>(w[2 * j + 1][2], w[2 * j + 1][3], &a[0][3], 4);
 }
 template <typename F>
-__device__ __forceinline__ void score_frag(uint32_t (&a)[F::NP][4], uint32_t scores, int m0, int j,
+__device__ __forceinline__ void score_frag(uint32_t (&a)[F::NO][4], uint32_t scores, int m0, int j,
                                            int lane) {
 #pragma unroll
-  for (int m = 0; m < F::NP; ++m)
+  for (int m = 0; m < F::NO; ++m)
     ldsm4(a[m], scores + m * F::SCORES + (m0 + (lane & 15)) * F::SCORE_ROW +
                     (j * 16 + (lane >> 4) * 8) * 2);
 }
@@ -412,10 +437,10 @@ __device__ __forceinline__ void put_scores(char *scores, const float (&w)[4], in
                                            int lane) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    uint32_t o[F::NP];
-    split<F::NP>(w[2 * h], w[2 * h + 1], o, 1);
+    uint32_t o[F::NO];
+    split<F::NO>(w[2 * h], w[2 * h + 1], o, 1);
 #pragma unroll
-    for (int m = 0; m < F::NP; ++m)
+    for (int m = 0; m < F::NO; ++m)
       *reinterpret_cast<uint32_t *>(scores + m * F::SCORES + (m0 + lane / 4 + 8 * h) * F::SCORE_ROW +
                                     (n0 + lane % 4 * 2) * 2) = o[m];
   }
@@ -430,17 +455,17 @@ __device__ __forceinline__ void scores_times_cols(float (&acc)[NT][4], Frag frag
 #pragma unroll
   for (int j = 0; j < F::C / 16; ++j) {
     if (!live(j)) continue;
-    uint32_t a[F::NP][4];
+    uint32_t a[F::NO][4];
     frag(a, j);
 #pragma unroll
     for (int n = 0; n < NT; n += 2) {
       uint32_t b[NY][4];
 #pragma unroll
       for (int i = 0; i < NY; ++i) frag_b_t<F::D>(b[i], y + i * F::TILE, n0 + n * 8, j * 16, lane);
-      mma_planes<F::NP, NY>(acc[n], acc[n + 1], small[n], small[n + 1], a, b);
+      mma_planes<F::NO, NY>(acc[n], acc[n + 1], small[n], small[n + 1], a, b);
     }
   }
-  add_small<true>(acc, small);
+  add_small<(F::NO > 1 || NY > 1)>(acc, small);
 }
 
 // A warp's 16 x COLS outputs to rows t0 + r0 + .. of a [L, width] tensor; with phi = elu + 1
@@ -512,14 +537,14 @@ template <typename F> constexpr uint32_t bwd_shared_bytes() {
 
 // The segment's own share of S (blockIdx.y = 0: segments 0 .. n - 2) or of G (1: segments 1 .. n - 1).
 template <typename F> constexpr uint32_t share_smem() {
-  return bwd_shared_bytes<F>() + (F::NP + F::NV) * F::TILE;
+  return bwd_shared_bytes<F>() + (F::NI + F::NV) * F::TILE;
 }
 template <typename F>
 __global__ void __launch_bounds__(F::THREADS) segment_share_kernel(const ChunkBwd p) {
   extern __shared__ __align__(128) char smem[];
   auto &sh = *reinterpret_cast<BwdShared<F> *>(smem);
   const uint32_t tiles = smem_u32(smem) + bwd_shared_bytes<F>();
-  constexpr uint32_t X = F::NP * F::TILE, STAGE = X + F::NV * F::TILE;
+  constexpr uint32_t X = F::NI * F::TILE;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int seq = blockIdx.x / (p.segments - 1), of = blockIdx.x % (p.segments - 1);
   const bool back = blockIdx.y != 0;
@@ -531,20 +556,20 @@ __global__ void __launch_bounds__(F::THREADS) segment_share_kernel(const ChunkBw
   const T *y = static_cast<const T *>(back ? p.dO : p.v) + ev;
   auto token = [&](int i) { return (back ? c1 - 1 - i : c0 + i) * F::C; };
   auto load = [&](int i) {
-    const uint32_t at = tiles;
-    load_tile<F, true>(at, x, p, p.n_k, token(i));
-    load_tile<F, false>(at + X, y, p, p.n_v, token(i));
+    TileRows<F> a, b;
+    a.fetch(x, p, p.n_k, token(i)), b.fetch(y, p, p.n_v, token(i));
+    a.template put<true>(tiles, p, p.n_k, token(i));
+    b.template put<false>(tiles + X, p, p.n_v, token(i));
   };
   StateRows<F> state;
   state.load(nullptr, p, warp, lane);
   double total = 0.0;
   for (int i = 0; i < n; ++i) {
-    const uint32_t at = tiles;
     load(i);
     chunk_decay<F::C>(p, seq, token(i) / F::C, sh.decay);
     __syncthreads();
     total += (double)sh.decay.lam[F::C - 1].x + sh.decay.lam[F::C - 1].y;
-    state.update(at, at + X, back ? sh.decay.head : sh.decay.tail, sh.decay.all, warp, lane);
+    state.update(tiles, tiles + X, back ? sh.decay.head : sh.decay.tail, sh.decay.all, warp, lane);
     __syncthreads();
   }
   const size_t slot = (size_t)seq * (p.segments - 1) + of;
@@ -555,17 +580,17 @@ __global__ void __launch_bounds__(F::THREADS) segment_share_kernel(const ChunkBw
 
 // dq: a walk forward over a segment's chunks.
 template <typename F> constexpr uint32_t grad_q_smem() {
-  return bwd_shared_bytes<F>() + (F::NP + 2 * F::NV) * F::TILE + F::NP * F::STATE +
-         F::SHARE * F::NP * F::SCORES;
+  return bwd_shared_bytes<F>() + (F::NI + 2 * F::NV) * F::TILE + F::NM * F::STATE +
+         F::SHARE * F::NO * F::SCORES;
 }
 template <typename F>
 __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_q_kernel(const ChunkBwd p) {
   extern __shared__ __align__(128) char smem[];
   auto &sh = *reinterpret_cast<BwdShared<F> *>(smem);
   char *state_tile = smem + bwd_shared_bytes<F>();
-  const uint32_t S = smem_u32(state_tile), tiles = S + F::NP * F::STATE;
-  constexpr uint32_t X = F::NP * F::TILE, Y = F::NV * F::TILE, STAGE = X + 2 * Y;
-  char *scores = state_tile + F::NP * F::STATE + STAGE;
+  const uint32_t S = smem_u32(state_tile), tiles = S + F::NM * F::STATE;
+  constexpr uint32_t X = F::NI * F::TILE, Y = F::NV * F::TILE;
+  char *scores = state_tile + F::NM * F::STATE + X + 2 * Y;
   constexpr int NT = F::COLS / 8;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int group = warp % F::ROWS, part = warp / F::ROWS;
@@ -577,11 +602,12 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_q_kernel(const Chu
   using T = typename F::T;
   const T *k = static_cast<const T *>(p.k) + ek, *v = static_cast<const T *>(p.v) + ev;
   const T *q = static_cast<const T *>(p.q) + ek, *dO = static_cast<const T *>(p.dO) + ev;
-  auto load = [&](int c) {
-    const uint32_t at = tiles;
-    load_tile<F, true>(at, k, p, p.n_k, c * F::C);
-    load_tile<F, false>(at + X, v, p, p.n_v, c * F::C);
-    load_tile<F, false>(at + X + Y, dO, p, p.n_v, c * F::C);
+  auto load = [&](int t) {
+    TileRows<F> a, b, c;
+    a.fetch(k, p, p.n_k, t), b.fetch(v, p, p.n_v, t), c.fetch(dO, p, p.n_v, t);
+    a.template put<true>(tiles, p, p.n_k, t);
+    b.template put<false>(tiles + X, p, p.n_v, t);
+    c.template put<false>(tiles + X + Y, p, p.n_v, t);
   };
   StateRows<F> state;
   state.load(seg ? p.U + ((size_t)seq * (p.segments - 1) + seg - 1) * es
@@ -590,10 +616,10 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_q_kernel(const Chu
   for (int c = c0; c < c1; ++c) {
     const int t0 = c * F::C;
     const uint32_t tk = tiles, tv = tk + X, td = tv + Y;
-    load(c);
+    load(t0);
     chunk_decay<F::C>(p, seq, c, sh.decay);
     __syncthreads();
-    if (p.keeps(c, c1))
+    if (F::NI > 1 && p.keeps(c, c1))
       keep_state<F>(p.kept + p.keep_slot(seq, c) * F::D * F::D, state_tile);
     // dO V^T . D: rows j of the group, tokens i <= j
     float w[F::C / 8][4] = {};
@@ -622,7 +648,7 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_q_kernel(const Chu
       }
     }
     float acc[NT][4] = {};
-    rows_times_rows<F, NT, F::NV, F::NP>(acc, td, F::TILE, r0, S, F::STATE, n0, lane,
+    rows_times_rows<F, NT, F::NV, F::NM>(acc, td, F::TILE, r0, S, F::STATE, n0, lane,
                                          [](int) { return true; });
     const float h0 = sh.decay.head[r0 + lane / 4], h1 = sh.decay.head[r0 + lane / 4 + 8];
 #pragma unroll
@@ -635,11 +661,11 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_q_kernel(const Chu
       }
     }
     if (F::SHARE) __syncthreads();
-    auto frag = [&](uint32_t (&a)[F::NP][4], int j) {
+    auto frag = [&](uint32_t (&a)[F::NO][4], int j) {
       if constexpr (F::SHARE) score_frag<F>(a, smem_u32(scores), r0, j, lane);
       else score_frag<F>(a, w, j);
     };
-    scores_times_cols<F, NT, F::NP>(acc, frag, tk, n0, lane, live);
+    scores_times_cols<F, NT, F::NI>(acc, frag, tk, n0, lane, live);
     store_rows<F, NT>(acc, static_cast<T *>(p.dq) + ek, q, p, p.n_k, t0 + r0, n0, lane);
     float around = 0.f;
     if (c + 1 < c1) {
@@ -677,17 +703,17 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_q_kernel(const Chu
 
 // dk and dv: a walk backward over a segment's chunks.
 template <typename F> constexpr uint32_t grad_kv_smem() {
-  return bwd_shared_bytes<F>() + 2 * (F::NP + F::NV) * F::TILE + F::NP * F::STATE +
-         2 * F::SHARE * F::NP * F::SCORES;
+  return bwd_shared_bytes<F>() + 2 * (F::NI + F::NV) * F::TILE + F::NM * F::STATE +
+         2 * F::SHARE * F::NO * F::SCORES;
 }
 template <typename F>
 __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_kv_kernel(const ChunkBwd p) {
   extern __shared__ __align__(128) char smem[];
   auto &sh = *reinterpret_cast<BwdShared<F> *>(smem);
   char *state_tile = smem + bwd_shared_bytes<F>();
-  const uint32_t G = smem_u32(state_tile), tiles = G + F::NP * F::STATE;
-  constexpr uint32_t X = F::NP * F::TILE, Y = F::NV * F::TILE, STAGE = 2 * (X + Y);
-  char *scores = state_tile + F::NP * F::STATE + STAGE;
+  const uint32_t G = smem_u32(state_tile), tiles = G + F::NM * F::STATE;
+  constexpr uint32_t X = F::NI * F::TILE, Y = F::NV * F::TILE;
+  char *scores = state_tile + F::NM * F::STATE + 2 * (X + Y);
   constexpr int NT = F::COLS / 8, CT = F::C / 8;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int group = warp % F::ROWS, part = warp / F::ROWS;
@@ -699,12 +725,14 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_kv_kernel(const Ch
   using T = typename F::T;
   const T *k = static_cast<const T *>(p.k) + ek, *v = static_cast<const T *>(p.v) + ev;
   const T *q = static_cast<const T *>(p.q) + ek, *dO = static_cast<const T *>(p.dO) + ev;
-  auto load = [&](int c) {
-    const uint32_t at = tiles;
-    load_tile<F, true>(at, q, p, p.n_k, c * F::C);
-    load_tile<F, true>(at + X, k, p, p.n_k, c * F::C);
-    load_tile<F, false>(at + 2 * X, v, p, p.n_v, c * F::C);
-    load_tile<F, false>(at + 2 * X + Y, dO, p, p.n_v, c * F::C);
+  auto load = [&](int t) {
+    TileRows<F> a, b, c, d;
+    a.fetch(q, p, p.n_k, t), b.fetch(k, p, p.n_k, t);
+    c.fetch(v, p, p.n_v, t), d.fetch(dO, p, p.n_v, t);
+    a.template put<true>(tiles, p, p.n_k, t);
+    b.template put<true>(tiles + X, p, p.n_k, t);
+    c.template put<false>(tiles + 2 * X, p, p.n_v, t);
+    d.template put<false>(tiles + 2 * X + Y, p, p.n_v, t);
   };
   StateRows<F> state;
   state.load(seg + 1 < p.segments ? p.W + ((size_t)seq * (p.segments - 1) + seg) * es
@@ -714,10 +742,10 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_kv_kernel(const Ch
     const int t0 = c * F::C;
     const uint32_t tq = tiles;
     const uint32_t tk = tq + X, tv = tk + X, td = tv + Y;
-    load(c);
+    load(t0);
     chunk_decay<F::C>(p, seq, c, sh.decay);
     __syncthreads();
-    if (p.keeps(c, c1)) {
+    if (F::NI > 1 && p.keeps(c, c1)) {
       float s = dot_kept<F>(p.kept + p.keep_slot(seq, c) * F::D * F::D, state_tile);
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
@@ -759,15 +787,15 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_kv_kernel(const Ch
       float sum[2] = {0.f, 0.f};
       if (live(part / 2)) {
         float x[4] = {}, y[4] = {};
-        score_tile<F, F::NP, F::NP>(x, tk, r0, tq, part * 8, lane);
+        score_tile<F, F::NI, F::NI>(x, tk, r0, tq, part * 8, lane);
         score_tile<F, F::NV, F::NV>(y, tv, r0, td, part * 8, lane);
         masked(x, y, part * 8, sum);
         put_scores<F>(scores, x, r0, part * 8, lane);
-        put_scores<F>(scores + F::NP * F::SCORES, y, r0, part * 8, lane);
+        put_scores<F>(scores + F::NO * F::SCORES, y, r0, part * 8, lane);
       }
       if (p.rc) put_cols(sum, part * 8);
     } else {
-      rows_times_rows<F, CT, F::NP, F::NP>(w, tk, F::TILE, r0, tq, F::TILE, 0, lane, live);
+      rows_times_rows<F, CT, F::NI, F::NI>(w, tk, F::TILE, r0, tq, F::TILE, 0, lane, live);
       rows_times_rows<F, CT, F::NV, F::NV>(dw, tv, F::TILE, r0, td, F::TILE, 0, lane, live);
 #pragma unroll
       for (int n = 0; n < CT; ++n) {
@@ -785,18 +813,18 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_kv_kernel(const Ch
           sh.pairs[F::SHARE ? part : 0][r0 + lane / 4 + 8 * h] = row_sum[h];
       }
     }
-    auto frag = [&](uint32_t (&a)[F::NP][4], int j) {
+    auto frag = [&](uint32_t (&a)[F::NO][4], int j) {
       if constexpr (F::SHARE) score_frag<F>(a, smem_u32(scores), r0, j, lane);
       else score_frag<F>(a, w, j);
     };
-    auto dfrag = [&](uint32_t (&a)[F::NP][4], int j) {
-      if constexpr (F::SHARE) score_frag<F>(a, smem_u32(scores) + F::NP * F::SCORES, r0, j, lane);
+    auto dfrag = [&](uint32_t (&a)[F::NO][4], int j) {
+      if constexpr (F::SHARE) score_frag<F>(a, smem_u32(scores) + F::NO * F::SCORES, r0, j, lane);
       else score_frag<F>(a, dw, j);
     };
     const float t_0 = sh.decay.tail[r0 + lane / 4], t_1 = sh.decay.tail[r0 + lane / 4 + 8];
     {
       float acc[NT][4] = {};
-      rows_times_cols<F, NT, F::NP, F::NP>(acc, tk, F::TILE, r0, G, F::STATE, n0, lane);
+      rows_times_cols<F, NT, F::NI, F::NO>(acc, tk, F::TILE, r0, G, F::STATE, n0, lane);
 #pragma unroll
       for (int n = 0; n < NT; ++n)
         acc[n][0] *= t_0, acc[n][1] *= t_0, acc[n][2] *= t_1, acc[n][3] *= t_1;
@@ -806,7 +834,7 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_kv_kernel(const Ch
     }
     {
       float acc[NT][4] = {};
-      rows_times_rows<F, NT, F::NV, F::NP>(acc, tv, F::TILE, r0, G, F::STATE, n0, lane,
+      rows_times_rows<F, NT, F::NV, F::NM>(acc, tv, F::TILE, r0, G, F::STATE, n0, lane,
                                            [](int) { return true; });
 #pragma unroll
       for (int n = 0; n < NT; ++n)
@@ -818,7 +846,7 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_kv_kernel(const Ch
           sh.rows[part][r0 + lane / 4 + 8] = d.y;
         }
       }
-      scores_times_cols<F, NT, F::NP>(acc, dfrag, tq, n0, lane, live);
+      scores_times_cols<F, NT, F::NI>(acc, dfrag, tq, n0, lane, live);
       store_rows<F, NT>(acc, static_cast<T *>(p.dk) + ek, k, p, p.n_k, t0 + r0, n0, lane);
     }
     const bool more = c > c0;
@@ -848,14 +876,17 @@ cudaError_t launch_segment_scan(const ChunkBwd &p, int seqs, cudaStream_t stream
 
 // The launches of one configuration.
 template <typename F> cudaError_t run_chunk_bwd(const ChunkBwd &p, int seqs, cudaStream_t stream) {
-  static int set_share[64], set_q[64], set_kv[64];
+  [[maybe_unused]] static int set_share[64];
+  static int set_q[64], set_kv[64];
   cudaError_t e;
-  if (p.segments > 1) {
-    auto share = segment_share_kernel<F>;
-    if ((e = tc::set_smem_once(share, share_smem<F>(), set_share)) != cudaSuccess) return e;
-    share<<<dim3((unsigned)(seqs * (p.segments - 1)), 2), F::THREADS, share_smem<F>(), stream>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    if ((e = launch_segment_scan(p, seqs, stream)) != cudaSuccess) return e;
+  if constexpr (F::NI > 1) {  // else there is one chunk
+    if (p.segments > 1) {
+      auto share = segment_share_kernel<F>;
+      if ((e = tc::set_smem_once(share, share_smem<F>(), set_share)) != cudaSuccess) return e;
+      share<<<dim3((unsigned)(seqs * (p.segments - 1)), 2), F::THREADS, share_smem<F>(), stream>>>(p);
+      if ((e = cudaGetLastError()) != cudaSuccess) return e;
+      if ((e = launch_segment_scan(p, seqs, stream)) != cudaSuccess) return e;
+    }
   }
   auto gq = grad_q_kernel<F>;
   auto gkv = grad_kv_kernel<F>;

@@ -1,6 +1,7 @@
 """Long sequences in the attention backward: slow per-head decays, whose gradient is one number a
 head, summed over every token, in which errors that stay from chunk to chunk would add up; and
-head widths that are padded on the way, cut into segments.  Needs a GB300."""
+head widths that are padded on the way, cut into segments; and many short sequences.  Needs a
+GB300."""
 import pytest
 import torch
 
@@ -93,3 +94,13 @@ def test_nothing_is_written_past_the_gradients(dtype, dk, dv):
     for t, out, pad in zip(want, outs, pads):
         assert torch.equal(t, out)
         assert (pad[:64] == 7).all() and (pad[-64:] == 7).all()
+
+
+@pytest.mark.parametrize("phi,kind", [("identity", "token"), ("identity", "none"), ("elu1", "head"),
+                                      ("identity", "logit")])
+@pytest.mark.parametrize("L,dk,dv", [(1, 64, 64), (5, 16, 32), (63, 64, 64), (64, 32, 64), (65, 64, 16)])
+def test_many_short_sequences(L, dk, dv, phi, kind):
+    """More sequences than SMs, of one chunk and just above it."""
+    B, H = 5, 32
+    check_attn(B, H, L, dk, dv, "bf16", phi, kind, states=L % 2 == 1)
+    check_attn(B, H, L, dk, dv, "bf16", phi, kind, states=False, want_decay_grad=False)
