@@ -15,7 +15,9 @@ cudaError_t launch_chunk_bwd_f32(const ChunkBwd &p, int seqs, bool wide, bool bf
 namespace {
 
 constexpr int kMaxPer = 512;  // chunks of a segment (the decays' kernel keeps sums of them)
-constexpr int kKeep = 1024;   // tokens from one kept state to the next
+// Tokens from one kept state to the next: with 1024 the gradients of 2 x 32 x 8192 x 128 with
+// per-head decays take 521 us, not 530, and ddecay is up to 7.6e-7 off, not 4.8e-7.
+constexpr int kKeep = 512;
 constexpr int kShort = 64;    // tokens of the bf16 kernels' one chunk
 
 // How a call runs: which planes, the chunk, the segments.
@@ -30,11 +32,10 @@ struct Plan {
 // The segments that take the least time on 152 SMs, in units of a chunk of both
 // walks: whole waves of blocks, each a segment's chunks and a start; with more than one
 // segment also the pass over their own shares, S and G in blocks of their own at 0.2 of a chunk's
-// time, and two launches.  It picks 2 segments for 2 x 32 x 8192 x 128 with decays (517 us; 1: 813,
-// 4: 588, 7: 610), 9 for 1 x 16 x 32768 x 128 (543; 4: 969, 19: 571), 2 for 4 x 16 x 4096 x 64
-// (130; 1: 189, 4: 140), 9 for 3 x 5 x 777 x 64 x 128 fp32 (103 when
-// compared, 100 now; 5: 141, 13: 125),
-// and a chunk each for one sequence of 300 tokens in fp32 (17; 5: 28, 1: 102).
+// time, and two launches.  Compared when the kernels were a few per cent from now, it picks 2 segments
+// for 2 x 32 x 8192 x 128 with decays (517 us; 1: 813, 4: 588, 7: 610), 9 for 1 x 16 x 32768 x 128
+// (543; 4: 969, 19: 571), 2 for 4 x 16 x 4096 x 64 (130; 1: 189, 4: 140), 9 for 3 x 5 x 777 x 64 x 128
+// fp32 (103; 5: 141, 13: 125), and a chunk each for one sequence of 300 tokens in fp32 (17; 5: 28, 1: 102).
 Plan make_plan(const ChunkBwdArgs &a, bool f32_out) {
   Plan p;
   p.wide = std::max(a.dk, a.dv) > 64;

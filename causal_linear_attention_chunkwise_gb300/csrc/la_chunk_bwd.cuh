@@ -30,9 +30,9 @@
 // around it (<G, e^L_C S>, which follows from chunk to chunk by the same sums).
 // Formed this way nothing cancels beyond one chunk; q dq - k dk summed from the
 // sequence's end would lose the short decays to the long sums.  Followed from chunk to chunk the
-// sums' errors stay, and a per-head decay's gradient adds them up over all tokens: every 1024
+// sums' errors stay, and a per-head decay's gradient adds them up over all tokens: every 512
 // tokens S is kept for the backward walk, which forms <G, e^L_C S> anew (2 x 32 x 8192 x 128
-// with per-head decays: 6e-7 off; 4.5e-6 without, growing with the length to the power 1.5).
+// with per-head decays: 4e-7 off; 4.5e-6 without, growing with the length to the power 1.5).
 //
 // Precision.  Products run in bf16 with fp32 sums.  With bf16 inputs and outputs the
 // decayed scores and the states round once to bf16 as operands (the state itself

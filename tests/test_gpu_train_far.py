@@ -48,10 +48,10 @@ def head_decay_grad(q, k, v, dO, decay):
 @pytest.mark.parametrize("dtype,dk,dv", [("bf16", 64, 64), ("bf16", 64, 32), ("f32", 64, 64)])
 def test_slow_head_decays(dtype, dk, dv):
     """The pairs around a chunk follow from those around the next one by two sums, and are
-    formed anew every 1024 tokens: at most 8 chunks of 128 tokens (16 and 32 smaller ones, with
-    as many tokens) follow one another.  A sum's products are cut, not rounded, 8 times (64 values
-    in steps of 16, in two products): 8 U of its size.  16 such sums with independent signs: 32 U,
-    2e-6 of the gradient's size.  As many sequences as there are SMs, so that they run whole."""
+    formed anew every 512 tokens: at most 4 chunks of 128 tokens (more smaller ones, with as
+    many tokens) follow one another.  A sum's products are cut, not rounded, 8 times (64 values in
+    steps of 16, in two products): 8 U of its size.  8 such sums with independent signs: 23 U, and
+    what the gradient's own sums are off: 32 U, 2e-6 of its size.  As many sequences as there are SMs, so that they run whole."""
     B, H, L = 4, 38, 8192
     g = torch.Generator("cuda").manual_seed(5)
     q, k = (torch.randn(B, H, L, dk, generator=g, device="cuda").mul_(0.2).to(DT[dtype])
