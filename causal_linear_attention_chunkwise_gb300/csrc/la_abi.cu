@@ -136,16 +136,68 @@ bool aligned_elt(const void *p, size_t elt) {
   return (reinterpret_cast<uintptr_t>(p) & (elt - 1)) == 0;
 }
 
-// A [B,H,L,d] tensor with strides: its token-major rows where it has them (they may
-// be a slice of a wider tensor), else all that it spans as one row.
-Rows head_rows(const void *p, int B, int H, int L, int d, long long bs, long long hs,
+// A [B,H,L,d] tensor with strides, in elements; its last axis is dense.
+struct Heads {
+  const void *p;
+  long long n[3], s[3];  // b, h, t
+  int d;
+  size_t elt;
+};
+Heads heads_of(const void *p, int B, int H, int L, int d, long long bs, long long hs,
                long long ts, size_t elt) {
-  const long long rows = (long long)B * L, width = (long long)H * d;
-  if ((H == 1 || hs == d) && (B == 1 || L == 1 || bs == L * ts) && (L == 1 || ts >= width) &&
-      (L > 1 || B == 1 || bs >= width))
-    return {p, rows, width, rows == 1 ? width : L == 1 ? bs : ts, elt};
-  const long long span = (B - 1) * bs + (H - 1) * hs + (L - 1) * ts + d;
-  return {p, 1, span, span, elt};
+  return {p, {B, H, L}, {bs, hs, ts}, d, elt};
+}
+// [B,L,H*d] rows `stride` elements apart, seen as such a tensor.
+Heads token_rows(const void *p, int B, int H, int L, int d, long long stride, size_t elt) {
+  return heads_of(p, B, H, L, d, L * stride, d, stride, elt);
+}
+// All that it spans, as one row.
+Rows span_of(const Heads &x) {
+  long long span = x.d;
+  for (int i = 0; i < 3; ++i) span += (x.n[i] - 1) * x.s[i];
+  return {x.p, 1, span, span, x.elt};
+}
+
+// One axis of the differences between two tensors' indices: lo .. hi times s.
+struct Axis {
+  long long s, lo, hi;
+};
+// Whether `delta` is a sum of multiples of the axes' strides, the largest first, and one of
+// lo .. hi.  Where a stride is shorter than what lies inside it there may be many ways to try:
+// they count as one that fits.
+bool reaches(const Axis *axis, int axes, long long lo, long long hi, long long delta) {
+  if (axes == 0) return lo <= delta && delta <= hi;
+  long long least = lo, most = hi;  // of what the axes inside this one add
+  for (int i = 1; i < axes; ++i) least += axis[i].lo * axis[i].s, most += axis[i].hi * axis[i].s;
+  const long long s = axis->s;
+  auto floor_div = [&](long long x) { return x / s - (x % s < 0); };
+  const long long first = -floor_div(most - delta), last = floor_div(delta - least);
+  const long long from = first > axis->lo ? first : axis->lo, to = last < axis->hi ? last : axis->hi;
+  if (to - from > 3) return true;
+  for (long long k = from; k <= to; ++k)
+    if (reaches(axis + 1, axes - 1, lo, hi, delta - k * s)) return true;
+  return false;
+}
+
+// Whether two such tensors share an element.  Tensors of one set of strides may interleave in any
+// way (slices of a packed projection, whatever the order of its axes, or of a longer batch); those
+// of unlike strides must not lie in one range.
+bool overlap(const Heads &a, const Heads &b) {
+  if (!a.p || !b.p) return false;
+  if (!overlap(span_of(a), span_of(b))) return false;
+  Axis axis[3];
+  int axes = 0;
+  for (int i = 0; i < 3; ++i) {
+    if (a.n[i] > 1 && b.n[i] > 1 && a.s[i] != b.s[i]) return true;
+    const long long s = a.n[i] > 1 ? a.s[i] : b.s[i];
+    if ((a.n[i] == 1 && b.n[i] == 1) || s == 0) continue;
+    int at = axes++;
+    for (; at > 0 && axis[at - 1].s < s; --at) axis[at] = axis[at - 1];
+    axis[at] = {s, 1 - b.n[i], a.n[i] - 1};
+  }
+  const long long bytes = (long long)(reinterpret_cast<uintptr_t>(b.p) -
+                                      reinterpret_cast<uintptr_t>(a.p));
+  return reaches(axis, axes, 1 - b.d, a.d - 1, bytes / (long long)a.elt);
 }
 
 // Whether no two elements of a [B,H,L,d] tensor lie in one place, as an output's may not.
@@ -181,12 +233,12 @@ la_status rotary(const char *fn, RotaryArgs a) {
   if (!a.k.p && !a.k_out.p) a.heads_k = 0;
   if (a.B == 0 || a.L == 0 || a.heads_q + a.heads_k == 0) return ok();
   const size_t elt = a.dtype == LA_F32 ? 4 : 2;
-  Rows in[2], out[2];
+  Heads in[2], out[2];
   const RotaryTensor x[] = {a.q, a.k}, y[] = {a.q_out, a.k_out};
   const int heads[] = {a.heads_q, a.heads_k};
   for (int i = 0; i < 2; ++i) {
     if (heads[i] == 0) {
-      in[i] = out[i] = Rows{nullptr, 0, 0, 0, elt};
+      in[i] = out[i] = Heads{nullptr, {}, {}, 0, elt};
       continue;
     }
     if (!x[i].p || !y[i].p)
@@ -198,8 +250,8 @@ la_status rotary(const char *fn, RotaryArgs a) {
         return fail(LA_ERR_INVALID_ARG, "%s: negative stride", fn);
     if (!own_places(a.B, heads[i], a.L, a.d, y[i].bs, y[i].hs, y[i].ts))
       return fail(LA_ERR_INVALID_ARG, "%s: an output's strides put two elements in one place", fn);
-    in[i] = head_rows(x[i].p, a.B, heads[i], a.L, a.d, x[i].bs, x[i].hs, x[i].ts, elt);
-    out[i] = head_rows(y[i].p, a.B, heads[i], a.L, a.d, y[i].bs, y[i].hs, y[i].ts, elt);
+    in[i] = heads_of(x[i].p, a.B, heads[i], a.L, a.d, x[i].bs, x[i].hs, x[i].ts, elt);
+    out[i] = heads_of(y[i].p, a.B, heads[i], a.L, a.d, y[i].bs, y[i].hs, y[i].ts, elt);
   }
   if (!a.inv_freq) return fail(LA_ERR_INVALID_ARG, "%s: inv_freq must be non-null", fn);
   for (const void *p : {static_cast<const void *>(a.inv_freq),
@@ -215,12 +267,15 @@ la_status rotary(const char *fn, RotaryArgs a) {
     const bool in_place = x[i].p == y[i].p && (a.B == 1 || x[i].bs == y[i].bs) &&
                           (heads[i] == 1 || x[i].hs == y[i].hs) &&
                           (a.L == 1 || x[i].ts == y[i].ts);
-    if ((!in_place && overlap(out[i], in[i])) || overlap(out[i], in[1 - i]) ||
-        overlap_any(out[i], par))
+    if ((!in_place && overlap(out[i], in[i])) || overlap(out[i], in[1 - i]))
       return fail(LA_ERR_INVALID_ARG, "%s: an output overlaps an input", fn);
   }
   if (overlap(out[0], out[1]))
     return fail(LA_ERR_INVALID_ARG, "%s: q_out and k_out overlap", fn);
+  for (const Heads &o : out)
+    if (overlap_any(span_of(o), par))
+      return fail(LA_ERR_INVALID_ARG,
+                  "%s: an output overlaps inv_freq, positions, offsets or lengths", fn);
   cudaError_t e = launch_rotary(a);
   if (e != cudaSuccess) return cuda_fail(e, fn);
   return ok();
@@ -701,19 +756,15 @@ la_status la_gated_norm_fwd(const void *x, long long x_b_stride, long long x_h_s
     return fail(LA_ERR_INVALID_ARG, "%s: pointers must be aligned to their elements", fn);
   if (!aligned16(weight) || !aligned16(bias))
     return fail(LA_ERR_INVALID_ARG, "%s: weight and bias must be 16-byte aligned", fn);
-  const long long rows = (long long)B * L;
-  const Rows yr{y, rows, width, y_stride, elt}, gr{gate, rows, width, gate_stride, elt};
-  const long long span = (B - 1) * x_b_stride + (H - 1) * x_h_stride + (L - 1) * x_t_stride + d;
-  Rows xr{x, 1, span, span, elt};
-  if ((H == 1 || x_h_stride == d) && (B == 1 || x_b_stride == L * x_t_stride) &&
-      (L == 1 || x_t_stride >= width))
-    xr = {x, rows, width, rows == 1 ? width : L == 1 ? x_b_stride : x_t_stride,
-          elt};  // token-major rows, which may be a slice
+  const Heads yh = token_rows(y, B, H, L, d, y_stride, elt);
   const Rows par[] = {params(weight, (long long)weight_heads * d),
                       params(bias, (long long)weight_heads * d)};
-  if (overlap(yr, xr) || (!(y == gate && y_stride == gate_stride) && overlap(yr, gr)) ||
-      overlap_any(yr, par))
+  if (overlap(yh, heads_of(x, B, H, L, d, x_b_stride, x_h_stride, x_t_stride, elt)) ||
+      (!(y == gate && y_stride == gate_stride) &&
+       overlap(yh, token_rows(gate, B, H, L, d, gate_stride, elt))))
     return fail(LA_ERR_INVALID_ARG, "%s: y overlaps an input", fn);
+  if (overlap_any(span_of(yh), par))
+    return fail(LA_ERR_INVALID_ARG, "%s: y overlaps weight or bias", fn);
   GatedNormArgs a{x, x_b_stride, x_h_stride, x_t_stride, gate, gate_stride, dtype, B, H, L, d,
                   norm, activation, gate_first, weight, bias, weight_heads, eps, y, y_stride,
                   static_cast<cudaStream_t>(cuda_stream)};
@@ -976,26 +1027,26 @@ la_status la_gated_norm_bwd(const void *dy, long long dy_stride, const void *x,
       return fail(LA_ERR_INVALID_ARG, "%s: pointers must be aligned to their elements", fn);
   if (!own_places(B, H, L, d, dx_b_stride, dx_h_stride, dx_t_stride))
     return fail(LA_ERR_INVALID_ARG, "%s: dx's strides put two elements in one place", fn);
-  const long long rows = (long long)B * L;
-  const Rows in[] = {{dy, rows, width, dy_stride, elt},
-                     head_rows(x, B, H, L, d, x_b_stride, x_h_stride, x_t_stride, elt),
-                     {gate, rows, width, gate_stride, elt}};
+  const Heads in[] = {token_rows(dy, B, H, L, d, dy_stride, elt),
+                      heads_of(x, B, H, L, d, x_b_stride, x_h_stride, x_t_stride, elt),
+                      token_rows(gate, B, H, L, d, gate_stride, elt)};
+  const Heads dxh = heads_of(dx, B, H, L, d, dx_b_stride, dx_h_stride, dx_t_stride, elt);
+  const Heads dzh = token_rows(dgate, B, H, L, d, dgate_stride, elt);
   const Rows par[] = {params(weight, wn), params(bias, wn)};
-  const Rows dxr = head_rows(dx, B, H, L, d, dx_b_stride, dx_h_stride, dx_t_stride, elt);
-  const Rows dzr{dgate, rows, width, dgate_stride, elt};
+  const Rows span[] = {span_of(in[0]), span_of(in[1]), span_of(in[2]), span_of(dxh), span_of(dzh)};
   const Rows dw = params(dweight, wn), dbr = params(dbias, wn);
   const bool x_place = dx == x && (B == 1 || dx_b_stride == x_b_stride) &&
                        (H == 1 || dx_h_stride == x_h_stride) &&
                        (L == 1 || dx_t_stride == x_t_stride);
   const bool dy_place = dgate && dgate == dy && dgate_stride == dy_stride;
   const bool z_place = dgate && dgate == gate && dgate_stride == gate_stride;
-  if (overlap(dxr, in[0]) || (!x_place && overlap(dxr, in[1])) || overlap(dxr, in[2]) ||
-      (!dy_place && overlap(dzr, in[0])) || overlap(dzr, in[1]) ||
-      (!z_place && overlap(dzr, in[2])) || overlap(dxr, dzr) || overlap_any(dxr, par) ||
-      overlap_any(dzr, par))
+  if (overlap(dxh, in[0]) || (!x_place && overlap(dxh, in[1])) || overlap(dxh, in[2]) ||
+      (!dy_place && overlap(dzh, in[0])) || overlap(dzh, in[1]) ||
+      (!z_place && overlap(dzh, in[2])) || overlap(dxh, dzh) || overlap_any(span[3], par) ||
+      overlap_any(span[4], par))
     return fail(LA_ERR_INVALID_ARG, "%s: an output overlaps an input or another output", fn);
   for (const Rows &w : {dw, dbr})
-    if (overlap_any(w, in) || overlap_any(w, par) || overlap(w, dxr) || overlap(w, dzr))
+    if (overlap_any(w, span) || overlap_any(w, par))
       return fail(LA_ERR_INVALID_ARG, "%s: an output overlaps an input or another output", fn);
   if (overlap(dw, dbr)) return fail(LA_ERR_INVALID_ARG, "%s: dweight and dbias overlap", fn);
   if (dweight || dbias) {
@@ -1006,8 +1057,7 @@ la_status la_gated_norm_bwd(const void *dy, long long dy_stride, const void *x,
     if (!aligned16(workspace))
       return fail(LA_ERR_INVALID_ARG, "%s: workspace must be 16-byte aligned", fn);
     const Rows ws = dense(workspace, need);
-    if (overlap_any(ws, in) || overlap_any(ws, par) || overlap(ws, dxr) || overlap(ws, dzr) ||
-        overlap(ws, dw) || overlap(ws, dbr))
+    if (overlap_any(ws, span) || overlap_any(ws, par) || overlap(ws, dw) || overlap(ws, dbr))
       return fail(LA_ERR_INVALID_ARG, "%s: the workspace overlaps an input or an output", fn);
   }
   GatedNormBwdArgs a{dy, dy_stride, x, x_b_stride, x_h_stride, x_t_stride, gate, gate_stride,

@@ -424,7 +424,10 @@ la_status la_residual_norm_fwd(const void *x, int dtype, const void *residual, i
  * only, parameters, their gradients, decays and states are fp32 and 16-byte
  * aligned (positions, offsets, lengths and frequencies 4-byte), outputs may
  * not overlap inputs except as stated, and a call gives the same bits on every
- * run.  Nothing of a forward call is kept: a backward call gets what it needs
+ * run.  [B,H,L,d] tensors of the same strides may interleave without sharing an
+ * element (the parts of a packed projection, whatever the order of its axes, at
+ * full length or a prefix of it); an output of other strides lies in a range of
+ * its own.  Nothing of a forward call is kept: a backward call gets what it needs
  * as arguments.
  *
  * A parameter's gradient is a sum over rows; it is formed in fp32 in a fixed
