@@ -19,18 +19,33 @@
 namespace la {
 namespace {
 
-// act(z) and its derivative of a cell of values: s = sigmoid(z); z s has s + z s (1 - s).
-__device__ __forceinline__ unsigned long long sigmoid2(unsigned long long z) {
-  return activate2(LA_ACT_SIGMOID, z);
+// sigmoid(z) and 1 - sigmoid(z) of a cell of values.  With e = e^-z they are 1 / (1 + e) and
+// e / (1 + e); as a difference from 1 the second would lose its digits above z = 10.  Where e
+// overflows the sigmoid is 0 and what its complement is multiplied by as well.
+constexpr float kMostExp = 0x1p126f;
+__device__ __forceinline__ void sigmoid_both(float z, float &s, float &rest) {
+  const float e = ex2_approx(-z * kLog2e);
+  s = rcp_approx(1.f + e);
+  rest = fminf(e, kMostExp) * s;
 }
-__device__ __forceinline__ float sigmoid2(float z) { return sigmoid(z); }
+__device__ __forceinline__ void sigmoid_both(unsigned long long z, unsigned long long &s,
+                                             unsigned long long &rest) {
+  float a, b, x, y;
+  unpack2(mul2(z, dup2(-kLog2e)), a, b);
+  a = ex2_approx(a), b = ex2_approx(b);
+  unpack2(add2(pack2(a, b), dup2(1.f)), x, y);
+  s = pack2(rcp_approx(x), rcp_approx(y));
+  rest = mul2(pack2(fminf(a, kMostExp), fminf(b, kMostExp)), s);
+}
 
+// act(z) and its derivative, with s = sigmoid(z): z s has s + z s (1 - s).
 template <int ACT, int V, typename C>
 __device__ __forceinline__ void act_and_slope(C z, C &a, C &slope) {
   if constexpr (ACT == LA_ACT_NONE) {
     a = z, slope = CellOf<V>::both(1.f);
   } else {
-    const C s = sigmoid2(z), rest = fma2(s, CellOf<V>::both(-1.f), CellOf<V>::both(1.f));
+    C s, rest;
+    sigmoid_both(z, s, rest);
     a = ACT == LA_ACT_SILU ? mul2(z, s) : s;
     slope = ACT == LA_ACT_SILU ? fma2(a, rest, s) : mul2(s, rest);
   }
