@@ -586,7 +586,8 @@ def la_rotary_frequencies(rotary_dim, base=10000.0, scaling="plain", factor=1.0,
     (``.cuda()`` them once) and the factor of q and k.  ``scaling``: "plain" |
     "linear" (positions interpolated by ``factor``) | "ntk" (a larger base) |
     "yarn" (pairs of fewer than ``slow`` turns over ``trained_length`` interpolated,
-    those of more than ``fast`` left, a blend between)."""
+    those of more than ``fast`` left, a blend linear in the pair's index between, from and
+    to whole pairs: what checkpoints with this scaling are trained with)."""
     inv_freq = torch.empty(max(rotary_dim // 2, 0), dtype=torch.float32)
     scale = torch.empty(1, dtype=torch.float32)
     _check(_native.load().la_rotary_frequencies(

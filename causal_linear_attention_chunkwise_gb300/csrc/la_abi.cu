@@ -865,17 +865,29 @@ la_status la_rotary_frequencies(int rotary_dim, double base, int scaling, double
     return fail(LA_ERR_INVALID_ARG, "%s: factor must be finite and at least 1", fn);
   if (scaling == LA_ROTARY_YARN &&
       (!(trained_length > 0) || !(slow >= 0) || !(fast > slow) || !std::isfinite(fast) ||
-       !std::isfinite(trained_length)))
-    return fail(LA_ERR_INVALID_ARG, "%s: needs trained_length > 0 and fast > slow >= 0", fn);
+       !std::isfinite(trained_length) || !(base > 1)))
+    return fail(LA_ERR_INVALID_ARG,
+                "%s: needs trained_length > 0, fast > slow >= 0 and base > 1", fn);
   if (scaling == LA_ROTARY_NTK && rotary_dim > 2)
     base *= std::pow(factor, rotary_dim / (rotary_dim - 2.0));
+  // YaRN: the pairs (as real numbers) that make `fast` and `slow` turns, rounded away from one
+  // another; both within the head's width, and never the same.
+  double fast_pair = 0, slow_pair = 1;
+  if (scaling == LA_ROTARY_YARN) {
+    auto pair_of = [&](double turns) {
+      return rotary_dim * std::log(trained_length / (turns * 6.283185307179586)) /
+             (2 * std::log(base));
+    };
+    fast_pair = std::fmax(std::floor(pair_of(fast)), 0.0);
+    slow_pair = std::fmin(std::ceil(pair_of(slow)), rotary_dim - 1.0);
+    if (!(slow_pair > fast_pair)) slow_pair = fast_pair + 1e-3;
+  }
   for (int i = 0; i < rotary_dim / 2; ++i) {
     double f = std::pow(base, -2.0 * i / rotary_dim);
     if (scaling == LA_ROTARY_LINEAR) f /= factor;
     if (scaling == LA_ROTARY_YARN) {
-      const double turns = trained_length * f / (6.283185307179586);
-      const double ramp = turns <= slow ? 0 : turns >= fast ? 1 : (turns - slow) / (fast - slow);
-      f = f / factor * (1 - ramp) + f * ramp;
+      const double to_slow = std::fmin(std::fmax((i - fast_pair) / (slow_pair - fast_pair), 0.0), 1.0);
+      f = f / factor * to_slow + f * (1 - to_slow);
     }
     inv_freq[i] = (float)f;
   }

@@ -441,16 +441,19 @@ la_status la_residual_norm_fwd(const void *x, int dtype, const void *residual, i
 #define LA_ROTARY_PLAIN  0  /* f_i = base^(-2 i / rotary_dim)                                */
 #define LA_ROTARY_LINEAR 1  /* f_i / factor: positions interpolated                          */
 #define LA_ROTARY_NTK    2  /* base * factor^(rotary_dim / (rotary_dim - 2)) as the base     */
-#define LA_ROTARY_YARN   3  /* f_i / factor for pairs of fewer than `slow` turns over the
-                               trained length, f_i for those of more than `fast`, a blend
-                               linear in the turns between them; scale 0.1 ln(factor) + 1    */
+#define LA_ROTARY_YARN   3  /* f_i up to pair `low`, f_i / factor from pair `high` on, a blend
+                               linear in the pair between them; scale 0.1 ln(factor) + 1     */
 
 /*
  * Rotary frequencies of the pairs, rounded once from 64 bits, into HOST memory:
  * inv_freq[rotary_dim / 2], and `scale` (NULL: not wanted), what la_rotary_fwd
  * takes as its scale.  factor >= 1 (unused by PLAIN); trained_length, fast and
- * slow are used by YARN alone (32 and 1 are customary).  Errors:
- * LA_ERR_INVALID_ARG.  (The pages leave out the rotation of their retention
+ * slow are used by YARN alone (32 and 1 are customary).  There pair p makes
+ * trained_length f_p / 2 pi turns over the trained length; low and high are the
+ * pairs of `fast` and of `slow` turns, as checkpoints trained with this scaling have
+ * them: p = rotary_dim ln(trained_length / (2 pi turns)) / (2 ln base), low rounded
+ * down (and at least 0), high up (at most rotary_dim - 1; where that is not above low,
+ * the pairs behind low are scaled in full).  Errors: LA_ERR_INVALID_ARG.  (The pages leave out the rotation of their retention
  * layer, "Linear / sparse attention tutorial" sections 2.4 and 10; these are the
  * operators that bring it.)
  */
