@@ -588,6 +588,8 @@ def la_rotary_frequencies(rotary_dim, base=10000.0, scaling="plain", factor=1.0,
     "yarn" (pairs of fewer than ``slow`` turns over ``trained_length`` interpolated,
     those of more than ``fast`` left, a blend linear in the pair's index between, from and
     to whole pairs: what checkpoints with this scaling are trained with)."""
+    if rotary_dim > _INT_MAX:
+        raise _too_large(rotary_dim)
     inv_freq = torch.empty(max(rotary_dim // 2, 0), dtype=torch.float32)
     scale = torch.empty(1, dtype=torch.float32)
     _check(_native.load().la_rotary_frequencies(
@@ -698,6 +700,8 @@ def la_rotary_bwd(dq, dk, inv_freq, positions=None, offsets=None, lengths=None,
 
 
 def la_chunk_bwd_workspace_bytes(B, H, L, d_k, d_v, chunk=64, dtype=torch.bfloat16) -> int:
+    if max(B, H, L, d_k, d_v, chunk) > _INT_MAX:
+        raise _too_large(B, H, L, d_k, d_v, chunk)
     return int(_native.load().la_chunk_bwd_workspace_bytes(B, H, L, d_k, d_v, chunk,
                                                            DTYPE[dtype]))
 
@@ -722,8 +726,8 @@ def la_chunk_bwd(q, k, v, dO, chunk=64, decay_kind="none", decay=None, S0=None, 
     shape, dtype = q.shape, q.dtype
     B, H, L, d_k = shape
     d_v = v.shape[-1]
-    if max(B, H, L, d_k, d_v) > _INT_MAX:
-        raise _too_large(B, H, L, d_k, d_v)
+    if max(B, H, L, d_k, d_v, chunk) > _INT_MAX:
+        raise _too_large(B, H, L, d_k, d_v, chunk)
     v_shape, state, f32 = (B, H, L, d_v), (B, H, d_k, d_v), torch.float32
     kind = DECAY[decay_kind]
     if (decay is None) != (kind == 0):
@@ -764,6 +768,8 @@ def la_chunk_bwd(q, k, v, dO, chunk=64, decay_kind="none", decay=None, S0=None, 
 
 
 def la_gated_norm_bwd_workspace_bytes(B, H, L, d, weight_heads=1) -> int:
+    if max(B, H, L, d, weight_heads) > _INT_MAX:
+        raise _too_large(B, H, L, d, weight_heads)
     return int(_native.load().la_gated_norm_bwd_workspace_bytes(B, H, L, d, weight_heads))
 
 
@@ -829,6 +835,8 @@ def la_gated_norm_bwd(dy, x, gate=None, weight=None, bias=None, norm="rms", acti
 
 
 def la_residual_norm_bwd_workspace_bytes(rows, D) -> int:
+    if D > _INT_MAX:
+        raise _too_large(D)
     return int(_native.load().la_residual_norm_bwd_workspace_bytes(rows, D))
 
 
