@@ -80,17 +80,19 @@ gated_norm_bwd_kernel(const GatedNormBwdArgs a, long long rows, float *part) {
   auto total = [](C c) { return CellOf<V>::sum(c); };
   int turn = 0;
   Raw<T, V> x[I], z[I], dy[I];
-  // Row r's head and token, carried along: a step adds (db, dt, dh), without divisions.
+  // Row r's head and token, carried along: a step adds (db, dt, dh), without divisions.  t is
+  // unsigned: a step past a sequence's end may take it to 2^31 and above.
   struct Place {
     long long b, bt;
-    int t, h;
+    unsigned t;
+    int h;
   };
   auto split = [&](long long row) {
     Place p;
     p.bt = own_head >= 0 ? row : div_index(row, a.H);
     p.h = own_head >= 0 ? own_head : (int)(row - p.bt * a.H);
     p.b = div_index(p.bt, a.L);
-    p.t = (int)(p.bt - p.b * a.L);
+    p.t = (unsigned)(p.bt - p.b * a.L);
     return p;
   };
   const Place stride = [&] {
@@ -101,7 +103,7 @@ gated_norm_bwd_kernel(const GatedNormBwdArgs a, long long rows, float *part) {
   auto advance = [&](Place p) {
     p.h += stride.h, p.bt += stride.bt, p.t += stride.t, p.b += stride.b;
     if (own_head < 0 && p.h >= a.H) p.h -= a.H, ++p.bt, ++p.t;
-    if (p.t >= a.L) p.t -= a.L, ++p.b;
+    if (p.t >= (unsigned)a.L) p.t -= a.L, ++p.b;
     return p;
   };
   auto fetch = [&](const Place &p) {
