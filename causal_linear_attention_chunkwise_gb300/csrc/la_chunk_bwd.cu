@@ -89,11 +89,15 @@ size_t lay_out(const ChunkBwdArgs &a, const Plan &plan, bool decay_grad, char *b
     float *rq = part(seqs * a.L), *rk = part(seqs * a.L), *rc = part(seqs * a.L);
     float *cs = plan.tc ? part(seqs * a.L) : nullptr, *rs = plan.tc ? part(seqs * a.L) : nullptr;
     float *around = part(seqs * plan.segments), *sums = part(seqs * plan.segments);
-    const size_t kept = seqs * (plan.chunks / (kKeep / plan.chunk)), width = plan.wide ? 128 : 64;
+    // Any chunk may hold a strong decay, and then keeps its state.
+    const size_t kept = seqs * (plan.chunks - 1), width = plan.wide ? 128 : 64;
     float *states = part(kept * width * width), *between = part(kept * kShares);
+    float *across = plan.tc ? part(2 * seqs * plan.chunks) : nullptr;
+    float *strong = part((seqs * plan.chunks + 3) / 4);
     if (p) {
       p->rq = rq, p->rk = rk, p->rc = rc, p->cs = cs, p->rs = rs, p->around = around;
-      p->kept = states, p->between = between;
+      p->kept = states, p->between = between, p->across = reinterpret_cast<float2 *>(across);
+      p->strong = reinterpret_cast<unsigned char *>(strong);
       *by_segment = sums;
     }
   }
@@ -131,8 +135,16 @@ __global__ void __launch_bounds__(256) chunk_decay_kernel(const ChunkBwd p, int 
   if (item >= (long long)seqs * p.chunks) return;
   const int seq = (int)(item / p.chunks), t0 = (int)(item % p.chunks) * C;
   float2 a[N];
+  bool strong = false;
 #pragma unroll
-  for (int i = 0; i < N; ++i) a[i] = log2_decay(p, seq, t0 + lane * N + i);
+  for (int i = 0; i < N; ++i) {
+    a[i] = log2_decay(p, seq, t0 + lane * N + i);
+    strong = strong || a[i].x < kStrong;
+  }
+  if (p.strong) {
+    strong = __any_sync(0xffffffffu, strong);
+    if (lane == 0) p.strong[item] = strong;
+  }
 #pragma unroll
   for (int i = 1; i < N; ++i) a[i] = two_sum(a[i - 1], a[i]);
   float2 run = a[N - 1];
@@ -190,39 +202,19 @@ __global__ void __launch_bounds__(256) segment_scan_kernel(const ChunkBwd p, int
   }
 }
 
-// The sum of v over the warp's lanes in front of this one (FRONT) or behind it, within groups of
-// WIDTH lanes.
-template <bool FRONT, int WIDTH> __device__ __forceinline__ float lanes_sum(float v, int lane) {
-  const int at = lane % WIDTH;
-  float x = v;
-#pragma unroll
-  for (int off = 1; off < WIDTH; off <<= 1) {
-    const float y = FRONT ? __shfl_up_sync(0xffffffffu, x, off, WIDTH)
-                          : __shfl_down_sync(0xffffffffu, x, off, WIDTH);
-    if (FRONT ? at >= off : at + off < WIDTH) x += y;
-  }
-  const float y = FRONT ? __shfl_up_sync(0xffffffffu, x, 1, WIDTH)
-                        : __shfl_down_sync(0xffffffffu, x, 1, WIDTH);
-  return FRONT ? at ? y : 0.f : at < WIDTH - 1 ? y : 0.f;
-}
-template <int WIDTH> __device__ __forceinline__ float group_sum(float v) {
-#pragma unroll
-  for (int off = WIDTH / 2; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-  return v;
-}
-
 // A block: the tokens of one segment.  Their decays' gradients are sums of pairs (i < t <= j):
-//     over s >= t of rq + cs, over s < t of rk + rs, within t's block of BLOCK tokens, and `around`
+//     over s >= t of rq + cs, over s < t of rk + rs, within t's block of BLOCK tokens, rc, and `around`
 // the block.  <G, e^L_C S>, the pairs around a chunk, is given for the segment's last chunk and
 // where a state was kept; with the chunk's rq it is <G, S> in front of the chunk, and that less the
 // next chunk's rk is the next one's.  Around a block of a chunk: those, the chunk's rq behind the block, its rk in front,
-// and its pairs across the block (from one to the next: less cs, plus rs).
+// and its pairs across the block.
 constexpr int kDecayWarps = 32;
 
 template <int C, int BLOCK>
 __global__ void __launch_bounds__(32 * kDecayWarps)
 decay_grad_kernel(const ChunkBwd p, float *ddecay, float *by_segment) {
   __shared__ float sum_q[kMaxPer], sum_k[kMaxPer], all[kMaxPer], around_of[kMaxPer];
+  __shared__ bool strong[kMaxPer];
   __shared__ double share[kDecayWarps];
   constexpr int N = C / 32, LANES = BLOCK / N, BLOCKS = C / BLOCK;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -239,11 +231,13 @@ decay_grad_kernel(const ChunkBwd p, float *ddecay, float *by_segment) {
     q = group_sum<32>(q), k = group_sum<32>(k);
     if (lane == 0) {
       sum_q[c] = q, sum_k[c] = k;
-      all[c] = p.lam[((size_t)seq * p.chunks + c0 + c) * C + C - 1].x;
+      const size_t at = (size_t)seq * p.chunks + c0 + c;
+      all[c] = p.lam[at * C + C - 1].x;
+      strong[c] = p.strong[at];
     }
   }
   __syncthreads();
-  // A thread: the chunks that follow from one given sum, and what they are off by at the next
+  // A thread: the chunks that follow from given sums, and what they are off by at the next
   // one, spread over them: half of what their errors add up to is left.
   auto given = [&](int c) {
     float x = 0.f;
@@ -253,7 +247,7 @@ decay_grad_kernel(const ChunkBwd p, float *ddecay, float *by_segment) {
   for (int x = c0 / p.every + threadIdx.x; x * p.every < c0 + n; x += 32 * kDecayWarps) {
     const int from = max(x * p.every - c0, 0), last = min((x + 1) * p.every - c0, n) - 1;
     float around = last == n - 1 ? p.around[(size_t)seq * p.segments + seg] : given(last);
-    int start = last;
+    int start = last;  // the last chunk whose sum was given
     for (int c = last; c >= from; --c) {
       around_of[c] = around;
       if (c == 0) break;
@@ -261,16 +255,20 @@ decay_grad_kernel(const ChunkBwd p, float *ddecay, float *by_segment) {
       // Past a decay of 2^-40 nothing of <G, S> is left but the rounding of the sum.
       if (all[c - 1] >= -40.f) around -= sum_k[c - 1];
       else around = 0.f, start = c - 1;
+      if (c > from && !strong[c - 1]) continue;
+      const float exact = given(c - 1);
+      if (start >= c) {
+        const float off = (around - exact) / (start - c + 1);
+        for (int i = c; i < start; ++i) around_of[i] -= off * (start - i);
+      }
+      around = exact, start = c - 1;
     }
-    if (from == 0) continue;
-    const float off = (around - given(from - 1)) / (start - from + 1);
-    for (int c = from; c < start; ++c) around_of[c] -= off * (start - c);
   }
   __syncthreads();
   double total = 0.0;
   for (int c = warp; c < n; c += kDecayWarps) {
     float q[N], k[N], r[N], cs[N], rs[N];
-    float sq = 0.f, sk = 0.f, sr = 0.f, scs = 0.f, srs = 0.f;
+    float sq = 0.f, sk = 0.f, scs = 0.f, srs = 0.f;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int t = (c0 + c) * C + lane * N + i;
@@ -280,43 +278,35 @@ decay_grad_kernel(const ChunkBwd p, float *ddecay, float *by_segment) {
       r[i] = live ? p.rc[base + t] : 0.f;
       cs[i] = BLOCKS > 1 && live ? p.cs[base + t] : 0.f;
       rs[i] = BLOCKS > 1 && live ? p.rs[base + t] : 0.f;
-      sq += q[i], sk += k[i], sr += r[i], scs += cs[i], srs += rs[i];
+      sq += q[i], sk += k[i], scs += cs[i], srs += rs[i];
     }
     float around = around_of[c];
     if (BLOCKS > 1) {
+      static_assert(BLOCKS == 1 || BLOCKS == 4, "blocks that others lie around: 1 and 2");
       const int block = lane / LANES;
       const float bq = group_sum<LANES>(sq), bk = group_sum<LANES>(sk);
-      const float bc = group_sum<LANES>(scs), br = group_sum<LANES>(srs);
-      float across = 0.f, mine = 0.f;  // pairs across block x
+      const float2 across = p.across[(size_t)seq * p.chunks + c0 + c];
 #pragma unroll
       for (int x = 0; x < BLOCKS; ++x) {
-        if (x > 0) across -= __shfl_sync(0xffffffffu, bc, x * LANES);
-        if (x == block && x > 0 && x < BLOCKS - 1) mine = across;
-        across += __shfl_sync(0xffffffffu, br, x * LANES);
         const float xq = __shfl_sync(0xffffffffu, bq, x * LANES);
         const float xk = __shfl_sync(0xffffffffu, bk, x * LANES);
         if (x > block) around += xq;
         if (x < block) around += xk;
       }
-      around += mine;
+      around += block == 1 ? across.x : block == 2 ? across.y : 0.f;
     }
     const float q_behind = lanes_sum<false, LANES>(sq + scs, lane);
     const float k_before = lanes_sum<true, LANES>(sk + srs, lane);
-    const float r_behind = lanes_sum<false, LANES>(sr, lane);
-    const float r_before = lanes_sum<true, LANES>(sr, lane);
-    const bool first = lane % LANES < LANES / 2;  // the shorter of two sums that agree
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int t = (c0 + c) * C + lane * N + i;
-      float g = q_behind, before = k_before, pairs = first ? -r_before : r_behind;
+      float g = q_behind, before = k_before;
 #pragma unroll
       for (int j = 0; j < N; ++j) {
         if (j >= i) g += q[j] + cs[j];
         if (j < i) before += k[j] + rs[j];
-        if (first && j < i) pairs -= r[j];
-        if (!first && j >= i) pairs += r[j];
       }
-      g += before + pairs + around;
+      g += before + r[i] + around;
       if (t >= p.L) continue;
       if (p.decay_kind == LA_DECAY_GATE_LOGIT) g *= -1.f / (1.f + expf(-p.decay[base + t]));
       if (p.decay_kind == LA_DECAY_HEAD) total += g;
@@ -385,7 +375,7 @@ cudaError_t launch_chunk_bwd(const ChunkBwdArgs &a) {
   ChunkBwd p{a.q, a.k, a.v, a.dO, a.dq, a.dk_out, a.dv_out, a.decay, a.S0, a.dS_final, a.dS0,
              a.H, a.L, a.dk, a.dv, a.phi, a.decay_kind, plan.chunks, plan.segments, plan.per,
              nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr,
-             nullptr, kKeep / plan.chunk};
+             nullptr, nullptr, nullptr, kKeep / plan.chunk};
   float *by_segment = nullptr;
   lay_out(a, plan, decay_grad, static_cast<char *>(a.workspace), &p, &by_segment);
   cudaError_t e = cudaSuccess;

@@ -25,14 +25,16 @@
 // orientation that its products need (dO V^T for dq, V dO^T and K Q^T for dk and dv).
 //
 // A decay's gradient counts the pairs (i < t <= j) that it lies between: pairs within
-// the chunk (row and column sums of Q K^T . dO V^T . D), pairs with one token in it (dot
+// the chunk (sums over Q K^T . dO V^T . D), pairs with one token in it (dot
 // products of the rows of dq's and dk's second terms with q and k), and pairs
 // around it (<G, e^L_C S>, which follows from chunk to chunk by the same sums).
-// Formed this way nothing cancels beyond one chunk; q dq - k dk summed from the
+// Those of a chunk are added up pair by pair, so that a token that nearly resets the state, whose
+// gradient is small beside its neighbours', has all of its digits; q dq - k dk summed from the
 // sequence's end would lose the short decays to the long sums.  Followed from chunk to chunk the
 // sums' errors stay, and a per-head decay's gradient adds them up over all tokens: every 512
-// tokens S is kept for the backward walk, which forms <G, e^L_C S> anew (2 x 32 x 8192 x 128
-// with per-head decays: 4e-7 off; 4.5e-6 without, growing with the length to the power 1.5).
+// tokens, and at every chunk in which one token decays by more than 2^-5, S is kept for the
+// backward walk, which forms <G, e^L_C S> anew (2 x 32 x 8192 x 128
+// with per-head decays: 4.8e-7 off; 4.5e-6 without, growing with the length to the power 1.5).
 //
 // Precision.  Products run in bf16 with fp32 sums.  With bf16 inputs and outputs the
 // decayed scores and the states round once to bf16 as operands (the state itself
@@ -56,6 +58,7 @@
 namespace la {
 
 constexpr int kShares = 16;  // warps whose sums a <G, S> is left as, at most
+constexpr float kStrong = -5.f;  // log2 of a strong decay of one token
 
 // What the kernels get: the tensors, and the plan.
 struct ChunkBwd {
@@ -71,20 +74,24 @@ struct ChunkBwd {
   float2 *lam;                 // [seq][chunks][C] log2 of the decay from a chunk's start to a
                                // token, as a sum of two floats (unused without a decay)
   // Shares of ddecay [seq][L], or null: the pairs of a token with tokens before its chunk (rq)
-  // and behind it (rk), of its block of the chunk (rc: as the later one less as the earlier one),
-  // and of the chunk's blocks before (cs) and behind (rs) its own, where a chunk has blocks.
+  // and behind it (rk), the pairs of its block of the chunk that it lies between (rc), and its
+  // pairs with the chunk's blocks before (cs) and behind (rs) its own, where a chunk has blocks.
   float *rq, *rk, *rc, *cs, *rs;
+  float2 *across;              // [seq][chunks] pairs of a chunk's blocks around block 1 and block 2
   float *around;               // [seq][segments] <G, e^L_C S> of a segment's last chunk
-  float *kept;                 // [seq][chunks / every] S before the last of `every` chunks
-  float *between;              // [seq][chunks / every][kShares] <G, e^L_C S> of that chunk
+  unsigned char *strong;       // [seq][chunks] whether a token of the chunk decays by kStrong
+  float *kept;                 // [seq][chunks - 1] S before a chunk that keeps() it
+  float *between;              // [seq][chunks - 1][kShares] <G, e^L_C S> of such a chunk
   int every;
 
-  // Whether chunk c, with its segment ending in front of c1, is one that S is kept for.
-  __device__ __forceinline__ bool keeps(int c, int c1) const {
-    return kept && c + 1 < c1 && (c + 1) % every == 0;
+  // Whether chunk c, with its segment ending in front of c1, is one that S is kept for: the last
+  // of `every` chunks, and one with a strong decay, whose token's gradient is so much smaller
+  // than its neighbours' that a difference of theirs would not leave much of it.
+  __device__ __forceinline__ bool keeps(int seq, int c, int c1) const {
+    return kept && c + 1 < c1 && ((c + 1) % every == 0 || strong[(size_t)seq * chunks + c]);
   }
   __device__ __forceinline__ size_t keep_slot(int seq, int c) const {
-    return (size_t)seq * (chunks / every) + c / every;
+    return (size_t)seq * (chunks - 1) + c;
   }
 };
 
@@ -110,6 +117,28 @@ template <typename T_, int D_, int C_, int NI_, int NM_> struct BwdConfig {
   static constexpr uint32_t STATE = D * D * 2;
   static_assert(WARPS % ROWS == 0 && COLS % 16 == 0, "whole column tiles");
 };
+
+// The sum of v over the warp's lanes in front of this one (FRONT) or behind it, within groups of
+// WIDTH lanes.
+template <bool FRONT, int WIDTH> __device__ __forceinline__ float lanes_sum(float v, int lane) {
+  const int at = lane % WIDTH;
+  float x = v;
+#pragma unroll
+  for (int off = 1; off < WIDTH; off <<= 1) {
+    const float y = FRONT ? __shfl_up_sync(0xffffffffu, x, off, WIDTH)
+                          : __shfl_down_sync(0xffffffffu, x, off, WIDTH);
+    if (FRONT ? at >= off : at + off < WIDTH) x += y;
+  }
+  const float y = FRONT ? __shfl_up_sync(0xffffffffu, x, 1, WIDTH)
+                        : __shfl_down_sync(0xffffffffu, x, 1, WIDTH);
+  return FRONT ? at ? y : 0.f : at < WIDTH - 1 ? y : 0.f;
+}
+// Their sum over such a group.
+template <int WIDTH> __device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+  for (int off = WIDTH / 2; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  return v;
+}
 
 // Per-chunk decay factors in shared memory.
 template <int C> struct ChunkDecay {
@@ -527,8 +556,8 @@ __device__ __forceinline__ float2 row_dots(const float (&acc)[NT][4], const void
 template <typename F> struct BwdShared {
   ChunkDecay<F::C> decay;
   float rows[F::SPLIT][F::C];  // row sums of the warps that share a group
-  float cols[F::ROWS][F::C];   // column sums of the groups
-  float pairs[F::SHARE ? F::SPLIT : 1][F::C];  // row sums of shared scores
+  float cols[F::ROWS][F::C];   // pairs of a group's rows that the chunk's tokens lie between
+  float pairs[F::SHARE ? F::SPLIT : 1][F::C];  // row sums of the pairs of shared scores
   float sum[F::WARPS];
 };
 template <typename F> constexpr uint32_t bwd_shared_bytes() {
@@ -616,10 +645,11 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_q_kernel(const Chu
   for (int c = c0; c < c1; ++c) {
     const int t0 = c * F::C;
     const uint32_t tk = tiles, tv = tk + X, td = tv + Y;
+    const bool keep = F::NI > 1 && p.keeps(seq, c, c1);
     load(t0);
     chunk_decay<F::C>(p, seq, c, sh.decay);
     __syncthreads();
-    if (F::NI > 1 && p.keeps(c, c1))
+    if (keep)
       keep_state<F>(p.kept + p.keep_slot(seq, c) * F::D * F::D, state_tile);
     // dO V^T . D: rows j of the group, tokens i <= j
     float w[F::C / 8][4] = {};
@@ -742,10 +772,11 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_kv_kernel(const Ch
     const int t0 = c * F::C;
     const uint32_t tq = tiles;
     const uint32_t tk = tq + X, tv = tk + X, td = tv + Y;
+    const bool keep = F::NI > 1 && p.keeps(seq, c, c1);
     load(t0);
     chunk_decay<F::C>(p, seq, c, sh.decay);
     __syncthreads();
-    if (F::NI > 1 && p.keeps(c, c1)) {
+    if (keep) {
       float s = dot_kept<F>(p.kept + p.keep_slot(seq, c) * F::D * F::D, state_tile);
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
@@ -756,23 +787,38 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_kv_kernel(const Ch
     // K Q^T . D and V dO^T . D: rows i of the group, tokens j >= i
     float w[CT][4] = {}, dw[CT][4] = {};
     auto live = [&](int j) { return j >= group; };
-    float row_sum[2] = {0.f, 0.f};
-    // Four scores of both: masked, decayed, and their pairs added up.
-    auto masked = [&](float (&x)[4], float (&y)[4], int col, float (&sum)[2]) {
+    // Four scores of both, masked and decayed, and their pairs.
+    auto masked = [&](float (&x)[4], float (&y)[4], int col, float (&pair)[4]) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int i = r0 + lane / 4 + e / 2 * 8, j = col + lane % 4 * 2 + e % 2;
         float f = 1.f;
         if (p.decay_kind != LA_DECAY_NONE)
           f = decay_between(sh.decay.lam[j], sh.decay.lam[i <= j ? i : j]);
-        const float pair = i < j ? x[e] * y[e] * f : 0.f;
-        row_sum[e / 2] += pair;
-        sum[e % 2] += pair;
+        pair[e] = i < j ? x[e] * y[e] * f : 0.f;
         x[e] = i <= j ? x[e] * f : 0.f;
         y[e] = i <= j ? y[e] * f : 0.f;
       }
     };
-    auto put_cols = [&](float (&sum)[2], int col) {
+    // The pairs i < t <= j for the tokens t of eight columns: j in them or, by `behind`, the sum of
+    // a row's pairs with the columns behind them.  A row's sum from each column on, which joins
+    // `behind`, then for each column the sum over the rows before it.
+    auto put_crossing = [&](const float (&pair)[4], int col, float (&behind)[2]) {
+      float sum[2] = {0.f, 0.f};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int at = lane % 4, i = r0 + lane / 4 + 8 * h, t = col + at * 2;
+        float from = pair[2 * h] + pair[2 * h + 1];  // on to the sum of this lane's and those behind
+        float x = __shfl_down_sync(0xffffffffu, from, 1, 4);
+        from += at < 3 ? x : 0.f;
+        x = __shfl_down_sync(0xffffffffu, from, 2, 4);
+        from += at < 2 ? x : 0.f;
+        x = __shfl_down_sync(0xffffffffu, from, 1, 4);
+        const float last = pair[2 * h + 1] + ((at < 3 ? x : 0.f) + behind[h]);
+        sum[0] += i < t ? pair[2 * h] + last : 0.f;
+        sum[1] += i < t + 1 ? last : 0.f;
+        behind[h] += __shfl_sync(0xffffffffu, from, 0, 4);
+      }
 #pragma unroll
       for (int off = 4; off < 32; off <<= 1) {
         sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], off);
@@ -783,34 +829,39 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_kv_kernel(const Ch
         sh.cols[group][col + lane * 2 + 1] = sum[1];
       }
     };
+    float behind[2] = {0.f, 0.f};
     if constexpr (F::SHARE) {
-      float sum[2] = {0.f, 0.f};
+      float pair[4] = {};
       if (live(part / 2)) {
         float x[4] = {}, y[4] = {};
         score_tile<F, F::NI, F::NI>(x, tk, r0, tq, part * 8, lane);
         score_tile<F, F::NV, F::NV>(y, tv, r0, td, part * 8, lane);
-        masked(x, y, part * 8, sum);
+        masked(x, y, part * 8, pair);
         put_scores<F>(scores, x, r0, part * 8, lane);
         put_scores<F>(scores + F::NO * F::SCORES, y, r0, part * 8, lane);
       }
-      if (p.rc) put_cols(sum, part * 8);
+      if (p.rc) {
+        put_crossing(pair, part * 8, behind);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)  // a row's pairs with the warp's columns, for those before them
+          if (lane % 4 == 0) sh.pairs[part][r0 + lane / 4 + 8 * h] = behind[h];
+      }
     } else {
       rows_times_rows<F, CT, F::NI, F::NI>(w, tk, F::TILE, r0, tq, F::TILE, 0, lane, live);
       rows_times_rows<F, CT, F::NV, F::NV>(dw, tv, F::TILE, r0, td, F::TILE, 0, lane, live);
+      constexpr int OWN = CT / F::SPLIT;  // columns (by 8) whose tokens a warp of the group adds up
+      float later[2] = {0.f, 0.f};
 #pragma unroll
-      for (int n = 0; n < CT; ++n) {
-        float sum[2] = {0.f, 0.f};
-        if (n / 2 >= group) masked(w[n], dw[n], n * 8, sum);
-        if (p.rc && part == 0) put_cols(sum, n * 8);
-      }
-    }
-    if (p.rc) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        row_sum[h] += __shfl_xor_sync(0xffffffffu, row_sum[h], 1);
-        row_sum[h] += __shfl_xor_sync(0xffffffffu, row_sum[h], 2);
-        if (lane % 4 == 0 && (F::SHARE || part == 0))
-          sh.pairs[F::SHARE ? part : 0][r0 + lane / 4 + 8 * h] = row_sum[h];
+      for (int n = CT - 1; n >= 0; --n) {
+        float pair[4] = {};
+        if (n / 2 >= group) masked(w[n], dw[n], n * 8, pair);
+        if (!p.rc || n / OWN < part) continue;
+        if (n / OWN > part) {
+          later[0] += pair[0] + pair[1], later[1] += pair[2] + pair[3];
+          continue;
+        }
+        if (n % OWN == OWN - 1) behind[0] = group_sum<4>(later[0]), behind[1] = group_sum<4>(later[1]);
+        put_crossing(pair, n * 8, behind);
       }
     }
     auto frag = [&](uint32_t (&a)[F::NO][4], int j) {
@@ -854,17 +905,25 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_kv_kernel(const Ch
     __syncthreads();
     if (p.rk) {
       const int t = threadIdx.x;
+      float others = 0.f;  // pairs of the rows before t with the columns of the warps behind t's
+      if constexpr (F::SHARE) {
+        static_assert(F::C == 32, "a warp holds a row of each");
+        if (warp == 0) {
+#pragma unroll
+          for (int i = 1; i < F::SPLIT; ++i) {
+            const float before = lanes_sum<true, 32>(sh.pairs[i][lane], lane);
+            if (i > lane / 8) others += before;
+          }
+        }
+      }
       if (t < F::C && t0 + t < p.L) {
         float s = 0.f, cols = 0.f;
 #pragma unroll
         for (int i = 0; i < F::SPLIT; ++i) s += sh.rows[i][t];
 #pragma unroll
         for (int i = 0; i < F::ROWS; ++i) cols += sh.cols[i][t];
-        // a token's pairs as the later one less those as the earlier one
-#pragma unroll
-        for (int i = 0; i < (F::SHARE ? F::SPLIT : 1); ++i) cols -= sh.pairs[i][t];
         p.rk[(size_t)seq * p.L + t0 + t] = s;
-        p.rc[(size_t)seq * p.L + t0 + t] = cols;
+        p.rc[(size_t)seq * p.L + t0 + t] = cols + others;
       }
     }
     if (more) state.planes(state_tile, warp, lane);

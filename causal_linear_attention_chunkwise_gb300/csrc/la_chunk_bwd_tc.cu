@@ -448,6 +448,23 @@ __device__ __forceinline__ void stage_8(uint4 *cell, const uint4 *raw, const flo
   *cell = make_uint4(la::pack_bf16(y[0], y[1]), la::pack_bf16(y[2], y[3]),
                      la::pack_bf16(y[4], y[5]), la::pack_bf16(y[6], y[7]));
 }
+// 16 values in each lane: the sum of value l % 16 over the 16 lanes of this half of the warp.  Each
+// step halves the values that a lane keeps.
+__device__ __forceinline__ float lanes_of_16(float (&v)[16], int lane) {
+#pragma unroll
+  for (int off = 8; off > 0; off >>= 1) {
+    const bool up = lane & off;
+#pragma unroll
+    for (int i = 0; i < off; ++i)
+      v[i] = (up ? v[i + off] : v[i]) + __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + off], off);
+  }
+  return v[0];
+}
+// The same of two: lo in the lanes below 16, hi in the others, each over both halves.
+__device__ __forceinline__ float lanes_of_2(float lo, float hi, int lane) {
+  const bool up = lane & 16;
+  return (up ? hi : lo) + __shfl_xor_sync(0xffffffffu, up ? lo : hi, 16);
+}
 __device__ __forceinline__ float dot_8(const uint4 &u, const float *f, float s) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -604,14 +621,14 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
   // NM = 3: Q K^T as well, in the scores' share's place or behind everything.
   constexpr uint32_t T_P = D == 128 ? T_OUT : 384;
   // the parts' sums of a row
-  constexpr uint32_t T_MORE = T_A + 64;
-  static_assert(T_MORE + 8 <= (D == 128 ? COLUMNS : T_P), "tensor memory");
+  constexpr uint32_t T_MORE = T_A + 64, T_CROSS = T_MORE + 8;
+  static_assert(T_CROSS + 32 <= (D == 128 ? COLUMNS : T_P), "tensor memory");
   extern __shared__ __align__(1024) unsigned char smem[];
   Block b;
   b.start(smem, SM::OFF_BAR, COLUMNS, err);
   float2 *lam = reinterpret_cast<float2 *>(smem + SM::OFF_LAM);
   float *fac = reinterpret_cast<float *>(smem + SM::OFF_FAC);
-  float *inside = reinterpret_cast<float *>(smem + SM::OFF_MORE);  // factors of pairs of one block
+  float *sums = reinterpret_cast<float *>(smem + SM::OFF_MORE);  // of warps
   const int seq = blockIdx.x / p.segments, seg = blockIdx.x % p.segments;
   const int c0 = seg * p.per, c1 = min(c0 + p.per, p.chunks);
   const size_t es = (size_t)p.n_k * p.n_v;
@@ -660,9 +677,9 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
     const bool more = c + 1 < c1;
     if (decays && b.part == 0) {
       next.put<false>(b, lam, fac);
-      if (NM == 3) inside[b.row] = decay_between(next.before, next.own);
       if (more) next.load(p, b, seq, c + 1);
     }
+    const bool keep = NM == 3 && DECAY && p.keeps(seq, c, c1);
     b.wait_full(stage(c), TWO ? (c - c0) >> 1 & 1 : phase);
     if (PHI) map_tile_tc<D>(smem + TK, smem + TK, p.L - t0, p.n_k);
     fence_proxy_async_smem();
@@ -693,11 +710,10 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
     const float2 own = decays ? lam[b.row] : make_float2(0.f, 0.f);
     const float2 end = decays ? lam[CT - 1] : make_float2(0.f, 0.f);
     const float2 all = exp2_two(end);
-    if (NM == 3 && DECAY && p.keeps(c, c1)) state.keep(p.kept + p.keep_slot(seq, c) * (D * D), b);
+    if (keep) state.keep(p.kept + p.keep_slot(seq, c) * (D * D), b);
     b.wait_mma(0, phase);
     // the scores as operand: row j, tokens i <= j
-    const float2 before = DECAY && b.quarter ? lam[b.quarter * 32 - 1] : make_float2(0.f, 0.f);
-    float pairs = 0.f, pairs_in = 0.f;  // with tokens of the blocks before, of this block
+    float pairs = 0.f;  // with tokens of the blocks before
     {
       const int block = b.part;
       const bool diagonal = block == b.quarter;
@@ -707,27 +723,34 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
         for (int e = 0; e < 16; ++e) w[e] = 0;
       } else {
         RowDecay decay;
-        if (DECAY) {
-          decay.start<false>(b, block, lam, fac, own);
-          if (NM == 3 && diagonal && b.narrow[block]) {  // grad_kv_tc_kernel's factors: see rc
-            decay.factors = inside + block * 32;
-            decay.mine = decay_between(own, before);
-          }
-        }
+        if (DECAY) decay.start<false>(b, block, lam, fac, own);
+        float run = 0.f;
 #pragma unroll
         for (int y = 0; y < 32; y += 16) {
           float f[16], d[16];
           load_16(b, T_S + block * 32 + y, f);
           if (DECAY) decay.get(y, d);
           if (NM == 3 && DECAY) {
-            float g[16], s[2] = {0.f, 0.f};
+            float g[16];
             load_16(b, T_P + block * 32 + y, g);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float pair = g[e] * d[e] * f[e];
-              s[e % 2] += !diagonal || y + e < b.lane ? pair : 0.f;
+            for (int e = 0; e < 16; ++e) g[e] *= d[e] * f[e];
+            if (diagonal) {
+              // Row j's pairs with the tokens in front of t, for the t that are not behind it: added
+              // over the rows they are the pairs i < t <= j, while the state's update runs.
+              uint32_t r[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                r[e] = __float_as_uint(y + e <= b.lane ? run : 0.f);
+                run += g[e];
+              }
+              tmem_st16(b.at(T_CROSS + y), r);
+            } else {
+              float s[2] = {0.f, 0.f};
+#pragma unroll
+              for (int e = 0; e < 16; ++e) s[e % 2] += g[e];
+              pairs += s[0] + s[1];
             }
-            (diagonal ? pairs_in : pairs) += s[0] + s[1];
           }
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
@@ -792,7 +815,15 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
         stage_8<PHI>(cell, cell, g + e);
       }
     }
-    if (NM == 3 && DECAY) b.leave(T_MORE, dot, pairs);
+    if (NM == 3 && DECAY) {
+      b.leave(T_MORE, dot, pairs);
+      if (b.quarter >= b.part + 2) {  // pairs of blocks with others between them
+        float s = pairs;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+        if (b.lane == 0) sums[b.quarter - 2 + b.part] = s;  // 2 and 0, 3 and 0, 3 and 1
+      }
+    }
     fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
@@ -801,10 +832,18 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
       tma_store_commit();
     }
     if (NM == 3 && DECAY && b.part == 0) b.gather(T_MORE, dot, pairs);
-    if (NM == 3 && p.rq && t < p.L) {
+    if (NM == 3 && DECAY && p.rq) {
       const size_t to = (size_t)seq * p.L + t;
-      if (b.part == 0) p.rq[to] = dot, p.cs[to] = pairs;
-      if (b.part == b.quarter) p.rc[to] = pairs_in;  // who has the diagonal
+      if (b.part == 0 && t < p.L) p.rq[to] = dot, p.cs[to] = pairs;
+      if (b.part == b.quarter) {  // who has the diagonal: lane t of 32 sums over the rows
+        float f[16], g[16];
+        load_16(b, T_CROSS, f);
+        load_16(b, T_CROSS + 16, g);
+        const float x = lanes_of_2(lanes_of_16(f, b.lane), lanes_of_16(g, b.lane), b.lane);
+        if (t < p.L) p.rc[to] = x;
+      }
+      if (threadIdx.x == 0)
+        p.across[(size_t)seq * p.chunks + c] = make_float2(sums[0] + sums[1], sums[1] + sums[2]);
     }
     if (more) {
       b.wait_mma(3, phase);
@@ -829,7 +868,6 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
   if (NM == 3 && p.rq) {
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) around += __shfl_xor_sync(0xffffffffu, around, off);
-    float *sums = inside;
     __syncthreads();
     if (b.lane == 0) sums[b.warp] = around;
     __syncthreads();
@@ -920,6 +958,7 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
       next.put<true>(b, lam, fac);
       if (more) next.load(p, b, seq, c - 1);
     }
+    const bool keep = NM == 3 && DECAY && p.keeps(seq, c, c1);
     b.wait_full(stage(c), TWO ? done >> 1 & 1 : phase);
     if (PHI) {
       map_tile_tc<D>(smem + TQ, smem + TQ, p.L - t0, p.n_k);
@@ -954,7 +993,7 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
     const float2 own = decays ? lam[b.row] : make_float2(0.f, 0.f);
     const float2 end = decays ? lam[CT - 1] : make_float2(0.f, 0.f);
     const float2 all = exp2_two(end);
-    if (NM == 3 && DECAY && p.keeps(c, c1)) {
+    if (keep) {
       float s = state.dot_kept(p.kept + p.keep_slot(seq, c) * (D * D), b);
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
@@ -966,7 +1005,7 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
     b.wait_mma(0, phase);
     // the scores as operands: row i, tokens j >= i
     uint32_t wp[16], wd[16];
-    float pairs = 0.f, pairs_in = 0.f;  // with tokens of the blocks behind, of this block
+    float pairs = 0.f;  // with tokens of the blocks behind
     const int block = b.part;
     const bool diagonal = block == b.quarter;
     if (block < b.quarter) {  // all in front of the warp's rows
@@ -981,14 +1020,11 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
         load_16(b, T_P + block * 32 + y, f);
         load_16(b, T_DP + block * 32 + y, g);
         if (DECAY) decay.get(y, d);
-        if (NM == 3 && DECAY) {
+        if (NM == 3 && DECAY && !diagonal) {
           float s[2] = {0.f, 0.f};
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float pair = f[e] * d[e] * g[e];
-            s[e % 2] += !diagonal || y + e > b.lane ? pair : 0.f;
-          }
-          (diagonal ? pairs_in : pairs) += s[0] + s[1];
+          for (int e = 0; e < 16; ++e) s[e % 2] += f[e] * d[e] * g[e];
+          pairs += s[0] + s[1];
         }
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
@@ -1054,9 +1090,6 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
     if (NM == 3 && p.rk && t < p.L) {
       const size_t to = (size_t)seq * p.L + t;
       if (b.part == 0) p.rk[to] = dot, p.rs[to] = pairs;
-      // A block's pairs enter rc as their later token's less as their earlier one's, and
-      // cancel in sums: both kernels form them from the same factors.
-      if (diagonal) p.rc[to] -= pairs_in;
     }
     if (update && decays) {
       decayed_rows<D, NM, CT>(smem + TQ, smem, 0, [&](int i) { return ex2_approx(lam[i].x); });

@@ -534,8 +534,10 @@ la_status la_rotary_bwd(const void *dq, long long q_b_stride, long long q_h_stri
  * With bf16 tensors, dq, dk and dv come from operands rounded once to bf16 (the
  * decayed scores, the states and, for elu + 1, phi's values), with fp32 sums and
  * states.  Where ddecay or dS0 is wanted those that they depend on keep fp32's
- * 24 bits, at about twice the work; with fp32 tensors all do.  A log decay below -200
- * counts as a decay of zero.
+ * 24 bits, at about twice the work; with fp32 tensors all do.  ddecay adds up the pairs
+ * that a token lies between, so that of a token that nearly resets the state, however
+ * small beside its neighbours', is as exact as theirs.  A log decay below -200 counts as a
+ * decay of zero.
  *
  * q, k, v, dO, dq, dk, dv and the states are 16-byte aligned, decays 4-byte.
  * Supported: d_k, d_v in {16, 32, 64, 128}, L up to 2^30.  L = 0 passes
