@@ -52,6 +52,7 @@ SIGNATURES = {
     "la_chunk_bwd": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp,
                           _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "la_chunk_bwd_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i, _i]),
+    "la_chunk_bwd_workspace_bytes_for": (_sz, [_i, _i, _i, _i, _i, _i, _i, _i, _i, _i]),
     "la_gated_norm_bwd": (_i, [_vp, _ll, _vp, _ll, _ll, _ll, _vp, _ll, _i, _i, _i, _i, _i, _i, _i,
                                _i, _vp, _vp, _i, _f, _vp, _ll, _ll, _ll, _vp, _ll, _vp, _vp, _vp,
                                _sz, _vp]),

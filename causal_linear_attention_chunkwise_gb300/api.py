@@ -706,6 +706,16 @@ def la_chunk_bwd_workspace_bytes(B, H, L, d_k, d_v, chunk=64, dtype=torch.bfloat
                                                            DTYPE[dtype]))
 
 
+def la_chunk_bwd_workspace_bytes_for(B, H, L, d_k, d_v, chunk=64, dtype=torch.bfloat16,
+                                     decay_kind="none", ddecay=False, dS0=False) -> int:
+    """What one call needs, with the feature map set now: ``ddecay`` and ``dS0`` whether those
+    gradients are formed.  (``la_chunk_bwd_workspace_bytes`` is enough for any call.)"""
+    if max(B, H, L, d_k, d_v, chunk) > _INT_MAX:
+        raise _too_large(B, H, L, d_k, d_v, chunk)
+    return int(_native.load().la_chunk_bwd_workspace_bytes_for(
+        B, H, L, d_k, d_v, chunk, DTYPE[dtype], DECAY[decay_kind], ddecay, dS0))
+
+
 def _dense(t, shape, dtype, what):
     if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous {dtype} {list(shape)}")
@@ -751,8 +761,9 @@ def la_chunk_bwd(q, k, v, dO, chunk=64, decay_kind="none", decay=None, S0=None, 
     lib = _native.load()
     ws = ws_bytes = 0
     if workspace is None:
-        workspace = _scratch(lib.la_chunk_bwd_workspace_bytes(B, H, L, d_k, d_v, chunk,
-                                                              DTYPE[dtype]), q, stream)
+        workspace = _scratch(lib.la_chunk_bwd_workspace_bytes_for(
+            B, H, L, d_k, d_v, chunk, DTYPE[dtype], kind, ddecay is not None, dS0 is not None), q,
+            stream)
     if workspace is not None:
         ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     status = lib.la_chunk_bwd(

@@ -136,6 +136,13 @@ bool aligned_elt(const void *p, size_t elt) {
   return (reinterpret_cast<uintptr_t>(p) & (elt - 1)) == 0;
 }
 
+// Sizes that la_chunk_bwd supports, with tokens to work on.
+bool chunk_bwd_sizes(int B, int H, int L, int d_k, int d_v, int chunk, int dtype) {
+  return B > 0 && H > 0 && L > 0 && L <= kMaxLen && (long long)B * H <= 0x7fffffffll &&
+         supported_d(d_k) && supported_d(d_v) && chunk >= 1 && chunk <= 64 &&
+         (dtype == LA_F32 || dtype == LA_BF16);
+}
+
 // A [B,H,L,d] tensor with strides, in elements; its last axis is dense.
 struct Heads {
   const void *p;
@@ -896,13 +903,21 @@ la_status la_rotary_frequencies(int rotary_dim, double base, int scaling, double
 }
 
 size_t la_chunk_bwd_workspace_bytes(int B, int H, int L, int d_k, int d_v, int chunk, int dtype) {
-  if (B <= 0 || H <= 0 || L <= 0 || L > kMaxLen || (long long)B * H > 0x7fffffffll ||
-      !supported_d(d_k) || !supported_d(d_v) || chunk < 1 || chunk > 64 ||
-      (dtype != LA_F32 && dtype != LA_BF16))
-    return 0;
+  if (!chunk_bwd_sizes(B, H, L, d_k, d_v, chunk, dtype)) return 0;
   ChunkBwdArgs a{};
   a.dtype = dtype; a.B = B; a.H = H; a.L = L; a.dk = d_k; a.dv = d_v;
   return chunk_bwd_workspace_bytes(a);
+}
+
+size_t la_chunk_bwd_workspace_bytes_for(int B, int H, int L, int d_k, int d_v, int chunk, int dtype,
+                                        int decay_kind, int ddecay, int dS0) {
+  if (!chunk_bwd_sizes(B, H, L, d_k, d_v, chunk, dtype) || decay_kind < LA_DECAY_NONE ||
+      decay_kind > LA_DECAY_GATE_LOGIT || (decay_kind == LA_DECAY_NONE && ddecay))
+    return 0;
+  ChunkBwdArgs a{};
+  a.dtype = dtype; a.B = B; a.H = H; a.L = L; a.dk = d_k; a.dv = d_v;
+  a.phi = g_phi.load(), a.decay_kind = decay_kind;
+  return chunk_bwd_workspace_need(a, ddecay != 0, dS0 != 0);
 }
 
 la_status la_chunk_bwd(const void *q, const void *k, const void *v, int dtype, int B, int H,
@@ -965,17 +980,15 @@ la_status la_chunk_bwd(const void *q, const void *k, const void *v, int dtype, i
   ChunkBwdArgs a{q, k, v, dO, dtype, B, H, L, d_k, d_v, g_phi.load(), decay_kind,
                  decay_kind == LA_DECAY_NONE ? nullptr : decay, S0, dS_final, dq, dk, dv, ddecay,
                  dS0, workspace, st};
-  const size_t need = chunk_bwd_workspace_bytes(a);
-  if (need > 0) {
-    if (!workspace || ws_bytes < need)
-      return fail(LA_ERR_INVALID_ARG, "%s: workspace of %zu bytes needed, %zu given", fn, need,
-                  workspace ? ws_bytes : (size_t)0);
-    if (!aligned16(workspace))
-      return fail(LA_ERR_INVALID_ARG, "%s: workspace must be 16-byte aligned", fn);
-    const Rows ws = dense(workspace, need);
-    if (overlap_any(ws, in) || overlap_any(ws, out) || overlap(ws, sf))
-      return fail(LA_ERR_INVALID_ARG, "%s: the workspace overlaps an input or an output", fn);
-  }
+  const size_t need = chunk_bwd_workspace_need(a, ddecay != nullptr, dS0 != nullptr);
+  if (!workspace || ws_bytes < need)
+    return fail(LA_ERR_INVALID_ARG, "%s: workspace of %zu bytes needed, %zu given", fn, need,
+                workspace ? ws_bytes : (size_t)0);
+  if (!aligned16(workspace))
+    return fail(LA_ERR_INVALID_ARG, "%s: workspace must be 16-byte aligned", fn);
+  const Rows ws = dense(workspace, need);
+  if (overlap_any(ws, in) || overlap_any(ws, out) || overlap(ws, sf))
+    return fail(LA_ERR_INVALID_ARG, "%s: the workspace overlaps an input or an output", fn);
   cudaError_t e = launch_chunk_bwd(a);
   if (e != cudaSuccess) return cuda_fail(e, fn);
   return ok();

@@ -354,6 +354,11 @@ cudaError_t launch_segment_scan(const ChunkBwd &p, int seqs, cudaStream_t stream
   return cudaSuccess;
 }
 
+size_t chunk_bwd_workspace_need(const ChunkBwdArgs &a, bool ddecay, bool dS0) {
+  const size_t need = lay_out(a, make_plan(a, ddecay || dS0), ddecay, nullptr, nullptr, nullptr);
+  return std::max(need, round_up(1));
+}
+
 size_t chunk_bwd_workspace_bytes(const ChunkBwdArgs &a) {
   // Enough for either feature map and any set of outputs.
   size_t most = 0;

@@ -227,6 +227,7 @@ struct ChunkBwdArgs {
   cudaStream_t stream;
 };
 size_t chunk_bwd_workspace_bytes(const ChunkBwdArgs &a);
+size_t chunk_bwd_workspace_need(const ChunkBwdArgs &a, bool ddecay, bool dS0);
 cudaError_t launch_chunk_bwd(const ChunkBwdArgs &a);
 
 // Backward passes of the norms around a block (width 1..16384).

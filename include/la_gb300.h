@@ -528,8 +528,10 @@ la_status la_rotary_bwd(const void *dq, long long q_b_stride, long long q_h_stri
  *   dS0        [B,H,d_k,d_v] fp32, the gradient of S0 (given or not), or NULL:
  *              a long sequence's pieces run back to front, each handing its
  *              dS0 on as the dS_final of the one before
- *   workspace  device scratch of la_chunk_bwd_workspace_bytes(...) bytes (for
- *              any feature map, decay and set of outputs)
+ *   workspace  device scratch of la_chunk_bwd_workspace_bytes_for(...) bytes,
+ *              which this call needs (with the feature map set now, its decay kind and
+ *              whether ddecay and dS0 are wanted), or of la_chunk_bwd_workspace_bytes(...),
+ *              enough for any of them
  *
  * With bf16 tensors, dq, dk and dv come from operands rounded once to bf16 (the
  * decayed scores, the states and, for elu + 1, phi's values), with fp32 sums and
@@ -549,6 +551,8 @@ la_status la_chunk_bwd(const void *q, const void *k, const void *v, int dtype, i
                        void *dv, float *ddecay, float *dS0, void *workspace, size_t ws_bytes,
                        void *cuda_stream);
 size_t la_chunk_bwd_workspace_bytes(int B, int H, int L, int d_k, int d_v, int chunk, int dtype);
+size_t la_chunk_bwd_workspace_bytes_for(int B, int H, int L, int d_k, int d_v, int chunk,
+                                        int dtype, int decay_kind, int ddecay, int dS0);
 
 /*
  * Backward pass of la_gated_norm_fwd, of the same arguments:
