@@ -15,8 +15,8 @@ cudaError_t launch_chunk_bwd_f32(const ChunkBwd &p, int seqs, bool wide, bool bf
 namespace {
 
 constexpr int kMaxPer = 512;  // chunks of a segment (the decays' kernel keeps sums of them)
-// Tokens from one kept state to the next: with 1024 the gradients of 2 x 32 x 8192 x 128 with
-// per-head decays take 521 us, not 530, and ddecay is up to 7.6e-7 off, not 4.8e-7.
+// Tokens from one kept state to the next, of slow decays: with 1024 the gradients of 2 x 32 x 8192 x
+// 128 with per-head decays took 521 us, not 530, and ddecay was up to 7.6e-7 off, not 4.8e-7.
 constexpr int kKeep = 512;
 constexpr int kShort = 64;    // tokens of the bf16 kernels' one chunk
 
@@ -32,7 +32,8 @@ struct Plan {
 // The segments that take the least time on 152 SMs, in units of a chunk of both
 // walks: whole waves of blocks, each a segment's chunks and a start; with more than one
 // segment also the pass over their own shares, S and G in blocks of their own at 0.2 of a chunk's
-// time, and two launches.  Compared when the kernels were a few per cent from now, it picks 2 segments
+// time, and two launches.  Compared when the kernels were up to 4% faster than now (the decays' kept
+// states and pairs came later), it picks 2 segments
 // for 2 x 32 x 8192 x 128 with decays (517 us; 1: 813, 4: 588, 7: 610), 9 for 1 x 16 x 32768 x 128
 // (543; 4: 969, 19: 571), 2 for 4 x 16 x 4096 x 64 (130; 1: 189, 4: 140), 9 for 3 x 5 x 777 x 64 x 128
 // fp32 (103; 5: 141, 13: 125), and a chunk each for one sequence of 300 tokens in fp32 (17; 5: 28, 1: 102).
@@ -43,7 +44,7 @@ Plan make_plan(const ChunkBwdArgs &a, bool f32_out) {
   p.planes = p.full || f32_out;
   // More narrow sequences of up to 64 tokens than there are SMs: tcgen05's block, of which an SM holds
   // one, stands alone with its start, its end and its few products.  64 x 32 x 64 x 64 with token
-  // decays 166 us, on tcgen05 252 (elu1 without: 110, 132); 8 x 32 x 64 x 64 30, 37; but 4 x 32 x 64
+  // decays 166 us from eager calls (146 in a graph), on tcgen05 252 (elu1 without: 110, 132); 8 x 32 x 64 x 64 30, 37; but 4 x 32 x 64
   // x 64 25, 21; 64 x 32 x 96 x 64 276, 256; 64 x 32 x 64 x 128 457, 458 (167, 137 without decays).
   p.tc = !p.full && !(a.L <= kShort && !p.wide && (long long)a.B * a.H > 152);
   p.chunk = p.tc ? 128 : p.full ? 32 : kShort;

@@ -19,8 +19,8 @@
 // segment's own share of S and G, a second one strings them together.
 //
 // Most bf16 calls run in la_chunk_bwd_tc.cu.  The kernels here take what enters as three bf16 planes,
-// fp32 tensors and phi = elu + 1 where an fp32 output is wanted (three planes of 128 tokens do
-// not fit beside one another there), and many short bf16 sequences.  A warp owns 16 tokens of a
+// fp32 tensors and phi = elu + 1 where an fp32 output is wanted (there is no such form there; at
+// width 128 three planes of 128 tokens would not fit), and many short bf16 sequences.  A warp owns 16 tokens of a
 // chunk (with others, which take other columns) and computes its rows of the score matrices in the
 // orientation that its products need (dO V^T for dq, V dO^T and K Q^T for dk and dv).
 //
@@ -516,8 +516,7 @@ __device__ __forceinline__ void store_rows(const float (&acc)[NT][4], void *dst,
       float f[2] = {acc[n][2 * h], acc[n][2 * h + 1]};
       if (raw && p.phi == LA_PHI_ELU1) {
         float y[2];
-        if constexpr (sizeof(T) == 4) load_raw<T, 2>(x + c).unpack(y);
-        else load_raw<T, 2>(x + c).unpack(y);
+        load_raw<T, 2>(x + c).unpack(y);
 #pragma unroll
         for (int e = 0; e < 2; ++e) f[e] *= y[e] > 0.f ? 1.f : expf(y[e]);
       }

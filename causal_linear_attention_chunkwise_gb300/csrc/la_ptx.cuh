@@ -317,8 +317,6 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const void *map, uint64_t
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
       : "memory");
 }
-// L2 policy for data read or written once: evicted before other lines, so a
-// stream of tiles does not push reused lines (other kernels' inputs, code) out.
 // The same box into L2 alone.
 __device__ __forceinline__ void tma_prefetch_3d(const void *map, int c0, int c1, int c2) {
   asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(map),
@@ -326,6 +324,8 @@ __device__ __forceinline__ void tma_prefetch_3d(const void *map, int c0, int c1,
                : "memory");
 }
 
+// L2 policy for data read or written once: evicted before other lines, so a
+// stream of tiles does not push reused lines (other kernels' inputs, code) out.
 __device__ __forceinline__ uint64_t l2_policy_evict_first() {
   uint64_t pol;
   asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(pol));
