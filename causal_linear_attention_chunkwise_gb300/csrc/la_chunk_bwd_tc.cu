@@ -1,7 +1,7 @@
 // la_chunk_bwd_tc.cu -- the backward walks on the 5th-gen tensor cores: bf16 inputs,
 // chunks of 128 tokens, widths padded to D = 64 or 128 (the copies fill with zeros and
 // leave out what lies past a row's end; mma.sync at these widths took 361 us for 4 x 16 x 4096 x
-// 32 x 64 with token decays, 468 for 2 x 16 x 4096 x 64 x 128, where these take 208 and 177).
+// 32 x 64 with token decays, 468 for 2 x 16 x 4096 x 64 x 128, where these take 198 and 163).
 //
 // The mathematics is la_chunk_bwd.cuh's, a chunk being one 128-row tile.  A
 // block of 512 threads owns a segment of a sequence and one chunk of it at a time, in
@@ -28,10 +28,16 @@
 // NM = 3: the state and the decayed operand as three bf16 planes, which hold all
 // of an fp32 value's bits, for the fp32 outputs (ddecay, dS0); one product each.
 //
-// What bounds it at D = 128, NM = 3: shared memory.  A chunk of grad_kv moves some 1.1 MB through
-// it (640 KB of them operands of the products, each of which takes its 512 clocks' whole
-// bandwidth), 9000 clocks of 13200; loads issued earlier, or dv's share scaled while dk's products
-// run, change nothing (545 us for 1 x 16 x 32768 x 128 gates with either, both or none).
+// What bounds it at D = 128, NM = 3: no unit by itself, but shared memory and the steps' order
+// together.  A chunk of grad_kv moves some 1.1 MB through shared memory (640 KB of them operands of
+// the products, each of which takes its 512 clocks' whole bandwidth), 9000 clocks of 13200; the
+// other third goes into five barriers of a block's 512 threads, and an SM holds one block (tensor
+// pipe 38% busy, shared memory 31% by the products and 22% by loads and stores, DRAM 48%).  Loads
+// issued earlier, or dv's share scaled while dk's products run, changed nothing (545 us, when it
+// took that, for 1 x 16 x 32768 x 128 gates with either, both or none).
+//
+// A call that wants dS0 alone leaves out the pairs and the row sums of ddecay (2 x 32 x 8192 x 128
+// with per-head decays and states: 478 us, with them 502).
 #include <cuda.h>
 
 #include <algorithm>
@@ -606,10 +612,11 @@ template <int D> constexpr int kStages = D == 64 ? 2 : 1;
 template <int D, int NM, bool PHI, bool DECAY>
 __global__ void __launch_bounds__(kThreads, 1)
 grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned int *err) {
-  // The fourth tile: q, where it is needed (for ddecay, for phi's derivative), then dq on its way out.
+  // The fourth tile: q, where it is needed (for ddecay, for phi's derivative), then dq on its way
+  // out.
   using SM = Smem<D, NM, 4, kStages<D>>;
   using ST = StateTile<D>;
-  constexpr bool TWO = kStages<D> == 2, HAS_Q = NM == 3 || PHI;
+  constexpr bool TWO = kStages<D> == 2, HAS_Q = (NM == 3 && DECAY) || PHI;
   // Tensor memory: dO V^T, the state's share, the scores' share, the scores as operand; the
   // state's update takes the place of dO V^T.
   constexpr uint32_t T_S = 0, T_IN = 128, T_OUT = 128 + D, T_A = 128 + 2 * D, COLUMNS = 512;
@@ -632,7 +639,7 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
   const int seq = blockIdx.x / p.segments, seg = blockIdx.x % p.segments;
   const int c0 = seg * p.per, c1 = min(c0 + p.per, p.chunks);
   const size_t es = (size_t)p.n_k * p.n_v;
-  constexpr bool decays = DECAY;
+  const bool shares = NM == 3 && DECAY && p.rq;  // of ddecay
   auto stage = [&](int c) { return TWO ? (c - c0) & 1 : 0; };
   auto tile = [&](int c, int i) {  // k, v, dO, q
     return SM::OFF_TILES + stage(c) * SM::STAGE + i * SM::TILE;
@@ -675,7 +682,7 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
     const uint32_t phase = (c - c0) & 1;
     const uint32_t TK = tile(c, 0), TV = tile(c, 1), TD = tile(c, 2), TQ = tile(c, 3);
     const bool more = c + 1 < c1;
-    if (decays && b.part == 0) {
+    if (DECAY && b.part == 0) {
       next.put<false>(b, lam, fac);
       if (more) next.load(p, b, seq, c + 1);
     }
@@ -689,7 +696,7 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
       tc_fence_after();
       const Operand a = along_row<SM::BOX>(b.base + TD);
       product<D>(b.tmem + T_S, a, along_row<SM::BOX>(b.base + TV), id_s, false);
-      if (NM == 3 && DECAY)
+      if (shares)
         product<D>(b.tmem + T_P, along_row<SM::BOX>(b.base + TQ), along_row<SM::BOX>(b.base + TK),
                    id_s, false);
       mma_commit(&b.mma[0]);
@@ -707,8 +714,8 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
         prefetch(c + 1);
       }
     }
-    const float2 own = decays ? lam[b.row] : make_float2(0.f, 0.f);
-    const float2 end = decays ? lam[CT - 1] : make_float2(0.f, 0.f);
+    const float2 own = DECAY ? lam[b.row] : make_float2(0.f, 0.f);
+    const float2 end = DECAY ? lam[CT - 1] : make_float2(0.f, 0.f);
     const float2 all = exp2_two(end);
     if (keep) state.keep(p.kept + p.keep_slot(seq, c) * (D * D), b);
     b.wait_mma(0, phase);
@@ -730,7 +737,7 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
           float f[16], d[16];
           load_16(b, T_S + block * 32 + y, f);
           if (DECAY) decay.get(y, d);
-          if (NM == 3 && DECAY) {
+          if (shares) {
             float g[16];
             load_16(b, T_P + block * 32 + y, g);
 #pragma unroll
@@ -776,14 +783,14 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
     if (threadIdx.x == kLeaderQ && more && !TWO) load_dO(c + 1);
     __syncwarp();
     if (more) {
-      if (decays) {
+      if (DECAY) {
         decayed_rows<D, NM, CT>(smem + TK, smem, 0, [&](int i) { return decay_between(end, lam[i]); });
         fence_proxy_async_smem();
         __syncthreads();
       }
       if (threadIdx.x == kLeaderQ) {  // the state's update, while dq leaves
         tc_fence_after();
-        if (decays) {
+        if (DECAY) {
 #pragma unroll
           for (int m = NM - 1; m >= 0; --m)
             product<CT>(b.tmem + T_S, along_col<SM::BOX>(b.base + m * SM::TILE), v, id_kv,
@@ -811,11 +818,11 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
 #pragma unroll
       for (int e = 0; e < 16; e += 8) {
         uint4 *cell = b.cell(TQ, b.part * N + x + e);
-        if (NM == 3) dot = dot_8(*cell, f + e, dot);
+        if (shares) dot = dot_8(*cell, f + e, dot);
         stage_8<PHI>(cell, cell, g + e);
       }
     }
-    if (NM == 3 && DECAY) {
+    if (shares) {
       b.leave(T_MORE, dot, pairs);
       if (b.quarter >= b.part + 2) {  // pairs of blocks with others between them
         float s = pairs;
@@ -831,8 +838,8 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
       store_tile_tma<D>(b, TQ, &maps.dq, t0, seq, p.n_k);
       tma_store_commit();
     }
-    if (NM == 3 && DECAY && b.part == 0) b.gather(T_MORE, dot, pairs);
-    if (NM == 3 && DECAY && p.rq) {
+    if (shares && b.part == 0) b.gather(T_MORE, dot, pairs);
+    if (shares) {
       const size_t to = (size_t)seq * p.L + t;
       if (b.part == 0 && t < p.L) p.rq[to] = dot, p.cs[to] = pairs;
       if (b.part == b.quarter) {  // who has the diagonal: lane t of 32 sums over the rows
@@ -855,7 +862,7 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
       __syncwarp();
       state.update(b, T_S, all);
       state.planes(b);
-    } else if (NM == 3 && p.rq) {  // <G, e^L_C S>: the pairs around the segment's last chunk
+    } else if (shares) {  // <G, e^L_C S>: the pairs around the segment's last chunk
       const float *G = seg + 1 < p.segments ? p.W + ((size_t)seq * (p.segments - 1) + seg) * es
                        : p.dSf ? p.dSf + (size_t)seq * es : nullptr;
       if (G) around = state.dot(G, b, p) * all.x;
@@ -865,7 +872,7 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
     if (c < c1) tc::drain_wait(&b.full[stage(c)], (TWO ? (c - c0) >> 1 : c - c0) & 1);
     tma_store_wait_all();
   }
-  if (NM == 3 && p.rq) {
+  if (shares) {
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) around += __shfl_xor_sync(0xffffffffu, around, off);
     __syncthreads();
@@ -913,7 +920,7 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
   const int seq = blockIdx.x / p.segments, seg = blockIdx.x % p.segments;
   const int c0 = seg * p.per, c1 = min(c0 + p.per, p.chunks), n = c1 - c0;
   const size_t es = (size_t)p.n_k * p.n_v;
-  constexpr bool decays = DECAY;
+  const bool shares = NM == 3 && DECAY && p.rk;  // of ddecay
   constexpr uint32_t MORE = SM::OFF_TILES + 4 * kStages<D> * SM::TILE;
   constexpr uint32_t OUT = MORE + PHI * SM::TILE;
   auto stage = [&](int c) { return TWO ? (c1 - 1 - c) & 1 : 0; };
@@ -954,7 +961,7 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
     const uint32_t TQ = tile(c, 0), TK = tile(c, 1), TV = tile(c, 2), TD = tile(c, 3);
     const uint32_t TKP = PHI ? MORE : TK, TDV = OWN ? OUT : TV, TDK = OWN ? OUT + SM::TILE : TK;
     const bool more = done + 1 < n, update = more || (p.dS0 && seg == 0);
-    if (decays && b.part == 0) {
+    if (DECAY && b.part == 0) {
       next.put<true>(b, lam, fac);
       if (more) next.load(p, b, seq, c - 1);
     }
@@ -990,8 +997,8 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
         prefetch(c - 1);
       }
     }
-    const float2 own = decays ? lam[b.row] : make_float2(0.f, 0.f);
-    const float2 end = decays ? lam[CT - 1] : make_float2(0.f, 0.f);
+    const float2 own = DECAY ? lam[b.row] : make_float2(0.f, 0.f);
+    const float2 end = DECAY ? lam[CT - 1] : make_float2(0.f, 0.f);
     const float2 all = exp2_two(end);
     if (keep) {
       float s = state.dot_kept(p.kept + p.keep_slot(seq, c) * (D * D), b);
@@ -1020,7 +1027,7 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
         load_16(b, T_P + block * 32 + y, f);
         load_16(b, T_DP + block * 32 + y, g);
         if (DECAY) decay.get(y, d);
-        if (NM == 3 && DECAY && !diagonal) {
+        if (shares && !diagonal) {
           float s[2] = {0.f, 0.f};
 #pragma unroll
           for (int e = 0; e < 16; ++e) s[e % 2] += f[e] * d[e] * g[e];
@@ -1049,7 +1056,7 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
     b.wait_mma(1, phase);
     const float tail = decay_between(end, own);
     float dot = 0.f;
-    if (decays) {  // the state's share, by each token's decay to the chunk's end
+    if (DECAY) {  // the state's share, by each token's decay to the chunk's end
 #pragma unroll
       for (int x = 0; x < 2 * N; x += 16) {
         const bool of_k = x >= N;
@@ -1063,13 +1070,13 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
           r[e] = __float_as_uint(f[e]);
         }
         tmem_st16(b.at((of_k ? T_K : T_V) + col), r);
-        if (NM == 3 && of_k) {
+        if (shares && of_k) {
 #pragma unroll
           for (int e = 0; e < 16; e += 8) dot = dot_8(*b.cell(TK, col + e), f + e, dot);
         }
       }
     }
-    if (NM == 3 && DECAY) b.leave(T_U, dot, pairs);
+    if (shares) b.leave(T_U, dot, pairs);
     tmem_st_wait();
     fence_proxy_async_smem();
     tc_fence_before();
@@ -1086,20 +1093,20 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
         if (EARLY_K) load_k(c - 1);
       }
     }
-    if (NM == 3 && DECAY && b.part == 0) b.gather(T_U, dot, pairs);
-    if (NM == 3 && p.rk && t < p.L) {
+    if (shares && b.part == 0) b.gather(T_U, dot, pairs);
+    if (shares && t < p.L) {
       const size_t to = (size_t)seq * p.L + t;
       if (b.part == 0) p.rk[to] = dot, p.rs[to] = pairs;
     }
-    if (update && decays) {
+    if (update && DECAY) {
       decayed_rows<D, NM, CT>(smem + TQ, smem, 0, [&](int i) { return ex2_approx(lam[i].x); });
       fence_proxy_async_smem();
     }
     tc_fence_before();
-    if (decays) __syncthreads();
+    if (DECAY) __syncthreads();
     if (threadIdx.x == kLeaderKV && update) {  // the state's update, while dk and dv leave
       tc_fence_after();
-      if (decays) {
+      if (DECAY) {
 #pragma unroll
         for (int m = NM - 1; m >= 0; --m)
           product<CT>(b.tmem + T_U, along_col<SM::BOX>(b.base + m * SM::TILE), dO, id_kv,

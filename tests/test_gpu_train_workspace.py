@@ -63,3 +63,26 @@ def test_a_call_without_fp32_gradients_allocates_little():
     api.la_chunk_bwd(q, k, v, dO, dq=outs[0], dk=outs[1], dv=outs[2])
     torch.cuda.synchronize()
     assert torch.cuda.max_memory_allocated() - before < 32 << 20
+
+
+@pytest.mark.parametrize("kind", ["head", "token", "logit"])
+@pytest.mark.parametrize("dtype,phi,dk,dv", [("bf16", "identity", 64, 64), ("bf16", "identity", 128, 128),
+                                             ("bf16", "identity", 32, 128), ("bf16", "elu1", 64, 64),
+                                             ("f32", "identity", 128, 64)])
+def test_state_gradient_without_the_decays(dtype, phi, dk, dv, kind):
+    """dS0 alone is formed as beside ddecay: the same bits, of dq, dk and dv too."""
+    api.la_set_feature_map(phi)
+    g = torch.Generator("cuda").manual_seed(dk)
+    B, H, L = 2, 3, 900
+    q, k, v, dO = (torch.randn(B, H, L, d, generator=g, device="cuda").mul_(0.4).to(DT[dtype])
+                   for d in (dk, dk, dv, dv))
+    decay = torch.randn(B, H, L, generator=g, device="cuda")
+    decay = {"head": -0.01 * decay[0, :, 0].abs(), "token": -decay.abs(), "logit": decay}[kind]
+    S0, dSf = (torch.randn(B, H, dk, dv, generator=g, device="cuda") for _ in range(2))
+    call = lambda ddecay: api.la_chunk_bwd(  # noqa: E731
+        q, k, v, dO, decay_kind=kind, decay=decay.contiguous(), S0=S0, dS_final=dSf, want_decay_grad=ddecay)
+    alone, both = call(False), call(True)
+    api.la_device_status()
+    assert alone[3] is None and both[3] is not None
+    for i in (0, 1, 2, 4):
+        assert torch.equal(alone[i], both[i])
