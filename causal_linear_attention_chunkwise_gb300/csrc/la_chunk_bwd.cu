@@ -92,7 +92,7 @@ size_t lay_out(const ChunkBwdArgs &a, const Plan &plan, bool decay_grad, char *b
     float *around = part(seqs * plan.segments), *sums = part(seqs * plan.segments);
     // Any chunk may hold a strong decay, and then keeps its state.
     const size_t kept = seqs * (plan.chunks - 1), width = plan.wide ? 128 : 64;
-    float *states = part(kept * width * width), *between = part(kept * kShares);
+    float *states = part(kept * (plan.tc ? width * width : es)), *between = part(kept * kShares);
     float *across = plan.tc ? part(2 * seqs * plan.chunks) : nullptr;
     float *strong = part((seqs * plan.chunks + 3) / 4);
     if (p) {

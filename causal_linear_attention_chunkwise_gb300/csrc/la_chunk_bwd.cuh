@@ -80,7 +80,8 @@ struct ChunkBwd {
   float2 *across;              // [seq][chunks] pairs of a chunk's blocks around block 1 and block 2
   float *around;               // [seq][segments] <G, e^L_C S> of a segment's last chunk
   unsigned char *strong;       // [seq][chunks] whether a token of the chunk decays by kStrong
-  float *kept;                 // [seq][chunks - 1] S before a chunk that keeps() it
+  float *kept;                 // [seq][chunks - 1] S before a chunk that keeps() it: d_k d_v
+                               // floats, on tcgen05 those of the padded widths
   float *between;              // [seq][chunks - 1][kShares] <G, e^L_C S> of such a chunk
   int every;
 
@@ -336,25 +337,32 @@ template <typename F> struct StateRows {
 // A state from its three planes in shared memory, which hold all of its bits, to global memory,
 // and the product of such a one with the state whose planes are there: from the registers,
 // both made the walks spill (3 x 5 x 777 x 64 x 128 fp32: 50 and 63 us against 40 and 57).
-template <typename F> __device__ __forceinline__ float plane_sum(const char *tile, int e) {
-  const uint32_t at = tile_offset<F::D>(e / F::D, e % F::D);
+template <typename F> __device__ __forceinline__ float plane_sum(const char *tile, int row, int col) {
+  const uint32_t at = tile_offset<F::D>(row, col);
   float s = 0.f;
 #pragma unroll
   for (int m = F::NM - 1; m >= 0; --m)
     s += __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(tile + m * F::STATE + at));
   return s;
 }
-template <typename F> __device__ __forceinline__ void keep_state(float *dst, const char *tile) {
+template <typename F>
+__device__ __forceinline__ void keep_state(float *dst, const char *tile, const ChunkBwd &p) {
+  const int shift = 31 - __clz(p.n_v), all = p.n_k << shift;  // the widths are powers of two
 #pragma unroll 4
-  for (int e = threadIdx.x; e < F::D * F::D; e += F::THREADS) dst[e] = plane_sum<F>(tile, e);
+  for (int e = threadIdx.x; e < all; e += F::THREADS)
+    dst[e] = plane_sum<F>(tile, e >> shift, e & (p.n_v - 1));
 }
 template <typename F>
-__device__ __forceinline__ float dot_kept(const float *src, const char *tile) {
+__device__ __forceinline__ float dot_kept(const float *src, const char *tile, const ChunkBwd &p) {
+  const int shift = 31 - __clz(p.n_v), all = p.n_k << shift;
   float s[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int e = threadIdx.x; e < F::D * F::D; e += 4 * F::THREADS)
+  for (int e = threadIdx.x; e < all; e += 4 * F::THREADS)
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      s[i] = fmaf(src[e + i * F::THREADS], plane_sum<F>(tile, e + i * F::THREADS), s[i]);
+    for (int i = 0; i < 4; ++i) {
+      const int x = e + i * F::THREADS;
+      if (x < all)
+        s[i] = fmaf(src[x], plane_sum<F>(tile, x >> shift, x & (p.n_v - 1)), s[i]);
+    }
   return (s[0] + s[1]) + (s[2] + s[3]);
 }
 
@@ -649,7 +657,7 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_q_kernel(const Chu
     chunk_decay<F::C>(p, seq, c, sh.decay);
     __syncthreads();
     if (keep)
-      keep_state<F>(p.kept + p.keep_slot(seq, c) * F::D * F::D, state_tile);
+      keep_state<F>(p.kept + p.keep_slot(seq, c) * es, state_tile, p);
     // dO V^T . D: rows j of the group, tokens i <= j
     float w[F::C / 8][4] = {};
     auto live = [&](int j) { return j <= group; };
@@ -776,7 +784,7 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_kv_kernel(const Ch
     chunk_decay<F::C>(p, seq, c, sh.decay);
     __syncthreads();
     if (keep) {
-      float s = dot_kept<F>(p.kept + p.keep_slot(seq, c) * F::D * F::D, state_tile);
+      float s = dot_kept<F>(p.kept + p.keep_slot(seq, c) * es, state_tile, p);
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
       float *to = p.between + p.keep_slot(seq, c) * kShares;

@@ -23,13 +23,14 @@ def parts(B, H, L, dk, dv, dtype, phi, kind, ddecay, dS0):
     full = dtype == "f32" or (phi == "elu1" and (ddecay or dS0))  # inputs as three planes
     tc = not full and not (L <= 64 and not wide and B * H > 152)
     C = 128 if tc else 32 if full else 64
-    seqs, chunks, width = B * H, -(-L // C), 128 if wide else 64
+    seqs, chunks = B * H, -(-L // C)
     n = 0
     if kind != "none":
         n += 8 * seqs * chunks * C                       # log decays, two floats a token
     if ddecay:
         n += 4 * seqs * L * (5 if tc else 3)             # shares
-        n += 4 * seqs * (chunks - 1) * (width * width + 16)  # kept states, <G, S> of them
+        state = (128 if wide else 64) ** 2 if tc else dk * dv
+        n += 4 * seqs * (chunks - 1) * (state + 16)      # kept states, <G, S> of them
         n += seqs * chunks * (9 if tc else 1)            # pairs around blocks, strong decays
     return n, 8 * seqs * dk * dv
 
