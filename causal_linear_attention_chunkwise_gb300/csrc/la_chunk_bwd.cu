@@ -44,8 +44,9 @@ Plan make_plan(const ChunkBwdArgs &a, bool f32_out) {
   p.planes = p.full || f32_out;
   // More narrow sequences of up to 64 tokens than there are SMs: tcgen05's block, of which an SM holds
   // one, stands alone with its start, its end and its few products.  64 x 32 x 64 x 64 with token
-  // decays 166 us from eager calls (146 in a graph), on tcgen05 252 (elu1 without: 110, 132); 8 x 32 x 64 x 64 30, 37; but 4 x 32 x 64
-  // x 64 25, 21; 64 x 32 x 96 x 64 276, 256; 64 x 32 x 64 x 128 457, 458 (167, 137 without decays).
+  // decays 147 us, on tcgen05 197 (elu1 without: 121, 138); 8 x 32 x 64 x 64 28, 31 (elu1 24, 21).  Timed
+  // from the host, before: 4 x 32 x 64 x 64 25, 21; 64 x 32 x 96 x 64 276, 256; 64 x 32 x 64 x 128 457, 458
+  // (167, 137 without decays).
   p.tc = !p.full && !(a.L <= kShort && !p.wide && (long long)a.B * a.H > 152);
   p.chunk = p.tc ? 128 : p.full ? 32 : kShort;
   p.chunks = (a.L + p.chunk - 1) / p.chunk;

@@ -37,8 +37,10 @@
 // with per-head decays: 4.8e-7 off; 4.5e-6 without, growing with the length to the power 1.5).
 //
 // Precision.  Products run in bf16 with fp32 sums.  With bf16 inputs and outputs the
-// decayed scores and the states round once to bf16 as operands (the state itself
-// stays fp32).  The fp32 outputs (ddecay, dS0) take those operands as three bf16
+// scores, the states and what a decay multiplies round once to bf16 as operands (the state itself
+// stays fp32), each about as large as the outputs' own rounding; phi's values of elu + 1 enter dq and dk
+// as two planes, for a third such would be theirs (dq and dk 3.0e-3 off with one plane, 2.35e-3
+// with two).  The fp32 outputs (ddecay, dS0) take those operands as three bf16
 // planes, which hold all of an fp32 value's bits; fp32 inputs, and phi = elu + 1
 // where an fp32 output is wanted, enter as three planes too (v and dO of bf16 inputs as one).
 //
@@ -97,12 +99,12 @@ struct ChunkBwd {
 };
 
 // T: element type; D: padded width (d_k, d_v <= D); C: tokens of a chunk; NI: planes of q
-// and k after phi; NM: planes of the states and of what enters them.
+// and k after phi (two, for outputs in bf16: phi's own rounding would be added to theirs); NM: planes of the states and of what enters them.
 template <typename T_, int D_, int C_, int NI_, int NM_> struct BwdConfig {
   using T = T_;
   static constexpr int D = D_, C = C_, NI = NI_, NM = NM_;
   static constexpr int NV = sizeof(T) == 2 ? 1 : NI;  // of v and dO, which are not mapped
-  static constexpr int NO = NI == 1 ? 1 : 3;          // planes of scores
+  static constexpr int NO = NI < 3 ? 1 : 3;           // planes of scores
   static constexpr int WARPS = D / 16;         // each owns 16 rows of the state
   static constexpr int ROWS = C / 16;          // groups of 16 tokens
   static constexpr int SPLIT = WARPS / ROWS;   // warps that share a group, by columns
@@ -217,9 +219,8 @@ template <typename F> struct TileRows {
       for (int k = 0; k < K; ++k) v[i][k] = load_raw<T, V>(from + k * V);
     }
   }
-  template <bool MAP>
+  template <bool MAP, int NP = MAP ? F::NI : F::NV>
   __device__ __forceinline__ void put(uint32_t tile, const ChunkBwd &p, int width, int t0) const {
-    constexpr int NP = MAP ? F::NI : F::NV;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       int row, col;
@@ -652,7 +653,7 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_q_kernel(const Chu
   for (int c = c0; c < c1; ++c) {
     const int t0 = c * F::C;
     const uint32_t tk = tiles, tv = tk + X, td = tv + Y;
-    const bool keep = F::NI > 1 && p.keeps(seq, c, c1);
+    const bool keep = F::NI == 3 && p.keeps(seq, c, c1);
     load(t0);
     chunk_decay<F::C>(p, seq, c, sh.decay);
     __syncthreads();
@@ -767,7 +768,8 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_kv_kernel(const Ch
     a.fetch(q, p, p.n_k, t), b.fetch(k, p, p.n_k, t);
     c.fetch(v, p, p.n_v, t), d.fetch(dO, p, p.n_v, t);
     a.template put<true>(tiles, p, p.n_k, t);
-    b.template put<true>(tiles + X, p, p.n_k, t);
+    // of phi(k), for dv alone, its rounding averages out
+    b.template put<true, F::NO>(tiles + X, p, p.n_k, t);
     c.template put<false>(tiles + 2 * X, p, p.n_v, t);
     d.template put<false>(tiles + 2 * X + Y, p, p.n_v, t);
   };
@@ -779,7 +781,7 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_kv_kernel(const Ch
     const int t0 = c * F::C;
     const uint32_t tq = tiles;
     const uint32_t tk = tq + X, tv = tk + X, td = tv + Y;
-    const bool keep = F::NI > 1 && p.keeps(seq, c, c1);
+    const bool keep = F::NI == 3 && p.keeps(seq, c, c1);
     load(t0);
     chunk_decay<F::C>(p, seq, c, sh.decay);
     __syncthreads();
@@ -854,7 +856,7 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_kv_kernel(const Ch
           if (lane % 4 == 0) sh.pairs[part][r0 + lane / 4 + 8 * h] = behind[h];
       }
     } else {
-      rows_times_rows<F, CT, F::NI, F::NI>(w, tk, F::TILE, r0, tq, F::TILE, 0, lane, live);
+      rows_times_rows<F, CT, F::NO, F::NO>(w, tk, F::TILE, r0, tq, F::TILE, 0, lane, live);
       rows_times_rows<F, CT, F::NV, F::NV>(dw, tv, F::TILE, r0, td, F::TILE, 0, lane, live);
       constexpr int OWN = CT / F::SPLIT;  // columns (by 8) whose tokens a warp of the group adds up
       float later[2] = {0.f, 0.f};
@@ -882,7 +884,7 @@ __global__ void __launch_bounds__(F::THREADS, F::BLOCKS) grad_kv_kernel(const Ch
     const float t_0 = sh.decay.tail[r0 + lane / 4], t_1 = sh.decay.tail[r0 + lane / 4 + 8];
     {
       float acc[NT][4] = {};
-      rows_times_cols<F, NT, F::NI, F::NO>(acc, tk, F::TILE, r0, G, F::STATE, n0, lane);
+      rows_times_cols<F, NT, F::NO, F::NO>(acc, tk, F::TILE, r0, G, F::STATE, n0, lane);
 #pragma unroll
       for (int n = 0; n < NT; ++n)
         acc[n][0] *= t_0, acc[n][1] *= t_0, acc[n][2] *= t_1, acc[n][3] *= t_1;
@@ -945,7 +947,7 @@ template <typename F> cudaError_t run_chunk_bwd(const ChunkBwd &p, int seqs, cud
   [[maybe_unused]] static int set_share[64];
   static int set_q[64], set_kv[64];
   cudaError_t e;
-  if constexpr (F::NI > 1) {  // else there is one chunk
+  if constexpr (F::NI == 3) {  // else there is one chunk
     if (p.segments > 1) {
       auto share = segment_share_kernel<F>;
       if ((e = tc::set_smem_once(share, share_smem<F>(), set_share)) != cudaSuccess) return e;

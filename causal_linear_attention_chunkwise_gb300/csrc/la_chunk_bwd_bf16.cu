@@ -5,8 +5,9 @@ namespace la {
 
 cudaError_t launch_chunk_bwd_bf16(const ChunkBwd &p, int seqs, bool planes, cudaStream_t stream) {
   using T = __nv_bfloat16;
-  return planes ? run_chunk_bwd<BwdConfig<T, 64, 64, 1, 3>>(p, seqs, stream)
-                : run_chunk_bwd<BwdConfig<T, 64, 64, 1, 1>>(p, seqs, stream);
+  if (planes) return run_chunk_bwd<BwdConfig<T, 64, 64, 1, 3>>(p, seqs, stream);
+  return p.phi == LA_PHI_ELU1 ? run_chunk_bwd<BwdConfig<T, 64, 64, 2, 1>>(p, seqs, stream)
+                              : run_chunk_bwd<BwdConfig<T, 64, 64, 1, 1>>(p, seqs, stream);
 }
 
 }  // namespace la

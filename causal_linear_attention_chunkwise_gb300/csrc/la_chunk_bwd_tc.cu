@@ -59,20 +59,28 @@ constexpr int kLeaderQ = 384, kLeaderKV = 96;
 constexpr uint32_t HI = smem_desc_sw128_hi(1024);
 static_assert(kThreads / 32 == kShares, "a share for each warp");
 
-// Shared memory of a walk with TILES input tiles (in STAGES sets).  The planes come first:
-// a D = 64 operand is read as one of 128 rows, whose other half may be anything.
-template <int D, int NM, int TILES, int STAGES> struct Smem {
+// Shared memory of a walk with TILES input tiles (in STAGES sets) and MORE others.  The planes come
+// first: a D = 64 operand is read as one of 128 rows, whose other half may be anything.
+template <int D, int NM, int TILES, int STAGES, int MORE = 0> struct Smem {
   static constexpr uint32_t BOX = CT * 128;         // 128 tokens x 64 columns
   static constexpr uint32_t TILE = D / 64 * BOX;
   static constexpr uint32_t OFF_TILES = NM * TILE;  // planes: of the decayed tile or the state
   static constexpr uint32_t STAGE = TILES * TILE;
-  static constexpr uint32_t OFF_LAM = OFF_TILES + STAGES * STAGE;  // float2 [CT]
+  static constexpr uint32_t OFF_EXTRA = OFF_TILES + STAGES * STAGE;
+  static constexpr uint32_t OFF_LAM = OFF_EXTRA + MORE * TILE;     // float2 [CT]
   static constexpr uint32_t OFF_FAC = OFF_LAM + CT * 8;            // float [CT]
   static constexpr uint32_t OFF_MORE = OFF_FAC + CT * 4;           // float [2 CT]
   static constexpr uint32_t OFF_BAR = OFF_MORE + 2 * CT * 4;
   static constexpr uint32_t BYTES = OFF_BAR + 128;
   static_assert(BYTES <= 232448, "exceeds the per-block shared memory limit");
 };
+// phi's values lie in shared memory as bf16, and what that rounding leaves out in a tile of its own
+// (low): with one plane alone, phi's rounding would be added to the outputs' own, 3.0e-3 of dq and dk
+// instead of 2.35e-3 (outputs rounded from fp32: 1.7e-3).  The products of scores take it as a second
+// product.  A state of 64 rows leaves half of the lanes of its update free, and the rows of low's share
+// take these (SPLIT): without a product more they become the state's second plane (4 x 16 x 4096 x 64:
+// 140 us; with a product of its own for low's share 150, without low 132).
+template <int D, bool PHI, bool DECAY> constexpr bool kSplit = PHI && !DECAY && D == 64;
 template <int D> struct StateTile {
   static constexpr uint32_t BOX = D * 128;  // 64 columns of a state
   static constexpr uint32_t PLANE = D / 64 * BOX;
@@ -177,6 +185,10 @@ template <uint32_t BOX> __device__ __forceinline__ Operand along_row(uint32_t ad
 template <uint32_t BOX> __device__ __forceinline__ Operand along_col(uint32_t addr) {
   return {smem_desc_sw128_lo(addr, BOX), 2048 >> 4, 0};
 }
+// 64 columns at addr and 64 at next, which lies behind it.
+__device__ __forceinline__ Operand along_cols(uint32_t addr, uint32_t next) {
+  return {smem_desc_sw128_lo(addr, next - addr), 2048 >> 4, 0};
+}
 __device__ __forceinline__ uint32_t word(const Operand &o, int kk) {
   return o.lo + kk * o.step + kk / 4 * o.wrap;
 }
@@ -223,31 +235,37 @@ __device__ __forceinline__ void store_tile_tma(const Block &b, uint32_t off,
     if (x * 64 < width) tma_store_3d(map, b.smem + off + x * CT * 128, x * 64, token, seq);
 }
 
-// dst = elu + 1 of a tile (dst may be the tile); rows past the last token and columns past the
-// width are zero.
-template <int D>
+// dst = elu + 1 of a tile (dst may be the tile) as bf16, and, LOW, low = what that rounding left out;
+// rows past the last token and columns past the width are zero.
+template <int D, bool LOW>
 __device__ __forceinline__ void map_tile_tc(const unsigned char *tile, unsigned char *dst,
-                                            int rows, int width) {
+                                            unsigned char *low, int rows, int width) {
 #pragma unroll
   for (int i = 0; i < CT * D / 8 / kThreads; ++i) {
     const int x = threadIdx.x + i * kThreads;
     const int row = x / 8 % CT, col = x / 8 / CT * 64 + ((x % 8) ^ (row & 7)) * 8;
     const bool live = row < rows && col < width;
     const uint4 u = reinterpret_cast<const uint4 *>(tile)[x];
-    uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    uint32_t out[1 + LOW][4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      w[e] = la::pack_bf16(tc::elu1_fast(bf16_lo(w[e])), tc::elu1_fast(bf16_hi(w[e])));
-      if (!live) w[e] = 0;
+      split<1 + LOW>(tc::elu1_fast(bf16_lo(w[e])), tc::elu1_fast(bf16_hi(w[e])), &out[0][e], 4);
+#pragma unroll
+      for (int n = 0; n < 1 + LOW; ++n)
+        if (!live) out[n][e] = 0;
     }
-    reinterpret_cast<uint4 *>(dst)[x] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4 *>(dst)[x] = make_uint4(out[0][0], out[0][1], out[0][2], out[0][3]);
+    if constexpr (LOW)
+      reinterpret_cast<uint4 *>(low)[x] = make_uint4(out[1][0], out[1][1], out[1][2], out[1][3]);
   }
 }
 
-// dst (NM planes) = weight(token) * tile, at the tile's own places: ROWS tokens from row0 on.
-template <int D, int NM, int ROWS, typename Weight>
-__device__ __forceinline__ void decayed_rows(const unsigned char *tile, unsigned char *dst,
-                                             int row0, Weight weight) {
+// dst (NM planes) = weight(token) * (tile + low), at the tile's own places: ROWS tokens from row0
+// on.  LOW: there is a low.
+template <int D, int NM, int ROWS, bool LOW, typename Weight>
+__device__ __forceinline__ void decayed_rows(const unsigned char *tile, const unsigned char *low,
+                                             unsigned char *dst, int row0, Weight weight) {
   constexpr uint32_t TILE = CT * D * 2;
 #pragma unroll 4
   for (int i = 0; i < ROWS * D / 8 / kThreads; ++i) {
@@ -256,10 +274,18 @@ __device__ __forceinline__ void decayed_rows(const unsigned char *tile, unsigned
     const uint4 u = reinterpret_cast<const uint4 *>(tile)[at];
     const float f = weight(row);
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    uint32_t l[4] = {0, 0, 0, 0};
+    if constexpr (LOW) {
+      const uint4 v = reinterpret_cast<const uint4 *>(low)[at];
+      l[0] = v.x, l[1] = v.y, l[2] = v.z, l[3] = v.w;
+    }
     uint32_t out[NM][4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      split<NM>(bf16_lo(w[e]) * f, bf16_hi(w[e]) * f, &out[0][e], 4);
+    for (int e = 0; e < 4; ++e) {
+      const float x = LOW ? bf16_lo(w[e]) + bf16_lo(l[e]) : bf16_lo(w[e]);
+      const float y = LOW ? bf16_hi(w[e]) + bf16_hi(l[e]) : bf16_hi(w[e]);
+      split<NM>(x * f, y * f, &out[0][e], 4);
+    }
 #pragma unroll
     for (int m = 0; m < NM; ++m)
       reinterpret_cast<uint4 *>(dst + m * TILE)[at] =
@@ -345,8 +371,9 @@ struct RowDecay {
 };
 
 // ---------------------------------------------------------------- the state
-// A thread's part of the state: row `row` (rows < D), N columns from N part on.
-template <int D, int NM> struct StateRow {
+// A thread's part of the state: row `row` (rows < D), N columns from N part on.  SPLIT: the rows from D
+// on hold the share of phi's low parts.
+template <int D, int NM, bool SPLIT = false> struct StateRow {
   static constexpr int N = D / PARTS;
   float c[N];
 
@@ -376,13 +403,15 @@ template <int D, int NM> struct StateRow {
   }
   // As planes of operand tiles [D][D] (64-column boxes).
   __device__ __forceinline__ void planes(const Block &b) const {
-    if (b.row >= D) return;
+    static_assert(!SPLIT || (NM == 1 && D == 64), "two planes, of 64 rows each");
+    if (!SPLIT && b.row >= D) return;
 #pragma unroll
     for (int i = 0; i < N; i += 8) {
       const int col = b.part * N + i;
       uint32_t w[NM][4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) split<NM>(c[i + 2 * e], c[i + 2 * e + 1], &w[0][e], 4);
+      // SPLIT: row 64 is the second plane's first
       unsigned char *at = b.smem + col / 64 * (D * 128) + b.row * 128 +
                           (((col % 64 / 8) ^ (b.row & 7)) << 4);
 #pragma unroll
@@ -394,7 +423,7 @@ template <int D, int NM> struct StateRow {
   // c <- all c + the update in tensor memory.  The tensor cores cut a sum's last bits
   // off; formed chunk by chunk and added here, the cuts do not add up.
   __device__ __forceinline__ void update(const Block &b, uint32_t col, float2 all) {
-    if (b.quarter * 32 >= D) return;
+    if (!SPLIT && b.quarter * 32 >= D) return;
     uint32_t r[N];
     if constexpr (N == 32) tmem_ld32(b.at(col + b.part * N), r);
     else tmem_ld16(b.at(col + b.part * N), r);
@@ -483,9 +512,12 @@ __device__ __forceinline__ float dot_8(const uint4 &u, const float *f, float s) 
 // The decayed tile is formed in two halves of 64 tokens, each while the products of the other
 // run; a chunk's sum is added to the state while the next one's products run.
 template <int D, int NM, bool PHI, bool DECAY>
+using ShareSmem = Smem<D, DECAY ? NM : 0, 2, 2, PHI ? DECAY ? 1 : 2 : 0>;
+template <int D, int NM, bool PHI, bool DECAY>
 __global__ void __launch_bounds__(kThreads, 1)
 segment_share_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned int *err) {
-  using SM = Smem<D, NM, 2, 2>;
+  using SM = ShareSmem<D, NM, PHI, DECAY>;
+  constexpr bool SPLIT = kSplit<D, PHI, DECAY>;
   constexpr uint32_t id_kv = idesc_bf16_f32(128, D, true, true), COLUMNS = 2 * D;
   extern __shared__ __align__(1024) unsigned char smem[];
   Block b;
@@ -508,7 +540,7 @@ segment_share_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, uns
     load(0);
     if (n > 1) load(1);
   }
-  StateRow<D, NM> state;
+  StateRow<D, NM, SPLIT> state;
   state.load(nullptr, b, p);
   double total = 0.0;
   // each thread of part 0: its token's log decay and the chunk's, a chunk ahead
@@ -536,8 +568,10 @@ segment_share_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, uns
     unsigned char *tile = smem + SM::OFF_TILES + (i & 1) * SM::STAGE;
     const uint32_t tile_at = smem_u32(tile), sum = b.tmem + (i & 1) * D;
     const Operand y = along_col<SM::BOX>(tile_at + SM::TILE);
+    // phi's low parts: without decays one of two tiles in turn, since the last chunk's may still be read
+    const uint32_t low = SM::OFF_EXTRA + (DECAY ? 0 : (i & 1) * SM::TILE);
     if (PHI) {
-      map_tile_tc<D>(tile, tile, p.L - chunk(i) * CT, p.n_k);
+      map_tile_tc<D, true>(tile, tile, smem + low, p.L - chunk(i) * CT, p.n_k);
       if (DECAY) __syncthreads();
     }
     if (DECAY) {
@@ -553,7 +587,7 @@ segment_share_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, uns
           }
         }
         const float *w = weights + (i & 1) * CT;
-        decayed_rows<D, NM, 64>(tile, smem, h * 64, [&](int t) { return w[t]; });
+        decayed_rows<D, NM, 64, PHI>(tile, smem + low, smem, h * 64, [&](int t) { return w[t]; });
         fence_proxy_async_smem();
         tc_fence_before();
         if ((stop = __syncthreads_or(b.failed))) break;
@@ -579,7 +613,10 @@ segment_share_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, uns
       if ((stop = __syncthreads_or(b.failed))) break;
       if (threadIdx.x == 0) {
         tc_fence_after();
-        product<CT>(sum, along_col<SM::BOX>(tile_at), y, id_kv, false);
+        constexpr bool TWO = PHI && !SPLIT;
+        if (TWO) product<CT>(sum, along_col<SM::BOX>(b.base + low), y, id_kv, false);
+        product<CT>(sum, SPLIT ? along_cols(tile_at, b.base + low) : along_col<SM::BOX>(tile_at), y,
+                    id_kv, TWO);
         mma_commit(&b.mma[1]);
       }
     }
@@ -594,6 +631,16 @@ segment_share_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, uns
     b.wait_mma(1, (n - 1) & 1);
     state.update(b, ((n - 1) & 1) * D, exp2_two(last));
     const size_t slot = (size_t)seq * (p.segments - 1) + of;
+    if constexpr (SPLIT) {  // both shares of the state in one
+      float *other = reinterpret_cast<float *>(smem) + b.row % D * D + b.part * (D / PARTS);
+      if (b.row >= D)
+#pragma unroll
+        for (int j = 0; j < D / PARTS; ++j) other[j] = state.c[j];
+      __syncthreads();
+      if (b.row < D)
+#pragma unroll
+        for (int j = 0; j < D / PARTS; ++j) state.c[j] += other[j];
+    }
     state.store((back ? p.W : p.U) + slot * p.n_k * p.n_v, b, p);
     if (threadIdx.x == 0 && (!back || seg == p.segments - 1))
       p.total[(size_t)seq * p.segments + seg] = (float)total;
@@ -604,8 +651,8 @@ segment_share_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, uns
 }
 
 // Sets of input tiles of the walks below: with two, which D = 64 has room for, a chunk's tiles are
-// loaded while the last chunk is worked on (4 x 16 x 4096 x 64 elu1: grad_q 45 us, grad_kv 58; with
-// one set 53 and 70).
+// loaded while the last chunk is worked on (4 x 16 x 4096 x 64 elu1, before phi's low parts: grad_q 45
+// us, grad_kv 58; with one set 53 and 70).
 template <int D> constexpr int kStages = D == 64 ? 2 : 1;
 
 // ---------------------------------------------------------------- dq
@@ -614,8 +661,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned int *err) {
   // The fourth tile: q, where it is needed (for ddecay, for phi's derivative), then dq on its way
   // out.
-  using SM = Smem<D, NM, 4, kStages<D>>;
+  using SM = Smem<D, NM, 4, kStages<D>, PHI>;
   using ST = StateTile<D>;
+  constexpr bool SPLIT = kSplit<D, PHI, DECAY>;
+  constexpr int NS = SPLIT ? 2 : NM;  // planes of the state
   constexpr bool TWO = kStages<D> == 2, HAS_Q = (NM == 3 && DECAY) || PHI;
   // Tensor memory: dO V^T, the state's share, the scores' share, the scores as operand; the
   // state's update takes the place of dO V^T.
@@ -628,6 +677,7 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
   // NM = 3: Q K^T as well, in the scores' share's place or behind everything.
   constexpr uint32_t T_P = D == 128 ? T_OUT : 384;
   // the parts' sums of a row
+  constexpr uint32_t LOW = SM::OFF_EXTRA;  // of phi(k)
   constexpr uint32_t T_MORE = T_A + 64, T_CROSS = T_MORE + 8;
   static_assert(T_CROSS + 32 <= (D == 128 ? COLUMNS : T_P), "tensor memory");
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -671,7 +721,7 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
   }
   TokenDecay next;
   next.load(p, b, seq, c0);
-  StateRow<D, NM> state;
+  StateRow<D, NM, SPLIT> state;
   state.load(seg ? p.U + ((size_t)seq * (p.segments - 1) + seg - 1) * es
                  : p.S0 ? p.S0 + (size_t)seq * es : nullptr, b, p);
   state.planes(b);
@@ -688,7 +738,7 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
     }
     const bool keep = NM == 3 && DECAY && p.keeps(seq, c, c1);
     b.wait_full(stage(c), TWO ? (c - c0) >> 1 & 1 : phase);
-    if (PHI) map_tile_tc<D>(smem + TK, smem + TK, p.L - t0, p.n_k);
+    if (PHI) map_tile_tc<D, true>(smem + TK, smem + TK, smem + LOW, p.L - t0, p.n_k);
     fence_proxy_async_smem();
     tc_fence_before();
     if (__syncthreads_or(b.failed)) break;
@@ -701,9 +751,9 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
                    id_s, false);
       mma_commit(&b.mma[0]);
 #pragma unroll
-      for (int m = NM - 1; m >= 0; --m)
+      for (int m = NS - 1; m >= 0; --m)
         product<D>(b.tmem + T_IN, a, along_row<ST::BOX>(b.base + m * ST::PLANE), id_in,
-                   m < NM - 1);
+                   m < NS - 1);
       mma_commit(&b.mma[1]);
       if (more && TWO) {
         tma_store_wait_read_all();  // the last chunk's dq
@@ -774,9 +824,11 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
     tc_fence_before();
     __syncthreads();
     const Operand k = along_col<SM::BOX>(b.base + TK), v = along_col<SM::BOX>(b.base + TV);
+    const Operand k_low = along_col<SM::BOX>(b.base + LOW);
     if (threadIdx.x == kLeaderQ) {  // the scores' share, while the decayed K is formed
       tc_fence_after();
-      product_ta<CT>(b.tmem + T_OUT, b.tmem + T_A, k, id_out, false);
+      if (PHI) product_ta<CT>(b.tmem + T_OUT, b.tmem + T_A, k_low, id_out, false);
+      product_ta<CT>(b.tmem + T_OUT, b.tmem + T_A, k, id_out, PHI);
       mma_commit(&b.mma[2]);
     }
     b.wait_mma(1, phase);  // the state's planes and dO are read
@@ -784,7 +836,8 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
     __syncwarp();
     if (more) {
       if (DECAY) {
-        decayed_rows<D, NM, CT>(smem + TK, smem, 0, [&](int i) { return decay_between(end, lam[i]); });
+        decayed_rows<D, NM, CT, PHI>(smem + TK, smem + LOW, smem, 0,
+                                     [&](int i) { return decay_between(end, lam[i]); });
         fence_proxy_async_smem();
         __syncthreads();
       }
@@ -796,7 +849,9 @@ grad_q_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned i
             product<CT>(b.tmem + T_S, along_col<SM::BOX>(b.base + m * SM::TILE), v, id_kv,
                         m < NM - 1);
         } else {
-          product<CT>(b.tmem + T_S, k, v, id_kv, false);
+          constexpr bool BOTH = PHI && !SPLIT;
+          if (BOTH) product<CT>(b.tmem + T_S, k_low, v, id_kv, false);
+          product<CT>(b.tmem + T_S, SPLIT ? along_cols(b.base + TK, b.base + LOW) : k, v, id_kv, BOTH);
         }
         mma_commit(&b.mma[3]);
       }
@@ -892,17 +947,20 @@ template <int D, int NM, bool PHI> constexpr bool kv_own_tiles() {
   return D == 64 || (NM == 1 && !PHI);
 }
 template <int D, int NM, bool PHI> constexpr int kv_tiles() {
-  return 4 * kStages<D> + PHI + (kv_own_tiles<D, NM, PHI>() ? 2 : 0);
+  return 4 * kStages<D> + 2 * PHI + (kv_own_tiles<D, NM, PHI>() ? 2 : 0);
 }
 template <int D, int NM, bool PHI, bool DECAY>
 __global__ void __launch_bounds__(kThreads, 1)
 grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned int *err) {
-  // A tile of its own holds phi(k) beside k, which its derivative needs.  dk and dv leave by
+  // A tile of its own holds phi(k) beside k, which its derivative needs, and another phi(q)'s low part
+  // (phi(k)'s would enter dv alone, where its rounding averages out).  dk and dv leave by
   // tiles of their own; where there is no room for them, by k's and v's, which then load
   // late (through the state's planes instead they kept these waiting: 256 us against 238).
   using SM = Smem<D, NM, kv_tiles<D, NM, PHI>(), 1>;
   using ST = StateTile<D>;
   constexpr bool TWO = kStages<D> == 2, OWN = kv_own_tiles<D, NM, PHI>(), EARLY_K = OWN && !PHI;
+  constexpr bool SPLIT = kSplit<D, PHI, DECAY>;
+  constexpr int NS = SPLIT ? 2 : NM;  // planes of the state
   // Tensor memory: K Q^T and V dO^T, dv, dk.  When the scores have been read their operands
   // take columns 0..63 and 192..255, the state's update those between.
   constexpr uint32_t T_P = 0, T_DP = 128, T_V = 256, T_K = 256 + D, COLUMNS = 512;
@@ -922,7 +980,7 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
   const size_t es = (size_t)p.n_k * p.n_v;
   const bool shares = NM == 3 && DECAY && p.rk;  // of ddecay
   constexpr uint32_t MORE = SM::OFF_TILES + 4 * kStages<D> * SM::TILE;
-  constexpr uint32_t OUT = MORE + PHI * SM::TILE;
+  constexpr uint32_t LOW = MORE + SM::TILE, OUT = MORE + 2 * PHI * SM::TILE;
   auto stage = [&](int c) { return TWO ? (c1 - 1 - c) & 1 : 0; };
   auto tile = [&](int c, int i) {  // q, k, v, dO
     return SM::OFF_TILES + (stage(c) * 4 + i) * SM::TILE;
@@ -950,7 +1008,7 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
   }
   TokenDecay next;
   next.load(p, b, seq, c1 - 1);
-  StateRow<D, NM> state;
+  StateRow<D, NM, SPLIT> state;
   state.load(seg + 1 < p.segments ? p.W + ((size_t)seq * (p.segments - 1) + seg) * es
              : p.dSf ? p.dSf + (size_t)seq * es : nullptr, b, p);
   state.planes(b);
@@ -968,8 +1026,8 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
     const bool keep = NM == 3 && DECAY && p.keeps(seq, c, c1);
     b.wait_full(stage(c), TWO ? done >> 1 & 1 : phase);
     if (PHI) {
-      map_tile_tc<D>(smem + TQ, smem + TQ, p.L - t0, p.n_k);
-      map_tile_tc<D>(smem + TK, smem + TKP, p.L - t0, p.n_k);
+      map_tile_tc<D, true>(smem + TQ, smem + TQ, smem + LOW, p.L - t0, p.n_k);
+      map_tile_tc<D, false>(smem + TK, smem + TKP, nullptr, p.L - t0, p.n_k);
     }
     if (OWN && threadIdx.x == kLeaderKV) tma_store_wait_read_all();
     fence_proxy_async_smem();
@@ -983,9 +1041,9 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
       mma_commit(&b.mma[0]);
       product<D>(b.tmem + T_V, ak, along_col<ST::BOX>(b.base), id_out, false);
 #pragma unroll
-      for (int m = NM - 1; m >= 0; --m)
+      for (int m = NS - 1; m >= 0; --m)
         product<D>(b.tmem + T_K, av, along_row<ST::BOX>(b.base + m * ST::PLANE), id_in,
-                   m < NM - 1);
+                   m < NS - 1);
       mma_commit(&b.mma[1]);
       if (more && TWO) {
         arm(c - 1);
@@ -1082,9 +1140,11 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
     tc_fence_before();
     __syncthreads();
     const Operand q = along_col<SM::BOX>(b.base + TQ), dO = along_col<SM::BOX>(b.base + TD);
+    const Operand q_low = along_col<SM::BOX>(b.base + LOW);
     if (threadIdx.x == kLeaderKV) {  // the scores' share, while the decayed Q is formed
       tc_fence_after();
       product_ta<CT>(b.tmem + T_V, b.tmem + T_AP, dO, id_out, true);
+      if (PHI) product_ta<CT>(b.tmem + T_K, b.tmem + T_ADP, q_low, id_out, true);
       product_ta<CT>(b.tmem + T_K, b.tmem + T_ADP, q, id_out, true);
       mma_commit(&b.mma[2]);
       if (more && !TWO) {
@@ -1099,7 +1159,8 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
       if (b.part == 0) p.rk[to] = dot, p.rs[to] = pairs;
     }
     if (update && DECAY) {
-      decayed_rows<D, NM, CT>(smem + TQ, smem, 0, [&](int i) { return ex2_approx(lam[i].x); });
+      decayed_rows<D, NM, CT, PHI>(smem + TQ, smem + LOW, smem, 0,
+                                   [&](int i) { return ex2_approx(lam[i].x); });
       fence_proxy_async_smem();
     }
     tc_fence_before();
@@ -1112,7 +1173,9 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
           product<CT>(b.tmem + T_U, along_col<SM::BOX>(b.base + m * SM::TILE), dO, id_kv,
                       m < NM - 1);
       } else {
-        product<CT>(b.tmem + T_U, q, dO, id_kv, false);
+        constexpr bool BOTH = PHI && !SPLIT;
+        if (BOTH) product<CT>(b.tmem + T_U, q_low, dO, id_kv, false);
+        product<CT>(b.tmem + T_U, SPLIT ? along_cols(b.base + TQ, b.base + LOW) : q, dO, id_kv, BOTH);
       }
       mma_commit(&b.mma[3]);
     }
@@ -1167,8 +1230,8 @@ grad_kv_tc_kernel(const __grid_constant__ Maps maps, const ChunkBwd p, unsigned 
 
 template <int D, int NM, bool PHI, bool DECAY>
 cudaError_t launch_tc(const ChunkBwd &p, int seqs, cudaStream_t stream) {
-  using SS = Smem<D, NM, 2, 2>;
-  using SQ = Smem<D, NM, 4, kStages<D>>;
+  using SS = ShareSmem<D, NM, PHI, DECAY>;
+  using SQ = Smem<D, NM, 4, kStages<D>, PHI>;
   using SK = Smem<D, NM, kv_tiles<D, NM, PHI>(), 1>;
   Maps m;
   const struct {
