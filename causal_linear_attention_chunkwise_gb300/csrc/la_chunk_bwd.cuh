@@ -20,7 +20,8 @@
 //
 // Most bf16 calls run in la_chunk_bwd_tc.cu.  The kernels here take what enters as three bf16 planes,
 // fp32 tensors and phi = elu + 1 where an fp32 output is wanted (there is no such form there; at
-// width 128 three planes of 128 tokens would not fit), and many short bf16 sequences.  A warp owns 16 tokens of a
+// width 128 three planes of 128 tokens would not fit), and many short bf16 sequences.  A warp owns 16
+// tokens of a
 // chunk (with others, which take other columns) and computes its rows of the score matrices in the
 // orientation that its products need (dO V^T for dq, V dO^T and K Q^T for dk and dv).
 //
@@ -99,7 +100,8 @@ struct ChunkBwd {
 };
 
 // T: element type; D: padded width (d_k, d_v <= D); C: tokens of a chunk; NI: planes of q
-// and k after phi (two, for outputs in bf16: phi's own rounding would be added to theirs); NM: planes of the states and of what enters them.
+// and k after phi (two, for outputs in bf16: phi's own rounding would be added to theirs); NM: planes
+// of the states and of what enters them.
 template <typename T_, int D_, int C_, int NI_, int NM_> struct BwdConfig {
   using T = T_;
   static constexpr int D = D_, C = C_, NI = NI_, NM = NM_;
